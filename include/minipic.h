@@ -342,6 +342,151 @@ typedef struct {
 minipic_status minipic_kv_append(minipic_dtype dtype, const minipic_kv_pool_mut* kv,
                                  const minipic_kv_append_batch* batch, minipic_stream_t stream);
 
+/* ------------------------------------------------------------------ 8-bit cache
+ * The position-free cache in half the bytes of bf16: keys (unrotated, as
+ * everywhere) and values as OCP e4m3 with one fp32 scale per (block, kv head)
+ * and pool; a stored value is its e4m3 value times that scale.  A block read at
+ * many offsets is quantised once, when it is appended.  Blocks are 16 keys. */
+typedef struct {
+  const void* k_pool;     /* [num_blocks][num_kv_heads][block_size][head_dim] e4m3, unrotated keys */
+  const void* v_pool;     /* same layout, values */
+  const float* k_scale;   /* [num_blocks][num_kv_heads], finite and >= 0 */
+  const float* v_scale;
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+  int32_t block_size;     /* must be 16 */
+  int32_t head_dim;       /* 64 or 128 */
+} minipic_kv_pool_q8;
+
+/* Writable view of the same. */
+typedef struct {
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t head_dim;
+} minipic_kv_pool_q8_mut;
+
+/* Quantise new keys and values into their slots (the mapping of
+ * minipic_kv_append; dtype f32 or bf16 is that of k_new and v_new).  Per block
+ * and kv head, K and V apart, with x the finite values that this call adds:
+ *   s = 2^k, the least k >= -100 with max |x| <= 448 * 2^k.
+ * A block whose first slot this call writes takes s; one that the call enters
+ * at a later slot keeps the rows before it and takes max(its scale, s), and
+ * when that grows those rows are re-rounded to it.  Values are x / scale
+ * rounded to the nearest e4m3 (ties to even); an infinite x is stored as the
+ * largest value (+-448 * scale) and sets MINIPIC_DEVERR_RANGE, a NaN stays one.
+ * Slots after the added rows keep their bytes.
+ * A block id outside [0, num_blocks) sets MINIPIC_DEVERR_BLOCK_ID and a key
+ * index outside the table MINIPIC_DEVERR_SEQ_LEN; such blocks are skipped.  A
+ * negative kv_start, or rows outside [0, total_new), sets
+ * MINIPIC_DEVERR_SEQ_LEN and skips the request.  Every block must be the
+ * target of at most one request of a call.  Asynchronous on `stream`. */
+minipic_status minipic_kv_append_q8(minipic_dtype dtype, const minipic_kv_pool_q8_mut* kv,
+                                    const minipic_kv_append_batch* batch, minipic_stream_t stream);
+
+/* Workspace bytes of minipic_attn_decode_q8 for this shape on the current
+ * device, enough with and without block weights. */
+size_t minipic_attn_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                             int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size);
+
+/* Decode attention over the 8-bit cache: minipic_attn_decode with the pool's
+ * values in place of stored ones (dtype f32 or bf16 is that of q and out; f32
+ * computes in fp32 throughout, bf16 uses fp16 tensor-core products with fp32
+ * accumulation and reads rope->cos_sin_f16, required there).  A NaN that a
+ * query attends to makes its output NaN; slots past a request's length are
+ * never read into a sum, whatever they hold.
+ * block_weights (may be NULL): device, dtype's type, 16-byte aligned,
+ * [batch][num_kv_heads][max_blocks_per_seq]: entry (r, g, b) receives the
+ * softmax weight of block b's keys, summed over them and over the query heads
+ * of kv head g (so it lies in [0, num_q_heads / num_kv_heads]); entries of
+ * blocks past the request's length are left as they were.
+ * workspace: zero it once after allocating it (the convention of
+ * minipic_attn_decode); calls of any shapes may follow one another on it as
+ * long as each has at most 16384 (request, kv head) pairs (else zero it when
+ * the shape changes); calls whose work overlaps on the GPU need workspaces of
+ * their own.  Errors as for minipic_attn_decode; UNSUPPORTED also for more than
+ * 65535 requests or kv heads. */
+minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
+                                      const minipic_rope* rope, const minipic_decode_batch* batch, float scale,
+                                      void* block_weights, void* workspace, size_t workspace_bytes,
+                                      minipic_stream_t stream);
+
+/* Workspace bytes of minipic_attn_prefill_q8: the batch's blocks in bf16, K and
+ * V, in request order (4 bytes per key, kv head and head dim element), and a table. */
+size_t minipic_attn_prefill_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t max_q_len, int32_t max_blocks_per_seq,
+                                              int32_t block_size);
+
+/* Chunked prefill over the 8-bit cache (the chunk's own keys are its last ones
+ * and were appended before): the gathered blocks are widened to bf16 in the
+ * workspace (exact where a scale is a power of two, as the append writes them,
+ * else rounded once) and minipic_attn_prefill's kernel runs over them.  bf16
+ * only.  The workspace needs no initial value and holds nothing between calls.
+ * Errors as for minipic_attn_prefill, WORKSPACE when it is too small,
+ * UNSUPPORTED when batch * max_blocks_per_seq * num_kv_heads * 16 exceeds
+ * 2^31 - 1. */
+minipic_status minipic_attn_prefill_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
+                                       const minipic_rope* rope, const minipic_prefill_batch* batch, float scale,
+                                       void* workspace, size_t workspace_bytes, minipic_stream_t stream);
+
+/* ------------------------------------------------------------------ eviction by attention weight
+ * Bounded contexts: decode records how much attention each block received, the
+ * caller accumulates it, and the least attended blocks leave the tables.  The
+ * blocks that stay keep their logical starts in block_starts, so nothing in
+ * the pool moves and no key changes its position. */
+
+/* Workspace bytes of minipic_attn_decode_weights for this shape. */
+size_t minipic_attn_decode_weights_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                  int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size);
+
+/* minipic_attn_decode that also writes block_weights (required; layout, type
+ * and workspace rules as for minipic_attn_decode_q8). */
+minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                                           const minipic_rope* rope, const minipic_decode_batch* batch, float scale,
+                                           void* block_weights, void* workspace, size_t workspace_bytes,
+                                           minipic_stream_t stream);
+
+/* One eviction step.  Every *_out may be the matching input (in place) or
+ * memory that overlaps no input. */
+typedef struct {
+  const void* block_weights;    /* [batch][num_kv_heads][max_blocks_per_seq] or NULL (no update) */
+  const float* scores;          /* [batch][max_blocks_per_seq] accumulated weight of each block */
+  const int32_t* block_tables;  /* [batch][max_blocks_per_seq] */
+  const int32_t* block_starts;  /* [batch][max_blocks_per_seq] */
+  const int32_t* seq_lens;      /* [batch] */
+  float* scores_out;
+  int32_t* block_tables_out;
+  int32_t* block_starts_out;
+  int32_t* seq_lens_out;
+  int32_t* evicted;             /* [batch][max_blocks_per_seq] physical ids that left, in table order, then -1 */
+  int32_t* n_evicted;           /* [batch] */
+  int32_t batch;
+  int32_t max_blocks_per_seq;
+  int32_t num_kv_heads;         /* of block_weights (ignored when it is NULL) */
+  int32_t budget;               /* blocks a request may keep, >= keep_first + keep_last */
+  int32_t keep_first;           /* >= 0: these first blocks always stay */
+  int32_t keep_last;            /* >= 1: so do these last ones (the block being written among them) */
+  float decay;                  /* finite, >= 0 */
+} minipic_kv_evict_batch;
+
+/* For each block b < ceil(seq_len / block_size) of each request:
+ *   score = decay * score + sum over kv heads of block_weights   (added in fp64, kept in fp32)
+ * and when a request has more than `budget` blocks, its first keep_first and
+ * last keep_last stay together with the best of the others by score (NaN is
+ * the worst; of equal scores the lower index stays) up to `budget`.  The
+ * outputs hold the kept blocks in order, seq_lens_out is shorter by
+ * block_size for each block that left, and the entries behind are -1 (tables),
+ * 0 (starts) and 0 (scores).  dtype is that of block_weights.  A length that is
+ * negative or above max_blocks_per_seq * 16 sets MINIPIC_DEVERR_SEQ_LEN and is
+ * clamped.  The pools are not touched: a block listed in `evicted` may still
+ * belong to other requests, which the caller's block accounting knows
+ * (minipic_prefix_cache_release).  Asynchronous on `stream`. */
+minipic_status minipic_kv_evict(minipic_dtype dtype, const minipic_kv_evict_batch* batch, minipic_stream_t stream);
+
 /* ------------------------------------------------------------------ host offload
  * Moving whole blocks between the pools and host memory (MiniPIC summary,
  * section 3, item 5: unrotated blocks move between GPU and host with no

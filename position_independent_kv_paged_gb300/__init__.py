@@ -16,10 +16,11 @@ with their positions; the kernels rotate both with the cos/sin table built by
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 __all__ = [
     "MiniPICError",
@@ -39,6 +40,15 @@ __all__ = [
     "kv_append",
     "kv_swap_out",
     "kv_swap_in",
+    "kv_append_q8",
+    "attn_decode_q8_workspace_size",
+    "attn_decode_q8",
+    "attn_prefill_q8_workspace_size",
+    "attn_prefill_q8",
+    "attn_decode_weights_workspace_size",
+    "attn_decode_weights",
+    "KVEvicted",
+    "kv_evict",
     "device_error",
     "block_hashes",
     "PrefixCache",
@@ -71,6 +81,20 @@ class _Append(ctypes.Structure):
                 ("kv_start", ctypes.c_void_p), ("block_tables", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("total_new", ctypes.c_int32), ("max_new_len", ctypes.c_int32),
                 ("max_blocks_per_seq", ctypes.c_int32)]
+
+
+class _KVQ8(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("block_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _Evict(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("block_weights", "scores", "block_tables", "block_starts", "seq_lens",
+                                               "scores_out", "block_tables_out", "block_starts_out", "seq_lens_out",
+                                               "evicted", "n_evicted")] + \
+               [(n, ctypes.c_int32) for n in ("batch", "max_blocks_per_seq", "num_kv_heads", "budget", "keep_first",
+                                              "keep_last")] + [("decay", ctypes.c_float)]
 
 
 class _Rope(ctypes.Structure):
@@ -148,6 +172,25 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         for fn in (L.minipic_kv_swap_out, L.minipic_kv_swap_in):
             fn.restype = ctypes.c_int
             fn.argtypes = [ctypes.c_int, ctypes.POINTER(_KV), c_vp, c_i32, c_vp, c_vp, c_vp]
+        L.minipic_kv_append_q8.restype = ctypes.c_int
+        L.minipic_kv_append_q8.argtypes = [ctypes.c_int, ctypes.POINTER(_KVQ8), ctypes.POINTER(_Append), c_vp]
+        L.minipic_attn_decode_q8_workspace_size.restype = c_sz
+        L.minipic_attn_decode_q8_workspace_size.argtypes = [c_i32] * 6
+        L.minipic_attn_decode_q8.restype = ctypes.c_int
+        L.minipic_attn_decode_q8.argtypes = [ctypes.c_int, c_i32, ctypes.POINTER(_KVQ8), ctypes.POINTER(_Rope),
+                                             ctypes.POINTER(_Decode), c_f, c_vp, c_vp, c_sz, c_vp]
+        L.minipic_attn_prefill_q8_workspace_size.restype = c_sz
+        L.minipic_attn_prefill_q8_workspace_size.argtypes = [c_i32] * 7
+        L.minipic_attn_prefill_q8.restype = ctypes.c_int
+        L.minipic_attn_prefill_q8.argtypes = [ctypes.c_int, c_i32, ctypes.POINTER(_KVQ8), ctypes.POINTER(_Rope),
+                                              ctypes.POINTER(_Prefill), c_f, c_vp, c_sz, c_vp]
+        L.minipic_attn_decode_weights_workspace_size.restype = c_sz
+        L.minipic_attn_decode_weights_workspace_size.argtypes = [c_i32] * 6
+        L.minipic_attn_decode_weights.restype = ctypes.c_int
+        L.minipic_attn_decode_weights.argtypes = [ctypes.c_int, c_i32, ctypes.POINTER(_KV), ctypes.POINTER(_Rope),
+                                                  ctypes.POINTER(_Decode), c_f, c_vp, c_vp, c_sz, c_vp]
+        L.minipic_kv_evict.restype = ctypes.c_int
+        L.minipic_kv_evict.argtypes = [ctypes.c_int, ctypes.POINTER(_Evict), c_vp]
         L.minipic_device_error.restype = ctypes.c_int
         L.minipic_device_error.argtypes = [ctypes.POINTER(c_i32), c_i32, c_vp]
         L.minipic_block_hashes.restype = ctypes.c_int
@@ -543,6 +586,259 @@ def kv_swap_in(host_k, host_v, block_ids, k_pool, v_pool, stream=None):
             raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of the pool's dtype")
     _check(L.minipic_kv_swap_in(_dtype_code(k_pool), ctypes.byref(kv), block_ids.data_ptr(), n,
                                 host_k.data_ptr(), host_v.data_ptr(), _stream(stream)), "minipic_kv_swap_in")
+
+
+# ---------------------------------------------------------------- 8-bit cache, block weights, eviction
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _current_device(*tensors):
+    """The calls act on the current device: every tensor has to live there."""
+    torch = _torch()
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _on(stream):
+    """Temporaries and outputs of a call on another stream belong to that stream."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _kv_q8(k_pool, v_pool, k_scale, v_scale) -> _KVQ8:
+    torch = _torch()
+    _need(k_pool, "k_pool", dtype=torch.float8_e4m3fn, ndim=4)
+    _need(v_pool, "v_pool", dtype=torch.float8_e4m3fn, ndim=4)
+    _need(k_scale, "k_scale", dtype=torch.float32, ndim=2)
+    _need(v_scale, "v_scale", dtype=torch.float32, ndim=2)
+    _shape(v_pool, "v_pool", k_pool.shape)
+    nb, hkv, bs, d = k_pool.shape
+    _shape(k_scale, "k_scale", (nb, hkv))
+    _shape(v_scale, "v_scale", (nb, hkv))
+    return _KVQ8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, hkv, bs, d)
+
+
+def kv_append_q8(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_pool, k_scale, v_scale,
+                 max_new_len=None, stream=None):
+    """Quantise new unrotated keys and values (float32 or bfloat16) into the
+    e4m3 pools [num_blocks, num_kv_heads, 16, head_dim], in place, with one
+    float32 scale per (block, kv head): the slots of ``kv_append``.  Scales are
+    powers of two; one grows when a new row needs it, and the rows that its
+    block already held are re-rounded to it.  ``max_new_len`` bounds every
+    request's count (read from cu_new_lens if None, which synchronizes)."""
+    torch = _torch()
+    L = load()
+    kv = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    _need(k_new, "k_new", ndim=3)
+    _need(v_new, "v_new", dtype=k_new.dtype, ndim=3)
+    _shape(k_new, "k_new", (k_new.shape[0], kv.num_kv_heads, kv.head_dim))
+    _shape(v_new, "v_new", k_new.shape)
+    for name, t in (("cu_new_lens", cu_new_lens), ("kv_start", kv_start)):
+        _need(t, name, dtype=torch.int32, ndim=1)
+    _need(block_tables, "block_tables", dtype=torch.int32, ndim=2)
+    B = kv_start.shape[0]
+    if cu_new_lens.shape[0] != B + 1 or block_tables.shape[0] != B:
+        raise ValueError("cu_new_lens must have batch + 1 entries and block_tables batch rows")
+    _current_device(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_pool, k_scale, v_scale)
+    if max_new_len is None:
+        max_new_len = int((cu_new_lens[1:] - cu_new_lens[:-1]).max().item()) if B else 0
+    ab = _Append(k_new.data_ptr(), v_new.data_ptr(), cu_new_lens.data_ptr(), kv_start.data_ptr(),
+                 block_tables.data_ptr(), B, k_new.shape[0], int(max_new_len), block_tables.shape[1])
+    _check(L.minipic_kv_append_q8(_dtype_code(k_new), ctypes.byref(kv), ctypes.byref(ab), _stream(stream)),
+           "minipic_kv_append_q8")
+
+
+def attn_decode_q8_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                  max_blocks_per_seq: int, block_size: int = 16) -> int:
+    return int(load().minipic_attn_decode_q8_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
+                                                            max_blocks_per_seq, block_size))
+
+
+def attn_decode_weights_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                       max_blocks_per_seq: int, block_size: int = 16) -> int:
+    return int(load().minipic_attn_decode_weights_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
+                                                                 max_blocks_per_seq, block_size))
+
+
+def _decode_weights(fn, where, size, q, kv, pools, block_tables, block_starts, seq_lens, q_pos, rope, scale, out,
+                    lse, block_weights, workspace, stream, need_f16, need_bf16):
+    torch = _torch()
+    B, Hq, d = q.shape
+    mb = block_tables.shape[1] if block_tables.dim() == 2 else -1
+    for name, t in (("block_tables", block_tables), ("block_starts", block_starts)):
+        _need(t, name, dtype=torch.int32, ndim=2)
+        _shape(t, name, (B, mb))
+    for name, t in (("seq_lens", seq_lens), ("q_pos", q_pos)):
+        _need(t, name, dtype=torch.int32, ndim=1)
+        _shape(t, name, (B,))
+    if d != kv.head_dim:
+        raise ValueError("q and the pools differ in head_dim")
+    if block_weights is not None:
+        _need(block_weights, "block_weights", dtype=q.dtype, ndim=3)
+        _shape(block_weights, "block_weights", (B, kv.num_kv_heads, mb))
+    if lse is not None:
+        _need(lse, "lse", dtype=torch.float32)
+        _shape(lse, "lse", (B, Hq))
+    rp = _rope_struct(rope, need_f16, need_bf16=need_bf16)
+    if out is not None:
+        _need(out, "out", dtype=q.dtype)
+        _shape(out, "out", q.shape)
+    if workspace is not None:
+        _need(workspace, "workspace")
+    cs = rope.cos_sin if isinstance(rope, RopeTable) else rope
+    _current_device(q, *pools, block_tables, block_starts, seq_lens, q_pos, cs, out, lse, block_weights, workspace)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            n = size(B, Hq, kv.num_kv_heads, d, mb, kv.block_size)
+            workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
+        db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
+                     q_pos.data_ptr(), B, mb, out.data_ptr(), _ptr(lse))
+        _check(fn(_dtype_code(q), Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), float(scale),
+                  _ptr(block_weights), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                  _stream(stream)), where)
+    return out, lse
+
+
+def attn_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, seq_lens, q_pos, rope,
+                   scale: float = 0.0, out=None, lse=None, block_weights=None, workspace=None, stream=None):
+    """One decode token per request over the e4m3 cache (pools and scales as
+    ``kv_append_q8`` writes them); q and out float32 or bfloat16.
+
+    ``block_weights`` (q's dtype, [B, num_kv_heads, max_blocks]) receives the
+    softmax weight of each block's keys, summed over the query heads of the kv
+    head; entries past a request's length are left as they were.  Returns
+    (out, lse) like ``attn_decode``.  A workspace passed in must have been
+    zeroed once."""
+    torch = _torch()
+    L = load()
+    _need(q, "q", ndim=3)
+    kv = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    bf16 = q.dtype == torch.bfloat16
+    return _decode_weights(L.minipic_attn_decode_q8, "minipic_attn_decode_q8", attn_decode_q8_workspace_size, q, kv,
+                           (k_pool, v_pool, k_scale, v_scale), block_tables, block_starts, seq_lens, q_pos, rope,
+                           scale, out, lse, block_weights, workspace, stream, bf16, False)
+
+
+def attn_decode_weights(q, k_pool, v_pool, block_tables, block_starts, seq_lens, q_pos, rope, block_weights,
+                        scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
+    """``attn_decode`` that also writes ``block_weights`` (as in
+    ``attn_decode_q8``), for eviction by attention weight."""
+    torch = _torch()
+    L = load()
+    _need(q, "q", ndim=3)
+    kv = _kv(k_pool, v_pool)
+    if k_pool.dtype != q.dtype:
+        raise TypeError("q and the pools must share a dtype")
+    _need(block_weights, "block_weights")
+    return _decode_weights(L.minipic_attn_decode_weights, "minipic_attn_decode_weights",
+                           attn_decode_weights_workspace_size, q, kv, (k_pool, v_pool), block_tables, block_starts,
+                           seq_lens, q_pos, rope, scale, out, lse, block_weights, workspace, stream, False,
+                           q.dtype == torch.bfloat16)
+
+
+def attn_prefill_q8_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_q_len: int,
+                                   max_blocks_per_seq: int, block_size: int = 16) -> int:
+    return int(load().minipic_attn_prefill_q8_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, max_q_len,
+                                                             max_blocks_per_seq, block_size))
+
+
+def attn_prefill_q8(q, cu_q_lens, q_pos, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, kv_lens,
+                    rope, max_q_len: int, scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
+    """Chunked prefill (bf16) over the e4m3 cache; the chunk's own keys are in
+    the cache already (``kv_append_q8``).  Returns (out, lse) like
+    ``attn_prefill``."""
+    torch = _torch()
+    L = load()
+    _need(q, "q", dtype=torch.bfloat16, ndim=3)
+    kv = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    total_q, Hq, d = q.shape
+    for name, t in (("block_tables", block_tables), ("block_starts", block_starts)):
+        _need(t, name, dtype=torch.int32, ndim=2)
+    for name, t in (("cu_q_lens", cu_q_lens), ("q_pos", q_pos), ("kv_lens", kv_lens)):
+        _need(t, name, dtype=torch.int32, ndim=1)
+    B, mb = kv_lens.shape[0], block_tables.shape[1]
+    _shape(cu_q_lens, "cu_q_lens", (B + 1,))
+    _shape(q_pos, "q_pos", (total_q,))
+    _shape(block_tables, "block_tables", (B, mb))
+    _shape(block_starts, "block_starts", (B, mb))
+    if d != kv.head_dim:
+        raise ValueError("q and the pools differ in head_dim")
+    if lse is not None:
+        _need(lse, "lse", dtype=torch.float32)
+        _shape(lse, "lse", (total_q, Hq))
+    if out is not None:
+        _need(out, "out", dtype=q.dtype)
+        _shape(out, "out", q.shape)
+    if workspace is not None:
+        _need(workspace, "workspace")
+    rp = _rope_struct(rope, True)
+    _current_device(q, cu_q_lens, q_pos, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, kv_lens,
+                    rope.cos_sin, out, lse, workspace)
+    with _on(stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            n = attn_prefill_q8_workspace_size(B, Hq, kv.num_kv_heads, d, max_q_len, mb, kv.block_size)
+            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        pb = _Prefill(q.data_ptr(), cu_q_lens.data_ptr(), q_pos.data_ptr(), block_tables.data_ptr(),
+                      block_starts.data_ptr(), kv_lens.data_ptr(), B, total_q, int(max_q_len), mb, out.data_ptr(),
+                      _ptr(lse))
+        _check(L.minipic_attn_prefill_q8(_dtype_code(q), Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(pb),
+                                         float(scale), workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)),
+               "minipic_attn_prefill_q8")
+    return out, lse
+
+
+class KVEvicted(NamedTuple):
+    """What ``kv_evict`` returns."""
+    scores: object
+    block_tables: object
+    block_starts: object
+    seq_lens: object
+    evicted: object
+    n_evicted: object
+
+
+def kv_evict(scores, block_tables, block_starts, seq_lens, budget: int, keep_first: int = 1, keep_last: int = 1,
+             block_weights=None, decay: float = 1.0, inplace: bool = False, stream=None) -> KVEvicted:
+    """One eviction step over the tables of a batch: scores (float32 [B,
+    max_blocks]) become decay * scores + block_weights summed over kv heads, and
+    a request with more than ``budget`` blocks keeps its first ``keep_first``
+    and last ``keep_last`` blocks and the best others by score.  Kept blocks
+    stay in order and keep their logical starts.  ``evicted`` lists the physical
+    ids that left (``n_evicted`` of them, then -1); whether they are free is for
+    the caller's block accounting.  With ``inplace`` the scores, tables, starts
+    and lengths are overwritten and returned."""
+    torch = _torch()
+    L = load()
+    _need(scores, "scores", dtype=torch.float32, ndim=2)
+    B, mb = scores.shape
+    for name, t in (("block_tables", block_tables), ("block_starts", block_starts)):
+        _need(t, name, dtype=torch.int32, ndim=2)
+        _shape(t, name, (B, mb))
+    _need(seq_lens, "seq_lens", dtype=torch.int32, ndim=1)
+    _shape(seq_lens, "seq_lens", (B,))
+    hkv, code = 0, F32
+    if block_weights is not None:
+        _need(block_weights, "block_weights", ndim=3)
+        hkv, code = block_weights.shape[1], _dtype_code(block_weights)
+        _shape(block_weights, "block_weights", (B, hkv, mb))
+    _current_device(scores, block_tables, block_starts, seq_lens, block_weights)
+    src = (scores, block_tables, block_starts, seq_lens)
+    with _on(stream):
+        dst = src if inplace else tuple(torch.empty_like(t) for t in src)
+        r = KVEvicted(*dst, torch.empty_like(block_tables), torch.empty_like(seq_lens))
+        eb = _Evict(_ptr(block_weights), *(t.data_ptr() for t in src), *(t.data_ptr() for t in r), B, mb, hkv,
+                    int(budget), int(keep_first), int(keep_last), float(decay))
+        _check(L.minipic_kv_evict(code, ctypes.byref(eb), _stream(stream)), "minipic_kv_evict")
+    return r
 
 
 # ---------------------------------------------------------------- span reuse (host)

@@ -77,11 +77,10 @@ minipic_status check_rope(const minipic_rope* rope, int head_dim) {
   return MINIPIC_OK;
 }
 
-// Validate a decode batch and fill the launch arguments (no launch).
-minipic_status build_decode(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
-                            const minipic_rope* rope, const minipic_decode_batch* b, float scale, void* workspace,
-                            size_t workspace_bytes, bool rotate, DecodeArgs* out_args, DecodePlan* out_plan,
-                            bool* empty) {
+// Validate a decode batch (no device work).
+minipic_status check_decode(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                            const minipic_rope* rope, const minipic_decode_batch* b, float scale, bool rotate,
+                            bool bf16_table, bool* empty) {
   *empty = false;
   if (dtype != MINIPIC_F32 && dtype != MINIPIC_BF16) return MINIPIC_ERR_INVALID;
   if (!b) return MINIPIC_ERR_INVALID;
@@ -92,7 +91,7 @@ minipic_status build_decode(minipic_dtype dtype, int32_t num_q_heads, const mini
     st = check_rope(rope, kv->head_dim);
     if (st != MINIPIC_OK) return st;
     // the tensor-core path reads the bf16 cos | sin | -sin rows
-    if (dtype == MINIPIC_BF16 && (!rope->cos_sin_bf16 || !aligned16(rope->cos_sin_bf16))) return MINIPIC_ERR_INVALID;
+    if (bf16_table && (!rope->cos_sin_bf16 || !aligned16(rope->cos_sin_bf16))) return MINIPIC_ERR_INVALID;
   }
   if (b->batch == 0) {
     *empty = true;
@@ -105,19 +104,12 @@ minipic_status build_decode(minipic_dtype dtype, int32_t num_q_heads, const mini
       !aligned16(b->block_starts))
     return MINIPIC_ERR_INVALID;
   if (!isfinite(scale)) return MINIPIC_ERR_INVALID;
+  return MINIPIC_OK;
+}
 
-  int* err = nullptr;
-  int sms = 0;
-  if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
-  const bool bf16 = dtype == MINIPIC_BF16;
-  const int G = num_q_heads / kv->num_kv_heads;
-  DecodePlan plan = plan_decode(b->batch, kv->num_kv_heads, G, kv->head_dim, b->max_blocks_per_seq,
-                                kv->block_size, bf16, sms);
-  DecodeWs ws = decode_ws(b->batch, num_q_heads, kv->num_kv_heads, kv->head_dim, plan.n_split);
-  if (ws.total > 0) {
-    if (!workspace || workspace_bytes < ws.total || !aligned16(workspace)) return MINIPIC_ERR_WORKSPACE;
-  }
-
+// Launch arguments of a validated decode batch, without its workspace.
+DecodeArgs decode_args(bool bf16, int32_t num_q_heads, const minipic_kv_pool* kv, const minipic_rope* rope,
+                       const minipic_decode_batch* b, float scale, const DecodePlan& plan, int* err) {
   DecodeArgs a{};
   a.q = b->q;
   a.k_pool = kv->k_pool;
@@ -126,19 +118,15 @@ minipic_status build_decode(minipic_dtype dtype, int32_t num_q_heads, const mini
   a.block_starts = b->block_starts;
   a.seq_lens = b->seq_lens;
   a.q_pos = b->q_pos;
-  a.cos_sin = rotate ? rope->cos_sin : nullptr;
-  a.cs_bf16 = rotate && bf16 ? rope->cos_sin_bf16 : nullptr;
-  a.max_pos = rotate ? rope->max_pos : 0;
+  a.cos_sin = rope ? rope->cos_sin : nullptr;
+  a.cs_bf16 = rope && bf16 ? rope->cos_sin_bf16 : nullptr;
+  a.max_pos = rope ? rope->max_pos : 0;
   a.out = b->out;
   a.lse = b->lse;
-  char* wsb = static_cast<char*>(workspace);
-  a.counters = ws.total ? reinterpret_cast<int*>(wsb) : nullptr;
-  a.part_o = ws.total ? reinterpret_cast<float*>(wsb + ws.cnt_bytes) : nullptr;
-  a.part_ml = ws.total ? reinterpret_cast<float*>(wsb + ws.cnt_bytes + ws.o_bytes) : nullptr;
   a.batch = b->batch;
   a.Hq = num_q_heads;
   a.Hkv = kv->num_kv_heads;
-  a.G = G;
+  a.G = num_q_heads / kv->num_kv_heads;
   a.D = kv->head_dim;
   a.BS = kv->block_size;
   a.num_blocks = kv->num_blocks;
@@ -148,8 +136,65 @@ minipic_status build_decode(minipic_dtype dtype, int32_t num_q_heads, const mini
   a.ctas_per_sm = plan.ctas_per_sm;
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)kv->head_dim);
   a.err = err;
+  return a;
+}
+
+// Validate a decode batch and fill the launch arguments (no launch).
+minipic_status build_decode(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                            const minipic_rope* rope, const minipic_decode_batch* b, float scale, void* workspace,
+                            size_t workspace_bytes, bool rotate, DecodeArgs* out_args, DecodePlan* out_plan,
+                            bool* empty) {
+  const bool bf16 = dtype == MINIPIC_BF16;
+  minipic_status st = check_decode(dtype, num_q_heads, kv, rope, b, scale, rotate, bf16, empty);
+  if (st != MINIPIC_OK || *empty) return st;
+
+  int* err = nullptr;
+  int sms = 0;
+  if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  const int G = num_q_heads / kv->num_kv_heads;
+  DecodePlan plan = plan_decode(b->batch, kv->num_kv_heads, G, kv->head_dim, b->max_blocks_per_seq,
+                                kv->block_size, bf16, sms);
+  DecodeWs ws = decode_ws(b->batch, num_q_heads, kv->num_kv_heads, kv->head_dim, plan.n_split);
+  if (ws.total > 0) {
+    if (!workspace || workspace_bytes < ws.total || !aligned16(workspace)) return MINIPIC_ERR_WORKSPACE;
+  }
+
+  DecodeArgs a = decode_args(bf16, num_q_heads, kv, rotate ? rope : nullptr, b, scale, plan, err);
+  char* wsb = static_cast<char*>(workspace);
+  a.counters = ws.total ? reinterpret_cast<int*>(wsb) : nullptr;
+  a.part_o = ws.total ? reinterpret_cast<float*>(wsb + ws.cnt_bytes) : nullptr;
+  a.part_ml = ws.total ? reinterpret_cast<float*>(wsb + ws.cnt_bytes + ws.o_bytes) : nullptr;
   *out_args = a;
   *out_plan = plan;
+  return MINIPIC_OK;
+}
+
+// Place the workspace of an e4m3 or block-weight decode.
+minipic_status place_weights_ws(DecodeArgs& a, void* block_weights, void* workspace, size_t workspace_bytes) {
+  const DecodeWsW w = decode_ws_weights(a.batch, a.Hq, a.Hkv, a.D, a.n_split, block_weights ? a.max_blocks : 0);
+  if (w.total > 0 && (!workspace || workspace_bytes < w.total || !aligned16(workspace))) return MINIPIC_ERR_WORKSPACE;
+  char* p = static_cast<char*>(workspace);
+  if (a.n_split > 1) {
+    a.counters = reinterpret_cast<int*>(p);
+    a.part_o = reinterpret_cast<float*>(p + w.cnt_bytes);
+    a.part_ml = reinterpret_cast<float*>(p + w.cnt_bytes + w.o_bytes);
+  }
+  if (block_weights) {
+    a.weights = block_weights;
+    a.w_lse = reinterpret_cast<float*>(p + w.cnt_bytes + w.o_bytes + w.ml_bytes);
+    a.w_raw = reinterpret_cast<float*>(p + w.cnt_bytes + w.o_bytes + w.ml_bytes + w.lse_bytes);
+  }
+  return MINIPIC_OK;
+}
+
+minipic_status check_pool_q8(const minipic_kv_pool_q8* kv, int32_t num_q_heads, bool need_ptrs, minipic_kv_pool* as) {
+  if (!kv) return MINIPIC_ERR_INVALID;
+  *as = minipic_kv_pool{kv->k_pool, kv->v_pool, kv->num_blocks, kv->num_kv_heads, kv->block_size, kv->head_dim};
+  const minipic_status st = check_pool(as, num_q_heads, need_ptrs);
+  if (st != MINIPIC_OK) return st;
+  if (need_ptrs && kv->num_blocks > 0 && (!kv->k_scale || !kv->v_scale)) return MINIPIC_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(kv->k_scale) & 3u || reinterpret_cast<uintptr_t>(kv->v_scale) & 3u)
+    return MINIPIC_ERR_INVALID;
   return MINIPIC_OK;
 }
 
@@ -278,6 +323,23 @@ DecodeWs decode_ws_layout(int batch, int Hq, int Hkv, int D, int n_split) {
   return w;
 }
 
+DecodeWsW decode_ws_weights(int batch, int Hq, int Hkv, int D, int n_split, int max_blocks) {
+  DecodeWsW w{0, 0, 0, 0, 0, 0};
+  if (n_split > 1) {
+    const size_t cnt = align_up((size_t)batch * Hkv * sizeof(int), 256);
+    w.cnt_bytes = cnt > kCounterRegion ? cnt : kCounterRegion;
+    w.o_bytes = align_up((size_t)batch * Hq * n_split * D * sizeof(float), 256);
+    w.ml_bytes = align_up((size_t)batch * Hq * n_split * 2 * sizeof(float), 256);
+  }
+  if (max_blocks > 0) {
+    w.cnt_bytes = w.cnt_bytes ? w.cnt_bytes : kCounterRegion;  // kept zero for calls that split
+    w.lse_bytes = align_up((size_t)batch * Hq * sizeof(float), 256);
+    w.raw_bytes = align_up((size_t)batch * Hq * max_blocks * sizeof(float), 256);
+  }
+  w.total = w.cnt_bytes + w.o_bytes + w.ml_bytes + w.lse_bytes + w.raw_bytes;
+  return w;
+}
+
 DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs, bool bf16, int num_sms) {
   (void)D;
   (void)bs;
@@ -318,6 +380,11 @@ DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs,
   p.split_blocks = (int)((max_blocks + n - 1) / n);
   p.n_split = (max_blocks + p.split_blocks - 1) / p.split_blocks;
   return p;
+}
+
+DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms) {
+  (void)bf16;
+  return plan_decode(batch, Hkv, G, D, max_blocks, 16, false, num_sms);
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan,
@@ -574,6 +641,238 @@ minipic_status minipic_device_error(int32_t* flags_out, int32_t clear, minipic_s
   }
   if (flags_out) *flags_out = v;
   return v ? MINIPIC_ERR_DEVICE_CHECK : MINIPIC_OK;
+}
+
+/* ---------------------------------------------------------------- block weights, 8-bit cache, eviction */
+
+namespace {
+
+constexpr int kMaxGridYZ = 65535;
+
+size_t weights_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t mb, int32_t bs, bool q8) {
+  if (batch <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || mb <= 0 || bs <= 0 || Hq % Hkv) return 0;
+  const int sms = current_sms();
+  size_t most = 0;
+  for (int bf16 = 0; bf16 < 2; ++bf16) {
+    const DecodePlan p = q8 ? plan_decode_q8(batch, Hkv, Hq / Hkv, D, mb, bf16 != 0, sms)
+                            : plan_decode(batch, Hkv, Hq / Hkv, D, mb, bs, false, sms);
+    const size_t n = decode_ws_weights(batch, Hq, Hkv, D, p.n_split, mb).total;
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+}  // namespace
+
+size_t minipic_attn_decode_weights_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                  int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size) {
+  return weights_ws_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, false);
+}
+
+minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                                           const minipic_rope* rope, const minipic_decode_batch* b, float scale,
+                                           void* block_weights, void* workspace, size_t workspace_bytes,
+                                           minipic_stream_t stream) {
+  const bool bf16 = dtype == MINIPIC_BF16;
+  bool empty = false;
+  minipic_status st = check_decode(dtype, num_q_heads, kv, rope, b, scale, true, bf16, &empty);
+  if (st != MINIPIC_OK || empty) return st;
+  if (!block_weights || !aligned16(block_weights)) return MINIPIC_ERR_INVALID;
+  if (b->batch > kMaxGridYZ || kv->num_kv_heads > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
+  int* err = nullptr;
+  int sms = 0;
+  if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  const DecodePlan plan = plan_decode(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
+                                      b->max_blocks_per_seq, kv->block_size, false, sms);
+  DecodeArgs a = decode_args(bf16, num_q_heads, kv, rope, b, scale, plan, err);
+  st = place_weights_ws(a, block_weights, workspace, workspace_bytes);
+  if (st != MINIPIC_OK) return st;
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = launch_decode_simt_weights(a, bf16, s);
+  if (e == cudaSuccess) e = launch_decode_merge(a, bf16, s);
+  if (e == cudaSuccess) e = launch_block_weights(a, bf16, s);
+  return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+}
+
+size_t minipic_attn_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                             int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size) {
+  return weights_ws_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, true);
+}
+
+minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
+                                      const minipic_rope* rope, const minipic_decode_batch* b, float scale,
+                                      void* block_weights, void* workspace, size_t workspace_bytes,
+                                      minipic_stream_t stream) {
+  const bool bf16 = dtype == MINIPIC_BF16;
+  bool empty = false;
+  if (!b) return MINIPIC_ERR_INVALID;
+  minipic_kv_pool pool{};
+  minipic_status st = check_pool_q8(kv, num_q_heads, b->batch > 0, &pool);
+  if (st != MINIPIC_OK) return st;
+  st = check_decode(dtype, num_q_heads, &pool, rope, b, scale, true, false, &empty);
+  if (st != MINIPIC_OK) return st;
+  // the tensor-core path rotates the query with the fp16 rows
+  if (bf16 && (!rope->cos_sin_f16 || !aligned16(rope->cos_sin_f16))) return MINIPIC_ERR_INVALID;
+  if (empty) return MINIPIC_OK;
+  if (!aligned16(block_weights)) return MINIPIC_ERR_INVALID;
+  if (b->batch > kMaxGridYZ || kv->num_kv_heads > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
+  int* err = nullptr;
+  int sms = 0;
+  if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  const DecodePlan plan = plan_decode_q8(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
+                                         b->max_blocks_per_seq, bf16, sms);
+  DecodeArgs a = decode_args(bf16, num_q_heads, &pool, rope, b, scale, plan, err);
+  a.k_scale = kv->k_scale;
+  a.v_scale = kv->v_scale;
+  st = place_weights_ws(a, block_weights, workspace, workspace_bytes);
+  if (st != MINIPIC_OK) return st;
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = launch_decode_simt_q8(a, bf16, s);
+  if (e == cudaSuccess) e = launch_decode_merge(a, bf16, s);
+  if (e == cudaSuccess && block_weights) e = launch_block_weights(a, bf16, s);
+  return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+}
+
+namespace {
+
+struct RestoreWs {
+  size_t pool_bytes, table_bytes, total;
+};
+RestoreWs restore_ws(int32_t batch, int32_t Hkv, int32_t D, int32_t mb) {
+  RestoreWs w{};
+  w.pool_bytes = align_up((size_t)batch * mb * Hkv * 16 * D * 2, 1024);
+  w.table_bytes = align_up((size_t)batch * mb * sizeof(int32_t), 256);
+  w.total = 2 * w.pool_bytes + w.table_bytes;
+  return w;
+}
+
+}  // namespace
+
+size_t minipic_attn_prefill_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t head_dim, int32_t max_q_len, int32_t max_blocks_per_seq,
+                                              int32_t block_size) {
+  (void)num_q_heads;
+  if (batch <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_q_len <= 0 || max_blocks_per_seq <= 0 ||
+      block_size <= 0)
+    return 0;
+  return restore_ws(batch, num_kv_heads, head_dim, max_blocks_per_seq).total;
+}
+
+minipic_status minipic_attn_prefill_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
+                                       const minipic_rope* rope, const minipic_prefill_batch* b, float scale,
+                                       void* workspace, size_t workspace_bytes, minipic_stream_t stream) {
+  if (!b) return MINIPIC_ERR_INVALID;
+  minipic_kv_pool pool{};
+  minipic_status st = check_pool_q8(kv, num_q_heads, b->batch > 0, &pool);
+  if (st != MINIPIC_OK) return st;
+  PrefillArgs p{};
+  bool empty = false;
+  st = build_prefill(dtype, num_q_heads, &pool, rope, b, scale, true, &p, &empty);
+  if (st != MINIPIC_OK || empty) return st;
+  const long long scratch_blocks = (long long)b->batch * b->max_blocks_per_seq;
+  if (b->batch > kMaxGridYZ || kv->num_kv_heads > kMaxGridYZ ||
+      scratch_blocks * kv->num_kv_heads * 16 > 0x7fffffffLL)  // TMA row coordinates are 32-bit
+    return MINIPIC_ERR_UNSUPPORTED;
+  const RestoreWs w = restore_ws(b->batch, kv->num_kv_heads, kv->head_dim, b->max_blocks_per_seq);
+  if (!workspace || workspace_bytes < w.total || !aligned16(workspace)) return MINIPIC_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  RestoreArgs ra{};
+  ra.k_pool = static_cast<const uint8_t*>(kv->k_pool);
+  ra.v_pool = static_cast<const uint8_t*>(kv->v_pool);
+  ra.k_scale = kv->k_scale;
+  ra.v_scale = kv->v_scale;
+  ra.block_tables = b->block_tables;
+  ra.kv_lens = b->kv_lens;
+  ra.k_out = reinterpret_cast<uint16_t*>(ws);
+  ra.v_out = reinterpret_cast<uint16_t*>(ws + w.pool_bytes);
+  ra.table_out = reinterpret_cast<int32_t*>(ws + 2 * w.pool_bytes);
+  ra.batch = b->batch;
+  ra.max_blocks = b->max_blocks_per_seq;
+  ra.num_blocks = kv->num_blocks;
+  ra.Hkv = kv->num_kv_heads;
+  ra.D = kv->head_dim;
+  p.k_pool = ra.k_out;
+  p.v_pool = ra.v_out;
+  p.block_tables = ra.table_out;
+  p.num_blocks = (int)scratch_blocks;
+  cudaError_t e = launch_kv_restore_q8(ra, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_prefill_tc(p, true, (cudaStream_t)stream);
+  return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+}
+
+minipic_status minipic_kv_append_q8(minipic_dtype dtype, const minipic_kv_pool_q8_mut* kv,
+                                    const minipic_kv_append_batch* b, minipic_stream_t stream) {
+  if (dtype != MINIPIC_F32 && dtype != MINIPIC_BF16) return MINIPIC_ERR_INVALID;
+  if (!kv || !b) return MINIPIC_ERR_INVALID;
+  if (kv->num_blocks < 0 || kv->num_kv_heads <= 0 || kv->block_size <= 0 || kv->head_dim <= 0)
+    return MINIPIC_ERR_INVALID;
+  if (b->batch < 0 || b->total_new < 0 || b->max_new_len < 0 || b->max_blocks_per_seq < 0)
+    return MINIPIC_ERR_INVALID;
+  if (kv->head_dim != 64 && kv->head_dim != 128) return MINIPIC_ERR_UNSUPPORTED;
+  if (kv->block_size != 16) return MINIPIC_ERR_UNSUPPORTED;
+  if (b->batch == 0 || b->total_new == 0 || b->max_new_len == 0) return MINIPIC_OK;
+  if (b->batch > kMaxGridYZ || b->max_blocks_per_seq == 0 || kv->num_blocks == 0) return MINIPIC_ERR_INVALID;
+  if (!b->k_new || !b->v_new || !b->cu_new_lens || !b->kv_start || !b->block_tables || !kv->k_pool ||
+      !kv->v_pool || !kv->k_scale || !kv->v_scale)
+    return MINIPIC_ERR_INVALID;
+  if (!aligned16(b->k_new) || !aligned16(b->v_new) || !aligned16(kv->k_pool) || !aligned16(kv->v_pool) ||
+      reinterpret_cast<uintptr_t>(kv->k_scale) & 3u || reinterpret_cast<uintptr_t>(kv->v_scale) & 3u)
+    return MINIPIC_ERR_INVALID;
+  AppendQ8Args a{};
+  if (device_info(&a.err, nullptr) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  a.k_new = b->k_new;
+  a.v_new = b->v_new;
+  a.cu_new = b->cu_new_lens;
+  a.kv_start = b->kv_start;
+  a.block_tables = b->block_tables;
+  a.k_pool = static_cast<uint8_t*>(kv->k_pool);
+  a.v_pool = static_cast<uint8_t*>(kv->v_pool);
+  a.k_scale = kv->k_scale;
+  a.v_scale = kv->v_scale;
+  a.batch = b->batch;
+  a.max_new = b->max_new_len;
+  a.total_new = b->total_new;
+  a.max_blocks = b->max_blocks_per_seq;
+  a.num_blocks = kv->num_blocks;
+  a.Hkv = kv->num_kv_heads;
+  a.D = kv->head_dim;
+  const cudaError_t e = launch_kv_append_q8(a, dtype == MINIPIC_BF16, (cudaStream_t)stream);
+  return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+}
+
+minipic_status minipic_kv_evict(minipic_dtype dtype, const minipic_kv_evict_batch* b, minipic_stream_t stream) {
+  if (dtype != MINIPIC_F32 && dtype != MINIPIC_BF16) return MINIPIC_ERR_INVALID;
+  if (!b) return MINIPIC_ERR_INVALID;
+  if (b->batch < 0 || b->max_blocks_per_seq < 0 || b->budget < 0 || b->keep_first < 0 || b->keep_last < 1 ||
+      (long long)b->keep_first + b->keep_last > b->budget || !isfinite(b->decay) || b->decay < 0.f)
+    return MINIPIC_ERR_INVALID;
+  if (b->block_weights && b->num_kv_heads <= 0) return MINIPIC_ERR_INVALID;
+  if (b->batch == 0) return MINIPIC_OK;
+  if (!b->scores || !b->block_tables || !b->block_starts || !b->seq_lens || !b->scores_out || !b->block_tables_out ||
+      !b->block_starts_out || !b->seq_lens_out || !b->evicted || !b->n_evicted)
+    return MINIPIC_ERR_INVALID;
+  EvictArgs a{};
+  if (device_info(&a.err, nullptr) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  a.weights = b->block_weights;
+  a.scores = b->scores;
+  a.block_tables = b->block_tables;
+  a.block_starts = b->block_starts;
+  a.seq_lens = b->seq_lens;
+  a.scores_out = b->scores_out;
+  a.tables_out = b->block_tables_out;
+  a.starts_out = b->block_starts_out;
+  a.lens_out = b->seq_lens_out;
+  a.evicted = b->evicted;
+  a.n_evicted = b->n_evicted;
+  a.batch = b->batch;
+  a.max_blocks = b->max_blocks_per_seq;
+  a.Hkv = b->num_kv_heads;
+  a.budget = b->budget;
+  a.keep_first = b->keep_first;
+  a.keep_last = b->keep_last;
+  a.decay = b->decay;
+  const cudaError_t e = launch_kv_evict(a, dtype == MINIPIC_BF16, (cudaStream_t)stream);
+  return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }
 
 }  // extern "C"

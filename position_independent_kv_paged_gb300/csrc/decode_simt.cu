@@ -9,7 +9,13 @@
 // key is rotated with two multiply-adds per element from the cos/sin table
 // row of its logical position (MiniPIC summary section 2.1: pi(j) =
 // start of the key's block in this request + slot).
+//
+// The cache is of the query's dtype, or e4m3 with one scale per (block, kv
+// head): a value is the byte's value times the block's scale, in fp32.  With
+// WTS the kernel also records, per (request, query head, block), log2 of the
+// block's sum of exp2(score) for block_weights.cu.
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 #include <math_constants.h>
 
 #include "internal.h"
@@ -28,6 +34,12 @@ template <>
 __device__ __forceinline__ float ld_f<__nv_bfloat16>(const __nv_bfloat16* p) {
   return __bfloat162float(__ldg(p));
 }
+template <>
+__device__ __forceinline__ float ld_f<__nv_fp8_e4m3>(const __nv_fp8_e4m3* p) {
+  __nv_fp8_e4m3 x;
+  x.__x = __ldg(reinterpret_cast<const unsigned char*>(p));
+  return static_cast<float>(x);
+}
 template <typename T>
 __device__ __forceinline__ void st_f(T* p, float v);
 template <>
@@ -41,8 +53,9 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-template <typename T, int D, int MAXG, bool ROPE>
+template <typename T, typename KV, int D, int MAXG, bool ROPE, bool WTS>
 __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
+  constexpr bool Q8 = sizeof(KV) == 1;
   constexpr int E = D / 32;  // elements per lane
   constexpr int H = E / 2;   // rotary pairs per lane
   constexpr int NW = 4;
@@ -53,8 +66,8 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
   const int s = blockIdx.x, g = blockIdx.y, r = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.G;
-  const T* __restrict__ kpool = static_cast<const T*>(a.k_pool);
-  const T* __restrict__ vpool = static_cast<const T*>(a.v_pool);
+  const KV* __restrict__ kpool = static_cast<const KV*>(a.k_pool);
+  const KV* __restrict__ vpool = static_cast<const KV*>(a.v_pool);
   const T* __restrict__ qg = static_cast<const T*>(a.q);
 
   int L = a.seq_lens[r];
@@ -114,21 +127,34 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
 
   for (int b = b_begin + warp; b < b_end; b += NW) {
     const int phys = a.block_tables[(size_t)r * a.max_blocks + b];
+    float* raw = WTS ? a.w_raw + (((size_t)r * a.Hkv + g) * a.max_blocks + b) * G : nullptr;
     if (phys < 0 || phys >= a.num_blocks) {
       if (lane == 0) atomicOr(a.err, kErrBlockId);
+      if (WTS && lane < G) raw[lane] = -CUDART_INF_F;
       continue;
     }
+    float bsum[MAXG];  // the block's part of l
+    if (WTS) {
+#pragma unroll
+      for (int h = 0; h < MAXG; ++h) bsum[h] = 0.f;
+    }
+    const float ks = Q8 ? __ldg(a.k_scale + (size_t)phys * a.Hkv + g) : 1.f;
+    const float vs = Q8 ? __ldg(a.v_scale + (size_t)phys * a.Hkv + g) : 1.f;
     const int start = ROPE ? a.block_starts[(size_t)r * a.max_blocks + b] : 0;
     const int nk = min(a.BS, L - b * a.BS);
     const size_t tile = ((size_t)phys * a.Hkv + g) * a.BS;
     for (int slot = 0; slot < nk; ++slot) {
-      const T* kp = kpool + (tile + slot) * D;
-      const T* vp = vpool + (tile + slot) * D;
+      const KV* kp = kpool + (tile + slot) * D;
+      const KV* vp = vpool + (tile + slot) * D;
       float k[E], v[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         k[e] = ld_f(kp + lane + 32 * e);
         v[e] = ld_f(vp + lane + 32 * e);
+        if (Q8) {
+          k[e] *= ks;
+          v[e] *= vs;
+        }
       }
       if (ROPE) {
         const int pos = start + slot;
@@ -160,8 +186,14 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
 #pragma unroll
           for (int e = 0; e < E; ++e) o[h][e] = fmaf(o[h][e], corr, p * v[e]);
           m[h] = mn;
+          if (WTS) bsum[h] = fmaf(bsum[h], corr, p);
         }
       }
+    }
+    if (WTS && lane == 0) {
+#pragma unroll
+      for (int h = 0; h < MAXG; ++h)
+        if (h < G) raw[h] = bsum[h] == 0.f ? -CUDART_INF_F : m[h] + log2f(bsum[h]);
     }
   }
 
@@ -192,8 +224,10 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
     const int hq = g * G + h;
     if (direct) {
       T* out = static_cast<T*>(a.out) + ((size_t)r * a.Hq + hq) * D + dim;
-      st_f<T>(out, Ls > 0.f ? O / Ls : 0.f);
-      if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
+      const bool any = Q8 ? Ls != 0.f : Ls > 0.f;  // over e4m3, a NaN sum stays one
+      st_f<T>(out, any ? O / Ls : 0.f);
+      if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = any ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
+      if (WTS && dim == 0) a.w_lse[(size_t)r * a.Hq + hq] = any ? M + log2f(Ls) : -CUDART_INF_F;
     } else {
       const size_t pi = ((size_t)r * a.Hq + hq) * a.n_split + s;
       a.part_o[pi * D + dim] = O;
@@ -227,34 +261,49 @@ __global__ void decode_merge_kernel(DecodeArgs a) {
       O = fmaf(a.part_o[(base + s) * a.D + dim], f, O);
     }
     T* out = static_cast<T*>(a.out) + ((size_t)r * a.Hq + hq) * a.D + dim;
-    st_f<T>(out, Ls > 0.f ? O / Ls : 0.f);
-    if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
+    const bool any = a.k_scale ? Ls != 0.f : Ls > 0.f;  // over e4m3, a NaN sum stays one
+    st_f<T>(out, any ? O / Ls : 0.f);
+    if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = any ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
+    if (dim == 0 && a.w_lse) a.w_lse[(size_t)r * a.Hq + hq] = any ? M + log2f(Ls) : -CUDART_INF_F;
   }
 }
 
-template <typename T, int D, bool ROPE>
+template <typename T, typename KV, int D, bool ROPE, bool WTS>
 cudaError_t dispatch_g(const DecodeArgs& a, cudaStream_t s) {
   dim3 grid(a.n_split, a.Hkv, a.batch);
   if (a.G <= 4)
-    decode_simt_kernel<T, D, 4, ROPE><<<grid, 128, 0, s>>>(a);
+    decode_simt_kernel<T, KV, D, 4, ROPE, WTS><<<grid, 128, 0, s>>>(a);
   else if (a.G <= 8)
-    decode_simt_kernel<T, D, 8, ROPE><<<grid, 128, 0, s>>>(a);
+    decode_simt_kernel<T, KV, D, 8, ROPE, WTS><<<grid, 128, 0, s>>>(a);
   else
-    decode_simt_kernel<T, D, 16, ROPE><<<grid, 128, 0, s>>>(a);
+    decode_simt_kernel<T, KV, D, 16, ROPE, WTS><<<grid, 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, bool ROPE>
+template <typename T, typename KV, bool ROPE, bool WTS = false>
 cudaError_t dispatch_d(const DecodeArgs& a, cudaStream_t s) {
-  return a.D == 64 ? dispatch_g<T, 64, ROPE>(a, s) : dispatch_g<T, 128, ROPE>(a, s);
+  return a.D == 64 ? dispatch_g<T, KV, 64, ROPE, WTS>(a, s) : dispatch_g<T, KV, 128, ROPE, WTS>(a, s);
+}
+
+template <typename T>
+cudaError_t dispatch_q8(const DecodeArgs& a, cudaStream_t s) {
+  return a.weights ? dispatch_d<T, __nv_fp8_e4m3, true, true>(a, s) : dispatch_d<T, __nv_fp8_e4m3, true>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_decode_simt(const DecodeArgs& a, bool bf16, bool rotate, cudaStream_t s) {
-  if (bf16)
-    return rotate ? dispatch_d<__nv_bfloat16, true>(a, s) : dispatch_d<__nv_bfloat16, false>(a, s);
-  return rotate ? dispatch_d<float, true>(a, s) : dispatch_d<float, false>(a, s);
+  using B = __nv_bfloat16;
+  if (bf16) return rotate ? dispatch_d<B, B, true>(a, s) : dispatch_d<B, B, false>(a, s);
+  return rotate ? dispatch_d<float, float, true>(a, s) : dispatch_d<float, float, false>(a, s);
+}
+
+cudaError_t launch_decode_simt_q8(const DecodeArgs& a, bool bf16, cudaStream_t s) {
+  return bf16 ? dispatch_q8<__nv_bfloat16>(a, s) : dispatch_q8<float>(a, s);
+}
+
+cudaError_t launch_decode_simt_weights(const DecodeArgs& a, bool bf16, cudaStream_t s) {
+  return bf16 ? dispatch_d<__nv_bfloat16, __nv_bfloat16, true, true>(a, s) : dispatch_d<float, float, true, true>(a, s);
 }
 
 cudaError_t launch_decode_merge(const DecodeArgs& a, bool bf16, cudaStream_t s) {

@@ -29,6 +29,13 @@ struct DecodeArgs {
   int ctas_per_sm;           // tensor-core decode: 3 (2 stages per warp) or 2 (3 stages) CTAs per SM
   float scale;               // softmax scale (1/sqrt(D) by default)
   int* err;                  // device error word
+  // e4m3 cache: one scale per (block, kv head) of each pool, else null
+  const float* k_scale;      // [num_blocks][Hkv]
+  const float* v_scale;
+  // block weights (null when not asked for)
+  void* weights;             // [B][Hkv][max_blocks] in the dtype of q: sum over the group of each block's softmax weight
+  float* w_raw;              // [B][Hkv][max_blocks][G] log2 of a block's unnormalised sum, per query head
+  float* w_lse;              // [B][Hq] log2 of the softmax denominator
 };
 
 // Arguments of one prefill launch.
@@ -69,11 +76,19 @@ struct DecodePlan {
   int ctas_per_sm;  // tensor-core path: resident CTAs per SM (3 or 2; 1 for more than 8 heads per group)
 };
 DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs, bool bf16, int num_sms);
+// The e4m3 decode's plan.
+DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan, cudaStream_t s);
 cudaError_t launch_decode_simt(const DecodeArgs& a, bool bf16, bool rotate, cudaStream_t s);
 cudaError_t launch_decode_mma(const DecodeArgs& a, bool rotate, cudaStream_t s);
 cudaError_t launch_decode_merge(const DecodeArgs& a, bool bf16, cudaStream_t s);
+// e4m3 cache; q and out f32 or bf16 (exact-precision kernel).
+cudaError_t launch_decode_simt_q8(const DecodeArgs& a, bool bf16, cudaStream_t s);
+// The exact-precision kernel over the f32 or bf16 cache, recording block weights.
+cudaError_t launch_decode_simt_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
+// w_raw and w_lse -> weights.
+cudaError_t launch_block_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, bool rotate, cudaStream_t s);
 // Head dim 128: CTA-pair (cta_group::2) form, called by launch_prefill_tc.
 cudaError_t launch_prefill_pair(const PrefillArgs& a, bool rotate, cudaStream_t s);
@@ -96,6 +111,56 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
+// Quantising append: the same token -> slot mapping into e4m3 pools with scales.
+struct AppendQ8Args {
+  const void* k_new;  // [total_new][Hkv][D] f32 or bf16
+  const void* v_new;
+  const int32_t* cu_new;
+  const int32_t* kv_start;
+  const int32_t* block_tables;
+  uint8_t* k_pool;  // [num_blocks][Hkv][16][D] e4m3
+  uint8_t* v_pool;
+  float* k_scale;   // [num_blocks][Hkv]
+  float* v_scale;
+  int batch, max_new, total_new, max_blocks, num_blocks, Hkv, D;
+  int* err;
+};
+cudaError_t launch_kv_append_q8(const AppendQ8Args& a, bool bf16, cudaStream_t s);
+
+// e4m3 blocks of a prefill batch -> bf16 blocks of a scratch pool in request order.
+struct RestoreArgs {
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_tables;  // [batch][max_blocks]
+  const int32_t* kv_lens;
+  uint16_t* k_out;              // [batch * max_blocks][Hkv][16][D] bf16
+  uint16_t* v_out;
+  int32_t* table_out;           // [batch][max_blocks] ids in the scratch pool (-1: unusable id)
+  int batch, max_blocks, num_blocks, Hkv, D;
+};
+cudaError_t launch_kv_restore_q8(const RestoreArgs& a, cudaStream_t s);
+
+// Eviction of whole blocks by accumulated attention weight.
+struct EvictArgs {
+  const void* weights;  // [batch][Hkv][max_blocks] f32 or bf16, or null
+  const float* scores;  // [batch][max_blocks]
+  const int32_t* block_tables;
+  const int32_t* block_starts;
+  const int32_t* seq_lens;
+  float* scores_out;    // outputs may be the inputs
+  int32_t* tables_out;
+  int32_t* starts_out;
+  int32_t* lens_out;
+  int32_t* evicted;     // [batch][max_blocks]
+  int32_t* n_evicted;   // [batch]
+  int batch, max_blocks, Hkv, budget, keep_first, keep_last;
+  float decay;
+  int* err;
+};
+cudaError_t launch_kv_evict(const EvictArgs& a, bool bf16, cudaStream_t s);
+
 // Whole-block copies between the pools and page-locked host memory.
 struct OffloadArgs {
   void* k_pool;  // [num_blocks][Hkv][16][D]
@@ -115,5 +180,15 @@ struct DecodeWs {
   size_t o_bytes, ml_bytes, cnt_bytes, total;
 };
 DecodeWs decode_ws_layout(int batch, int Hq, int Hkv, int D, int n_split);
+
+// Byte layout of the workspace of the e4m3 and the block-weight decode: the
+// completion counters in a region of their own size whatever the split count
+// (so that calls of other shapes on the same workspace find it zero), then the
+// partials, the denominators and the raw block sums.
+struct DecodeWsW {
+  size_t cnt_bytes, o_bytes, ml_bytes, lse_bytes, raw_bytes, total;
+};
+constexpr size_t kCounterRegion = 65536;
+DecodeWsW decode_ws_weights(int batch, int Hq, int Hkv, int D, int n_split, int max_blocks);
 
 }  // namespace minipic

@@ -223,6 +223,18 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+// ---------------------------------------------------------------- e4m3 (exact in fp16)
+// Two e4m3 bytes (the low 16 bits) -> f16x2, byte 0 in the low half.
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(w));
+  return d;
+}
+__device__ __forceinline__ float2 e4m3x2_to_f2(uint32_t w) {
+  const uint32_t h = e4m3x2_to_h2(w);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // ---------------------------------------------------------------- packed fp32 pairs (sm_100+ f32x2)
 __device__ __forceinline__ uint64_t f2(float lo, float hi) {
   uint64_t d;
