@@ -383,8 +383,19 @@ DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs,
 }
 
 DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms) {
-  (void)bf16;
-  return plan_decode(batch, Hkv, G, D, max_blocks, 16, false, num_sms);
+  if (!bf16) return plan_decode(batch, Hkv, G, D, max_blocks, 16, false, num_sms);
+  DecodePlan p{max_blocks, 1, true, G > 8 ? 2 : 3};
+  const long long resident = (long long)num_sms * p.ctas_per_sm;
+  const long long total = (long long)batch * Hkv * max_blocks;
+  const long long waves = 4;
+  long long est = (total + resident * waves - 1) / (resident * waves);
+  if (est < 32) est = 32;
+  if (est > 512) est = 512;  // the kernel stages a split's block metadata in shared memory
+  if (est >= max_blocks) return p;
+  const long long n = (max_blocks + est - 1) / est;
+  p.split_blocks = (int)((max_blocks + n - 1) / n);
+  p.n_split = (max_blocks + p.split_blocks - 1) / p.split_blocks;
+  return p;
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan,
@@ -716,6 +727,7 @@ minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, 
   if (empty) return MINIPIC_OK;
   if (!aligned16(block_weights)) return MINIPIC_ERR_INVALID;
   if (b->batch > kMaxGridYZ || kv->num_kv_heads > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
+  if ((long long)kv->num_blocks * kv->num_kv_heads * 16 > 0x7fffffffLL) return MINIPIC_ERR_UNSUPPORTED;  // TMA rows
   int* err = nullptr;
   int sms = 0;
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
@@ -727,8 +739,11 @@ minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, 
   st = place_weights_ws(a, block_weights, workspace, workspace_bytes);
   if (st != MINIPIC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = launch_decode_simt_q8(a, bf16, s);
-  if (e == cudaSuccess) e = launch_decode_merge(a, bf16, s);
+  a.cs_f16 = rope->cos_sin_f16;
+  // the tensor-core kernel merges its splits itself; with no pool there is nothing to map and every key is masked
+  const bool mma = plan.use_mma && kv->num_blocks > 0;
+  cudaError_t e = mma ? launch_decode_q8(a, s) : launch_decode_simt_q8(a, bf16, s);
+  if (e == cudaSuccess && !mma) e = launch_decode_merge(a, bf16, s);
   if (e == cudaSuccess && block_weights) e = launch_block_weights(a, bf16, s);
   return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }

@@ -32,6 +32,7 @@ struct DecodeArgs {
   // e4m3 cache: one scale per (block, kv head) of each pool, else null
   const float* k_scale;      // [num_blocks][Hkv]
   const float* v_scale;
+  const uint16_t* cs_f16;    // [max_pos][D] fp16 cos | sin (e4m3 tensor-core path), or null
   // block weights (null when not asked for)
   void* weights;             // [B][Hkv][max_blocks] in the dtype of q: sum over the group of each block's softmax weight
   float* w_raw;              // [B][Hkv][max_blocks][G] log2 of a block's unnormalised sum, per query head
@@ -85,6 +86,8 @@ cudaError_t launch_decode_mma(const DecodeArgs& a, bool rotate, cudaStream_t s);
 cudaError_t launch_decode_merge(const DecodeArgs& a, bool bf16, cudaStream_t s);
 // e4m3 cache; q and out f32 or bf16 (exact-precision kernel).
 cudaError_t launch_decode_simt_q8(const DecodeArgs& a, bool bf16, cudaStream_t s);
+// e4m3 cache, bf16 q and out, tensor cores.
+cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t s);
 // The exact-precision kernel over the f32 or bf16 cache, recording block weights.
 cudaError_t launch_decode_simt_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
 // w_raw and w_lse -> weights.
