@@ -390,7 +390,7 @@ DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool
   const long long waves = 4;
   long long est = (total + resident * waves - 1) / (resident * waves);
   if (est < 32) est = 32;
-  if (est > 512) est = 512;  // the kernel stages a split's block metadata in shared memory
+  if (est > kQ8MaxSplit) est = kQ8MaxSplit;
   if (est >= max_blocks) return p;
   const long long n = (max_blocks + est - 1) / est;
   p.split_blocks = (int)((max_blocks + n - 1) / n);

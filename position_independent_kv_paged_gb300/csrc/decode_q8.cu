@@ -6,7 +6,7 @@
 // gist.science 2606.13126, section 2.1).
 //
 // Work: one CTA = (split, kv head, request); each of its warps owns every NW-th
-// 16-key block of the split and runs its own TMA ring.  A (block, head) tile is
+// 16-key block of the split, two at a time, and runs its own TMA ring.  A (block, head) tile is
 // 16 d contiguous bytes; the tensor map sees the pool as lines of 128 bytes (one
 // key at d 128, two at d 64) and swizzles them, so that the key-row reads and
 // the transposing reads of V are free of bank conflicts.  The fp16 cos | sin row
@@ -46,7 +46,7 @@ namespace {
 using ptx::U4;
 
 constexpr int kWarps = 4;
-constexpr int kMaxSplit = 512;                // split_blocks cap (planner)
+constexpr int kMaxSplit = kQ8MaxSplit;        // split_blocks cap (planner)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;               // a reference moves when exceeded by 2^8
@@ -57,13 +57,14 @@ template <int D, int NS>
 struct Lay {
   static constexpr int TILE = 16 * D;              // bytes of one (block, head) tile of K or V
   static constexpr int LINES = TILE / 128;         // 128-byte lines of a tile
-  static constexpr int STAGE = 2 * TILE;
+  static constexpr int STAGE = 4 * TILE;           // K and V of two blocks
   static constexpr int ROWB = 2 * D;               // one fp16 cos | sin row
   static constexpr int MT = D / 16;                // M tiles of O^T
   static constexpr int STAGES = kWarps * NS * STAGE;
-  static constexpr int ROWS = STAGES;                           // [warp][stage] table rows
-  static constexpr int META = ROWS + kWarps * NS * ROWB;        // [split block] int4
-  static constexpr int BARS = META + kMaxSplit * 16;
+  static constexpr int ROWS = STAGES;                               // [warp][stage][2] table rows
+  static constexpr int META = ROWS + kWarps * NS * 2 * ROWB;        // [split block, padded to pairs] int4
+  static constexpr int MASK = META + (kMaxSplit + 2 * kWarps) * 16;  // [same] uint32
+  static constexpr int BARS = MASK + (kMaxSplit + 2 * kWarps) * 4;
   static constexpr int OST = D + 4;                             // padded row stride of the merge
   static constexpr int MERGE_W = (48 + 16 * OST) * 4;           // ms[16], l[16], mt[16], O[16][OST] of one warp
   static constexpr int MERGE = kWarps * MERGE_W;                // overlays stages, rows and meta
@@ -101,10 +102,15 @@ __device__ __forceinline__ uint32_t distance(int t, int b) {
   return b > t ? (uint32_t)b - (uint32_t)t : (uint32_t)t - (uint32_t)b;
 }
 
-template <int D, int NT, bool WTS, int NS, int CPS>
+// DUAL (groups of up to 4 heads): the 8 columns of a product hold the group's heads twice, columns 0-3 with the
+// query rotated for the first block of a pair and 4-7 for the second, so the query rotation and the softmax run
+// once for two blocks; each block's products use their half of the columns, and the two halves are states of
+// their own until the merge.
+template <int D, int NT, bool DUAL, bool WTS, int NS, int CPS>
 __global__ void __launch_bounds__(kWarps * 32, CPS)
     decode_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const DecodeArgs a) {
+  static_assert(!DUAL || NT == 1, "two half groups fill one column tile");
   using LY = Lay<D, NS>;
   constexpr int NW = kWarps;
   constexpr int NH = D / 32;  // 4-dim words of x (and of y) a thread holds per key: 4 at d 128, 2 at d 64
@@ -112,13 +118,14 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t sbase = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - ptx::smem_addr(smem_raw));
-  const uint32_t bar_base = sbase + LY::BARS;
   int4* meta = reinterpret_cast<int4*>(sgen + LY::META);
+  uint32_t* vmask = reinterpret_cast<uint32_t*>(sgen + LY::MASK);
 
   const int split = blockIdx.x, hk = blockIdx.y, r = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, tig = lane & 3;
   const int G = a.G, mb = a.max_blocks;
+  const uint32_t bar0 = sbase + LY::BARS + warp * NS * 8;
 
   int L = a.seq_lens[r];
   const int Lmax = (int)min((long long)mb * 16, 2147483632LL);
@@ -132,53 +139,85 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
   const int b_begin = split * a.split_blocks;
   const int b_end = min(nblk, b_begin + a.split_blocks);
   const int span = b_end - b_begin;
-  const int nmine = span > warp ? (span - warp + NW - 1) / NW : 0;
+  const int nmine = span > warp ? (span - warp + NW - 1) / NW : 0;  // blocks of this warp
+  const int npair = (nmine + 1) >> 1;
   int tq = a.q_pos[r];
   if (tq < 0 || tq >= a.max_pos) {
     if (threadIdx.x == 0 && split == 0) atomicOr(a.err, kErrPosition);
     tq = 0;
   }
 
-  const uint16_t* cs16 = a.cs_f16;
-  // lane 0: issue the k-th block of this warp into its stage (K, V, and the cos | sin row of |t - start|)
-  auto issue_blk = [&](int k, int phys, int start) {
-    const int stg = k % NS;
-    const uint32_t bar = bar_base + (warp * NS + stg) * 8;
-    const uint32_t dst = sbase + (warp * NS + stg) * LY::STAGE;
-    if (phys < 0 || phys >= a.num_blocks) {
-      ptx::mbar_arrive(bar);  // nothing to load; the consumer masks the block
-      return;
-    }
+  // What a block needs: x = first line of its tiles (-1: nothing to load), y = table row of |t - start| with the
+  // sign of the angle in bit 31.
+  auto place = [&](int phys, int start) {
     const uint32_t ad = distance(tq, start);
-    const bool row_ok = ad < (uint32_t)a.max_pos;
-    ptx::mbar_arrive_expect_tx(bar, 2 * LY::TILE + (row_ok ? LY::ROWB : 0));
-    const int y = (phys * a.Hkv + hk) * LY::LINES;
-    ptx::tma_load_2d(dst, &kmap, 0, y, bar);
-    ptx::tma_load_2d(dst + LY::TILE, &vmap, 0, y, bar);
-    if (row_ok)
-      ptx::bulk_load(sbase + LY::ROWS + (warp * NS + stg) * LY::ROWB, cs16 + (size_t)ad * D, LY::ROWB, bar);
+    const bool ok = phys >= 0 && phys < a.num_blocks && ad < (uint32_t)a.max_pos;
+    return make_int2(ok ? (phys * a.Hkv + hk) * LY::LINES : -1, (int)(ad | (start > tq ? 0x80000000u : 0u)));
+  };
+  // lane 0: issue a pair of blocks into stage stg (K, V and the cos | sin row of each)
+  auto issue = [&](int stg, int2 p0, int2 p1) {
+    const uint32_t bar = bar0 + stg * 8;
+    const uint32_t dst = sbase + (warp * NS + stg) * LY::STAGE;
+    const uint32_t row = sbase + LY::ROWS + (warp * NS + stg) * 2 * LY::ROWB;
+    const int n = (p0.x >= 0) + (p1.x >= 0);
+    ptx::mbar_arrive_expect_tx(bar, n * (2 * LY::TILE + LY::ROWB));
+    if (p0.x >= 0) {
+      ptx::tma_load_2d(dst, &kmap, 0, p0.x, bar);
+      ptx::tma_load_2d(dst + LY::TILE, &vmap, 0, p0.x, bar);
+      ptx::bulk_load(row, a.cs_f16 + (size_t)(p0.y & 0x7fffffff) * D, LY::ROWB, bar);
+    }
+    if (p1.x >= 0) {
+      ptx::tma_load_2d(dst + 2 * LY::TILE, &kmap, 0, p1.x, bar);
+      ptx::tma_load_2d(dst + 3 * LY::TILE, &vmap, 0, p1.x, bar);
+      ptx::bulk_load(row + LY::ROWB, a.cs_f16 + (size_t)(p1.y & 0x7fffffff) * D, LY::ROWB, bar);
+    }
   };
   {
     const int* bt = a.block_tables + (size_t)r * mb + b_begin;
     const int* bs = a.block_starts + (size_t)r * mb + b_begin;
     if (lane == 0) {
 #pragma unroll
-      for (int st = 0; st < NS; ++st) ptx::mbar_init(bar_base + (warp * NS + st) * 8, 1);
+      for (int st = 0; st < NS; ++st) ptx::mbar_init(bar0 + st * 8, 1);
       ptx::fence_barrier_init();
       ptx::fence_proxy_async_smem();
       // the first copies start at once, from the tables in global memory
-      const int pre = nmine < NS ? nmine : NS;
-      for (int k = 0; k < pre; ++k) issue_blk(k, __ldg(bt + warp + NW * k), __ldg(bs + warp + NW * k));
-    }
-    // per block: id, start, score factor (softmax scale * log2 e * key scale), log2 of the value scale
-    for (int i = threadIdx.x; i < span; i += NW * 32) {
-      const int phys = __ldg(bt + i);
-      float ks = 0.f, lv = -CUDART_INF_F;
-      if (phys >= 0 && phys < a.num_blocks) {
-        ks = __ldg(a.k_scale + (size_t)phys * a.Hkv + hk) * (a.scale * kLog2e);
-        lv = log2f(__ldg(a.v_scale + (size_t)phys * a.Hkv + hk));
+#pragma unroll 1
+      for (int p = 0; p < NS && p < npair; ++p) {
+        const int i0 = warp + 2 * NW * p, i1 = i0 + NW;
+        const int2 p0 = place(__ldg(bt + i0), __ldg(bs + i0));
+        issue(p, p0, i1 < span ? place(__ldg(bt + i1), __ldg(bs + i1)) : make_int2(-1, 0));
       }
-      meta[i] = make_int4(phys, __ldg(bs + i), __float_as_int(ks), __float_as_int(lv));
+    }
+    // per block, once for the CTA: place, score factor (softmax scale * log2 e * key scale), log2 of the value
+    // scale (finite), and the mask of its usable slots (bit 16: the values are zero)
+    for (int i = threadIdx.x; i < span + 2 * NW; i += NW * 32) {
+      int2 pl = make_int2(-1, 0);
+      float ks = 0.f, lv = 0.f;
+      uint32_t m = 0u;
+      if (i < span) {
+        const int phys = __ldg(bt + i), start = __ldg(bs + i);
+        pl = place(phys, start);
+        const int nk = min(16, L - (b_begin + i) * 16);
+        if (phys < 0 || phys >= a.num_blocks) {
+          atomicOr(a.err, kErrBlockId);
+        } else {
+          const uint32_t all = (1u << nk) - 1u;
+          m = all;
+          // keys whose position falls outside the table are masked
+          if (pl.x < 0 || start <= -16 || start >= a.max_pos) m = 0u;
+          else if (start < 0) m &= 0xffffu << -start;
+          else if (start > a.max_pos - nk) m &= (1u << (a.max_pos - start)) - 1u;
+          if (m != all) atomicOr(a.err, kErrPosition);
+          ks = __ldg(a.k_scale + (size_t)phys * a.Hkv + hk) * (a.scale * kLog2e);
+          lv = log2f(__ldg(a.v_scale + (size_t)phys * a.Hkv + hk));
+          if (lv < kMinLog) {  // scale 0, or below what is told apart from it
+            lv = 0.f;
+            m |= 0x10000u;
+          }
+        }
+      }
+      meta[i] = make_int4(pl.x, pl.y, __float_as_int(ks), __float_as_int(lv));
+      vmask[i] = m;
     }
   }
 
@@ -200,13 +239,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
     }
   }
 
-  // unrotated queries of this thread's heads (g8 + 8 nt), scaled to fp16, and the power of two taken out of
-  // the heads of its score columns (2 tig + j + 8 nt)
+  // unrotated queries of this thread's heads (column g8 + 8 nt), scaled to fp16, and the power of two taken out
+  // of the heads of its score columns (2 tig + j + 8 nt)
   uint32_t qx[NT][2 * NH], qy[NT][2 * NH];
   float qf[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int head = 8 * nt + g8;
+    const int head = DUAL ? (g8 & 3) : 8 * nt + g8;
     const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)r * a.Hq + (size_t)hk * G + head) * D + f0;
     uint32_t wx[2 * NH], wy[2 * NH];
     float amax = 0.f;
@@ -233,6 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
       qf[nt][j] = __int_as_float((__shfl_sync(FULL, ex, (2 * tig + j) * 4) + 127) << 23);
   }
 
+  // references: ms of the scores (denominator l), mt of the scores plus log2 of the value scale (O)
   float ms[NT][2], mt[NT][2], l[NT][2];
   float oacc[LY::MT][NT][4];
 #pragma unroll
@@ -247,111 +287,86 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
 
   __syncthreads();  // meta visible
 
-  bool timed_out = false;
-  int k_stop = nmine;
-  for (int k = 0; k < nmine; ++k) {
-    const int i = warp + NW * k;
-    const int b = b_begin + i;
-    const int stg = k % NS;
-    const uint32_t kbase = sbase + (warp * NS + stg) * LY::STAGE;
-    const uint32_t vbase = kbase + LY::TILE;
-    const uint32_t rowb = sbase + LY::ROWS + (warp * NS + stg) * LY::ROWB;
-
-    const int4 md = meta[i];
-    const int phys = md.x, start = md.y;
-    const float ksf = __int_as_float(md.z);
-    float lv = __int_as_float(md.w);
-    const bool ok = phys >= 0 && phys < a.num_blocks;
-    const int nk = min(16, L - b * 16);
-    bool v0 = ok && ks0 < nk, v1 = ok && ks0 + 8 < nk;
-    if (!ok && lane == 0) atomicOr(a.err, kErrBlockId);
-    const bool near = distance(tq, start) < (uint32_t)a.max_pos;
-    if (ok && !(near && start >= 0 && start <= a.max_pos - nk)) {
-      // keys whose position falls outside the table are masked
-      const long long p0 = (long long)start + ks0;
-      const bool in0 = p0 >= 0 && p0 < a.max_pos && near;
-      const bool in1 = p0 + 8 >= 0 && p0 + 8 < a.max_pos && near;
-      if (__any_sync(FULL, (v0 && !in0) || (v1 && !in1)) && lane == 0) atomicOr(a.err, kErrPosition);
-      v0 = v0 && in0;
-      v1 = v1 && in1;
+  // the rotated query words of column tile nt, R_{t - start} q, from a staged cos | sin row
+  auto rotate_q = [&](uint32_t row, int y, uint32_t (&bx)[NT][2 * NH], uint32_t (&by)[NT][2 * NH]) {
+    uint32_t cw[2 * NH], sw[2 * NH];
+#pragma unroll
+    for (int u = 0; u < NH / 2; ++u) {
+      const U4 c = ptx::lds128(row + 2 * f0 + 16 * u);
+      const U4 s = ptx::lds128(row + D + 2 * f0 + 16 * u);
+      cw[4 * u] = c.x; cw[4 * u + 1] = c.y; cw[4 * u + 2] = c.z; cw[4 * u + 3] = c.w;
+      sw[4 * u] = s.x; sw[4 * u + 1] = s.y; sw[4 * u + 2] = s.z; sw[4 * u + 3] = s.w;
     }
-    const bool zero_v = lv < kMinLog;  // scale 0 (or below what is told apart from it): the values are zero
-    lv = zero_v ? 0.f : lv;
-    const bool part = !__all_sync(FULL, v0 && v1) || zero_v;
-
-    const bool arrived = ptx::mbar_wait(bar_base + (warp * NS + stg) * 8, (uint32_t)((k / NS) & 1));
-    if (!__all_sync(FULL, arrived)) {
-      if (lane == 0) atomicOr(a.err, kErrTimeout);
-      timed_out = true;
-      k_stop = k;
-      break;
+    if (__any_sync(FULL, y < 0)) {  // a key ahead of the query: the sine takes the angle's sign
+      const uint32_t sgn = (uint32_t)(y >> 31) & 0x80008000u;
+#pragma unroll
+      for (int e = 0; e < 2 * NH; ++e) sw[e] ^= sgn;
     }
-
-    // S^T = K' Q'^T, two accumulation chains (the x and the y halves of the pairs)
-    float sx[NT][4], sy[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sx[nt][e] = sy[nt][e] = 0.f;
-    {
-      uint32_t kx[2][NH], ky[2][NH], cw[2 * NH], sw[2 * NH];
+      for (int e = 0; e < 2 * NH; ++e) rotate(qx[nt][e], qy[nt][e], cw[e], sw[e], bx[nt][e], by[nt][e]);
+  };
+  // S^T = K' Q'^T of one block
+  auto scores = [&](uint32_t kbase, const uint32_t (&bx)[NT][2 * NH], const uint32_t (&by)[NT][2 * NH],
+                    float (&sc)[NT][4]) {
+    uint32_t kx[2][NH], ky[2][NH];
 #pragma unroll
-      for (int row = 0; row < 2; ++row) {
-        if constexpr (D == 128) {
-          const U4 x = ptx::lds128(kbase + at<D>(ks0 + 8 * row, tig));
-          const U4 y = ptx::lds128(kbase + at<D>(ks0 + 8 * row, tig + 4));
-          kx[row][0] = x.x; kx[row][1] = x.y; kx[row][2] = x.z; kx[row][3] = x.w;
-          ky[row][0] = y.x; ky[row][1] = y.y; ky[row][2] = y.z; ky[row][3] = y.w;
-        } else {
-          const uint2 x = ptx::lds64(kbase + at<D>(ks0 + 8 * row, tig >> 1) + 8 * (tig & 1));
-          const uint2 y = ptx::lds64(kbase + at<D>(ks0 + 8 * row, 2 + (tig >> 1)) + 8 * (tig & 1));
-          kx[row][0] = x.x; kx[row][1] = x.y;
-          ky[row][0] = y.x; ky[row][1] = y.y;
-        }
-      }
-      // cos and sin of t - start for this thread's frequencies; sin takes the angle's sign
-      const uint32_t sgn = start > tq ? 0x80008000u : 0u;
-#pragma unroll
-      for (int u = 0; u < NH / 2; ++u) {
-        const U4 c = ptx::lds128(rowb + 2 * f0 + 16 * u);
-        const U4 s = ptx::lds128(rowb + D + 2 * f0 + 16 * u);
-        cw[4 * u] = c.x; cw[4 * u + 1] = c.y; cw[4 * u + 2] = c.z; cw[4 * u + 3] = c.w;
-        sw[4 * u] = s.x ^ sgn; sw[4 * u + 1] = s.y ^ sgn; sw[4 * u + 2] = s.z ^ sgn; sw[4 * u + 3] = s.w ^ sgn;
-      }
-#pragma unroll
-      for (int w = 0; w < NH; ++w) {  // 4 pairs of each key row
-        uint32_t x[2][2], y[2][2];    // [row][dims 0-1, 2-3]
-#pragma unroll
-        for (int row = 0; row < 2; ++row)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t hx = ptx::e4m3x2_to_h2(e ? kx[row][w] >> 16 : kx[row][w] & 0xffffu);
-            const uint32_t hy = ptx::e4m3x2_to_h2(e ? ky[row][w] >> 16 : ky[row][w] & 0xffffu);
-            rotate(hx, hy, rc[row][2 * w + e], rs[row][2 * w + e], x[row][e], y[row][e]);
-          }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint32_t bx[2], by[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            rotate(qx[nt][2 * w + e], qy[nt][2 * w + e], cw[2 * w + e], sw[2 * w + e], bx[e], by[e]);
-          ptx::mma_f16_16816(sx[nt], x[0][0], x[1][0], x[0][1], x[1][1], bx[0], bx[1]);
-          ptx::mma_f16_16816(sy[nt], y[0][0], y[1][0], y[0][1], y[1][1], by[0], by[1]);
-        }
+    for (int row = 0; row < 2; ++row) {
+      if constexpr (D == 128) {
+        const U4 x = ptx::lds128(kbase + at<D>(ks0 + 8 * row, tig));
+        const U4 y = ptx::lds128(kbase + at<D>(ks0 + 8 * row, tig + 4));
+        kx[row][0] = x.x; kx[row][1] = x.y; kx[row][2] = x.z; kx[row][3] = x.w;
+        ky[row][0] = y.x; ky[row][1] = y.y; ky[row][2] = y.z; ky[row][3] = y.w;
+      } else {
+        const uint2 x = ptx::lds64(kbase + at<D>(ks0 + 8 * row, tig >> 1) + 8 * (tig & 1));
+        const uint2 y = ptx::lds64(kbase + at<D>(ks0 + 8 * row, 2 + (tig >> 1)) + 8 * (tig & 1));
+        kx[row][0] = x.x; kx[row][1] = x.y;
+        ky[row][0] = y.x; ky[row][1] = y.y;
       }
     }
-
-    // online softmax over the 16 keys, per head column
-    uint32_t pb0[NT], pb1[NT];
-    float sc[NT][4];
+    // two accumulation chains (the x and the y halves of the pairs)
+    float sy[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[nt][e] = sy[nt][e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < NH; ++w) {  // 4 pairs of each key row
+      uint32_t x[2][2], y[2][2];    // [row][dims 0-1, 2-3]
+#pragma unroll
+      for (int row = 0; row < 2; ++row) {
+        uint32_t hx[2], hy[2];
+        ptx::e4m3x4_to_h2(kx[row][w], hx[0], hx[1]);
+        ptx::e4m3x4_to_h2(ky[row][w], hy[0], hy[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          rotate(hx[e], hy[e], rc[row][2 * w + e], rs[row][2 * w + e], x[row][e], y[row][e]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        ptx::mma_f16_16816(sc[nt], x[0][0], x[1][0], x[0][1], x[1][1], bx[nt][2 * w], bx[nt][2 * w + 1]);
+        ptx::mma_f16_16816(sy[nt], y[0][0], y[1][0], y[0][1], y[1][1], by[nt][2 * w], by[nt][2 * w + 1]);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[nt][e] += sy[nt][e];
+  };
+  // one step of the online softmax over 16 keys; m, ks and lv are those of the columns' block, wb the block
+  // whose sum is recorded
+  auto softmax = [&](float (&sc)[NT][4], uint32_t m, float ks, float lv, int wb, uint32_t (&pb0)[NT],
+                     uint32_t (&pb1)[NT]) {
+    const bool v0 = (m >> ks0) & 1u, v1 = (m >> (ks0 + 8)) & 1u;
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float f = fminf(ksf * qf[nt][j], 3.4e38f);  // finite: a product of 0 stays 0
-        sc[nt][j] = v0 ? (sx[nt][j] + sy[nt][j]) * f : -CUDART_INF_F;
-        sc[nt][2 + j] = v1 ? (sx[nt][2 + j] + sy[nt][2 + j]) * f : -CUDART_INF_F;
+        const float f = fminf(ks * qf[nt][j], 3.4e38f);  // finite: a product of 0 stays 0
+        sc[nt][j] = v0 ? sc[nt][j] * f : -CUDART_INF_F;
+        sc[nt][2 + j] = v1 ? sc[nt][2 + j] * f : -CUDART_INF_F;
         over |= fmaxf(sc[nt][j], sc[nt][2 + j]) > fminf(ms[nt][j], mt[nt][j] - lv) + kRescale;
       }
     if (__any_sync(FULL, over)) {  // rare: move the references, rescale what was summed
@@ -370,9 +385,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
           mt[nt][j] = mtn;
           l[nt][j] *= cs;
 #pragma unroll
-          for (int m = 0; m < LY::MT; ++m) {
-            oacc[m][nt][j] *= ct;
-            oacc[m][nt][2 + j] *= ct;
+          for (int mm = 0; mm < LY::MT; ++mm) {
+            oacc[mm][nt][j] *= ct;
+            oacc[mm][nt][2 + j] *= ct;
           }
         }
     }
@@ -381,74 +396,125 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
       float pv[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float rs_ = ms[nt][j] == -CUDART_INF_F ? 0.f : ms[nt][j];
-        const float rt = (mt[nt][j] == -CUDART_INF_F ? 0.f : mt[nt][j]) - lv - kHead;
-        float e = ex2(sc[nt][j] - rs_) + ex2(sc[nt][2 + j] - rs_);
-        pv[j] = ex2(sc[nt][j] - rt);
-        pv[2 + j] = ex2(sc[nt][2 + j] - rt);
+        const float ref = ms[nt][j] == -CUDART_INF_F ? 0.f : ms[nt][j];
+        // P = e * 2^(ms - mt + lv + 7); the cap only meets scores whose e is 0
+        const float w = ex2(fminf(ref - (mt[nt][j] == -CUDART_INF_F ? 0.f : mt[nt][j]) + lv + kHead, 126.f));
+        const float ea = ex2(sc[nt][j] - ref), eb = ex2(sc[nt][2 + j] - ref);
+        pv[j] = ea * w;
+        pv[2 + j] = eb * w;
+        float e = ea + eb;
         l[nt][j] += e;
         if constexpr (WTS) {
           e += __shfl_xor_sync(FULL, e, 4);
           e += __shfl_xor_sync(FULL, e, 8);
           e += __shfl_xor_sync(FULL, e, 16);
-          const int head = 8 * nt + 2 * tig + j;
-          if (g8 == 0 && head < G)
-            a.w_raw[(((size_t)r * a.Hkv + hk) * mb + b) * G + head] = e == 0.f ? -CUDART_INF_F : rs_ + log2f(e);
+          const int head = DUAL ? (2 * tig + j) & 3 : 8 * nt + 2 * tig + j;
+          if (g8 == 0 && head < G && wb < b_end)
+            a.w_raw[(((size_t)r * a.Hkv + hk) * mb + wb) * G + head] = e == 0.f ? -CUDART_INF_F : ref + log2f(e);
         }
       }
       pb0[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[0], pv[1]));  // keys 0..7
       pb1[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[2], pv[3]));  // keys 8..15
     }
-
-    // O^T += V^T P^T, two M tiles (16-byte chunks) per read
-    uint32_t klo = FULL, khi = FULL;  // which of keys (2 tig, 2 tig + 1) and + 8 count
+  };
+  // O^T += V^T P^T of one block, two M tiles (16-byte chunks) per read
+  const int v_key = frag_slot(lane & 7) + 8 * ((lane >> 3) & 1), v_chunk = lane >> 4;
+  auto values = [&](uint32_t vbase, uint32_t m, const uint32_t (&pb0)[NT], const uint32_t (&pb1)[NT]) {
+    uint32_t klo = FULL, khi = FULL;  // which of this lane's keys (rows 2 tig, 2 tig + 1, and + 8) count
+    const bool part = m != 0xffffu;
     if (part) {
-      const unsigned b0 = __ballot_sync(FULL, v0), b1 = __ballot_sync(FULL, v1);  // bit 4 g: fragment row g
-      const int s0 = 8 * tig, s1 = 8 * tig + 4;                                  // rows 2 tig, 2 tig + 1
-      klo = zero_v ? 0u : ((b0 >> s0) & 1u ? 0xffffu : 0u) | ((b0 >> s1) & 1u ? 0xffff0000u : 0u);
-      khi = zero_v ? 0u : ((b1 >> s0) & 1u ? 0xffffu : 0u) | ((b1 >> s1) & 1u ? 0xffff0000u : 0u);
+      const uint32_t u = m & 0x10000u ? 0u : m >> frag_slot(2 * tig), w = m & 0x10000u ? 0u : m >> frag_slot(2 * tig + 1);
+      klo = (u & 1u ? 0xffffu : 0u) | (w & 1u ? 0xffff0000u : 0u);
+      khi = (u & 0x100u ? 0xffffu : 0u) | (w & 0x100u ? 0xffff0000u : 0u);
     }
-    {
-      const int mi = lane >> 3, rr = lane & 7;
-      const int key = frag_slot(rr) + 8 * (mi & 1);
 #pragma unroll
-      for (int m = 0; m < LY::MT; m += 2) {
-        uint32_t w[4];
-        ptx::ldsm_x4_trans(vbase + at<D>(key, m + (mi >> 1)), w[0], w[1], w[2], w[3]);
-        if (part) {
-          w[0] &= klo;
-          w[1] &= khi;
-          w[2] &= klo;
-          w[3] &= khi;
-        }
+    for (int mm = 0; mm < LY::MT; mm += 2) {
+      uint32_t w[4];
+      ptx::ldsm_x4_trans(vbase + at<D>(v_key, mm + v_chunk), w[0], w[1], w[2], w[3]);
+      if (part) {
+        w[0] &= klo;
+        w[1] &= khi;
+        w[2] &= klo;
+        w[3] &= khi;
+      }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          // bytes (key 0: dims 0, 1; key 1: dims 0, 1) -> dim 0 of both keys, dim 1 of both keys
-          const uint32_t lo = __byte_perm(w[2 * u], 0u, 0x3120), hi = __byte_perm(w[2 * u + 1], 0u, 0x3120);
-          const uint32_t a0 = ptx::e4m3x2_to_h2(lo & 0xffffu), a1 = ptx::e4m3x2_to_h2(lo >> 16);
-          const uint32_t a2 = ptx::e4m3x2_to_h2(hi & 0xffffu), a3 = ptx::e4m3x2_to_h2(hi >> 16);
+      for (int u = 0; u < 2; ++u) {
+        // bytes (key 0: dims 0, 1; key 1: dims 0, 1) -> dim 0 of both keys, dim 1 of both keys
+        uint32_t a0, a1, a2, a3;
+        ptx::e4m3x4_to_h2(__byte_perm(w[2 * u], 0u, 0x3120), a0, a1);
+        ptx::e4m3x4_to_h2(__byte_perm(w[2 * u + 1], 0u, 0x3120), a2, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) ptx::mma_f16_16816(oacc[m + u][nt], a0, a1, a2, a3, pb0[nt], pb1[nt]);
-        }
+        for (int nt = 0; nt < NT; ++nt) ptx::mma_f16_16816(oacc[mm + u][nt], a0, a1, a2, a3, pb0[nt], pb1[nt]);
       }
     }
+  };
 
+  bool timed_out = false;
+  int p_stop = npair;
+  int stg = 0;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int p = 0; p < npair; ++p) {
+    const int i0 = warp + 2 * NW * p;  // blocks i0 and i0 + NW of the split
+    const uint32_t kbase = sbase + (warp * NS + stg) * LY::STAGE;
+    const uint32_t rowb = sbase + LY::ROWS + (warp * NS + stg) * 2 * LY::ROWB;
+    const uint32_t m0 = vmask[i0], m1 = vmask[i0 + NW];
+
+    const bool arrived = ptx::mbar_wait(bar0 + stg * 8, phase);
+    if (!__all_sync(FULL, arrived)) {
+      if (lane == 0) atomicOr(a.err, kErrTimeout);
+      timed_out = true;
+      p_stop = p;
+      break;
+    }
+    uint32_t bx[NT][2 * NH], by[NT][2 * NH], pb0[NT], pb1[NT];
+    float sc[NT][4];
+    if constexpr (DUAL) {
+      const int2 mq = reinterpret_cast<const int2*>(meta + i0 + (g8 >= 4 ? NW : 0))[0];  // of this query column
+      const int4 mc = meta[i0 + (tig >= 2 ? NW : 0)];                                   // of these score columns
+      rotate_q(rowb + (g8 >= 4 ? LY::ROWB : 0), mq.y, bx, by);
+      float s1[NT][4];
+      scores(kbase, bx, by, sc);
+      scores(kbase + 2 * LY::TILE, bx, by, s1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[0][e] = tig >= 2 ? s1[0][e] : sc[0][e];
+      softmax(sc, tig >= 2 ? m1 : m0, __int_as_float(mc.z), __int_as_float(mc.w),
+              b_begin + i0 + (tig >= 2 ? NW : 0), pb0, pb1);
+      const uint32_t z0[1] = {g8 < 4 ? pb0[0] : 0u}, z1[1] = {g8 < 4 ? pb1[0] : 0u};
+      const uint32_t y0[1] = {g8 < 4 ? 0u : pb0[0]}, y1[1] = {g8 < 4 ? 0u : pb1[0]};
+      values(kbase + LY::TILE, m0, z0, z1);
+      values(kbase + 3 * LY::TILE, m1, y0, y1);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int4 md = meta[i0 + u * NW];
+        const uint32_t m = u ? m1 : m0;
+        rotate_q(rowb + u * LY::ROWB, md.y, bx, by);
+        scores(kbase + 2 * u * LY::TILE, bx, by, sc);
+        softmax(sc, m, __int_as_float(md.z), __int_as_float(md.w), b_begin + i0 + u * NW, pb0, pb1);
+        values(kbase + (2 * u + 1) * LY::TILE, m, pb0, pb1);
+      }
+    }
     __syncwarp();
-    if (lane == 0 && k + NS < nmine) {
-      const int4 nx = meta[i + NW * NS];
-      issue_blk(k + NS, nx.x, nx.y);
+    if (lane == 0 && p + NS < npair) {
+      const int n0 = i0 + 2 * NW * NS;
+      issue(stg, *reinterpret_cast<const int2*>(meta + n0), *reinterpret_cast<const int2*>(meta + n0 + NW));
+    }
+    if (++stg == NS) {
+      stg = 0;
+      phase ^= 1u;
     }
   }
 
   if (timed_out && lane == 0) {
-    // blocks k_stop .. k_stop + NS - 1 were issued and not consumed
-    const int last = min(nmine, k_stop + NS);
-    for (int k2 = k_stop; k2 < last; ++k2)
-      ptx::mbar_wait(bar_base + (warp * NS + k2 % NS) * 8, (uint32_t)((k2 / NS) & 1), 100000000ull);
+    // pairs p_stop .. p_stop + NS - 1 were issued and not consumed
+    const int last = min(npair, p_stop + NS);
+    for (int p = p_stop; p < last; ++p)
+      ptx::mbar_wait(bar0 + (p % NS) * 8, (uint32_t)((p / NS) & 1), 100000000ull);
   }
   __syncthreads();  // every copy has landed and been read: the merge overlays the stages
 
-  // per-warp state: ms[16], l[16], mt[16], O[16][OST]
+  // per-warp state: ms[16], l[16], mt[16], O[16][OST], by column
   {
     float* w = reinterpret_cast<float*>(sgen + warp * LY::MERGE_W);
 #pragma unroll
@@ -478,20 +544,25 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
   const bool direct = n_valid == 1;
   for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
     const int head = idx / D, dim = idx - head * D;
+    constexpr int NST = DUAL ? 2 * NW : NW;  // states of a head: warps, and half columns 4 apart
+    auto state = [&](int w) {
+      return reinterpret_cast<const float*>(sgen + (w % NW) * LY::MERGE_W);
+    };
+    auto column = [&](int w) { return head + (w / NW) * 4; };
     float M = -CUDART_INF_F, T = -CUDART_INF_F;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float* p = reinterpret_cast<const float*>(sgen + w * LY::MERGE_W);
-      M = fmaxf(M, p[head]);
-      T = fmaxf(T, p[32 + head]);
+    for (int w = 0; w < NST; ++w) {
+      M = fmaxf(M, state(w)[column(w)]);
+      T = fmaxf(T, state(w)[32 + column(w)]);
     }
     float Ls = 0.f, O = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float* p = reinterpret_cast<const float*>(sgen + w * LY::MERGE_W);
-      // a warp that saw no finite reference still hands on its NaNs
-      Ls = fmaf(p[16 + head], p[head] == -CUDART_INF_F ? 1.f : exp2f(p[head] - M), Ls);
-      O = fmaf(p[48 + head * LY::OST + dim], p[32 + head] == -CUDART_INF_F ? 1.f : exp2f(p[32 + head] - T), O);
+    for (int w = 0; w < NST; ++w) {
+      const float* p = state(w);
+      const int c = column(w);
+      // a state without a finite reference still hands on its NaNs
+      Ls = fmaf(p[16 + c], p[c] == -CUDART_INF_F ? 1.f : exp2f(p[c] - M), Ls);
+      O = fmaf(p[48 + c * LY::OST + dim], p[32 + c] == -CUDART_INF_F ? 1.f : exp2f(p[32 + c] - T), O);
     }
     const float up = T == -CUDART_INF_F ? 1.f : exp2f(T - kHead - (M == -CUDART_INF_F ? 0.f : M));
     O = Ls == 0.f ? 0.f : O / Ls * up;
@@ -540,24 +611,26 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
   if (threadIdx.x == 0) a.counters[(size_t)r * a.Hkv + hk] = 0;
 }
 
-template <int D, int NT, bool WTS, int NS, int CPS>
+template <int D, int NT, bool DUAL, bool WTS, int NS, int CPS>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
+  const auto kernel = decode_q8_kernel<D, NT, DUAL, WTS, NS, CPS>;
   const int smem = Lay<D, NS>::TOTAL + 1024;
   static bool done[64] = {false};
-  cudaError_t e = set_smem_once(decode_q8_kernel<D, NT, WTS, NS, CPS>, smem, done);
+  cudaError_t e = set_smem_once(kernel, smem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const long long lines = (long long)a.num_blocks * a.Hkv * Lay<D, NS>::LINES;
   if (!make_q8_map(&km, a.k_pool, lines, Lay<D, NS>::LINES) || !make_q8_map(&vm, a.v_pool, lines, Lay<D, NS>::LINES))
     return cudaErrorInvalidValue;
   const dim3 grid((unsigned)a.n_split, (unsigned)a.Hkv, (unsigned)a.batch);
-  decode_q8_kernel<D, NT, WTS, NS, CPS><<<grid, kWarps * 32, smem, s>>>(km, vm, a);
+  kernel<<<grid, kWarps * 32, smem, s>>>(km, vm, a);
   return cudaGetLastError();
 }
 
 template <int D, bool WTS>
 cudaError_t launch_d(const DecodeArgs& a, cudaStream_t s) {
-  return a.G > 8 ? launch_t<D, 2, WTS, 3, 2>(a, s) : launch_t<D, 1, WTS, 3, 3>(a, s);
+  if (a.G > 8) return launch_t<D, 2, false, WTS, 2, 2>(a, s);
+  return a.G > 4 ? launch_t<D, 1, false, WTS, 2, 3>(a, s) : launch_t<D, 1, true, WTS, 2, 3>(a, s);
 }
 
 }  // namespace

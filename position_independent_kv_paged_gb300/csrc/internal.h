@@ -77,7 +77,9 @@ struct DecodePlan {
   int ctas_per_sm;  // tensor-core path: resident CTAs per SM (3 or 2; 1 for more than 8 heads per group)
 };
 DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs, bool bf16, int num_sms);
-// The e4m3 decode's plan.
+// The e4m3 decode's plan; its tensor-core kernel stages the block metadata of
+// splits up to kQ8MaxSplit blocks in shared memory.
+constexpr int kQ8MaxSplit = 256;
 DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan, cudaStream_t s);

@@ -141,15 +141,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_q8_kernel(AppendQ8Args 
         for (int i = sub; i < s0; i += RPP) {
           uint2* q = reinterpret_cast<uint2*>(pool + i * D + col);
           const uint2 w = *q;
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t pr = ((e < 2 ? w.x : w.y) >> (16 * (e & 1))) & 0xffffu;
-            const float2 z = ptx::e4m3x2_to_f2(pr);
-            y[2 * e] = z.x * f;
-            y[2 * e + 1] = z.y * f;
-          }
-          *q = make_uint2(pack4(y[0], y[1], y[2], y[3]), pack4(y[4], y[5], y[6], y[7]));
+          const float4 u = ptx::e4m3x4_to_f4(w.x), v = ptx::e4m3x4_to_f4(w.y);
+          *q = make_uint2(pack4(u.x * f, u.y * f, u.z * f, u.w * f), pack4(v.x * f, v.y * f, v.z * f, v.w * f));
         }
       }
     }

@@ -26,9 +26,9 @@ __device__ __forceinline__ void widen16(const uint4& w, float s, uint4& lo, uint
   uint32_t o[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 a = ptx::e4m3x2_to_f2(in[i] & 0xffffu), b = ptx::e4m3x2_to_f2(in[i] >> 16);
-    o[2 * i] = ptx::pack_bf16(a.x * s, a.y * s);
-    o[2 * i + 1] = ptx::pack_bf16(b.x * s, b.y * s);
+    const float4 x = ptx::e4m3x4_to_f4(in[i]);
+    o[2 * i] = ptx::pack_bf16(x.x * s, x.y * s);
+    o[2 * i + 1] = ptx::pack_bf16(x.z * s, x.w * s);
   }
   lo = make_uint4(o[0], o[1], o[2], o[3]);
   hi = make_uint4(o[4], o[5], o[6], o[7]);

@@ -239,15 +239,19 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------- e4m3 (exact in fp16)
-// Two e4m3 bytes (the low 16 bits) -> f16x2, byte 0 in the low half.
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w) {
-  uint32_t d;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(d) : "r"(w));
-  return d;
+// Four e4m3 bytes -> two f16x2 (bytes 0, 1 and bytes 2, 3).
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
-__device__ __forceinline__ float2 e4m3x2_to_f2(uint32_t w) {
-  const uint32_t h = e4m3x2_to_h2(w);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// Four e4m3 bytes -> fp32.
+__device__ __forceinline__ float4 e4m3x4_to_f4(uint32_t w) {
+  uint32_t lo, hi;
+  e4m3x4_to_h2(w, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // ---------------------------------------------------------------- packed fp32 pairs (sm_100+ f32x2)
