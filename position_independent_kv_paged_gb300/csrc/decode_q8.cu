@@ -68,7 +68,8 @@ struct Lay {
   static constexpr int OST = D + 4;                             // padded row stride of the merge
   static constexpr int MERGE_W = (48 + 16 * OST) * 4;           // ms[16], l[16], mt[16], O[16][OST] of one warp
   static constexpr int MERGE = kWarps * MERGE_W;                // overlays stages, rows and meta
-  static constexpr int TOTAL = (BARS + kWarps * NS * 8) > MERGE ? (BARS + kWarps * NS * 8) : MERGE;
+  static constexpr int TOTAL = BARS + kWarps * NS * 8;
+  static_assert(MERGE <= BARS, "the merge overlays what the loop no longer reads");
 };
 
 // Slot held by MMA fragment row g (row g + 8 holds slot + 8): rows read together by a quarter warp differ in bit 2.
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
           if (pl.x < 0 || start <= -16 || start >= a.max_pos) m = 0u;
           else if (start < 0) m &= 0xffffu << -start;
           else if (start > a.max_pos - nk) m &= (1u << (a.max_pos - start)) - 1u;
+          if (a.max_pos < 16) m &= (1u << a.max_pos) - 1u;  // R_slot reaches as far as the table
           if (m != all) atomicOr(a.err, kErrPosition);
           ks = __ldg(a.k_scale + (size_t)phys * a.Hkv + hk) * (a.scale * kLog2e);
           lv = log2f(__ldg(a.v_scale + (size_t)phys * a.Hkv + hk));
@@ -225,17 +227,16 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
   const int ks0 = frag_slot(g8);
   const int f0 = 4 * NH * tig;
 
-  // R_slot of both rows, fp16
+  // R_slot of both rows, fp16 (a slot past a table of fewer rows is masked)
   uint32_t rc[2][2 * NH], rs[2][2 * NH];
 #pragma unroll
   for (int row = 0; row < 2; ++row) {
-    const float* t = a.cos_sin + (size_t)min(ks0 + 8 * row, a.max_pos - 1) * D + f0;
+    const uint16_t* t = a.cs_f16 + (size_t)min(ks0 + 8 * row, a.max_pos - 1) * D + f0;
 #pragma unroll
-    for (int e = 0; e < 2 * NH; ++e) {
-      const float2 c = __ldg(reinterpret_cast<const float2*>(t + 2 * e));
-      const float2 sn = __ldg(reinterpret_cast<const float2*>(t + D / 2 + 2 * e));
-      rc[row][e] = ptx::pack_f16(c.x, c.y);
-      rs[row][e] = ptx::pack_f16(sn.x, sn.y);
+    for (int u = 0; u < NH / 2; ++u) {
+      const uint4 c = __ldg(reinterpret_cast<const uint4*>(t) + u), sn = __ldg(reinterpret_cast<const uint4*>(t + D / 2) + u);
+      rc[row][4 * u] = c.x; rc[row][4 * u + 1] = c.y; rc[row][4 * u + 2] = c.z; rc[row][4 * u + 3] = c.w;
+      rs[row][4 * u] = sn.x; rs[row][4 * u + 1] = sn.y; rs[row][4 * u + 2] = sn.z; rs[row][4 * u + 3] = sn.w;
     }
   }
 
@@ -328,10 +329,6 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
     // two accumulation chains (the x and the y halves of the pairs)
     float sy[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[nt][e] = sy[nt][e] = 0.f;
-#pragma unroll
     for (int w = 0; w < NH; ++w) {  // 4 pairs of each key row
       uint32_t x[2][2], y[2][2];    // [row][dims 0-1, 2-3]
 #pragma unroll
@@ -345,8 +342,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        ptx::mma_f16_16816(sc[nt], x[0][0], x[1][0], x[0][1], x[1][1], bx[nt][2 * w], bx[nt][2 * w + 1]);
-        ptx::mma_f16_16816(sy[nt], y[0][0], y[1][0], y[0][1], y[1][1], by[nt][2 * w], by[nt][2 * w + 1]);
+        if (w == 0) {
+          ptx::mma_f16_16816_set(sc[nt], x[0][0], x[1][0], x[0][1], x[1][1], bx[nt][0], bx[nt][1]);
+          ptx::mma_f16_16816_set(sy[nt], y[0][0], y[1][0], y[0][1], y[1][1], by[nt][0], by[nt][1]);
+        } else {
+          ptx::mma_f16_16816(sc[nt], x[0][0], x[1][0], x[0][1], x[1][1], bx[nt][2 * w], bx[nt][2 * w + 1]);
+          ptx::mma_f16_16816(sy[nt], y[0][0], y[1][0], y[0][1], y[1][1], by[nt][2 * w], by[nt][2 * w + 1]);
+        }
       }
     }
 #pragma unroll
@@ -449,30 +451,19 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
     }
   };
 
-  bool timed_out = false;
-  int p_stop = npair;
-  int stg = 0;
-  uint32_t phase = 0;
-#pragma unroll 1
-  for (int p = 0; p < npair; ++p) {
+  // one pair from stage `stg` (a compile-time constant: every shared address is a per-thread base and an immediate)
+  const uint32_t wbase = sbase + warp * NS * LY::STAGE, wrow = sbase + LY::ROWS + warp * NS * 2 * LY::ROWB;
+  auto step = [&](const int stg, const int p, const uint32_t phase) -> bool {
     const int i0 = warp + 2 * NW * p;  // blocks i0 and i0 + NW of the split
-    const uint32_t kbase = sbase + (warp * NS + stg) * LY::STAGE;
-    const uint32_t rowb = sbase + LY::ROWS + (warp * NS + stg) * 2 * LY::ROWB;
+    const uint32_t kbase = wbase + stg * LY::STAGE, rowb = wrow + stg * 2 * LY::ROWB;
     const uint32_t m0 = vmask[i0], m1 = vmask[i0 + NW];
-
-    const bool arrived = ptx::mbar_wait(bar0 + stg * 8, phase);
-    if (!__all_sync(FULL, arrived)) {
-      if (lane == 0) atomicOr(a.err, kErrTimeout);
-      timed_out = true;
-      p_stop = p;
-      break;
-    }
+    if (!__all_sync(FULL, ptx::mbar_wait(bar0 + stg * 8, phase))) return false;
     uint32_t bx[NT][2 * NH], by[NT][2 * NH], pb0[NT], pb1[NT];
     float sc[NT][4];
     if constexpr (DUAL) {
-      const int2 mq = reinterpret_cast<const int2*>(meta + i0 + (g8 >= 4 ? NW : 0))[0];  // of this query column
-      const int4 mc = meta[i0 + (tig >= 2 ? NW : 0)];                                   // of these score columns
-      rotate_q(rowb + (g8 >= 4 ? LY::ROWB : 0), mq.y, bx, by);
+      const int mq = meta[i0 + (g8 >= 4 ? NW : 0)].y;   // of this query column's block
+      const int4 mc = meta[i0 + (tig >= 2 ? NW : 0)];   // of these score columns' block
+      rotate_q(rowb + (g8 >= 4 ? LY::ROWB : 0), mq, bx, by);
       float s1[NT][4];
       scores(kbase, bx, by, sc);
       scores(kbase + 2 * LY::TILE, bx, by, s1);
@@ -500,11 +491,23 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
       const int n0 = i0 + 2 * NW * NS;
       issue(stg, *reinterpret_cast<const int2*>(meta + n0), *reinterpret_cast<const int2*>(meta + n0 + NW));
     }
-    if (++stg == NS) {
-      stg = 0;
-      phase ^= 1u;
+    return true;
+  };
+  bool timed_out = false;
+  int p_stop = npair;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int p = 0; p < npair; p += NS, phase ^= 1u) {
+#pragma unroll
+    for (int stg = 0; stg < NS; ++stg) {
+      if (p + stg < npair && !timed_out && !step(stg, p + stg, phase)) {
+        timed_out = true;
+        p_stop = p + stg;
+      }
     }
+    if (timed_out) break;
   }
+  if (timed_out && lane == 0) atomicOr(a.err, kErrTimeout);
 
   if (timed_out && lane == 0) {
     // pairs p_stop .. p_stop + NS - 1 were issued and not consumed
