@@ -6,11 +6,14 @@
 // gist.science 2606.13126, section 2.1).
 //
 // Work: one CTA = (split, kv head, request); each of its warps owns every NW-th
-// 16-key block of the split, two at a time, and runs its own TMA ring.  A (block, head) tile is
-// 16 d contiguous bytes; the tensor map sees the pool as lines of 128 bytes (one
-// key at d 128, two at d 64) and swizzles them, so that the key-row reads and
-// the transposing reads of V are free of bank conflicts.  The fp16 cos | sin row
-// of the block's query rotation comes with them.
+// 16-key block of the split, two at a time, and runs its own ring of stages.  A
+// (block, head) tile is 16 d contiguous bytes, lines of 128 bytes (one key at d
+// 128, two at d 64) whose 16-byte chunks are stored at chunk ^ (line mod 8), so
+// that the key-row reads and the transposing reads of V are free of bank
+// conflicts.  The fp16 cos | sin row of the block's query rotation comes with
+// them.  The copies are cp.async of the whole warp (18 instructions for a pair of
+// blocks at d 128): one thread issuing tensor copies took about 120 issue slots
+// per pair, a quarter of the kernel's, and the kernel is bound by issue.
 //
 // Per block, with t the query's position, b the block's start, s the slot:
 //   score = (R_{t-b} q) . (R_s k8) * (k scale) * softmax scale
@@ -39,6 +42,7 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "tmap.cuh"
+#include <cuda_fp16.h>
 
 namespace minipic {
 namespace {
@@ -51,12 +55,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;               // a reference moves when exceeded by 2^8
 constexpr float kHead = 7.f;                  // P of a key at its reference is 2^7
+constexpr float kNone = -3e38f;               // a reference before the first key
 constexpr float kMinLog = -100.f;             // log2 of the smallest value scale told apart from zero
 
 template <int D, int NS>
 struct Lay {
   static constexpr int TILE = 16 * D;              // bytes of one (block, head) tile of K or V
-  static constexpr int LINES = TILE / 128;         // 128-byte lines of a tile
   static constexpr int STAGE = 4 * TILE;           // K and V of two blocks
   static constexpr int ROWB = 2 * D;               // one fp16 cos | sin row
   static constexpr int MT = D / 16;                // M tiles of O^T
@@ -64,12 +68,11 @@ struct Lay {
   static constexpr int ROWS = STAGES;                               // [warp][stage][2] table rows
   static constexpr int META = ROWS + kWarps * NS * 2 * ROWB;        // [split block, padded to pairs] int4
   static constexpr int MASK = META + (kMaxSplit + 2 * kWarps) * 16;  // [same] uint32
-  static constexpr int BARS = MASK + (kMaxSplit + 2 * kWarps) * 4;
   static constexpr int OST = D + 4;                             // padded row stride of the merge
   static constexpr int MERGE_W = (48 + 16 * OST) * 4;           // ms[16], l[16], mt[16], O[16][OST] of one warp
   static constexpr int MERGE = kWarps * MERGE_W;                // overlays stages, rows and meta
-  static constexpr int TOTAL = BARS + kWarps * NS * 8;
-  static_assert(MERGE <= BARS, "the merge overlays what the loop no longer reads");
+  static constexpr int TOTAL = MASK + (kMaxSplit + 2 * kWarps) * 4;
+  static_assert(MERGE <= TOTAL, "the merge overlays what the loop no longer reads");
 };
 
 // Slot held by MMA fragment row g (row g + 8 holds slot + 8): rows read together by a quarter warp differ in bit 2.
@@ -108,17 +111,14 @@ __device__ __forceinline__ uint32_t distance(int t, int b) {
 // once for two blocks; each block's products use their half of the columns, and the two halves are states of
 // their own until the merge.
 template <int D, int NT, bool DUAL, bool WTS, int NS, int CPS>
-__global__ void __launch_bounds__(kWarps * 32, CPS)
-    decode_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                     const DecodeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(!DUAL || NT == 1, "two half groups fill one column tile");
   using LY = Lay<D, NS>;
   constexpr int NW = kWarps;
   constexpr int NH = D / 32;  // 4-dim words of x (and of y) a thread holds per key: 4 at d 128, 2 at d 64
   constexpr unsigned FULL = 0xffffffffu;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t sbase = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
-  uint8_t* sgen = smem_raw + (sbase - ptx::smem_addr(smem_raw));
+  extern __shared__ __align__(128) uint8_t sgen[];
+  const uint32_t sbase = ptx::smem_addr(sgen);
   int4* meta = reinterpret_cast<int4*>(sgen + LY::META);
   uint32_t* vmask = reinterpret_cast<uint32_t*>(sgen + LY::MASK);
 
@@ -126,7 +126,6 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, tig = lane & 3;
   const int G = a.G, mb = a.max_blocks;
-  const uint32_t bar0 = sbase + LY::BARS + warp * NS * 8;
 
   int L = a.seq_lens[r];
   const int Lmax = (int)min((long long)mb * 16, 2147483632LL);
@@ -148,46 +147,50 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
     tq = 0;
   }
 
-  // What a block needs: x = first line of its tiles (-1: nothing to load), y = table row of |t - start| with the
+  // What a block needs: x = its (block, head) tile (-1: nothing usable), y = table row of |t - start| with the
   // sign of the angle in bit 31.
   auto place = [&](int phys, int start) {
     const uint32_t ad = distance(tq, start);
     const bool ok = phys >= 0 && phys < a.num_blocks && ad < (uint32_t)a.max_pos;
-    return make_int2(ok ? (phys * a.Hkv + hk) * LY::LINES : -1, (int)(ad | (start > tq ? 0x80000000u : 0u)));
+    return make_int2(ok ? phys * a.Hkv + hk : -1, (int)(ad | (start > tq ? 0x80000000u : 0u)));
   };
-  // lane 0: issue a pair of blocks into stage stg (K, V and the cos | sin row of each)
-  auto issue = [&](int stg, int2 p0, int2 p1) {
-    const uint32_t bar = bar0 + stg * 8;
-    const uint32_t dst = sbase + (warp * NS + stg) * LY::STAGE;
-    const uint32_t row = sbase + LY::ROWS + (warp * NS + stg) * 2 * LY::ROWB;
-    const int n = (p0.x >= 0) + (p1.x >= 0);
-    ptx::mbar_arrive_expect_tx(bar, n * (2 * LY::TILE + LY::ROWB));
-    if (p0.x >= 0) {
-      ptx::tma_load_2d(dst, &kmap, 0, p0.x, bar);
-      ptx::tma_load_2d(dst + LY::TILE, &vmap, 0, p0.x, bar);
-      ptx::bulk_load(row, a.cs_f16 + (size_t)(p0.y & 0x7fffffff) * D, LY::ROWB, bar);
+  // The warp copies a pair of blocks into a stage: lane -> 16 bytes of each tile's next 512, swizzled, and of the
+  // two table rows.  A block with nothing usable copies tile 0 and row 0, which its mask keeps out.
+  const uint32_t wbase = sbase + warp * NS * LY::STAGE, wrow = sbase + LY::ROWS + warp * NS * 2 * LY::ROWB;
+  const uint32_t sw0 = (uint32_t)((lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4));  // lines 0-3; 4-7: ^ 64
+  const uint8_t* kg = static_cast<const uint8_t*>(a.k_pool) + 16 * lane;
+  const uint8_t* vg = static_cast<const uint8_t*>(a.v_pool) + 16 * lane;
+  constexpr int RL = LY::ROWB / 16;  // lanes of a table row
+  const uint8_t* rg = reinterpret_cast<const uint8_t*>(a.cs_f16) + 16 * (lane % RL);
+  auto issue = [&](const int stg, int2 p0, int2 p1) {
+    const uint32_t dst = wbase + stg * LY::STAGE;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const size_t tile = (size_t)max(u ? p1.x : p0.x, 0) * LY::TILE;
+#pragma unroll
+      for (int i = 0; i < LY::TILE / 512; ++i) {
+        const uint32_t to = dst + 2 * u * LY::TILE + 512 * i + (i & 1 ? sw0 ^ 64u : sw0);
+        ptx::cp_async16(to, kg + tile + 512 * i);
+        ptx::cp_async16(to + LY::TILE, vg + tile + 512 * i);
+      }
     }
-    if (p1.x >= 0) {
-      ptx::tma_load_2d(dst + 2 * LY::TILE, &kmap, 0, p1.x, bar);
-      ptx::tma_load_2d(dst + 3 * LY::TILE, &vmap, 0, p1.x, bar);
-      ptx::bulk_load(row + LY::ROWB, a.cs_f16 + (size_t)(p1.y & 0x7fffffff) * D, LY::ROWB, bar);
-    }
+    const int2 pr = lane < RL ? p0 : p1;
+    if (lane < 2 * RL)
+      ptx::cp_async16(wrow + stg * 2 * LY::ROWB + 16 * lane,
+                      rg + (size_t)(pr.x < 0 ? 0 : pr.y & 0x7fffffff) * LY::ROWB);
   };
   {
     const int* bt = a.block_tables + (size_t)r * mb + b_begin;
     const int* bs = a.block_starts + (size_t)r * mb + b_begin;
-    if (lane == 0) {
+    // the first copies start at once, from the tables in global memory
 #pragma unroll
-      for (int st = 0; st < NS; ++st) ptx::mbar_init(bar0 + st * 8, 1);
-      ptx::fence_barrier_init();
-      ptx::fence_proxy_async_smem();
-      // the first copies start at once, from the tables in global memory
-#pragma unroll 1
-      for (int p = 0; p < NS && p < npair; ++p) {
-        const int i0 = warp + 2 * NW * p, i1 = i0 + NW;
+    for (int p = 0; p < NS; ++p) {
+      const int i0 = warp + 2 * NW * p, i1 = i0 + NW;
+      if (p < npair) {
         const int2 p0 = place(__ldg(bt + i0), __ldg(bs + i0));
         issue(p, p0, i1 < span ? place(__ldg(bt + i1), __ldg(bs + i1)) : make_int2(-1, 0));
       }
+      ptx::cp_async_commit();
     }
     // per block, once for the CTA: place, score factor (softmax scale * log2 e * key scale), log2 of the value
     // scale (finite), and the mask of its usable slots (bit 16: the values are zero)
@@ -274,11 +277,14 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
   }
 
   // references: ms of the scores (denominator l), mt of the scores plus log2 of the value scale (O)
-  float ms[NT][2], mt[NT][2], l[NT][2];
+  // (before the first key a finite value far below any score, so that no difference of two is undefined), and
+  // dl = ms - mt + 7
+  float ms[NT][2], mt[NT][2], dl[NT][2], l[NT][2];
   float oacc[LY::MT][NT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    ms[nt][0] = ms[nt][1] = mt[nt][0] = mt[nt][1] = -CUDART_INF_F;
+    ms[nt][0] = ms[nt][1] = mt[nt][0] = mt[nt][1] = kNone;
+    dl[nt][0] = dl[nt][1] = kHead;
     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
     for (int m = 0; m < LY::MT; ++m)
@@ -381,10 +387,10 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
           bm = fmaxf(bm, __shfl_xor_sync(FULL, bm, 8));
           bm = fmaxf(bm, __shfl_xor_sync(FULL, bm, 16));
           const float msn = fmaxf(ms[nt][j], bm), mtn = fmaxf(mt[nt][j], bm + lv);
-          const float cs = msn == -CUDART_INF_F ? 1.f : ex2(ms[nt][j] - msn);
-          const float ct = mtn == -CUDART_INF_F ? 1.f : ex2(mt[nt][j] - mtn);
+          const float cs = ex2(ms[nt][j] - msn), ct = ex2(mt[nt][j] - mtn);
           ms[nt][j] = msn;
           mt[nt][j] = mtn;
+          dl[nt][j] = msn - mtn + kHead;
           l[nt][j] *= cs;
 #pragma unroll
           for (int mm = 0; mm < LY::MT; ++mm) {
@@ -398,10 +404,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
       float pv[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float ref = ms[nt][j] == -CUDART_INF_F ? 0.f : ms[nt][j];
         // P = e * 2^(ms - mt + lv + 7); the cap only meets scores whose e is 0
-        const float w = ex2(fminf(ref - (mt[nt][j] == -CUDART_INF_F ? 0.f : mt[nt][j]) + lv + kHead, 126.f));
-        const float ea = ex2(sc[nt][j] - ref), eb = ex2(sc[nt][2 + j] - ref);
+        const float w = ex2(fminf(dl[nt][j] + lv, 126.f));
+        const float ea = ex2(sc[nt][j] - ms[nt][j]), eb = ex2(sc[nt][2 + j] - ms[nt][j]);
         pv[j] = ea * w;
         pv[2 + j] = eb * w;
         float e = ea + eb;
@@ -412,7 +417,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
           e += __shfl_xor_sync(FULL, e, 16);
           const int head = DUAL ? (2 * tig + j) & 3 : 8 * nt + 2 * tig + j;
           if (g8 == 0 && head < G && wb < b_end)
-            a.w_raw[(((size_t)r * a.Hkv + hk) * mb + wb) * G + head] = e == 0.f ? -CUDART_INF_F : ref + log2f(e);
+            a.w_raw[(((size_t)r * a.Hkv + hk) * mb + wb) * G + head] =
+                e == 0.f ? -CUDART_INF_F : ms[nt][j] + log2f(e);
         }
       }
       pb0[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[0], pv[1]));  // keys 0..7
@@ -452,12 +458,12 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
   };
 
   // one pair from stage `stg` (a compile-time constant: every shared address is a per-thread base and an immediate)
-  const uint32_t wbase = sbase + warp * NS * LY::STAGE, wrow = sbase + LY::ROWS + warp * NS * 2 * LY::ROWB;
-  auto step = [&](const int stg, const int p, const uint32_t phase) -> bool {
+  auto step = [&](const int stg, const int p) {
     const int i0 = warp + 2 * NW * p;  // blocks i0 and i0 + NW of the split
     const uint32_t kbase = wbase + stg * LY::STAGE, rowb = wrow + stg * 2 * LY::ROWB;
     const uint32_t m0 = vmask[i0], m1 = vmask[i0 + NW];
-    if (!__all_sync(FULL, ptx::mbar_wait(bar0 + stg * 8, phase))) return false;
+    ptx::cp_async_wait<NS - 1>();
+    __syncwarp();  // every lane's part of the stage has landed
     uint32_t bx[NT][2 * NH], by[NT][2 * NH], pb0[NT], pb1[NT];
     float sc[NT][4];
     if constexpr (DUAL) {
@@ -486,36 +492,21 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
         values(kbase + (2 * u + 1) * LY::TILE, m, pb0, pb1);
       }
     }
-    __syncwarp();
-    if (lane == 0 && p + NS < npair) {
+    __syncwarp();  // every lane has read the stage
+    if (p + NS < npair) {
       const int n0 = i0 + 2 * NW * NS;
       issue(stg, *reinterpret_cast<const int2*>(meta + n0), *reinterpret_cast<const int2*>(meta + n0 + NW));
     }
-    return true;
+    ptx::cp_async_commit();
   };
-  bool timed_out = false;
-  int p_stop = npair;
-  uint32_t phase = 0;
 #pragma unroll 1
-  for (int p = 0; p < npair; p += NS, phase ^= 1u) {
+  for (int p = 0; p < npair; p += NS) {
 #pragma unroll
-    for (int stg = 0; stg < NS; ++stg) {
-      if (p + stg < npair && !timed_out && !step(stg, p + stg, phase)) {
-        timed_out = true;
-        p_stop = p + stg;
-      }
-    }
-    if (timed_out) break;
+    for (int stg = 0; stg < NS; ++stg)
+      if (p + stg < npair) step(stg, p + stg);
   }
-  if (timed_out && lane == 0) atomicOr(a.err, kErrTimeout);
-
-  if (timed_out && lane == 0) {
-    // pairs p_stop .. p_stop + NS - 1 were issued and not consumed
-    const int last = min(npair, p_stop + NS);
-    for (int p = p_stop; p < last; ++p)
-      ptx::mbar_wait(bar0 + (p % NS) * 8, (uint32_t)((p / NS) & 1), 100000000ull);
-  }
-  __syncthreads();  // every copy has landed and been read: the merge overlays the stages
+  ptx::cp_async_wait<0>();
+  __syncthreads();  // every stage has been read: the merge overlays them
 
   // per-warp state: ms[16], l[16], mt[16], O[16][OST], by column
   {
@@ -552,7 +543,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
       return reinterpret_cast<const float*>(sgen + (w % NW) * LY::MERGE_W);
     };
     auto column = [&](int w) { return head + (w / NW) * 4; };
-    float M = -CUDART_INF_F, T = -CUDART_INF_F;
+    float M = kNone, T = kNone;
 #pragma unroll
     for (int w = 0; w < NST; ++w) {
       M = fmaxf(M, state(w)[column(w)]);
@@ -563,13 +554,11 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
     for (int w = 0; w < NST; ++w) {
       const float* p = state(w);
       const int c = column(w);
-      // a state without a finite reference still hands on its NaNs
-      Ls = fmaf(p[16 + c], p[c] == -CUDART_INF_F ? 1.f : exp2f(p[c] - M), Ls);
-      O = fmaf(p[48 + c * LY::OST + dim], p[32 + c] == -CUDART_INF_F ? 1.f : exp2f(p[32 + c] - T), O);
+      Ls = fmaf(p[16 + c], exp2f(p[c] - M), Ls);
+      O = fmaf(p[48 + c * LY::OST + dim], exp2f(p[32 + c] - T), O);
     }
-    const float up = T == -CUDART_INF_F ? 1.f : exp2f(T - kHead - (M == -CUDART_INF_F ? 0.f : M));
-    O = Ls == 0.f ? 0.f : O / Ls * up;
-    const float lse2 = Ls == 0.f ? -CUDART_INF_F : (M == -CUDART_INF_F ? 0.f : M) + log2f(Ls);
+    O = Ls == 0.f ? 0.f : O / Ls * exp2f(T - M - kHead);
+    const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
     const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
     if (direct) {
       static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(O);
@@ -617,16 +606,12 @@ __global__ void __launch_bounds__(kWarps * 32, CPS)
 template <int D, int NT, bool DUAL, bool WTS, int NS, int CPS>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
   const auto kernel = decode_q8_kernel<D, NT, DUAL, WTS, NS, CPS>;
-  const int smem = Lay<D, NS>::TOTAL + 1024;
+  const int smem = Lay<D, NS>::TOTAL;
   static bool done[64] = {false};
   cudaError_t e = set_smem_once(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  CUtensorMap km, vm;
-  const long long lines = (long long)a.num_blocks * a.Hkv * Lay<D, NS>::LINES;
-  if (!make_q8_map(&km, a.k_pool, lines, Lay<D, NS>::LINES) || !make_q8_map(&vm, a.v_pool, lines, Lay<D, NS>::LINES))
-    return cudaErrorInvalidValue;
   const dim3 grid((unsigned)a.n_split, (unsigned)a.Hkv, (unsigned)a.batch);
-  kernel<<<grid, kWarps * 32, smem, s>>>(km, vm, a);
+  kernel<<<grid, kWarps * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -51,19 +51,6 @@ inline bool make_pool_block_map(CUtensorMap* m, const void* base, long long rows
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// An e4m3 pool as lines of 128 bytes; one box brings the `box_lines` lines of a (block, head) tile.
-inline bool make_q8_map(CUtensorMap* m, const void* base, long long lines, int box_lines) {
-  auto fn = tmap_encode_fn();
-  if (!fn || lines <= 0) return false;
-  cuuint64_t dims[2] = {128, (cuuint64_t)lines};
-  cuuint64_t strides[1] = {128};
-  cuuint32_t box[2] = {128, (cuuint32_t)box_lines};
-  cuuint32_t es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Set the dynamic shared-memory limit of a kernel once per device.
 template <typename K>
 inline cudaError_t set_smem_once(K kernel, int bytes, bool (&done)[64]) {
