@@ -444,7 +444,12 @@ size_t minipic_attn_decode_weights_workspace_size(int32_t batch, int32_t num_q_h
                                                   int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size);
 
 /* minipic_attn_decode that also writes block_weights (required; layout, type
- * and workspace rules as for minipic_attn_decode_q8). */
+ * and workspace rules as for minipic_attn_decode_q8, and like that call it never
+ * reads a masked slot into a sum and passes an attended NaN on).  bf16 takes the
+ * score product in fp16, rotated with rope->cos_sin_f16 (required; the bf16 rows
+ * are not read), because the weights show the scores' error: key elements have to
+ * stay within +-65504 (beyond, the rows that attend to them become NaN); queries
+ * of any size are fine. */
 minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
                                            const minipic_rope* rope, const minipic_decode_batch* batch, float scale,
                                            void* block_weights, void* workspace, size_t workspace_bytes,

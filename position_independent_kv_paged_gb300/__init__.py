@@ -665,7 +665,7 @@ def attn_decode_weights_workspace_size(batch: int, num_q_heads: int, num_kv_head
 
 
 def _decode_weights(fn, where, size, q, kv, pools, block_tables, block_starts, seq_lens, q_pos, rope, scale, out,
-                    lse, block_weights, workspace, stream, need_f16, need_bf16):
+                    lse, block_weights, workspace, stream, need_f16):
     torch = _torch()
     B, Hq, d = q.shape
     mb = block_tables.shape[1] if block_tables.dim() == 2 else -1
@@ -683,7 +683,7 @@ def _decode_weights(fn, where, size, q, kv, pools, block_tables, block_starts, s
     if lse is not None:
         _need(lse, "lse", dtype=torch.float32)
         _shape(lse, "lse", (B, Hq))
-    rp = _rope_struct(rope, need_f16, need_bf16=need_bf16)
+    rp = _rope_struct(rope, need_f16)
     if out is not None:
         _need(out, "out", dtype=q.dtype)
         _shape(out, "out", q.shape)
@@ -719,16 +719,16 @@ def attn_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_star
     L = load()
     _need(q, "q", ndim=3)
     kv = _kv_q8(k_pool, v_pool, k_scale, v_scale)
-    bf16 = q.dtype == torch.bfloat16
     return _decode_weights(L.minipic_attn_decode_q8, "minipic_attn_decode_q8", attn_decode_q8_workspace_size, q, kv,
                            (k_pool, v_pool, k_scale, v_scale), block_tables, block_starts, seq_lens, q_pos, rope,
-                           scale, out, lse, block_weights, workspace, stream, bf16, False)
+                           scale, out, lse, block_weights, workspace, stream, q.dtype == torch.bfloat16)
 
 
 def attn_decode_weights(q, k_pool, v_pool, block_tables, block_starts, seq_lens, q_pos, rope, block_weights,
                         scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
     """``attn_decode`` that also writes ``block_weights`` (as in
-    ``attn_decode_q8``), for eviction by attention weight."""
+    ``attn_decode_q8``), for eviction by attention weight.  bf16 takes the score
+    product in fp16 (keys within +-65504)."""
     torch = _torch()
     L = load()
     _need(q, "q", ndim=3)
@@ -738,7 +738,7 @@ def attn_decode_weights(q, k_pool, v_pool, block_tables, block_starts, seq_lens,
     _need(block_weights, "block_weights")
     return _decode_weights(L.minipic_attn_decode_weights, "minipic_attn_decode_weights",
                            attn_decode_weights_workspace_size, q, kv, (k_pool, v_pool), block_tables, block_starts,
-                           seq_lens, q_pos, rope, scale, out, lse, block_weights, workspace, stream, False,
+                           seq_lens, q_pos, rope, scale, out, lse, block_weights, workspace, stream,
                            q.dtype == torch.bfloat16)
 
 

@@ -666,7 +666,7 @@ size_t weights_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_
   size_t most = 0;
   for (int bf16 = 0; bf16 < 2; ++bf16) {
     const DecodePlan p = q8 ? plan_decode_q8(batch, Hkv, Hq / Hkv, D, mb, bf16 != 0, sms)
-                            : plan_decode(batch, Hkv, Hq / Hkv, D, mb, bs, false, sms);
+                            : plan_decode(batch, Hkv, Hq / Hkv, D, mb, bs, bf16 != 0, sms);
     const size_t n = decode_ws_weights(batch, Hq, Hkv, D, p.n_split, mb).total;
     most = n > most ? n : most;
   }
@@ -686,21 +686,27 @@ minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_he
                                            minipic_stream_t stream) {
   const bool bf16 = dtype == MINIPIC_BF16;
   bool empty = false;
-  minipic_status st = check_decode(dtype, num_q_heads, kv, rope, b, scale, true, bf16, &empty);
-  if (st != MINIPIC_OK || empty) return st;
+  minipic_status st = check_decode(dtype, num_q_heads, kv, rope, b, scale, true, false, &empty);
+  if (st != MINIPIC_OK) return st;
+  // the tensor-core path rotates with the fp16 rows
+  if (bf16 && (!rope->cos_sin_f16 || !aligned16(rope->cos_sin_f16))) return MINIPIC_ERR_INVALID;
+  if (empty) return MINIPIC_OK;
   if (!block_weights || !aligned16(block_weights)) return MINIPIC_ERR_INVALID;
   if (b->batch > kMaxGridYZ || kv->num_kv_heads > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
   int* err = nullptr;
   int sms = 0;
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
   const DecodePlan plan = plan_decode(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
-                                      b->max_blocks_per_seq, kv->block_size, false, sms);
+                                      b->max_blocks_per_seq, kv->block_size, bf16, sms);
   DecodeArgs a = decode_args(bf16, num_q_heads, kv, rope, b, scale, plan, err);
   st = place_weights_ws(a, block_weights, workspace, workspace_bytes);
   if (st != MINIPIC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = launch_decode_simt_weights(a, bf16, s);
-  if (e == cudaSuccess) e = launch_decode_merge(a, bf16, s);
+  a.cs_f16 = rope->cos_sin_f16;
+  // as for attn_decode: the tensor-core kernel merges its splits itself, with no pool every key is masked
+  const bool mma = plan.use_mma && kv->num_blocks > 0;
+  cudaError_t e = mma ? launch_decode_mma_weights(a, s) : launch_decode_simt_weights(a, bf16, s);
+  if (e == cudaSuccess && !mma) e = launch_decode_merge(a, bf16, s);
   if (e == cudaSuccess) e = launch_block_weights(a, bf16, s);
   return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
     const int hq = g * G + h;
     if (direct) {
       T* out = static_cast<T*>(a.out) + ((size_t)r * a.Hq + hq) * D + dim;
-      const bool any = Q8 ? Ls != 0.f : Ls > 0.f;  // over e4m3, a NaN sum stays one
+      const bool any = Q8 || WTS ? Ls != 0.f : Ls > 0.f;  // over e4m3 or with block weights, a NaN sum stays one
       st_f<T>(out, any ? O / Ls : 0.f);
       if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = any ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
       if (WTS && dim == 0) a.w_lse[(size_t)r * a.Hq + hq] = any ? M + log2f(Ls) : -CUDART_INF_F;
@@ -261,7 +261,7 @@ __global__ void decode_merge_kernel(DecodeArgs a) {
       O = fmaf(a.part_o[(base + s) * a.D + dim], f, O);
     }
     T* out = static_cast<T*>(a.out) + ((size_t)r * a.Hq + hq) * a.D + dim;
-    const bool any = a.k_scale ? Ls != 0.f : Ls > 0.f;  // over e4m3, a NaN sum stays one
+    const bool any = a.k_scale || a.w_lse ? Ls != 0.f : Ls > 0.f;  // as in the split kernel
     st_f<T>(out, any ? O / Ls : 0.f);
     if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = any ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
     if (dim == 0 && a.w_lse) a.w_lse[(size_t)r * a.Hq + hq] = any ? M + log2f(Ls) : -CUDART_INF_F;

@@ -90,8 +90,10 @@ cudaError_t launch_decode_merge(const DecodeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_decode_simt_q8(const DecodeArgs& a, bool bf16, cudaStream_t s);
 // e4m3 cache, bf16 q and out, tensor cores.
 cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t s);
-// The exact-precision kernel over the f32 or bf16 cache, recording block weights.
+// The exact-precision kernel over the f32 cache (or a bf16 one of no blocks), recording block weights.
 cudaError_t launch_decode_simt_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
+// The bf16 tensor-core kernel, recording block weights (num_blocks > 0).
+cudaError_t launch_decode_mma_weights(const DecodeArgs& a, cudaStream_t s);
 // w_raw and w_lse -> weights.
 cudaError_t launch_block_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, bool rotate, cudaStream_t s);

@@ -70,7 +70,8 @@ def test_decode_weights_refusals(lib):
     assert call(Hq=5) == 1
     assert call(bw=None) == 1                                  # the weights are what the call is for
     assert call(bw=0xD008) == 1
-    assert call(rp=rope(b16=None)) == 1                        # the bf16 decode's table
+    assert call(rp=rope(f16=None)) == 1                        # the fp16 rows
+    assert call(rp=rope(f16=0xB008)) == 1
     assert call(db=decode(B=65536)) == 2
     assert call(db=decode(B=0)) == 0
 

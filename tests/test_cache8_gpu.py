@@ -162,8 +162,7 @@ def test_one_workspace_for_calls_of_other_shapes(env, dtype):
 @pytest.mark.parametrize("dtype,Hq,Hkv,d", [("f32", 8, 2, 64), ("bf16", 4, 2, 64), ("bf16", 32, 2, 64),
                                             ("bf16", 8, 1, 128), ("bf16", 28, 4, 128), ("bf16", 16, 1, 128)])
 def test_decode_weights_over_the_unquantised_cache(env, dtype, Hq, Hkv, d):
-    """out and lse as attn_decode gives them; weights against float64.  The bf16 decode rotates in bf16: three half
-    steps of 2^-8 on either side in place of fp16's."""
+    """out near attn_decode's, out and weights against float64 (scores from fp16 products; P is bf16)."""
     torch, mp, dev = env
     lens = [300, 0, 1, 16, 47, 2050, 17, 800]
     w = W.irregular_decode(21, dtype, seq_lens=lens, Hq=Hq, Hkv=Hkv, d=d)
@@ -179,11 +178,55 @@ def test_decode_weights_over_the_unquantised_cache(env, dtype, Hq, Hkv, d):
     k, v = (oracle.widen(x, dtype) for x in (w.kv.k_pool, w.kv.v_pool))
     ref = c8.attention(oracle.widen(w.decode.q, dtype), np.arange(len(lens) + 1), w.decode.q_pos, k, v,
                        w.decode.block_tables, w.decode.block_starts, lens, w.rope_base)
-    big = dict(ref, smax=ref["smax"] * (8 if dtype == "bf16" else 1))
-    check_attention(f64(out), big, dtype, d, max(lens), p_half=2.0 ** -8 if dtype == "bf16" else None)
-    check_weights(f64(bw), big, dtype, d, lens, 7.0)
+    check_attention(f64(out), ref, dtype, d, max(lens), p_half=2.0 ** -8 if dtype == "bf16" else None)
+    check_weights(f64(bw), ref, dtype, d, lens, 7.0)
     assert float((out.float() - out0.float()).abs().max()) <= (2e-2 if dtype == "bf16" else 1e-5)
     assert mp.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("f32", 8, 2, 64), ("bf16", 8, 2, 64), ("bf16", 8, 1, 128),
+                                            ("bf16", 16, 1, 128)])
+def test_decode_weights_with_nan_in_masked_and_attended_slots(env, dtype, Hq, Hkv, d):
+    """Slots past the lengths hold NaN and one request has bad blocks: nothing of them shows; an attended NaN does."""
+    torch, mp, dev = env
+    lens = [35, 300, 7, 48]
+    w = W.irregular_decode(22, dtype, seq_lens=lens, Hq=Hq, Hkv=Hkv, d=d, pool_blocks=40)
+    D = w.decode
+    blocks = iter(np.random.default_rng(22).permutation(40))   # each block in one place: the generator repeats them
+    for r, n in enumerate(lens):
+        for b in range(-(-n // 16)):
+            D.block_tables[r, b] = next(blocks)
+    nan = np.float32(np.nan) if dtype == "f32" else np.uint16(0x7fc0)
+    for r, n in enumerate(lens):
+        if n % 16:
+            for p in (w.kv.k_pool, w.kv.v_pool):
+                p[D.block_tables[r, n // 16], :, n % 16:] = nan
+    D.block_tables[1, 3] = 10 ** 6
+    t = upload_decode(w, torch, dev)
+    rope = mp.rope_table(w.max_pos, d, w.rope_base, device=dev)
+    mb = t["block_tables"].shape[1]
+
+    def call():
+        bw = torch.zeros(len(lens), Hkv, mb, dtype=t["q"].dtype, device=dev)
+        out, _ = mp.attn_decode_weights(t["q"], t["k_pool"], t["v_pool"], t["block_tables"], t["block_starts"],
+                                        t["seq_lens"], t["q_pos"], rope, bw)
+        torch.cuda.synchronize()
+        return f64(out), f64(bw)
+    mp.device_error(clear=True)
+    out, bw = call()
+    assert mp.device_error(clear=True) == 1
+    k, v = (oracle.widen(x, dtype) for x in (w.kv.k_pool, w.kv.v_pool))
+    ref = c8.attention(oracle.widen(D.q, dtype), np.arange(len(lens) + 1), D.q_pos, k, v, D.block_tables,
+                       D.block_starts, lens, w.rope_base)
+    check_attention(out, ref, dtype, d, max(lens), p_half=2.0 ** -8 if dtype == "bf16" else None)
+    check_weights(bw, ref, dtype, d, lens, 0.0)
+    t["v_pool"][int(D.block_tables[3, 1]), 0, 4, 5] = float("nan")
+    t["k_pool"][int(D.block_tables[0, 0]), Hkv - 1, 2, 1] = float("nan")
+    out, bw = call()
+    assert mp.device_error(clear=True) == 1
+    G = Hq // Hkv
+    assert np.all(np.isnan(out[3, :G, 5])) and np.all(np.isfinite(out[3, :, 6]))
+    assert np.all(np.isnan(out[0, -G:])) and np.all(np.isnan(bw[0, -1, :3]))
 
 
 # ------------------------------------------------------------------------------------------------ prefill
