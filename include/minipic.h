@@ -479,7 +479,8 @@ typedef struct {
 } minipic_kv_evict_batch;
 
 /* For each block b < ceil(seq_len / block_size) of each request:
- *   score = decay * score + sum over kv heads of block_weights   (added in fp64, kept in fp32)
+ *   score = decay * score + sum over kv heads of block_weights   (added with twice fp32's
+ *                                                            precision, rounded to fp32 once)
  * and when a request has more than `budget` blocks, its first keep_first and
  * last keep_last stay together with the best of the others by score (NaN is
  * the worst; of equal scores the lower index stays) up to `budget`.  The

@@ -590,18 +590,40 @@ def kv_swap_in(host_k, host_v, block_ids, k_pool, v_pool, stream=None):
 
 # ---------------------------------------------------------------- 8-bit cache, block weights, eviction
 
-def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _current_device(*tensors):
-    """The calls act on the current device: every tensor has to live there."""
+def _args(*specs):
+    """Check (name, tensor, dtype, shape) of every argument that is not None:
+    contiguous CUDA tensors of that dtype and shape, all on the current device
+    (the one the calls act on)."""
     torch = _torch()
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    for name, t, dtype, shape in specs:
+        if t is None or (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and
+                         t.is_contiguous() and t.get_device() == dev):
+            continue
+        _need(t, name, dtype=dtype, ndim=len(shape))
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+
+
+def _sizes(t, name, ndim):
+    """The shape of the tensor that gives a call its sizes."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    return t.shape
+
+
+def _rope16(rope, d, need_f16):
+    """ABI view of a table for the calls that read its float32 and, for bf16, its float16 form; and its specs."""
+    torch = _torch()
+    f32, f16 = (rope.cos_sin, rope.cos_sin_f16) if isinstance(rope, RopeTable) else (rope, None)
+    if need_f16 and f16 is None:
+        raise TypeError("this call needs the RopeTable built by rope_table() (it carries the float16 table)")
+    n = _sizes(f32, "rope", 2)[0]
+    return (_Rope(f32.data_ptr(), n, d, _ptr(f16), None),
+            (("rope", f32, torch.float32, (n, d)), ("rope f16", f16, torch.float16, (n, d))))
 
 
 def _on(stream):
@@ -609,17 +631,15 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
 
 
-def _kv_q8(k_pool, v_pool, k_scale, v_scale) -> _KVQ8:
+def _kv_q8(k_pool, v_pool, k_scale, v_scale):
+    """ABI view of an e4m3 cache, and its specs."""
     torch = _torch()
-    _need(k_pool, "k_pool", dtype=torch.float8_e4m3fn, ndim=4)
-    _need(v_pool, "v_pool", dtype=torch.float8_e4m3fn, ndim=4)
-    _need(k_scale, "k_scale", dtype=torch.float32, ndim=2)
-    _need(v_scale, "v_scale", dtype=torch.float32, ndim=2)
-    _shape(v_pool, "v_pool", k_pool.shape)
-    nb, hkv, bs, d = k_pool.shape
-    _shape(k_scale, "k_scale", (nb, hkv))
-    _shape(v_scale, "v_scale", (nb, hkv))
-    return _KVQ8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, hkv, bs, d)
+    shape = nb, hkv, bs, d = _sizes(k_pool, "k_pool", 4)
+    specs = (("k_pool", k_pool, torch.float8_e4m3fn, shape), ("v_pool", v_pool, torch.float8_e4m3fn, shape),
+             ("k_scale", k_scale, torch.float32, (nb, hkv)), ("v_scale", v_scale, torch.float32, (nb, hkv)))
+    if not all(isinstance(x[1], torch.Tensor) for x in specs):
+        raise TypeError("pools and scales must be torch.Tensors")
+    return _KVQ8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, hkv, bs, d), specs
 
 
 def kv_append_q8(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_pool, k_scale, v_scale,
@@ -632,24 +652,20 @@ def kv_append_q8(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_po
     request's count (read from cu_new_lens if None, which synchronizes)."""
     torch = _torch()
     L = load()
-    kv = _kv_q8(k_pool, v_pool, k_scale, v_scale)
-    _need(k_new, "k_new", ndim=3)
-    _need(v_new, "v_new", dtype=k_new.dtype, ndim=3)
-    _shape(k_new, "k_new", (k_new.shape[0], kv.num_kv_heads, kv.head_dim))
-    _shape(v_new, "v_new", k_new.shape)
-    for name, t in (("cu_new_lens", cu_new_lens), ("kv_start", kv_start)):
-        _need(t, name, dtype=torch.int32, ndim=1)
-    _need(block_tables, "block_tables", dtype=torch.int32, ndim=2)
-    B = kv_start.shape[0]
-    if cu_new_lens.shape[0] != B + 1 or block_tables.shape[0] != B:
-        raise ValueError("cu_new_lens must have batch + 1 entries and block_tables batch rows")
-    _current_device(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_pool, k_scale, v_scale)
+    kv, specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    total = _sizes(k_new, "k_new", 3)[0]
+    B, mb = _sizes(block_tables, "block_tables", 2)
+    code = _dtype_code(k_new)
+    new = (total, kv.num_kv_heads, kv.head_dim)
+    _args(("k_new", k_new, k_new.dtype, new), ("v_new", v_new, k_new.dtype, new),
+          ("cu_new_lens", cu_new_lens, torch.int32, (B + 1,)), ("kv_start", kv_start, torch.int32, (B,)),
+          ("block_tables", block_tables, torch.int32, (B, mb)), *specs)
     if max_new_len is None:
         max_new_len = int((cu_new_lens[1:] - cu_new_lens[:-1]).max().item()) if B else 0
     ab = _Append(k_new.data_ptr(), v_new.data_ptr(), cu_new_lens.data_ptr(), kv_start.data_ptr(),
-                 block_tables.data_ptr(), B, k_new.shape[0], int(max_new_len), block_tables.shape[1])
-    _check(L.minipic_kv_append_q8(_dtype_code(k_new), ctypes.byref(kv), ctypes.byref(ab), _stream(stream)),
-           "minipic_kv_append_q8")
+                 block_tables.data_ptr(), B, total, int(max_new_len), mb)
+    st = L.minipic_kv_append_q8(code, ctypes.byref(kv), ctypes.byref(ab), _stream(stream))
+    _check(st, "minipic_kv_append_q8")
 
 
 def attn_decode_q8_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -664,33 +680,19 @@ def attn_decode_weights_workspace_size(batch: int, num_q_heads: int, num_kv_head
                                                                  max_blocks_per_seq, block_size))
 
 
-def _decode_weights(fn, where, size, q, kv, pools, block_tables, block_starts, seq_lens, q_pos, rope, scale, out,
-                    lse, block_weights, workspace, stream, need_f16):
+def _decode_weights(fn, where, size, q, kv, specs, block_tables, block_starts, seq_lens, q_pos, rope, scale, out,
+                    lse, block_weights, workspace, stream):
     torch = _torch()
-    B, Hq, d = q.shape
-    mb = block_tables.shape[1] if block_tables.dim() == 2 else -1
-    for name, t in (("block_tables", block_tables), ("block_starts", block_starts)):
-        _need(t, name, dtype=torch.int32, ndim=2)
-        _shape(t, name, (B, mb))
-    for name, t in (("seq_lens", seq_lens), ("q_pos", q_pos)):
-        _need(t, name, dtype=torch.int32, ndim=1)
-        _shape(t, name, (B,))
-    if d != kv.head_dim:
-        raise ValueError("q and the pools differ in head_dim")
-    if block_weights is not None:
-        _need(block_weights, "block_weights", dtype=q.dtype, ndim=3)
-        _shape(block_weights, "block_weights", (B, kv.num_kv_heads, mb))
-    if lse is not None:
-        _need(lse, "lse", dtype=torch.float32)
-        _shape(lse, "lse", (B, Hq))
-    rp = _rope_struct(rope, need_f16)
-    if out is not None:
-        _need(out, "out", dtype=q.dtype)
-        _shape(out, "out", q.shape)
+    B, Hq, d = shape = _sizes(q, "q", 3)
+    mb = _sizes(block_tables, "block_tables", 2)[1]
+    code, i32 = _dtype_code(q), torch.int32
+    rp, rope_specs = _rope16(rope, kv.head_dim, code == BF16)
+    _args(("q", q, q.dtype, (B, Hq, kv.head_dim)), *specs, ("block_tables", block_tables, i32, (B, mb)),
+          ("block_starts", block_starts, i32, (B, mb)), ("seq_lens", seq_lens, i32, (B,)),
+          ("q_pos", q_pos, i32, (B,)), *rope_specs, ("out", out, q.dtype, shape), ("lse", lse, torch.float32, (B, Hq)),
+          ("block_weights", block_weights, q.dtype, (B, kv.num_kv_heads, mb)))
     if workspace is not None:
-        _need(workspace, "workspace")
-    cs = rope.cos_sin if isinstance(rope, RopeTable) else rope
-    _current_device(q, *pools, block_tables, block_starts, seq_lens, q_pos, cs, out, lse, block_weights, workspace)
+        _args(("workspace", workspace, workspace.dtype, workspace.shape))
     with _on(stream):
         if out is None:
             out = torch.empty_like(q)
@@ -699,9 +701,9 @@ def _decode_weights(fn, where, size, q, kv, pools, block_tables, block_starts, s
             workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
         db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
                      q_pos.data_ptr(), B, mb, out.data_ptr(), _ptr(lse))
-        _check(fn(_dtype_code(q), Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), float(scale),
-                  _ptr(block_weights), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                  _stream(stream)), where)
+        st = fn(code, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), float(scale), _ptr(block_weights),
+                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
+        _check(st, where)
     return out, lse
 
 
@@ -715,13 +717,11 @@ def attn_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_star
     head; entries past a request's length are left as they were.  Returns
     (out, lse) like ``attn_decode``.  A workspace passed in must have been
     zeroed once."""
-    torch = _torch()
     L = load()
-    _need(q, "q", ndim=3)
-    kv = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    kv, specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
     return _decode_weights(L.minipic_attn_decode_q8, "minipic_attn_decode_q8", attn_decode_q8_workspace_size, q, kv,
-                           (k_pool, v_pool, k_scale, v_scale), block_tables, block_starts, seq_lens, q_pos, rope,
-                           scale, out, lse, block_weights, workspace, stream, q.dtype == torch.bfloat16)
+                           specs, block_tables, block_starts, seq_lens, q_pos, rope, scale, out, lse, block_weights,
+                           workspace, stream)
 
 
 def attn_decode_weights(q, k_pool, v_pool, block_tables, block_starts, seq_lens, q_pos, rope, block_weights,
@@ -729,17 +729,15 @@ def attn_decode_weights(q, k_pool, v_pool, block_tables, block_starts, seq_lens,
     """``attn_decode`` that also writes ``block_weights`` (as in
     ``attn_decode_q8``), for eviction by attention weight.  bf16 takes the score
     product in fp16 (keys within +-65504)."""
-    torch = _torch()
     L = load()
-    _need(q, "q", ndim=3)
-    kv = _kv(k_pool, v_pool)
-    if k_pool.dtype != q.dtype:
-        raise TypeError("q and the pools must share a dtype")
-    _need(block_weights, "block_weights")
+    nb, hkv, bs, d = shape = _sizes(k_pool, "k_pool", 4)
+    if block_weights is None or not isinstance(v_pool, _torch().Tensor):
+        raise TypeError("block_weights and v_pool must be torch.Tensors")
+    kv = _KV(k_pool.data_ptr(), v_pool.data_ptr(), nb, hkv, bs, d)
     return _decode_weights(L.minipic_attn_decode_weights, "minipic_attn_decode_weights",
-                           attn_decode_weights_workspace_size, q, kv, (k_pool, v_pool), block_tables, block_starts,
-                           seq_lens, q_pos, rope, scale, out, lse, block_weights, workspace, stream,
-                           q.dtype == torch.bfloat16)
+                           attn_decode_weights_workspace_size, q, kv,
+                           (("k_pool", k_pool, q.dtype, shape), ("v_pool", v_pool, q.dtype, shape)), block_tables,
+                           block_starts, seq_lens, q_pos, rope, scale, out, lse, block_weights, workspace, stream)
 
 
 def attn_prefill_q8_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_q_len: int,
@@ -755,31 +753,17 @@ def attn_prefill_q8(q, cu_q_lens, q_pos, k_pool, v_pool, k_scale, v_scale, block
     ``attn_prefill``."""
     torch = _torch()
     L = load()
-    _need(q, "q", dtype=torch.bfloat16, ndim=3)
-    kv = _kv_q8(k_pool, v_pool, k_scale, v_scale)
-    total_q, Hq, d = q.shape
-    for name, t in (("block_tables", block_tables), ("block_starts", block_starts)):
-        _need(t, name, dtype=torch.int32, ndim=2)
-    for name, t in (("cu_q_lens", cu_q_lens), ("q_pos", q_pos), ("kv_lens", kv_lens)):
-        _need(t, name, dtype=torch.int32, ndim=1)
-    B, mb = kv_lens.shape[0], block_tables.shape[1]
-    _shape(cu_q_lens, "cu_q_lens", (B + 1,))
-    _shape(q_pos, "q_pos", (total_q,))
-    _shape(block_tables, "block_tables", (B, mb))
-    _shape(block_starts, "block_starts", (B, mb))
-    if d != kv.head_dim:
-        raise ValueError("q and the pools differ in head_dim")
-    if lse is not None:
-        _need(lse, "lse", dtype=torch.float32)
-        _shape(lse, "lse", (total_q, Hq))
-    if out is not None:
-        _need(out, "out", dtype=q.dtype)
-        _shape(out, "out", q.shape)
+    kv, specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    total_q, Hq, d = shape = _sizes(q, "q", 3)
+    B, mb = _sizes(block_tables, "block_tables", 2)
+    i32 = torch.int32
+    rp, rope_specs = _rope16(rope, kv.head_dim, True)
+    _args(("q", q, torch.bfloat16, (total_q, Hq, kv.head_dim)), ("cu_q_lens", cu_q_lens, i32, (B + 1,)),
+          ("q_pos", q_pos, i32, (total_q,)), *specs, ("block_tables", block_tables, i32, (B, mb)),
+          ("block_starts", block_starts, i32, (B, mb)), ("kv_lens", kv_lens, i32, (B,)), *rope_specs,
+          ("out", out, torch.bfloat16, shape), ("lse", lse, torch.float32, (total_q, Hq)))
     if workspace is not None:
-        _need(workspace, "workspace")
-    rp = _rope_struct(rope, True)
-    _current_device(q, cu_q_lens, q_pos, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, kv_lens,
-                    rope.cos_sin, out, lse, workspace)
+        _args(("workspace", workspace, workspace.dtype, workspace.shape))
     with _on(stream):
         if out is None:
             out = torch.empty_like(q)
@@ -789,10 +773,10 @@ def attn_prefill_q8(q, cu_q_lens, q_pos, k_pool, v_pool, k_scale, v_scale, block
         pb = _Prefill(q.data_ptr(), cu_q_lens.data_ptr(), q_pos.data_ptr(), block_tables.data_ptr(),
                       block_starts.data_ptr(), kv_lens.data_ptr(), B, total_q, int(max_q_len), mb, out.data_ptr(),
                       _ptr(lse))
-        _check(L.minipic_attn_prefill_q8(_dtype_code(q), Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(pb),
-                                         float(scale), workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(), _stream(stream)),
-               "minipic_attn_prefill_q8")
+        st = L.minipic_attn_prefill_q8(BF16, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(pb), float(scale),
+                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                       _stream(stream))
+        _check(st, "minipic_attn_prefill_q8")
     return out, lse
 
 
@@ -818,19 +802,13 @@ def kv_evict(scores, block_tables, block_starts, seq_lens, budget: int, keep_fir
     and lengths are overwritten and returned."""
     torch = _torch()
     L = load()
-    _need(scores, "scores", dtype=torch.float32, ndim=2)
-    B, mb = scores.shape
-    for name, t in (("block_tables", block_tables), ("block_starts", block_starts)):
-        _need(t, name, dtype=torch.int32, ndim=2)
-        _shape(t, name, (B, mb))
-    _need(seq_lens, "seq_lens", dtype=torch.int32, ndim=1)
-    _shape(seq_lens, "seq_lens", (B,))
-    hkv, code = 0, F32
+    B, mb = shape = _sizes(scores, "scores", 2)
+    hkv, code, i32 = 0, F32, torch.int32
     if block_weights is not None:
-        _need(block_weights, "block_weights", ndim=3)
-        hkv, code = block_weights.shape[1], _dtype_code(block_weights)
-        _shape(block_weights, "block_weights", (B, hkv, mb))
-    _current_device(scores, block_tables, block_starts, seq_lens, block_weights)
+        hkv, code = _sizes(block_weights, "block_weights", 3)[1], _dtype_code(block_weights)
+        _args(("block_weights", block_weights, block_weights.dtype, (B, hkv, mb)))
+    _args(("scores", scores, torch.float32, shape), ("block_tables", block_tables, i32, shape),
+          ("block_starts", block_starts, i32, shape), ("seq_lens", seq_lens, i32, (B,)))
     src = (scores, block_tables, block_starts, seq_lens)
     with _on(stream):
         dst = src if inplace else tuple(torch.empty_like(t) for t in src)

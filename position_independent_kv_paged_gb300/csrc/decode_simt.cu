@@ -143,7 +143,79 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
     const int start = ROPE ? a.block_starts[(size_t)r * a.max_blocks + b] : 0;
     const int nk = min(a.BS, L - b * a.BS);
     const size_t tile = ((size_t)phys * a.Hkv + g) * a.BS;
-    for (int slot = 0; slot < nk; ++slot) {
+    if constexpr (Q8 || WTS) {
+      // four keys at a time: their loads and their lane sums overlap (128 keys per request: 21 -> TT us)
+      for (int s0 = 0; s0 < nk; s0 += 4) {
+        float k[4][E], v[4][E];
+        bool ok[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int slot = min(s0 + u, nk - 1);
+          const KV* kp = kpool + (tile + slot) * D;
+          const KV* vp = vpool + (tile + slot) * D;
+          const long long pos = (long long)start + slot;
+          ok[u] = s0 + u < nk;
+          if (ok[u] && ROPE && (pos < 0 || pos >= a.max_pos)) {
+            if (lane == 0) atomicOr(a.err, kErrPosition);
+            ok[u] = false;
+          }
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            k[u][e] = ld_f(kp + lane + 32 * e) * ks;
+            v[u][e] = ld_f(vp + lane + 32 * e) * vs;
+            v[u][e] = ok[u] ? v[u][e] : 0.f;  // a masked slot may hold a NaN
+          }
+          if (ROPE) {
+            const float* row = a.cos_sin + (size_t)(ok[u] ? pos : 0) * D;
+#pragma unroll
+            for (int e = 0; e < H; ++e) {
+              const float c = __ldg(row + lane + 32 * e);
+              const float sn = __ldg(row + D / 2 + lane + 32 * e);
+              const float x = k[u][e], y = k[u][e + H];
+              k[u][e] = fmaf(x, c, -y * sn);
+              k[u][e + H] = fmaf(y, c, x * sn);
+            }
+          }
+        }
+        if (!(ok[0] || ok[1] || ok[2] || ok[3])) continue;
+#pragma unroll
+        for (int h = 0; h < MAXG; ++h) {
+          if (h < G) {
+            float dot[4], p[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              dot[u] = 0.f;
+#pragma unroll
+              for (int e = 0; e < E; ++e) dot[u] = fmaf(qr[h][e], k[u][e], dot[u]);
+            }
+            float mn = m[h];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              dot[u] = ok[u] ? warp_sum(dot[u]) * sl2 : -CUDART_INF_F;
+              mn = fmaxf(mn, dot[u]);
+            }
+            const float corr = exp2f(m[h] - mn);
+            float psum = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              p[u] = exp2f(dot[u] - mn);
+              psum += p[u];
+            }
+            l[h] = fmaf(l[h], corr, psum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              float acc = o[h][e] * corr;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) acc = fmaf(p[u], v[u][e], acc);
+              o[h][e] = acc;
+            }
+            m[h] = mn;
+            if (WTS) bsum[h] = fmaf(bsum[h], corr, psum);
+          }
+        }
+      }
+    }
+    for (int slot = 0; slot < (Q8 || WTS ? 0 : nk); ++slot) {
       const KV* kp = kpool + (tile + slot) * D;
       const KV* vp = vpool + (tile + slot) * D;
       float k[E], v[E];
@@ -151,10 +223,6 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
       for (int e = 0; e < E; ++e) {
         k[e] = ld_f(kp + lane + 32 * e);
         v[e] = ld_f(vp + lane + 32 * e);
-        if (Q8) {
-          k[e] *= ks;
-          v[e] *= vs;
-        }
       }
       if (ROPE) {
         const int pos = start + slot;
@@ -186,7 +254,6 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
 #pragma unroll
           for (int e = 0; e < E; ++e) o[h][e] = fmaf(o[h][e], corr, p * v[e]);
           m[h] = mn;
-          if (WTS) bsum[h] = fmaf(bsum[h], corr, p);
         }
       }
     }

@@ -53,6 +53,13 @@ struct Row8<__nv_bfloat16> {
   uint4 v;
   __device__ __forceinline__ void load(const void* p) { v = __ldcs(static_cast<const uint4*>(p)); }
   __device__ __forceinline__ void clear() { v = make_uint4(0u, 0u, 0u, 0u); }
+  // largest |x|, an infinity included, NaN left out
+  __device__ __forceinline__ float amax() const {
+    __nv_bfloat162 m = __habs2(pair(v.x));
+    m = __hmax2(__hmax2(m, __habs2(pair(v.y))), __hmax2(__habs2(pair(v.z)), __habs2(pair(v.w))));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+  static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t w = (i >> 1) == 0 ? v.x : (i >> 1) == 1 ? v.y : (i >> 1) == 2 ? v.z : v.w;
     return (i & 1) ? ptx::bf_hi(w) : ptx::bf_lo(w);
@@ -66,6 +73,10 @@ struct Row8<float> {
     b = __ldcs(static_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float amax() const {
+    return fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                 fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+  }
   __device__ __forceinline__ float get(int i) const {
     const float4& q = i < 4 ? a : b;
     return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
@@ -120,18 +131,23 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_q8_kernel(AppendQ8Args 
       else x[p].clear();
     }
     float amax = 0.f;
-    bool inf = false;
 #pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = fabsf(x[p].get(e));
-        inf |= y == __int_as_float(0x7f800000);
-        if (y <= 3.402823466e38f) amax = fmaxf(amax, y);  // infinities and NaN set no scale
-      }
+    for (int p = 0; p < NP; ++p) amax = fmaxf(amax, x[p].amax());
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
-    if (inf) atomicOr(a.err, kErrRange);
+    if (amax > 3.402823466e38f) {  // an infinity sets no scale: the largest finite value does
+      if (lane == 0) atomicOr(a.err, kErrRange);
+      amax = 0.f;
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = fabsf(x[p].get(e));
+          if (y <= 3.402823466e38f) amax = fmaxf(amax, y);
+        }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, o));
+    }
     float s = scale_for(amax);
     if (s0) {
       s = fmaxf(old, s);
@@ -146,18 +162,29 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_q8_kernel(AppendQ8Args 
         }
       }
     }
-    // x / s: exact as a product where s is a power of two (1 / s is one too); a caller's other scale divides
-    const bool p2 = (__float_as_int(s) & 0x7fffff) == 0;
-    const float inv = __fdiv_rn(1.f, s);
+    if ((__float_as_int(s) & 0x7fffff) == 0) {  // a power of two: x / s is the exact product with 1 / s
+      const float inv = __fdiv_rn(1.f, s);
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int i = p * RPP + sub;
-      float y[8];
+      for (int p = 0; p < NP; ++p) {
+        const int i = p * RPP + sub;
+        float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = p2 ? x[p].get(e) * inv : __fdiv_rn(x[p].get(e), s);
-      if (i < n)
+        for (int e = 0; e < 8; ++e) y[e] = x[p].get(e) * inv;
+        if (i < n)
+          *reinterpret_cast<uint2*>(pool + (s0 + i) * D + col) =
+              make_uint2(pack4(y[0], y[1], y[2], y[3]), pack4(y[4], y[5], y[6], y[7]));
+      }
+    } else {  // another scale that the caller's block had
+#pragma unroll 1
+      for (int i = sub; i < n; i += RPP) {
+        Row8<T> z;
+        z.load(src + (size_t)i * a.Hkv * D);
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = __fdiv_rn(z.get(e), s);
         *reinterpret_cast<uint2*>(pool + (s0 + i) * D + col) =
             make_uint2(pack4(y[0], y[1], y[2], y[3]), pack4(y[4], y[5], y[6], y[7]));
+      }
     }
     if (lane == 0) *scale = s;
   }

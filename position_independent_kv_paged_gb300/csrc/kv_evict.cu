@@ -7,17 +7,21 @@
 // logical starts in the table, so dropping one moves nothing in the pool and
 // re-rotates nothing: this is integer work on the tables alone.
 //
-// One CTA per request.  The score's terms are added in 64 bits and kept in 32,
-// so that their order does not show in the ranking.  The budget-th best score
-// comes from a radix selection (four passes of 8 bits over an order-preserving
-// integer image of the float), ties are cut by index, and one ordered pass
-// compacts: a kept entry only ever moves to a lower index, and each chunk is
-// read before the barrier that its writes wait for, so outputs may be the
-// inputs.  Latency-bound: a few passes over 4 to 20 bytes a block.
+// One CTA per request.  The score's terms are added with twice fp32's precision
+// (error-free sums of fp32 pairs: FP64 runs at 2 operations a cycle and SM here,
+// and took a third of the kernel) and rounded to fp32 once, so that their order
+// does not show in the ranking.  The budget-th best score comes from a radix
+// selection over an order-preserving integer image of the float (11, 11 and 10
+// bits; the images stay in shared memory while they fit), ties are cut by index,
+// and one ordered pass compacts, four blocks per thread: a kept entry only ever
+// moves to a lower index, and each chunk is read before the barrier that its
+// writes wait for, so outputs may be the inputs.  Latency-bound: a few passes
+// over 4 to 20 bytes a block.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
 #include "internal.h"
+#include "tmap.cuh"
 
 namespace minipic {
 namespace {
@@ -36,30 +40,38 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix of the flags over the CTA, and their total (every thread calls).
-__device__ __forceinline__ int scan_flags(bool f, int* warp_sums, int& total) {
+// hi + lo += x, with hi the rounded sum and lo what it lacks (Knuth's two-sum).
+__device__ __forceinline__ void add_exact(float& hi, float& lo, float x) {
+  const float s = __fadd_rn(hi, x), t = __fsub_rn(s, hi);
+  lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(x, t));
+  hi = s;
+}
+
+// Exclusive prefix of c over the CTA, and the total (every thread calls; two barriers).
+__device__ __forceinline__ int scan(int c, int* warp_sums, int& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const unsigned m = __ballot_sync(FULL, f);
-  if (lane == 0) warp_sums[w] = __popc(m);
+  int pre = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(FULL, pre, o);
+    if (lane >= o) pre += y;
+  }
+  if (lane == 31) warp_sums[w] = pre;
   __syncthreads();
   const int mine = warp_sums[lane];  // kNW == 32
-  int before = lane < w ? mine : 0, all = mine;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    before += __shfl_xor_sync(FULL, before, o);
-    all += __shfl_xor_sync(FULL, all, o);
-  }
-  total = all;
+  const int before = __reduce_add_sync(FULL, lane < w ? mine : 0);
+  total = __reduce_add_sync(FULL, mine);
   __syncthreads();
-  return before + __popc(m & ((1u << lane) - 1u));
+  return before + pre - c;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) kv_evict_kernel(EvictArgs a) {
-  static_assert(kNW == 32, "scan_flags");
-  __shared__ int hist[256];
+__global__ void __launch_bounds__(kThreads) kv_evict_kernel(EvictArgs a, int smem_keys) {
+  static_assert(kNW == 32, "scan");
+  __shared__ int hist[2048];
   __shared__ int warp_sums[kNW];
-  __shared__ int s_digit, s_left;
+  __shared__ int s_digit, s_left, s_count;
+  extern __shared__ uint32_t skeys[];  // [smem_keys]
   const int r = blockIdx.x, tid = threadIdx.x, mb = a.max_blocks;
   const size_t row = (size_t)r * mb;
   int L = a.seq_lens[r];
@@ -68,80 +80,110 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(EvictArgs a) {
     L = L < 0 ? 0 : (int)min(16LL * mb, 2147483647LL);
   }
   const int n = (int)(((long long)L + 15) >> 4);
+  const bool cut = n > a.budget;
+  const bool in_smem = n <= smem_keys;
   for (int b = tid; b < n; b += kThreads) {
-    double s = (double)a.scores[row + b] * (double)a.decay;
+    const float old = a.scores[row + b];
+    float hi = __fmul_rn(old, a.decay);
+    float lo = fabsf(hi) < 3.4e38f ? __fmaf_rn(old, a.decay, -hi) : 0.f;
     if (a.weights) {
       const T* w = static_cast<const T*>(a.weights) + (size_t)r * a.Hkv * mb + b;
-      for (int g = 0; g < a.Hkv; ++g) s += (double)to_f(w[(size_t)g * mb]);
+      for (int g0 = 0; g0 < a.Hkv; g0 += 8) {  // eight loads at a time
+        float x[8];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) x[g] = g0 + g < a.Hkv ? to_f(w[(size_t)(g0 + g) * mb]) : 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) add_exact(hi, lo, x[g]);
+      }
     }
-    a.scores_out[row + b] = (float)s;
+    const float s = fabsf(hi) < 3.4e38f ? hi + lo : hi;  // infinities and NaN have no remainder
+    a.scores_out[row + b] = s;
+    if (cut && in_smem) skeys[b] = rank_key(s);
   }
   __syncthreads();  // this CTA reads back what it wrote
   auto held = [&](int b) { return b < a.keep_first || b >= n - a.keep_last; };
-  const bool cut = n > a.budget;
-  uint32_t least = 0u;  // key of the last kept candidate
-  int ties = 0;         // candidates of that key that stay
+  auto key = [&](int b) { return in_smem ? skeys[b] : rank_key(a.scores_out[row + b]); };
+  uint32_t least = 0xffffffffu;  // image of the last kept candidate
+  int ties = 0, equal = 0;       // candidates of that image that stay, and all of them
   if (cut) {
-    int left = a.budget - min(a.keep_first, n) - min(a.keep_last, n);  // n > budget >= keep_first + keep_last
+    int left = a.budget - a.keep_first - a.keep_last;  // n > budget >= keep_first + keep_last
     uint32_t mask = 0u;
-    for (int shift = 24; shift >= 0 && left > 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kThreads) hist[i] = 0;
+    if (left > 0) least = 0u;
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && left > 0; ++pass) {
+      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), digits = pass == 2 ? 1024 : 2048;
+      for (int i = tid; i < 2048; i += kThreads) hist[i] = 0;
       __syncthreads();
       for (int b = tid; b < n; b += kThreads) {
         if (held(b)) continue;
-        const uint32_t k = rank_key(a.scores_out[row + b]);
-        if ((k & mask) == (least & mask)) atomicAdd(&hist[(k >> shift) & 255u], 1);
+        const uint32_t k = key(b);
+        if ((k & mask) == (least & mask)) atomicAdd(&hist[(k >> shift) & (digits - 1)], 1);
       }
       __syncthreads();
-      if (tid < 32) {  // lane l: digits 255 - 8 l down to 248 - 8 l
-        int c = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c += hist[255 - 8 * tid - i];
-        int pre = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(FULL, pre, o);
-          if (tid >= o) pre += y;
-        }
-        pre -= c;
-        if (pre < left && left <= pre + c) {
-          int d = 255 - 8 * tid;
-          while (pre + hist[d] < left) pre += hist[d--];
-          s_digit = d;
-          s_left = left - pre;
-        }
+      // thread t: digits 2047 - 2 t and 2046 - 2 t, so that the prefix counts from the largest
+      const int h0 = hist[2047 - 2 * tid], h1 = hist[2046 - 2 * tid];
+      int tot;
+      const int pre = scan(h0 + h1, warp_sums, tot);
+      if (pre < left && left <= pre + h0 + h1) {
+        const bool first = left <= pre + h0;
+        s_digit = first ? 2047 - 2 * tid : 2046 - 2 * tid;
+        s_left = left - pre - (first ? 0 : h0);
+        s_count = first ? h0 : h1;
       }
       __syncthreads();
       least |= (uint32_t)s_digit << shift;
       left = s_left;
-      mask |= 255u << shift;
+      equal = s_count;
+      mask |= (uint32_t)(digits - 1) << shift;
+      __syncthreads();  // read before the next pass writes them
     }
     ties = left;
-    if (a.budget - min(a.keep_first, n) - min(a.keep_last, n) <= 0) least = 0xffffffffu;
   }
-  int kept = 0, gone = 0, tied = 0;
-  for (int base = 0; base < n; base += kThreads) {
-    const int b = base + tid;
-    const bool in = b < n;
-    const float s = in ? a.scores_out[row + b] : 0.f;
-    const int phys = in ? a.block_tables[row + b] : 0, st = in ? a.block_starts[row + b] : 0;
-    const bool cand = in && cut && !held(b);
-    const uint32_t k = cand ? rank_key(s) : 0u;
-    int tot;
-    const int tr = tied + scan_flags(cand && k == least, warp_sums, tot);
-    tied += tot;
-    const bool keep = in && (!cand || k > least || (k == least && tr < ties));
-    const int kr = scan_flags(keep, warp_sums, tot);  // its barriers also order the reads above before the writes
-    if (keep) {
-      const size_t to = row + kept + kr;
-      a.scores_out[to] = s;
-      a.tables_out[to] = phys;
-      a.starts_out[to] = st;
-    } else if (in) {
-      a.evicted[row + gone + tid - kr] = phys;
+  constexpr int PER = 4;
+  int kept = 0, tied = 0;
+  for (int base = 0; base < n; base += PER * kThreads) {
+    const int b0 = base + PER * tid;
+    float sc[PER];
+    int ph[PER], st[PER];
+    uint32_t ks[PER];
+    int eq = 0;
+    unsigned keep = 0u;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = b0 + i;
+      const bool in = b < n;
+      sc[i] = in ? a.scores_out[row + b] : 0.f;
+      ph[i] = in ? a.block_tables[row + b] : 0;
+      st[i] = in ? a.block_starts[row + b] : 0;
+      ks[i] = rank_key(sc[i]);
+      const bool cand = in && cut && !held(b);
+      eq += cand && ks[i] == least;
+      keep |= (in && (!cand || ks[i] >= least) ? 1u : 0u) << i;
     }
+    int tot;
+    if (ties != equal) {  // not all of the last image's candidates stay: those of the lowest index do
+      int tr = tied + scan(eq, warp_sums, tot);
+      tied += tot;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int b = b0 + i;
+        if (b < n && cut && !held(b) && ks[i] == least && tr++ >= ties) keep &= ~(1u << i);
+      }
+    }
+    int kr = kept + scan(__popc(keep), warp_sums, tot);  // its barriers also order the reads above before the writes
     kept += tot;
-    gone += min(n - base, kThreads) - tot;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = b0 + i;
+      if ((keep >> i) & 1u) {
+        a.scores_out[row + kr] = sc[i];
+        a.tables_out[row + kr] = ph[i];
+        a.starts_out[row + kr] = st[i];
+        ++kr;
+      } else if (b < n) {
+        a.evicted[row + b - kr] = ph[i];  // b - kr blocks before this one left
+      }
+    }
   }
   __syncthreads();
   for (int b = kept + tid; b < mb; b += kThreads) {
@@ -149,19 +191,29 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(EvictArgs a) {
     a.tables_out[row + b] = -1;
     a.starts_out[row + b] = 0;
   }
-  for (int b = gone + tid; b < mb; b += kThreads) a.evicted[row + b] = -1;
+  for (int b = n - kept + tid; b < mb; b += kThreads) a.evicted[row + b] = -1;
   if (tid == 0) {
-    a.lens_out[r] = L - 16 * gone;
-    a.n_evicted[r] = gone;
+    a.lens_out[r] = L - 16 * (n - kept);
+    a.n_evicted[r] = n - kept;
   }
+}
+
+constexpr int kMaxKeys = 49152;  // images held in shared memory (192 KB)
+
+template <typename T>
+cudaError_t launch_t(const EvictArgs& a, cudaStream_t s) {
+  static bool done[64] = {false};
+  const cudaError_t e = set_smem_once(kv_evict_kernel<T>, kMaxKeys * 4, done);
+  if (e != cudaSuccess) return e;
+  const int keys = a.max_blocks < kMaxKeys ? a.max_blocks : kMaxKeys;
+  kv_evict_kernel<T><<<a.batch, kThreads, (size_t)keys * 4, s>>>(a, keys);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs& a, bool bf16, cudaStream_t s) {
-  if (bf16) kv_evict_kernel<__nv_bfloat16><<<a.batch, kThreads, 0, s>>>(a);
-  else kv_evict_kernel<float><<<a.batch, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return bf16 ? launch_t<__nv_bfloat16>(a, s) : launch_t<float>(a, s);
 }
 
 }  // namespace minipic

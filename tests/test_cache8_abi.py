@@ -161,28 +161,81 @@ def test_binding_checks_types_and_shapes(lib):
     pool = torch.zeros(4, 2, 16, 64, dtype=torch.uint8).view(torch.float8_e4m3fn)
     sc, i2, i1 = torch.ones(4, 2), torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
     q, tab = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(16, 64)
+    both, p4 = mp.RopeTable(tab, tab.half()), torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA tensor"):
-        mp.attn_decode_q8(q, pool, pool, sc, sc, i2, i2, i1, i1, tab)
+        mp.attn_decode_q8(q, pool, pool, sc, sc, i2, i2, i1, i1, both)
     with pytest.raises(ValueError, match="CUDA tensor"):
-        mp.attn_decode_weights(q, q, q, i2, i2, i1, i1, tab, q)
+        mp.attn_decode_weights(q, p4, p4, i2, i2, i1, i1, both, torch.zeros(1, 2, 4, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="CUDA tensor"):
-        mp.attn_prefill_q8(q, i1, i1, pool, pool, sc, sc, i2, i2, i1, tab, 1)
+        mp.attn_prefill_q8(q, i1, i1, pool, pool, sc, sc, i2, i2, i1, both, 1)
     with pytest.raises(ValueError, match="CUDA tensor"):
-        mp.kv_append_q8(q, q, i1, i1, i2, pool, pool, sc, sc)
+        mp.kv_append_q8(q[:, :2], q[:, :2], i1, i1, i2, pool, pool, sc, sc)
     with pytest.raises(ValueError, match="CUDA tensor"):
         mp.kv_evict(torch.zeros(1, 4), i2, i2, i1, 4)
 
 
-class FakeCuda:
-    """Stands in for a tensor on another device (the box has one GPU)."""
-
-    def __init__(self, index):
-        self.device = type("D", (), {"index": index, "__str__": lambda s: f"cuda:{index}"})()
-
-
 def test_binding_refuses_tensors_of_another_device(monkeypatch):
+    """The box has one GPU: a tensor that says it lives on the second one."""
     torch = pytest.importorskip("torch")
+
+    class Far(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    mp._current_device(FakeCuda(0), None)
-    with pytest.raises(ValueError, match="current device is cuda:0"):
-        mp._current_device(FakeCuda(0), FakeCuda(1))
+    with pytest.raises(ValueError, match="q is on cuda:1, but the current device is cuda:0"):
+        mp._args(("q", torch.zeros(2, 3).as_subclass(Far), torch.float32, (2, 3)))
+
+
+def test_binding_checks_shapes_before_the_call(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+
+    class Here(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    calls = []
+    monkeypatch.setattr(mp, "_stream", lambda s: calls.append(1))
+
+    def z(*s, dtype=torch.float32):
+        return torch.zeros(*s).to(dtype).as_subclass(Here)
+    i32, f8, bf = torch.int32, torch.float8_e4m3fn, torch.bfloat16
+    good = dict(scores=z(2, 4), block_tables=z(2, 4, dtype=i32), block_starts=z(2, 4, dtype=i32),
+                seq_lens=z(2, dtype=i32), budget=2, block_weights=z(2, 3, 4))
+    for k, bad in (("scores", z(2, 5)), ("block_tables", z(2, 4)), ("block_starts", z(3, 4, dtype=i32)),
+                   ("seq_lens", z(3, dtype=i32)), ("block_weights", z(2, 3, 5)),
+                   ("block_weights", z(2, 3, 4, dtype=torch.float16)), ("scores", z(4, 2).t())):
+        with pytest.raises((ValueError, TypeError)):
+            mp.kv_evict(**dict(good, **{k: bad}))
+    pools = dict(k_pool=z(5, 2, 16, 64, dtype=f8), v_pool=z(5, 2, 16, 64, dtype=f8), k_scale=z(5, 2), v_scale=z(5, 2))
+    dec = dict(q=z(3, 4, 64, dtype=bf), **pools, block_tables=z(3, 6, dtype=i32), block_starts=z(3, 6, dtype=i32),
+               seq_lens=z(3, dtype=i32), q_pos=z(3, dtype=i32),
+               rope=mp.RopeTable(z(32, 64), z(32, 64, dtype=torch.float16)), block_weights=z(3, 2, 6, dtype=bf))
+    for k, bad in (("q", z(3, 4, 128, dtype=bf)), ("q", z(3, 4, 64, dtype=torch.float16)),
+                   ("v_pool", z(5, 2, 16, 128, dtype=f8)), ("k_pool", z(5, 2, 16, 64)), ("k_scale", z(5, 3)),
+                   ("v_scale", z(2, 5).t()), ("block_tables", z(2, 6, dtype=i32)), ("block_starts", z(3, 5, dtype=i32)),
+                   ("seq_lens", z(4, dtype=i32)), ("q_pos", z(3)), ("rope", z(32, 64)),
+                   ("rope", mp.RopeTable(z(32, 128), z(32, 128, dtype=torch.float16))),
+                   ("block_weights", z(3, 2, 6)), ("block_weights", z(3, 2, 7, dtype=bf)), ("out", z(3, 4, 64)),
+                   ("lse", z(3, 2))):
+        with pytest.raises((ValueError, TypeError)):
+            mp.attn_decode_q8(**dict(dec, **{k: bad}))
+    app = dict(k_new=z(7, 2, 64, dtype=bf), v_new=z(7, 2, 64, dtype=bf), cu_new_lens=z(4, dtype=i32),
+               kv_start=z(3, dtype=i32), block_tables=z(3, 6, dtype=i32), **pools, max_new_len=3)
+    for k, bad in (("k_new", z(7, 3, 64, dtype=bf)), ("v_new", z(7, 2, 64)), ("cu_new_lens", z(3, dtype=i32)),
+                   ("kv_start", z(4, dtype=i32)), ("block_tables", z(2, 6, dtype=i32))):
+        with pytest.raises((ValueError, TypeError)):
+            mp.kv_append_q8(**dict(app, **{k: bad}))
+    pre = dict(q=z(7, 4, 64, dtype=bf), cu_q_lens=z(4, dtype=i32), q_pos=z(7, dtype=i32), **pools,
+               block_tables=z(3, 6, dtype=i32), block_starts=z(3, 6, dtype=i32), kv_lens=z(3, dtype=i32),
+               rope=dec["rope"], max_q_len=3)
+    for k, bad in (("q", z(7, 4, 64)), ("cu_q_lens", z(3, dtype=i32)), ("q_pos", z(6, dtype=i32)),
+                   ("kv_lens", z(2, dtype=i32)), ("rope", z(32, 64)), ("out", z(7, 4, 64))):
+        with pytest.raises((ValueError, TypeError)):
+            mp.attn_prefill_q8(**dict(pre, **{k: bad}))
+    assert not calls   # nothing got as far as a launch
