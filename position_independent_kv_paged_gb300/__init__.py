@@ -16,7 +16,6 @@ with their positions; the kernels rotate both with the cos/sin table built by
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -606,6 +605,11 @@ def _args(*specs):
         raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{dev}")
 
 
+def _any(name, t):
+    """Specs of an optional buffer of any type."""
+    return () if t is None else ((name, t, t.dtype, t.shape),)
+
+
 def _sizes(t, name, ndim):
     """The shape of the tensor that gives a call its sizes."""
     if not isinstance(t, _torch().Tensor):
@@ -626,9 +630,18 @@ def _rope16(rope, d, need_f16):
             (("rope", f32, torch.float32, (n, d)), ("rope f16", f16, torch.float16, (n, d))))
 
 
-def _on(stream):
-    """Temporaries and outputs of a call on another stream belong to that stream."""
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+def _run(stream, call):
+    """call(cuda_stream) on `stream`, the current one if None.  Temporaries and
+    outputs that the call allocates belong to the stream that uses them."""
+    torch = _torch()
+    if stream is None:
+        # the current stream's handle without a Stream object (2.8 us of a call's 30)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return call(raw(torch.cuda.current_device()) if raw else _stream(None))
+    if stream.device.index != torch.cuda.current_device():
+        raise ValueError(f"stream of {stream.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _kv_q8(k_pool, v_pool, k_scale, v_scale):
@@ -664,8 +677,8 @@ def kv_append_q8(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_po
         max_new_len = int((cu_new_lens[1:] - cu_new_lens[:-1]).max().item()) if B else 0
     ab = _Append(k_new.data_ptr(), v_new.data_ptr(), cu_new_lens.data_ptr(), kv_start.data_ptr(),
                  block_tables.data_ptr(), B, total, int(max_new_len), mb)
-    st = L.minipic_kv_append_q8(code, ctypes.byref(kv), ctypes.byref(ab), _stream(stream))
-    _check(st, "minipic_kv_append_q8")
+    _check(_run(stream, lambda s: L.minipic_kv_append_q8(code, ctypes.byref(kv), ctypes.byref(ab), s)),
+           "minipic_kv_append_q8")
 
 
 def attn_decode_q8_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -690,21 +703,20 @@ def _decode_weights(fn, where, size, q, kv, specs, block_tables, block_starts, s
     _args(("q", q, q.dtype, (B, Hq, kv.head_dim)), *specs, ("block_tables", block_tables, i32, (B, mb)),
           ("block_starts", block_starts, i32, (B, mb)), ("seq_lens", seq_lens, i32, (B,)),
           ("q_pos", q_pos, i32, (B,)), *rope_specs, ("out", out, q.dtype, shape), ("lse", lse, torch.float32, (B, Hq)),
-          ("block_weights", block_weights, q.dtype, (B, kv.num_kv_heads, mb)))
-    if workspace is not None:
-        _args(("workspace", workspace, workspace.dtype, workspace.shape))
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
+          ("block_weights", block_weights, q.dtype, (B, kv.num_kv_heads, mb)), *_any("workspace", workspace))
+
+    def call(s):
+        o = torch.empty_like(q) if out is None else out
+        ws = workspace
+        if ws is None:
             n = size(B, Hq, kv.num_kv_heads, d, mb, kv.block_size)
-            workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
+            ws = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
         db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
-                     q_pos.data_ptr(), B, mb, out.data_ptr(), _ptr(lse))
-        st = fn(code, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), float(scale), _ptr(block_weights),
-                workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream))
-        _check(st, where)
-    return out, lse
+                     q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
+        _check(fn(code, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), float(scale), _ptr(block_weights),
+                  ws.data_ptr(), ws.nbytes, s), where)
+        return o, lse
+    return _run(stream, call)
 
 
 def attn_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, seq_lens, q_pos, rope,
@@ -761,23 +773,22 @@ def attn_prefill_q8(q, cu_q_lens, q_pos, k_pool, v_pool, k_scale, v_scale, block
     _args(("q", q, torch.bfloat16, (total_q, Hq, kv.head_dim)), ("cu_q_lens", cu_q_lens, i32, (B + 1,)),
           ("q_pos", q_pos, i32, (total_q,)), *specs, ("block_tables", block_tables, i32, (B, mb)),
           ("block_starts", block_starts, i32, (B, mb)), ("kv_lens", kv_lens, i32, (B,)), *rope_specs,
-          ("out", out, torch.bfloat16, shape), ("lse", lse, torch.float32, (total_q, Hq)))
-    if workspace is not None:
-        _args(("workspace", workspace, workspace.dtype, workspace.shape))
-    with _on(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if workspace is None:
+          ("out", out, torch.bfloat16, shape), ("lse", lse, torch.float32, (total_q, Hq)),
+          *_any("workspace", workspace))
+
+    def call(s):
+        o = torch.empty_like(q) if out is None else out
+        ws = workspace
+        if ws is None:
             n = attn_prefill_q8_workspace_size(B, Hq, kv.num_kv_heads, d, max_q_len, mb, kv.block_size)
-            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
         pb = _Prefill(q.data_ptr(), cu_q_lens.data_ptr(), q_pos.data_ptr(), block_tables.data_ptr(),
-                      block_starts.data_ptr(), kv_lens.data_ptr(), B, total_q, int(max_q_len), mb, out.data_ptr(),
+                      block_starts.data_ptr(), kv_lens.data_ptr(), B, total_q, int(max_q_len), mb, o.data_ptr(),
                       _ptr(lse))
-        st = L.minipic_attn_prefill_q8(BF16, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(pb), float(scale),
-                                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                       _stream(stream))
-        _check(st, "minipic_attn_prefill_q8")
-    return out, lse
+        _check(L.minipic_attn_prefill_q8(BF16, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(pb), float(scale),
+                                         ws.data_ptr(), ws.nbytes, s), "minipic_attn_prefill_q8")
+        return o, lse
+    return _run(stream, call)
 
 
 class KVEvicted(NamedTuple):
@@ -810,13 +821,15 @@ def kv_evict(scores, block_tables, block_starts, seq_lens, budget: int, keep_fir
     _args(("scores", scores, torch.float32, shape), ("block_tables", block_tables, i32, shape),
           ("block_starts", block_starts, i32, shape), ("seq_lens", seq_lens, i32, (B,)))
     src = (scores, block_tables, block_starts, seq_lens)
-    with _on(stream):
+
+    def call(s):
         dst = src if inplace else tuple(torch.empty_like(t) for t in src)
         r = KVEvicted(*dst, torch.empty_like(block_tables), torch.empty_like(seq_lens))
-        eb = _Evict(_ptr(block_weights), *(t.data_ptr() for t in src), *(t.data_ptr() for t in r), B, mb, hkv,
+        eb = _Evict(_ptr(block_weights), *[t.data_ptr() for t in src], *[t.data_ptr() for t in r], B, mb, hkv,
                     int(budget), int(keep_first), int(keep_last), float(decay))
-        _check(L.minipic_kv_evict(code, ctypes.byref(eb), _stream(stream)), "minipic_kv_evict")
-    return r
+        _check(L.minipic_kv_evict(code, ctypes.byref(eb), s), "minipic_kv_evict")
+        return r
+    return _run(stream, call)
 
 
 # ---------------------------------------------------------------- span reuse (host)

@@ -200,7 +200,7 @@ def test_binding_checks_shapes_before_the_call(lib, monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     calls = []
-    monkeypatch.setattr(mp, "_stream", lambda s: calls.append(1))
+    monkeypatch.setattr(mp, "_run", lambda stream, call: calls.append(1))
 
     def z(*s, dtype=torch.float32):
         return torch.zeros(*s).to(dtype).as_subclass(Here)
