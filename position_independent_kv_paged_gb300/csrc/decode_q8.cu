@@ -39,6 +39,8 @@
 // meet a NaN byte).
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "tmap.cuh"
@@ -147,12 +149,11 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     tq = 0;
   }
 
-  // What a block needs: x = its (block, head) tile (-1: nothing usable), y = table row of |t - start| with the
-  // sign of the angle in bit 31.
+  // What a block needs: x = its (block, head) tile (-1: nothing usable), y = table row of |t - start|.
   auto place = [&](int phys, int start) {
     const uint32_t ad = distance(tq, start);
     const bool ok = phys >= 0 && phys < a.num_blocks && ad < (uint32_t)a.max_pos;
-    return make_int2(ok ? phys * a.Hkv + hk : -1, (int)(ad | (start > tq ? 0x80000000u : 0u)));
+    return make_int2(ok ? phys * a.Hkv + hk : -1, ok ? (int)ad : 0);
   };
   // The warp copies a pair of blocks into a stage: lane -> 16 bytes of each tile's next 512, swizzled, and of the
   // two table rows.  A block with nothing usable copies tile 0 and row 0, which its mask keeps out.
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     const int2 pr = lane < RL ? p0 : p1;
     if (lane < 2 * RL)
       ptx::cp_async16(wrow + stg * 2 * LY::ROWB + 16 * lane,
-                      rg + (size_t)(pr.x < 0 ? 0 : pr.y & 0x7fffffff) * LY::ROWB);
+                      rg + (size_t)pr.y * LY::ROWB);
   };
   {
     const int* bt = a.block_tables + (size_t)r * mb + b_begin;
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       ptx::cp_async_commit();
     }
     // per block, once for the CTA: place, score factor (softmax scale * log2 e * key scale), log2 of the value
-    // scale (finite), and the mask of its usable slots (bit 16: the values are zero)
+    // scale (finite), and the mask of its usable slots (bit 16: the values are zero, bit 17: the angle is negative)
     for (int i = threadIdx.x; i < span + 2 * NW; i += NW * 32) {
       int2 pl = make_int2(-1, 0);
       float ks = 0.f, lv = 0.f;
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
             lv = 0.f;
             m |= 0x10000u;
           }
+          if (start > tq) m |= 0x20000u;
         }
       }
       meta[i] = make_int4(pl.x, pl.y, __float_as_int(ks), __float_as_int(lv));
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   __syncthreads();  // meta visible
 
   // the rotated query words of column tile nt, R_{t - start} q, from a staged cos | sin row
-  auto rotate_q = [&](uint32_t row, int y, uint32_t (&bx)[NT][2 * NH], uint32_t (&by)[NT][2 * NH]) {
+  auto rotate_q = [&](auto plain, uint32_t row, uint32_t m, uint32_t (&bx)[NT][2 * NH], uint32_t (&by)[NT][2 * NH]) {
     uint32_t cw[2 * NH], sw[2 * NH];
 #pragma unroll
     for (int u = 0; u < NH / 2; ++u) {
@@ -304,8 +306,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       cw[4 * u] = c.x; cw[4 * u + 1] = c.y; cw[4 * u + 2] = c.z; cw[4 * u + 3] = c.w;
       sw[4 * u] = s.x; sw[4 * u + 1] = s.y; sw[4 * u + 2] = s.z; sw[4 * u + 3] = s.w;
     }
-    if (__any_sync(FULL, y < 0)) {  // a key ahead of the query: the sine takes the angle's sign
-      const uint32_t sgn = (uint32_t)(y >> 31) & 0x80008000u;
+    if constexpr (!decltype(plain)::value) {  // a key ahead of the query: the sine takes the angle's sign
+      const uint32_t sgn = m & 0x20000u ? 0x80008000u : 0u;
 #pragma unroll
       for (int e = 0; e < 2 * NH; ++e) sw[e] ^= sgn;
     }
@@ -362,11 +364,12 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[nt][e] += sy[nt][e];
   };
+  float* const w_base = WTS ? a.w_raw + ((size_t)r * a.Hkv + hk) * mb * G : nullptr;
   // one step of the online softmax over 16 keys; m, ks and lv are those of the columns' block, wb the block
   // whose sum is recorded
-  auto softmax = [&](float (&sc)[NT][4], uint32_t m, float ks, float lv, int wb, uint32_t (&pb0)[NT],
+  auto softmax = [&](auto plain, float (&sc)[NT][4], uint32_t m, float ks, float lv, int wb, uint32_t (&pb0)[NT],
                      uint32_t (&pb1)[NT]) {
-    const bool v0 = (m >> ks0) & 1u, v1 = (m >> (ks0 + 8)) & 1u;
+    const bool v0 = decltype(plain)::value || ((m >> ks0) & 1u), v1 = decltype(plain)::value || ((m >> (ks0 + 8)) & 1u);
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -417,8 +420,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
           e += __shfl_xor_sync(FULL, e, 16);
           const int head = DUAL ? (2 * tig + j) & 3 : 8 * nt + 2 * tig + j;
           if (g8 == 0 && head < G && wb < b_end)
-            a.w_raw[(((size_t)r * a.Hkv + hk) * mb + wb) * G + head] =
-                e == 0.f ? -CUDART_INF_F : ms[nt][j] + log2f(e);
+            w_base[(size_t)wb * G + head] = e == 0.f ? -CUDART_INF_F : ms[nt][j] + log2f(e);
         }
       }
       pb0[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[0], pv[1]));  // keys 0..7
@@ -427,10 +429,10 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   };
   // O^T += V^T P^T of one block, two M tiles (16-byte chunks) per read
   const int v_key = frag_slot(lane & 7) + 8 * ((lane >> 3) & 1), v_chunk = lane >> 4;
-  auto values = [&](uint32_t vbase, uint32_t m, const uint32_t (&pb0)[NT], const uint32_t (&pb1)[NT]) {
+  auto values = [&](auto plain, uint32_t vbase, uint32_t m, const uint32_t (&pb0)[NT], const uint32_t (&pb1)[NT]) {
     uint32_t klo = FULL, khi = FULL;  // which of this lane's keys (rows 2 tig, 2 tig + 1, and + 8) count
-    const bool part = m != 0xffffu;
-    if (part) {
+    constexpr bool part = !decltype(plain)::value;
+    if constexpr (part) {
       const uint32_t u = m & 0x10000u ? 0u : m >> frag_slot(2 * tig), w = m & 0x10000u ? 0u : m >> frag_slot(2 * tig + 1);
       klo = (u & 1u ? 0xffffu : 0u) | (w & 1u ? 0xffff0000u : 0u);
       khi = (u & 0x100u ? 0xffffu : 0u) | (w & 0x100u ? 0xffff0000u : 0u);
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     for (int mm = 0; mm < LY::MT; mm += 2) {
       uint32_t w[4];
       ptx::ldsm_x4_trans(vbase + at<D>(v_key, mm + v_chunk), w[0], w[1], w[2], w[3]);
-      if (part) {
+      if constexpr (part) {
         w[0] &= klo;
         w[1] &= khi;
         w[2] &= klo;
@@ -457,6 +459,35 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     }
   };
 
+  auto pair = [&](auto plain, uint32_t kbase, uint32_t rowb, int i0, uint32_t m0, uint32_t m1) {
+    uint32_t bx[NT][2 * NH], by[NT][2 * NH], pb0[NT], pb1[NT];
+    float sc[NT][4];
+    if constexpr (DUAL) {
+      const int4 mc = meta[i0 + (tig >= 2 ? NW : 0)];  // of these score columns' block
+      rotate_q(plain, rowb + (g8 >= 4 ? LY::ROWB : 0), g8 >= 4 ? m1 : m0, bx, by);
+      float s1[NT][4];
+      scores(kbase, bx, by, sc);
+      scores(kbase + 2 * LY::TILE, bx, by, s1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[0][e] = tig >= 2 ? s1[0][e] : sc[0][e];
+      softmax(plain, sc, tig >= 2 ? m1 : m0, __int_as_float(mc.z), __int_as_float(mc.w),
+              b_begin + i0 + (tig >= 2 ? NW : 0), pb0, pb1);
+      const uint32_t z0[1] = {g8 < 4 ? pb0[0] : 0u}, z1[1] = {g8 < 4 ? pb1[0] : 0u};
+      const uint32_t y0[1] = {g8 < 4 ? 0u : pb0[0]}, y1[1] = {g8 < 4 ? 0u : pb1[0]};
+      values(plain, kbase + LY::TILE, m0, z0, z1);
+      values(plain, kbase + 3 * LY::TILE, m1, y0, y1);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int4 md = meta[i0 + u * NW];
+        const uint32_t m = u ? m1 : m0;
+        rotate_q(plain, rowb + u * LY::ROWB, m, bx, by);
+        scores(kbase + 2 * u * LY::TILE, bx, by, sc);
+        softmax(plain, sc, m, __int_as_float(md.z), __int_as_float(md.w), b_begin + i0 + u * NW, pb0, pb1);
+        values(plain, kbase + (2 * u + 1) * LY::TILE, m, pb0, pb1);
+      }
+    }
+  };
   // one pair from stage `stg` (a compile-time constant: every shared address is a per-thread base and an immediate)
   auto step = [&](const int stg, const int p) {
     const int i0 = warp + 2 * NW * p;  // blocks i0 and i0 + NW of the split
@@ -464,34 +495,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     const uint32_t m0 = vmask[i0], m1 = vmask[i0 + NW];
     ptx::cp_async_wait<NS - 1>();
     __syncwarp();  // every lane's part of the stage has landed
-    uint32_t bx[NT][2 * NH], by[NT][2 * NH], pb0[NT], pb1[NT];
-    float sc[NT][4];
-    if constexpr (DUAL) {
-      const int mq = meta[i0 + (g8 >= 4 ? NW : 0)].y;   // of this query column's block
-      const int4 mc = meta[i0 + (tig >= 2 ? NW : 0)];   // of these score columns' block
-      rotate_q(rowb + (g8 >= 4 ? LY::ROWB : 0), mq, bx, by);
-      float s1[NT][4];
-      scores(kbase, bx, by, sc);
-      scores(kbase + 2 * LY::TILE, bx, by, s1);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sc[0][e] = tig >= 2 ? s1[0][e] : sc[0][e];
-      softmax(sc, tig >= 2 ? m1 : m0, __int_as_float(mc.z), __int_as_float(mc.w),
-              b_begin + i0 + (tig >= 2 ? NW : 0), pb0, pb1);
-      const uint32_t z0[1] = {g8 < 4 ? pb0[0] : 0u}, z1[1] = {g8 < 4 ? pb1[0] : 0u};
-      const uint32_t y0[1] = {g8 < 4 ? 0u : pb0[0]}, y1[1] = {g8 < 4 ? 0u : pb1[0]};
-      values(kbase + LY::TILE, m0, z0, z1);
-      values(kbase + 3 * LY::TILE, m1, y0, y1);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int4 md = meta[i0 + u * NW];
-        const uint32_t m = u ? m1 : m0;
-        rotate_q(rowb + u * LY::ROWB, md.y, bx, by);
-        scores(kbase + 2 * u * LY::TILE, bx, by, sc);
-        softmax(sc, m, __int_as_float(md.z), __int_as_float(md.w), b_begin + i0 + u * NW, pb0, pb1);
-        values(kbase + (2 * u + 1) * LY::TILE, m, pb0, pb1);
-      }
-    }
+    // both blocks whole and behind the query: no masks, no signs
+    if (m0 == 0xffffu && m1 == 0xffffu) pair(std::true_type{}, kbase, rowb, i0, m0, m1);
+    else pair(std::false_type{}, kbase, rowb, i0, m0, m1);
     __syncwarp();  // every lane has read the stage
     if (p + NS < npair) {
       const int n0 = i0 + 2 * NW * NS;
@@ -618,7 +624,8 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
 template <int D, bool WTS>
 cudaError_t launch_d(const DecodeArgs& a, cudaStream_t s) {
   if (a.G > 8) return launch_t<D, 2, false, WTS, 2, 2>(a, s);
-  return a.G > 4 ? launch_t<D, 1, false, WTS, 2, 3>(a, s) : launch_t<D, 1, true, WTS, 2, 3>(a, s);
+  constexpr int CPS = D == 64 ? 4 : 3;
+  return a.G > 4 ? launch_t<D, 1, false, WTS, 2, CPS>(a, s) : launch_t<D, 1, true, WTS, 2, CPS>(a, s);
 }
 
 }  // namespace
