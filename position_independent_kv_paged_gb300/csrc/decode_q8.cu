@@ -8,9 +8,8 @@
 // Work: one CTA = (split, kv head, request); each of its warps owns every NW-th
 // 16-key block of the split, two at a time, and runs its own ring of stages.  A
 // (block, head) tile is 16 d contiguous bytes, lines of 128 bytes (one key at d
-// 128, two at d 64) whose 16-byte chunks are stored at chunk ^ (line mod 8), so
-// that the key-row reads and the transposing reads of V are free of bank
-// conflicts.  The fp16 cos | sin row of the block's query rotation comes with
+// 128, two at d 64) whose 16-byte chunks are stored permuted (mix below), so that
+// the key-row reads and the transposing reads of V are free of bank conflicts.  The fp16 cos | sin row of the block's query rotation comes with
 // them.  The copies are cp.async of the whole warp (18 instructions for a pair of
 // blocks at d 128): one thread issuing tensor copies took about 120 issue slots
 // per pair, a quarter of the kernel's, and the kernel is bound by issue.
@@ -31,9 +30,9 @@
 //    where they matter, and a weight 2^-31 of the largest is still above zero),
 //    the denominator 2^(s - ms) in fp32.  Both references move only when a value
 //    exceeds them by more than 2^8 (P then is below 2^15).
-//  - A V fragment is widened from one transposing 16-bit read: its byte pairs
-//    are two head dims of a key, so the even and odd dims become two rows of
-//    the same M tile.
+//  - V fragments come from transposing byte reads: a register holds a head dim of
+//    four consecutive keys, whose pairs widen straight into the operand; the
+//    fragment rows of the scores are numbered to match.
 // Slots past the request's length, blocks with a bad id, keys past the table and
 // zero-scale values are masked in the scores and cleared in V (P = 0 must not
 // meet a NaN byte).
@@ -77,15 +76,22 @@ struct Lay {
   static_assert(MERGE <= TOTAL, "the merge overlays what the loop no longer reads");
 };
 
-// Slot held by MMA fragment row g (row g + 8 holds slot + 8): rows read together by a quarter warp differ in bit 2.
-__device__ __forceinline__ int frag_slot(int g) { return (g >> 1) | ((g & 1) << 2); }
+// Slot held by MMA fragment row g < 8 (row g + 8 holds slot + 2): rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are the four
+// consecutive keys that lane t's transposing read of V brings.
+__device__ __forceinline__ int frag_slot(int g) { return (g >> 1) * 4 + (g & 1); }
 
-// Byte offset of 16-byte chunk c of key `key` in a swizzled tile.
+// Chunk c of 128-byte line `line` of a tile is stored at chunk c ^ mix(line).  Eight consecutive keys' equal chunks
+// (V) and two rows 2 t, 2 t + 1 times four chunks (K) then lie in different banks.
+template <int D>
+__host__ __device__ constexpr int mix(int line) {
+  return D == 128 ? ((line & 1) << 2) | ((line >> 1) & 3) : line & 7;
+}
+// Byte offset of 16-byte chunk c of key `key`.
 template <int D>
 __device__ __forceinline__ uint32_t at(int key, int c) {
-  if constexpr (D == 128) return (uint32_t)(key * 128 + ((c ^ (key & 7)) << 4));
-  const int line = key >> 1;
-  return (uint32_t)(line * 128 + ((((key & 1) * 4 + c) ^ (line & 7)) << 4));
+  const int line = D == 128 ? key : key >> 1;
+  const int ch = D == 128 ? c : (key & 1) * 4 + c;
+  return (uint32_t)(line * 128 + ((ch ^ mix<D>(line)) << 4));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -158,7 +164,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   // The warp copies a pair of blocks into a stage: lane -> 16 bytes of each tile's next 512, swizzled, and of the
   // two table rows.  A block with nothing usable copies tile 0 and row 0, which its mask keeps out.
   const uint32_t wbase = sbase + warp * NS * LY::STAGE, wrow = sbase + LY::ROWS + warp * NS * 2 * LY::ROWB;
-  const uint32_t sw0 = (uint32_t)((lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4));  // lines 0-3; 4-7: ^ 64
+  const uint32_t sw0 = (uint32_t)((lane >> 3) * 128 + (((lane & 7) ^ mix<D>(lane >> 3)) << 4));  // lines 0-3
+  constexpr uint32_t kOdd = mix<D>(4) << 4;                                                     // lines 4-7: ^ this
   const uint8_t* kg = static_cast<const uint8_t*>(a.k_pool) + 16 * lane;
   const uint8_t* vg = static_cast<const uint8_t*>(a.v_pool) + 16 * lane;
   constexpr int RL = LY::ROWB / 16;  // lanes of a table row
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       const size_t tile = (size_t)max(u ? p1.x : p0.x, 0) * LY::TILE;
 #pragma unroll
       for (int i = 0; i < LY::TILE / 512; ++i) {
-        const uint32_t to = dst + 2 * u * LY::TILE + 512 * i + (i & 1 ? sw0 ^ 64u : sw0);
+        const uint32_t to = dst + 2 * u * LY::TILE + 512 * i + (i & 1 ? sw0 ^ kOdd : sw0);
         ptx::cp_async16(to, kg + tile + 512 * i);
         ptx::cp_async16(to + LY::TILE, vg + tile + 512 * i);
       }
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     }
   }
 
-  // this thread's key rows (slots ks0, ks0 + 8) and rotary pairs (f0 .. f0 + 4 NH - 1 with + d/2)
+  // this thread's key rows (slots ks0, ks0 + 2) and rotary pairs (f0 .. f0 + 4 NH - 1 with + d/2)
   const int ks0 = frag_slot(g8);
   const int f0 = 4 * NH * tig;
 
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   uint32_t rc[2][2 * NH], rs[2][2 * NH];
 #pragma unroll
   for (int row = 0; row < 2; ++row) {
-    const uint16_t* t = a.cs_f16 + (size_t)min(ks0 + 8 * row, a.max_pos - 1) * D + f0;
+    const uint16_t* t = a.cs_f16 + (size_t)min(ks0 + 2 * row, a.max_pos - 1) * D + f0;
 #pragma unroll
     for (int u = 0; u < NH / 2; ++u) {
       const uint4 c = __ldg(reinterpret_cast<const uint4*>(t) + u), sn = __ldg(reinterpret_cast<const uint4*>(t + D / 2) + u);
@@ -323,13 +330,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
 #pragma unroll
     for (int row = 0; row < 2; ++row) {
       if constexpr (D == 128) {
-        const U4 x = ptx::lds128(kbase + at<D>(ks0 + 8 * row, tig));
-        const U4 y = ptx::lds128(kbase + at<D>(ks0 + 8 * row, tig + 4));
+        const U4 x = ptx::lds128(kbase + at<D>(ks0 + 2 * row, tig));
+        const U4 y = ptx::lds128(kbase + at<D>(ks0 + 2 * row, tig + 4));
         kx[row][0] = x.x; kx[row][1] = x.y; kx[row][2] = x.z; kx[row][3] = x.w;
         ky[row][0] = y.x; ky[row][1] = y.y; ky[row][2] = y.z; ky[row][3] = y.w;
       } else {
-        const uint2 x = ptx::lds64(kbase + at<D>(ks0 + 8 * row, tig >> 1) + 8 * (tig & 1));
-        const uint2 y = ptx::lds64(kbase + at<D>(ks0 + 8 * row, 2 + (tig >> 1)) + 8 * (tig & 1));
+        const uint2 x = ptx::lds64(kbase + at<D>(ks0 + 2 * row, tig >> 1) + 8 * (tig & 1));
+        const uint2 y = ptx::lds64(kbase + at<D>(ks0 + 2 * row, 2 + (tig >> 1)) + 8 * (tig & 1));
         kx[row][0] = x.x; kx[row][1] = x.y;
         ky[row][0] = y.x; ky[row][1] = y.y;
       }
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   // whose sum is recorded
   auto softmax = [&](auto plain, float (&sc)[NT][4], uint32_t m, float ks, float lv, int wb, uint32_t (&pb0)[NT],
                      uint32_t (&pb1)[NT]) {
-    const bool v0 = decltype(plain)::value || ((m >> ks0) & 1u), v1 = decltype(plain)::value || ((m >> (ks0 + 8)) & 1u);
+    const bool v0 = decltype(plain)::value || ((m >> ks0) & 1u), v1 = decltype(plain)::value || ((m >> (ks0 + 2)) & 1u);
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -404,7 +411,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float pv[4];
+      float pv[4], es[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         // P = e * 2^(ms - mt + lv + 7); the cap only meets scores whose e is 0
@@ -412,47 +419,42 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
         const float ea = ex2(sc[nt][j] - ms[nt][j]), eb = ex2(sc[nt][2 + j] - ms[nt][j]);
         pv[j] = ea * w;
         pv[2 + j] = eb * w;
-        float e = ea + eb;
-        l[nt][j] += e;
-        if constexpr (WTS) {
-          e += __shfl_xor_sync(FULL, e, 4);
-          e += __shfl_xor_sync(FULL, e, 8);
-          e += __shfl_xor_sync(FULL, e, 16);
-          const int head = DUAL ? (2 * tig + j) & 3 : 8 * nt + 2 * tig + j;
-          if (g8 == 0 && head < G && wb < b_end)
-            w_base[(size_t)wb * G + head] = e == 0.f ? -CUDART_INF_F : ms[nt][j] + log2f(e);
-        }
+        es[j] = ea + eb;
+        l[nt][j] += es[j];
       }
-      pb0[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[0], pv[1]));  // keys 0..7
-      pb1[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[2], pv[3]));  // keys 8..15
+      if constexpr (WTS) {
+        // the block's sum of each column over the fragment rows: the first step leaves even rows with column 0 and
+        // odd rows with column 1, so two columns take three shuffles
+        const bool odd = g8 & 1;
+        float e = (odd ? es[1] : es[0]) + __shfl_xor_sync(FULL, odd ? es[0] : es[1], 4);
+        e += __shfl_xor_sync(FULL, e, 8);
+        e += __shfl_xor_sync(FULL, e, 16);
+        const int head = DUAL ? (2 * tig + g8) & 3 : 8 * nt + 2 * tig + g8;
+        if (g8 < 2 && head < G && wb < b_end)
+          w_base[(size_t)wb * G + head] = e == 0.f ? -CUDART_INF_F : (odd ? ms[nt][1] : ms[nt][0]) + log2f(e);
+      }
+      pb0[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[0], pv[1]));  // fragment rows 0 .. 7
+      pb1[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[2], pv[3]));  // rows 8 .. 15
     }
   };
   // O^T += V^T P^T of one block, two M tiles (16-byte chunks) per read
-  const int v_key = frag_slot(lane & 7) + 8 * ((lane >> 3) & 1), v_chunk = lane >> 4;
+  const int v_key = lane & 15, v_chunk = lane >> 4;
   auto values = [&](auto plain, uint32_t vbase, uint32_t m, const uint32_t (&pb0)[NT], const uint32_t (&pb1)[NT]) {
-    uint32_t klo = FULL, khi = FULL;  // which of this lane's keys (rows 2 tig, 2 tig + 1, and + 8) count
     constexpr bool part = !decltype(plain)::value;
+    uint32_t use = FULL;  // which of this lane's four keys count, as bytes
     if constexpr (part) {
-      const uint32_t u = m & 0x10000u ? 0u : m >> frag_slot(2 * tig), w = m & 0x10000u ? 0u : m >> frag_slot(2 * tig + 1);
-      klo = (u & 1u ? 0xffffu : 0u) | (w & 1u ? 0xffff0000u : 0u);
-      khi = (u & 0x100u ? 0xffffu : 0u) | (w & 0x100u ? 0xffff0000u : 0u);
+      const uint32_t u = m & 0x10000u ? 0u : m >> (4 * tig);
+      use = (u & 1u ? 0xffu : 0u) | (u & 2u ? 0xff00u : 0u) | (u & 4u ? 0xff0000u : 0u) | (u & 8u ? 0xff000000u : 0u);
     }
 #pragma unroll
     for (int mm = 0; mm < LY::MT; mm += 2) {
       uint32_t w[4];
-      ptx::ldsm_x4_trans(vbase + at<D>(v_key, mm + v_chunk), w[0], w[1], w[2], w[3]);
-      if constexpr (part) {
-        w[0] &= klo;
-        w[1] &= khi;
-        w[2] &= klo;
-        w[3] &= khi;
-      }
+      ptx::ldsm_b8_trans_x2(vbase + at<D>(v_key, mm + v_chunk), w[0], w[1], w[2], w[3]);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        // bytes (key 0: dims 0, 1; key 1: dims 0, 1) -> dim 0 of both keys, dim 1 of both keys
+      for (int u = 0; u < 2; ++u) {  // head dims 16 (mm + u) + g8 and + 8
         uint32_t a0, a1, a2, a3;
-        ptx::e4m3x4_to_h2(__byte_perm(w[2 * u], 0u, 0x3120), a0, a1);
-        ptx::e4m3x4_to_h2(__byte_perm(w[2 * u + 1], 0u, 0x3120), a2, a3);
+        ptx::e4m3x4_to_h2(part ? w[2 * u] & use : w[2 * u], a0, a2);
+        ptx::e4m3x4_to_h2(part ? w[2 * u + 1] & use : w[2 * u + 1], a1, a3);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) ptx::mma_f16_16816(oacc[mm + u][nt], a0, a1, a2, a3, pb0[nt], pb1[nt]);
       }
@@ -533,8 +535,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
         }
 #pragma unroll
         for (int m = 0; m < LY::MT; ++m) {
-          float2 o = make_float2(oacc[m][nt][j], oacc[m][nt][2 + j]);
-          *reinterpret_cast<float2*>(w + 48 + head * LY::OST + 16 * m + 2 * g8) = o;
+          w[48 + head * LY::OST + 16 * m + g8] = oacc[m][nt][j];
+          w[48 + head * LY::OST + 16 * m + g8 + 8] = oacc[m][nt][2 + j];
         }
       }
   }

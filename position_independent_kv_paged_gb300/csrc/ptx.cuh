@@ -205,6 +205,15 @@ __device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t& r0, uint3
                : "r"(addr)
                : "memory");
 }
+// Two 16 x 16 byte matrices, transposed: lanes 0-15 and 16-31 give the addresses of their 16-byte rows.  With
+// lane = 4 g + t, r0 / r2 hold bytes (rows 4 t .. 4 t + 3) of column g of the first / second, r1 / r3 of column g + 8.
+__device__ __forceinline__ void ldsm_b8_trans_x2(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
+                                                 uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
