@@ -135,7 +135,60 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   const int g8 = lane >> 2, tig = lane & 3;
   const int G = a.G, mb = a.max_blocks;
 
+  // Every load that depends on nothing comes first, so that a CTA's start costs about two round trips to memory
+  // (ids, then scales): the table entries of this warp's first pairs and of the staging below (bounded by the
+  // table's width, whatever the length), the slot rotations and the query.
+  const int b_begin = split * a.split_blocks;
+  const int* bt = a.block_tables + (size_t)r * mb + b_begin;
+  const int* bs = a.block_starts + (size_t)r * mb + b_begin;
+  const int tab = min(a.split_blocks, mb - b_begin);  // entries of this split that the table has
   int L = a.seq_lens[r];
+  int tq = a.q_pos[r];
+  int e_phys = -1, e_start = 0;  // lane 2 p + u: block u of this warp's pair p
+  if (lane < 2 * NS && warp + NW * lane < tab) {
+    e_phys = __ldg(bt + warp + NW * lane);
+    e_start = __ldg(bs + warp + NW * lane);
+  }
+  constexpr int kPer = kMaxSplit / (NW * 32);  // staged entries of a thread
+  int t_phys[kPer], t_start[kPer];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int i = threadIdx.x + u * NW * 32;
+    t_phys[u] = i < tab ? __ldg(bt + i) : -1;
+    t_start[u] = i < tab ? __ldg(bs + i) : 0;
+  }
+
+  // this thread's key rows (slots ks0, ks0 + 2) and rotary pairs (f0 .. f0 + 4 NH - 1 with + d/2)
+  const int ks0 = frag_slot(g8);
+  const int f0 = 4 * NH * tig;
+  // R_slot of both rows, fp16 (a slot past a table of fewer rows is masked)
+  uint32_t rc[2][2 * NH], rs[2][2 * NH];
+#pragma unroll
+  for (int row = 0; row < 2; ++row) {
+    const uint16_t* t = a.cs_f16 + (size_t)min(ks0 + 2 * row, a.max_pos - 1) * D + f0;
+#pragma unroll
+    for (int u = 0; u < NH / 2; ++u) {
+      const uint4 c = __ldg(reinterpret_cast<const uint4*>(t) + u), sn = __ldg(reinterpret_cast<const uint4*>(t + D / 2) + u);
+      rc[row][4 * u] = c.x; rc[row][4 * u + 1] = c.y; rc[row][4 * u + 2] = c.z; rc[row][4 * u + 3] = c.w;
+      rs[row][4 * u] = sn.x; rs[row][4 * u + 1] = sn.y; rs[row][4 * u + 2] = sn.z; rs[row][4 * u + 3] = sn.w;
+    }
+  }
+  // unrotated queries of this thread's heads (column g8 + 8 nt)
+  uint32_t qx[NT][2 * NH], qy[NT][2 * NH];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int head = DUAL ? (g8 & 3) : 8 * nt + g8;
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)r * a.Hq + (size_t)hk * G + head) * D + f0;
+#pragma unroll
+    for (int u = 0; u < NH / 2; ++u) {
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 x = head < G ? __ldg(reinterpret_cast<const uint4*>(p) + u) : z;
+      const uint4 y = head < G ? __ldg(reinterpret_cast<const uint4*>(p + D / 2) + u) : z;
+      qx[nt][4 * u] = x.x; qx[nt][4 * u + 1] = x.y; qx[nt][4 * u + 2] = x.z; qx[nt][4 * u + 3] = x.w;
+      qy[nt][4 * u] = y.x; qy[nt][4 * u + 1] = y.y; qy[nt][4 * u + 2] = y.z; qy[nt][4 * u + 3] = y.w;
+    }
+  }
+
   const int Lmax = (int)min((long long)mb * 16, 2147483632LL);
   if (L < 0 || L > Lmax) {
     if (threadIdx.x == 0 && split == 0) atomicOr(a.err, kErrSeqLen);
@@ -144,12 +197,10 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   const int nblk = (int)(((long long)L + 15) >> 4);
   const int n_valid = max(1, (nblk + a.split_blocks - 1) / a.split_blocks);
   if (split >= n_valid) return;
-  const int b_begin = split * a.split_blocks;
   const int b_end = min(nblk, b_begin + a.split_blocks);
   const int span = b_end - b_begin;
   const int nmine = span > warp ? (span - warp + NW - 1) / NW : 0;  // blocks of this warp
   const int npair = (nmine + 1) >> 1;
-  int tq = a.q_pos[r];
   if (tq < 0 || tq >= a.max_pos) {
     if (threadIdx.x == 0 && split == 0) atomicOr(a.err, kErrPosition);
     tq = 0;
@@ -187,27 +238,33 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       ptx::cp_async16(wrow + stg * 2 * LY::ROWB + 16 * lane,
                       rg + (size_t)pr.y * LY::ROWB);
   };
-  {
-    const int* bt = a.block_tables + (size_t)r * mb + b_begin;
-    const int* bs = a.block_starts + (size_t)r * mb + b_begin;
-    // the first copies start at once, from the tables in global memory
+  // the first copies start at once
 #pragma unroll
-    for (int p = 0; p < NS; ++p) {
-      const int i0 = warp + 2 * NW * p, i1 = i0 + NW;
-      if (p < npair) {
-        const int2 p0 = place(__ldg(bt + i0), __ldg(bs + i0));
-        issue(p, p0, i1 < span ? place(__ldg(bt + i1), __ldg(bs + i1)) : make_int2(-1, 0));
-      }
-      ptx::cp_async_commit();
+  for (int p = 0; p < NS; ++p) {
+    const int2 p0 = place(__shfl_sync(FULL, e_phys, 2 * p), __shfl_sync(FULL, e_start, 2 * p));
+    const int2 p1 = place(__shfl_sync(FULL, e_phys, 2 * p + 1), __shfl_sync(FULL, e_start, 2 * p + 1));
+    if (p < npair) issue(p, p0, warp + NW * (2 * p + 1) < span ? p1 : make_int2(-1, 0));
+    ptx::cp_async_commit();
+  }
+  // per block, once for the CTA: place, score factor (softmax scale * log2 e * key scale), log2 of the value
+  // scale (finite), and the mask of its usable slots (bit 16: the values are zero, bit 17: the angle is negative)
+  {
+    float t_ks[kPer], t_vs[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int i = threadIdx.x + u * NW * 32;
+      const bool in = i < span && t_phys[u] >= 0 && t_phys[u] < a.num_blocks;
+      t_ks[u] = in ? __ldg(a.k_scale + (size_t)t_phys[u] * a.Hkv + hk) : 0.f;
+      t_vs[u] = in ? __ldg(a.v_scale + (size_t)t_phys[u] * a.Hkv + hk) : 0.f;
     }
-    // per block, once for the CTA: place, score factor (softmax scale * log2 e * key scale), log2 of the value
-    // scale (finite), and the mask of its usable slots (bit 16: the values are zero, bit 17: the angle is negative)
-    for (int i = threadIdx.x; i < span + 2 * NW; i += NW * 32) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int i = threadIdx.x + u * NW * 32;
       int2 pl = make_int2(-1, 0);
       float ks = 0.f, lv = 0.f;
       uint32_t m = 0u;
       if (i < span) {
-        const int phys = __ldg(bt + i), start = __ldg(bs + i);
+        const int phys = t_phys[u], start = t_start[u];
         pl = place(phys, start);
         const int nk = min(16, L - (b_begin + i) * 16);
         if (phys < 0 || phys >= a.num_blocks) {
@@ -221,8 +278,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
           else if (start > a.max_pos - nk) m &= (1u << (a.max_pos - start)) - 1u;
           if (a.max_pos < 16) m &= (1u << a.max_pos) - 1u;  // R_slot reaches as far as the table
           if (m != all) atomicOr(a.err, kErrPosition);
-          ks = __ldg(a.k_scale + (size_t)phys * a.Hkv + hk) * (a.scale * kLog2e);
-          lv = log2f(__ldg(a.v_scale + (size_t)phys * a.Hkv + hk));
+          ks = t_ks[u] * (a.scale * kLog2e);
+          lv = log2f(t_vs[u]);
           if (lv < kMinLog) {  // scale 0, or below what is told apart from it
             lv = 0.f;
             m |= 0x10000u;
@@ -233,42 +290,21 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       meta[i] = make_int4(pl.x, pl.y, __float_as_int(ks), __float_as_int(lv));
       vmask[i] = m;
     }
-  }
-
-  // this thread's key rows (slots ks0, ks0 + 2) and rotary pairs (f0 .. f0 + 4 NH - 1 with + d/2)
-  const int ks0 = frag_slot(g8);
-  const int f0 = 4 * NH * tig;
-
-  // R_slot of both rows, fp16 (a slot past a table of fewer rows is masked)
-  uint32_t rc[2][2 * NH], rs[2][2 * NH];
-#pragma unroll
-  for (int row = 0; row < 2; ++row) {
-    const uint16_t* t = a.cs_f16 + (size_t)min(ks0 + 2 * row, a.max_pos - 1) * D + f0;
-#pragma unroll
-    for (int u = 0; u < NH / 2; ++u) {
-      const uint4 c = __ldg(reinterpret_cast<const uint4*>(t) + u), sn = __ldg(reinterpret_cast<const uint4*>(t + D / 2) + u);
-      rc[row][4 * u] = c.x; rc[row][4 * u + 1] = c.y; rc[row][4 * u + 2] = c.z; rc[row][4 * u + 3] = c.w;
-      rs[row][4 * u] = sn.x; rs[row][4 * u + 1] = sn.y; rs[row][4 * u + 2] = sn.z; rs[row][4 * u + 3] = sn.w;
+    if (threadIdx.x < 2 * NW) {  // pairs of a full split reach past its last entry
+      meta[kMaxSplit + threadIdx.x] = make_int4(-1, 0, 0, 0);
+      vmask[kMaxSplit + threadIdx.x] = 0u;
     }
   }
 
-  // unrotated queries of this thread's heads (column g8 + 8 nt), scaled to fp16, and the power of two taken out
-  // of the heads of its score columns (2 tig + j + 8 nt)
-  uint32_t qx[NT][2 * NH], qy[NT][2 * NH];
+  // the queries scaled to fp16, and the power of two taken out of the heads of the score columns (2 tig + j + 8 nt)
   float qf[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int head = DUAL ? (g8 & 3) : 8 * nt + g8;
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)r * a.Hq + (size_t)hk * G + head) * D + f0;
-    uint32_t wx[2 * NH], wy[2 * NH];
     float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2 * NH; ++e) {
-      wx[e] = head < G ? __ldg(reinterpret_cast<const uint32_t*>(p) + e) : 0u;
-      wy[e] = head < G ? __ldg(reinterpret_cast<const uint32_t*>(p + D / 2) + e) : 0u;
-      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(ptx::bf_lo(wx[e])), fabsf(ptx::bf_hi(wx[e]))),
-                               fmaxf(fabsf(ptx::bf_lo(wy[e])), fabsf(ptx::bf_hi(wy[e])))));
-    }
+    for (int e = 0; e < 2 * NH; ++e)
+      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(ptx::bf_lo(qx[nt][e])), fabsf(ptx::bf_hi(qx[nt][e]))),
+                               fmaxf(fabsf(ptx::bf_lo(qy[nt][e])), fabsf(ptx::bf_hi(qy[nt][e])))));
     amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 2));
     // exponent of the largest element (at most 127, an infinity's; a row of zeros or subnormals takes -126)
@@ -277,8 +313,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     const float down = __int_as_float((127 - ex) << 23);
 #pragma unroll
     for (int e = 0; e < 2 * NH; ++e) {
-      qx[nt][e] = ptx::pack_f16(ptx::bf_lo(wx[e]) * down, ptx::bf_hi(wx[e]) * down);
-      qy[nt][e] = ptx::pack_f16(ptx::bf_lo(wy[e]) * down, ptx::bf_hi(wy[e]) * down);
+      qx[nt][e] = ptx::pack_f16(ptx::bf_lo(qx[nt][e]) * down, ptx::bf_hi(qx[nt][e]) * down);
+      qy[nt][e] = ptx::pack_f16(ptx::bf_lo(qy[nt][e]) * down, ptx::bf_hi(qy[nt][e]) * down);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -479,7 +515,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       values(plain, kbase + LY::TILE, m0, z0, z1);
       values(plain, kbase + 3 * LY::TILE, m1, y0, y1);
     } else {
-#pragma unroll
+#pragma unroll 1
       for (int u = 0; u < 2; ++u) {
         const int4 md = meta[i0 + u * NW];
         const uint32_t m = u ? m1 : m0;
