@@ -169,12 +169,21 @@ minipic_status build_decode(minipic_dtype dtype, int32_t num_q_heads, const mini
   return MINIPIC_OK;
 }
 
+// Partial results of an e4m3 or block-weight decode, one head each: two per CTA of the e4m3 tensor-core kernel's
+// grid, else one per split and query head.
+long long count_partials(const DecodePlan& p, bool q8, int batch, int Hq, int G) {
+  if (q8 && p.use_mma) return 2LL * p.n_split * G;
+  return p.n_split > 1 ? (long long)batch * Hq * p.n_split : 0;
+}
+
 // Place the workspace of an e4m3 or block-weight decode.
-minipic_status place_weights_ws(DecodeArgs& a, void* block_weights, void* workspace, size_t workspace_bytes) {
-  const DecodeWsW w = decode_ws_weights(a.batch, a.Hq, a.Hkv, a.D, a.n_split, block_weights ? a.max_blocks : 0);
+minipic_status place_weights_ws(DecodeArgs& a, const DecodePlan& plan, void* block_weights, void* workspace,
+                                size_t workspace_bytes) {
+  const long long partials = count_partials(plan, a.k_scale != nullptr, a.batch, a.Hq, a.G);
+  const DecodeWsW w = decode_ws_weights(a.batch, a.Hq, a.Hkv, a.D, partials, block_weights ? a.max_blocks : 0);
   if (w.total > 0 && (!workspace || workspace_bytes < w.total || !aligned16(workspace))) return MINIPIC_ERR_WORKSPACE;
   char* p = static_cast<char*>(workspace);
-  if (a.n_split > 1) {
+  if (partials > 0) {
     a.counters = reinterpret_cast<int*>(p);
     a.part_o = reinterpret_cast<float*>(p + w.cnt_bytes);
     a.part_ml = reinterpret_cast<float*>(p + w.cnt_bytes + w.o_bytes);
@@ -323,13 +332,13 @@ DecodeWs decode_ws_layout(int batch, int Hq, int Hkv, int D, int n_split) {
   return w;
 }
 
-DecodeWsW decode_ws_weights(int batch, int Hq, int Hkv, int D, int n_split, int max_blocks) {
+DecodeWsW decode_ws_weights(int batch, int Hq, int Hkv, int D, long long partials, int max_blocks) {
   DecodeWsW w{0, 0, 0, 0, 0, 0};
-  if (n_split > 1) {
+  if (partials > 0) {
     const size_t cnt = align_up((size_t)batch * Hkv * sizeof(int), 256);
     w.cnt_bytes = cnt > kCounterRegion ? cnt : kCounterRegion;
-    w.o_bytes = align_up((size_t)batch * Hq * n_split * D * sizeof(float), 256);
-    w.ml_bytes = align_up((size_t)batch * Hq * n_split * 2 * sizeof(float), 256);
+    w.o_bytes = align_up((size_t)partials * D * sizeof(float), 256);
+    w.ml_bytes = align_up((size_t)partials * 2 * sizeof(float), 256);
   }
   if (max_blocks > 0) {
     w.cnt_bytes = w.cnt_bytes ? w.cnt_bytes : kCounterRegion;  // kept zero for calls that split
@@ -384,17 +393,12 @@ DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs,
 
 DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms) {
   if (!bf16) return plan_decode(batch, Hkv, G, D, max_blocks, 16, false, num_sms);
-  DecodePlan p{max_blocks, 1, true, G > 8 ? 2 : 3};
-  const long long resident = (long long)num_sms * p.ctas_per_sm;
+  // tensor-core path: as many CTAs as fit the device at once (the kernel's occupancy: its registers at head dim
+  // 128 hold 3 CTAs of 4 warps per SM, 2 for groups above 8 heads; at 64 four), or as there are blocks
+  DecodePlan p{max_blocks, 1, true, G > 8 ? 2 : (D == 64 ? 4 : 3)};
   const long long total = (long long)batch * Hkv * max_blocks;
-  const long long waves = 4;
-  long long est = (total + resident * waves - 1) / (resident * waves);
-  if (est < 32) est = 32;
-  if (est > kQ8MaxSplit) est = kQ8MaxSplit;
-  if (est >= max_blocks) return p;
-  const long long n = (max_blocks + est - 1) / est;
-  p.split_blocks = (int)((max_blocks + n - 1) / n);
-  p.n_split = (max_blocks + p.split_blocks - 1) / p.split_blocks;
+  const long long resident = (long long)num_sms * p.ctas_per_sm;
+  p.n_split = (int)(total < resident ? total : resident);
   return p;
 }
 
@@ -667,7 +671,7 @@ size_t weights_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_
   for (int bf16 = 0; bf16 < 2; ++bf16) {
     const DecodePlan p = q8 ? plan_decode_q8(batch, Hkv, Hq / Hkv, D, mb, bf16 != 0, sms)
                             : plan_decode(batch, Hkv, Hq / Hkv, D, mb, bs, bf16 != 0, sms);
-    const size_t n = decode_ws_weights(batch, Hq, Hkv, D, p.n_split, mb).total;
+    const size_t n = decode_ws_weights(batch, Hq, Hkv, D, count_partials(p, q8, batch, Hq, Hq / Hkv), mb).total;
     most = n > most ? n : most;
   }
   return most;
@@ -699,7 +703,7 @@ minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_he
   const DecodePlan plan = plan_decode(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
                                       b->max_blocks_per_seq, kv->block_size, bf16, sms);
   DecodeArgs a = decode_args(bf16, num_q_heads, kv, rope, b, scale, plan, err);
-  st = place_weights_ws(a, block_weights, workspace, workspace_bytes);
+  st = place_weights_ws(a, plan, block_weights, workspace, workspace_bytes);
   if (st != MINIPIC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
   a.cs_f16 = rope->cos_sin_f16;
@@ -742,7 +746,7 @@ minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, 
   DecodeArgs a = decode_args(bf16, num_q_heads, &pool, rope, b, scale, plan, err);
   a.k_scale = kv->k_scale;
   a.v_scale = kv->v_scale;
-  st = place_weights_ws(a, block_weights, workspace, workspace_bytes);
+  st = place_weights_ws(a, plan, block_weights, workspace, workspace_bytes);
   if (st != MINIPIC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
   a.cs_f16 = rope->cos_sin_f16;

@@ -5,8 +5,15 @@
 // unrotated and rotated here at pi(j) = start[r][block] + slot (MiniPIC summary,
 // gist.science 2606.13126, section 2.1).
 //
-// Work: one CTA = (split, kv head, request); each of its warps owns every NW-th
-// 16-key block of the split, two at a time, and runs its own ring of stages.  A
+// Work: the blocks of all (request, kv head) pairs form one list, request by
+// request; a resident grid cuts it into equal ranges, one per CTA, whatever the
+// lengths are (they are on the device).  A CTA walks its range pair by pair: a pair
+// that lies inside one range is written at once, one that is cut leaves a partial
+// result per CTA, and the last of them to arrive merges them in order.  Against a
+// grid of (split, kv head, request) this has no partly filled last wave, and pays
+// a start (5 us: table entries, scales, queries, first tiles) once or twice per
+// CTA instead of per split.  Within a pair each warp owns every NW-th 16-key
+// block, two at a time, and runs its own ring of stages.  A
 // (block, head) tile is 16 d contiguous bytes, lines of 128 bytes (one key at d
 // 128, two at d 64) whose 16-byte chunks are stored permuted (mix below), so that
 // the key-row reads and the transposing reads of V are free of bank conflicts.  The fp16 cos | sin row of the block's query rotation comes with
@@ -50,8 +57,9 @@ namespace {
 
 using ptx::U4;
 
-constexpr int kWarps = 4;
-constexpr int kMaxSplit = kQ8MaxSplit;        // split_blocks cap (planner)
+constexpr int kWarps = kQ8Warps;
+constexpr int kChunk = 256;                   // blocks whose metadata is staged at a time
+constexpr int kMinRange = 32;                 // blocks of a CTA, unless there are fewer in all
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;               // a reference moves when exceeded by 2^8
@@ -67,12 +75,12 @@ struct Lay {
   static constexpr int MT = D / 16;                // M tiles of O^T
   static constexpr int STAGES = kWarps * NS * STAGE;
   static constexpr int ROWS = STAGES;                               // [warp][stage][2] table rows
-  static constexpr int META = ROWS + kWarps * NS * 2 * ROWB;        // [split block, padded to pairs] int4
-  static constexpr int MASK = META + (kMaxSplit + 2 * kWarps) * 16;  // [same] uint32
+  static constexpr int META = ROWS + kWarps * NS * 2 * ROWB;        // [chunk block, padded to pairs] int4
+  static constexpr int MASK = META + (kChunk + 2 * kWarps) * 16;  // [same] uint32
   static constexpr int OST = D + 4;                             // padded row stride of the merge
   static constexpr int MERGE_W = (48 + 16 * OST) * 4;           // ms[16], l[16], mt[16], O[16][OST] of one warp
   static constexpr int MERGE = kWarps * MERGE_W;                // overlays stages, rows and meta
-  static constexpr int TOTAL = MASK + (kMaxSplit + 2 * kWarps) * 4;
+  static constexpr int TOTAL = MASK + (kChunk + 2 * kWarps) * 4;
   static_assert(MERGE <= TOTAL, "the merge overlays what the loop no longer reads");
 };
 
@@ -109,6 +117,11 @@ __device__ __forceinline__ void rotate(uint32_t x, uint32_t y, uint32_t c, uint3
   yo = u32(__hfma2(h2(x), h2(s), __hmul2(h2(y), h2(c))));
 }
 
+// Blocks of a request's length (clamped to its table).
+__device__ __forceinline__ int blocks_of(int L, int mb) {
+  return L <= 0 ? 0 : min((L >> 4) + ((L & 15) != 0), mb);
+}
+
 // |t - b| for any two 32-bit integers
 __device__ __forceinline__ uint32_t distance(int t, int b) {
   return b > t ? (uint32_t)b - (uint32_t)t : (uint32_t)t - (uint32_t)b;
@@ -130,33 +143,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   int4* meta = reinterpret_cast<int4*>(sgen + LY::META);
   uint32_t* vmask = reinterpret_cast<uint32_t*>(sgen + LY::MASK);
 
-  const int split = blockIdx.x, hk = blockIdx.y, r = blockIdx.z;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, tig = lane & 3;
   const int G = a.G, mb = a.max_blocks;
-
-  // Every load that depends on nothing comes first, so that a CTA's start costs about two round trips to memory
-  // (ids, then scales): the table entries of this warp's first pairs and of the staging below (bounded by the
-  // table's width, whatever the length), the slot rotations and the query.
-  const int b_begin = split * a.split_blocks;
-  const int* bt = a.block_tables + (size_t)r * mb + b_begin;
-  const int* bs = a.block_starts + (size_t)r * mb + b_begin;
-  const int tab = min(a.split_blocks, mb - b_begin);  // entries of this split that the table has
-  int L = a.seq_lens[r];
-  int tq = a.q_pos[r];
-  int e_phys = -1, e_start = 0;  // lane 2 p + u: block u of this warp's pair p
-  if (lane < 2 * NS && warp + NW * lane < tab) {
-    e_phys = __ldg(bt + warp + NW * lane);
-    e_start = __ldg(bs + warp + NW * lane);
-  }
-  constexpr int kPer = kMaxSplit / (NW * 32);  // staged entries of a thread
-  int t_phys[kPer], t_start[kPer];
-#pragma unroll
-  for (int u = 0; u < kPer; ++u) {
-    const int i = threadIdx.x + u * NW * 32;
-    t_phys[u] = i < tab ? __ldg(bt + i) : -1;
-    t_start[u] = i < tab ? __ldg(bs + i) : 0;
-  }
 
   // this thread's key rows (slots ks0, ks0 + 2) and rotary pairs (f0 .. f0 + 4 NH - 1 with + d/2)
   const int ks0 = frag_slot(g8);
@@ -173,41 +162,86 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       rs[row][4 * u] = sn.x; rs[row][4 * u + 1] = sn.y; rs[row][4 * u + 2] = sn.z; rs[row][4 * u + 3] = sn.w;
     }
   }
-  // unrotated queries of this thread's heads (column g8 + 8 nt)
-  uint32_t qx[NT][2 * NH], qy[NT][2 * NH];
+  // ---- this CTA's range [x0, x1) of the list, and the pair it is at.  In shared memory: registers that live
+  // through the main loop are what bounds the CTAs per SM.
+  __shared__ long long s_part[NW];
+  __shared__ struct {
+    long long x0, x1, total, n_cta;
+    int r, hk, nblk, L;   // the pair: request, kv head, blocks, length
+    int b_begin, left;    // its first block in this range, blocks of the range from there on
+    int last;
+  } sg;
+  auto cta_total = [&](int v, int& before) {  // sum of v over the CTA, and over the threads before this one
+    int pre = v;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int head = DUAL ? (g8 & 3) : 8 * nt + g8;
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)r * a.Hq + (size_t)hk * G + head) * D + f0;
-#pragma unroll
-    for (int u = 0; u < NH / 2; ++u) {
-      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      const uint4 x = head < G ? __ldg(reinterpret_cast<const uint4*>(p) + u) : z;
-      const uint4 y = head < G ? __ldg(reinterpret_cast<const uint4*>(p + D / 2) + u) : z;
-      qx[nt][4 * u] = x.x; qx[nt][4 * u + 1] = x.y; qx[nt][4 * u + 2] = x.z; qx[nt][4 * u + 3] = x.w;
-      qy[nt][4 * u] = y.x; qy[nt][4 * u + 1] = y.y; qy[nt][4 * u + 2] = y.z; qy[nt][4 * u + 3] = y.w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(FULL, pre, o);
+      if (lane >= o) pre += y;
     }
+    __syncthreads();
+    if (lane == 31) s_part[warp] = pre;
+    __syncthreads();
+    long long sum = 0;
+    before = pre - v;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before += (int)s_part[w];
+      sum += s_part[w];
+    }
+    return sum;
+  };
+  long long total = 0;
+  for (int base = 0; base < a.batch; base += NW * 32) {
+    const int i = base + threadIdx.x;
+    const int Li = i < a.batch ? a.seq_lens[i] : 0;
+    if ((Li < 0 || (long long)Li > 16LL * mb) && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
+    int unused;
+    total += cta_total(blocks_of(Li, mb), unused);
   }
-
-  const int Lmax = (int)min((long long)mb * 16, 2147483632LL);
-  if (L < 0 || L > Lmax) {
-    if (threadIdx.x == 0 && split == 0) atomicOr(a.err, kErrSeqLen);
-    L = L < 0 ? 0 : Lmax;
+  // requests with no key
+  for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
+    if (blocks_of(a.seq_lens[i], mb)) continue;
+    for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32)
+      static_cast<__nv_bfloat16*>(a.out)[(size_t)i * a.Hq * D + e] = __float2bfloat16_rn(0.f);
+    if (a.lse)
+      for (int e = threadIdx.x; e < a.Hq; e += NW * 32) a.lse[(size_t)i * a.Hq + e] = -CUDART_INF_F;
   }
-  const int nblk = (int)(((long long)L + 15) >> 4);
-  const int n_valid = max(1, (nblk + a.split_blocks - 1) / a.split_blocks);
-  if (split >= n_valid) return;
-  const int b_end = min(nblk, b_begin + a.split_blocks);
-  const int span = b_end - b_begin;
-  const int nmine = span > warp ? (span - warp + NW - 1) / NW : 0;  // blocks of this warp
-  const int npair = (nmine + 1) >> 1;
-  if (tq < 0 || tq >= a.max_pos) {
-    if (threadIdx.x == 0 && split == 0) atomicOr(a.err, kErrPosition);
-    tq = 0;
+  total *= a.Hkv;
+  {
+    const long long n_cta = min((long long)gridDim.x, (total + kMinRange - 1) / kMinRange);
+    if (blockIdx.x >= n_cta) return;
+    const long long x0 = blockIdx.x * total / n_cta, x1 = (blockIdx.x + 1) * total / n_cta;
+    long long first = 0;  // blocks (one kv head) of the requests before `base`
+    for (int base = 0; base < a.batch; base += NW * 32) {
+      const int i = base + threadIdx.x;
+      const int Li = i < a.batch ? a.seq_lens[i] : 0;
+      const int n = blocks_of(Li, mb);
+      int before;
+      const long long sum = cta_total(n, before);
+      const long long at = (first + before) * a.Hkv;
+      if (x0 >= at && x0 < at + (long long)n * a.Hkv) {
+        sg.x0 = x0;
+        sg.x1 = x1;
+        sg.total = total;
+        sg.n_cta = n_cta;
+        sg.r = i;
+        sg.hk = (int)((x0 - at) / n);
+        sg.nblk = n;
+        sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
+        sg.b_begin = (int)((x0 - at) % n);
+        sg.left = (int)(x1 - x0);
+      }
+      first += sum;
+      if (first * a.Hkv > x0) break;
+    }
+    __syncthreads();
   }
+  int b0 = 0, span = 0, npair = 0;               // the chunk's first block, blocks, pairs of this warp
+  uint32_t qx[NT][2 * NH], qy[NT][2 * NH];       // queries of this thread's heads (column g8 + 8 nt), fp16
+  __shared__ float2 s_qf[NT][4];                 // the power of two taken out of those of columns 2 tig + j + 8 nt
 
   // What a block needs: x = its (block, head) tile (-1: nothing usable), y = table row of |t - start|.
-  auto place = [&](int phys, int start) {
+  auto place = [&](int phys, int start, int tq, int hk) {
     const uint32_t ad = distance(tq, start);
     const bool ok = phys >= 0 && phys < a.num_blocks && ad < (uint32_t)a.max_pos;
     return make_int2(ok ? phys * a.Hkv + hk : -1, ok ? (int)ad : 0);
@@ -238,22 +272,60 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       ptx::cp_async16(wrow + stg * 2 * LY::ROWB + 16 * lane,
                       rg + (size_t)pr.y * LY::ROWB);
   };
-  // the first copies start at once
-#pragma unroll
-  for (int p = 0; p < NS; ++p) {
-    const int2 p0 = place(__shfl_sync(FULL, e_phys, 2 * p), __shfl_sync(FULL, e_start, 2 * p));
-    const int2 p1 = place(__shfl_sync(FULL, e_phys, 2 * p + 1), __shfl_sync(FULL, e_start, 2 * p + 1));
-    if (p < npair) issue(p, p0, warp + NW * (2 * p + 1) < span ? p1 : make_int2(-1, 0));
-    ptx::cp_async_commit();
-  }
-  // per block, once for the CTA: place, score factor (softmax scale * log2 e * key scale), log2 of the value
-  // scale (finite), and the mask of its usable slots (bit 16: the values are zero, bit 17: the angle is negative)
-  {
-    float t_ks[kPer], t_vs[kPer];
+  // Start of a chunk: the first copies, and per block, once for the CTA: place, score factor (softmax scale *
+  // log2 e * key scale), log2 of the value scale (finite), and the mask of its usable slots (bit 16: the values are
+  // zero, bit 17: the angle is negative).  With FIRST (of a pair) also its query.  Every load that depends on
+  // nothing else comes first, so that a start costs about two round trips to memory (ids, then scales).
+  auto start_chunk = [&](bool first) {
+    const int r = sg.r, hk = sg.hk;
+    int tq = __ldg(a.q_pos + r);
+    const int* bt = a.block_tables + (size_t)r * mb + b0;
+    const int* bs = a.block_starts + (size_t)r * mb + b0;
+    int e_phys = -1, e_start = 0;  // lane 2 p + u: block u of this warp's pair p
+    if (lane < 2 * NS && warp + NW * lane < span) {
+      e_phys = __ldg(bt + warp + NW * lane);
+      e_start = __ldg(bs + warp + NW * lane);
+    }
+    constexpr int kPer = kChunk / (NW * 32);  // staged entries of a thread
+    int t_phys[kPer], t_start[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int i = threadIdx.x + u * NW * 32;
-      const bool in = i < span && t_phys[u] >= 0 && t_phys[u] < a.num_blocks;
+      t_phys[u] = i < span ? __ldg(bt + i) : -1;
+      t_start[u] = i < span ? __ldg(bs + i) : 0;
+    }
+    if (first) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int head = DUAL ? (g8 & 3) : 8 * nt + g8;
+        const __nv_bfloat16* p =
+            static_cast<const __nv_bfloat16*>(a.q) + ((size_t)r * a.Hq + (size_t)hk * G + head) * D + f0;
+#pragma unroll
+        for (int u = 0; u < NH / 2; ++u) {
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+          const uint4 x = head < G ? __ldg(reinterpret_cast<const uint4*>(p) + u) : z;
+          const uint4 y = head < G ? __ldg(reinterpret_cast<const uint4*>(p + D / 2) + u) : z;
+          qx[nt][4 * u] = x.x; qx[nt][4 * u + 1] = x.y; qx[nt][4 * u + 2] = x.z; qx[nt][4 * u + 3] = x.w;
+          qy[nt][4 * u] = y.x; qy[nt][4 * u + 1] = y.y; qy[nt][4 * u + 2] = y.z; qy[nt][4 * u + 3] = y.w;
+        }
+      }
+    }
+    if (tq < 0 || tq >= a.max_pos) {
+      if (threadIdx.x == 0) atomicOr(a.err, kErrPosition);
+      tq = 0;
+    }
+    __syncthreads();  // the metadata and the merge of what came before have been read
+#pragma unroll
+    for (int p = 0; p < NS; ++p) {
+      const int2 p0 = place(__shfl_sync(FULL, e_phys, 2 * p), __shfl_sync(FULL, e_start, 2 * p), tq, hk);
+      const int2 p1 = place(__shfl_sync(FULL, e_phys, 2 * p + 1), __shfl_sync(FULL, e_start, 2 * p + 1), tq, hk);
+      if (p < npair) issue(p, p0, warp + NW * (2 * p + 1) < span ? p1 : make_int2(-1, 0));
+      ptx::cp_async_commit();
+    }
+    float t_ks[kPer], t_vs[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const bool in = t_phys[u] >= 0 && t_phys[u] < a.num_blocks;
       t_ks[u] = in ? __ldg(a.k_scale + (size_t)t_phys[u] * a.Hkv + hk) : 0.f;
       t_vs[u] = in ? __ldg(a.v_scale + (size_t)t_phys[u] * a.Hkv + hk) : 0.f;
     }
@@ -265,8 +337,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       uint32_t m = 0u;
       if (i < span) {
         const int phys = t_phys[u], start = t_start[u];
-        pl = place(phys, start);
-        const int nk = min(16, L - (b_begin + i) * 16);
+        pl = place(phys, start, tq, hk);
+        const int nk = min(16, sg.L - (b0 + i) * 16);
         if (phys < 0 || phys >= a.num_blocks) {
           atomicOr(a.err, kErrBlockId);
         } else {
@@ -290,55 +362,39 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       meta[i] = make_int4(pl.x, pl.y, __float_as_int(ks), __float_as_int(lv));
       vmask[i] = m;
     }
-    if (threadIdx.x < 2 * NW) {  // pairs of a full split reach past its last entry
-      meta[kMaxSplit + threadIdx.x] = make_int4(-1, 0, 0, 0);
-      vmask[kMaxSplit + threadIdx.x] = 0u;
+    if (threadIdx.x < 2 * NW) {  // the pairs of a full chunk reach past its last entry
+      meta[kChunk + threadIdx.x] = make_int4(-1, 0, 0, 0);
+      vmask[kChunk + threadIdx.x] = 0u;
     }
-  }
-
-  // the queries scaled to fp16, and the power of two taken out of the heads of the score columns (2 tig + j + 8 nt)
-  float qf[NT][2];
+    if (first) {  // the queries scaled to fp16
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float amax = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        float amax = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2 * NH; ++e)
-      amax = fmaxf(amax, fmaxf(fmaxf(fabsf(ptx::bf_lo(qx[nt][e])), fabsf(ptx::bf_hi(qx[nt][e]))),
-                               fmaxf(fabsf(ptx::bf_lo(qy[nt][e])), fabsf(ptx::bf_hi(qy[nt][e])))));
-    amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 2));
-    // exponent of the largest element (at most 127, an infinity's; a row of zeros or subnormals takes -126)
-    int ex = (__float_as_int(amax) >> 23) - 127;
-    ex = ex < -126 ? -126 : (ex > 126 ? 126 : ex);
-    const float down = __int_as_float((127 - ex) << 23);
+        for (int e = 0; e < 2 * NH; ++e)
+          amax = fmaxf(amax, fmaxf(fmaxf(fabsf(ptx::bf_lo(qx[nt][e])), fabsf(ptx::bf_hi(qx[nt][e]))),
+                                   fmaxf(fabsf(ptx::bf_lo(qy[nt][e])), fabsf(ptx::bf_hi(qy[nt][e])))));
+        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 2));
+        // exponent of the largest element (at most 127, an infinity's; a row of zeros or subnormals takes -126)
+        int ex = (__float_as_int(amax) >> 23) - 127;
+        ex = ex < -126 ? -126 : (ex > 126 ? 126 : ex);
+        const float down = __int_as_float((127 - ex) << 23);
 #pragma unroll
-    for (int e = 0; e < 2 * NH; ++e) {
-      qx[nt][e] = ptx::pack_f16(ptx::bf_lo(qx[nt][e]) * down, ptx::bf_hi(qx[nt][e]) * down);
-      qy[nt][e] = ptx::pack_f16(ptx::bf_lo(qy[nt][e]) * down, ptx::bf_hi(qy[nt][e]) * down);
+        for (int e = 0; e < 2 * NH; ++e) {
+          qx[nt][e] = ptx::pack_f16(ptx::bf_lo(qx[nt][e]) * down, ptx::bf_hi(qx[nt][e]) * down);
+          qy[nt][e] = ptx::pack_f16(ptx::bf_lo(qy[nt][e]) * down, ptx::bf_hi(qy[nt][e]) * down);
+        }
+        if (warp == 0 && tig == 0) reinterpret_cast<float*>(s_qf[nt])[g8] = __int_as_float((ex + 127) << 23);
+      }
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      qf[nt][j] = __int_as_float((__shfl_sync(FULL, ex, (2 * tig + j) * 4) + 127) << 23);
-  }
+    __syncthreads();  // metadata visible
+  };
 
   // references: ms of the scores (denominator l), mt of the scores plus log2 of the value scale (O)
-  // (before the first key a finite value far below any score, so that no difference of two is undefined), and
-  // dl = ms - mt + 7
-  float ms[NT][2], mt[NT][2], dl[NT][2], l[NT][2];
+  // (before the first key a finite value far below any score, so that no difference of two is undefined)
+  float ms[NT][2], mt[NT][2], l[NT][2];
   float oacc[LY::MT][NT][4];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    ms[nt][0] = ms[nt][1] = mt[nt][0] = mt[nt][1] = kNone;
-    dl[nt][0] = dl[nt][1] = kHead;
-    l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-    for (int m = 0; m < LY::MT; ++m)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) oacc[m][nt][k] = 0.f;
-  }
-
-  __syncthreads();  // meta visible
-
   // the rotated query words of column tile nt, R_{t - start} q, from a staged cos | sin row
   auto rotate_q = [&](auto plain, uint32_t row, uint32_t m, uint32_t (&bx)[NT][2 * NH], uint32_t (&by)[NT][2 * NH]) {
     uint32_t cw[2 * NH], sw[2 * NH];
@@ -407,7 +463,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[nt][e] += sy[nt][e];
   };
-  float* const w_base = WTS ? a.w_raw + ((size_t)r * a.Hkv + hk) * mb * G : nullptr;
+  float* w_base = nullptr;  // raw sums of the pair
   // one step of the online softmax over 16 keys; m, ks and lv are those of the columns' block, wb the block
   // whose sum is recorded
   auto softmax = [&](auto plain, float (&sc)[NT][4], uint32_t m, float ks, float lv, int wb, uint32_t (&pb0)[NT],
@@ -415,14 +471,16 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     const bool v0 = decltype(plain)::value || ((m >> ks0) & 1u), v1 = decltype(plain)::value || ((m >> (ks0 + 2)) & 1u);
     bool over = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 qf = s_qf[nt][tig];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float f = fminf(ks * qf[nt][j], 3.4e38f);  // finite: a product of 0 stays 0
+        const float f = fminf(ks * (j ? qf.y : qf.x), 3.4e38f);  // finite: a product of 0 stays 0
         sc[nt][j] = v0 ? sc[nt][j] * f : -CUDART_INF_F;
         sc[nt][2 + j] = v1 ? sc[nt][2 + j] * f : -CUDART_INF_F;
         over |= fmaxf(sc[nt][j], sc[nt][2 + j]) > fminf(ms[nt][j], mt[nt][j] - lv) + kRescale;
       }
+    }
     if (__any_sync(FULL, over)) {  // rare: move the references, rescale what was summed
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -436,7 +494,6 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
           const float cs = ex2(ms[nt][j] - msn), ct = ex2(mt[nt][j] - mtn);
           ms[nt][j] = msn;
           mt[nt][j] = mtn;
-          dl[nt][j] = msn - mtn + kHead;
           l[nt][j] *= cs;
 #pragma unroll
           for (int mm = 0; mm < LY::MT; ++mm) {
@@ -451,7 +508,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         // P = e * 2^(ms - mt + lv + 7); the cap only meets scores whose e is 0
-        const float w = ex2(fminf(dl[nt][j] + lv, 126.f));
+        const float w = ex2(fminf(ms[nt][j] - mt[nt][j] + (lv + kHead), 126.f));
         const float ea = ex2(sc[nt][j] - ms[nt][j]), eb = ex2(sc[nt][2 + j] - ms[nt][j]);
         pv[j] = ea * w;
         pv[2 + j] = eb * w;
@@ -466,7 +523,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
         e += __shfl_xor_sync(FULL, e, 8);
         e += __shfl_xor_sync(FULL, e, 16);
         const int head = DUAL ? (2 * tig + g8) & 3 : 8 * nt + 2 * tig + g8;
-        if (g8 < 2 && head < G && wb < b_end)
+        if (g8 < 2 && head < G && wb < b0 + span)
           w_base[(size_t)wb * G + head] = e == 0.f ? -CUDART_INF_F : (odd ? ms[nt][1] : ms[nt][0]) + log2f(e);
       }
       pb0[nt] = ptx::movmatrix_trans(ptx::pack_f16(pv[0], pv[1]));  // fragment rows 0 .. 7
@@ -509,7 +566,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[0][e] = tig >= 2 ? s1[0][e] : sc[0][e];
       softmax(plain, sc, tig >= 2 ? m1 : m0, __int_as_float(mc.z), __int_as_float(mc.w),
-              b_begin + i0 + (tig >= 2 ? NW : 0), pb0, pb1);
+              b0 + i0 + (tig >= 2 ? NW : 0), pb0, pb1);
       const uint32_t z0[1] = {g8 < 4 ? pb0[0] : 0u}, z1[1] = {g8 < 4 ? pb1[0] : 0u};
       const uint32_t y0[1] = {g8 < 4 ? 0u : pb0[0]}, y1[1] = {g8 < 4 ? 0u : pb1[0]};
       values(plain, kbase + LY::TILE, m0, z0, z1);
@@ -521,14 +578,14 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
         const uint32_t m = u ? m1 : m0;
         rotate_q(plain, rowb + u * LY::ROWB, m, bx, by);
         scores(kbase + 2 * u * LY::TILE, bx, by, sc);
-        softmax(plain, sc, m, __int_as_float(md.z), __int_as_float(md.w), b_begin + i0 + u * NW, pb0, pb1);
+        softmax(plain, sc, m, __int_as_float(md.z), __int_as_float(md.w), b0 + i0 + u * NW, pb0, pb1);
         values(plain, kbase + (2 * u + 1) * LY::TILE, m, pb0, pb1);
       }
     }
   };
   // one pair from stage `stg` (a compile-time constant: every shared address is a per-thread base and an immediate)
   auto step = [&](const int stg, const int p) {
-    const int i0 = warp + 2 * NW * p;  // blocks i0 and i0 + NW of the split
+    const int i0 = warp + 2 * NW * p;  // blocks i0 and i0 + NW of the chunk
     const uint32_t kbase = wbase + stg * LY::STAGE, rowb = wrow + stg * 2 * LY::ROWB;
     const uint32_t m0 = vmask[i0], m1 = vmask[i0 + NW];
     ptx::cp_async_wait<NS - 1>();
@@ -544,107 +601,155 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     ptx::cp_async_commit();
   };
 #pragma unroll 1
-  for (int p = 0; p < npair; p += NS) {
+  while (true) {
+    if (WTS) w_base = a.w_raw + ((size_t)sg.r * a.Hkv + sg.hk) * mb * G;
 #pragma unroll
-    for (int stg = 0; stg < NS; ++stg)
-      if (p + stg < npair) step(stg, p + stg);
-  }
-  ptx::cp_async_wait<0>();
-  __syncthreads();  // every stage has been read: the merge overlays them
-
-  // per-warp state: ms[16], l[16], mt[16], O[16][OST], by column
-  {
-    float* w = reinterpret_cast<float*>(sgen + warp * LY::MERGE_W);
+    for (int nt = 0; nt < NT; ++nt) {
+      ms[nt][0] = ms[nt][1] = mt[nt][0] = mt[nt][1] = kNone;
+      l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int m = 0; m < LY::MT; ++m)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float s = l[nt][j];
-        s += __shfl_xor_sync(FULL, s, 4);
-        s += __shfl_xor_sync(FULL, s, 8);
-        s += __shfl_xor_sync(FULL, s, 16);
-        const int head = 8 * nt + 2 * tig + j;
-        if (g8 == 0) {
-          w[head] = ms[nt][j];
-          w[16 + head] = s;
-          w[32 + head] = mt[nt][j];
-        }
+        for (int k = 0; k < 4; ++k) oacc[m][nt][k] = 0.f;
+    }
+#pragma unroll 1
+    for (b0 = sg.b_begin;;) {
+      span = min(kChunk, min(sg.nblk, sg.b_begin + sg.left) - b0);
+      npair = span > warp ? (span - warp + 2 * NW - 1) / (2 * NW) : 0;
+      start_chunk(b0 == sg.b_begin);
+#pragma unroll 1
+      for (int p = 0; p < npair; p += NS) {
 #pragma unroll
-        for (int m = 0; m < LY::MT; ++m) {
-          w[48 + head * LY::OST + 16 * m + g8] = oacc[m][nt][j];
-          w[48 + head * LY::OST + 16 * m + g8 + 8] = oacc[m][nt][2 + j];
-        }
+        for (int stg = 0; stg < NS; ++stg)
+          if (p + stg < npair) step(stg, p + stg);
       }
-  }
-  __syncthreads();
+      ptx::cp_async_wait<0>();
+      b0 += span;
+      if (b0 >= sg.nblk || b0 >= sg.b_begin + sg.left) break;
+    }
+    __syncthreads();  // every stage has been read: the merge overlays them
+    const int r = sg.r, hk = sg.hk, b_begin = sg.b_begin, nblk = sg.nblk, b_end = b0;
 
-  // the CTA's output of each head, already divided by its denominator: values no larger than V's
-  const bool direct = n_valid == 1;
-  for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
-    const int head = idx / D, dim = idx - head * D;
-    constexpr int NST = DUAL ? 2 * NW : NW;  // states of a head: warps, and half columns 4 apart
-    auto state = [&](int w) {
-      return reinterpret_cast<const float*>(sgen + (w % NW) * LY::MERGE_W);
-    };
-    auto column = [&](int w) { return head + (w / NW) * 4; };
-    float M = kNone, T = kNone;
+    // per-warp state: ms[16], l[16], mt[16], O[16][OST], by column
+    {
+      float* w = reinterpret_cast<float*>(sgen + warp * LY::MERGE_W);
 #pragma unroll
-    for (int w = 0; w < NST; ++w) {
-      M = fmaxf(M, state(w)[column(w)]);
-      T = fmaxf(T, state(w)[32 + column(w)]);
-    }
-    float Ls = 0.f, O = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int w = 0; w < NST; ++w) {
-      const float* p = state(w);
-      const int c = column(w);
-      Ls = fmaf(p[16 + c], exp2f(p[c] - M), Ls);
-      O = fmaf(p[48 + c * LY::OST + dim], exp2f(p[32 + c] - T), O);
+        for (int j = 0; j < 2; ++j) {
+          float s = l[nt][j];
+          s += __shfl_xor_sync(FULL, s, 4);
+          s += __shfl_xor_sync(FULL, s, 8);
+          s += __shfl_xor_sync(FULL, s, 16);
+          const int head = 8 * nt + 2 * tig + j;
+          if (g8 == 0) {
+            w[head] = ms[nt][j];
+            w[16 + head] = s;
+            w[32 + head] = mt[nt][j];
+          }
+#pragma unroll
+          for (int m = 0; m < LY::MT; ++m) {
+            w[48 + head * LY::OST + 16 * m + g8] = oacc[m][nt][j];
+            w[48 + head * LY::OST + 16 * m + g8 + 8] = oacc[m][nt][2 + j];
+          }
+        }
     }
-    O = Ls == 0.f ? 0.f : O / Ls * exp2f(T - M - kHead);
-    const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
-    const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
-    if (direct) {
-      static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(O);
-      if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
-      if (WTS && dim == 0) a.w_lse[hq] = lse2;
-    } else {
-      const size_t pi = hq * a.n_split + split;
-      a.part_o[pi * D + dim] = O;
-      if (dim == 0) a.part_ml[pi] = lse2;
-    }
-  }
-  if (direct) return;
+    __syncthreads();
 
-  // the last split of this (request, kv head) to finish merges all of them and resets the counter
-  __shared__ int s_last;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = atomicAdd(a.counters + (size_t)r * a.Hkv + hk, 1) == n_valid - 1;
-  }
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
-    const int head = idx / D, dim = idx - head * D;
-    const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
-    const size_t base = hq * a.n_split;
-    float M = -CUDART_INF_F;
-    for (int s = 0; s < n_valid; ++s) M = fmaxf(M, __ldcg(a.part_ml + base + s));
-    float Ls = 0.f, O = 0.f;
-    for (int s = 0; s < n_valid; ++s) {
-      const float m = __ldcg(a.part_ml + base + s);
-      const float f = m == -CUDART_INF_F ? 0.f : exp2f(m - M);
-      Ls += f;
-      O = fmaf(__ldcg(a.part_o + (base + s) * D + dim), f, O);
+    // the CTA's output of each head, already divided by its denominator: values no larger than V's
+    const bool direct = b_begin == 0 && b_end == nblk;
+    for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
+      const int head = idx / D, dim = idx - head * D;
+      constexpr int NST = DUAL ? 2 * NW : NW;  // states of a head: warps, and half columns 4 apart
+      auto state = [&](int w) {
+        return reinterpret_cast<const float*>(sgen + (w % NW) * LY::MERGE_W);
+      };
+      auto column = [&](int w) { return head + (w / NW) * 4; };
+      float M = kNone, T = kNone;
+#pragma unroll
+      for (int w = 0; w < NST; ++w) {
+        M = fmaxf(M, state(w)[column(w)]);
+        T = fmaxf(T, state(w)[32 + column(w)]);
+      }
+      float Ls = 0.f, O = 0.f;
+#pragma unroll
+      for (int w = 0; w < NST; ++w) {
+        const float* p = state(w);
+        const int c = column(w);
+        Ls = fmaf(p[16 + c], exp2f(p[c] - M), Ls);
+        O = fmaf(p[48 + c * LY::OST + dim], exp2f(p[32 + c] - T), O);
+      }
+      O = Ls == 0.f ? 0.f : O / Ls * exp2f(T - M - kHead);
+      const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
+      const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
+      if (direct) {
+        static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(O);
+        if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
+        if (WTS && dim == 0) a.w_lse[hq] = lse2;
+      } else {
+        // a pair cut in front is this CTA's first (slot 0), one cut behind its last (slot 1)
+        const size_t pi = (size_t)(2 * blockIdx.x + (b_begin == 0)) * G + head;
+        a.part_o[pi * D + dim] = O;
+        if (dim == 0) a.part_ml[pi] = lse2;
+      }
     }
-    const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
-    static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(Ls == 0.f ? 0.f : O / Ls);
-    if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
-    if (WTS && dim == 0) a.w_lse[hq] = lse2;
+  if (!direct) {
+      // CTAs c1 .. c2 hold parts of this pair; the last of them to arrive merges them in order
+      const long long ps = b_begin ? sg.x0 - b_begin : sg.x1 - (b_end - b_begin);  // the pair's place in the list
+      auto owner = [&](long long x) { return ((x + 1) * sg.n_cta - 1) / sg.total; };
+      const int c1 = (int)owner(ps), c2 = (int)owner(ps + nblk - 1);
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        __threadfence();
+        sg.last = atomicAdd(a.counters + (size_t)r * a.Hkv + hk, 1) == c2 - c1;
+      }
+      __syncthreads();
+      if (sg.last) {
+        __threadfence();
+        for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
+          const int head = idx / D, dim = idx - head * D;
+          auto slot = [&](int c) { return (size_t)(2 * c + (c == c1)) * G + head; };
+          float M = -CUDART_INF_F;
+          for (int c = c1; c <= c2; ++c) M = fmaxf(M, __ldcg(a.part_ml + slot(c)));
+          float Ls = 0.f, O = 0.f;
+          for (int c = c1; c <= c2; ++c) {
+            const float m = __ldcg(a.part_ml + slot(c));
+            const float f = m == -CUDART_INF_F ? 0.f : exp2f(m - M);
+            Ls += f;
+            O = fmaf(__ldcg(a.part_o + slot(c) * D + dim), f, O);
+          }
+          const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
+          const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
+          static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(Ls == 0.f ? 0.f : O / Ls);
+          if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
+          if (WTS && dim == 0) a.w_lse[hq] = lse2;
+        }
+        if (threadIdx.x == 0) a.counters[(size_t)r * a.Hkv + hk] = 0;
+      }
+    }
+    const int left = sg.left - (b_end - b_begin);
+    if (left <= 0) break;
+    __syncthreads();  // the pair has been read
+    if (threadIdx.x == 0) {
+      sg.left = left;
+      sg.b_begin = 0;
+      sg.hk = hk + 1;
+      if (hk + 1 == a.Hkv) {
+        sg.hk = 0;
+        int i = r, n = 0, Li = 0;
+        while (n == 0 && ++i < a.batch) {  // a later request has blocks, as the range goes on
+          Li = a.seq_lens[i];
+          n = blocks_of(Li, mb);
+        }
+        if (n == 0) sg.left = 0;  // not reached
+        sg.r = min(i, a.batch - 1);
+        sg.nblk = n;
+        sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
+      }
+    }
+    __syncthreads();
+    if (sg.left <= 0) break;
   }
-  if (threadIdx.x == 0) a.counters[(size_t)r * a.Hkv + hk] = 0;
 }
 
 template <int D, int NT, bool DUAL, bool WTS, int NS, int CPS>
@@ -654,8 +759,7 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
   static bool done[64] = {false};
   cudaError_t e = set_smem_once(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)a.n_split, (unsigned)a.Hkv, (unsigned)a.batch);
-  kernel<<<grid, kWarps * 32, smem, s>>>(a);
+  kernel<<<a.n_split, kWarps * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 

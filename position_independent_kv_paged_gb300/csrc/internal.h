@@ -25,7 +25,7 @@ struct DecodeArgs {
   int* counters;             // [B][Hkv] finished splits (zero between calls), null when n_split == 1
   int batch, Hq, Hkv, G, D, BS, num_blocks, max_blocks;
   int split_blocks;          // blocks per split
-  int n_split;               // splits per (request, kv head)
+  int n_split;               // splits per (request, kv head); e4m3 tensor-core path: CTAs
   int ctas_per_sm;           // tensor-core decode: 3 (2 stages per warp) or 2 (3 stages) CTAs per SM
   float scale;               // softmax scale (1/sqrt(D) by default)
   int* err;                  // device error word
@@ -77,9 +77,9 @@ struct DecodePlan {
   int ctas_per_sm;  // tensor-core path: resident CTAs per SM (3 or 2; 1 for more than 8 heads per group)
 };
 DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs, bool bf16, int num_sms);
-// The e4m3 decode's plan; its tensor-core kernel stages the block metadata of
-// splits up to kQ8MaxSplit blocks in shared memory.
-constexpr int kQ8MaxSplit = 256;
+// The e4m3 decode's plan.  Its tensor-core kernel runs a resident grid: n_split is
+// the number of CTAs (of kQ8Warps warps), each with two partial results.
+constexpr int kQ8Warps = 4;
 DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan, cudaStream_t s);
@@ -196,6 +196,8 @@ struct DecodeWsW {
   size_t cnt_bytes, o_bytes, ml_bytes, lse_bytes, raw_bytes, total;
 };
 constexpr size_t kCounterRegion = 65536;
-DecodeWsW decode_ws_weights(int batch, int Hq, int Hkv, int D, int n_split, int max_blocks);
+// partials: partial results of one head each (0: none), counters and partials
+// only where the call may leave some.
+DecodeWsW decode_ws_weights(int batch, int Hq, int Hkv, int D, long long partials, int max_blocks);
 
 }  // namespace minipic
