@@ -397,7 +397,9 @@ DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool
   // 128 hold 3 CTAs of 4 warps per SM, 2 for groups above 8 heads; at 64 four), or as there are blocks
   DecodePlan p{max_blocks, 1, true, G > 8 ? 2 : (D == 64 ? 4 : 3)};
   const long long total = (long long)batch * Hkv * max_blocks;
-  const long long resident = (long long)num_sms * p.ctas_per_sm;
+  long long resident = (long long)num_sms * p.ctas_per_sm;
+  const int most = G > 8 ? kQ8MaxCtas / 2 : kQ8MaxCtas;  // the kernel's merge holds a weight per CTA and head
+  if (resident > most) resident = most;
   p.n_split = (int)(total < resident ? total : resident);
   return p;
 }

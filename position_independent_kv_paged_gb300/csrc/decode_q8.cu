@@ -59,7 +59,7 @@ using ptx::U4;
 
 constexpr int kWarps = kQ8Warps;
 constexpr int kChunk = 256;                   // blocks whose metadata is staged at a time
-constexpr int kMinRange = 32;                 // blocks of a CTA, unless there are fewer in all
+constexpr int kMinRange = 64;                 // blocks of a CTA, unless there are fewer in all (16, 32 and 128: slower)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;               // a reference moves when exceeded by 2^8
@@ -82,6 +82,7 @@ struct Lay {
   static constexpr int MERGE = kWarps * MERGE_W;                // overlays stages, rows and meta
   static constexpr int TOTAL = MASK + (kChunk + 2 * kWarps) * 4;
   static_assert(MERGE <= TOTAL, "the merge overlays what the loop no longer reads");
+  static_assert(kQ8MaxCtas * 8 * 4 <= STAGES, "so do the weights of the parts (half the CTAs for groups above 8)");
 };
 
 // Slot held by MMA fragment row g < 8 (row g + 8 holds slot + 2): rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are the four
@@ -190,34 +191,41 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     }
     return sum;
   };
-  long long total = 0;
+  long long total = 0, sum = 0;
+  int pairs = 0, zero = 0, Li = 0, n = 0, before = 0;
   for (int base = 0; base < a.batch; base += NW * 32) {
     const int i = base + threadIdx.x;
-    const int Li = i < a.batch ? a.seq_lens[i] : 0;
+    Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
+    n = blocks_of(Li, mb);
     if ((Li < 0 || (long long)Li > 16LL * mb) && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
-    int unused;
-    total += cta_total(blocks_of(Li, mb), unused);
+    total += sum = cta_total(n, before);
+    pairs += __syncthreads_count(n > 0);
+    zero |= i < a.batch && n == 0 && i % gridDim.x == blockIdx.x;
   }
-  // requests with no key
-  for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
-    if (blocks_of(a.seq_lens[i], mb)) continue;
-    for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32)
-      static_cast<__nv_bfloat16*>(a.out)[(size_t)i * a.Hq * D + e] = __float2bfloat16_rn(0.f);
-    if (a.lse)
-      for (int e = threadIdx.x; e < a.Hq; e += NW * 32) a.lse[(size_t)i * a.Hq + e] = -CUDART_INF_F;
+  if (__syncthreads_or(zero)) {  // requests with no key, shared out over the grid
+    for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
+      if (blocks_of(__ldg(a.seq_lens + i), mb)) continue;
+      for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32)
+        static_cast<__nv_bfloat16*>(a.out)[(size_t)i * a.Hq * D + e] = __float2bfloat16_rn(0.f);
+      if (a.lse)
+        for (int e = threadIdx.x; e < a.Hq; e += NW * 32) a.lse[(size_t)i * a.Hq + e] = -CUDART_INF_F;
+    }
   }
   total *= a.Hkv;
   {
-    const long long n_cta = min((long long)gridDim.x, (total + kMinRange - 1) / kMinRange);
+    // ranges of at least kMinRange blocks, but no fewer of them than pairs
+    const long long want = max((total + kMinRange - 1) / kMinRange, (long long)pairs * a.Hkv);
+    const long long n_cta = min((long long)gridDim.x, want);
     if (blockIdx.x >= n_cta) return;
     const long long x0 = blockIdx.x * total / n_cta, x1 = (blockIdx.x + 1) * total / n_cta;
     long long first = 0;  // blocks (one kv head) of the requests before `base`
     for (int base = 0; base < a.batch; base += NW * 32) {
       const int i = base + threadIdx.x;
-      const int Li = i < a.batch ? a.seq_lens[i] : 0;
-      const int n = blocks_of(Li, mb);
-      int before;
-      const long long sum = cta_total(n, before);
+      if (a.batch > NW * 32) {  // else the one pass above still holds them
+        Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
+        n = blocks_of(Li, mb);
+        sum = cta_total(n, before);
+      }
       const long long at = (first + before) * a.Hkv;
       if (x0 >= at && x0 < at + (long long)n * a.Hkv) {
         sg.x0 = x0;
@@ -254,7 +262,6 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
   const uint8_t* kg = static_cast<const uint8_t*>(a.k_pool) + 16 * lane;
   const uint8_t* vg = static_cast<const uint8_t*>(a.v_pool) + 16 * lane;
   constexpr int RL = LY::ROWB / 16;  // lanes of a table row
-  const uint8_t* rg = reinterpret_cast<const uint8_t*>(a.cs_f16) + 16 * (lane % RL);
   auto issue = [&](const int stg, int2 p0, int2 p1) {
     const uint32_t dst = wbase + stg * LY::STAGE;
 #pragma unroll
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
     const int2 pr = lane < RL ? p0 : p1;
     if (lane < 2 * RL)
       ptx::cp_async16(wrow + stg * 2 * LY::ROWB + 16 * lane,
-                      rg + (size_t)pr.y * LY::ROWB);
+                      reinterpret_cast<const uint8_t*>(a.cs_f16) + 16 * (lane % RL) + (size_t)pr.y * LY::ROWB);
   };
   // Start of a chunk: the first copies, and per block, once for the CTA: place, score factor (softmax scale *
   // log2 e * key scale), log2 of the value scale (finite), and the mask of its usable slots (bit 16: the values are
@@ -706,23 +713,50 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_q8_kernel(const __gri
       __syncthreads();
       if (sg.last) {
         __threadfence();
-        for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
-          const int head = idx / D, dim = idx - head * D;
-          auto slot = [&](int c) { return (size_t)(2 * c + (c == c1)) * G + head; };
-          float M = -CUDART_INF_F;
-          for (int c = c1; c <= c2; ++c) M = fmaxf(M, __ldcg(a.part_ml + slot(c)));
-          float Ls = 0.f, O = 0.f;
-          for (int c = c1; c <= c2; ++c) {
-            const float m = __ldcg(a.part_ml + slot(c));
-            const float f = m == -CUDART_INF_F ? 0.f : exp2f(m - M);
-            Ls += f;
-            O = fmaf(__ldcg(a.part_o + slot(c) * D + dim), f, O);
+        // weights of the parts first (one read of their log sums), then the weighted sum, four dims a thread
+        const int n_part = c2 - c1 + 1;
+        float* wt = reinterpret_cast<float*>(sgen);  // [part][G], over what the stages held
+        auto slot = [&](int c) { return (size_t)(2 * (c1 + c) + (c == 0)) * G; };
+        for (int i = threadIdx.x; i < n_part * G; i += NW * 32) wt[i] = __ldcg(a.part_ml + slot(i / G) + i % G);
+        __syncthreads();
+        for (int head = warp; head < G; head += NW) {
+          float M = -CUDART_INF_F, Ls = 0.f;
+          for (int c = lane; c < n_part; c += 32) M = fmaxf(M, wt[c * G + head]);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, o));
+          for (int c = lane; c < n_part; c += 32) {
+            const float m = wt[c * G + head];
+            Ls += m == -CUDART_INF_F ? 0.f : exp2f(m - M);
           }
-          const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) Ls += __shfl_xor_sync(FULL, Ls, o);
+          for (int c = lane; c < n_part; c += 32) {
+            const float m = wt[c * G + head];
+            wt[c * G + head] = m == -CUDART_INF_F ? 0.f : exp2f(m - M) / Ls;
+          }
+          if (lane == 0) {
+            const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
+            const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
+            if (a.lse) a.lse[hq] = lse2 * kLn2;
+            if (WTS) a.w_lse[hq] = lse2;
+          }
+        }
+        __syncthreads();
+        for (int idx = threadIdx.x; idx < G * D / 4; idx += NW * 32) {
+          const int head = idx / (D / 4), dim = (idx % (D / 4)) * 4;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int c = 0; c < n_part; ++c) {
+            const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(c) + head) * D + dim));
+            const float w = wt[c * G + head];
+            o.x = fmaf(p.x, w, o.x);
+            o.y = fmaf(p.y, w, o.y);
+            o.z = fmaf(p.z, w, o.z);
+            o.w = fmaf(p.w, w, o.w);
+          }
           const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
-          static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(Ls == 0.f ? 0.f : O / Ls);
-          if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
-          if (WTS && dim == 0) a.w_lse[hq] = lse2;
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + hq * D + dim) =
+              make_uint2(ptx::pack_bf16(o.x, o.y), ptx::pack_bf16(o.z, o.w));
         }
         if (threadIdx.x == 0) a.counters[(size_t)r * a.Hkv + hk] = 0;
       }

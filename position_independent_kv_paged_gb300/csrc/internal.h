@@ -79,7 +79,7 @@ struct DecodePlan {
 DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs, bool bf16, int num_sms);
 // The e4m3 decode's plan.  Its tensor-core kernel runs a resident grid: n_split is
 // the number of CTAs (of kQ8Warps warps), each with two partial results.
-constexpr int kQ8Warps = 4;
+constexpr int kQ8Warps = 4, kQ8MaxCtas = 4 * 160;
 DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan, cudaStream_t s);
