@@ -595,14 +595,19 @@ def _args(*specs):
     (the one the calls act on)."""
     torch = _torch()
     dev = torch.cuda.current_device() if torch.cuda.is_initialized() else None
-    for name, t, dtype, shape in specs:
-        if t is None or (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and
-                         t.is_contiguous() and t.get_device() == dev):
-            continue
-        _need(t, name, dtype=dtype, ndim=len(shape))
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{dev}")
+    try:
+        for name, t, dtype, shape in specs:
+            if t is not None and not (t.dtype is dtype and t.get_device() == dev and t.shape == shape and
+                                      t.is_contiguous()):
+                break
+        else:
+            return
+    except AttributeError:  # no tensor
+        pass
+    _need(t, name, dtype=dtype, ndim=len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} is on cuda:{t.get_device()}, but the current device is cuda:{dev}")
 
 
 def _any(name, t):
@@ -612,22 +617,28 @@ def _any(name, t):
 
 def _sizes(t, name, ndim):
     """The shape of the tensor that gives a call its sizes."""
-    if not isinstance(t, _torch().Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
-    return t.shape
+    try:
+        shape = t.shape
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch.Tensor") from None
+    if len(shape) != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {len(shape)}")
+    return shape
 
 
 def _rope16(rope, d, need_f16):
-    """ABI view of a table for the calls that read its float32 and, for bf16, its float16 form; and its specs."""
+    """Specs of a table for the calls that read its float32 and, for bf16, its float16 form."""
     torch = _torch()
     f32, f16 = (rope.cos_sin, rope.cos_sin_f16) if isinstance(rope, RopeTable) else (rope, None)
     if need_f16 and f16 is None:
         raise TypeError("this call needs the RopeTable built by rope_table() (it carries the float16 table)")
     n = _sizes(f32, "rope", 2)[0]
-    return (_Rope(f32.data_ptr(), n, d, _ptr(f16), None),
-            (("rope", f32, torch.float32, (n, d)), ("rope f16", f16, torch.float16, (n, d))))
+    return ("rope", f32, torch.float32, (n, d)), ("rope f16", f16, torch.float16, (n, d))
+
+
+def _rope16_struct(specs) -> _Rope:
+    (_, f32, _, (n, d)), (_, f16, _, _) = specs
+    return _Rope(f32.data_ptr(), n, d, _ptr(f16), None)
 
 
 def _run(stream, call):
@@ -645,14 +656,16 @@ def _run(stream, call):
 
 
 def _kv_q8(k_pool, v_pool, k_scale, v_scale):
-    """ABI view of an e4m3 cache, and its specs."""
+    """Specs of an e4m3 cache."""
     torch = _torch()
-    shape = nb, hkv, bs, d = _sizes(k_pool, "k_pool", 4)
-    specs = (("k_pool", k_pool, torch.float8_e4m3fn, shape), ("v_pool", v_pool, torch.float8_e4m3fn, shape),
-             ("k_scale", k_scale, torch.float32, (nb, hkv)), ("v_scale", v_scale, torch.float32, (nb, hkv)))
-    if not all(isinstance(x[1], torch.Tensor) for x in specs):
-        raise TypeError("pools and scales must be torch.Tensors")
-    return _KVQ8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, hkv, bs, d), specs
+    shape = nb, hkv, _, _ = _sizes(k_pool, "k_pool", 4)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    return (("k_pool", k_pool, f8, shape), ("v_pool", v_pool, f8, shape), ("k_scale", k_scale, f32, (nb, hkv)),
+            ("v_scale", v_scale, f32, (nb, hkv)))
+
+
+def _kv_q8_struct(specs) -> _KVQ8:
+    return _KVQ8(*[x[1].data_ptr() for x in specs], *specs[0][3])
 
 
 def kv_append_q8(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_pool, k_scale, v_scale,
@@ -665,16 +678,17 @@ def kv_append_q8(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_po
     request's count (read from cu_new_lens if None, which synchronizes)."""
     torch = _torch()
     L = load()
-    kv, specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
     total = _sizes(k_new, "k_new", 3)[0]
     B, mb = _sizes(block_tables, "block_tables", 2)
     code = _dtype_code(k_new)
-    new = (total, kv.num_kv_heads, kv.head_dim)
+    new = (total, k_pool.shape[1], k_pool.shape[3])
     _args(("k_new", k_new, k_new.dtype, new), ("v_new", v_new, k_new.dtype, new),
           ("cu_new_lens", cu_new_lens, torch.int32, (B + 1,)), ("kv_start", kv_start, torch.int32, (B,)),
           ("block_tables", block_tables, torch.int32, (B, mb)), *specs)
     if max_new_len is None:
         max_new_len = int((cu_new_lens[1:] - cu_new_lens[:-1]).max().item()) if B else 0
+    kv = _kv_q8_struct(specs)
     ab = _Append(k_new.data_ptr(), v_new.data_ptr(), cu_new_lens.data_ptr(), kv_start.data_ptr(),
                  block_tables.data_ptr(), B, total, int(max_new_len), mb)
     _check(_run(stream, lambda s: L.minipic_kv_append_q8(code, ctypes.byref(kv), ctypes.byref(ab), s)),
@@ -693,23 +707,25 @@ def attn_decode_weights_workspace_size(batch: int, num_q_heads: int, num_kv_head
                                                                  max_blocks_per_seq, block_size))
 
 
-def _decode_weights(fn, where, size, q, kv, specs, block_tables, block_starts, seq_lens, q_pos, rope, scale, out,
-                    lse, block_weights, workspace, stream):
+def _decode_weights(fn, where, size, struct, q, specs, block_tables, block_starts, seq_lens, q_pos, rope, scale,
+                    out, lse, block_weights, workspace, stream):
     torch = _torch()
     B, Hq, d = shape = _sizes(q, "q", 3)
     mb = _sizes(block_tables, "block_tables", 2)[1]
-    code, i32 = _dtype_code(q), torch.int32
-    rp, rope_specs = _rope16(rope, kv.head_dim, code == BF16)
-    _args(("q", q, q.dtype, (B, Hq, kv.head_dim)), *specs, ("block_tables", block_tables, i32, (B, mb)),
+    _, hkv, bs, kd = specs[0][3]
+    dt, code, i32 = q.dtype, _dtype_code(q), torch.int32
+    rope_specs = _rope16(rope, kd, code == BF16)
+    _args(("q", q, dt, (B, Hq, kd)), *specs, ("block_tables", block_tables, i32, (B, mb)),
           ("block_starts", block_starts, i32, (B, mb)), ("seq_lens", seq_lens, i32, (B,)),
-          ("q_pos", q_pos, i32, (B,)), *rope_specs, ("out", out, q.dtype, shape), ("lse", lse, torch.float32, (B, Hq)),
-          ("block_weights", block_weights, q.dtype, (B, kv.num_kv_heads, mb)), *_any("workspace", workspace))
+          ("q_pos", q_pos, i32, (B,)), *rope_specs, ("out", out, dt, shape), ("lse", lse, torch.float32, (B, Hq)),
+          ("block_weights", block_weights, dt, (B, hkv, mb)), *_any("workspace", workspace))
+    kv, rp = struct(specs), _rope16_struct(rope_specs)
 
     def call(s):
         o = torch.empty_like(q) if out is None else out
         ws = workspace
         if ws is None:
-            n = size(B, Hq, kv.num_kv_heads, d, mb, kv.block_size)
+            n = size(B, Hq, hkv, d, mb, bs)
             ws = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
         db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
                      q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
@@ -730,9 +746,9 @@ def attn_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_star
     (out, lse) like ``attn_decode``.  A workspace passed in must have been
     zeroed once."""
     L = load()
-    kv, specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
-    return _decode_weights(L.minipic_attn_decode_q8, "minipic_attn_decode_q8", attn_decode_q8_workspace_size, q, kv,
-                           specs, block_tables, block_starts, seq_lens, q_pos, rope, scale, out, lse, block_weights,
+    specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    return _decode_weights(L.minipic_attn_decode_q8, "minipic_attn_decode_q8", attn_decode_q8_workspace_size,
+                           _kv_q8_struct, q, specs, block_tables, block_starts, seq_lens, q_pos, rope, scale, out, lse, block_weights,
                            workspace, stream)
 
 
@@ -742,12 +758,12 @@ def attn_decode_weights(q, k_pool, v_pool, block_tables, block_starts, seq_lens,
     ``attn_decode_q8``), for eviction by attention weight.  bf16 takes the score
     product in fp16 (keys within +-65504)."""
     L = load()
-    nb, hkv, bs, d = shape = _sizes(k_pool, "k_pool", 4)
-    if block_weights is None or not isinstance(v_pool, _torch().Tensor):
-        raise TypeError("block_weights and v_pool must be torch.Tensors")
-    kv = _KV(k_pool.data_ptr(), v_pool.data_ptr(), nb, hkv, bs, d)
+    shape = _sizes(k_pool, "k_pool", 4)
+    _sizes(block_weights, "block_weights", 3)
+    _sizes(q, "q", 3)
     return _decode_weights(L.minipic_attn_decode_weights, "minipic_attn_decode_weights",
-                           attn_decode_weights_workspace_size, q, kv,
+                           attn_decode_weights_workspace_size,
+                           lambda sp: _KV(sp[0][1].data_ptr(), sp[1][1].data_ptr(), *sp[0][3]), q,
                            (("k_pool", k_pool, q.dtype, shape), ("v_pool", v_pool, q.dtype, shape)), block_tables,
                            block_starts, seq_lens, q_pos, rope, scale, out, lse, block_weights, workspace, stream)
 
@@ -765,22 +781,24 @@ def attn_prefill_q8(q, cu_q_lens, q_pos, k_pool, v_pool, k_scale, v_scale, block
     ``attn_prefill``."""
     torch = _torch()
     L = load()
-    kv, specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
+    _, hkv, bs, kd = specs[0][3]
     total_q, Hq, d = shape = _sizes(q, "q", 3)
     B, mb = _sizes(block_tables, "block_tables", 2)
     i32 = torch.int32
-    rp, rope_specs = _rope16(rope, kv.head_dim, True)
-    _args(("q", q, torch.bfloat16, (total_q, Hq, kv.head_dim)), ("cu_q_lens", cu_q_lens, i32, (B + 1,)),
+    rope_specs = _rope16(rope, kd, True)
+    _args(("q", q, torch.bfloat16, (total_q, Hq, kd)), ("cu_q_lens", cu_q_lens, i32, (B + 1,)),
           ("q_pos", q_pos, i32, (total_q,)), *specs, ("block_tables", block_tables, i32, (B, mb)),
           ("block_starts", block_starts, i32, (B, mb)), ("kv_lens", kv_lens, i32, (B,)), *rope_specs,
           ("out", out, torch.bfloat16, shape), ("lse", lse, torch.float32, (total_q, Hq)),
           *_any("workspace", workspace))
+    kv, rp = _kv_q8_struct(specs), _rope16_struct(rope_specs)
 
     def call(s):
         o = torch.empty_like(q) if out is None else out
         ws = workspace
         if ws is None:
-            n = attn_prefill_q8_workspace_size(B, Hq, kv.num_kv_heads, d, max_q_len, mb, kv.block_size)
+            n = attn_prefill_q8_workspace_size(B, Hq, hkv, d, max_q_len, mb, bs)
             ws = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
         pb = _Prefill(q.data_ptr(), cu_q_lens.data_ptr(), q_pos.data_ptr(), block_tables.data_ptr(),
                       block_starts.data_ptr(), kv_lens.data_ptr(), B, total_q, int(max_q_len), mb, o.data_ptr(),
