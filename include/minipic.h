@@ -409,23 +409,27 @@ size_t minipic_attn_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads,
  * long as each has at most 16384 (request, kv head) pairs (else zero it when
  * the shape changes); calls whose work overlaps on the GPU need workspaces of
  * their own.  Errors as for minipic_attn_decode; UNSUPPORTED also for more than
- * 65535 requests or kv heads. */
+ * 65535 requests or kv heads, num_blocks * num_kv_heads * 16 or
+ * batch * max_blocks_per_seq above 2^31 - 1, or 2^38 table entries times kv
+ * heads. */
 minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
                                       const minipic_rope* rope, const minipic_decode_batch* batch, float scale,
                                       void* block_weights, void* workspace, size_t workspace_bytes,
                                       minipic_stream_t stream);
 
-/* Workspace bytes of minipic_attn_prefill_q8: the batch's blocks in bf16, K and
+/* Workspace bytes of minipic_attn_prefill_q8: the batch's blocks in 16 bits, K and
  * V, in request order (4 bytes per key, kv head and head dim element), and a table. */
 size_t minipic_attn_prefill_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                               int32_t head_dim, int32_t max_q_len, int32_t max_blocks_per_seq,
                                               int32_t block_size);
 
 /* Chunked prefill over the 8-bit cache (the chunk's own keys are its last ones
- * and were appended before): the gathered blocks are widened to bf16 in the
- * workspace (exact where a scale is a power of two, as the append writes them,
- * else rounded once) and minipic_attn_prefill's kernel runs over them.  bf16
- * only.  The workspace needs no initial value and holds nothing between calls.
+ * and were appended before): the gathered blocks are widened in the workspace --
+ * keys rotated in fp32 at their positions and rounded to fp16 (outside its range:
+ * MINIPIC_DEVERR_RANGE), values to bf16 (exact where a scale is a power of two, as
+ * the append writes them, else rounded once) -- and minipic_attn_prefill's kernel
+ * runs over them.  bf16 only.  The workspace needs no initial value and holds
+ * nothing between calls; calls whose work overlaps need workspaces of their own.
  * Errors as for minipic_attn_prefill, WORKSPACE when it is too small,
  * UNSUPPORTED when batch * max_blocks_per_seq * num_kv_heads * 16 exceeds
  * 2^31 - 1. */

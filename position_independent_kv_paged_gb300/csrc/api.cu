@@ -739,7 +739,11 @@ minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, 
   if (empty) return MINIPIC_OK;
   if (!aligned16(block_weights)) return MINIPIC_ERR_INVALID;
   if (b->batch > kMaxGridYZ || kv->num_kv_heads > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
-  if ((long long)kv->num_blocks * kv->num_kv_heads * 16 > 0x7fffffffLL) return MINIPIC_ERR_UNSUPPORTED;  // TMA rows
+  // tile numbers, sums of lengths in blocks and the blocks of one CTA's range are 32-bit
+  const long long entries = (long long)b->batch * b->max_blocks_per_seq;
+  if ((long long)kv->num_blocks * kv->num_kv_heads * 16 > 0x7fffffffLL || entries > 0x7fffffffLL ||
+      entries * kv->num_kv_heads > (1LL << 38))
+    return MINIPIC_ERR_UNSUPPORTED;
   int* err = nullptr;
   int sms = 0;
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
@@ -809,7 +813,11 @@ minipic_status minipic_attn_prefill_q8(minipic_dtype dtype, int32_t num_q_heads,
   ra.k_scale = kv->k_scale;
   ra.v_scale = kv->v_scale;
   ra.block_tables = b->block_tables;
+  ra.block_starts = b->block_starts;
   ra.kv_lens = b->kv_lens;
+  ra.cos_sin = p.cos_sin;
+  ra.max_pos = p.max_pos;
+  ra.err = p.err;
   ra.k_out = reinterpret_cast<uint16_t*>(ws);
   ra.v_out = reinterpret_cast<uint16_t*>(ws + w.pool_bytes);
   ra.table_out = reinterpret_cast<int32_t*>(ws + 2 * w.pool_bytes);
@@ -823,7 +831,7 @@ minipic_status minipic_attn_prefill_q8(minipic_dtype dtype, int32_t num_q_heads,
   p.block_tables = ra.table_out;
   p.num_blocks = (int)scratch_blocks;
   cudaError_t e = launch_kv_restore_q8(ra, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = launch_prefill_tc(p, true, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = launch_prefill_rotated(p, (cudaStream_t)stream);
   return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }
 

@@ -36,7 +36,7 @@
 //
 // With WTS the body also records, per (request, query head, block), log2 of the
 // block's sum of 2^score, and the denominators, for block_weights.cu: three
-// shuffles and one small store per head column and block.  It takes the score
+// shuffles and one small store per two head columns and block.  It takes the score
 // product in fp16 instead (keys and the query, scaled by a power of two to a
 // largest element in [1, 2), widen exactly from bf16 and are rotated with the
 // fp16 table): weights are exponentials of the scores, and bf16's three roundings
@@ -543,7 +543,7 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
     bool any_corr = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float pv[4];
+      float pv[4], es[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float f = WTS ? qcol[nt][j] : qs;
@@ -560,17 +560,22 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
         const float pa = exp2f(sa - muse), pbv = exp2f(sb - muse);
         lrun[nt][j] = fmaf(lrun[nt][j], corr[nt][j], pa + pbv);
         mrun[nt][j] = mnew;
-        if constexpr (WTS) {
-          float e = pa + pbv;
-          e += __shfl_xor_sync(0xffffffffu, e, 4);
-          e += __shfl_xor_sync(0xffffffffu, e, 8);
-          e += __shfl_xor_sync(0xffffffffu, e, 16);
-          const int head = 8 * nt + 2 * tig + j;
-          if (g8 == 0 && head < G)
-            a.w_raw[(((size_t)r * a.Hkv + hk) * mb + b) * G + head] = e == 0.f ? -CUDART_INF_F : muse + log2f(e);
-        }
+        if constexpr (WTS) es[j] = pa + pbv;
         pv[j] = pa;
         pv[2 + j] = pbv;
+      }
+      if constexpr (WTS) {
+        // sums of both columns over the fragment rows: the first step leaves even rows with column 0 and odd rows
+        // with column 1
+        const bool odd = g8 & 1;
+        float e = (odd ? es[1] : es[0]) + __shfl_xor_sync(0xffffffffu, odd ? es[0] : es[1], 4);
+        e += __shfl_xor_sync(0xffffffffu, e, 8);
+        e += __shfl_xor_sync(0xffffffffu, e, 16);
+        const int head = 8 * nt + 2 * tig + g8;
+        const float m = odd ? mrun[nt][1] : mrun[nt][0];
+        if (g8 < 2 && head < G)
+          a.w_raw[(((size_t)r * a.Hkv + hk) * mb + b) * G + head] =
+              e == 0.f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.f : m) + log2f(e);
       }
       pb0[nt] = ptx::movmatrix_trans(ptx::pack_bf16(pv[0], pv[1]));  // keys 0..7
       pb1[nt] = ptx::movmatrix_trans(ptx::pack_bf16(pv[2], pv[3]));  // keys 8..15

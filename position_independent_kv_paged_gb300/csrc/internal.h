@@ -99,6 +99,9 @@ cudaError_t launch_block_weights(const DecodeArgs& a, bool bf16, cudaStream_t s)
 cudaError_t launch_prefill_tc(const PrefillArgs& a, bool rotate, cudaStream_t s);
 // Head dim 128: CTA-pair (cta_group::2) form, called by launch_prefill_tc.
 cudaError_t launch_prefill_pair(const PrefillArgs& a, bool rotate, cudaStream_t s);
+// Both over a pool whose keys are rotated already at their positions, as fp16.
+cudaError_t launch_prefill_rotated(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefill_pair_rotated(const PrefillArgs& a, cudaStream_t s);
 // One grid of prefill tiles followed by decode splits (both with rotation).
 cudaError_t launch_mixed(const PrefillArgs& p, const DecodeArgs& d, cudaStream_t s);
 // Head dim 128: one grid of CTA-pair prefill clusters and decode clusters.
@@ -134,18 +137,23 @@ struct AppendQ8Args {
 };
 cudaError_t launch_kv_append_q8(const AppendQ8Args& a, bool bf16, cudaStream_t s);
 
-// e4m3 blocks of a prefill batch -> bf16 blocks of a scratch pool in request order.
+// e4m3 blocks of a prefill batch -> 16-bit blocks of a scratch pool in request
+// order, keys rotated at their positions (fp16), values bf16.
 struct RestoreArgs {
   const uint8_t* k_pool;
   const uint8_t* v_pool;
   const float* k_scale;
   const float* v_scale;
   const int32_t* block_tables;  // [batch][max_blocks]
+  const int32_t* block_starts;
   const int32_t* kv_lens;
-  uint16_t* k_out;              // [batch * max_blocks][Hkv][16][D] bf16
-  uint16_t* v_out;
+  const float* cos_sin;         // [max_pos][D]
+  int max_pos;
+  uint16_t* k_out;              // [batch * max_blocks][Hkv][16][D] fp16
+  uint16_t* v_out;              // bf16
   int32_t* table_out;           // [batch][max_blocks] ids in the scratch pool (-1: unusable id)
   int batch, max_blocks, num_blocks, Hkv, D;
+  int* err;
 };
 cudaError_t launch_kv_restore_q8(const RestoreArgs& a, cudaStream_t s);
 

@@ -123,8 +123,9 @@ __device__ __forceinline__ void rot_pack(U4& x, U4& y, const uint64_t (&c2)[4], 
 
 // One CTA computes query-tile pair `pair` of request r and kv head hk and
 // loads every K~/V box it reads itself.  vmap_p is the block view of the V pool
-// (make_pool_block_map).
-template <int D, bool ROPE, int NB = kNB, int NSK = kNSK, int NSV = kNSV>
+// (make_pool_block_map).  With ROPE and not KROT the pool holds the keys rotated
+// already, in fp16.
+template <int D, bool ROPE, int NB = kNB, int NSK = kNSK, int NSV = kNSV, bool KROT = ROPE>
 __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p,
                                              const PrefillLaunch2& L, const int pair, const int n_pairs,
                                              const int hk, const int r, uint8_t* smem_raw) {
@@ -239,7 +240,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
             m[2 * NB + lane] = (flag & 1) ? my_ph : -1;
           }
           const unsigned kv = __ballot_sync(FULL, flag & 1);
-          const unsigned rw = __ballot_sync(FULL, ROPE && (flag & 3) == 3);
+          const unsigned rw = __ballot_sync(FULL, KROT && (flag & 3) == 3);
           const int ph_l = __shfl_sync(FULL, my_ph, blk);
           const int st_l = __shfl_sync(FULL, my_st, blk);
           __syncwarp();
@@ -251,7 +252,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
               const uint32_t dst = sbase + G_::OFF_K + s * G_::KTILE + hh * (BN * 128) + blk * 2048;
               ptx::tma_load_2d(dst, &kmap, 64 * hh, (ph_l * a.Hkv + hk) * 16, bar(G_::B_KFULL + s));
             }
-          } else if (ROPE && lane < NB * G_::HALVES + NB) {
+          } else if (KROT && lane < NB * G_::HALVES + NB) {
             if ((rw >> blk) & 1u) {
               const uint32_t dst = sbase + G_::OFF_RS + (s * NB + blk) * G_::ROWB;
               ptx::bulk_load(dst, a.cos_sin + (size_t)st_l * D, G_::ROWB, bar(G_::B_KFULL + s));
@@ -420,7 +421,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
     const int sp = (rt / G_::NFG) & 7;
     const int bg = rt / (G_::NFG * 8);
     uint64_t rsc[2][4], rss[2][4];
-    if constexpr (ROPE) {
+    if constexpr (KROT) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float* tr = a.cos_sin + (size_t)min(2 * sp + k, a.max_pos - 1) * D;
@@ -441,7 +442,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
       }
       const int* m = meta + 3 * NB * s;
       uint8_t* sk = sg + G_::OFF_K + s * G_::KTILE;
-      if constexpr (ROPE) {
+      if constexpr (KROT) {
         // loads for every key first (stage and start rows are always addressable),
         // stores only for valid keys: no branch between keys, so their loads overlap
         uint32_t wk = 0u;  // fp16 range watch over the stored keys

@@ -176,8 +176,10 @@ __device__ __forceinline__ void regs_dec() {
 }
 
 // One CTA of the pair that computes query-tile pair `pair` of request r and kv
-// head hk (both CTAs of a cluster call it with the same item).
-template <bool ROPE, int NSK, int NSV>
+// head hk (both CTAs of a cluster call it with the same item).  With ROPE and
+// not KROT the pool holds the keys rotated already, in fp16: the query is
+// prepared as with rotation and the key tiles go to the product as they arrive.
+template <bool ROPE, int NSK, int NSV, bool KROT = ROPE>
 __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensorMap& vmap, const PairLaunch& L,
                                          const int pair, const int hk, const int r, uint8_t* smem_raw) {
   using P_ = PP<NSK, NSV>;
@@ -461,7 +463,7 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
         if (lane == 0) atomicOr(a.err, kErrTimeout);
         break;
       }
-      if constexpr (ROPE) {
+      if constexpr (KROT) {
         const int* m = meta + P_::META * s;
         uint8_t* sk = sg + P_::OFF_K + s * P_::KTILE;
         // every load first (an unusable key reads table row 0), stores only for
@@ -768,13 +770,14 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
   ptx::cluster_sync_relaxed();  // neither CTA leaves while the pair's TMEM is being released
 }
 
-template <bool ROPE, int NSK, int NSV>
+template <bool ROPE, int NSK, int NSV, bool KROT>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const PairLaunch L) {
   extern __shared__ uint8_t smem_raw[];
   // heaviest (latest) query-tile pairs first
-  pair_cta<ROPE, NSK, NSV>(kmap, vmap, L, L.n_pairs - 1 - (int)(blockIdx.x >> 1), blockIdx.y, blockIdx.z, smem_raw);
+  pair_cta<ROPE, NSK, NSV, KROT>(kmap, vmap, L, L.n_pairs - 1 - (int)(blockIdx.x >> 1), blockIdx.y, blockIdx.z,
+                                 smem_raw);
 }
 
 // Mixed continuous batch in one launch (the device side of interleaved
@@ -860,12 +863,12 @@ cudaError_t launch_mixed_t(const PrefillArgs& p, const DecodeArgs& d, cudaStream
   return cudaLaunchKernelEx(&cfg, mixed_pair_kernel<NT>, km, vm, kb, vb, L, d, (int)n_pre, (int)n_dec);
 }
 
-template <bool ROPE>
+template <bool ROPE, bool KROT = ROPE>
 cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
   using P_ = PP<kNSK, kNSV>;
   const int smem = P_::TOTAL + 1024;
   static bool done[64] = {false};
-  cudaError_t e = set_smem_once(prefill_pair_kernel<ROPE, kNSK, kNSV>, smem, done);
+  cudaError_t e = set_smem_once(prefill_pair_kernel<ROPE, kNSK, kNSV, KROT>, smem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const long long rows = (long long)a.num_blocks * a.Hkv * 16;
@@ -884,7 +887,7 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<ROPE, kNSK, kNSV>, km, vm, L);
+  return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<ROPE, kNSK, kNSV, KROT>, km, vm, L);
 }
 
 }  // namespace
@@ -892,6 +895,10 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
 cudaError_t launch_prefill_pair(const PrefillArgs& a, bool rotate, cudaStream_t s) {
   if (a.D != D) return cudaErrorInvalidValue;
   return rotate ? launch_t<true>(a, s) : launch_t<false>(a, s);
+}
+
+cudaError_t launch_prefill_pair_rotated(const PrefillArgs& a, cudaStream_t s) {
+  return a.D == D ? launch_t<true, false>(a, s) : cudaErrorInvalidValue;
 }
 
 cudaError_t launch_mixed_pair(const PrefillArgs& p, const DecodeArgs& d, cudaStream_t s) {

@@ -54,6 +54,9 @@ def test_decode_q8_refusals(lib):
     assert call_decode(lib, scale=float("nan")) == 1
     assert call_decode(lib, bw=0x8004) == 1                   # misaligned block weights
     assert call_decode(lib, db=decode(B=65536)) == 2
+    assert call_decode(lib, db=decode(B=60000, mb=40000)) == 2   # 32-bit sums of blocks
+    assert call_decode(lib, kv=kvq8(nb=2 ** 30)) == 2            # 32-bit tile numbers
+    assert call_decode(lib, Hq=60000, kv=kvq8(nb=1, hkv=60000), db=decode(B=100, mb=10 ** 6)) == 2
     assert call_decode(lib, db=decode(B=0)) == 0
     f = lib.minipic_attn_decode_q8
     assert f(1, 4, None, REF(rope()), REF(decode()), 0.0, None, None, 0, None) == 1

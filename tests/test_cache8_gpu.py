@@ -159,6 +159,129 @@ def test_one_workspace_for_calls_of_other_shapes(env, dtype):
         check_decode(env, cases[i], decode(env, cases[i], workspace=ws, weights=i != 1))
 
 
+def torch_reference(torch, t, base, Hkv):
+    """The reference of cache8.attention for one row per request, in float64 on the GPU (for sizes numpy is slow at)."""
+    q, B = t["q"].double(), t["q"].shape[0]
+    Hq, d = q.shape[1:]
+    G, mb = Hq // Hkv, t["block_tables"].shape[1]
+    res = {k: np.zeros((B, Hq, d)) for k in ("out", "spread", "mass")}
+    res.update(lse=np.full((B, Hq), -np.inf), smax=np.zeros((B, Hq)), weights=np.zeros((B, Hkv, mb)))
+
+    def turn(x, pos):   # [..., n, d] rotated at pos [n]
+        i = torch.arange(d // 2, device=x.device, dtype=torch.float64)
+        a = pos.double()[:, None] * base ** (-2 * i / d)
+        x1, x2 = x[..., :d // 2], x[..., d // 2:]
+        return torch.cat([x1 * a.cos() - x2 * a.sin(), x2 * a.cos() + x1 * a.sin()], -1)
+    for r in range(B):
+        n = int(t["seq_lens"][r])
+        if not n:
+            continue
+        j = torch.arange(n, device=q.device)
+        blk = t["block_tables"][r].long()[j // 16]
+        pos = t["block_starts"][r].long()[j // 16] + j % 16
+        qr = turn(q[r], t["q_pos"][r].expand(Hq))
+        for g in range(Hkv):
+            k, v = (t[x + "_pool"].view(torch.uint8)[blk, g, j % 16].view(torch.float8_e4m3fn).double() *
+                    t[x + "_scale"].double()[blk, g][:, None] for x in "kv")
+            k = turn(k, pos)
+            h = slice(g * G, (g + 1) * G)
+            s = qr[h] @ k.T / d ** 0.5
+            p = torch.softmax(s, 1)
+            o = p @ v
+            res["out"][r, h], res["lse"][r, h] = f64(o), f64(torch.logsumexp(s, 1))
+            res["mass"][r, h] = f64(p @ v.abs())
+            for i in range(G):
+                res["spread"][r, g * G + i] = f64(p[i] @ (v - o[i]).abs())
+            res["smax"][r, h] = f64(qr[h].norm(dim=1) * k.norm(dim=1).max() / d ** 0.5)
+            w = torch.zeros(-(-n // 16) * 16, dtype=torch.float64, device=q.device)
+            w[:n] = p.sum(0)
+            res["weights"][r, g, :w.numel() // 16] = f64(w.view(-1, 16).sum(1))
+    return res
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d", [
+    ([0, 3, 40, 0, 17, 1, 64] * 45, 4, 2, 64),           # more requests than a CTA has threads, many of them empty
+    ([40000], 8, 1, 128),                                 # one pair shared by many CTAs
+    ([70001, 5, 90000], 20, 2, 64),                       # groups of 10
+    ([33000, 0, 60000, 16, 52017, 49999], 28, 28, 128),   # ranges longer than one staging of metadata
+    ([33000, 0, 60000, 16, 52017, 49999], 56, 8, 128),
+])
+def test_decode_at_sizes_that_cut_pairs_and_ranges(env, lens, Hq, Hkv, d):
+    torch, mp, dev = env
+    g = torch.Generator(device=dev).manual_seed(len(lens) + Hq)
+    B, mb = len(lens), -(-max(lens) // 16)
+    n = torch.tensor(lens, device=dev)
+    nb = int(((n + 15) // 16).sum()) + 1
+    order = torch.randperm(nb, generator=g, device=dev)
+    used = torch.arange(mb, device=dev) * 16 < n[:, None]
+    tables = torch.full((B, mb), -1, dtype=torch.int32, device=dev)
+    tables[used] = order[:int(used.sum())].int()
+    gaps = torch.randint(0, 3, (B, mb), generator=g, device=dev).cumsum(1)
+    starts = torch.where(used, torch.arange(mb, device=dev) * 16 + gaps, 0).int()
+    t = {}
+    for x in "kv":
+        y = torch.randn(nb, Hkv, 16, d, generator=g, device=dev)
+        s = torch.exp2(torch.ceil(torch.log2(y.abs().amax((2, 3)) / 448)))
+        t[x + "_scale"], t[x + "_pool"] = s, (y / s[..., None, None]).to(torch.float8_e4m3fn)
+    last = (n - 1).clamp(min=0)
+    t.update(q=torch.randn(B, Hq, d, generator=g, device=dev).bfloat16(), block_tables=tables, block_starts=starts,
+             seq_lens=n.int(), q_pos=(starts.long().gather(1, (last // 16)[:, None])[:, 0] + last % 16 + 1).int())
+    rope = mp.rope_table(int(starts.max()) + 40, d, 1e4, device=dev)
+    ref = torch_reference(torch, t, 1e4, Hkv)
+    ws = torch.zeros(mp.attn_decode_q8_workspace_size(B, Hq, Hkv, d, mb), dtype=torch.uint8, device=dev)
+    outs = []
+    for weights in (True, False, True):
+        bw = torch.full((B, Hkv, mb), 7.0, dtype=torch.bfloat16, device=dev) if weights else None
+        lse = torch.empty(B, Hq, device=dev)
+        out, _ = mp.attn_decode_q8(t["q"], t["k_pool"], t["v_pool"], t["k_scale"], t["v_scale"], tables, starts,
+                                   t["seq_lens"], t["q_pos"], rope, lse=lse, block_weights=bw, workspace=ws)
+        torch.cuda.synchronize()
+        check_attention(f64(out), ref, "bf16", d, max(lens))
+        fin = np.isfinite(ref["lse"])
+        assert np.array_equal(np.isfinite(f64(lse)), fin)
+        assert np.abs(f64(lse)[fin] - ref["lse"][fin]).max() <= 1e-2
+        if weights:
+            check_weights(f64(bw), ref, "bf16", d, lens, 7.0)
+        outs.append((out, lse, bw))
+    assert all(torch.equal(a, b) for a, b in zip(outs[0], outs[2]))   # the parts merge in a fixed order
+    assert mp.device_error() == 0
+
+
+def test_two_graphs_on_one_workspace(env):
+    """Two captured calls of different shapes share a workspace and are replayed in turn."""
+    torch, mp, dev = env
+    cases = [Case(60, (2500, 300), 8, 2, 128, "bf16"), Case(61, (40,) * 30 + (900,), 4, 4, 64, "bf16")]
+    ws = torch.zeros(max(mp.attn_decode_q8_workspace_size(len(c.lens), c.Hq, c.Hkv, c.d, c.tables.shape[1])
+                         for c in cases), dtype=torch.uint8, device=dev)
+    runs = []
+    for c in cases:
+        t = c.device(torch, dev)
+        rope = mp.rope_table(c.max_pos, c.d, c.base, device=dev)
+        out = torch.empty_like(t["q"])
+        bw = torch.zeros(len(c.lens), c.Hkv, c.tables.shape[1], dtype=torch.bfloat16, device=dev)
+
+        def call(t=t, rope=rope, out=out, bw=bw):
+            mp.attn_decode_q8(t["q"], t["k_pool"], t["v_pool"], t["k_scale"], t["v_scale"], t["block_tables"],
+                              t["block_starts"], t["seq_lens"], t["q_pos"], rope, out=out, block_weights=bw,
+                              workspace=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        runs.append((c, g, out, bw, t))
+    for _ in range(3):
+        for c, g, out, bw, _t in runs:
+            out.zero_()
+            bw.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    for c, g, out, bw, _t in runs:
+        ref = c.reference()
+        check_attention(f64(out), ref, "bf16", c.d, max(c.lens))
+        check_weights(f64(bw), ref, "bf16", c.d, c.lens, 0.0)
+
+
 @pytest.mark.parametrize("dtype,Hq,Hkv,d", [("f32", 8, 2, 64), ("bf16", 4, 2, 64), ("bf16", 32, 2, 64),
                                             ("bf16", 8, 1, 128), ("bf16", 28, 4, 128), ("bf16", 16, 1, 128)])
 def test_decode_weights_over_the_unquantised_cache(env, dtype, Hq, Hkv, d):
