@@ -22,9 +22,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) block_weights_kernel(DecodeArgs a) {
   const int r = blockIdx.z, g = blockIdx.y;
   const int b = blockIdx.x * kThreads + threadIdx.x;
-  int L = a.seq_lens[r];
-  L = L < 0 ? 0 : min(L, a.max_blocks * a.BS);
-  if (b >= (L + a.BS - 1) / a.BS) return;
+  const int L = a.seq_lens[r];
+  if (L <= 0 || b >= min((L >> 4) + ((L & 15) != 0), a.max_blocks)) return;
   const size_t at = ((size_t)r * a.Hkv + g) * a.max_blocks + b;
   const float* raw = a.w_raw + at * a.G;
   const float* lse = a.w_lse + (size_t)r * a.Hq + (size_t)g * a.G;
