@@ -169,17 +169,17 @@ minipic_status build_decode(minipic_dtype dtype, int32_t num_q_heads, const mini
   return MINIPIC_OK;
 }
 
-// Partial results of an e4m3 or block-weight decode, one head each: two per CTA of the e4m3 tensor-core kernel's
-// grid, else one per split and query head.
-long long count_partials(const DecodePlan& p, bool q8, int batch, int Hq, int G) {
-  if (q8 && p.use_mma) return 2LL * p.n_split * G;
+// Partial results of an e4m3 or block-weight decode, one head each: two per CTA of the tensor-core kernel's grid,
+// else one per split and query head.
+long long count_partials(const DecodePlan& p, int batch, int Hq, int G) {
+  if (p.use_mma) return 2LL * p.n_split * G;
   return p.n_split > 1 ? (long long)batch * Hq * p.n_split : 0;
 }
 
 // Place the workspace of an e4m3 or block-weight decode.
 minipic_status place_weights_ws(DecodeArgs& a, const DecodePlan& plan, void* block_weights, void* workspace,
                                 size_t workspace_bytes) {
-  const long long partials = count_partials(plan, a.k_scale != nullptr, a.batch, a.Hq, a.G);
+  const long long partials = count_partials(plan, a.batch, a.Hq, a.G);
   const DecodeWsW w = decode_ws_weights(a.batch, a.Hq, a.Hkv, a.D, partials, block_weights ? a.max_blocks : 0);
   if (w.total > 0 && (!workspace || workspace_bytes < w.total || !aligned16(workspace))) return MINIPIC_ERR_WORKSPACE;
   char* p = static_cast<char*>(workspace);
@@ -391,14 +391,14 @@ DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs,
   return p;
 }
 
-DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms) {
+DecodePlan plan_decode_list(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms) {
   if (!bf16) return plan_decode(batch, Hkv, G, D, max_blocks, 16, false, num_sms);
   // tensor-core path: as many CTAs as fit the device at once (the kernel's occupancy: its registers at head dim
   // 128 hold 3 CTAs of 4 warps per SM, 2 for groups above 8 heads; at 64 four), or as there are blocks
   DecodePlan p{max_blocks, 1, true, G > 8 ? 2 : (D == 64 ? 4 : 3)};
   const long long total = (long long)batch * Hkv * max_blocks;
   long long resident = (long long)num_sms * p.ctas_per_sm;
-  const int most = G > 8 ? kQ8MaxCtas / 2 : kQ8MaxCtas;  // the kernel's merge holds a weight per CTA and head
+  const int most = G > 8 ? kListMaxCtas / 2 : kListMaxCtas;  // the kernel's merge holds a weight per CTA and head
   if (resident > most) resident = most;
   p.n_split = (int)(total < resident ? total : resident);
   return p;
@@ -666,24 +666,31 @@ namespace {
 
 constexpr int kMaxGridYZ = 65535;
 
-size_t weights_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t mb, int32_t bs, bool q8) {
+size_t weights_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t mb, int32_t bs) {
   if (batch <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || mb <= 0 || bs <= 0 || Hq % Hkv) return 0;
   const int sms = current_sms();
   size_t most = 0;
   for (int bf16 = 0; bf16 < 2; ++bf16) {
-    const DecodePlan p = q8 ? plan_decode_q8(batch, Hkv, Hq / Hkv, D, mb, bf16 != 0, sms)
-                            : plan_decode(batch, Hkv, Hq / Hkv, D, mb, bs, bf16 != 0, sms);
-    const size_t n = decode_ws_weights(batch, Hq, Hkv, D, count_partials(p, q8, batch, Hq, Hq / Hkv), mb).total;
+    const DecodePlan p = plan_decode_list(batch, Hkv, Hq / Hkv, D, mb, bf16 != 0, sms);
+    const size_t n = decode_ws_weights(batch, Hq, Hkv, D, count_partials(p, batch, Hq, Hq / Hkv), mb).total;
     most = n > most ? n : most;
   }
   return most;
+}
+
+// What the one-list decode's 32-bit numbers hold: tile numbers, sums of lengths in blocks, the blocks of a CTA's range.
+bool list_fits(const minipic_kv_pool& kv, const minipic_decode_batch& b) {
+  const long long entries = (long long)b.batch * b.max_blocks_per_seq;
+  return b.batch <= kMaxGridYZ && kv.num_kv_heads <= kMaxGridYZ &&
+         (long long)kv.num_blocks * kv.num_kv_heads * 16 <= 0x7fffffffLL && entries <= 0x7fffffffLL &&
+         entries * kv.num_kv_heads <= (1LL << 38);
 }
 
 }  // namespace
 
 size_t minipic_attn_decode_weights_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                   int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size) {
-  return weights_ws_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, false);
+  return weights_ws_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size);
 }
 
 minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
@@ -698,20 +705,20 @@ minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_he
   if (bf16 && (!rope->cos_sin_f16 || !aligned16(rope->cos_sin_f16))) return MINIPIC_ERR_INVALID;
   if (empty) return MINIPIC_OK;
   if (!block_weights || !aligned16(block_weights)) return MINIPIC_ERR_INVALID;
-  if (b->batch > kMaxGridYZ || kv->num_kv_heads > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
+  if (!list_fits(*kv, *b)) return MINIPIC_ERR_UNSUPPORTED;
   int* err = nullptr;
   int sms = 0;
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
-  const DecodePlan plan = plan_decode(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
-                                      b->max_blocks_per_seq, kv->block_size, bf16, sms);
+  const DecodePlan plan = plan_decode_list(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
+                                           b->max_blocks_per_seq, bf16, sms);
   DecodeArgs a = decode_args(bf16, num_q_heads, kv, rope, b, scale, plan, err);
   st = place_weights_ws(a, plan, block_weights, workspace, workspace_bytes);
   if (st != MINIPIC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
   a.cs_f16 = rope->cos_sin_f16;
-  // as for attn_decode: the tensor-core kernel merges its splits itself, with no pool every key is masked
+  // the tensor-core kernel merges its parts itself; with no pool every key is masked
   const bool mma = plan.use_mma && kv->num_blocks > 0;
-  cudaError_t e = mma ? launch_decode_mma_weights(a, s) : launch_decode_simt_weights(a, bf16, s);
+  cudaError_t e = mma ? launch_decode_weights(a, s) : launch_decode_simt_weights(a, bf16, s);
   if (e == cudaSuccess && !mma) e = launch_decode_merge(a, bf16, s);
   if (e == cudaSuccess) e = launch_block_weights(a, bf16, s);
   return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
@@ -719,7 +726,7 @@ minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_he
 
 size_t minipic_attn_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                              int32_t head_dim, int32_t max_blocks_per_seq, int32_t block_size) {
-  return weights_ws_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, true);
+  return weights_ws_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size);
 }
 
 minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
@@ -738,17 +745,12 @@ minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, 
   if (bf16 && (!rope->cos_sin_f16 || !aligned16(rope->cos_sin_f16))) return MINIPIC_ERR_INVALID;
   if (empty) return MINIPIC_OK;
   if (!aligned16(block_weights)) return MINIPIC_ERR_INVALID;
-  if (b->batch > kMaxGridYZ || kv->num_kv_heads > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
-  // tile numbers, sums of lengths in blocks and the blocks of one CTA's range are 32-bit
-  const long long entries = (long long)b->batch * b->max_blocks_per_seq;
-  if ((long long)kv->num_blocks * kv->num_kv_heads * 16 > 0x7fffffffLL || entries > 0x7fffffffLL ||
-      entries * kv->num_kv_heads > (1LL << 38))
-    return MINIPIC_ERR_UNSUPPORTED;
+  if (!list_fits(pool, *b)) return MINIPIC_ERR_UNSUPPORTED;
   int* err = nullptr;
   int sms = 0;
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
-  const DecodePlan plan = plan_decode_q8(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
-                                         b->max_blocks_per_seq, bf16, sms);
+  const DecodePlan plan = plan_decode_list(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
+                                           b->max_blocks_per_seq, bf16, sms);
   DecodeArgs a = decode_args(bf16, num_q_heads, &pool, rope, b, scale, plan, err);
   a.k_scale = kv->k_scale;
   a.v_scale = kv->v_scale;
@@ -756,7 +758,7 @@ minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, 
   if (st != MINIPIC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
   a.cs_f16 = rope->cos_sin_f16;
-  // the tensor-core kernel merges its splits itself; with no pool there is nothing to map and every key is masked
+  // the tensor-core kernel merges its parts itself; with no pool every key is masked
   const bool mma = plan.use_mma && kv->num_blocks > 0;
   cudaError_t e = mma ? launch_decode_q8(a, s) : launch_decode_simt_q8(a, bf16, s);
   if (e == cudaSuccess && !mma) e = launch_decode_merge(a, bf16, s);

@@ -33,15 +33,6 @@
 // row per block instead of sixteen.  The rows are the bf16 form of the table
 // over signed angles (cos | sin | -sin of t - b, 384 bytes at d 128): the
 // rotation reads its bf16 operands directly, whatever the sign of t - b.
-//
-// With WTS the body also records, per (request, query head, block), log2 of the
-// block's sum of 2^score, and the denominators, for block_weights.cu: three
-// shuffles and one small store per two head columns and block.  It takes the score
-// product in fp16 instead (keys and the query, scaled by a power of two to a
-// largest element in [1, 2), widen exactly from bf16 and are rotated with the
-// fp16 table): weights are exponentials of the scores, and bf16's three roundings
-// of either operand showed in them (output error 5.4e-3 of its norm at d 64 where
-// the fp16 form has 2e-3).  Keys past fp16's range become infinite there.
 #pragma once
 
 #include <math_constants.h>
@@ -133,27 +124,6 @@ __device__ __forceinline__ void rotate_pair_bf16(U4& x, U4& y, const uint32_t (&
   y = U4{yo[0], yo[1], yo[2], yo[3]};
 }
 
-// bf16 pairs -> fp16 pairs (exact from 2^-14 to 65504)
-__device__ __forceinline__ U4 bf_to_h(const U4& v) {
-  return U4{ptx::pack_f16(ptx::bf_lo(v.x), ptx::bf_hi(v.x)), ptx::pack_f16(ptx::bf_lo(v.y), ptx::bf_hi(v.y)),
-            ptx::pack_f16(ptx::bf_lo(v.z), ptx::bf_hi(v.z)), ptx::pack_f16(ptx::bf_lo(v.w), ptx::bf_hi(v.w))};
-}
-// The rotation in packed fp16; sg flips the sine's sign (0 or 0x80008000).
-__device__ __forceinline__ void rotate_pair_f16(U4& x, U4& y, const uint32_t (&c)[4], const uint32_t (&s)[4],
-                                                uint32_t sg) {
-  const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-  const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
-  uint32_t xo[4], yo[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t sk = s[k] ^ sg;
-    xo[k] = ptx::fma_h2(yw[k], sk ^ 0x80008000u, ptx::mul_h2(xw[k], c[k]));
-    yo[k] = ptx::fma_h2(xw[k], sk, ptx::mul_h2(yw[k], c[k]));
-  }
-  x = U4{xo[0], xo[1], xo[2], xo[3]};
-  y = U4{yo[0], yo[1], yo[2], yo[3]};
-}
-
 __device__ __forceinline__ uint32_t w_of(const U4& v, int k) {
   return k == 0 ? v.x : (k == 1 ? v.y : (k == 2 ? v.z : v.w));
 }
@@ -178,8 +148,7 @@ struct Smem {
 // may have left).  With BLOCKMAP the tensor maps are 3-D views of the pools
 // (64 columns x rows x 64-column halves) and one box brings a whole K or V tile
 // of a block in the [half][key][64] layout: one copy instead of two.
-template <int D, int NT, bool ROPE, int NW = kWarps, int NS = kStages, int BAR = 0, bool BLOCKMAP = false,
-          bool WTS = false>
+template <int D, int NT, bool ROPE, int NW = kWarps, int NS = kStages, int BAR = 0, bool BLOCKMAP = false>
 __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p,
                                            const DecodeArgs& a, const int split, const int hk, const int r,
                                            uint8_t* smem_raw) {
@@ -237,8 +206,7 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
       neg = delta < 0 ? 1 : 0;
       row_ok = ad < a.max_pos;
     }
-    constexpr int ROWB = WTS ? 2 * D : SM::ROWB;  // fp16 cos | sin, or the bf16 row over signed angles
-    ptx::mbar_arrive_expect_tx(bar, 2 * GE::TILE + (row_ok ? ROWB : 0));
+    ptx::mbar_arrive_expect_tx(bar, 2 * GE::TILE + (row_ok ? SM::ROWB : 0));
     const int y = (phys * a.Hkv + hk) * 16;
     if constexpr (BLOCKMAP) {
       ptx::tma_load_3d(kdst, &kmap, 0, y, 0, bar);
@@ -252,7 +220,7 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
     }
     if (row_ok)
       ptx::bulk_load(sbase + SM::ROWS + (warp * NS + stg) * SM::ROWB,
-                     WTS ? a.cs_f16 + (size_t)ad * D : a.cs_bf16 + ((size_t)ad * 2 + neg) * (3 * D / 2), ROWB, bar);
+                     a.cs_bf16 + ((size_t)ad * 2 + neg) * (3 * D / 2), SM::ROWB, bar);
   };
 
   // Each worker warp's lane 0 initialises its stage barriers.  With 3 stages
@@ -311,34 +279,6 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
     }
   }
   const float qs = a.scale * kLog2e;  // applied to the scores; softmax runs in base 2
-  float qcol[NT][2];  // the same with the power of two that left the query of each score column (WTS)
-  if constexpr (WTS) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < GE::NCH; ++i)
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          amax = fmaxf(amax, fmaxf(fabsf(ptx::bf_lo(w_of(qraw[nt][i], w))), fabsf(ptx::bf_hi(w_of(qraw[nt][i], w)))));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      int ex = (__float_as_int(amax) >> 23) - 127;
-      ex = ex < -126 ? -126 : (ex > 126 ? 126 : ex);
-      const float down = __int_as_float((127 - ex) << 23);
-#pragma unroll
-      for (int i = 0; i < GE::NCH; ++i) {
-        const U4 q = qraw[nt][i];
-        qraw[nt][i] = U4{ptx::pack_f16(ptx::bf_lo(q.x) * down, ptx::bf_hi(q.x) * down),
-                         ptx::pack_f16(ptx::bf_lo(q.y) * down, ptx::bf_hi(q.y) * down),
-                         ptx::pack_f16(ptx::bf_lo(q.z) * down, ptx::bf_hi(q.z) * down),
-                         ptx::pack_f16(ptx::bf_lo(q.w) * down, ptx::bf_hi(q.w) * down)};
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        qcol[nt][j] = fminf(qs * __int_as_float((__shfl_sync(0xffffffffu, ex, (2 * tig + j) * 4) + 127) << 23), 3.4e38f);
-    }
-  }
 
   // R_s for the two key rows (slots ks0, ks0 + 8) of this thread: cos and sin
   // of the slot angles as bf16 pairs (-sin is formed at use: holding it too
@@ -346,21 +286,8 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
   uint32_t rcb[2][GE::NPAIR][4], rsb[2][GE::NPAIR][4];
   int tq = 0;
   if constexpr (ROPE) {
-    if constexpr (WTS) {
 #pragma unroll
-      for (int row = 0; row < 2; ++row) {
-        const uint16_t* t = a.cs_f16 + (size_t)min(ks0 + 8 * row, a.max_pos - 1) * D;
-#pragma unroll
-        for (int p = 0; p < GE::NPAIR; ++p) {
-          const uint4 c = __ldg(reinterpret_cast<const uint4*>(t + ch.fbase[p]));
-          const uint4 sn = __ldg(reinterpret_cast<const uint4*>(t + D / 2 + ch.fbase[p]));
-          rcb[row][p][0] = c.x; rcb[row][p][1] = c.y; rcb[row][p][2] = c.z; rcb[row][p][3] = c.w;
-          rsb[row][p][0] = sn.x; rsb[row][p][1] = sn.y; rsb[row][p][2] = sn.z; rsb[row][p][3] = sn.w;
-        }
-      }
-    }
-#pragma unroll
-    for (int row = 0; row < (WTS ? 0 : 2); ++row) {
+    for (int row = 0; row < 2; ++row) {
       const int srow = min(ks0 + 8 * row, a.max_pos - 1);
       const float* t = a.cos_sin + (size_t)srow * D;
 #pragma unroll
@@ -458,17 +385,6 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
       for (int p = 0; p < GE::NPAIR; ++p) {
         const U4 cw = ptx::lds128(rowb + 2 * ch.fbase[p]);
         const U4 sw = ptx::lds128(rowb + D + 2 * ch.fbase[p]);
-        if constexpr (WTS) {
-          const uint32_t cb[4] = {cw.x, cw.y, cw.z, cw.w}, sb[4] = {sw.x, sw.y, sw.z, sw.w};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            U4 x = qraw[nt][ch.first[p]], y = qraw[nt][ch.second[p]];
-            rotate_pair_f16(x, y, cb, sb, delta < 0 ? 0x80008000u : 0u);
-            qw[nt][ch.first[p]] = x;
-            qw[nt][ch.second[p]] = y;
-          }
-          continue;
-        }
         const U4 nw = ptx::lds128(rowb + 2 * D + 2 * ch.fbase[p]);
         const uint32_t cb[4] = {cw.x, cw.y, cw.z, cw.w};
         const uint32_t sb[4] = {sw.x, sw.y, sw.z, sw.w};
@@ -495,12 +411,6 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
 #pragma unroll
         for (int p = 0; p < GE::NPAIR; ++p)
         {
-          if constexpr (WTS) {
-            kr[row][ch.first[p]] = bf_to_h(kr[row][ch.first[p]]);
-            kr[row][ch.second[p]] = bf_to_h(kr[row][ch.second[p]]);
-            rotate_pair_f16(kr[row][ch.first[p]], kr[row][ch.second[p]], rcb[row][p], rsb[row][p], 0u);
-            continue;
-          }
           const uint32_t nn[4] = {rsb[row][p][0] ^ 0x80008000u, rsb[row][p][1] ^ 0x80008000u,
                                   rsb[row][p][2] ^ 0x80008000u, rsb[row][p][3] ^ 0x80008000u};
           rotate_pair_bf16(kr[row][ch.first[p]], kr[row][ch.second[p]], rcb[row][p], rsb[row][p], nn);
@@ -521,11 +431,7 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
         const uint32_t a2 = w_of(kr[0][c], 2 * u + 1), a3 = w_of(kr[1][c], 2 * u + 1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if (WTS && u == 0)
-            ptx::mma_f16_16816(sacc[nt], a0, a1, a2, a3, w_of(qw[nt][c], 0), w_of(qw[nt][c], 1));
-          else if (WTS)
-            ptx::mma_f16_16816(sacc2[nt], a0, a1, a2, a3, w_of(qw[nt][c], 2), w_of(qw[nt][c], 3));
-          else if (u == 0)
+          if (u == 0)
             ptx::mma_bf16_16816(sacc[nt], a0, a1, a2, a3, w_of(qw[nt][c], 0), w_of(qw[nt][c], 1));
           else
             ptx::mma_bf16_16816(sacc2[nt], a0, a1, a2, a3, w_of(qw[nt][c], 2), w_of(qw[nt][c], 3));
@@ -543,12 +449,11 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
     bool any_corr = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float pv[4], es[2];
+      float pv[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float f = WTS ? qcol[nt][j] : qs;
-        const float sa = v0 ? sacc[nt][j] * f : -CUDART_INF_F;
-        const float sb = v1 ? sacc[nt][2 + j] * f : -CUDART_INF_F;
+        const float sa = v0 ? sacc[nt][j] * qs : -CUDART_INF_F;
+        const float sb = v1 ? sacc[nt][2 + j] * qs : -CUDART_INF_F;
         float bm = fmaxf(sa, sb);
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 4));
         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 8));
@@ -560,22 +465,8 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
         const float pa = exp2f(sa - muse), pbv = exp2f(sb - muse);
         lrun[nt][j] = fmaf(lrun[nt][j], corr[nt][j], pa + pbv);
         mrun[nt][j] = mnew;
-        if constexpr (WTS) es[j] = pa + pbv;
         pv[j] = pa;
         pv[2 + j] = pbv;
-      }
-      if constexpr (WTS) {
-        // sums of both columns over the fragment rows: the first step leaves even rows with column 0 and odd rows
-        // with column 1
-        const bool odd = g8 & 1;
-        float e = (odd ? es[1] : es[0]) + __shfl_xor_sync(0xffffffffu, odd ? es[0] : es[1], 4);
-        e += __shfl_xor_sync(0xffffffffu, e, 8);
-        e += __shfl_xor_sync(0xffffffffu, e, 16);
-        const int head = 8 * nt + 2 * tig + g8;
-        const float m = odd ? mrun[nt][1] : mrun[nt][0];
-        if (g8 < 2 && head < G)
-          a.w_raw[(((size_t)r * a.Hkv + hk) * mb + b) * G + head] =
-              e == 0.f ? -CUDART_INF_F : (m == -CUDART_INF_F ? 0.f : m) + log2f(e);
       }
       pb0[nt] = ptx::movmatrix_trans(ptx::pack_bf16(pv[0], pv[1]));  // keys 0..7
       pb1[nt] = ptx::movmatrix_trans(ptx::pack_bf16(pv[2], pv[3]));  // keys 8..15
@@ -597,30 +488,11 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
     {
       const int mi = lane >> 3, rr = lane & 7;
       const int key = frag_slot(rr) + 8 * (mi >> 1);
-      bool part = false;
-      uint32_t klo = 0xffffffffu, khi = 0xffffffffu;  // which of fragment rows (2 tig, 2 tig + 1) and + 8 count
-      if constexpr (WTS) {
-        part = !__all_sync(0xffffffffu, v0 && v1);
-        if (part) {
-          const unsigned b0 = __ballot_sync(0xffffffffu, v0) >> (8 * tig);  // row g is at bit 4 g
-          const unsigned b1 = __ballot_sync(0xffffffffu, v1) >> (8 * tig);
-          klo = (b0 & 1u ? 0xffffu : 0u) | (b0 & 16u ? 0xffff0000u : 0u);
-          khi = (b1 & 1u ? 0xffffu : 0u) | (b1 & 16u ? 0xffff0000u : 0u);
-        }
-      }
 #pragma unroll
       for (int mt = 0; mt < GE::MT; ++mt) {
         const int cg = 2 * mt + (mi & 1);
         uint32_t a0, a1, a2, a3;
         ptx::ldsm_x4_trans(vbase + swz(cg >> 3, key, cg & 7), a0, a1, a2, a3);
-        if constexpr (WTS) {  // a masked slot's bytes (a NaN, say) never meet its weight of 0
-          if (part) {
-            a0 &= klo;
-            a1 &= klo;
-            a2 &= khi;
-            a3 &= khi;
-          }
-        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) ptx::mma_bf16_16816(oacc[mt][nt], a0, a1, a2, a3, pb0[nt], pb1[nt]);
       }
@@ -699,10 +571,8 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
     const int hq = hk * G + head;
     if (direct) {
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)r * a.Hq + hq) * D + dim;
-      const bool any = WTS ? Ls != 0.f : Ls > 0.f;  // with block weights, a NaN sum stays one
-      *out = __float2bfloat16_rn(any ? O / Ls : 0.f);
-      if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = any ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
-      if (WTS && dim == 0) a.w_lse[(size_t)r * a.Hq + hq] = any ? M + log2f(Ls) : -CUDART_INF_F;
+      *out = __float2bfloat16_rn(Ls > 0.f ? O / Ls : 0.f);
+      if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
     } else {
       const size_t pi = ((size_t)r * a.Hq + hq) * a.n_split + split;
       a.part_o[pi * D + dim] = O;
@@ -740,10 +610,8 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
       O = fmaf(__ldcg(a.part_o + (base + s) * D + dim), f, O);
     }
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((size_t)r * a.Hq + hq) * D + dim;
-    const bool any = WTS ? Ls != 0.f : Ls > 0.f;
-    *out = __float2bfloat16_rn(any ? O / Ls : 0.f);
-    if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = any ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
-    if (WTS && dim == 0) a.w_lse[(size_t)r * a.Hq + hq] = any ? M + log2f(Ls) : -CUDART_INF_F;
+    *out = __float2bfloat16_rn(Ls > 0.f ? O / Ls : 0.f);
+    if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = Ls > 0.f ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
   }
   if (threadIdx.x == 0) a.counters[(size_t)r * a.Hkv + hk] = 0;
 }

@@ -25,14 +25,14 @@ struct DecodeArgs {
   int* counters;             // [B][Hkv] finished splits (zero between calls), null when n_split == 1
   int batch, Hq, Hkv, G, D, BS, num_blocks, max_blocks;
   int split_blocks;          // blocks per split
-  int n_split;               // splits per (request, kv head); e4m3 tensor-core path: CTAs
+  int n_split;               // splits per (request, kv head); one list of blocks: CTAs
   int ctas_per_sm;           // tensor-core decode: 3 (2 stages per warp) or 2 (3 stages) CTAs per SM
   float scale;               // softmax scale (1/sqrt(D) by default)
   int* err;                  // device error word
   // e4m3 cache: one scale per (block, kv head) of each pool, else null
   const float* k_scale;      // [num_blocks][Hkv]
   const float* v_scale;
-  const uint16_t* cs_f16;    // [max_pos][D] fp16 cos | sin (e4m3 tensor-core path), or null
+  const uint16_t* cs_f16;    // [max_pos][D] fp16 cos | sin (one list of blocks), or null
   // block weights (null when not asked for)
   void* weights;             // [B][Hkv][max_blocks] in the dtype of q: sum over the group of each block's softmax weight
   float* w_raw;              // [B][Hkv][max_blocks][G] log2 of a block's unnormalised sum, per query head
@@ -77,10 +77,11 @@ struct DecodePlan {
   int ctas_per_sm;  // tensor-core path: resident CTAs per SM (3 or 2; 1 for more than 8 heads per group)
 };
 DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs, bool bf16, int num_sms);
-// The e4m3 decode's plan.  Its tensor-core kernel runs a resident grid: n_split is
-// the number of CTAs (of kQ8Warps warps), each with two partial results.
-constexpr int kQ8Warps = 4, kQ8MaxCtas = 4 * 160;
-DecodePlan plan_decode_q8(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
+// Plan of the decode that takes all blocks as one list (e4m3, or bf16 with block
+// weights).  Its tensor-core kernel runs a resident grid: n_split is the number of
+// CTAs (of kListWarps warps), each with two partial results.
+constexpr int kListWarps = 4, kListMaxCtas = 4 * 160;
+DecodePlan plan_decode_list(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan, cudaStream_t s);
 cudaError_t launch_decode_simt(const DecodeArgs& a, bool bf16, bool rotate, cudaStream_t s);
@@ -92,8 +93,8 @@ cudaError_t launch_decode_simt_q8(const DecodeArgs& a, bool bf16, cudaStream_t s
 cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t s);
 // The exact-precision kernel over the f32 cache (or a bf16 one of no blocks), recording block weights.
 cudaError_t launch_decode_simt_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
-// The bf16 tensor-core kernel, recording block weights (num_blocks > 0).
-cudaError_t launch_decode_mma_weights(const DecodeArgs& a, cudaStream_t s);
+// bf16 cache, tensor cores, recording block weights (num_blocks > 0).
+cudaError_t launch_decode_weights(const DecodeArgs& a, cudaStream_t s);
 // w_raw and w_lse -> weights.
 cudaError_t launch_block_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, bool rotate, cudaStream_t s);
