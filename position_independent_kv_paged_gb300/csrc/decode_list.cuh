@@ -54,9 +54,8 @@
 //    which 0.30 GB from HBM.  Issue: 288 instructions a block and warp (the key
 //    rotation alone is 64, the widening 96), 53 % of the issue slots used.
 //  - 8 x 131072 keys, 64 / 8 heads, with block weights: 330 us, the same bound.
-//  - the first batch over the bf16 cache, with block weights: BFW_US us (the grid of
-//    splits with tensor copies that it replaced took 257 us and 669 instructions a
-//    block).
+//  - the first batch over the bf16 cache, with block weights: 187 us, 2.15 GB read
+//    (a grid of splits with tensor copies took 257 us and 669 instructions a block).
 //  - 128 ragged contexts to 32768 keys, 28 / 4 heads, nothing shared: HBM, 2.2 GB at
 //    6.3 TB/s (0.93 of the measured copy bandwidth).
 #pragma once
@@ -203,7 +202,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     long long x0, x1, total, n_cta;
     int r, hk, nblk, L;   // the pair: request, kv head, blocks, length
     int b_begin, left;    // its first block in this range, blocks of the range from there on
-    int last;
+    int whole, last;      // one part of a pair per CTA; last to finish its pair
   } sg;
   auto cta_total = [&](int v, int& before) {  // sum of v over the CTA, and over the threads before this one
     int pre = v;
@@ -246,36 +245,58 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   }
   total *= a.Hkv;
   {
-    // ranges of at least kMinRange blocks, but no fewer of them than pairs
-    const long long want = max((total + kMinRange - 1) / kMinRange, (long long)pairs * a.Hkv);
+    // A batch that does not fill the grid is cut into parts of pairs instead, one per CTA, so that no CTA walks two
+    // pairs one after the other.  A part costs about 0.12 us a block, joining the parts of a pair about 5 us and more
+    // with their number and the group's heads.  So pairs of up to 64 blocks are cut to 8 or 16 where that fits (1024
+    // keys, 8 heads: 11 us, against 12 to 13 in parts of 32 or whole) and else left whole (128 pairs of 64 blocks: 15 us
+    // against 16 in halves), longer ones to 32 (8192 keys: 15.4 us against 16.3 in 16) or, above 8 heads, 64.
+    const long long all_pairs = (long long)pairs * a.Hkv;
+    int part = total <= 64 * all_pairs ? 8 : (NT == 1 ? 32 : 64);
+    while (part <= kMinRange && total / part + all_pairs > (long long)gridDim.x) part = part == 16 ? 64 : part * 2;
+    const bool whole = part <= kMinRange;
+    // else equal ranges of the list, of at least kMinRange blocks, but no fewer of them than pairs
+    const long long want = max((total + kMinRange - 1) / kMinRange, all_pairs);
     const long long n_cta = min((long long)gridDim.x, want);
-    if (blockIdx.x >= n_cta) return;
-    const long long x0 = blockIdx.x * total / n_cta, x1 = (blockIdx.x + 1) * total / n_cta;
-    long long first = 0;  // blocks (one kv head) of the requests before `base`
+    if (blockIdx.x >= n_cta && !whole) return;
+    const long long x0 = whole ? blockIdx.x : blockIdx.x * total / n_cta;
+    const long long x1 = (blockIdx.x + 1) * total / n_cta;
+    if (threadIdx.x == 0) sg.r = -1;
+    long long first = 0;  // blocks or parts (of one kv head) of the requests before `base`
     for (int base = 0; base < a.batch; base += NW * 32) {
       const int i = base + threadIdx.x;
       if (a.batch > NW * 32) {  // else the one pass above still holds them
         Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
         n = blocks_of(Li, mb);
-        sum = cta_total(n, before);
       }
+      const int units = whole ? (n + part - 1) / part : n;
+      if (a.batch > NW * 32 || whole) sum = cta_total(units, before);
       const long long at = (first + before) * a.Hkv;
-      if (x0 >= at && x0 < at + (long long)n * a.Hkv) {
-        sg.x0 = x0;
-        sg.x1 = x1;
-        sg.total = total;
-        sg.n_cta = n_cta;
+      if (x0 >= at && x0 < at + (long long)units * a.Hkv) {
+        const int k = (int)((x0 - at) % units);
         sg.r = i;
-        sg.hk = (int)((x0 - at) / n);
+        sg.hk = (int)((x0 - at) / units);
         sg.nblk = n;
         sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
-        sg.b_begin = (int)((x0 - at) % n);
-        sg.left = (int)(x1 - x0);
+        sg.whole = whole;
+        if (whole) {
+          sg.b_begin = (int)((long long)k * n / units);
+          sg.left = (int)((long long)(k + 1) * n / units) - sg.b_begin;
+          sg.x0 = x0 - k;           // the pair's first CTA
+          sg.x1 = sg.x0 + units - 1;  // ... and its last
+        } else {
+          sg.b_begin = k;
+          sg.left = (int)(x1 - x0);
+          sg.x0 = x0;
+          sg.x1 = x1;
+          sg.total = total;
+          sg.n_cta = n_cta;
+        }
       }
       first += sum;
       if (first * a.Hkv > x0) break;
     }
     __syncthreads();
+    if (sg.r < 0) return;  // more CTAs than parts
   }
   int b0 = 0, span = 0, n_stage = 0;             // the chunk's first block, blocks, stages of this warp
   uint32_t qx[NT][2 * NH], qy[NT][2 * NH];       // queries of this thread's heads (column g8 + 8 nt), fp16
@@ -781,9 +802,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     }
   if (!direct) {
       // CTAs c1 .. c2 hold parts of this pair; the last of them to arrive merges them in order
-      const long long ps = b_begin ? sg.x0 - b_begin : sg.x1 - (b_end - b_begin);  // the pair's place in the list
-      auto owner = [&](long long x) { return ((x + 1) * sg.n_cta - 1) / sg.total; };
-      const int c1 = (int)owner(ps), c2 = (int)owner(ps + nblk - 1);
+      int c1 = (int)sg.x0, c2 = (int)sg.x1;
+      if (!sg.whole) {
+        const long long ps = b_begin ? sg.x0 - b_begin : sg.x1 - (b_end - b_begin);  // the pair's place in the list
+        auto owner = [&](long long x) { return ((x + 1) * sg.n_cta - 1) / sg.total; };
+        c1 = (int)owner(ps);
+        c2 = (int)owner(ps + nblk - 1);
+      }
       __syncthreads();
       if (threadIdx.x == 0) {
         __threadfence();
