@@ -11,21 +11,21 @@
 // that lies inside one range is written at once, one that is cut leaves a partial
 // result per CTA, and the last of them to arrive merges them in order.  Against a
 // grid of (split, kv head, request) this has no partly filled last wave, and pays
-// a start (5 us: table entries, scales, queries, first tiles) once or twice per
+// a start (table entries, scales, queries, first tiles) once or twice per
 // CTA instead of per split.  Within a pair each warp owns every NW-th 16-key
 // block and runs its own ring of stages, each of two e4m3 blocks or one bf16 block.
 // A (block, head) tile is contiguous in the pool; its 16-byte chunks are stored
 // permuted in shared memory (mix below), so that the key-row reads and the
 // transposing reads of V are free of bank conflicts.  The fp16 cos | sin row of the
 // block's query rotation comes with them.  The copies are cp.async of the whole
-// warp (17 instructions a stage at d 128): one thread issuing tensor copies took
-// about 120 issue slots per stage, a sixth of the kernel's, and the kernel is bound
-// by issue.
+// warp (17 instructions a stage at d 128): in place of one thread's tensor copies,
+// and with the references made finite in the same step, they brought 431 warp
+// instructions per block to 375, and the kernel is bound by issue.
 //
 // Per block, with t the query's position, b the block's start, s the slot:
 //   score = (R_{t-b} q) . (R_s k) * (k scale) * softmax scale
 // e4m3 widens to fp16 exactly, bf16 within fp16's range (a key beyond it becomes
-// infinite; bf16 operands would show in the weights: three roundings of 2^-8 each,
+// infinite; bf16 operands would show: three roundings of 2^-8 each,
 // an output error of 5.4e-3 of its norm at d 64 where this has 2e-3).  R_s is constant per lane, R_{t-b} q is formed once
 // per block, both in packed fp16, and S^T = K' Q'^T, O^T += V^T P^T run as
 // mma.sync m16n8k16 with fp32 accumulation (keys, then head dims, as M; up to 8
@@ -51,13 +51,13 @@
 // What bounds it and what it measured (GB300; 3 CTAs of 4 warps per SM, held there
 // by registers: 168 a thread):
 //  - 64 requests x 8192 keys, 32 / 8 heads, spans shared: 120 us, 1.07 GB read of
-//    which 0.30 GB from HBM.  Issue: 288 instructions a block and warp (the key
-//    rotation alone is 64, the widening 96), 53 % of the issue slots used.
+//    which 0.30 GB from HBM.  Issue: 282 instructions a block and warp (81 of
+//    them fp16 rotation, 66 conversions, 16 matrix products), 53 % of the issue slots used.
 //  - 8 x 131072 keys, 64 / 8 heads, with block weights: 330 us, the same bound.
 //  - the first batch over the bf16 cache, with block weights: 187 us, 2.15 GB read
 //    (a grid of splits with tensor copies took 257 us and 669 instructions a block).
-//  - 128 ragged contexts to 32768 keys, 28 / 4 heads, nothing shared: HBM, 2.2 GB at
-//    6.3 TB/s (0.93 of the measured copy bandwidth).
+//  - 128 ragged contexts to 32768 keys, 28 / 4 heads, nothing shared: HBM, 2.29 GB at
+//    6.45 TB/s (0.95 of the measured copy bandwidth).
 #pragma once
 
 #include <cuda_fp16.h>
