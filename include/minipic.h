@@ -96,7 +96,9 @@ typedef enum { MINIPIC_F32 = 0, MINIPIC_BF16 = 1 } minipic_dtype;
 #define MINIPIC_DEVERR_TIMEOUT    8  /* a bounded wait for an asynchronous copy gave up (results invalid) */
 #define MINIPIC_DEVERR_RANGE     16  /* prefill: a rotated key or scaled, rotated query element is outside the
                                         fp16 range of the QK^T operands (|x| > 65504); the score rows that
-                                        use it are undefined (inf or NaN), all other rows are unaffected */
+                                        use it are undefined (inf or NaN), all other rows are unaffected.
+                                        kv_append_q8: a new key or value is infinite and was stored as the
+                                        largest value of its block's scale */
 
 /* The paged KV pool (device memory, caller-owned). */
 typedef struct {
@@ -384,7 +386,9 @@ typedef struct {
  * index outside the table MINIPIC_DEVERR_SEQ_LEN; such blocks are skipped.  A
  * negative kv_start, or rows outside [0, total_new), sets
  * MINIPIC_DEVERR_SEQ_LEN and skips the request.  Every block must be the
- * target of at most one request of a call.  Asynchronous on `stream`. */
+ * target of at most one table entry of a call (of one request, and once in its
+ * table): two writers of a block leave a mixture of both.  Asynchronous on
+ * `stream`. */
 minipic_status minipic_kv_append_q8(minipic_dtype dtype, const minipic_kv_pool_q8_mut* kv,
                                     const minipic_kv_append_batch* batch, minipic_stream_t stream);
 
@@ -409,9 +413,9 @@ size_t minipic_attn_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads,
  * long as each has at most 16384 (request, kv head) pairs (else zero it when
  * the shape changes); calls whose work overlaps on the GPU need workspaces of
  * their own.  Errors as for minipic_attn_decode; UNSUPPORTED also for more than
- * 65535 requests or kv heads, num_blocks * num_kv_heads * 16 or
- * batch * max_blocks_per_seq above 2^31 - 1, or 2^38 table entries times kv
- * heads. */
+ * 65535 requests or kv heads, max_blocks_per_seq of 2^27 or more,
+ * num_blocks * num_kv_heads * 16 or batch * max_blocks_per_seq above 2^31 - 1,
+ * or more than 2^38 table entries times kv heads. */
 minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
                                       const minipic_rope* rope, const minipic_decode_batch* batch, float scale,
                                       void* block_weights, void* workspace, size_t workspace_bytes,

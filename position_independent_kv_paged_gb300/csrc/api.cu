@@ -678,11 +678,13 @@ size_t weights_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_
   return most;
 }
 
-// What the one-list decode's 32-bit numbers hold: tile numbers, sums of lengths in blocks, the blocks of a CTA's range.
+// What the decodes' 32-bit numbers hold: tile numbers, sums of lengths in blocks, the blocks of a CTA's range, the
+// keys of a table.
 bool list_fits(const minipic_kv_pool& kv, const minipic_decode_batch& b) {
   const long long entries = (long long)b.batch * b.max_blocks_per_seq;
   return b.batch <= kMaxGridYZ && kv.num_kv_heads <= kMaxGridYZ &&
          (long long)kv.num_blocks * kv.num_kv_heads * 16 <= 0x7fffffffLL && entries <= 0x7fffffffLL &&
+         b.max_blocks_per_seq < (1 << 27) &&
          entries * kv.num_kv_heads <= (1LL << 38);
 }
 

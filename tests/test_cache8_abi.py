@@ -56,6 +56,8 @@ def test_decode_q8_refusals(lib):
     assert call_decode(lib, db=decode(B=65536)) == 2
     assert call_decode(lib, db=decode(B=60000, mb=40000)) == 2   # 32-bit sums of blocks
     assert call_decode(lib, kv=kvq8(nb=2 ** 30)) == 2            # 32-bit tile numbers
+    for dtype in (0, 1):
+        assert call_decode(lib, dtype=dtype, db=decode(mb=2 ** 27)) == 2   # 32-bit numbers of keys
     assert call_decode(lib, Hq=60000, kv=kvq8(nb=1, hkv=60000), db=decode(B=100, mb=10 ** 6)) == 2
     assert call_decode(lib, db=decode(B=0)) == 0
     f = lib.minipic_attn_decode_q8
