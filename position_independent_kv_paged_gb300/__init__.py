@@ -748,8 +748,8 @@ def attn_decode_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_star
     L = load()
     specs = _kv_q8(k_pool, v_pool, k_scale, v_scale)
     return _decode_weights(L.minipic_attn_decode_q8, "minipic_attn_decode_q8", attn_decode_q8_workspace_size,
-                           _kv_q8_struct, q, specs, block_tables, block_starts, seq_lens, q_pos, rope, scale, out, lse, block_weights,
-                           workspace, stream)
+                           _kv_q8_struct, q, specs, block_tables, block_starts, seq_lens, q_pos, rope, scale, out, lse,
+                           block_weights, workspace, stream)
 
 
 def attn_decode_weights(q, k_pool, v_pool, block_tables, block_starts, seq_lens, q_pos, rope, block_weights,

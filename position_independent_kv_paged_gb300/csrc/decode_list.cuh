@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     const bool whole = part <= kMinRange;
     // else equal ranges of the list, of at least kMinRange blocks, but no fewer of them than pairs
     const long long want = max((total + kMinRange - 1) / kMinRange, all_pairs);
-    const long long n_cta = min((long long)gridDim.x, want);
+    const long long n_cta = max(1LL, min((long long)gridDim.x, want));  // 1: no request has a key
     if (blockIdx.x >= n_cta && !whole) return;
     const long long x0 = whole ? blockIdx.x : blockIdx.x * total / n_cta;
     const long long x1 = (blockIdx.x + 1) * total / n_cta;

@@ -247,6 +247,32 @@ def test_decode_at_sizes_that_cut_pairs_and_ranges(env, lens, Hq, Hkv, d):
     assert mp.device_error() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B", [1, 300])
+def test_a_batch_without_any_key(env, dtype, B):
+    """Zero lengths throughout: out 0, lse -inf, the weights left as they were."""
+    torch, mp, dev = env
+    ty = dict(f32=torch.float32, bf16=torch.bfloat16)[dtype]
+    Hq, Hkv, d, mb = 8, 2, 64, 3
+    q = torch.ones(B, Hq, d, dtype=ty, device=dev)
+    pool = torch.ones(4, Hkv, 16, d, device=dev)
+    sc = torch.ones(4, Hkv, device=dev)
+    tables, starts = (torch.zeros(B, mb, dtype=torch.int32, device=dev) for _ in range(2))
+    lens, pos = (torch.zeros(B, dtype=torch.int32, device=dev) for _ in range(2))
+    rope = mp.rope_table(64, d, 1e4, device=dev)
+    for q8 in (True, False):
+        bw = torch.full((B, Hkv, mb), 7.0, dtype=ty, device=dev)
+        out, lse = torch.full_like(q, 5.0), torch.full((B, Hq), 5.0, device=dev)
+        if q8:
+            p8 = pool.to(torch.float8_e4m3fn)
+            mp.attn_decode_q8(q, p8, p8, sc, sc, tables, starts, lens, pos, rope, out=out, lse=lse, block_weights=bw)
+        else:
+            mp.attn_decode_weights(q, pool.to(ty), pool.to(ty), tables, starts, lens, pos, rope, bw, out=out, lse=lse)
+        torch.cuda.synchronize()
+        assert (out == 0).all() and (lse == -float("inf")).all() and (bw == 7.0).all()
+    assert mp.device_error() == 0
+
+
 def test_two_graphs_on_one_workspace(env):
     """Two captured calls of different shapes share a workspace and are replayed in turn."""
     torch, mp, dev = env
