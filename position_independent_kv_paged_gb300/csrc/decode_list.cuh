@@ -26,7 +26,7 @@
 //   score = (R_{t-b} q) . (R_s k) * (k scale) * softmax scale
 // e4m3 widens to fp16 exactly, bf16 within fp16's range (a key beyond it becomes
 // infinite; bf16 operands would show: three roundings of 2^-8 each,
-// an output error of 5.4e-3 of its norm at d 64 where this has 2e-3).  R_s is constant per lane, R_{t-b} q is formed once
+// an output error of 5.4e-3 of its norm at d 64 where this has 2.2e-3).  R_s is constant per lane, R_{t-b} q is formed once
 // per block, both in packed fp16, and S^T = K' Q'^T, O^T += V^T P^T run as
 // mma.sync m16n8k16 with fp32 accumulation (keys, then head dims, as M; up to 8
 // query heads as N, so a group of 8 wastes nothing and the operands come from
