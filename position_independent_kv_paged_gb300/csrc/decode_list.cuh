@@ -223,6 +223,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     }
     return sum;
   };
+  // No owner until a thread below finds the pair.  Stored before the barriers of the first pass, which order it before
+  // that thread's store: a batch of up to one pass in equal ranges meets no other barrier in between.
+  if (threadIdx.x == 0) sg.r = -1;
   long long total = 0, sum = 0;
   int pairs = 0, zero = 0, Li = 0, n = 0, before = 0;
   for (int base = 0; base < a.batch; base += NW * 32) {
@@ -260,7 +263,6 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     if (blockIdx.x >= n_cta && !whole) return;
     const long long x0 = whole ? blockIdx.x : blockIdx.x * total / n_cta;
     const long long x1 = (blockIdx.x + 1) * total / n_cta;
-    if (threadIdx.x == 0) sg.r = -1;
     long long first = 0;  // blocks or parts (of one kv head) of the requests before `base`
     for (int base = 0; base < a.batch; base += NW * 32) {
       const int i = base + threadIdx.x;

@@ -1,0 +1,68 @@
+"""The decode over one list of blocks (8-bit cache; bf16 cache with block weights): how the list is shared out, the
+range of its operands, and its workspace."""
+
+import numpy as np
+import pytest
+
+from cache8_util import check_attention, check_weights, score_error
+from list_util import call, f64, make_batch, reference, workspace_size
+
+pytestmark = pytest.mark.gpu
+
+P_HALF = {"e4m3": 2.0 ** -11, "bf16": 2.0 ** -8}   # rounding of P
+COUNTERS = 65536                                     # bytes of the completion counters
+
+
+@pytest.fixture(scope="module")
+def env():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from position_independent_kv_paged_gb300 import _build
+    _build.build()
+    import position_independent_kv_paged_gb300 as mp
+    mp.load()
+    mp.device_error(clear=True)
+    return torch, mp, torch.device("cuda:0")
+
+
+def check(torch, t, out, lse, bw, what="", ref=None):
+    ref = ref or reference(torch, t)
+    d, lens = t["q"].shape[2], t["seq_lens"].tolist()
+    check_attention(f64(out), ref, "bf16", d, max(lens), what, p_half=P_HALF[t["kv"]])
+    fin = np.isfinite(ref["lse"])
+    assert np.array_equal(np.isneginf(f64(lse)), ~fin), what
+    # the denominator's terms carry the scores' errors and 2^-11 covers ex2 and the sums
+    assert np.all(np.abs(f64(lse)[fin] - ref["lse"][fin]) <= (score_error(ref, "bf16", d) + 2.0 ** -11 + 1e-5)[fin]), what
+    if bw is not None:
+        check_weights(f64(bw), ref, "bf16", d, lens, 7.0, what)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hkv,d,top", [(40, 8, 2, 128, 17000), (64, 8, 4, 64, 6000), (97, 14, 2, 128, 4000),
+                                            (128, 32, 2, 64, 5000)])
+def test_up_to_128_requests_that_fill_the_grid(env, kv, B, Hq, Hkv, d, top):
+    """Ragged requests, some without a key, in equal ranges of the list: every CTA finds its pair, whichever warp holds
+    it, call after call; the counters are zero again after each."""
+    torch, mp, dev = env
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in np.where(rng.random(B) < 0.2, 0, rng.integers(1, top, B))]
+    lens[-1] = top
+    t = make_batch(torch, dev, lens, Hq, Hkv, d, kv, B)
+    # parts of up to 64 blocks, one a CTA, would not fit the grid: equal ranges
+    grid = torch.cuda.get_device_properties(dev).multi_processor_count * (2 if Hq > 8 * Hkv else 4 if d == 64 else 3)
+    assert sum(-(-n // 16) for n in lens) * Hkv // 64 + sum(n > 0 for n in lens) * Hkv > grid
+    rope = mp.rope_table(t["max_pos"], d, t["base"], device=dev)
+    ws = torch.zeros(workspace_size(mp, t), dtype=torch.uint8, device=dev)
+    mb, first = t["block_tables"].shape[1], None
+    for i in range(25):
+        out = torch.full_like(t["q"], float("nan"))
+        lse = torch.full((B, Hq), float("nan"), device=dev)
+        bw = torch.full((B, Hkv, mb), 7.0, dtype=torch.bfloat16, device=dev)
+        call(mp, torch, t, rope, out, lse, bw, ws)
+        assert not ws[:COUNTERS].any(), i
+        if first is None:
+            first = (out, lse, bw)
+            check(torch, t, out, lse, bw)
+        assert all(torch.equal(a, b) for a, b in zip(first, (out, lse, bw))), i
+    assert mp.device_error() == 0
