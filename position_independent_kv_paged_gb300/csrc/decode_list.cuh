@@ -83,6 +83,7 @@ constexpr float kRescale = 8.f;               // a reference moves when exceeded
 constexpr float kHeadQ8 = 7.f;                // e4m3: P of a key at its reference is 2^7
 constexpr float kNone = -3e38f;               // a reference before the first key
 constexpr float kMinLog = -100.f;             // log2 of the smallest value scale told apart from zero
+constexpr float kNoValue = -3e38f;            // log2 of a value scale of zero: finite, and no score brings it near a reference
 
 // Shared-memory plan; Q8: e4m3 cache (else bf16).
 template <int D, int NS, bool Q8>
@@ -419,8 +420,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
           if (m != all) atomicOr(a.err, kErrPosition);
           ks = (Q8 ? t_ks[u] : 1.f) * (a.scale * kLog2e);
           lv = Q8 ? log2f(t_vs[u]) : 0.f;
-          if (lv < kMinLog) {  // scale 0, or below what is told apart from it
-            lv = 0.f;
+          if (lv < kMinLog) {  // scale 0, or below what is told apart from it: it must not raise mt for the others
+            lv = kNoValue;
             m |= 0x10000u;
           }
           if (start > tq) m |= 0x20000u;

@@ -4,7 +4,8 @@ range of its operands, and its workspace."""
 import numpy as np
 import pytest
 
-from cache8_util import check_attention, check_weights, score_error
+from cache8_util import Case, check_attention, check_weights, score_error
+import workloads as W
 from list_util import call, f64, make_batch, reference, workspace_size
 
 pytestmark = pytest.mark.gpu
@@ -66,3 +67,41 @@ def test_up_to_128_requests_that_fill_the_grid(env, kv, B, Hq, Hkv, d, top):
             check(torch, t, out, lse, bw)
         assert all(torch.equal(a, b) for a, b in zip(first, (out, lse, bw))), i
     assert mp.device_error() == 0
+
+
+def run_case(env, c):
+    """(out, lse, weights) of a cache8_util.Case over the e4m3 cache."""
+    torch, mp, dev = env
+    t = c.device(torch, dev)
+    B, mb = c.tables.shape
+    out = torch.full_like(t["q"], float("nan"))
+    lse = torch.full((B, c.Hq), float("nan"), device=dev)
+    bw = torch.full((B, c.Hkv, mb), 7.0, dtype=t["q"].dtype, device=dev)
+    mp.attn_decode_q8(t["q"], t["k_pool"], t["v_pool"], t["k_scale"], t["v_scale"], t["block_tables"], t["block_starts"],
+                      t["seq_lens"], t["q_pos"], mp.rope_table(c.max_pos, c.d, c.base, device=dev), out=out, lse=lse,
+                      block_weights=bw)
+    torch.cuda.synchronize()
+    return out, lse, bw
+
+
+def check_case(c, got, what=""):
+    """Errors against float64; outputs of any size: the part of the bound that is absolute is far below them."""
+    out, lse, bw = got
+    ref = c.reference()
+    check_attention(f64(out), ref, c.dtype, c.d, max(c.lens), what)
+    assert np.all(np.abs(f64(lse) - ref["lse"]) <= score_error(ref, c.dtype, c.d) + 2.0 ** -11 + 1e-5), what
+    check_weights(f64(bw), ref, c.dtype, c.d, c.lens, 7.0, what)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (8, 2, 128), (16, 2, 128), (16, 1, 64)])
+@pytest.mark.parametrize("log", [-22, -34, -60])
+def test_blocks_of_zero_values_among_small_scales(env, dtype, Hq, Hkv, d, log):
+    """A value scale of zero takes no precision from blocks whose scales are small: bytes near 2^2 times 2^-22 to 2^-60."""
+    c = Case(70, (400, 90, 16), Hq, Hkv, d, dtype, share=False)
+    c.scale[1] = np.where(np.isnan(c.scale[1]), np.nan, 2.0 ** log)
+    for r, n in enumerate((25, 6, 0)):
+        c.scale[1][c.tables[r, :n:3]] = 0.0   # every warp (each takes every fourth or eighth block) has both kinds
+    got = run_case(env, c)
+    assert np.all(f64(got[0])[2] != 0)
+    check_case(c, got, f"{dtype} {log}")
