@@ -82,7 +82,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;               // a reference moves when exceeded by 2^8
 constexpr float kHeadQ8 = 7.f;                // e4m3: P of a key at its reference is 2^7
 constexpr float kNone = -3e38f;               // a reference before the first key
-constexpr float kMinLog = -100.f;             // log2 of the smallest value scale told apart from zero
 constexpr float kNoValue = -3e38f;            // log2 of a value scale of zero: finite, and no score brings it near a reference
 
 // Shared-memory plan; Q8: e4m3 cache (else bf16).
@@ -420,7 +419,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
           if (m != all) atomicOr(a.err, kErrPosition);
           ks = (Q8 ? t_ks[u] : 1.f) * (a.scale * kLog2e);
           lv = Q8 ? log2f(t_vs[u]) : 0.f;
-          if (lv < kMinLog) {  // scale 0, or below what is told apart from it: it must not raise mt for the others
+          if (Q8 && t_vs[u] == 0.f) {  // it must not raise mt for the others
             lv = kNoValue;
             m |= 0x10000u;
           }
@@ -789,7 +788,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         Ls = fmaf(p[16 + c], exp2f(p[c] - M), Ls);
         O = fmaf(p[48 + c * LY::OST + dim], exp2f(p[32 + c] - T), O);
       }
-      O = Ls == 0.f ? 0.f : O / Ls * exp2f(T - M - kHead);
+      // the power in two factors: value scales down to fp32's least are 2^-149, past one factor's range with kHead
+      const float e = T - M - kHead, e1 = fmaxf(e, -80.f);
+      O = Ls == 0.f ? 0.f : O / Ls * exp2f(e1) * exp2f(e - e1);
       const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
       const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
       if (direct) {

@@ -105,3 +105,19 @@ def test_blocks_of_zero_values_among_small_scales(env, dtype, Hq, Hkv, d, log):
     got = run_case(env, c)
     assert np.all(f64(got[0])[2] != 0)
     check_case(c, got, f"{dtype} {log}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (8, 1, 128), (16, 1, 64)])
+@pytest.mark.parametrize("log", [-99, -105, -118, -130, 60])
+def test_value_scales_of_any_exponent(env, dtype, Hq, Hkv, d, log):
+    """The caller's own scales reach down to fp32's subnormals, where the outputs still are numbers of their type."""
+    c = Case(71, (3000, 90, 16), Hq, Hkv, d, dtype, share=False)
+    c.scale[1] = np.where(np.isnan(c.scale[1]), np.nan, 2.0 ** log)
+    out = f64(run_case(env, c)[0])
+    ref = c.reference()
+    eps = float(np.median(score_error(ref, dtype, d)))
+    # the output's rounding (relative to the largest where it is subnormal) and the scores' typical error
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -20
+    for r in range(3):
+        assert np.linalg.norm(out[r] - ref["out"][r]) <= (half + 2 * eps) * np.linalg.norm(ref["out"][r])
