@@ -47,10 +47,15 @@
  * -----------------------
  *  The caller owns every buffer.  The library allocates no device memory; entry
  *  points that need scratch take a caller-provided workspace whose size is given
- *  by the matching *_workspace_size query.  The decode workspace starts with
+ *  by the matching *_workspace_size query.  A decode workspace starts with
  *  one completion counter per (request, kv head): zero the workspace once after
  *  allocating it; every call leaves those counters zero again (after a call that
- *  reports MINIPIC_DEVERR_TIMEOUT, zero it again before reuse).  All calls are asynchronous on the
+ *  reports MINIPIC_DEVERR_TIMEOUT, zero it again before reuse).  The counters have
+ *  64 KB to themselves in every decode call (minipic_attn_decode and its
+ *  prerotated form, _mixed, _decode_q8, _decode_weights), so calls of any kind and
+ *  shape may follow one another on one workspace that is large enough for each, as
+ *  long as each has at most 16384 (request, kv head) pairs (else zero it when the
+ *  shape or the call changes).  All calls are asynchronous on the
  *  given stream (cudaStream_t; NULL = legacy default stream) and act on the
  *  device current at the call.  Inputs must stay valid until the work completes.
  *  The library looks up the device address of its error word once per device
@@ -266,7 +271,7 @@ minipic_status minipic_attn_decode_prerotated(minipic_dtype dtype, int32_t num_q
  *  - The looked-up address is kept for the life of the process: do not use
  *    the library across cudaDeviceReset (or any teardown of the device's
  *    primary context) on that device. */
-#define MINIPIC_NOALLOC_SCRATCH_BYTES ((size_t)16 << 20)
+#define MINIPIC_NOALLOC_SCRATCH_BYTES (((size_t)16 << 20) + 65536) /* 16 MiB and the counters */
 minipic_status minipic_attn_decode_noalloc(minipic_dtype dtype, int32_t num_q_heads,
                                            const minipic_kv_pool* kv, const minipic_rope* rope,
                                            const minipic_decode_batch* batch, float scale,
@@ -408,11 +413,9 @@ size_t minipic_attn_decode_q8_workspace_size(int32_t batch, int32_t num_q_heads,
  * softmax weight of block b's keys, summed over them and over the query heads
  * of kv head g (so it lies in [0, num_q_heads / num_kv_heads]); entries of
  * blocks past the request's length are left as they were.
- * workspace: zero it once after allocating it (the convention of
- * minipic_attn_decode); calls of any shapes may follow one another on it as
- * long as each has at most 16384 (request, kv head) pairs (else zero it when
- * the shape changes); calls whose work overlaps on the GPU need workspaces of
- * their own.  Errors as for minipic_attn_decode; UNSUPPORTED also for more than
+ * workspace: zero it once after allocating it; it may be shared with the other
+ * decode calls (see above), one after the other: calls whose work overlaps on the
+ * GPU need workspaces of their own.  Errors as for minipic_attn_decode; UNSUPPORTED also for more than
  * 65535 requests or kv heads, max_blocks_per_seq of 2^27 or more,
  * num_blocks * num_kv_heads * 16 or batch * max_blocks_per_seq above 2^31 - 1,
  * or more than 2^38 table entries times kv heads. */

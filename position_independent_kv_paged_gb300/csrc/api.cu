@@ -51,6 +51,12 @@ int current_sms() {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Bytes of a decode workspace's counters, the same region whatever the call and its split count.
+size_t counter_bytes(int batch, int Hkv) {
+  const size_t cnt = align_up((size_t)batch * Hkv * sizeof(int), 256);
+  return cnt > kCounterRegion ? cnt : kCounterRegion;
+}
+
 DecodeWs decode_ws(int batch, int Hq, int Hkv, int D, int n_split) {
   return decode_ws_layout(batch, Hq, Hkv, D, n_split);
 }
@@ -325,7 +331,7 @@ void replan_mixed_decode(DecodeArgs& a, int num_sms) {
 DecodeWs decode_ws_layout(int batch, int Hq, int Hkv, int D, int n_split) {
   DecodeWs w{0, 0, 0, 0};
   if (n_split <= 1) return w;
-  w.cnt_bytes = align_up((size_t)batch * Hkv * sizeof(int), 256);
+  w.cnt_bytes = counter_bytes(batch, Hkv);
   w.o_bytes = align_up((size_t)batch * Hq * n_split * D * sizeof(float), 256);
   w.ml_bytes = align_up((size_t)batch * Hq * n_split * 2 * sizeof(float), 256);
   w.total = w.cnt_bytes + w.o_bytes + w.ml_bytes;
@@ -335,8 +341,7 @@ DecodeWs decode_ws_layout(int batch, int Hq, int Hkv, int D, int n_split) {
 DecodeWsW decode_ws_weights(int batch, int Hq, int Hkv, int D, long long partials, int max_blocks) {
   DecodeWsW w{0, 0, 0, 0, 0, 0};
   if (partials > 0) {
-    const size_t cnt = align_up((size_t)batch * Hkv * sizeof(int), 256);
-    w.cnt_bytes = cnt > kCounterRegion ? cnt : kCounterRegion;
+    w.cnt_bytes = counter_bytes(batch, Hkv);
     w.o_bytes = align_up((size_t)partials * D * sizeof(float), 256);
     w.ml_bytes = align_up((size_t)partials * 2 * sizeof(float), 256);
   }

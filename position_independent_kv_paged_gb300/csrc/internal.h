@@ -190,6 +190,12 @@ struct OffloadArgs {
 };
 cudaError_t launch_kv_offload(const OffloadArgs& a, bool to_host, int num_sms, cudaStream_t s);
 
+// Bytes at the start of every decode workspace that hold its completion counters
+// (more only where 16384 pairs of request and kv head do not do), whatever the
+// call, its shape and its split count: no call leaves anything else there, so
+// calls of all kinds on one workspace find the counters zero.
+constexpr size_t kCounterRegion = 65536;
+
 // Byte layout of the decode workspace: one completion counter per (request,
 // kv head) first, then partial outputs and partial (max, sum) pairs.
 struct DecodeWs {
@@ -198,13 +204,10 @@ struct DecodeWs {
 DecodeWs decode_ws_layout(int batch, int Hq, int Hkv, int D, int n_split);
 
 // Byte layout of the workspace of the e4m3 and the block-weight decode: the
-// completion counters in a region of their own size whatever the split count
-// (so that calls of other shapes on the same workspace find it zero), then the
-// partials, the denominators and the raw block sums.
+// completion counters, then the partials, the denominators and the raw block sums.
 struct DecodeWsW {
   size_t cnt_bytes, o_bytes, ml_bytes, lse_bytes, raw_bytes, total;
 };
-constexpr size_t kCounterRegion = 65536;
 // partials: partial results of one head each (0: none), counters and partials
 // only where the call may leave some.
 DecodeWsW decode_ws_weights(int batch, int Hq, int Hkv, int D, long long partials, int max_blocks);

@@ -121,3 +121,44 @@ def test_value_scales_of_any_exponent(env, dtype, Hq, Hkv, d, log):
     half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -20
     for r in range(3):
         assert np.linalg.norm(out[r] - ref["out"][r]) <= (half + 2 * eps) * np.linalg.norm(ref["out"][r])
+
+
+def test_one_workspace_for_every_decode_call(env):
+    """A zeroed workspace serves attn_decode, its prerotated form, attn_mixed and the calls of one list in any order:
+    each result is that of the same call on a fresh workspace, and the counters stay zero."""
+    torch, mp, dev = env
+    few = make_batch(torch, dev, [5000, 17, 9000], 16, 2, 128, "bf16", 5)          # few pairs, many splits
+    many = [make_batch(torch, dev, [900 + 7 * i for i in range(90)], 8, 2, 128, kv, 6) for kv in ("bf16", "e4m3")]
+    ropes = {id(t): mp.rope_table(t["max_pos"], 128, t["base"], device=dev) for t in (few, *many)}
+
+    def plain(t, ws, prerotated=False):
+        a = (t["q"], t["k_pool"], t["v_pool"], t["block_tables"], t["block_starts"], t["seq_lens"], t["q_pos"])
+        f = mp.attn_decode_prerotated if prerotated else mp.attn_decode
+        return f(*a, *(() if prerotated else (ropes[id(t)],)), workspace=ws)[:1]
+
+    def listed(t, ws):
+        B, Hq, _ = t["q"].shape
+        out, bw = torch.empty_like(t["q"]), torch.zeros(B, t["Hkv"], t["block_tables"].shape[1], dtype=torch.bfloat16,
+                                                        device=dev)
+        call(mp, torch, t, ropes[id(t)], out, None, bw, ws)
+        return out, bw
+
+    def mixed(t, ws):
+        i32 = dict(dtype=torch.int32, device=dev)
+        p = dict(q=t["q"][:1], cu_q_lens=torch.tensor([0, 1], **i32), q_pos=t["q_pos"][:1],
+                 block_tables=t["block_tables"][:1], block_starts=t["block_starts"][:1], kv_lens=t["seq_lens"][:1],
+                 max_q_len=1)
+        dd = {k: t[k] for k in ("q", "block_tables", "block_starts", "seq_lens", "q_pos")}
+        return mp.attn_mixed(p, dd, t["k_pool"], t["v_pool"], ropes[id(t)], workspace=ws)[::2]
+    calls = [lambda ws: plain(few, ws), lambda ws: listed(many[0], ws), lambda ws: plain(few, ws, True),
+             lambda ws: listed(many[1], ws), lambda ws: mixed(few, ws), lambda ws: plain(many[0], ws),
+             lambda ws: listed(few, ws)]
+    n = max(max(workspace_size(mp, t), mp.decode_workspace_size(t["q"].shape[0], t["q"].shape[1], 2, 128,
+                                                                t["block_tables"].shape[1])) for t in (few, *many))
+    alone = [f(torch.zeros(n, dtype=torch.uint8, device=dev)) for f in calls]
+    ws = torch.zeros(n, dtype=torch.uint8, device=dev)
+    for i in (0, 1, 2, 3, 4, 5, 6, 5, 4, 3, 2, 1, 0, 6, 3, 0, 3):
+        got = calls[i](ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, alone[i])), i
+        assert not ws[:COUNTERS].any(), i
+    assert mp.device_error() == 0
