@@ -458,9 +458,10 @@ size_t minipic_attn_decode_weights_workspace_size(int32_t batch, int32_t num_q_h
  * and workspace rules as for minipic_attn_decode_q8, and like that call it never
  * reads a masked slot into a sum and passes an attended NaN on).  bf16 takes the
  * score product in fp16, rotated with rope->cos_sin_f16 (required; the bf16 rows
- * are not read), because the weights show the scores' error: key elements have to
- * stay within +-65504 (beyond, the rows that attend to them become NaN); queries
- * of any size are fine. */
+ * are not read), because the weights show the scores' error.  Keys and queries of
+ * any finite size are fine: rows of keys outside fp16's range are scaled by a power
+ * of two (a request and kv head with a key beyond 46340 is gone through twice).  An
+ * attended key with an infinite element leaves the rows that attend to it undefined. */
 minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
                                            const minipic_rope* rope, const minipic_decode_batch* batch, float scale,
                                            void* block_weights, void* workspace, size_t workspace_bytes,

@@ -756,7 +756,7 @@ def attn_decode_weights(q, k_pool, v_pool, block_tables, block_starts, seq_lens,
                         scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
     """``attn_decode`` that also writes ``block_weights`` (as in
     ``attn_decode_q8``), for eviction by attention weight.  bf16 takes the score
-    product in fp16 (keys within +-65504)."""
+    product in fp16, with rows of keys outside its range scaled."""
     L = load()
     shape = _sizes(k_pool, "k_pool", 4)
     _sizes(block_weights, "block_weights", 3)

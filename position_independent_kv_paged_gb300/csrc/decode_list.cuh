@@ -24,8 +24,9 @@
 //
 // Per block, with t the query's position, b the block's start, s the slot:
 //   score = (R_{t-b} q) . (R_s k) * (k scale) * softmax scale
-// e4m3 widens to fp16 exactly, bf16 within fp16's range (a key beyond it becomes
-// infinite; bf16 operands would show: three roundings of 2^-8 each,
+// e4m3 widens to fp16 exactly, bf16 within fp16's range, with rows outside it scaled
+// by a power of two where that matters (kFactor below; the test of that costs 2.7 %.
+// bf16 operands would show: three roundings of 2^-8 each,
 // an output error of 5.4e-3 of its norm at d 64 where this has 2.2e-3).  R_s is constant per lane, R_{t-b} q is formed once
 // per block, both in packed fp16, and S^T = K' Q'^T, O^T += V^T P^T run as
 // mma.sync m16n8k16 with fp32 accumulation (keys, then head dims, as M; up to 8
@@ -54,7 +55,7 @@
 //    which 0.30 GB from HBM.  Issue: 282 instructions a block and warp (81 of
 //    them fp16 rotation, 66 conversions, 16 matrix products), 53 % of the issue slots used.
 //  - 8 x 131072 keys, 64 / 8 heads, with block weights: 330 us, the same bound.
-//  - the first batch over the bf16 cache, with block weights: 187 us, 2.15 GB read
+//  - the first batch over the bf16 cache, with block weights: 190 us, 2.15 GB read
 //    (a grid of splits with tensor copies took 257 us and 669 instructions a block).
 //  - 128 ragged contexts to 32768 keys, 28 / 4 heads, nothing shared: HBM, 2.29 GB at
 //    6.45 TB/s (0.95 of the measured copy bandwidth).
@@ -82,6 +83,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;               // a reference moves when exceeded by 2^8
 constexpr float kHeadQ8 = 7.f;                // e4m3: P of a key at its reference is 2^7
 constexpr float kNone = -3e38f;               // a reference before the first key
+constexpr float kKeyMin = 0x1p-10f, kKeyMax = 0x1p15f;  // largest element of a bf16 key row that fp16 holds well
+constexpr uint32_t kWide = 0x40000u;          // mask bit: the key rows may need scaling
 constexpr float kNoValue = -3e38f;            // log2 of a value scale of zero: finite, and no score brings it near a reference
 
 // Shared-memory plan; Q8: e4m3 cache (else bf16).
@@ -130,6 +133,51 @@ __device__ __forceinline__ uint32_t at(int key, int c) {
   const int line = Q8 && D == 64 ? key >> 1 : key;
   const int ch = Q8 && D == 64 ? (key & 1) * 4 + c : c;
   return (uint32_t)(line * LN::BYTES + ((ch ^ LN::mix(line)) << 4));
+}
+
+// bf16 keys: a row whose largest element is outside [kKeyMin, kKeyMax] would lose bits in fp16 or leave it (rotated, an
+// element grows by up to sqrt(2)).  A block with such a row has its rows scaled, where they lie in shared memory, to a
+// largest element in [1, 2); returned are the powers of two that the scores of this lane's rows then lack.  Rare, and a
+// function of its own, so that its registers are not the loop's.
+template <int D>
+__device__ __noinline__ float2 rescale_rows(uint32_t kbase, int ks0, int tig) {
+  constexpr unsigned FULL = 0xffffffffu;
+  auto chunk = [&](int row, int u) {  // this lane's chunks of its rows: no other lane reads them
+    return kbase + at<D, false>(ks0 + 2 * row, (D == 128 ? 2 * tig + (u & 1) : tig) + (u >= D / 64 ? D / 16 : 0));
+  };
+  float m[2] = {0.f, 0.f};
+  bool off = false;
+#pragma unroll
+  for (int row = 0; row < 2; ++row) {
+#pragma unroll 1
+    for (int u = 0; u < D / 32; ++u) {
+      const U4 x = ptx::lds128(chunk(row, u));
+      auto larger = [&](uint32_t w) { m[row] = fmaxf(m[row], fmaxf(fabsf(ptx::bf_lo(w)), fabsf(ptx::bf_hi(w)))); };
+      larger(x.x);
+      larger(x.y);
+      larger(x.z);
+      larger(x.w);
+    }
+    m[row] = fmaxf(m[row], __shfl_xor_sync(FULL, m[row], 1));
+    m[row] = fmaxf(m[row], __shfl_xor_sync(FULL, m[row], 2));
+    off |= m[row] != 0.f && !(m[row] >= kKeyMin && m[row] <= kKeyMax);
+  }
+  if (!__any_sync(FULL, off)) return make_float2(1.f, 1.f);
+  float up[2];
+#pragma unroll
+  for (int row = 0; row < 2; ++row) {
+    const int ex = max(-126, min(126, (__float_as_int(m[row]) >> 23) - 127));
+    const float down = __int_as_float((127 - ex) << 23);
+    up[row] = __int_as_float((ex + 127) << 23);
+#pragma unroll 1
+    for (int u = 0; u < D / 32; ++u) {
+      const U4 x = ptx::lds128(chunk(row, u));
+      auto scaled = [&](uint32_t w) { return ptx::pack_bf16(ptx::bf_lo(w) * down, ptx::bf_hi(w) * down); };
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(row, u)), "r"(scaled(x.x)), "r"(scaled(x.y)),
+                   "r"(scaled(x.z)), "r"(scaled(x.w)) : "memory");
+    }
+  }
+  return make_float2(up[0], up[1]);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -203,6 +251,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     int r, hk, nblk, L;   // the pair: request, kv head, blocks, length
     int b_begin, left;    // its first block in this range, blocks of the range from there on
     int whole, last;      // one part of a pair per CTA; last to finish its pair
+    int large, wide;      // the pair's key rows may need scaling: its queries are large; it was seen to need it
+    int redo;             // the pair has to be gone through again, wide
   } sg;
   auto cta_total = [&](int v, int& before) {  // sum of v over the CTA, and over the threads before this one
     int pre = v;
@@ -225,7 +275,10 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   };
   // No owner until a thread below finds the pair.  Stored before the barriers of the first pass, which order it before
   // that thread's store: a batch of up to one pass in equal ranges meets no other barrier in between.
-  if (threadIdx.x == 0) sg.r = -1;
+  if (threadIdx.x == 0) {
+    sg.r = -1;
+    sg.large = sg.wide = sg.redo = 0;
+  }
   long long total = 0, sum = 0;
   int pairs = 0, zero = 0, Li = 0, n = 0, before = 0;
   for (int base = 0; base < a.batch; base += NW * 32) {
@@ -300,6 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     __syncthreads();
     if (sg.r < 0) return;  // more CTAs than parts
   }
+  constexpr float kFactor = 8192.f / D;
   int b0 = 0, span = 0, n_stage = 0;             // the chunk's first block, blocks, stages of this warp
   uint32_t qx[NT][2 * NH], qy[NT][2 * NH];       // queries of this thread's heads (column g8 + 8 nt), fp16
   __shared__ float2 s_qf[NT][4];                 // the power of two taken out of those of columns 2 tig + j + 8 nt
@@ -389,6 +443,42 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       if (p < n_stage) issue(p, p0, p1);
       ptx::cp_async_commit();
     }
+    auto scale_queries = [&] {  // to fp16
+      bool large = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2 * NH; ++e)
+          amax = fmaxf(amax, fmaxf(fmaxf(fabsf(ptx::bf_lo(qx[nt][e])), fabsf(ptx::bf_hi(qx[nt][e]))),
+                                   fmaxf(fabsf(ptx::bf_lo(qy[nt][e])), fabsf(ptx::bf_hi(qy[nt][e])))));
+        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 2));
+        // exponent of the largest element (at most 127, an infinity's; a row of zeros or subnormals takes -126)
+        int ex = (__float_as_int(amax) >> 23) - 127;
+        ex = ex < -126 ? -126 : (ex > 126 ? 126 : ex);
+        const float down = __int_as_float((127 - ex) << 23);
+#pragma unroll
+        for (int e = 0; e < 2 * NH; ++e) {
+          qx[nt][e] = ptx::pack_f16(ptx::bf_lo(qx[nt][e]) * down, ptx::bf_hi(qx[nt][e]) * down);
+          qy[nt][e] = ptx::pack_f16(ptx::bf_lo(qy[nt][e]) * down, ptx::bf_hi(qy[nt][e]) * down);
+        }
+        const float up = __int_as_float((ex + 127) << 23);
+        if (warp == 0 && tig == 0) reinterpret_cast<float*>(s_qf[nt])[g8] = up;
+        large |= up * (a.scale * kLog2e) > kFactor;
+      }
+      return large;
+    };
+    [[maybe_unused]] bool wide = false;
+    if constexpr (!Q8) {
+      if (first) {
+        const bool large = __any_sync(FULL, scale_queries());  // every warp holds every head of the pair
+        if (threadIdx.x == 0) sg.large = large;
+        wide = large || sg.wide;
+      } else {
+        wide = sg.large || sg.wide;
+      }
+    }
     float t_ks[kPer], t_vs[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
@@ -424,6 +514,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
             m |= 0x10000u;
           }
           if (start > tq) m |= 0x20000u;
+          if (wide) m |= kWide;
         }
       }
       meta[i] = make_int4(pl.x, pl.y, __float_as_int(ks), __float_as_int(lv));
@@ -433,31 +524,16 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       meta[kChunk + threadIdx.x] = make_int4(-1, 0, 0, 0);
       vmask[kChunk + threadIdx.x] = 0u;
     }
-    if (first) {  // the queries scaled to fp16
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float amax = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2 * NH; ++e)
-          amax = fmaxf(amax, fmaxf(fmaxf(fabsf(ptx::bf_lo(qx[nt][e])), fabsf(ptx::bf_hi(qx[nt][e]))),
-                                   fmaxf(fabsf(ptx::bf_lo(qy[nt][e])), fabsf(ptx::bf_hi(qy[nt][e])))));
-        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(FULL, amax, 2));
-        // exponent of the largest element (at most 127, an infinity's; a row of zeros or subnormals takes -126)
-        int ex = (__float_as_int(amax) >> 23) - 127;
-        ex = ex < -126 ? -126 : (ex > 126 ? 126 : ex);
-        const float down = __int_as_float((127 - ex) << 23);
-#pragma unroll
-        for (int e = 0; e < 2 * NH; ++e) {
-          qx[nt][e] = ptx::pack_f16(ptx::bf_lo(qx[nt][e]) * down, ptx::bf_hi(qx[nt][e]) * down);
-          qy[nt][e] = ptx::pack_f16(ptx::bf_lo(qy[nt][e]) * down, ptx::bf_hi(qy[nt][e]) * down);
-        }
-        if (warp == 0 && tig == 0) reinterpret_cast<float*>(s_qf[nt])[g8] = __int_as_float((ex + 127) << 23);
-      }
-    }
+    if constexpr (Q8)
+      if (first) scale_queries();
     __syncthreads();  // metadata visible
   };
 
+  // bf16 keys.  A key beyond fp16 makes its row's every product infinite or NaN: the softmax sees that, and the pair
+  // is gone through again with every row looked at.  A small key loses bits, at most 3.4 * 2^-25 of a rotated element,
+  // 2^-9 of a score's binary logarithm (the rounding of P) while the scores' factor is up to kFactor (queries up to
+  // 500 at the default scale); beyond, the rows are looked at from the start.  So a batch of usual sizes pays only a
+  // sum and a comparison a block.
   // references: ms of the scores (denominator l), mt of the scores plus log2 of the value scale (O)
   // (before the first key a finite value far below any score, so that no difference of two is undefined)
   float ms[NT][2], mt[NT][2], l[NT][2];
@@ -550,22 +626,33 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   float* w_base = nullptr;  // raw sums of the pair
   // one step of the online softmax over 16 keys; m, ks and lv are those of the columns' block, wb the block
   // whose sum is recorded
-  auto softmax = [&](auto plain, float (&sc)[NT][4], uint32_t m, float ks, float lv, int wb, uint32_t (&pb0)[NT],
-                     uint32_t (&pb1)[NT]) {
+  auto softmax = [&](auto plain, float (&sc)[NT][4], [[maybe_unused]] const float (&kf)[2], uint32_t m, float ks, float lv,
+                     int wb, uint32_t (&pb0)[NT], uint32_t (&pb1)[NT]) {
     const bool v0 = decltype(plain)::value || ((m >> ks0) & 1u), v1 = decltype(plain)::value || ((m >> (ks0 + 2)) & 1u);
     bool over = false;
+    [[maybe_unused]] bool beyond = false;
+    if constexpr (!Q8) {
+      if constexpr (decltype(plain)::value) beyond = !(fabsf(sc[0][0]) + fabsf(sc[0][2]) < 3e38f);
+      else beyond = !(m & kWide) && ((v0 && !(fabsf(sc[0][0]) < 3e38f)) || (v1 && !(fabsf(sc[0][2]) < 3e38f)));
+      over = beyond;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 qf = s_qf[nt][tig];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float f = fminf(ks * (j ? qf.y : qf.x), 3.4e38f);  // finite: a product of 0 stays 0
-        sc[nt][j] = v0 ? sc[nt][j] * f : -CUDART_INF_F;
-        sc[nt][2 + j] = v1 ? sc[nt][2 + j] * f : -CUDART_INF_F;
+        // finite: a product of 0 stays 0
+        constexpr bool one = Q8 || decltype(plain)::value;
+        const float q = j ? qf.y : qf.x;
+        const float f0 = fminf(ks * (one ? q : q * kf[0]), 3.4e38f), f1 = one ? f0 : fminf(ks * (q * kf[1]), 3.4e38f);
+        sc[nt][j] = v0 ? sc[nt][j] * f0 : -CUDART_INF_F;
+        sc[nt][2 + j] = v1 ? sc[nt][2 + j] * f1 : -CUDART_INF_F;
         over |= fmaxf(sc[nt][j], sc[nt][2 + j]) > (Q8 ? fminf(ms[nt][j], mt[nt][j] - lv) : ms[nt][j]) + kRescale;
       }
     }
     if (__any_sync(FULL, over)) {  // rare: move the references, rescale what was summed
+      if constexpr (!Q8)
+        if (beyond) sg.redo = 1;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -664,7 +751,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
 
   auto pair = [&](auto plain, uint32_t kbase, uint32_t rowb, int i0, uint32_t m0, uint32_t m1) {
     uint32_t bx[NT][2 * NH], by[NT][2 * NH], pb0[NT], pb1[NT];
-    float sc[NT][4];
+    float sc[NT][4], kf[2] = {1.f, 1.f};
     if constexpr (DUAL) {
       const int4 mc = meta[i0 + (tig >= 2 ? NW : 0)];  // of these score columns' block
       rotate_q(plain, rowb + (g8 >= 4 ? LY::ROWB : 0), g8 >= 4 ? m1 : m0, bx, by);
@@ -673,7 +760,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       scores(kbase + 2 * LY::TILE, bx, by, s1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sc[0][e] = tig >= 2 ? s1[0][e] : sc[0][e];
-      softmax(plain, sc, tig >= 2 ? m1 : m0, __int_as_float(mc.z), __int_as_float(mc.w),
+      softmax(plain, sc, kf, tig >= 2 ? m1 : m0, __int_as_float(mc.z), __int_as_float(mc.w),
               b0 + i0 + (tig >= 2 ? NW : 0), pb0, pb1);
       const uint32_t z0[1] = {g8 < 4 ? pb0[0] : 0u}, z1[1] = {g8 < 4 ? pb1[0] : 0u};
       const uint32_t y0[1] = {g8 < 4 ? 0u : pb0[0]}, y1[1] = {g8 < 4 ? 0u : pb1[0]};
@@ -684,9 +771,15 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       for (int u = 0; u < BPS; ++u) {
         const int4 md = meta[i0 + u * NW];
         const uint32_t m = u ? m1 : m0;
+        if constexpr (!Q8 && !decltype(plain)::value)
+          if (m & kWide) {
+            const float2 up = rescale_rows<D>(kbase, ks0, tig);
+            kf[0] = up.x;
+            kf[1] = up.y;
+          }
         rotate_q(plain, rowb + u * LY::ROWB, m, bx, by);
         scores(kbase + 2 * u * LY::TILE, bx, by, sc);
-        softmax(plain, sc, m, __int_as_float(md.z), __int_as_float(md.w), b0 + i0 + u * NW, pb0, pb1);
+        softmax(plain, sc, kf, m, __int_as_float(md.z), __int_as_float(md.w), b0 + i0 + u * NW, pb0, pb1);
         values(plain, kbase + (2 * u + 1) * LY::TILE, m, pb0, pb1);
       }
     }
@@ -737,6 +830,16 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       if (b0 >= sg.nblk || b0 >= sg.b_begin + sg.left) break;
     }
     __syncthreads();  // every stage has been read: the merge overlays them
+    if constexpr (!Q8)
+      if (sg.redo) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          sg.redo = 0;
+          sg.wide = 1;
+        }
+        __syncthreads();
+        continue;
+      }
     const int r = sg.r, hk = sg.hk, b_begin = sg.b_begin, nblk = sg.nblk, b_end = b0;
 
     // per-warp state: ms[16], l[16], mt[16], O[16][OST], by column
@@ -874,6 +977,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     __syncthreads();  // the pair has been read
     if (threadIdx.x == 0) {
       sg.left = left;
+      sg.wide = 0;
       sg.b_begin = 0;
       sg.hk = hk + 1;
       if (hk + 1 == a.Hkv) {

@@ -162,3 +162,51 @@ def test_one_workspace_for_every_decode_call(env):
         assert all(torch.equal(a, b) for a, b in zip(got, alone[i])), i
         assert not ws[:COUNTERS].any(), i
     assert mp.device_error() == 0
+
+
+def decode_weights(env, t):
+    torch, mp, dev = env
+    B, Hq, d = t["q"].shape
+    out = torch.full_like(t["q"], float("nan"))
+    lse = torch.full((B, Hq), float("nan"), device=dev)
+    bw = torch.full((B, t["Hkv"], t["block_tables"].shape[1]), 7.0, dtype=torch.bfloat16, device=dev)
+    call(mp, torch, t, mp.rope_table(t["max_pos"], d, t["base"], device=dev), out, lse, bw, None)
+    torch.cuda.synchronize()
+    return out, lse, bw
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 1, 128), (32, 2, 128), (16, 1, 64)])
+@pytest.mark.parametrize("log", [17, 100, 117, -12, -20, -45, -110])
+def test_bf16_keys_of_any_size(env, Hq, Hkv, d, log):
+    """Keys far outside fp16's range against queries that bring the scores back, in one kv head; the others' keys as
+    they come.  Powers of two, so the operands are the same numbers."""
+    torch, mp, dev = env
+    t = make_batch(torch, dev, [700, 33, 1, 200], Hq, Hkv, d, "bf16", 80)
+    G = Hq // Hkv
+    t["k_pool"][:, 0] *= 2.0 ** log
+    t["q"][:, :G] *= 2.0 ** -log
+    check(torch, t, *decode_weights(env, t), f"2^{log}")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (8, 1, 128), (32, 2, 128)])
+def test_bf16_keys_of_sizes_that_differ_within_a_block(env, Hq, Hkv, d):
+    """Rows between 2^-30 and 2^-14 of one block, rows of zeros, quarters of zeros, and pairs near 6e4 whose rotation
+    leaves fp16; slots past the lengths hold huge values and infinities."""
+    torch, mp, dev = env
+    lens = [700, 33, 1, 200]
+    t = make_batch(torch, dev, lens, Hq, Hkv, d, "bf16", 81)
+    g = torch.Generator(device=dev).manual_seed(3)
+    e = torch.randint(-30, -13, t["k_pool"].shape[:3], generator=g, device=dev)
+    t["k_pool"] *= torch.exp2(e)[..., None].bfloat16()
+    t["k_pool"][::3, :, 5] = 0
+    t["k_pool"][::2, :, :, :d // 8] = 0
+    t["q"] *= 2.0 ** 16
+    for r, n in enumerate(lens):
+        if n % 16:
+            t["k_pool"][int(t["block_tables"][r, n // 16]), :, n % 16:] = float("inf") if r & 1 else 3e38
+    check(torch, t, *decode_weights(env, t), "small")
+    t = make_batch(torch, dev, lens, Hq, Hkv, d, "bf16", 82)
+    t["k_pool"] = (t["k_pool"].float() * 16000).clamp(-6.4e4, 6.4e4).bfloat16()
+    t["q"] *= 2.0 ** -14
+    check(torch, t, *decode_weights(env, t), "large")
+    assert mp.device_error() == 0
