@@ -224,6 +224,15 @@ def _stream(stream) -> Optional[int]:
     return s.cuda_stream
 
 
+def _longest(cu_lens, stream) -> int:
+    """The largest count of prefix sums that work on ``stream`` may still be writing."""
+    torch = _torch()
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return int((cu_lens[1:] - cu_lens[:-1]).max().item())
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     if t.dtype == torch.float32:
@@ -542,7 +551,7 @@ def kv_append(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_pool,
     if cu_new_lens.shape[0] != B + 1 or block_tables.shape[0] != B:
         raise ValueError("cu_new_lens must have batch + 1 entries and block_tables batch rows")
     if max_new_len is None:
-        max_new_len = int((cu_new_lens[1:] - cu_new_lens[:-1]).max().item()) if B else 0
+        max_new_len = _longest(cu_new_lens, stream) if B else 0
     ab = _Append(k_new.data_ptr(), v_new.data_ptr(), cu_new_lens.data_ptr(), kv_start.data_ptr(),
                  block_tables.data_ptr(), B, k_new.shape[0], int(max_new_len), block_tables.shape[1])
     _check(L.minipic_kv_append(_dtype_code(k_pool), ctypes.byref(kv), ctypes.byref(ab), _stream(stream)),
@@ -687,7 +696,7 @@ def kv_append_q8(k_new, v_new, cu_new_lens, kv_start, block_tables, k_pool, v_po
           ("cu_new_lens", cu_new_lens, torch.int32, (B + 1,)), ("kv_start", kv_start, torch.int32, (B,)),
           ("block_tables", block_tables, torch.int32, (B, mb)), *specs)
     if max_new_len is None:
-        max_new_len = int((cu_new_lens[1:] - cu_new_lens[:-1]).max().item()) if B else 0
+        max_new_len = _longest(cu_new_lens, stream) if B else 0
     kv = _kv_q8_struct(specs)
     ab = _Append(k_new.data_ptr(), v_new.data_ptr(), cu_new_lens.data_ptr(), kv_start.data_ptr(),
                  block_tables.data_ptr(), B, total, int(max_new_len), mb)
