@@ -232,6 +232,9 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
             if (my_ph >= 0 && my_ph < a.num_blocks) flag |= 1;
             else atomicOr(a.err, kErrBlockId);
             if (!ROPE || (my_st >= 0 && my_st < a.max_pos)) flag |= 2;
+            // keys outside the table are masked, with a start outside it the whole block
+            if (ROPE && (flag & 1) && (my_st < 0 || my_st > a.max_pos - min(16, kvl - 16 * (NB * u + lane))))
+              atomicOr(a.err, kErrPosition);
           }
           int* m = meta + 3 * NB * s;
           if (lane < NB) {

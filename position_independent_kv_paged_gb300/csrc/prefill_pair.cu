@@ -327,8 +327,11 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
                 bits = nk >= 16 ? 0xffffu : (1u << nk) - 1u;
                 if (ROPE) {
                   const int room = a.max_pos - my_st;
+                  if (mine && room < nk) atomicOr(a.err, kErrPosition);
                   bits &= room >= 16 ? 0xffffu : (1u << room) - 1u;
                 }
+              } else if (mine && (flag & 1)) {
+                atomicOr(a.err, kErrPosition);  // the start lies outside the table: masked whole
               }
               mask16[(u % kMaskRing) * kTileBlocks + lane] = (uint16_t)bits;
             }
