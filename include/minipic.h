@@ -68,7 +68,10 @@
  *  any launch.  Device data (block ids, positions, lengths) is checked inside
  *  the kernels: an out-of-range block id or position is skipped (treated as a
  *  masked key) and a bit is set in a device error word that
- *  minipic_device_error() reads and clears.
+ *  minipic_device_error() reads and clears.  Of a block that starts before
+ *  position 0 the f32 calls mask the slots before it; the bf16 decode calls mask
+ *  the whole block where the query's position minus its start is max_pos or more
+ *  (no table row holds that angle), the prefill calls always.
  */
 #ifndef MINIPIC_H
 #define MINIPIC_H
@@ -290,7 +293,8 @@ size_t minipic_attn_prefill_workspace_size(int32_t batch, int32_t num_q_heads, i
  * required); the query is rotated in fp32 with the fp32 table.  The rotated q
  * and k are fp16 for the QK^T product (10-bit mantissa: rotated elements must
  * stay within +-65504; an element outside sets MINIPIC_DEVERR_RANGE and the
- * rows that read it are undefined); softmax weights and V are bf16 for the P.V product;
+ * rows that read it are undefined; elements under 2^-14 are held to 2^-25 absolute);
+ * softmax weights and V are bf16 for the P.V product;
  * accumulation is fp32.  bf16 only (f32 returns UNSUPPORTED).  The workspace
  * is not used (size 0).  Errors as for decode. */
 minipic_status minipic_attn_prefill(minipic_dtype dtype, int32_t num_q_heads,
@@ -432,8 +436,8 @@ size_t minipic_attn_prefill_q8_workspace_size(int32_t batch, int32_t num_q_heads
 
 /* Chunked prefill over the 8-bit cache (the chunk's own keys are its last ones
  * and were appended before): the gathered blocks are widened in the workspace --
- * keys rotated in fp32 at their positions and rounded to fp16 (outside its range:
- * MINIPIC_DEVERR_RANGE), values to bf16 (exact where a scale is a power of two, as
+ * keys rotated in fp32 at their positions and rounded to fp16 (outside its range, or
+ * NaN: MINIPIC_DEVERR_RANGE; under 2^-14: to 2^-25 absolute), values to bf16 (exact where a scale is a power of two, as
  * the append writes them, else rounded once) -- and minipic_attn_prefill's kernel
  * runs over them.  bf16 only.  The workspace needs no initial value and holds
  * nothing between calls; calls whose work overlaps need workspaces of their own.

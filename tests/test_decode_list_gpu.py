@@ -210,3 +210,26 @@ def test_bf16_keys_of_sizes_that_differ_within_a_block(env, Hq, Hkv, d):
     t["q"] *= 2.0 ** -14
     check(torch, t, *decode_weights(env, t), "large")
     assert mp.device_error() == 0
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (4, 2, 64), (16, 1, 64)])
+def test_blocks_that_start_before_the_table(env, kv, Hq, Hkv, d):
+    """Slots before position 0 are masked; where the query is so far on that no table row holds the angle to the
+    block's start, the whole block is.  Flagged either way."""
+    torch, mp, dev = env
+    for near in (True, False):
+        t = make_batch(torch, dev, [200, 64], Hq, Hkv, d, kv, 95)
+        t["block_starts"][0, 3] = -5
+        mp.device_error(clear=True)
+        t["q_pos"][0] = t["max_pos"] - (6 if near else 1)   # distance to the block's start: max_pos - 1 or + 4
+        B, mb = t["block_tables"].shape
+        out, lse = torch.empty_like(t["q"]), torch.empty(B, Hq, device=dev)
+        bw = torch.full((B, Hkv, mb), 7.0, dtype=torch.bfloat16, device=dev)
+        call(mp, torch, t, mp.rope_table(t["max_pos"], d, t["base"], device=dev), out, lse, bw, None)
+        torch.cuda.synchronize()
+        assert mp.device_error(clear=True) == 2
+        if not near:
+            t["block_tables"][0, 3] = -1    # for the reference
+        check(torch, t, out, lse, bw, str(near))
+        assert near or (bw[0, :, 3] == 0).all()
