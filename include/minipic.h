@@ -439,7 +439,7 @@ size_t minipic_attn_prefill_q8_workspace_size(int32_t batch, int32_t num_q_heads
  * keys rotated in fp32 at their positions and rounded to fp16 (outside its range, or
  * NaN: MINIPIC_DEVERR_RANGE; under 2^-14: to 2^-25 absolute), values to bf16 (exact where a scale is a power of two, as
  * the append writes them, else rounded once) -- and minipic_attn_prefill's kernel
- * runs over them.  bf16 only.  The workspace needs no initial value and holds
+ * runs over them.  A NaN key or value makes the rows that attend to it NaN, whole.  bf16 only.  The workspace needs no initial value and holds
  * nothing between calls; calls whose work overlaps need workspaces of their own.
  * Errors as for minipic_attn_prefill, WORKSPACE when it is too small,
  * UNSUPPORTED when batch * max_blocks_per_seq * num_kv_heads * 16 exceeds

@@ -8,6 +8,9 @@
 //           significant bits)
 // Slots past the request's length or the rotary table are written as zeros, so that
 // what a masked slot happens to hold (NaN bytes included) never meets a product.
+// A NaN value of a key in use would meet the weight 0 of the rows that must not see
+// it yet, and make them NaN: it becomes 0 and its key NaN, whose scores the causal
+// mask replaces, so the rows that do attend to it are NaN whole and no others are.
 //
 // Memory-bound: 1 byte read and 2 written per value, plus cos | sin rows that the
 // kv heads of a block share through L1.  Measured on 8 requests of 416 blocks, 8
@@ -23,6 +26,9 @@ namespace minipic {
 namespace {
 
 constexpr int kThreads = 256;
+
+// Any NaN (0x7f, 0xff) among four e4m3 bytes?
+__device__ __forceinline__ bool has_nan(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv_restore_q8_kernel(RestoreArgs a) {
@@ -45,12 +51,14 @@ __global__ void __launch_bounds__(kThreads) kv_restore_q8_kernel(RestoreArgs a) 
   uint4* ko = reinterpret_cast<uint4*>(a.k_out) + to * chunks * 2;
   uint4* vo = reinterpret_cast<uint4*>(a.v_out) + to * chunks * 2;
   // values: 16 at a time
+  bool nan = false;
   for (int i = threadIdx.x; i < chunks; i += kThreads) {
     const int h = i / CPT, slot = (i % CPT) / CPR;
     const long long pos = (long long)start + slot;
     const bool use = slot < nk && pos >= 0 && pos < a.max_pos;
     const uint4 v = use ? __ldg(vp + i) : zero;
     const float s = __ldg(a.v_scale + (size_t)phys * a.Hkv + h);
+    nan |= has_nan(v.x) || has_nan(v.y) || has_nan(v.z) || has_nan(v.w);
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t o[8];
 #pragma unroll
@@ -100,6 +108,19 @@ __global__ void __launch_bounds__(kThreads) kv_restore_q8_kernel(RestoreArgs a) 
     ko[(row + D / 2 + f0) / 8] = yo;
   }
   if (over) atomicOr(a.err, kErrRange);
+  if (__syncthreads_or(nan)) {  // rare: NaN values; what is written again was written before the barrier
+    for (int i = threadIdx.x; i < chunks; i += kThreads) {
+      const int h = i / CPT, slot = (i % CPT) / CPR;
+      const long long pos = (long long)start + slot;
+      const uint4 v = slot < nk && pos >= 0 && pos < a.max_pos ? __ldg(vp + i) : zero;
+      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+      for (int e = 0; e < 16; ++e) {
+        if (((in[e / 4] >> (8 * (e % 4))) & 0x7fu) != 0x7fu) continue;
+        a.v_out[(to * chunks + i) * 16 + e] = 0;
+        a.k_out[to * chunks * 16 + (size_t)(h * 16 + slot) * D] = 0x7e00;  // several write the same
+      }
+    }
+  }
 }
 
 }  // namespace

@@ -77,3 +77,20 @@ def test_8bit_keys_outside_fp16_are_flagged(env, Hq, Hkv, d):
             np.where(np.arange(Hq)[None, :, None] < G, 0, good[k]) for k in ("out", "spread", "mass", "smax")}
     check_attention(np.where(np.arange(Hq)[None, :, None] < G, 0, out), part, "bf16", d, 200, p_half=2.0 ** -8)
     check_attention(out[70:], {k: v[70:] for k, v in good.items() if k != "weights"}, "bf16", d, 200, p_half=2.0 ** -8)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (4, 2, 64)])
+def test_8bit_prefill_passes_nan_on(env, Hq, Hkv, d):
+    """A NaN key or value makes the rows of its head group that attend to it NaN; the rows of the chunk before it, whose
+    causal mask excludes it, stay right, as do the other heads."""
+    c = Case(92, (96, 64), Hq, Hkv, d, "bf16", q_lens=(96, 64), share=False)
+    good = c.reference(causal=True)
+    c.pool[0][c.tables[0, 2], 0, 3, 5] = 0x7f            # key 35 of request 0
+    c.pool[1][c.tables[1, 1], Hkv - 1, 2, 7] = 0xff      # value of key 18 of request 1
+    out, lse, err = prefill(env, c, "e4m3")
+    G = Hq // Hkv
+    assert np.all(np.isnan(out[35:96, :G])) and np.all(np.isnan(out[96 + 18:, -G:]))
+    ok = np.ones(out.shape, bool)
+    ok[35:96, :G] = ok[96 + 18:, -G:] = False
+    zeroed = {k: np.where(ok, v, 0) if v.ndim == 3 else v for k, v in good.items() if k in ("out", "spread", "mass", "smax")}
+    check_attention(np.where(ok, out, 0), zeroed, "bf16", d, 96, p_half=2.0 ** -8)
