@@ -501,8 +501,10 @@ typedef struct {
  * last keep_last stay together with the best of the others by score (NaN is
  * the worst; of equal scores the lower index stays) up to `budget`.  The
  * outputs hold the kept blocks in order, seq_lens_out is shorter by
- * block_size for each block that left, and the entries behind are -1 (tables),
- * 0 (starts) and 0 (scores).  dtype is that of block_weights.  A length that is
+ * block_size for each block that left, and all entries behind are -1 (tables),
+ * 0 (starts) and 0 (scores), whether a block left or not: blocks that a table
+ * holds ahead of its length leave it without being listed in `evicted`, so put
+ * the next block in after this call, when the last one is full.  dtype is that of block_weights.  A length that is
  * negative or above max_blocks_per_seq * 16 sets MINIPIC_DEVERR_SEQ_LEN and is
  * clamped.  The pools are not touched: a block listed in `evicted` may still
  * belong to other requests, which the caller's block accounting knows

@@ -836,7 +836,9 @@ def kv_evict(scores, block_tables, block_starts, seq_lens, budget: int, keep_fir
     and last ``keep_last`` blocks and the best others by score.  Kept blocks
     stay in order and keep their logical starts.  ``evicted`` lists the physical
     ids that left (``n_evicted`` of them, then -1); whether they are free is for
-    the caller's block accounting.  With ``inplace`` the scores, tables, starts
+    the caller's block accounting.  Entries behind the kept blocks are cleared
+    (-1, starts and scores 0), blocks reserved there among them, which are not
+    listed.  With ``inplace`` the scores, tables, starts
     and lengths are overwritten and returned."""
     torch = _torch()
     L = load()
