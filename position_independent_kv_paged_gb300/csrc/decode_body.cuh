@@ -98,6 +98,7 @@ struct Chunks {
 // slot + 8).  Rows read together by a quarter warp then differ in bit 2 of the
 // slot, which keeps the swizzled key-row reads conflict-free.
 __device__ __forceinline__ int frag_slot(int g) { return (g >> 1) | ((g & 1) << 2); }
+__device__ __forceinline__ int frag_row(int slot) { return ((slot & 3) << 1) | (slot >> 2); }  // its inverse
 
 // Byte offset of (half, key, chunk) in a swizzled [half][16 keys][128 B] tile.
 __device__ __forceinline__ uint32_t swz(int half, int key, int chunk) {
@@ -482,6 +483,19 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
             oacc[mt][nt][j] *= corr[nt][j];
             oacc[mt][nt][2 + j] *= corr[nt][j];
           }
+    }
+
+    // V of masked keys is cleared (nothing was loaded for a bad id, a slot past the length may hold anything): their
+    // weight 0 must not meet a NaN or an infinity.  Whole blocks, nearly all, pass by.
+    if (!__all_sync(0xffffffffu, v0 && v1)) {
+      const uint32_t live = __ballot_sync(0xffffffffu, v0), live8 = __ballot_sync(0xffffffffu, v1);  // lane 4 g: row g
+      for (int i = lane; i < 16 * (D / 8); i += 32) {
+        const int slot = i / (D / 8), c = i % (D / 8);
+        if (((slot < 8 ? live : live8) >> (4 * frag_row(slot & 7))) & 1u) continue;
+        *reinterpret_cast<uint4*>(sgen + (vbase - sbase) + swz(c >> 3, slot, c & 7)) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      ptx::fence_proxy_async_smem();  // before the stage's next copy
+      __syncwarp();
     }
 
     // O^T += V^T P^T
