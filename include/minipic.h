@@ -224,6 +224,7 @@ size_t minipic_attn_decode_workspace_size(int32_t batch, int32_t num_q_heads, in
  * log-sum-exp merge of the splits).  Rotates q at q_pos and every gathered key
  * at its pi(j) from the table.  dtype selects f32 or bf16 for q, pools and out
  * (arithmetic is fp32; bf16 uses tensor-core products with bf16 operands).
+ * What masked slots hold never shows.
  * workspace: device, >= minipic_attn_decode_workspace_size(...) bytes
  * (may be NULL when that size is 0).  Errors: INVALID, UNSUPPORTED, WORKSPACE,
  * CUDA; device-data problems are reported by minipic_device_error. */
@@ -295,8 +296,11 @@ size_t minipic_attn_prefill_workspace_size(int32_t batch, int32_t num_q_heads, i
  * stay within +-65504; an element outside sets MINIPIC_DEVERR_RANGE and the
  * rows that read it are undefined; elements under 2^-14 are held to 2^-25 absolute);
  * softmax weights and V are bf16 for the P.V product;
- * accumulation is fp32.  bf16 only (f32 returns UNSUPPORTED).  The workspace
- * is not used (size 0).  Errors as for decode. */
+ * accumulation is fp32.  V of every slot of a block that a request reads must be
+ * finite, those past its length and the chunk's later keys among them: a masked
+ * key's weight is 0, which meets V in the product (keys may hold anything).  bf16
+ * only (f32 returns UNSUPPORTED).  The workspace is not used (size 0).  Errors as
+ * for decode. */
 minipic_status minipic_attn_prefill(minipic_dtype dtype, int32_t num_q_heads,
                                     const minipic_kv_pool* kv, const minipic_rope* rope,
                                     const minipic_prefill_batch* batch, float scale,

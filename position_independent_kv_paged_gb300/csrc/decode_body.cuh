@@ -94,6 +94,11 @@ struct Chunks {
   }
 };
 
+// |t - b| for any two 32-bit integers (a table's start may be any value until it has been checked)
+__device__ __forceinline__ uint32_t angle_distance(int t, int b) {
+  return b > t ? (uint32_t)b - (uint32_t)t : (uint32_t)t - (uint32_t)b;
+}
+
 // Physical key (slot) held by MMA fragment row g (g < 8; row g + 8 holds
 // slot + 8).  Rows read together by a quarter warp then differ in bit 2 of the
 // slot, which keeps the swizzled key-row reads conflict-free.
@@ -199,13 +204,13 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
       ptx::mbar_arrive(bar);  // nothing to load; the consumer masks the block
       return;
     }
-    int ad = 0, neg = 0;
+    uint32_t ad = 0;
+    int neg = 0;
     bool row_ok = false;
     if constexpr (ROPE) {
-      const int delta = tqv - start;
-      ad = delta < 0 ? -delta : delta;
-      neg = delta < 0 ? 1 : 0;
-      row_ok = ad < a.max_pos;
+      ad = angle_distance(tqv, start);
+      neg = start > tqv ? 1 : 0;
+      row_ok = ad < (uint32_t)a.max_pos;
     }
     ptx::mbar_arrive_expect_tx(bar, 2 * GE::TILE + (row_ok ? SM::ROWB : 0));
     const int y = (phys * a.Hkv + hk) * 16;
@@ -357,14 +362,12 @@ __device__ __forceinline__ void decode_cta(const CUtensorMap* kmap_p, const CUte
     const int nk = min(16, L - b * 16);
     bool v0 = ok && ks0 < nk, v1 = ok && ks0 + 8 < nk;
     if (!ok && lane == 0) atomicOr(a.err, kErrBlockId);
-    int delta = 0;
     if constexpr (ROPE) {
-      delta = tq - start;
-      const int ad = delta < 0 ? -delta : delta;
-      if (ok && !(ad < a.max_pos && start >= 0 && start + nk - 1 < a.max_pos)) {
+      const bool row_ok = angle_distance(tq, start) < (uint32_t)a.max_pos;
+      if (ok && !(row_ok && start >= 0 && start <= a.max_pos - nk)) {
         // keys whose position falls outside the table are masked
-        const bool p0 = start + ks0 >= 0 && start + ks0 < a.max_pos && ad < a.max_pos;
-        const bool p1 = start + ks0 + 8 >= 0 && start + ks0 + 8 < a.max_pos && ad < a.max_pos;
+        const bool p0 = row_ok && start >= -ks0 && start < a.max_pos - ks0;
+        const bool p1 = row_ok && start >= -ks0 - 8 && start < a.max_pos - ks0 - 8;
         if (__any_sync(0xffffffffu, (v0 && !p0) || (v1 && !p1)) && lane == 0) atomicOr(a.err, kErrPosition);
         v0 = v0 && p0;
         v1 = v1 && p1;
