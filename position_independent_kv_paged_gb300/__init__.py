@@ -16,6 +16,7 @@ with their positions; the kernels rotate both with the cos/sin table built by
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -224,12 +225,19 @@ def _stream(stream) -> Optional[int]:
     return s.cuda_stream
 
 
+def _on(stream):
+    """Context of the stream of a call (None: the current one): what the call allocates and clears belongs to it."""
+    torch = _torch()
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def _longest(cu_lens, stream) -> int:
     """The largest count of prefix sums that work on ``stream`` may still be writing."""
-    torch = _torch()
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    with torch.cuda.stream(stream):
+    with _on(stream):
         return int((cu_lens[1:] - cu_lens[:-1]).max().item())
 
 
@@ -381,14 +389,16 @@ def _decode(q, k_pool, v_pool, block_tables, block_starts, seq_lens, q_pos, rope
     _need(seq_lens, "seq_lens", dtype=torch.int32, ndim=1)
     _need(q_pos, "q_pos", dtype=torch.int32, ndim=1)
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     _need(out, "out", dtype=q.dtype)
     if lse is not None:
         _need(lse, "lse", dtype=torch.float32)
     mb = block_tables.shape[1]
     if workspace is None:
         n = decode_workspace_size(B, Hq, kv.num_kv_heads, d, mb, kv.block_size)
-        workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
     db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
                  q_pos.data_ptr(), B, mb, out.data_ptr(), _ptr(lse))
     ws_ptr, ws_n = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -439,7 +449,8 @@ def _prefill(q, cu_q_lens, q_pos, k_pool, v_pool, block_tables, block_starts, kv
     for name, t in (("cu_q_lens", cu_q_lens), ("q_pos", q_pos), ("kv_lens", kv_lens)):
         _need(t, name, dtype=torch.int32, ndim=1)
     if out is None:
-        out = torch.empty_like(q)
+        with _on(stream):
+            out = torch.empty_like(q)
     if lse is not None:
         _need(lse, "lse", dtype=torch.float32)
     B = kv_lens.shape[0]
@@ -455,7 +466,8 @@ def _prefill(q, cu_q_lens, q_pos, k_pool, v_pool, block_tables, block_starts, kv
     rp = _rope_struct(rope, True)
     if workspace is None:
         n = prefill_workspace_size(B, Hq, kv.num_kv_heads, d, max_q_len, mb, kv.block_size)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
     st = L.minipic_attn_prefill(_dtype_code(q), Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(pb),
                                 float(scale), workspace.data_ptr(),
                                 workspace.numel() * workspace.element_size(), _stream(stream))
@@ -499,8 +511,9 @@ def attn_mixed(prefill: dict, decode: dict, k_pool, v_pool, rope, scale: float =
         _need(decode[nm], "decode " + nm, dtype=torch.int32, ndim=2)
     for nm in ("seq_lens", "q_pos"):
         _need(decode[nm], "decode " + nm, dtype=torch.int32, ndim=1)
-    pout = prefill.get("out") if prefill.get("out") is not None else torch.empty_like(pq)
-    dout = decode.get("out") if decode.get("out") is not None else torch.empty_like(dq)
+    with _on(stream):
+        pout = prefill.get("out") if prefill.get("out") is not None else torch.empty_like(pq)
+        dout = decode.get("out") if decode.get("out") is not None else torch.empty_like(dq)
     plse, dlse = prefill.get("lse"), decode.get("lse")
     Hq = pq.shape[1]
     pb = _Prefill(pq.data_ptr(), prefill["cu_q_lens"].data_ptr(), prefill["q_pos"].data_ptr(),
@@ -513,7 +526,8 @@ def attn_mixed(prefill: dict, decode: dict, k_pool, v_pool, rope, scale: float =
     if workspace is None:
         n = decode_workspace_size(dq.shape[0], Hq, kv.num_kv_heads, kv.head_dim, decode["block_tables"].shape[1],
                                   kv.block_size)
-        workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=dq.device)
+        with _on(stream):
+            workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=dq.device)
     st = L.minipic_attn_mixed(_dtype_code(pq), Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(pb),
                               ctypes.byref(db), float(scale), workspace.data_ptr(),
                               workspace.numel() * workspace.element_size(), _stream(stream))
