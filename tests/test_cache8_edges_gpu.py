@@ -1,5 +1,6 @@
 """The 8-bit cache's calls and the block-weight decode at the ends of their ranges."""
 
+import numpy as np
 import pytest
 
 from cache8_util import Case, check_attention, check_weights
@@ -153,3 +154,53 @@ def test_tables_of_few_positions(env, f32, max_pos):
         dtype = "f32" if f32 else "bf16"
         check_attention(f64(out), ref, dtype, 64, 33, p_half=None if f32 or kv == "e4m3" else 2.0 ** -8)
         check_weights(f64(bw), ref, dtype, 64, [33, 3], 7.0)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "bf16"])
+@pytest.mark.parametrize("f32", [False, True])
+def test_many_short_requests(env, kv, f32):
+    """More pairs than the device holds CTAs: none is split."""
+    torch, mp, dev = env
+    lens = [(37 * i) % 100 for i in range(400)]
+    t = make_batch(torch, dev, lens, 8, 2, 64, kv, 11)
+    out, lse, bw = decode(env, as_f32(torch, t) if f32 else t)
+    ref = reference(torch, t)
+    dtype = "f32" if f32 else "bf16"
+    check_attention(f64(out), ref, dtype, 64, 100, p_half=None if f32 or kv == "e4m3" else 2.0 ** -8)
+    check_weights(f64(bw), ref, dtype, 64, lens, 7.0)
+    assert mp.device_error() == 0
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_evict_tables_too_wide_for_shared_memory(env, inplace):
+    """Above 49152 blocks the selection reads the scores back from memory."""
+    torch, mp, dev = env
+    rng = np.random.default_rng(12)
+    B, mb = 3, 60_000
+    lens = np.array([mb * 16 - 5, 50_001 * 16, 49_000 * 16])
+    tables, starts = rng.integers(0, 1 << 20, (B, mb)), rng.integers(0, 1 << 20, (B, mb))
+    scores = rng.choice(np.float32([0.5, 1.0, 2.0, np.nan]), (B, mb)) * rng.choice(np.float32([1.0, 3.0]), (B, mb))
+    # weights from few values, so that many scores are equal
+    w = torch.from_numpy(rng.choice(np.float32([0.0, 0.25, 1.5]), (B, 2, mb))).to(dev).bfloat16()
+    for budget, first, last in ((30_000, 1, 1), (59_999, 4, 7), (11, 4, 7)):
+        a = [torch.from_numpy(np.ascontiguousarray(x)).to(dev) for x in
+             (scores, tables.astype(np.int32), starts.astype(np.int32), lens.astype(np.int32))]
+        got = mp.kv_evict(*a, budget, keep_first=first, keep_last=last, block_weights=w, decay=0.75, inplace=inplace)
+        torch.cuda.synchronize()
+        got = {k: v.cpu().numpy() for k, v in got._asdict().items()}
+        for r in range(B):
+            n = -(-int(lens[r]) // 16)
+            s = (scores[r, :n].astype(np.float64) * 0.75 + f64(w)[r, :, :n].sum(0)).astype(np.float32)
+            keep = np.ones(n, bool)
+            if n > budget:
+                cand = np.arange(first, n - last)
+                rank = np.where(np.isnan(s[cand]), -np.inf, s[cand])
+                order = cand[np.lexsort((cand, -rank))]          # best first, of equal ones the lower index
+                keep[order[budget - first - last:]] = False
+            m = int(keep.sum())
+            for name, x, fill in (("scores", s, 0), ("block_tables", tables[r, :n], -1), ("block_starts", starts[r, :n], 0)):
+                assert np.array_equal(got[name][r, :m], x[keep], equal_nan=name == "scores"), (name, r, budget)
+                assert (got[name][r, m:] == fill).all()
+            assert np.array_equal(got["evicted"][r, :n - m], tables[r, :n][~keep]) and (got["evicted"][r, n - m:] == -1).all()
+            assert got["n_evicted"][r] == n - m and got["seq_lens"][r] == lens[r] - 16 * (n - m)
+    assert mp.device_error() == 0
