@@ -25,21 +25,23 @@
 // Per block, with t the query's position, b the block's start, s the slot:
 //   score = (R_{t-b} q) . (R_s k) * (k scale) * softmax scale
 // e4m3 widens to fp16 exactly, bf16 within fp16's range, with rows outside it scaled
-// by a power of two where that matters (kFactor below; the test of that costs 2.7 %.
-// bf16 operands would show: three roundings of 2^-8 each,
-// an output error of 5.4e-3 of its norm at d 64 where this has 2.2e-3).  R_s is constant per lane, R_{t-b} q is formed once
-// per block, both in packed fp16, and S^T = K' Q'^T, O^T += V^T P^T run as
+// by a power of two where that matters (kFactor below; the test costs 2.7 %).  bf16
+// operands would show: three roundings of 2^-8 each, an output error of 5.4e-3 of its
+// norm at d 64 where this has 2.2e-3.  R_s is constant per lane, R_{t-b} q is formed
+// once per block, both in packed fp16, and S^T = K' Q'^T, O^T += V^T P^T run as
 // mma.sync m16n8k16 with fp32 accumulation (keys, then head dims, as M; up to 8
 // query heads as N, so a group of 8 wastes nothing and the operands come from
-// registers: the tcgen05 form needs M >= 64 and would take the widened, rotated
-// keys through shared memory again).
+// registers).  For one request at a time: the tcgen05 form needs M >= 64 and would
+// take the widened, rotated keys through shared memory again.  Several requests that
+// read one block could share both, in a list ordered by physical block; not built.
 //  - The query is scaled by a power of two per head to a largest element in
 //    [1, 2) first, so that fp16 holds it whatever its size.
 //  - bf16: P is 2^(s - ms) in bf16 and V enters as it is.
 //  - e4m3: V bytes stay unscaled in the product; the block's scale rides on P.  P is
 //    2^(s + log2 vscale - mt + 7) in fp16 with a running reference mt of its own
 //    (so blocks whose scales differ by any factor keep fp16's full precision
-//    where they matter, and a weight 2^-31 of the largest is still above zero),
+//    where they matter, and a weight 2^-31 of the largest is still above zero; a
+//    block whose scale is zero does not count in mt),
 //    the denominator 2^(s - ms) in fp32.  Both references move only when a value
 //    exceeds them by more than 2^8 (P then is below 2^15).
 //  - V fragments come from transposing byte reads: a register holds a head dim of
@@ -51,14 +53,16 @@
 //
 // What bounds it and what it measured (GB300; 3 CTAs of 4 warps per SM, held there
 // by registers: 168 a thread):
-//  - 64 requests x 8192 keys, 32 / 8 heads, spans shared: 120 us, 1.07 GB read of
+//  - 64 requests x 8192 keys, 32 / 8 heads, spans shared: 119 us, 1.07 GB read of
 //    which 0.30 GB from HBM.  Issue: 282 instructions a block and warp (81 of
 //    them fp16 rotation, 66 conversions, 16 matrix products), 53 % of the issue slots used.
 //  - 8 x 131072 keys, 64 / 8 heads, with block weights: 330 us, the same bound.
 //  - the first batch over the bf16 cache, with block weights: 190 us, 2.15 GB read
-//    (a grid of splits with tensor copies took 257 us and 669 instructions a block).
+//    (a grid of splits with tensor copies took 257 us and 669 instructions a block);
+//    317 us with queries so large that every row is looked at, 604 us with keys
+//    beyond fp16, whose pairs are gone through twice.
 //  - 128 ragged contexts to 32768 keys, 28 / 4 heads, nothing shared: HBM, 2.29 GB at
-//    6.45 TB/s (0.95 of the measured copy bandwidth).
+//    6.40 TB/s (0.94 of the measured copy bandwidth).
 #pragma once
 
 #include <cuda_fp16.h>
