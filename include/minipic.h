@@ -515,6 +515,128 @@ typedef struct {
  * (minipic_prefix_cache_release).  Asynchronous on `stream`. */
 minipic_status minipic_kv_evict(minipic_dtype dtype, const minipic_kv_evict_batch* batch, minipic_stream_t stream);
 
+/* ------------------------------------------------------------------ attention over selected blocks
+ * Long contexts read in part: every block of the cache has a summary, a cheap
+ * score ranks the blocks for each decode token, and attention reads the best
+ * ones only.  Nothing leaves the tables (minipic_kv_evict is the call for that):
+ * the next token may select other blocks.
+ *
+ * The summary of a block with n keys, per kv head, is m = (1/n) sum_s R_s k~_s over
+ * its slots s.  (R_{t-b} q)^T m is then the mean of the block's scores for the
+ * query at t when the block starts at b: like the keys it holds no position, and
+ * one summary serves every request that shares the block. */
+
+/* Write the summaries of the blocks that an append wrote into: the call's
+ * arguments are the append's (k_new and v_new are not read and may be NULL), the
+ * keys those that the pool holds now, up to key kv_start + count of each request.
+ * means: [num_blocks][num_kv_heads][head_dim] of dtype, 16-byte aligned; sums are
+ * fp32, rounded once; blocks that the append did not touch keep theirs.  kv->v_pool is
+ * not read.  rope: rows 0 to 15 of cos_sin are read (UNSUPPORTED for a table of
+ * fewer).  Entries that the append skips are skipped, with its error bits.  Every
+ * block must be the target of at most one table entry of a call.  The q8 form reads the
+ * 8-bit cache (dtype is that of the means).  Asynchronous on `stream`. */
+minipic_status minipic_kv_block_means(minipic_dtype dtype, const minipic_kv_pool* kv, const minipic_rope* rope,
+                                      const minipic_kv_append_batch* batch, void* means, minipic_stream_t stream);
+minipic_status minipic_kv_block_means_q8(minipic_dtype dtype, const minipic_kv_pool_q8* kv, const minipic_rope* rope,
+                                         const minipic_kv_append_batch* batch, void* means, minipic_stream_t stream);
+
+typedef struct {
+  const void* q;                /* [batch][num_q_heads][head_dim], unrotated */
+  const void* means;            /* [num_blocks][num_kv_heads][head_dim] of q's type */
+  const int32_t* block_tables;  /* [batch][max_blocks_per_seq] */
+  const int32_t* block_starts;  /* [batch][max_blocks_per_seq] */
+  const int32_t* seq_lens;      /* [batch] */
+  const int32_t* q_pos;         /* [batch] */
+  int32_t batch;
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+  int32_t head_dim;             /* 64 or 128 */
+  float* scores;                /* [batch][num_kv_heads][max_blocks_per_seq] */
+} minipic_block_scores_batch;
+
+/* scores[r][g][b] = the largest over the query heads of kv head g of scale *
+ * (R_{q_pos} q)^T (R_{block_starts} m), the mean score of block b's keys: fp32
+ * arithmetic with rope->cos_sin, NaN if a product is.  -infinity past the request's
+ * length, for a block id outside the pool and for a start outside [0, max_pos) (with
+ * the error bits; a negative start is outside whatever its slots).  dtype is that of
+ * q and means.  UNSUPPORTED above 65535 requests or kv heads, or for
+ * max_blocks_per_seq of 2^27 or more.  Asynchronous on `stream`. */
+minipic_status minipic_block_scores(minipic_dtype dtype, int32_t num_q_heads, const minipic_block_scores_batch* batch,
+                                    const minipic_rope* rope, float scale, minipic_stream_t stream);
+
+typedef struct {
+  const float* scores;          /* [batch][num_kv_heads][max_blocks_per_seq] */
+  const int32_t* seq_lens;      /* [batch] */
+  int32_t* selected;            /* [batch][num_kv_heads][budget] */
+  int32_t batch;
+  int32_t num_kv_heads;
+  int32_t max_blocks_per_seq;
+  int32_t budget;               /* blocks of a (request, kv head), >= 1 and >= keep_first + keep_last */
+  int32_t keep_first;           /* >= 0: these first blocks are always selected */
+  int32_t keep_last;            /* >= 0: so are these last ones (1 keeps the block being written) */
+} minipic_block_select_batch;
+
+/* The blocks that each (request, kv head) attends to: all of them when the request
+ * has at most `budget`, else its first keep_first, its last keep_last and the best
+ * of the others by score (NaN is the worst; of equal scores the lower index), up to
+ * `budget`.  selected receives their numbers in the request's table, ascending, then
+ * -1.  Scores past the request's length are not read.  A length that is negative or
+ * above max_blocks_per_seq * 16 sets MINIPIC_DEVERR_SEQ_LEN and is clamped.
+ * UNSUPPORTED for max_blocks_per_seq of 2^27 or more.  Asynchronous on `stream`. */
+minipic_status minipic_block_select(const minipic_block_select_batch* batch, minipic_stream_t stream);
+
+/* Workspace bytes of minipic_attn_decode_selected and its q8 form. */
+size_t minipic_attn_decode_selected_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim, int32_t max_selected, int32_t block_size);
+
+/* minipic_attn_decode over the selected blocks alone: kv head g of request r attends
+ * to the keys of blocks selected[r][g][i] (numbers in the request's table, in any
+ * order; device int32 [batch][num_kv_heads][max_selected]) that lie below its length.
+ * Of a request with n blocks the first min(n, max_selected) entries are read; -1 is an
+ * unused entry, another number outside [0, n) sets MINIPIC_DEVERR_BLOCK_ID and is
+ * masked, and a block that is listed twice counts twice.  A (request, kv head) with no
+ * key gets out = 0, lse = -inf.  Arithmetic, ranges, what masked slots and NaN do,
+ * workspace rules and errors are those of minipic_attn_decode_weights (q8 form: of
+ * minipic_attn_decode_q8). */
+minipic_status minipic_attn_decode_selected(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                                            const minipic_rope* rope, const minipic_decode_batch* batch, float scale,
+                                            const int32_t* selected, int32_t max_selected, void* workspace,
+                                            size_t workspace_bytes, minipic_stream_t stream);
+minipic_status minipic_attn_decode_selected_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
+                                               const minipic_rope* rope, const minipic_decode_batch* batch,
+                                               float scale, const int32_t* selected, int32_t max_selected,
+                                               void* workspace, size_t workspace_bytes, minipic_stream_t stream);
+
+/* ------------------------------------------------------------------ shared prefixes
+ * Batches whose requests begin with the same blocks at the same positions (a system
+ * prompt, a document that many questions are about): their keys are read and rotated
+ * once for the whole group. */
+typedef struct {
+  const int32_t* cu_requests;    /* [num_prefixes + 1], ascending from >= 0 to <= batch: requests cu[p] .. cu[p+1]-1
+                                    share prefix p; requests outside every group share nothing */
+  const int32_t* prefix_blocks;  /* [num_prefixes] full blocks of the prefix: the first entries of the group's rows
+                                    of block_tables and block_starts, the same in each row of a request that long */
+  int32_t num_prefixes;
+  int32_t max_requests;          /* an upper bound of every group's requests (grid planning) */
+  int32_t max_prefix_blocks;     /* an upper bound of every prefix (grid planning) */
+} minipic_prefix_groups;
+
+/* Workspace bytes of minipic_attn_decode_prefix for this shape. */
+size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                 int32_t head_dim, int32_t max_blocks_per_seq, int32_t num_prefixes,
+                                                 int32_t max_requests, int32_t max_prefix_blocks, int32_t block_size);
+
+/* minipic_attn_decode for such a batch: the same arguments, tables and result (each
+ * request attends to all its seq_lens keys), with the groups.  Only full blocks are
+ * shared, as in the prefix cache.  A request of a group that is shorter than the
+ * prefix (an empty row of a padded batch) reads its own keys and shares nothing.
+ * bf16 only (f32 returns UNSUPPORTED; head dim 64 or 128). */
+minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                                          const minipic_rope* rope, const minipic_decode_batch* batch,
+                                          const minipic_prefix_groups* groups, float scale, void* workspace,
+                                          size_t workspace_bytes, minipic_stream_t stream);
+
 /* ------------------------------------------------------------------ host offload
  * Moving whole blocks between the pools and host memory (MiniPIC summary,
  * section 3, item 5: unrotated blocks move between GPU and host with no

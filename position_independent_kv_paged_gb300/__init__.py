@@ -49,6 +49,15 @@ __all__ = [
     "attn_decode_weights",
     "KVEvicted",
     "kv_evict",
+    "kv_block_means",
+    "kv_block_means_q8",
+    "block_scores",
+    "block_select",
+    "attn_decode_selected_workspace_size",
+    "attn_decode_selected",
+    "attn_decode_selected_q8",
+    "attn_decode_prefix_workspace_size",
+    "attn_decode_prefix",
     "device_error",
     "block_hashes",
     "PrefixCache",
@@ -95,6 +104,23 @@ class _Evict(ctypes.Structure):
                                                "evicted", "n_evicted")] + \
                [(n, ctypes.c_int32) for n in ("batch", "max_blocks_per_seq", "num_kv_heads", "budget", "keep_first",
                                               "keep_last")] + [("decay", ctypes.c_float)]
+
+
+class _Scores(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "means", "block_tables", "block_starts", "seq_lens", "q_pos")] + \
+               [(n, ctypes.c_int32) for n in ("batch", "max_blocks_per_seq", "num_blocks", "num_kv_heads",
+                                              "head_dim")] + [("scores", ctypes.c_void_p)]
+
+
+class _Select(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("scores", "seq_lens", "selected")] + \
+               [(n, ctypes.c_int32) for n in ("batch", "num_kv_heads", "max_blocks_per_seq", "budget", "keep_first",
+                                              "keep_last")]
+
+
+class _Prefixes(ctypes.Structure):
+    _fields_ = [("cu_requests", ctypes.c_void_p), ("prefix_blocks", ctypes.c_void_p), ("num_prefixes", ctypes.c_int32),
+                ("max_requests", ctypes.c_int32), ("max_prefix_blocks", ctypes.c_int32)]
 
 
 class _Rope(ctypes.Structure):
@@ -191,6 +217,29 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
                                                   ctypes.POINTER(_Decode), c_f, c_vp, c_vp, c_sz, c_vp]
         L.minipic_kv_evict.restype = ctypes.c_int
         L.minipic_kv_evict.argtypes = [ctypes.c_int, ctypes.POINTER(_Evict), c_vp]
+        L.minipic_kv_block_means.restype = ctypes.c_int
+        L.minipic_kv_block_means.argtypes = [ctypes.c_int, ctypes.POINTER(_KV), ctypes.POINTER(_Rope),
+                                             ctypes.POINTER(_Append), c_vp, c_vp]
+        L.minipic_kv_block_means_q8.restype = ctypes.c_int
+        L.minipic_kv_block_means_q8.argtypes = [ctypes.c_int, ctypes.POINTER(_KVQ8), ctypes.POINTER(_Rope),
+                                                ctypes.POINTER(_Append), c_vp, c_vp]
+        L.minipic_block_scores.restype = ctypes.c_int
+        L.minipic_block_scores.argtypes = [ctypes.c_int, c_i32, ctypes.POINTER(_Scores), ctypes.POINTER(_Rope), c_f,
+                                           c_vp]
+        L.minipic_block_select.restype = ctypes.c_int
+        L.minipic_block_select.argtypes = [ctypes.POINTER(_Select), c_vp]
+        L.minipic_attn_decode_selected_workspace_size.restype = c_sz
+        L.minipic_attn_decode_selected_workspace_size.argtypes = [c_i32] * 6
+        for fn, pool in ((L.minipic_attn_decode_selected, _KV), (L.minipic_attn_decode_selected_q8, _KVQ8)):
+            fn.restype = ctypes.c_int
+            fn.argtypes = [ctypes.c_int, c_i32, ctypes.POINTER(pool), ctypes.POINTER(_Rope), ctypes.POINTER(_Decode),
+                           c_f, c_vp, c_i32, c_vp, c_sz, c_vp]
+        L.minipic_attn_decode_prefix_workspace_size.restype = c_sz
+        L.minipic_attn_decode_prefix_workspace_size.argtypes = [c_i32] * 9
+        L.minipic_attn_decode_prefix.restype = ctypes.c_int
+        L.minipic_attn_decode_prefix.argtypes = [ctypes.c_int, c_i32, ctypes.POINTER(_KV), ctypes.POINTER(_Rope),
+                                                 ctypes.POINTER(_Decode), ctypes.POINTER(_Prefixes), c_f, c_vp, c_sz,
+                                                 c_vp]
         L.minipic_device_error.restype = ctypes.c_int
         L.minipic_device_error.argtypes = [ctypes.POINTER(c_i32), c_i32, c_vp]
         L.minipic_block_hashes.restype = ctypes.c_int
@@ -872,6 +921,224 @@ def kv_evict(scores, block_tables, block_starts, seq_lens, budget: int, keep_fir
                     int(budget), int(keep_first), int(keep_last), float(decay))
         _check(L.minipic_kv_evict(code, ctypes.byref(eb), s), "minipic_kv_evict")
         return r
+    return _run(stream, call)
+
+
+# ---------------------------------------------------------------- selected blocks, shared prefixes
+
+def _table32(rope, d):
+    """Specs of a table for the calls that read its float32 form alone."""
+    f32 = rope.cos_sin if isinstance(rope, RopeTable) else rope
+    return "rope", f32, _torch().float32, (_sizes(f32, "rope", 2)[0], d)
+
+
+def _means(fn, where, kv, specs, shape, cu_new_lens, kv_start, block_tables, rope, means, max_new_len, stream):
+    torch = _torch()
+    nb, hkv, _, d = shape
+    i32 = torch.int32
+    B, mb = _sizes(block_tables, "block_tables", 2)
+    _sizes(means, "means", 3)
+    code, table = _dtype_code(means), _table32(rope, d)
+    _args(("cu_new_lens", cu_new_lens, i32, (B + 1,)), ("kv_start", kv_start, i32, (B,)),
+          ("block_tables", block_tables, i32, (B, mb)), *specs, table, ("means", means, means.dtype, (nb, hkv, d)))
+    if max_new_len is None:
+        max_new_len = _longest(cu_new_lens, stream) if B else 0
+    ab = _Append(None, None, cu_new_lens.data_ptr(), kv_start.data_ptr(), block_tables.data_ptr(), B, int(max_new_len),
+                 int(max_new_len), mb)   # of the counts the call only asks whether there are any
+    rp = _Rope(table[1].data_ptr(), table[3][0], d, None, None)
+    _check(_run(stream, lambda s: fn(code, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(ab), means.data_ptr(), s)),
+           where)
+
+
+def kv_block_means(cu_new_lens, kv_start, block_tables, k_pool, rope, means, max_new_len=None, stream=None):
+    """Write the summaries of the blocks that ``kv_append`` wrote into (call it
+    after, with the append's arguments): ``means`` [num_blocks, num_kv_heads,
+    head_dim] of the pool's dtype receives the mean of each block's keys, each
+    rotated by its slot.  Blocks that the append did not touch keep theirs.
+    ``max_new_len`` as in ``kv_append``."""
+    L = load()
+    shape = nb, hkv, bs, d = _sizes(k_pool, "k_pool", 4)
+    _sizes(means, "means", 3)
+    _means(L.minipic_kv_block_means, "minipic_kv_block_means", _KV(k_pool.data_ptr(), None, nb, hkv, bs, d),
+           (("k_pool", k_pool, means.dtype, shape),), shape, cu_new_lens, kv_start, block_tables, rope, means,
+           max_new_len, stream)
+
+
+def kv_block_means_q8(cu_new_lens, kv_start, block_tables, k_pool, k_scale, rope, means, max_new_len=None, stream=None):
+    """``kv_block_means`` over the e4m3 cache, after ``kv_append_q8``; ``means``
+    float32 or bfloat16 (the dtype of the queries)."""
+    torch = _torch()
+    L = load()
+    shape = nb, hkv, bs, d = _sizes(k_pool, "k_pool", 4)
+    _sizes(k_scale, "k_scale", 2)
+    _means(L.minipic_kv_block_means_q8, "minipic_kv_block_means_q8",
+           _KVQ8(k_pool.data_ptr(), None, k_scale.data_ptr(), None, nb, hkv, bs, d),
+           (("k_pool", k_pool, torch.float8_e4m3fn, shape), ("k_scale", k_scale, torch.float32, (nb, hkv))), shape,
+           cu_new_lens, kv_start, block_tables, rope, means, max_new_len, stream)
+
+
+def block_scores(q, means, block_tables, block_starts, seq_lens, q_pos, rope, scale: float = 0.0, out=None,
+                 stream=None):
+    """Score every block of the tables for one query token per request: float32
+    [B, num_kv_heads, max_blocks], the largest over the kv head's query heads of
+    the mean score of the block's keys (q and ``means`` float32 or bfloat16);
+    -inf past a request's length."""
+    torch = _torch()
+    L = load()
+    B, Hq, d = _sizes(q, "q", 3)
+    nb, hkv, _ = _sizes(means, "means", 3)
+    mb = _sizes(block_tables, "block_tables", 2)[1]
+    code, i32, table = _dtype_code(q), torch.int32, _table32(rope, d)
+    _args(("q", q, q.dtype, (B, Hq, d)), ("means", means, q.dtype, (nb, hkv, d)),
+          ("block_tables", block_tables, i32, (B, mb)), ("block_starts", block_starts, i32, (B, mb)),
+          ("seq_lens", seq_lens, i32, (B,)), ("q_pos", q_pos, i32, (B,)), table,
+          ("out", out, torch.float32, (B, hkv, mb)))
+    rp = _Rope(table[1].data_ptr(), table[3][0], d, None, None)
+
+    def call(s):
+        o = torch.empty((B, hkv, mb), dtype=torch.float32, device=q.device) if out is None else out
+        sb = _Scores(q.data_ptr(), means.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(),
+                     seq_lens.data_ptr(), q_pos.data_ptr(), B, mb, nb, hkv, d, o.data_ptr())
+        _check(L.minipic_block_scores(code, Hq, ctypes.byref(sb), ctypes.byref(rp), float(scale), s),
+               "minipic_block_scores")
+        return o
+    return _run(stream, call)
+
+
+def block_select(scores, seq_lens, budget: int, keep_first: int = 1, keep_last: int = 1, out=None, stream=None):
+    """The blocks that each (request, kv head) attends to: int32 [B,
+    num_kv_heads, budget], ascending numbers in the request's table, then -1.
+    A request with more than ``budget`` blocks takes its first ``keep_first``
+    and last ``keep_last`` and the best others by score (float32 [B,
+    num_kv_heads, max_blocks]; NaN is the worst, of equal ones the lower index)."""
+    torch = _torch()
+    L = load()
+    B, hkv, mb = shape = _sizes(scores, "scores", 3)
+    budget = int(budget)
+    _args(("scores", scores, torch.float32, shape), ("seq_lens", seq_lens, torch.int32, (B,)),
+          ("out", out, torch.int32, (B, hkv, budget)))
+
+    def call(s):
+        o = torch.empty((B, hkv, max(budget, 0)), dtype=torch.int32, device=scores.device) if out is None else out
+        sb = _Select(scores.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), B, hkv, mb, budget, int(keep_first),
+                     int(keep_last))
+        _check(L.minipic_block_select(ctypes.byref(sb), s), "minipic_block_select")
+        return o
+    return _run(stream, call)
+
+
+def attn_decode_selected_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                        max_selected: int, block_size: int = 16) -> int:
+    return int(load().minipic_attn_decode_selected_workspace_size(batch, num_q_heads, num_kv_heads, head_dim,
+                                                                  max_selected, block_size))
+
+
+def _decode_selected(fn, where, struct, q, specs, block_tables, block_starts, seq_lens, q_pos, rope, selected, scale,
+                     out, lse, workspace, stream):
+    torch = _torch()
+    B, Hq, d = shape = _sizes(q, "q", 3)
+    mb = _sizes(block_tables, "block_tables", 2)[1]
+    S = _sizes(selected, "selected", 3)[2]
+    _, hkv, bs, kd = specs[0][3]
+    dt, code, i32 = q.dtype, _dtype_code(q), torch.int32
+    rope_specs = _rope16(rope, kd, code == BF16)
+    _args(("q", q, dt, (B, Hq, kd)), *specs, ("block_tables", block_tables, i32, (B, mb)),
+          ("block_starts", block_starts, i32, (B, mb)), ("seq_lens", seq_lens, i32, (B,)),
+          ("q_pos", q_pos, i32, (B,)), *rope_specs, ("selected", selected, i32, (B, hkv, S)),
+          ("out", out, dt, shape), ("lse", lse, torch.float32, (B, Hq)), *_any("workspace", workspace))
+    kv, rp = struct(specs), _rope16_struct(rope_specs)
+
+    def call(s):
+        o = torch.empty_like(q) if out is None else out
+        ws = workspace
+        if ws is None:
+            n = attn_decode_selected_workspace_size(B, Hq, hkv, d, S, bs)
+            ws = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
+        db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
+                     q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
+        _check(fn(code, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), float(scale), selected.data_ptr(), S,
+                  ws.data_ptr(), ws.nbytes, s), where)
+        return o, lse
+    return _run(stream, call)
+
+
+def attn_decode_selected(q, k_pool, v_pool, block_tables, block_starts, seq_lens, q_pos, rope, selected,
+                         scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
+    """``attn_decode`` over the selected blocks alone: kv head g of request r
+    attends to blocks ``selected[r, g]`` of its table (int32 [B, num_kv_heads,
+    n], as ``block_select`` writes them; -1: unused).  Returns (out, lse).  A
+    workspace passed in must have been zeroed once."""
+    L = load()
+    shape = _sizes(k_pool, "k_pool", 4)
+    _sizes(q, "q", 3)
+    return _decode_selected(L.minipic_attn_decode_selected, "minipic_attn_decode_selected",
+                            lambda sp: _KV(sp[0][1].data_ptr(), sp[1][1].data_ptr(), *sp[0][3]), q,
+                            (("k_pool", k_pool, q.dtype, shape), ("v_pool", v_pool, q.dtype, shape)), block_tables,
+                            block_starts, seq_lens, q_pos, rope, selected, scale, out, lse, workspace, stream)
+
+
+def attn_decode_selected_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, seq_lens, q_pos, rope,
+                            selected, scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
+    """``attn_decode_selected`` over the e4m3 cache (pools and scales as
+    ``kv_append_q8`` writes them)."""
+    L = load()
+    return _decode_selected(L.minipic_attn_decode_selected_q8, "minipic_attn_decode_selected_q8", _kv_q8_struct, q,
+                            _kv_q8(k_pool, v_pool, k_scale, v_scale), block_tables, block_starts, seq_lens, q_pos,
+                            rope, selected, scale, out, lse, workspace, stream)
+
+
+def attn_decode_prefix_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                                      max_blocks_per_seq: int, num_prefixes: int, max_requests: int,
+                                      max_prefix_blocks: int, block_size: int = 16) -> int:
+    return int(load().minipic_attn_decode_prefix_workspace_size(
+        batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_prefixes, max_requests, max_prefix_blocks,
+        block_size))
+
+
+def attn_decode_prefix(q, k_pool, v_pool, block_tables, block_starts, seq_lens, q_pos, rope, cu_requests,
+                       prefix_blocks, max_requests=None, max_prefix_blocks=None, scale: float = 0.0, out=None,
+                       lse=None, workspace=None, stream=None):
+    """``attn_decode`` (bfloat16) for a batch whose requests share prefixes: the
+    tables of requests ``cu_requests[p]`` .. ``cu_requests[p + 1] - 1`` begin
+    with the same ``prefix_blocks[p]`` full blocks at the same starts, whose keys
+    are read once for the group (int32 [P + 1] and [P]).  ``max_requests`` and
+    ``max_prefix_blocks`` bound every group's requests and prefix (read from the
+    device if None, which synchronizes).  Returns (out, lse) like
+    ``attn_decode``.  A workspace passed in must have been zeroed once."""
+    torch = _torch()
+    L = load()
+    kshape = _sizes(k_pool, "k_pool", 4)
+    _, hkv, bs, kd = kshape
+    B, Hq, d = shape = _sizes(q, "q", 3)
+    mb = _sizes(block_tables, "block_tables", 2)[1]
+    P = _sizes(prefix_blocks, "prefix_blocks", 1)[0]
+    bf, i32 = torch.bfloat16, torch.int32
+    rope_specs = _rope16(rope, kd, True)
+    _args(("q", q, bf, (B, Hq, kd)), ("k_pool", k_pool, bf, kshape), ("v_pool", v_pool, bf, kshape),
+          ("block_tables", block_tables, i32, (B, mb)), ("block_starts", block_starts, i32, (B, mb)),
+          ("seq_lens", seq_lens, i32, (B,)), ("q_pos", q_pos, i32, (B,)), *rope_specs,
+          ("cu_requests", cu_requests, i32, (P + 1,)), ("prefix_blocks", prefix_blocks, i32, (P,)),
+          ("out", out, bf, shape), ("lse", lse, torch.float32, (B, Hq)), *_any("workspace", workspace))
+    if max_requests is None:
+        max_requests = _longest(cu_requests, stream) if P else 0
+    if max_prefix_blocks is None:
+        with _on(stream):
+            max_prefix_blocks = int(prefix_blocks.max().item()) if P else 0
+    kv, rp = _KV(k_pool.data_ptr(), v_pool.data_ptr(), *kshape), _rope16_struct(rope_specs)
+    groups = _Prefixes(cu_requests.data_ptr(), prefix_blocks.data_ptr(), P, int(max_requests), int(max_prefix_blocks))
+
+    def call(s):
+        o = torch.empty_like(q) if out is None else out
+        ws = workspace
+        if ws is None:
+            n = attn_decode_prefix_workspace_size(B, Hq, hkv, d, mb, P, max_requests, max_prefix_blocks, bs)
+            ws = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
+        db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
+                     q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
+        _check(L.minipic_attn_decode_prefix(BF16, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db),
+                                            ctypes.byref(groups), float(scale), ws.data_ptr(), ws.nbytes, s),
+               "minipic_attn_decode_prefix")
+        return o, lse
     return _run(stream, call)
 
 

@@ -919,4 +919,239 @@ minipic_status minipic_kv_evict(minipic_dtype dtype, const minipic_kv_evict_batc
   return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }
 
+/* ---------------------------------------------------------------- selected blocks, shared prefixes */
+
+namespace {
+
+// Decode over selected blocks: lists of at most S blocks a pair.
+size_t selected_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t S, int32_t bs) {
+  if (batch <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || S <= 0 || bs <= 0 || Hq % Hkv) return 0;
+  const int sms = current_sms();
+  size_t most = 0;
+  for (int bf16 = 0; bf16 < 2; ++bf16) {
+    const DecodePlan p = plan_decode_list(batch, Hkv, Hq / Hkv, D, S, bf16 != 0, sms);
+    const size_t n = decode_ws_weights(batch, Hq, Hkv, D, count_partials(p, batch, Hq, Hq / Hkv), 0).total;
+    most = n > most ? n : most;
+  }
+  return most;
+}
+
+minipic_status decode_selected(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                               const float* k_scale, const float* v_scale, const minipic_rope* rope,
+                               const minipic_decode_batch* b, float scale, const int32_t* selected,
+                               int32_t max_selected, void* workspace, size_t workspace_bytes, cudaStream_t s) {
+  const bool bf16 = dtype == MINIPIC_BF16;
+  bool empty = false;
+  minipic_status st = check_decode(dtype, num_q_heads, kv, rope, b, scale, true, false, &empty);
+  if (st != MINIPIC_OK) return st;
+  // the tensor-core path rotates the query with the fp16 rows
+  if (bf16 && (!rope->cos_sin_f16 || !aligned16(rope->cos_sin_f16))) return MINIPIC_ERR_INVALID;
+  if (max_selected <= 0) return MINIPIC_ERR_INVALID;
+  if (empty) return MINIPIC_OK;
+  if (!selected || (reinterpret_cast<uintptr_t>(selected) & 3u)) return MINIPIC_ERR_INVALID;
+  if (!list_fits(*kv, *b) || (long long)b->batch * max_selected > 0x7fffffffLL || max_selected >= (1 << 27))
+    return MINIPIC_ERR_UNSUPPORTED;
+  int* err = nullptr;
+  int sms = 0;
+  if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  // the lists are no longer than the tables; the workspace is sized by max_selected alone
+  const DecodePlan plan =
+      plan_decode_list(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim, max_selected, bf16, sms);
+  DecodeArgs a = decode_args(bf16, num_q_heads, kv, rope, b, scale, plan, err);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.selected = selected;
+  a.max_sel = max_selected;
+  st = place_weights_ws(a, plan, nullptr, workspace, workspace_bytes);
+  if (st != MINIPIC_OK) return st;
+  a.cs_f16 = rope->cos_sin_f16;
+  // the tensor-core kernel merges its parts itself; with no pool every key is masked
+  const bool mma = plan.use_mma && kv->num_blocks > 0;
+  cudaError_t e = !mma ? launch_decode_simt_selected(a, bf16, s)
+                       : (k_scale ? launch_decode_selected_q8(a, s) : launch_decode_selected(a, s));
+  if (e == cudaSuccess && !mma) e = launch_decode_merge(a, bf16, s);
+  return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+}
+
+minipic_status block_means(minipic_dtype dtype, const void* k_pool, const float* k_scale, int32_t num_blocks,
+                           int32_t Hkv, int32_t bs, int32_t D, const minipic_rope* rope,
+                           const minipic_kv_append_batch* b, void* means, cudaStream_t s) {
+  if (dtype != MINIPIC_F32 && dtype != MINIPIC_BF16) return MINIPIC_ERR_INVALID;
+  if (!b || num_blocks < 0 || Hkv <= 0 || bs <= 0 || D <= 0) return MINIPIC_ERR_INVALID;
+  if (b->batch < 0 || b->total_new < 0 || b->max_new_len < 0 || b->max_blocks_per_seq < 0) return MINIPIC_ERR_INVALID;
+  if (D != 64 && D != 128) return MINIPIC_ERR_UNSUPPORTED;
+  if (bs != 16) return MINIPIC_ERR_UNSUPPORTED;
+  const minipic_status st = check_rope(rope, D);
+  if (st != MINIPIC_OK) return st;
+  if (rope->max_pos < bs) return MINIPIC_ERR_UNSUPPORTED;  // a row for each slot
+  if (b->batch == 0 || b->total_new == 0 || b->max_new_len == 0) return MINIPIC_OK;
+  if (b->batch > kMaxGridYZ || b->max_blocks_per_seq == 0 || num_blocks == 0) return MINIPIC_ERR_INVALID;
+  if (!b->cu_new_lens || !b->kv_start || !b->block_tables || !k_pool || !means) return MINIPIC_ERR_INVALID;
+  if (!aligned16(k_pool) || !aligned16(means)) return MINIPIC_ERR_INVALID;
+  MeansArgs a{};
+  if (device_info(&a.err, nullptr) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  a.k_pool = k_pool;
+  a.k_scale = k_scale;
+  a.cu_new = b->cu_new_lens;
+  a.kv_start = b->kv_start;
+  a.block_tables = b->block_tables;
+  a.cos_sin = rope->cos_sin;
+  a.means = means;
+  a.batch = b->batch;
+  a.max_new = b->max_new_len;
+  a.max_blocks = b->max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.Hkv = Hkv;
+  a.D = D;
+  return launch_block_means(a, dtype == MINIPIC_BF16, s) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+}
+
+}  // namespace
+
+minipic_status minipic_kv_block_means(minipic_dtype dtype, const minipic_kv_pool* kv, const minipic_rope* rope,
+                                      const minipic_kv_append_batch* batch, void* means, minipic_stream_t stream) {
+  if (!kv) return MINIPIC_ERR_INVALID;
+  return block_means(dtype, kv->k_pool, nullptr, kv->num_blocks, kv->num_kv_heads, kv->block_size, kv->head_dim, rope,
+                     batch, means, (cudaStream_t)stream);
+}
+
+minipic_status minipic_kv_block_means_q8(minipic_dtype dtype, const minipic_kv_pool_q8* kv, const minipic_rope* rope,
+                                         const minipic_kv_append_batch* batch, void* means, minipic_stream_t stream) {
+  if (!kv) return MINIPIC_ERR_INVALID;
+  if (kv->num_blocks > 0 && (!kv->k_scale || (reinterpret_cast<uintptr_t>(kv->k_scale) & 3u)))
+    return MINIPIC_ERR_INVALID;
+  return block_means(dtype, kv->k_pool, kv->k_scale, kv->num_blocks, kv->num_kv_heads, kv->block_size, kv->head_dim,
+                     rope, batch, means, (cudaStream_t)stream);
+}
+
+minipic_status minipic_block_scores(minipic_dtype dtype, int32_t num_q_heads, const minipic_block_scores_batch* b,
+                                    const minipic_rope* rope, float scale, minipic_stream_t stream) {
+  if (dtype != MINIPIC_F32 && dtype != MINIPIC_BF16) return MINIPIC_ERR_INVALID;
+  if (!b || b->batch < 0 || b->max_blocks_per_seq < 0) return MINIPIC_ERR_INVALID;
+  const minipic_kv_pool shape{nullptr, nullptr, b->num_blocks, b->num_kv_heads, 16, b->head_dim};
+  minipic_status st = check_pool(&shape, num_q_heads, false);
+  if (st != MINIPIC_OK) return st;
+  st = check_rope(rope, b->head_dim);
+  if (st != MINIPIC_OK) return st;
+  if (!isfinite(scale)) return MINIPIC_ERR_INVALID;
+  if (b->batch == 0) return MINIPIC_OK;
+  if (b->max_blocks_per_seq == 0) return MINIPIC_ERR_INVALID;
+  if (!b->q || !b->block_tables || !b->block_starts || !b->seq_lens || !b->q_pos || !b->scores ||
+      (b->num_blocks > 0 && !b->means))
+    return MINIPIC_ERR_INVALID;
+  if (!aligned16(b->q) || !aligned16(b->means) || !aligned16(b->scores)) return MINIPIC_ERR_INVALID;
+  if (b->batch > kMaxGridYZ || b->num_kv_heads > kMaxGridYZ || b->max_blocks_per_seq >= (1 << 27))
+    return MINIPIC_ERR_UNSUPPORTED;
+  ScoresArgs a{};
+  int sms = 0;
+  if (device_info(&a.err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  a.q = b->q;
+  a.means = b->means;
+  a.block_tables = b->block_tables;
+  a.block_starts = b->block_starts;
+  a.seq_lens = b->seq_lens;
+  a.q_pos = b->q_pos;
+  a.cos_sin = rope->cos_sin;
+  a.max_pos = rope->max_pos;
+  a.scores = b->scores;
+  a.batch = b->batch;
+  a.Hq = num_q_heads;
+  a.Hkv = b->num_kv_heads;
+  a.G = num_q_heads / b->num_kv_heads;
+  a.D = b->head_dim;
+  a.num_blocks = b->num_blocks;
+  a.max_blocks = b->max_blocks_per_seq;
+  a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)b->head_dim);
+  return launch_block_scores(a, dtype == MINIPIC_BF16, sms, (cudaStream_t)stream) == cudaSuccess ? MINIPIC_OK
+                                                                                                 : MINIPIC_ERR_CUDA;
+}
+
+minipic_status minipic_block_select(const minipic_block_select_batch* b, minipic_stream_t stream) {
+  if (!b || b->batch < 0 || b->num_kv_heads <= 0 || b->max_blocks_per_seq < 0 || b->budget <= 0 || b->keep_first < 0 ||
+      b->keep_last < 0 || (long long)b->keep_first + b->keep_last > b->budget)
+    return MINIPIC_ERR_INVALID;
+  if (b->batch == 0) return MINIPIC_OK;
+  if (b->max_blocks_per_seq == 0 || !b->scores || !b->seq_lens || !b->selected) return MINIPIC_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(b->scores) | reinterpret_cast<uintptr_t>(b->selected)) & 3u)
+    return MINIPIC_ERR_INVALID;
+  if (b->max_blocks_per_seq >= (1 << 27) || (long long)b->batch * b->num_kv_heads > 0x7fffffffLL)
+    return MINIPIC_ERR_UNSUPPORTED;
+  SelectArgs a{};
+  if (device_info(&a.err, nullptr) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  a.scores = b->scores;
+  a.seq_lens = b->seq_lens;
+  a.selected = b->selected;
+  a.batch = b->batch;
+  a.Hkv = b->num_kv_heads;
+  a.max_blocks = b->max_blocks_per_seq;
+  a.budget = b->budget;
+  a.keep_first = b->keep_first;
+  a.keep_last = b->keep_last;
+  return launch_block_select(a, (cudaStream_t)stream) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+}
+
+size_t minipic_attn_decode_selected_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim, int32_t max_selected, int32_t block_size) {
+  return selected_ws_size(batch, num_q_heads, num_kv_heads, head_dim, max_selected, block_size);
+}
+
+minipic_status minipic_attn_decode_selected(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                                            const minipic_rope* rope, const minipic_decode_batch* batch, float scale,
+                                            const int32_t* selected, int32_t max_selected, void* workspace,
+                                            size_t workspace_bytes, minipic_stream_t stream) {
+  return decode_selected(dtype, num_q_heads, kv, nullptr, nullptr, rope, batch, scale, selected, max_selected,
+                         workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+minipic_status minipic_attn_decode_selected_q8(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool_q8* kv,
+                                               const minipic_rope* rope, const minipic_decode_batch* batch,
+                                               float scale, const int32_t* selected, int32_t max_selected,
+                                               void* workspace, size_t workspace_bytes, minipic_stream_t stream) {
+  if (!batch) return MINIPIC_ERR_INVALID;
+  minipic_kv_pool pool{};
+  const minipic_status st = check_pool_q8(kv, num_q_heads, batch->batch > 0, &pool);
+  if (st != MINIPIC_OK) return st;
+  return decode_selected(dtype, num_q_heads, &pool, kv->k_scale, kv->v_scale, rope, batch, scale, selected,
+                         max_selected, workspace, workspace_bytes, (cudaStream_t)stream);
+}
+
+size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                 int32_t head_dim, int32_t max_blocks_per_seq, int32_t num_prefixes,
+                                                 int32_t max_requests, int32_t max_prefix_blocks, int32_t block_size) {
+  if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_blocks_per_seq <= 0 ||
+      block_size <= 0 || num_prefixes < 0 || max_requests < 0 || max_prefix_blocks < 0 || num_q_heads % num_kv_heads)
+    return 0;
+  const DecodePlan p = plan_decode_list(batch, num_kv_heads, num_q_heads / num_kv_heads, head_dim, max_blocks_per_seq,
+                                        true, current_sms());
+  return decode_ws_weights(batch, num_q_heads, num_kv_heads, head_dim,
+                           count_partials(p, batch, num_q_heads, num_q_heads / num_kv_heads), 0)
+      .total;
+}
+
+minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
+                                          const minipic_rope* rope, const minipic_decode_batch* b,
+                                          const minipic_prefix_groups* groups, float scale, void* workspace,
+                                          size_t workspace_bytes, minipic_stream_t stream) {
+  if (dtype != MINIPIC_BF16) return dtype == MINIPIC_F32 ? MINIPIC_ERR_UNSUPPORTED : MINIPIC_ERR_INVALID;
+  bool empty = false;
+  minipic_status st = check_decode(dtype, num_q_heads, kv, rope, b, scale, true, false, &empty);
+  if (st != MINIPIC_OK) return st;
+  if (!rope->cos_sin_f16 || !aligned16(rope->cos_sin_f16)) return MINIPIC_ERR_INVALID;
+  if (!groups || groups->num_prefixes < 0 || groups->max_requests < 0 || groups->max_prefix_blocks < 0)
+    return MINIPIC_ERR_INVALID;
+  if (groups->num_prefixes > 0 && (!groups->cu_requests || !groups->prefix_blocks)) return MINIPIC_ERR_INVALID;
+  if (empty) return MINIPIC_OK;
+  if (!list_fits(*kv, *b) || kv->num_blocks == 0) return kv->num_blocks == 0 ? MINIPIC_ERR_INVALID : MINIPIC_ERR_UNSUPPORTED;
+  int* err = nullptr;
+  int sms = 0;
+  if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  const DecodePlan plan = plan_decode_list(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
+                                           b->max_blocks_per_seq, true, sms);
+  DecodeArgs a = decode_args(true, num_q_heads, kv, rope, b, scale, plan, err);
+  st = place_weights_ws(a, plan, nullptr, workspace, workspace_bytes);
+  if (st != MINIPIC_OK) return st;
+  a.cs_f16 = rope->cos_sin_f16;
+  return launch_decode_prefix(a, (cudaStream_t)stream) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+}
+
 }  // extern "C"

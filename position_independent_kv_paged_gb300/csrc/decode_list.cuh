@@ -213,7 +213,12 @@ __device__ __forceinline__ uint32_t distance(int t, int b) {
 // query rotated for the first block of a pair and 4-7 for the second, so the query rotation and the softmax run
 // once for two blocks; each block's products use their half of the columns, and the two halves are states of
 // their own until the merge.
-template <bool Q8, int D, int NT, bool DUAL, bool WTS, int NS, int CPS>
+//
+// LIST: which of a request's blocks a pair's list holds.  kAll: all of them.  kSelected: the entries of selected[r][kv
+// head], block numbers of the request's table, the first min(blocks, max_sel) of them.
+enum List { kAll, kSelected };
+
+template <bool Q8, int D, int NT, bool DUAL, bool WTS, int NS, int CPS, List LIST>
 __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(!DUAL || (NT == 1 && Q8), "two half groups fill one column tile");
   using LY = Lay<D, NS, Q8>;
@@ -231,6 +236,12 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, tig = lane & 3;
   const int G = a.G, mb = a.max_blocks;
+
+  // blocks that the list of a request of length Li holds for each of its kv heads
+  auto listed = [&](int Li) {
+    const int n = blocks_of(Li, mb);
+    return LIST == kSelected ? min(n, a.max_sel) : n;
+  };
 
   // this thread's key rows (slots ks0, ks0 + 2) and rotary pairs (f0 .. f0 + 4 NH - 1 with + d/2)
   const int ks0 = frag_slot(g8);
@@ -288,7 +299,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   for (int base = 0; base < a.batch; base += NW * 32) {
     const int i = base + threadIdx.x;
     Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
-    n = blocks_of(Li, mb);
+    n = listed(Li);
     if ((Li < 0 || (long long)Li > 16LL * mb) && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
     total += sum = cta_total(n, before);
     pairs += __syncthreads_count(n > 0);
@@ -296,7 +307,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   }
   if (__syncthreads_or(zero)) {  // requests with no key, shared out over the grid
     for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
-      if (blocks_of(__ldg(a.seq_lens + i), mb)) continue;
+      if (listed(__ldg(a.seq_lens + i))) continue;
       for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32)
         static_cast<__nv_bfloat16*>(a.out)[(size_t)i * a.Hq * D + e] = __float2bfloat16_rn(0.f);
       if (a.lse)
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       const int i = base + threadIdx.x;
       if (a.batch > NW * 32) {  // else the one pass above still holds them
         Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
-        n = blocks_of(Li, mb);
+        n = listed(Li);
       }
       const int units = whole ? (n + part - 1) / part : n;
       if (a.batch > NW * 32 || whole) sum = cta_total(units, before);
@@ -400,20 +411,34 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   auto start_chunk = [&](bool first) {
     const int r = sg.r, hk = sg.hk;
     int tq = __ldg(a.q_pos + r);
-    const int* bt = a.block_tables + (size_t)r * mb + b0;
-    const int* bs = a.block_starts + (size_t)r * mb + b0;
+    const int* bt = a.block_tables + (size_t)r * mb + (LIST == kAll ? b0 : 0);
+    const int* bs = a.block_starts + (size_t)r * mb + (LIST == kAll ? b0 : 0);
+    // selected blocks: the list holds their numbers; one outside the request's blocks has no table entry
+    [[maybe_unused]] const int* sel = LIST == kSelected ? a.selected + ((size_t)r * a.Hkv + hk) * a.max_sel + b0 : nullptr;
+    [[maybe_unused]] const int n_blocks = LIST == kSelected ? blocks_of(sg.L, mb) : 0;
+    auto has_entry = [&](int b) { return LIST == kAll || (b >= 0 && b < n_blocks); };
     int e_phys = -1, e_start = 0;  // lane BPS p + u: block u of this warp's stage p
     if (lane < BPS * NS && warp + NW * lane < span) {
-      e_phys = __ldg(bt + warp + NW * lane);
-      e_start = __ldg(bs + warp + NW * lane);
+      int b = warp + NW * lane;
+      if constexpr (LIST == kSelected) b = __ldg(sel + b);
+      if (has_entry(b)) {
+        e_phys = __ldg(bt + b);
+        e_start = __ldg(bs + b);
+      }
     }
     constexpr int kPer = kChunk / (NW * 32);  // staged entries of a thread
-    int t_phys[kPer], t_start[kPer];
+    int t_blk[kPer], t_phys[kPer], t_start[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int i = threadIdx.x + u * NW * 32;
-      t_phys[u] = i < span ? __ldg(bt + i) : -1;
-      t_start[u] = i < span ? __ldg(bs + i) : 0;
+      t_blk[u] = LIST == kSelected ? (i < span ? __ldg(sel + i) : -1) : i;
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int i = threadIdx.x + u * NW * 32;
+      const bool in = i < span && has_entry(t_blk[u]);
+      t_phys[u] = in ? __ldg(bt + t_blk[u]) : -1;
+      t_start[u] = in ? __ldg(bs + t_blk[u]) : 0;
     }
     if (first) {
 #pragma unroll
@@ -499,9 +524,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       if (i < span) {
         const int phys = t_phys[u], start = t_start[u];
         pl = place(phys, start, tq, hk);
-        const int nk = min(16, sg.L - (b0 + i) * 16);
+        const int nk = min(16, sg.L - (LIST == kAll ? b0 + i : t_blk[u]) * 16);
         if (phys < 0 || phys >= a.num_blocks) {
-          atomicOr(a.err, kErrBlockId);
+          if (LIST != kSelected || t_blk[u] != -1) atomicOr(a.err, kErrBlockId);  // -1: an unused entry
         } else {
           const uint32_t all = (1u << nk) - 1u;
           m = all;
@@ -989,7 +1014,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         int i = r, n = 0, Li = 0;
         while (n == 0 && ++i < a.batch) {  // a later request has blocks, as the range goes on
           Li = a.seq_lens[i];
-          n = blocks_of(Li, mb);
+          n = listed(Li);
         }
         if (n == 0) sg.left = 0;  // not reached
         sg.r = min(i, a.batch - 1);
@@ -1003,9 +1028,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
 }
 
 // kernel<<<...>>> with its shared memory; a.n_split CTAs.
-template <bool Q8, int D, int NT, bool DUAL, bool WTS, int NS, int CPS>
+template <bool Q8, int D, int NT, bool DUAL, bool WTS, int NS, int CPS, List LIST>
 cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
-  const auto kernel = decode_list_kernel<Q8, D, NT, DUAL, WTS, NS, CPS>;
+  const auto kernel = decode_list_kernel<Q8, D, NT, DUAL, WTS, NS, CPS, LIST>;
   const int smem = Lay<D, NS, Q8>::TOTAL;
   static bool done[64] = {false};
   cudaError_t e = set_smem_once(kernel, smem, done);
@@ -1015,13 +1040,13 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
 }
 
 // Groups of up to 4 heads take two e4m3 blocks at once, of more than 8 two column tiles.
-template <bool Q8, int D, bool WTS>
+template <bool Q8, int D, bool WTS, List LIST = kAll>
 cudaError_t launch_d(const DecodeArgs& a, cudaStream_t s) {
-  if (a.G > 8) return launch_t<Q8, D, 2, false, WTS, 2, 2>(a, s);
+  if (a.G > 8) return launch_t<Q8, D, 2, false, WTS, 2, 2, LIST>(a, s);
   constexpr int CPS = D == 64 ? 4 : 3;
   if constexpr (Q8)
-    if (a.G <= 4) return launch_t<Q8, D, 1, true, WTS, 2, CPS>(a, s);
-  return launch_t<Q8, D, 1, false, WTS, 2, CPS>(a, s);
+    if (a.G <= 4) return launch_t<Q8, D, 1, true, WTS, 2, CPS, LIST>(a, s);
+  return launch_t<Q8, D, 1, false, WTS, 2, CPS, LIST>(a, s);
 }
 
 }  // namespace decode_list

@@ -53,7 +53,14 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-template <typename T, typename KV, int D, int MAXG, bool ROPE, bool WTS>
+// Blocks of a request that its lists hold (all of them, or the selected ones).
+__device__ __forceinline__ int listed(const DecodeArgs& a, int L) {
+  const int n = (L + a.BS - 1) / a.BS;
+  return a.selected ? min(n, a.max_sel) : n;
+}
+
+// SEL: only the blocks that selected[r][kv head] names.
+template <typename T, typename KV, int D, int MAXG, bool ROPE, bool WTS, bool SEL>
 __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
   constexpr bool Q8 = sizeof(KV) == 1;
   constexpr int E = D / 32;  // elements per lane
@@ -76,7 +83,7 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
     if (threadIdx.x == 0 && s == 0) atomicOr(a.err, kErrSeqLen);
     L = L < 0 ? 0 : Lmax;
   }
-  const int nblk = (L + a.BS - 1) / a.BS;
+  const int nblk = SEL ? listed(a, L) : (L + a.BS - 1) / a.BS;
   const int n_valid = max(1, (nblk + a.split_blocks - 1) / a.split_blocks);
   if (s >= n_valid) return;
   const int b_begin = s * a.split_blocks;
@@ -125,7 +132,12 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
   }
   const float sl2 = a.scale * kLog2e;
 
-  for (int b = b_begin + warp; b < b_end; b += NW) {
+  for (int i = b_begin + warp; i < b_end; i += NW) {
+    const int b = SEL ? a.selected[((size_t)r * a.Hkv + g) * a.max_sel + i] : i;
+    if (SEL && (b < 0 || b >= (L + a.BS - 1) / a.BS)) {
+      if (b != -1 && lane == 0) atomicOr(a.err, kErrBlockId);  // -1: an unused entry
+      continue;
+    }
     const int phys = a.block_tables[(size_t)r * a.max_blocks + b];
     float* raw = WTS ? a.w_raw + (((size_t)r * a.Hkv + g) * a.max_blocks + b) * G : nullptr;
     if (phys < 0 || phys >= a.num_blocks) {
@@ -143,7 +155,7 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
     const int start = ROPE ? a.block_starts[(size_t)r * a.max_blocks + b] : 0;
     const int nk = min(a.BS, L - b * a.BS);
     const size_t tile = ((size_t)phys * a.Hkv + g) * a.BS;
-    if constexpr (Q8 || WTS) {
+    if constexpr (Q8 || WTS || SEL) {
       // four keys at a time: their loads and their lane sums overlap (two requests of 128 keys, d 64: 21 -> 17 us)
       for (int s0 = 0; s0 < nk; s0 += 4) {
         float k[4][E], v[4][E];
@@ -215,7 +227,7 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
         }
       }
     }
-    for (int slot = 0; slot < (Q8 || WTS ? 0 : nk); ++slot) {
+    for (int slot = 0; slot < (Q8 || WTS || SEL ? 0 : nk); ++slot) {
       const KV* kp = kpool + (tile + slot) * D;
       const KV* vp = vpool + (tile + slot) * D;
       float k[E], v[E];
@@ -291,7 +303,7 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(DecodeArgs a) {
     const int hq = g * G + h;
     if (direct) {
       T* out = static_cast<T*>(a.out) + ((size_t)r * a.Hq + hq) * D + dim;
-      const bool any = Q8 || WTS ? Ls != 0.f : Ls > 0.f;  // over e4m3 or with block weights, a NaN sum stays one
+      const bool any = Q8 || WTS || SEL ? Ls != 0.f : Ls > 0.f;  // in all but the plain call, a NaN sum stays one
       st_f<T>(out, any ? O / Ls : 0.f);
       if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = any ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
       if (WTS && dim == 0) a.w_lse[(size_t)r * a.Hq + hq] = any ? M + log2f(Ls) : -CUDART_INF_F;
@@ -313,8 +325,7 @@ __global__ void decode_merge_kernel(DecodeArgs a) {
   int L = a.seq_lens[r];
   const int Lmax = a.max_blocks * a.BS;
   L = L < 0 ? 0 : (L > Lmax ? Lmax : L);
-  const int nblk = (L + a.BS - 1) / a.BS;
-  const int n_valid = max(1, (nblk + a.split_blocks - 1) / a.split_blocks);
+  const int n_valid = max(1, (listed(a, L) + a.split_blocks - 1) / a.split_blocks);
   if (n_valid <= 1) return;  // written directly by the split kernel
   const size_t base = ((size_t)r * a.Hq + hq) * a.n_split;
   float M = -CUDART_INF_F;
@@ -328,28 +339,28 @@ __global__ void decode_merge_kernel(DecodeArgs a) {
       O = fmaf(a.part_o[(base + s) * a.D + dim], f, O);
     }
     T* out = static_cast<T*>(a.out) + ((size_t)r * a.Hq + hq) * a.D + dim;
-    const bool any = a.k_scale || a.w_lse ? Ls != 0.f : Ls > 0.f;  // as in the split kernel
+    const bool any = a.k_scale || a.w_lse || a.selected ? Ls != 0.f : Ls > 0.f;  // as in the split kernel
     st_f<T>(out, any ? O / Ls : 0.f);
     if (dim == 0 && a.lse) a.lse[(size_t)r * a.Hq + hq] = any ? (M + log2f(Ls)) * kLn2 : -CUDART_INF_F;
     if (dim == 0 && a.w_lse) a.w_lse[(size_t)r * a.Hq + hq] = any ? M + log2f(Ls) : -CUDART_INF_F;
   }
 }
 
-template <typename T, typename KV, int D, bool ROPE, bool WTS>
+template <typename T, typename KV, int D, bool ROPE, bool WTS, bool SEL>
 cudaError_t dispatch_g(const DecodeArgs& a, cudaStream_t s) {
   dim3 grid(a.n_split, a.Hkv, a.batch);
   if (a.G <= 4)
-    decode_simt_kernel<T, KV, D, 4, ROPE, WTS><<<grid, 128, 0, s>>>(a);
+    decode_simt_kernel<T, KV, D, 4, ROPE, WTS, SEL><<<grid, 128, 0, s>>>(a);
   else if (a.G <= 8)
-    decode_simt_kernel<T, KV, D, 8, ROPE, WTS><<<grid, 128, 0, s>>>(a);
+    decode_simt_kernel<T, KV, D, 8, ROPE, WTS, SEL><<<grid, 128, 0, s>>>(a);
   else
-    decode_simt_kernel<T, KV, D, 16, ROPE, WTS><<<grid, 128, 0, s>>>(a);
+    decode_simt_kernel<T, KV, D, 16, ROPE, WTS, SEL><<<grid, 128, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-template <typename T, typename KV, bool ROPE, bool WTS = false>
+template <typename T, typename KV, bool ROPE, bool WTS = false, bool SEL = false>
 cudaError_t dispatch_d(const DecodeArgs& a, cudaStream_t s) {
-  return a.D == 64 ? dispatch_g<T, KV, 64, ROPE, WTS>(a, s) : dispatch_g<T, KV, 128, ROPE, WTS>(a, s);
+  return a.D == 64 ? dispatch_g<T, KV, 64, ROPE, WTS, SEL>(a, s) : dispatch_g<T, KV, 128, ROPE, WTS, SEL>(a, s);
 }
 
 template <typename T>
@@ -371,6 +382,14 @@ cudaError_t launch_decode_simt_q8(const DecodeArgs& a, bool bf16, cudaStream_t s
 
 cudaError_t launch_decode_simt_weights(const DecodeArgs& a, bool bf16, cudaStream_t s) {
   return bf16 ? dispatch_d<__nv_bfloat16, __nv_bfloat16, true, true>(a, s) : dispatch_d<float, float, true, true>(a, s);
+}
+
+cudaError_t launch_decode_simt_selected(const DecodeArgs& a, bool bf16, cudaStream_t s) {
+  using B = __nv_bfloat16;
+  if (a.k_scale)
+    return bf16 ? dispatch_d<B, __nv_fp8_e4m3, true, false, true>(a, s)
+                : dispatch_d<float, __nv_fp8_e4m3, true, false, true>(a, s);
+  return bf16 ? dispatch_d<B, B, true, false, true>(a, s) : dispatch_d<float, float, true, false, true>(a, s);
 }
 
 cudaError_t launch_decode_merge(const DecodeArgs& a, bool bf16, cudaStream_t s) {

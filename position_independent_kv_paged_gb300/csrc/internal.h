@@ -37,6 +37,9 @@ struct DecodeArgs {
   void* weights;             // [B][Hkv][max_blocks] in the dtype of q: sum over the group of each block's softmax weight
   float* w_raw;              // [B][Hkv][max_blocks][G] log2 of a block's unnormalised sum, per query head
   float* w_lse;              // [B][Hq] log2 of the softmax denominator
+  // selected blocks (null: all)
+  const int32_t* selected;   // [B][Hkv][max_sel] numbers of blocks in the request's table, -1: unused
+  int max_sel;
 };
 
 // Arguments of one prefill launch.
@@ -95,6 +98,12 @@ cudaError_t launch_decode_q8(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_simt_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
 // bf16 cache, tensor cores, recording block weights (num_blocks > 0).
 cudaError_t launch_decode_weights(const DecodeArgs& a, cudaStream_t s);
+// Only the selected blocks: exact-precision kernel (any cache), and tensor cores (bf16 q and out, num_blocks > 0).
+cudaError_t launch_decode_simt_selected(const DecodeArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_decode_selected(const DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_decode_selected_q8(const DecodeArgs& a, cudaStream_t s);
+// Shared prefixes, bf16, tensor cores (num_blocks > 0).
+cudaError_t launch_decode_prefix(const DecodeArgs& a, cudaStream_t s);
 // w_raw and w_lse -> weights.
 cudaError_t launch_block_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, bool rotate, cudaStream_t s);
@@ -176,6 +185,47 @@ struct EvictArgs {
   int* err;
 };
 cudaError_t launch_kv_evict(const EvictArgs& a, bool bf16, cudaStream_t s);
+
+// Summaries of the blocks that an append wrote into.
+struct MeansArgs {
+  const void* k_pool;           // [num_blocks][Hkv][16][D] f32 / bf16 like the means, or e4m3
+  const float* k_scale;         // [num_blocks][Hkv] (e4m3), else null
+  const int32_t* cu_new;        // the append's
+  const int32_t* kv_start;
+  const int32_t* block_tables;  // [batch][max_blocks]
+  const float* cos_sin;         // rows 0 .. 15 are read
+  void* means;                  // [num_blocks][Hkv][D]
+  int batch, max_new, max_blocks, num_blocks, Hkv, D;
+  int* err;
+};
+cudaError_t launch_block_means(const MeansArgs& a, bool bf16, cudaStream_t s);
+
+// Mean score of every block of the tables for one query token per request.
+struct ScoresArgs {
+  const void* q;      // [batch][Hq][D] f32 / bf16
+  const void* means;  // [num_blocks][Hkv][D] of q's type
+  const int32_t* block_tables;
+  const int32_t* block_starts;
+  const int32_t* seq_lens;
+  const int32_t* q_pos;
+  const float* cos_sin;
+  int max_pos;
+  float* scores;      // [batch][Hkv][max_blocks]
+  int batch, Hq, Hkv, G, D, num_blocks, max_blocks;
+  float scale;
+  int* err;
+};
+cudaError_t launch_block_scores(const ScoresArgs& a, bool bf16, int num_sms, cudaStream_t s);
+
+// The best blocks of each (request, kv head) by score.
+struct SelectArgs {
+  const float* scores;       // [batch][Hkv][max_blocks]
+  const int32_t* seq_lens;
+  int32_t* selected;         // [batch][Hkv][budget]
+  int batch, Hkv, max_blocks, budget, keep_first, keep_last;
+  int* err;
+};
+cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t s);
 
 // Whole-block copies between the pools and page-locked host memory.
 struct OffloadArgs {
