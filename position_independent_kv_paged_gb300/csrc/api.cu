@@ -6,6 +6,7 @@
 
 #include "../../include/minipic.h"
 #include "internal.h"
+#include "prefix.cuh"
 
 namespace minipic {
 
@@ -1115,16 +1116,57 @@ minipic_status minipic_attn_decode_selected_q8(minipic_dtype dtype, int32_t num_
                          max_selected, workspace, workspace_bytes, (cudaStream_t)stream);
 }
 
+namespace {
+
+// Parts of each prefix.  The kernel of the shared part keeps a cluster of two SMs busy per (pair of query tiles, kv
+// head, part) at head dim 128, one SM at 64, and takes waves * (tiles of a part + its start and end, about three
+// tiles' time): the count of parts that makes this least, from the planning bounds.
+int prefix_split(int num_prefixes, int max_requests, int max_prefix_blocks, int Hkv, int G, int D, int sms) {
+  const int tq = 128 / G, tile = D == 128 ? prefix::kTileBlocks<128> : prefix::kTileBlocks<64>;
+  const long long units = (long long)num_prefixes * Hkv * ((max_requests + 2LL * tq - 1) / (2 * tq));
+  const int slots = D == 128 ? (sms / 2 > 0 ? sms / 2 : 1) : sms, tiles = (int)((max_prefix_blocks + tile - 1LL) / tile);
+  int best = 1;
+  long long least = -1;
+  for (int n = 1; n <= prefix::kMaxSplit && n <= (tiles > 0 ? tiles : 1) && (long long)n * Hkv <= kMaxGridYZ; ++n) {
+    const long long cost = ((units * n + slots - 1) / slots) * ((tiles + n - 1) / n + 3);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+struct PrefixWs {
+  int n_split;  // 0: nothing is shared
+  DecodePlan plan;
+  size_t list_bytes, o_bytes, lse_bytes, total;
+};
+PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, int max_requests, int max_prefix_blocks,
+                   int sms) {
+  PrefixWs w{};
+  const int G = Hq / Hkv;
+  w.plan = plan_decode_list(batch, Hkv, G, D, mb, true, sms);
+  w.list_bytes = decode_ws_weights(batch, Hq, Hkv, D, count_partials(w.plan, batch, Hq, G), 0).total;
+  if (num_prefixes > 0 && max_requests >= prefix::kMinRequests && max_prefix_blocks > 0 && G <= 16) {
+    w.n_split = prefix_split(num_prefixes, max_requests, max_prefix_blocks, Hkv, G, D, sms);
+    w.o_bytes = align_up((size_t)batch * Hq * w.n_split * D * sizeof(float), 256);
+    w.lse_bytes = align_up((size_t)batch * Hq * w.n_split * sizeof(float), 256);
+  }
+  w.total = w.list_bytes + w.o_bytes + w.lse_bytes;
+  return w;
+}
+
+}  // namespace
+
 size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                  int32_t head_dim, int32_t max_blocks_per_seq, int32_t num_prefixes,
                                                  int32_t max_requests, int32_t max_prefix_blocks, int32_t block_size) {
   if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_blocks_per_seq <= 0 ||
       block_size <= 0 || num_prefixes < 0 || max_requests < 0 || max_prefix_blocks < 0 || num_q_heads % num_kv_heads)
     return 0;
-  const DecodePlan p = plan_decode_list(batch, num_kv_heads, num_q_heads / num_kv_heads, head_dim, max_blocks_per_seq,
-                                        true, current_sms());
-  return decode_ws_weights(batch, num_q_heads, num_kv_heads, head_dim,
-                           count_partials(p, batch, num_q_heads, num_q_heads / num_kv_heads), 0)
+  return prefix_ws(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_prefixes, max_requests,
+                   max_prefix_blocks, current_sms())
       .total;
 }
 
@@ -1145,13 +1187,56 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
   int* err = nullptr;
   int sms = 0;
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
-  const DecodePlan plan = plan_decode_list(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
-                                           b->max_blocks_per_seq, true, sms);
-  DecodeArgs a = decode_args(true, num_q_heads, kv, rope, b, scale, plan, err);
-  st = place_weights_ws(a, plan, nullptr, workspace, workspace_bytes);
+  if (groups->num_prefixes > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
+  const PrefixWs w = prefix_ws(b->batch, num_q_heads, kv->num_kv_heads, kv->head_dim, b->max_blocks_per_seq,
+                               groups->num_prefixes, groups->max_requests, groups->max_prefix_blocks, sms);
+  if (!workspace || workspace_bytes < w.total || !aligned16(workspace)) return MINIPIC_ERR_WORKSPACE;
+  DecodeArgs a = decode_args(true, num_q_heads, kv, rope, b, scale, w.plan, err);
+  st = place_weights_ws(a, w.plan, nullptr, workspace, w.list_bytes);
   if (st != MINIPIC_OK) return st;
   a.cs_f16 = rope->cos_sin_f16;
-  return launch_decode_prefix(a, (cudaStream_t)stream) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+  a.cu_requests = groups->cu_requests;
+  a.prefix_blocks = groups->prefix_blocks;
+  // groups that the planning bounds rule out share nothing
+  a.n_prefix = w.n_split > 0 ? groups->num_prefixes : 0;
+  a.max_requests = groups->max_requests;
+  a.prefix_split = w.n_split;
+  char* ws = static_cast<char*>(workspace) + w.list_bytes;
+  a.prefix_o = reinterpret_cast<const float*>(ws);
+  a.prefix_lse = reinterpret_cast<const float*>(ws + w.o_bytes);
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (w.n_split > 0) {
+    PrefillArgs p{};
+    p.q = a.q;
+    p.cu_q_lens = groups->cu_requests;
+    p.q_pos = a.q_pos;
+    p.k_pool = a.k_pool;
+    p.v_pool = a.v_pool;
+    p.block_tables = a.block_tables;
+    p.block_starts = a.block_starts;
+    p.kv_lens = a.seq_lens;
+    p.cos_sin = rope->cos_sin;
+    p.cos_sin16 = rope->cos_sin_f16;
+    p.max_pos = rope->max_pos;
+    p.batch = groups->num_prefixes;
+    p.total_q = b->batch;
+    p.max_q_len = groups->max_requests;
+    p.Hq = a.Hq;
+    p.Hkv = a.Hkv;
+    p.G = a.G;
+    p.D = a.D;
+    p.BS = a.BS;
+    p.num_blocks = a.num_blocks;
+    p.max_blocks = a.max_blocks;
+    p.scale = a.scale;
+    p.err = err;
+    p.prefix_blocks = groups->prefix_blocks;
+    p.n_split = w.n_split;
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_lse = reinterpret_cast<float*>(ws + w.o_bytes);
+    if (launch_prefix(p, s) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  }
+  return launch_decode_prefix(a, s) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -71,6 +71,7 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "prefix.cuh"
 #include "ptx.cuh"
 #include "tmap.cuh"
 
@@ -108,7 +109,7 @@ struct Lay {
   static constexpr int MERGE = kWarps * MERGE_W;                // overlays stages, rows and meta
   static constexpr int TOTAL = MASK + (kChunk + 2 * kWarps) * 4;
   static_assert(MERGE <= TOTAL, "the merge overlays what the loop no longer reads");
-  static_assert(kListMaxCtas * 8 * 4 <= STAGES, "so do the weights of the parts (half the CTAs for groups above 8)");
+  static_assert((kListMaxCtas + prefix::kMaxSplit) * 8 * 4 <= STAGES, "so do the weights of the parts (half the CTAs for groups above 8)");
 };
 
 // Slot held by MMA fragment row g < 8 (row g + 8 holds slot + 2): rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are four
@@ -215,8 +216,24 @@ __device__ __forceinline__ uint32_t distance(int t, int b) {
 // their own until the merge.
 //
 // LIST: which of a request's blocks a pair's list holds.  kAll: all of them.  kSelected: the entries of selected[r][kv
-// head], block numbers of the request's table, the first min(blocks, max_sel) of them.
-enum List { kAll, kSelected };
+// head], block numbers of the request's table, the first min(blocks, max_sel) of them.  kPrefix: the blocks behind
+// the prefix that a request shares with its group; the attention to the prefix is joined with theirs in the merge.
+enum List { kAll, kSelected, kPrefix };
+
+// Blocks that request i of length L shares with its group: the group's, if the request holds them all.
+__device__ __forceinline__ int shared_blocks(const DecodeArgs& a, int i, int L) {
+  int lo = 0, hi = a.n_prefix;  // groups that begin at request i or before it
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(a.cu_requests + mid) <= i) lo = mid + 1;
+    else hi = mid;
+  }
+  if (lo == 0) return 0;
+  bool bad;
+  const prefix::Group g =
+      prefix::group(a.cu_requests, a.prefix_blocks, lo - 1, a.batch, a.max_blocks, a.max_requests, bad);
+  return i >= g.q0 && i < g.q0 + g.n && L >= 16LL * g.blocks ? g.blocks : 0;
+}
 
 template <bool Q8, int D, int NT, bool DUAL, bool WTS, int NS, int CPS, List LIST>
 __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __grid_constant__ DecodeArgs a) {
@@ -237,10 +254,11 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   const int g8 = lane >> 2, tig = lane & 3;
   const int G = a.G, mb = a.max_blocks;
 
-  // blocks that the list of a request of length Li holds for each of its kv heads
-  auto listed = [&](int Li) {
+  // blocks that the list of request i, of length Li, holds for each of its kv heads
+  auto listed = [&]([[maybe_unused]] int i, int Li) {
     const int n = blocks_of(Li, mb);
-    return LIST == kSelected ? min(n, a.max_sel) : n;
+    if constexpr (LIST == kPrefix) return n ? n - shared_blocks(a, i, Li) : 0;
+    else return LIST == kSelected ? min(n, a.max_sel) : n;
   };
 
   // this thread's key rows (slots ks0, ks0 + 2) and rotary pairs (f0 .. f0 + 4 NH - 1 with + d/2)
@@ -268,6 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     int whole, last;      // one part of a pair per CTA; last to finish its pair
     int large, wide;      // the pair's key rows may need scaling: its queries are large; it was seen to need it
     int redo;             // the pair has to be gone through again, wide
+    int first;            // kPrefix: blocks that the pair's request shares, which its list leaves out
   } sg;
   auto cta_total = [&](int v, int& before) {  // sum of v over the CTA, and over the threads before this one
     int pre = v;
@@ -299,15 +318,63 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   for (int base = 0; base < a.batch; base += NW * 32) {
     const int i = base + threadIdx.x;
     Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
-    n = listed(Li);
+    n = i < a.batch ? listed(i, Li) : 0;
     if ((Li < 0 || (long long)Li > 16LL * mb) && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
     total += sum = cta_total(n, before);
     pairs += __syncthreads_count(n > 0);
     zero |= i < a.batch && n == 0 && i % gridDim.x == blockIdx.x;
   }
-  if (__syncthreads_or(zero)) {  // requests with no key, shared out over the grid
+  if constexpr (LIST == kPrefix) {
+    if (blockIdx.x == 0)
+      for (int p = threadIdx.x; p < a.n_prefix; p += NW * 32) {
+        bool bad;
+        prefix::group(a.cu_requests, a.prefix_blocks, p, a.batch, mb, a.max_requests, bad);
+        if (bad) atomicOr(a.err, kErrSeqLen);
+      }
+  }
+  // Parts of the prefix of a request that shares `first` blocks: part s holds a tile, and the attention to it is joined
+  // with what the request has (O over its denominator, and log2 of that).
+  [[maybe_unused]] auto prefix_part = [&](int first, int s) {
+    constexpr int TB = prefix::kTileBlocks<D>;
+    int t0, t1;
+    prefix::part((first + TB - 1) / TB, s, a.prefix_split, t0, t1);
+    return first > 0 && t0 < t1;
+  };
+  [[maybe_unused]] auto join_prefix = [&](int first, size_t hq, int dim, float& O, float& lse2) {
+    const float* pl = a.prefix_lse + hq * a.prefix_split;
+    const float* po = a.prefix_o + hq * a.prefix_split * D + dim;
+    float M = lse2;
+    for (int s = 0; s < a.prefix_split; ++s)
+      if (prefix_part(first, s)) M = fmaxf(M, __ldcg(pl + s));
+    if (M == -CUDART_INF_F) return;
+    const float w0 = exp2f(lse2 - M);
+    float sum = w0, acc = O * w0;
+    for (int s = 0; s < a.prefix_split; ++s)
+      if (prefix_part(first, s)) {
+        const float w = exp2f(__ldcg(pl + s) - M);
+        sum += w;
+        acc = fmaf(__ldcg(po + (size_t)s * D), w, acc);
+      }
+    O = acc / sum;
+    lse2 = M + log2f(sum);
+  };
+  if (__syncthreads_or(zero)) {  // requests whose list is empty, shared out over the grid
     for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
-      if (listed(__ldg(a.seq_lens + i))) continue;
+      const int L = __ldg(a.seq_lens + i);
+      if (listed(i, L)) continue;
+      if constexpr (LIST == kPrefix) {
+        const int first = shared_blocks(a, i, L);
+        if (first > 0) {  // the request ends with its prefix
+          for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32) {
+            const size_t hq = (size_t)i * a.Hq + e / D;
+            float O = 0.f, lse2 = -CUDART_INF_F;
+            join_prefix(first, hq, e % D, O, lse2);
+            static_cast<__nv_bfloat16*>(a.out)[hq * D + e % D] = __float2bfloat16_rn(O);
+            if (a.lse && e % D == 0) a.lse[hq] = lse2 * kLn2;
+          }
+          continue;
+        }
+      }
       for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32)
         static_cast<__nv_bfloat16*>(a.out)[(size_t)i * a.Hq * D + e] = __float2bfloat16_rn(0.f);
       if (a.lse)
@@ -336,7 +403,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       const int i = base + threadIdx.x;
       if (a.batch > NW * 32) {  // else the one pass above still holds them
         Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
-        n = listed(Li);
+        n = i < a.batch ? listed(i, Li) : 0;
       }
       const int units = whole ? (n + part - 1) / part : n;
       if (a.batch > NW * 32 || whole) sum = cta_total(units, before);
@@ -347,6 +414,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         sg.hk = (int)((x0 - at) / units);
         sg.nblk = n;
         sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
+        sg.first = LIST == kPrefix ? blocks_of(Li, mb) - n : 0;
         sg.whole = whole;
         if (whole) {
           sg.b_begin = (int)((long long)k * n / units);
@@ -411,12 +479,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   auto start_chunk = [&](bool first) {
     const int r = sg.r, hk = sg.hk;
     int tq = __ldg(a.q_pos + r);
-    const int* bt = a.block_tables + (size_t)r * mb + (LIST == kAll ? b0 : 0);
-    const int* bs = a.block_starts + (size_t)r * mb + (LIST == kAll ? b0 : 0);
+    const int at0 = LIST == kSelected ? 0 : b0 + (LIST == kPrefix ? sg.first : 0);  // the chunk's place in the tables
+    const int* bt = a.block_tables + (size_t)r * mb + at0;
+    const int* bs = a.block_starts + (size_t)r * mb + at0;
     // selected blocks: the list holds their numbers; one outside the request's blocks has no table entry
     [[maybe_unused]] const int* sel = LIST == kSelected ? a.selected + ((size_t)r * a.Hkv + hk) * a.max_sel + b0 : nullptr;
     [[maybe_unused]] const int n_blocks = LIST == kSelected ? blocks_of(sg.L, mb) : 0;
-    auto has_entry = [&](int b) { return LIST == kAll || (b >= 0 && b < n_blocks); };
+    auto has_entry = [&](int b) { return LIST != kSelected || (b >= 0 && b < n_blocks); };
     int e_phys = -1, e_start = 0;  // lane BPS p + u: block u of this warp's stage p
     if (lane < BPS * NS && warp + NW * lane < span) {
       int b = warp + NW * lane;
@@ -524,7 +593,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       if (i < span) {
         const int phys = t_phys[u], start = t_start[u];
         pl = place(phys, start, tq, hk);
-        const int nk = min(16, sg.L - (LIST == kAll ? b0 + i : t_blk[u]) * 16);
+        const int nk = min(16, sg.L - (at0 + t_blk[u]) * 16);
         if (phys < 0 || phys >= a.num_blocks) {
           if (LIST != kSelected || t_blk[u] != -1) atomicOr(a.err, kErrBlockId);  // -1: an unused entry
         } else {
@@ -923,9 +992,11 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       // the power in two factors: value scales down to fp32's least are 2^-149, past one factor's range with kHead
       const float e = T - M - kHead, e1 = fmaxf(e, -80.f);
       O = Ls == 0.f ? 0.f : O / Ls * exp2f(e1) * exp2f(e - e1);
-      const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
+      float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
       const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
       if (direct) {
+        if constexpr (LIST == kPrefix)
+          if (sg.first > 0) join_prefix(sg.first, hq, dim, O, lse2);
         static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(O);
         if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
         if (WTS && dim == 0) a.w_lse[hq] = lse2;
@@ -954,10 +1025,18 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       if (sg.last) {
         __threadfence();
         // weights of the parts first (one read of their log sums), then the weighted sum, four dims a thread
-        const int n_part = c2 - c1 + 1;
+        // (kPrefix: the parts of the prefix follow those of the list)
+        const int n_list = c2 - c1 + 1, n_part = n_list + (LIST == kPrefix && sg.first > 0 ? a.prefix_split : 0);
         float* wt = reinterpret_cast<float*>(sgen);  // [part][G], over what the stages held
         auto slot = [&](int c) { return (size_t)(2 * (c1 + c) + (c == 0)) * G; };
-        for (int i = threadIdx.x; i < n_part * G; i += NW * 32) wt[i] = __ldcg(a.part_ml + slot(i / G) + i % G);
+        [[maybe_unused]] auto pslot = [&](int c, int head) {
+          return ((size_t)r * a.Hq + (size_t)hk * G + head) * a.prefix_split + (c - n_list);
+        };
+        for (int i = threadIdx.x; i < n_part * G; i += NW * 32) {
+          const int c = i / G, head = i % G;
+          if (LIST != kPrefix || c < n_list) wt[i] = __ldcg(a.part_ml + slot(c) + head);
+          else wt[i] = prefix_part(sg.first, c - n_list) ? __ldcg(a.prefix_lse + pslot(c, head)) : -CUDART_INF_F;
+        }
         __syncthreads();
         for (int head = warp; head < G; head += NW) {
           float M = -CUDART_INF_F, Ls = 0.f;
@@ -987,7 +1066,12 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
           float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
           for (int c = 0; c < n_part; ++c) {
-            const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(c) + head) * D + dim));
+            const float* from = a.part_o + (slot(c) + head) * D + dim;
+            if constexpr (LIST == kPrefix) {
+              if (c >= n_list && !prefix_part(sg.first, c - n_list)) continue;
+              if (c >= n_list) from = a.prefix_o + pslot(c, head) * D + dim;
+            }
+            const float4 p = __ldcg(reinterpret_cast<const float4*>(from));
             const float w = wt[c * G + head];
             o.x = fmaf(p.x, w, o.x);
             o.y = fmaf(p.y, w, o.y);
@@ -1014,12 +1098,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         int i = r, n = 0, Li = 0;
         while (n == 0 && ++i < a.batch) {  // a later request has blocks, as the range goes on
           Li = a.seq_lens[i];
-          n = listed(Li);
+          n = listed(i, Li);
         }
         if (n == 0) sg.left = 0;  // not reached
         sg.r = min(i, a.batch - 1);
         sg.nblk = n;
         sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
+        sg.first = LIST == kPrefix ? blocks_of(Li, mb) - n : 0;
       }
     }
     __syncthreads();

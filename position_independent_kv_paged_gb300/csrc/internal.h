@@ -40,6 +40,12 @@ struct DecodeArgs {
   // selected blocks (null: all)
   const int32_t* selected;   // [B][Hkv][max_sel] numbers of blocks in the request's table, -1: unused
   int max_sel;
+  // shared prefixes (null: none), whose part of the attention a kernel before has computed
+  const int32_t* cu_requests;    // [n_prefix + 1]
+  const int32_t* prefix_blocks;  // [n_prefix]
+  int n_prefix, max_requests, prefix_split;
+  const float* prefix_o;         // [B][Hq][prefix_split][D]
+  const float* prefix_lse;       // [B][Hq][prefix_split] log2
 };
 
 // Arguments of one prefill launch.
@@ -60,6 +66,12 @@ struct PrefillArgs {
   int batch, total_q, max_q_len, Hq, Hkv, G, D, BS, num_blocks, max_blocks;
   float scale;
   int* err;
+  // shared prefixes (launch_prefix): a query row is a request, total_q the requests of the batch, `batch` the groups,
+  // cu_q_lens their requests, kv_lens and the tables those of the requests, max_q_len a bound of a group's requests
+  const int32_t* prefix_blocks;  // [batch]
+  int n_split;                   // parts of a prefix
+  float* part_o;                 // [total_q][Hq][n_split][D], divided by the part's denominator
+  float* part_lse;               // [total_q][Hq][n_split] log2 of it
 };
 
 // Error bits (mirror MINIPIC_DEVERR_* of the public header).
@@ -102,7 +114,8 @@ cudaError_t launch_decode_weights(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_simt_selected(const DecodeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_decode_selected(const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_selected_q8(const DecodeArgs& a, cudaStream_t s);
-// Shared prefixes, bf16, tensor cores (num_blocks > 0).
+// The rest of a batch with shared prefixes, joined with the partial results of launch_prefix: bf16, tensor cores
+// (num_blocks > 0).
 cudaError_t launch_decode_prefix(const DecodeArgs& a, cudaStream_t s);
 // w_raw and w_lse -> weights.
 cudaError_t launch_block_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
@@ -112,6 +125,9 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, bool rotate, cudaStream_t 
 // Both over a pool whose keys are rotated already at their positions, as fp16.
 cudaError_t launch_prefill_rotated(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_pair_rotated(const PrefillArgs& a, cudaStream_t s);
+// The attention of groups of requests to the prefix they share, into partial results (bf16).
+cudaError_t launch_prefix(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_prefix_pair(const PrefillArgs& a, cudaStream_t s);
 // One grid of prefill tiles followed by decode splits (both with rotation).
 cudaError_t launch_mixed(const PrefillArgs& p, const DecodeArgs& d, cudaStream_t s);
 // Head dim 128: one grid of CTA-pair prefill clusters and decode clusters.

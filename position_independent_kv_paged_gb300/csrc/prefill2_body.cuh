@@ -28,6 +28,7 @@
 #include <math_constants.h>
 
 #include "internal.h"
+#include "prefix.cuh"
 #include "ptx.cuh"
 #include "umma.cuh"
 
@@ -124,11 +125,16 @@ __device__ __forceinline__ void rot_pack(U4& x, U4& y, const uint64_t (&c2)[4], 
 // One CTA computes query-tile pair `pair` of request r and kv head hk and
 // loads every K~/V box it reads itself.  vmap_p is the block view of the V pool
 // (make_pool_block_map).  With ROPE and not KROT the pool holds the keys rotated
-// already, in fp16.
-template <int D, bool ROPE, int NB = kNB, int NSK = kNSK, int NSV = kNSV, bool KROT = ROPE>
+// already, in fp16.  PREFIX: r is a group of requests that share their first
+// blocks, one query row each; every row sees every key of part `split` of those
+// blocks, and the result goes to the partial results of the decode that joins it
+// with each request's other keys (decode_list.cuh).
+template <int D, bool ROPE, int NB = kNB, int NSK = kNSK, int NSV = kNSV, bool KROT = ROPE, bool PREFIX = false>
 __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p,
                                              const PrefillLaunch2& L, const int pair, const int n_pairs,
-                                             const int hk, const int r, uint8_t* smem_raw) {
+                                             const int hk, const int r, uint8_t* smem_raw,
+                                             [[maybe_unused]] const int split = 0) {
+  static_assert(!PREFIX || NB == prefix::kTileBlocks<D>, "the parts of a prefix are whole tiles");
   using G_ = PG2<D, NB, NSK, NSV>;
   constexpr int BN = G_::BN;
   const PrefillArgs& a = L.a;
@@ -144,16 +150,39 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.G, TQ = L.tq, mb = a.max_blocks;
-  const int q0 = a.cu_q_lens[r];
-  const int ql = a.cu_q_lens[r + 1] - q0;
   const int tok0 = 2 * pair * TQ;  // first token of query tile 0
-  if (tid == 0 && pair == n_pairs - 1 && ql > n_pairs * 2 * TQ) atomicOr(a.err, kErrSeqLen);
+  int q0, ql, kvl, t_first = 0, t_end = 0;  // PREFIX: key tiles t_first .. t_end - 1
+  int trow = r;                             // row of the tables
+  if constexpr (PREFIX) {
+    bool bad;
+    const prefix::Group gr = prefix::group(a.cu_q_lens, a.prefix_blocks, r, a.total_q, mb, a.max_q_len, bad);
+    if (gr.blocks == 0 || tok0 >= gr.n) return;
+    q0 = gr.q0;
+    ql = gr.n;
+    kvl = 16 * gr.blocks;
+    prefix::part((gr.blocks + NB - 1) / NB, split, a.n_split, t_first, t_end);
+    if (t_first == t_end) return;
+    // the first request that holds the whole prefix; every warp looks for itself
+    trow = -1;
+    for (int i = 0; i < ql && trow < 0; i += 32) {
+      const unsigned has =
+          __ballot_sync(0xffffffffu, i + lane < ql && __ldg(a.kv_lens + q0 + min(i + lane, ql - 1)) >= kvl);
+      if (has) trow = q0 + i + __ffs(has) - 1;
+    }
+    if (trow < 0) return;
+  } else {
+    q0 = a.cu_q_lens[r];
+    ql = a.cu_q_lens[r + 1] - q0;
+    if (tid == 0 && pair == n_pairs - 1 && ql > n_pairs * 2 * TQ) atomicOr(a.err, kErrSeqLen);
+  }
   auto has_rows = [&](int pr) { return pr >= 0 && ql > 0 && 2 * pr * TQ < ql; };
   if (!has_rows(pair)) return;
-  int kvl = a.kv_lens[r];
-  if (kvl < ql || kvl > mb * 16) {
-    if (tid == 0 && pair == 0) atomicOr(a.err, kErrSeqLen);
-    kvl = min(kvl, mb * 16);
+  if constexpr (!PREFIX) {
+    kvl = a.kv_lens[r];
+    if (kvl < ql || kvl > mb * 16) {
+      if (tid == 0 && pair == 0) atomicOr(a.err, kErrSeqLen);
+      kvl = min(kvl, mb * 16);
+    }
   }
   const int nblk = (kvl + 15) >> 4;
   auto tiles_of = [&](int pr) {  // key tiles the rows of query-tile pair pr reach
@@ -162,7 +191,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
     const int lim_last = kvl - ql + t0 + min(2 * TQ, ql - t0) - 1;
     return lim_last >= 0 ? lim_last / BN + 1 : 0;
   };
-  const int n_kt = tiles_of(pair);  // key tiles this CTA loads and computes on
+  const int n_kt = PREFIX ? t_end - t_first : tiles_of(pair);  // key tiles this CTA loads and computes on
 
   // ------------------------------------------------------------ setup
   if (tid == 0) {
@@ -209,12 +238,12 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(NB * G_::HALVES + NB <= 32, "one lane per copy");
     if (n_kt > 0) {
-      const int* bt = a.block_tables + (size_t)r * mb;
-      const int* bs = a.block_starts + (size_t)r * mb;
+      const int* bt = a.block_tables + (size_t)trow * mb;
+      const int* bs = a.block_starts + (size_t)trow * mb;
       const int blk = lane % NB, hh = lane / NB;
       int my_ph = -1, my_st = 0;  // lanes < NB: block NB u + lane of the next K~ tile
       auto fetch = [&](int t) {
-        const int b = NB * t + lane;
+        const int b = NB * (t_first + t) + lane;
         const bool in = lane < NB && b < nblk;
         my_ph = in ? __ldg(bt + b) : -1;
         my_st = in ? __ldg(bs + b) : 0;
@@ -228,19 +257,21 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
           if (lane == 0 && u >= NSK) w = ptx::mbar_wait(bar(G_::B_KFREE + s), ((u / NSK) - 1) & 1);
           if (!__shfl_sync(FULL, w, 0)) { ok = false; break; }
           int flag = 0;
-          if (lane < NB && NB * u + lane < nblk) {
+          const int b = NB * (t_first + u) + lane;
+          if (lane < NB && b < nblk) {
             if (my_ph >= 0 && my_ph < a.num_blocks) flag |= 1;
             else atomicOr(a.err, kErrBlockId);
             if (!ROPE || (my_st >= 0 && my_st < a.max_pos)) flag |= 2;
             // keys outside the table are masked, with a start outside it the whole block
-            if (ROPE && (flag & 1) && (my_st < 0 || my_st > a.max_pos - min(16, kvl - 16 * (NB * u + lane))))
+            if (ROPE && (flag & 1) && (my_st < 0 || my_st > a.max_pos - min(16, kvl - 16 * b)))
               atomicOr(a.err, kErrPosition);
           }
           int* m = meta + 3 * NB * s;
           if (lane < NB) {
             m[lane] = my_st;
             m[NB + lane] = flag;
-            m[2 * NB + lane] = (flag & 1) ? my_ph : -1;
+            // PREFIX: values of a block that is masked whole are not loaded (any may be NaN there)
+            m[2 * NB + lane] = (PREFIX ? flag == 3 : (flag & 1) != 0) ? my_ph : -1;
           }
           const unsigned kv = __ballot_sync(FULL, flag & 1);
           const unsigned rw = __ballot_sync(FULL, KROT && (flag & 3) == 3);
@@ -467,7 +498,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
           for (int k = 0; k < 2; ++k) {
             const int slot = 2 * sp + k;
             const int key = blk * 16 + slot;
-            const bool v = (flag & 3) == 3 && t * BN + key < kvl && start + slot < a.max_pos;
+            const bool v = (flag & 3) == 3 && (t_first + t) * BN + key < kvl && start + slot < a.max_pos;
             U4* px = reinterpret_cast<U4*>(sk + swz(key, fg));
             U4* py = reinterpret_cast<U4*>(sk + ((D == 128) ? BN * 128 + swz(key, fg) : swz(key, fg + 4)));
             U4 x = *px, y = *py;
@@ -493,7 +524,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
       for (int blk = rw; blk < NB; blk += kRotThreads / 32) {
         const int flag = m[NB + blk];
         const int start = m[blk];
-        const bool v = lane < 16 && (flag & 3) == 3 && t * BN + blk * 16 + lane < kvl &&
+        const bool v = lane < 16 && (flag & 3) == 3 && (t_first + t) * BN + blk * 16 + lane < kvl &&
                        (!ROPE || start + lane < a.max_pos);
         const uint32_t bits = __ballot_sync(0xffffffffu, v);
         if (lane == 0) mask16[(t % kMaskRing) * NB + blk] = (uint16_t)bits;
@@ -511,9 +542,10 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
     const int row = tid & 127;    // TMEM lane
     const int rtok = row / G, rh = row - rtok * G;
     const int tq = tok0 + i * TQ + rtok;
-    const bool row_ok = rtok < TQ && tq < ql;
-    const int lim = kvl - ql + tq;                        // last key this row attends
-    const int lim_first = kvl - ql + tok0 + i * TQ;       // ... the tile's first row attends
+    bool row_ok = rtok < TQ && tq < ql;
+    if (PREFIX && row_ok) row_ok = __ldg(a.kv_lens + q0 + tq) >= kvl;  // shorter requests read their own keys
+    const int lim = PREFIX ? kvl - 1 : kvl - ql + tq;                  // last key this row attends
+    const int lim_first = PREFIX ? kvl - 1 : kvl - ql + tok0 + i * TQ;  // ... the tile's first row attends
     const uint32_t lane_base = ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = tmem + 128 * i + lane_base;
     const uint32_t t_o = tmem + 256 + 128 * i + lane_base;
@@ -542,8 +574,8 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
         mw[w] = (uint32_t)mk[2 * w] | ((uint32_t)mk[2 * w + 1] << 16);
         mall &= mw[w];
       }
-      const bool full = mall == 0xffffffffu && t * BN + BN - 1 <= lim_first;
-      const int kb0 = t * BN;
+      const int kb0 = (t_first + t) * BN;
+      const bool full = mall == 0xffffffffu && kb0 + BN - 1 <= lim_first;
       umma::tmem_wait_ld();
       float mx;
       if (full) {
@@ -628,7 +660,9 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
     umma::fence_after_sync();
     const int hq = hk * G + rh;
     __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(q0 + tq) * a.Hq + hq) * D;
-    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+    [[maybe_unused]] const size_t pi = PREFIX ? ((size_t)(q0 + tq) * a.Hq + hq) * a.n_split + split : 0;
+    const bool any = PREFIX ? l_run != 0.f : l_run > 0.f;  // PREFIX: a NaN sum stays one
+    const float inv = any ? 1.f / l_run : 0.f;
 #pragma unroll
     for (int part = 0; part < D / 32; ++part) {
       uint32_t v[32];
@@ -639,7 +673,15 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0u;
       }
-      if (row_ok) {
+      if constexpr (PREFIX) {
+        if (row_ok) {
+          float4* o = reinterpret_cast<float4*>(a.part_o + pi * D + part * 32);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o[j] = make_float4(__uint_as_float(v[4 * j]) * inv, __uint_as_float(v[4 * j + 1]) * inv,
+                               __uint_as_float(v[4 * j + 2]) * inv, __uint_as_float(v[4 * j + 3]) * inv);
+        }
+      } else if (row_ok) {
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           uint4 o;
@@ -651,7 +693,9 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
         }
       }
     }
-    if (row_ok && a.lse)
+    if constexpr (PREFIX) {
+      if (row_ok) a.part_lse[pi] = any ? m_use + log2f(l_run) : -CUDART_INF_F;
+    } else if (row_ok && a.lse)
       a.lse[(size_t)(q0 + tq) * a.Hq + hq] = l_run > 0.f ? (m_use + log2f(l_run)) * kLn2 : -CUDART_INF_F;
   }
 

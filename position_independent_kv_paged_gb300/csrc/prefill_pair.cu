@@ -51,6 +51,7 @@
 
 #include "decode_body.cuh"
 #include "internal.h"
+#include "prefix.cuh"
 #include "ptx.cuh"
 #include "tmap.cuh"
 #include "umma.cuh"
@@ -63,6 +64,7 @@ using ptx::U4;
 constexpr int D = 128;
 constexpr int kHalfBlocks = 5;                 // blocks of a key tile held by one CTA
 constexpr int kTileBlocks = 2 * kHalfBlocks;   // blocks of a key tile
+static_assert(kTileBlocks == prefix::kTileBlocks<D>, "the parts of a prefix are whole tiles");
 constexpr int BN = 16 * kTileBlocks;           // 160 keys per tile
 constexpr int BH = 16 * kHalfBlocks;           // 80 keys per CTA
 constexpr int kMaskRing = 8;
@@ -179,9 +181,14 @@ __device__ __forceinline__ void regs_dec() {
 // head hk (both CTAs of a cluster call it with the same item).  With ROPE and
 // not KROT the pool holds the keys rotated already, in fp16: the query is
 // prepared as with rotation and the key tiles go to the product as they arrive.
-template <bool ROPE, int NSK, int NSV, bool KROT = ROPE>
+// PREFIX: r is a group of requests that share their first blocks, one query row
+// each instead of a chunk; every row sees every key of part `split` of those
+// blocks, and the result goes to the partial results of the decode that joins it
+// with each request's other keys (decode_list.cuh).
+template <bool ROPE, int NSK, int NSV, bool KROT = ROPE, bool PREFIX = false>
 __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensorMap& vmap, const PairLaunch& L,
-                                         const int pair, const int hk, const int r, uint8_t* smem_raw) {
+                                         const int pair, const int hk, const int r, uint8_t* smem_raw,
+                                         [[maybe_unused]] const int split = 0) {
   using P_ = PP<NSK, NSV>;
   const PrefillArgs& a = L.a;
   const uint32_t sbase = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -199,10 +206,31 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t crank = ptx::cluster_rank();
   const int G = a.G, TQ = L.tq, mb = a.max_blocks;
-  const int q0 = a.cu_q_lens[r];
-  const int ql = a.cu_q_lens[r + 1] - q0;
+  int q0, ql, kvl = 0, t_first = 0, t_end = 0;  // PREFIX: key tiles t_first .. t_end - 1
+  int trow = r;                                  // row of the tables
+  if constexpr (PREFIX) {
+    bool bad;
+    const prefix::Group gr = prefix::group(a.cu_q_lens, a.prefix_blocks, r, a.total_q, mb, a.max_q_len, bad);
+    if (gr.blocks == 0 || 2 * pair * TQ >= gr.n) return;  // decided alike in both CTAs of the pair
+    q0 = gr.q0;
+    ql = gr.n;
+    kvl = 16 * gr.blocks;
+    prefix::part((gr.blocks + kTileBlocks - 1) / kTileBlocks, split, a.n_split, t_first, t_end);
+    if (t_first == t_end) return;
+    // the first request that holds the whole prefix; every warp looks for itself
+    trow = -1;
+    for (int i = 0; i < ql && trow < 0; i += 32) {
+      const unsigned has = __ballot_sync(FULL, i + lane < ql && __ldg(a.kv_lens + q0 + min(i + lane, ql - 1)) >= kvl);
+      if (has) trow = q0 + i + __ffs(has) - 1;
+    }
+    if (trow < 0) return;
+  } else {
+    q0 = a.cu_q_lens[r];
+    ql = a.cu_q_lens[r + 1] - q0;
+  }
   const int tok0 = (2 * pair + (int)crank) * TQ;  // first token of this CTA's query tile
-  if (tid == 0 && crank == 0 && pair == L.n_pairs - 1 && ql > L.n_pairs * 2 * TQ) atomicOr(a.err, kErrSeqLen);
+  if (!PREFIX && tid == 0 && crank == 0 && pair == L.n_pairs - 1 && ql > L.n_pairs * 2 * TQ)
+    atomicOr(a.err, kErrSeqLen);
 
   // Loads whose latency the setup below hides: warps 0-3's query row and its
   // position, and the K~ producer's table entries of the first tile.
@@ -226,20 +254,25 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
     }
   }
   int pre_ph = -1, pre_st = 0;
-  if (warp == kTmaWarp && lane < kTileBlocks && lane < mb) {
-    pre_ph = __ldg(a.block_tables + (size_t)r * mb + lane);
-    pre_st = __ldg(a.block_starts + (size_t)r * mb + lane);
+  if (warp == kTmaWarp && lane < kTileBlocks && kTileBlocks * t_first + lane < mb) {
+    pre_ph = __ldg(a.block_tables + (size_t)trow * mb + kTileBlocks * t_first + lane);
+    pre_st = __ldg(a.block_starts + (size_t)trow * mb + kTileBlocks * t_first + lane);
   }
-  if (ql <= 0 || 2 * pair * TQ >= ql) return;  // decided alike in both CTAs of the pair
-  int kvl = a.kv_lens[r];
-  if (kvl < ql || kvl > mb * 16) {
-    if (tid == 0 && crank == 0 && pair == 0) atomicOr(a.err, kErrSeqLen);
-    kvl = min(kvl, mb * 16);
+  int n_kt;
+  if constexpr (PREFIX) {
+    n_kt = t_end - t_first;
+  } else {
+    if (ql <= 0 || 2 * pair * TQ >= ql) return;  // decided alike in both CTAs of the pair
+    kvl = a.kv_lens[r];
+    if (kvl < ql || kvl > mb * 16) {
+      if (tid == 0 && crank == 0 && pair == 0) atomicOr(a.err, kErrSeqLen);
+      kvl = min(kvl, mb * 16);
+    }
+    // key tiles reached by the pair's last row
+    const int lim_last = kvl - ql + min(2 * (pair + 1) * TQ, ql) - 1;
+    n_kt = lim_last >= 0 ? lim_last / BN + 1 : 0;
   }
   const int nblk = (kvl + 15) >> 4;
-  // key tiles reached by the pair's last row
-  const int lim_last = kvl - ql + min(2 * (pair + 1) * TQ, ql) - 1;
-  const int n_kt = lim_last >= 0 ? lim_last / BN + 1 : 0;
 
   // ------------------------------------------------------------ setup
   if (tid == 0) {
@@ -290,29 +323,30 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
       // blocks.  The slot is rewritten for tile u + 8 only after QK(u + 4),
       // which follows PV(u + 2): every reader is past tile u by then.
       if (n_kt > 0) {
-        const int* bt = a.block_tables + (size_t)r * mb;
-        const int* bs = a.block_starts + (size_t)r * mb;
+        const int* bt = a.block_tables + (size_t)trow * mb;
+        const int* bs = a.block_starts + (size_t)trow * mb;
         const int kb = lane % kHalfBlocks, hh = lane / kHalfBlocks;   // copy lanes: block, 64-column half
         const int src = kHalfBlocks * (int)crank + kb;               // lane holding that block's entries
         const int own = lane - kHalfBlocks * (int)crank;             // 0..4 on this CTA's block lanes
         const bool mine = own >= 0 && own < kHalfBlocks;
         int my_ph = -1, my_st = 0;
         auto fetch = [&](int u) {
-          const int b = kTileBlocks * u + lane;
+          const int b = kTileBlocks * (t_first + u) + lane;
           const bool in = lane < kTileBlocks && b < nblk;
           my_ph = in ? __ldg(bt + b) : -1;
           my_st = in ? __ldg(bs + b) : 0;
         };
         bool ok = true;
-        my_ph = lane < kTileBlocks && lane < nblk ? pre_ph : -1;  // tile 0, loaded before the setup
-        my_st = lane < kTileBlocks && lane < nblk ? pre_st : 0;
+        const bool in0 = lane < kTileBlocks && kTileBlocks * t_first + lane < nblk;
+        my_ph = in0 ? pre_ph : -1;  // the first tile, loaded before the setup
+        my_st = in0 ? pre_st : 0;
         for (int u = 0; u < n_kt; ++u) {
           {
             const int s = u % NSK;
             bool w = true;
             if (lane == 0 && u >= NSK) w = ptx::mbar_wait(bar(P_::B_KFREE + s), ((u / NSK) - 1) & 1);
             if (!__shfl_sync(FULL, w, 0)) { ok = false; break; }
-            const int b = kTileBlocks * u + lane;
+            const int b = kTileBlocks * (t_first + u) + lane;
             int flag = 0;  // bit 0: usable block id, bit 1: usable start
             if (lane < kTileBlocks && b < nblk) {
               if (my_ph >= 0 && my_ph < a.num_blocks) flag |= 1;
@@ -340,7 +374,9 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
               m[own] = my_st;
               m[kHalfBlocks + own] = flag;
             }
-            if (lane < kTileBlocks) vblk[(u % kMaskRing) * kTileBlocks + lane] = (flag & 1) ? my_ph : -1;
+            // PREFIX: values of a block that is masked whole are not loaded (any may be NaN there)
+            if (lane < kTileBlocks)
+              vblk[(u % kMaskRing) * kTileBlocks + lane] = (flag & (PREFIX ? 2 : 0)) == (PREFIX ? 2 : 0) && (flag & 1) ? my_ph : -1;
             const unsigned kv = __ballot_sync(FULL, mine && (flag & 1));
             const int ph_l = __shfl_sync(FULL, my_ph, src);
             __syncwarp();
@@ -478,7 +514,7 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
           const int flag = m[kHalfBlocks + blk];
           const int start = m[blk];
           const int key = blk * 16 + sl;
-          vs[blk] = (flag & 3) == 3 && t * BN + key0 + key < kvl && start + sl < a.max_pos;
+          vs[blk] = (flag & 3) == 3 && (t_first + t) * BN + key0 + key < kvl && start + sl < a.max_pos;
           // row start + sl of the fp16 table: cos (64) | sin (64); this thread's 8 frequencies
           const uint16_t* rg = a.cos_sin16 + (size_t)(vs[blk] ? start + sl : 0) * D;
           const uint4 c4 = __ldg(reinterpret_cast<const uint4*>(rg + 8 * fg));
@@ -521,9 +557,10 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
     const int row = 32 * qd + lane;
     const int rtok = row / G, rh = row - rtok * G;
     const int tq = tok0 + rtok;
-    const bool row_ok = rtok < TQ && tq < ql;
-    const int lim = kvl - ql + tq;         // last key this row attends
-    const int lim_first = kvl - ql + tok0;  // ... the tile's first row attends
+    bool row_ok = rtok < TQ && tq < ql;
+    if (PREFIX && row_ok) row_ok = __ldg(a.kv_lens + q0 + tq) >= kvl;  // shorter requests read their own keys
+    const int lim = PREFIX ? kvl - 1 : kvl - ql + tq;          // last key this row attends
+    const int lim_first = PREFIX ? kvl - 1 : kvl - ql + tok0;  // ... the tile's first row attends
     const uint32_t lane_base = (uint32_t)(32 * qd) << 16;
     const uint32_t t_o = tmem + kColO + lane_base + 64 * h;
     const uint32_t nb_id = 1 + qd;  // named barrier of warps qd, qd + 4
@@ -625,7 +662,7 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
         mw[k] = mk[k];
         mall &= mw[k];
       }
-      const int kb0 = t * BN + BH * h;
+      const int kb0 = (t_first + t) * BN + BH * h;
       const bool full = mall == 0xffffu && kb0 + BH - 1 <= lim_first;
       umma::tmem_wait_ld();
       float mx = -CUDART_INF_F;
@@ -737,7 +774,9 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
     umma::fence_after_sync();
     const int hq = hk * G + rh;
     __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(q0 + tq) * a.Hq + hq) * D + 64 * h;
-    const float inv = l_tot > 0.f ? 1.f / l_tot : 0.f;
+    [[maybe_unused]] const size_t pi = PREFIX ? ((size_t)(q0 + tq) * a.Hq + hq) * a.n_split + split : 0;
+    const bool any = PREFIX ? l_tot != 0.f : l_tot > 0.f;  // PREFIX: a NaN sum stays one
+    const float inv = any ? 1.f / l_tot : 0.f;
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       uint32_t v[32];
@@ -748,7 +787,15 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] = 0u;
       }
-      if (row_ok) {
+      if constexpr (PREFIX) {
+        if (row_ok) {
+          float4* o = reinterpret_cast<float4*>(a.part_o + pi * D + 64 * h + part * 32);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            o[j] = make_float4(__uint_as_float(v[4 * j]) * inv, __uint_as_float(v[4 * j + 1]) * inv,
+                               __uint_as_float(v[4 * j + 2]) * inv, __uint_as_float(v[4 * j + 3]) * inv);
+        }
+      } else if (row_ok) {
 #pragma unroll
         for (int j = 0; j < 32; j += 8) {
           uint4 o;
@@ -760,7 +807,9 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
         }
       }
     }
-    if (row_ok && h == 0 && a.lse)
+    if constexpr (PREFIX) {
+      if (row_ok && h == 0) a.part_lse[pi] = any ? m_use + log2f(l_tot) : -CUDART_INF_F;
+    } else if (row_ok && h == 0 && a.lse)
       a.lse[(size_t)(q0 + tq) * a.Hq + hq] = l_tot > 0.f ? (m_use + log2f(l_tot)) * kLn2 : -CUDART_INF_F;
   }
 
@@ -781,6 +830,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // heaviest (latest) query-tile pairs first
   pair_cta<ROPE, NSK, NSV, KROT>(kmap, vmap, L, L.n_pairs - 1 - (int)(blockIdx.x >> 1), blockIdx.y, blockIdx.z,
                                  smem_raw);
+}
+
+// Grid: 2 x query-tile pairs, kv head x part, group.
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_pair_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const PairLaunch L) {
+  extern __shared__ uint8_t smem_raw[];
+  pair_cta<true, kNSK, kNSV, true, true>(kmap, vmap, L, (int)(blockIdx.x >> 1), (int)(blockIdx.y % L.a.Hkv), blockIdx.z,
+                                         smem_raw, (int)(blockIdx.y / L.a.Hkv));
 }
 
 // Mixed continuous batch in one launch (the device side of interleaved
@@ -866,12 +924,13 @@ cudaError_t launch_mixed_t(const PrefillArgs& p, const DecodeArgs& d, cudaStream
   return cudaLaunchKernelEx(&cfg, mixed_pair_kernel<NT>, km, vm, kb, vb, L, d, (int)n_pre, (int)n_dec);
 }
 
-template <bool ROPE, bool KROT = ROPE>
-cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
+using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const PairLaunch);
+
+// kernel<<<(2 x pairs, gy, gz), clusters of two>>>
+cudaError_t launch_pairs(PairKernel kernel, bool (&done)[64], const PrefillArgs& a, int gy, int gz, cudaStream_t s) {
   using P_ = PP<kNSK, kNSV>;
   const int smem = P_::TOTAL + 1024;
-  static bool done[64] = {false};
-  cudaError_t e = set_smem_once(prefill_pair_kernel<ROPE, kNSK, kNSV, KROT>, smem, done);
+  cudaError_t e = set_smem_once(kernel, smem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const long long rows = (long long)a.num_blocks * a.Hkv * 16;
@@ -879,7 +938,7 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
   PairLaunch L{a, 128 / a.G, 0};
   L.n_pairs = (a.max_q_len + 2 * L.tq - 1) / (2 * L.tq);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * L.n_pairs), (unsigned)a.Hkv, (unsigned)a.batch);
+  cfg.gridDim = dim3((unsigned)(2 * L.n_pairs), (unsigned)gy, (unsigned)gz);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -890,7 +949,13 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<ROPE, kNSK, kNSV, KROT>, km, vm, L);
+  return cudaLaunchKernelEx(&cfg, kernel, km, vm, L);
+}
+
+template <bool ROPE, bool KROT = ROPE>
+cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
+  static bool done[64] = {false};
+  return launch_pairs(prefill_pair_kernel<ROPE, kNSK, kNSV, KROT>, done, a, a.Hkv, a.batch, s);
 }
 
 }  // namespace
@@ -902,6 +967,12 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, bool rotate, cudaStream_t 
 
 cudaError_t launch_prefill_pair_rotated(const PrefillArgs& a, cudaStream_t s) {
   return a.D == D ? launch_t<true, false>(a, s) : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_prefix_pair(const PrefillArgs& a, cudaStream_t s) {
+  if (a.D != D) return cudaErrorInvalidValue;
+  static bool done[64] = {false};
+  return launch_pairs(prefix_pair_kernel, done, a, a.Hkv * a.n_split, a.batch, s);
 }
 
 cudaError_t launch_mixed_pair(const PrefillArgs& p, const DecodeArgs& d, cudaStream_t s) {

@@ -177,6 +177,19 @@ def test_nan_passes_on_to_the_rows_that_attend_to_it(env):
         assert not nan.any()
 
 
+def test_bad_group_data_is_flagged(env):
+    """Groups outside the batch and prefixes longer than the tables set the length bit; nothing is read out of range,
+    and requests that such a group does not hold are computed."""
+    torch, mp, dev = env
+    t = groups(torch, dev, [400, 420, 440, 460], [0, 2, 4], [10, 12], 8, 2, 128, 17)
+    want = run(env, t)[0]
+    for cu, blocks in (([0, 2, 9], [10, 12]), ([0, 2, 4], [10, 10 ** 6]), ([0, 2, 1], [10, 12]), ([0, 2, 4], [10, -3])):
+        t["cu"], t["blocks"] = i32(torch, dev, cu), i32(torch, dev, blocks)
+        got = run(env, t, max_requests=2, max_prefix_blocks=12)[0]
+        assert mp.device_error(clear=True) == 4, (cu, blocks)
+        assert torch.equal(got[:2], want[:2])
+
+
 def test_captured_and_on_a_side_stream(env):
     """Capture runs nothing, replay equals the call, two captured graphs share a workspace one after the other, and a
     call on a side stream allocates and clears its own while the current one is behind."""
