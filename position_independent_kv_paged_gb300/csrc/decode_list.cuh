@@ -109,6 +109,7 @@ struct Lay {
   static constexpr int MERGE = kWarps * MERGE_W;                // overlays stages, rows and meta
   static constexpr int TOTAL = MASK + (kChunk + 2 * kWarps) * 4;
   static_assert(MERGE <= TOTAL, "the merge overlays what the loop no longer reads");
+  static_assert(MERGE + 16 * prefix::kMaxSplit * 4 <= TOTAL, "the prefix's parts lie behind it");
   static_assert((kListMaxCtas + prefix::kMaxSplit) * 8 * 4 <= STAGES, "so do the weights of the parts (half the CTAs for groups above 8)");
 };
 
@@ -332,31 +333,34 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         if (bad) atomicOr(a.err, kErrSeqLen);
       }
   }
-  // Parts of the prefix of a request that shares `first` blocks: part s holds a tile, and the attention to it is joined
-  // with what the request has (O over its denominator, and log2 of that).
-  [[maybe_unused]] auto prefix_part = [&](int first, int s) {
-    constexpr int TB = prefix::kTileBlocks<D>;
-    int t0, t1;
-    prefix::part((first + TB - 1) / TB, s, a.prefix_split, t0, t1);
-    return first > 0 && t0 < t1;
-  };
-  [[maybe_unused]] auto join_prefix = [&](int first, size_t hq, int dim, float& O, float& lse2) {
-    const float* pl = a.prefix_lse + hq * a.prefix_split;
-    const float* po = a.prefix_o + hq * a.prefix_split * D + dim;
+  // O (over its denominator, lse2 the log2 of that) joined with the n parts of the request's prefix, four dims; pl: their
+  // log2 denominators
+  [[maybe_unused]] auto join_prefix = [&](int n, const float* pl, const float* po, float4& O, float& lse2) {
     float M = lse2;
-    for (int s = 0; s < a.prefix_split; ++s)
-      if (prefix_part(first, s)) M = fmaxf(M, __ldcg(pl + s));
+    for (int s = 0; s < n; ++s) M = fmaxf(M, pl[s]);
     if (M == -CUDART_INF_F) return;
-    const float w0 = exp2f(lse2 - M);
-    float sum = w0, acc = O * w0;
-    for (int s = 0; s < a.prefix_split; ++s)
-      if (prefix_part(first, s)) {
-        const float w = exp2f(__ldcg(pl + s) - M);
-        sum += w;
-        acc = fmaf(__ldcg(po + (size_t)s * D), w, acc);
-      }
-    O = acc / sum;
+    float sum = exp2f(lse2 - M);
+    O.x *= sum;
+    O.y *= sum;
+    O.z *= sum;
+    O.w *= sum;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float w = exp2f(pl[s] - M);
+      const float4 p = __ldcg(reinterpret_cast<const float4*>(po + (size_t)s * D));
+      sum += w;
+      O.x = fmaf(p.x, w, O.x);
+      O.y = fmaf(p.y, w, O.y);
+      O.z = fmaf(p.z, w, O.z);
+      O.w = fmaf(p.w, w, O.w);
+    }
+    const float inv = 1.f / sum;
+    O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
     lse2 = M + log2f(sum);
+  };
+  [[maybe_unused]] auto store4 = [&](size_t hq, int dim, const float4& o) {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + hq * D + dim) =
+        make_uint2(ptx::pack_bf16(o.x, o.y), ptx::pack_bf16(o.z, o.w));
   };
   if (__syncthreads_or(zero)) {  // requests whose list is empty, shared out over the grid
     for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
@@ -365,12 +369,14 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       if constexpr (LIST == kPrefix) {
         const int first = shared_blocks(a, i, L);
         if (first > 0) {  // the request ends with its prefix
-          for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32) {
-            const size_t hq = (size_t)i * a.Hq + e / D;
-            float O = 0.f, lse2 = -CUDART_INF_F;
-            join_prefix(first, hq, e % D, O, lse2);
-            static_cast<__nv_bfloat16*>(a.out)[hq * D + e % D] = __float2bfloat16_rn(O);
-            if (a.lse && e % D == 0) a.lse[hq] = lse2 * kLn2;
+          for (int e = threadIdx.x; e < a.Hq * (D / 4); e += NW * 32) {
+            const size_t hq = (size_t)i * a.Hq + e / (D / 4), at = hq * a.prefix_split;
+            const int dim = 4 * (e % (D / 4));
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            float lse2 = -CUDART_INF_F;
+            join_prefix(prefix::parts<D>(first, a.prefix_split), a.prefix_lse + at, a.prefix_o + at * D + dim, O, lse2);
+            store4(hq, dim, O);
+            if (a.lse && dim == 0) a.lse[hq] = lse2 * kLn2;
           }
           continue;
         }
@@ -939,6 +945,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         continue;
       }
     const int r = sg.r, hk = sg.hk, b_begin = sg.b_begin, nblk = sg.nblk, b_end = b0;
+    // kPrefix: log2 denominators of the prefix's parts, behind what the merge overlays
+    [[maybe_unused]] const int n_pre = LIST == kPrefix && sg.first > 0 ? prefix::parts<D>(sg.first, a.prefix_split) : 0;
+    [[maybe_unused]] float* pre_lse = reinterpret_cast<float*>(sgen + LY::MERGE);
+    [[maybe_unused]] const size_t pre_at = ((size_t)r * a.Hq + (size_t)hk * G) * a.prefix_split;  // + head * prefix_split + part
+    if constexpr (LIST == kPrefix)
+      for (int i = threadIdx.x; i < G * n_pre; i += NW * 32)
+        pre_lse[i] = __ldcg(a.prefix_lse + pre_at + (size_t)(i / n_pre) * a.prefix_split + i % n_pre);
 
     // per-warp state: ms[16], l[16], mt[16], O[16][OST], by column
     {
@@ -968,7 +981,33 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
 
     // the CTA's output of each head, already divided by its denominator: values no larger than V's
     const bool direct = b_begin == 0 && b_end == nblk;
-    for (int idx = threadIdx.x; idx < G * D; idx += NW * 32) {
+    if (LIST == kPrefix && direct && n_pre > 0) {  // as below, four dims a thread
+      for (int idx = threadIdx.x; idx < G * D / 4; idx += NW * 32) {
+        const int head = idx / (D / 4), dim = 4 * (idx % (D / 4));
+        float M = kNone;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, reinterpret_cast<const float*>(sgen + w * LY::MERGE_W)[head]);
+        float Ls = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float* p = reinterpret_cast<const float*>(sgen + w * LY::MERGE_W);
+          const float e = exp2f(p[head] - M);
+          const float4 o = *reinterpret_cast<const float4*>(p + 48 + head * LY::OST + dim);
+          Ls = fmaf(p[16 + head], e, Ls);
+          O = make_float4(fmaf(o.x, e, O.x), fmaf(o.y, e, O.y), fmaf(o.z, e, O.z), fmaf(o.w, e, O.w));
+        }
+        const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
+        O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+        float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
+        join_prefix(n_pre, pre_lse + head * n_pre, a.prefix_o + (pre_at + (size_t)head * a.prefix_split) * D + dim, O,
+                    lse2);
+        const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
+        store4(hq, dim, O);
+        if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
+      }
+    }
+    for (int idx = threadIdx.x; idx < (LIST == kPrefix && direct && n_pre > 0 ? 0 : G * D); idx += NW * 32) {
       const int head = idx / D, dim = idx - head * D;
       constexpr int NST = DUAL ? 2 * NW : NW;  // states of a head: warps, and half columns 4 apart
       auto state = [&](int w) {
@@ -992,11 +1031,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       // the power in two factors: value scales down to fp32's least are 2^-149, past one factor's range with kHead
       const float e = T - M - kHead, e1 = fmaxf(e, -80.f);
       O = Ls == 0.f ? 0.f : O / Ls * exp2f(e1) * exp2f(e - e1);
-      float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
+      const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
       const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
       if (direct) {
-        if constexpr (LIST == kPrefix)
-          if (sg.first > 0) join_prefix(sg.first, hq, dim, O, lse2);
         static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(O);
         if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
         if (WTS && dim == 0) a.w_lse[hq] = lse2;
@@ -1026,16 +1063,14 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         __threadfence();
         // weights of the parts first (one read of their log sums), then the weighted sum, four dims a thread
         // (kPrefix: the parts of the prefix follow those of the list)
-        const int n_list = c2 - c1 + 1, n_part = n_list + (LIST == kPrefix && sg.first > 0 ? a.prefix_split : 0);
+        const int n_list = c2 - c1 + 1, n_part = n_list + n_pre;
         float* wt = reinterpret_cast<float*>(sgen);  // [part][G], over what the stages held
         auto slot = [&](int c) { return (size_t)(2 * (c1 + c) + (c == 0)) * G; };
-        [[maybe_unused]] auto pslot = [&](int c, int head) {
-          return ((size_t)r * a.Hq + (size_t)hk * G + head) * a.prefix_split + (c - n_list);
-        };
+        [[maybe_unused]] auto pslot = [&](int c, int head) { return pre_at + (size_t)head * a.prefix_split + (c - n_list); };
         for (int i = threadIdx.x; i < n_part * G; i += NW * 32) {
           const int c = i / G, head = i % G;
           if (LIST != kPrefix || c < n_list) wt[i] = __ldcg(a.part_ml + slot(c) + head);
-          else wt[i] = prefix_part(sg.first, c - n_list) ? __ldcg(a.prefix_lse + pslot(c, head)) : -CUDART_INF_F;
+          else wt[i] = __ldcg(a.prefix_lse + pslot(c, head));
         }
         __syncthreads();
         for (int head = warp; head < G; head += NW) {
@@ -1067,10 +1102,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
 #pragma unroll 4
           for (int c = 0; c < n_part; ++c) {
             const float* from = a.part_o + (slot(c) + head) * D + dim;
-            if constexpr (LIST == kPrefix) {
-              if (c >= n_list && !prefix_part(sg.first, c - n_list)) continue;
-              if (c >= n_list) from = a.prefix_o + pslot(c, head) * D + dim;
-            }
+            if (LIST == kPrefix && c >= n_list) from = a.prefix_o + pslot(c, head) * D + dim;
             const float4 p = __ldcg(reinterpret_cast<const float4*>(from));
             const float w = wt[c * G + head];
             o.x = fmaf(p.x, w, o.x);

@@ -160,8 +160,10 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
     q0 = gr.q0;
     ql = gr.n;
     kvl = 16 * gr.blocks;
-    prefix::part((gr.blocks + NB - 1) / NB, split, a.n_split, t_first, t_end);
-    if (t_first == t_end) return;
+    const int tiles = prefix::tiles<D>(gr.blocks), parts = prefix::parts<D>(gr.blocks, a.n_split);
+    if (split >= parts) return;
+    t_first = (int)((long long)split * tiles / parts);
+    t_end = (int)((long long)(split + 1) * tiles / parts);
     // the first request that holds the whole prefix; every warp looks for itself
     trow = -1;
     for (int i = 0; i < ql && trow < 0; i += 32) {

@@ -27,17 +27,21 @@ __device__ __forceinline__ Group group(const int32_t* cu, const int32_t* blocks,
   return g;
 }
 
-// Tiles [t0, t1) of part s of n_split, of a prefix of `tiles` key tiles.
-__device__ __forceinline__ void part(int tiles, int s, int n_split, int& t0, int& t1) {
-  t0 = (int)((long long)s * tiles / n_split);
-  t1 = (int)((long long)(s + 1) * tiles / n_split);
-}
-
 // Blocks of a key tile of the kernel that computes the shared part.
 template <int D>
 constexpr int kTileBlocks = D == 128 ? 10 : 6;
 // Parts of a prefix, at most.
 constexpr int kMaxSplit = 64;
+
+// Key tiles of a prefix, and the parts it is cut into: n_split, or one a tile.
+template <int D>
+__device__ __forceinline__ int tiles(int blocks) {
+  return (blocks + kTileBlocks<D> - 1) / kTileBlocks<D>;
+}
+template <int D>
+__device__ __forceinline__ int parts(int blocks, int n_split) {
+  return min(n_split, tiles<D>(blocks));
+}
 
 }  // namespace prefix
 }  // namespace minipic
