@@ -410,6 +410,16 @@ DecodePlan plan_decode_list(int batch, int Hkv, int G, int D, int max_blocks, bo
   return p;
 }
 
+DecodePlan plan_decode_lists(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms) {
+  DecodePlan p = plan_decode_list(batch, Hkv, G, D, max_blocks, bf16, num_sms);
+  // With many more pairs than CTAs at once, a CTA each: equal ranges of the list would make every CTA cut, and join, two
+  // of them (2048 pairs of 1 to 32 blocks behind a prefix, with that: 381 us against 463).  With a few more, the
+  // ranges' even end counts for more (512 pairs of 64 blocks: 39.6 us against 40.9).
+  const long long pairs = (long long)batch * Hkv;
+  if (bf16 && pairs >= 2LL * p.n_split && pairs < (1 << 20)) p.n_split += (int)pairs;
+  return p;
+}
+
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan,
                           cudaStream_t s) {
   // the tensor-core kernel merges its splits itself; the SIMT path merges in a second kernel
@@ -930,7 +940,7 @@ size_t selected_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32
   const int sms = current_sms();
   size_t most = 0;
   for (int bf16 = 0; bf16 < 2; ++bf16) {
-    const DecodePlan p = plan_decode_list(batch, Hkv, Hq / Hkv, D, S, bf16 != 0, sms);
+    const DecodePlan p = plan_decode_lists(batch, Hkv, Hq / Hkv, D, S, bf16 != 0, sms);
     const size_t n = decode_ws_weights(batch, Hq, Hkv, D, count_partials(p, batch, Hq, Hq / Hkv), 0).total;
     most = n > most ? n : most;
   }
@@ -957,7 +967,7 @@ minipic_status decode_selected(minipic_dtype dtype, int32_t num_q_heads, const m
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
   // the lists are no longer than the tables; the workspace is sized by max_selected alone
   const DecodePlan plan =
-      plan_decode_list(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim, max_selected, bf16, sms);
+      plan_decode_lists(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim, max_selected, bf16, sms);
   DecodeArgs a = decode_args(bf16, num_q_heads, kv, rope, b, scale, plan, err);
   a.k_scale = k_scale;
   a.v_scale = v_scale;
@@ -1118,42 +1128,39 @@ minipic_status minipic_attn_decode_selected_q8(minipic_dtype dtype, int32_t num_
 
 namespace {
 
-// Parts of each prefix.  The kernel of the shared part keeps a cluster of two SMs busy per (pair of query tiles, kv
-// head, part) at head dim 128, one SM at 64, and takes waves * (tiles of a part + its start and end, about three
-// tiles' time): the count of parts that makes this least, from the planning bounds.
-int prefix_split(int num_prefixes, int max_requests, int max_prefix_blocks, int Hkv, int G, int D, int sms) {
-  const int tq = 128 / G, tile = D == 128 ? prefix::kTileBlocks<128> : prefix::kTileBlocks<64>;
-  const long long units = (long long)num_prefixes * Hkv * ((max_requests + 2LL * tq - 1) / (2 * tq));
-  const int slots = D == 128 ? (sms / 2 > 0 ? sms / 2 : 1) : sms, tiles = (int)((max_prefix_blocks + tile - 1LL) / tile);
-  int best = 1;
-  long long least = -1;
-  for (int n = 1; n <= prefix::kMaxSplit && n <= (tiles > 0 ? tiles : 1) && (long long)n * Hkv <= kMaxGridYZ; ++n) {
-    const long long cost = ((units * n + slots - 1) / slots) * ((tiles + n - 1) / n + 3);
-    if (least < 0 || cost < least) {
-      least = cost;
-      best = n;
-    }
-  }
-  return best;
-}
-
+// The shared part's items (a pair of query tiles, a kv head, a part of the prefix each) and workspace.  They are cut on
+// the device, where the groups are; here their number is bounded: a part of a prefix is worth having from about 8
+// tiles on, and 8 waves of items balance well enough.
 struct PrefixWs {
-  int n_split;  // 0: nothing is shared
   DecodePlan plan;
-  size_t list_bytes, o_bytes, lse_bytes, total;
+  int n_slots, max_waves;
+  long long items;  // 0: nothing is shared
+  size_t list_bytes, group_bytes, o_bytes, lse_bytes, total;
 };
 PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, int max_requests, int max_prefix_blocks,
                    int sms) {
   PrefixWs w{};
   const int G = Hq / Hkv;
-  w.plan = plan_decode_list(batch, Hkv, G, D, mb, true, sms);
+  w.plan = plan_decode_lists(batch, Hkv, G, D, mb, true, sms);
   w.list_bytes = decode_ws_weights(batch, Hq, Hkv, D, count_partials(w.plan, batch, Hq, G), 0).total;
   if (num_prefixes > 0 && max_requests >= prefix::kMinRequests && max_prefix_blocks > 0 && G <= 16) {
-    w.n_split = prefix_split(num_prefixes, max_requests, max_prefix_blocks, Hkv, G, D, sms);
-    w.o_bytes = align_up((size_t)batch * Hq * w.n_split * D * sizeof(float), 256);
-    w.lse_bytes = align_up((size_t)batch * Hq * w.n_split * sizeof(float), 256);
+    const int tq = 128 / G, tile = D == 128 ? prefix::kTileBlocks<128> : prefix::kTileBlocks<64>;
+    w.n_slots = D == 128 ? (sms > 1 ? sms / 2 : 1) : sms;  // a cluster of two SMs an item, or one SM
+    // query-tile pairs: of all requests together, and one more a group that ends inside one
+    const long long most = max_requests < batch ? max_requests : batch, groups = num_prefixes < batch ? num_prefixes : batch;
+    const long long each = groups * ((most + 2 * tq - 1) / (2 * tq)), all = batch / (2 * tq) + groups;
+    const long long units = Hkv * (each < all ? each : all);
+    const long long tiles = (max_prefix_blocks + tile - 1LL) / tile;
+    const long long waves = (units * tiles + 8LL * w.n_slots - 1) / (8LL * w.n_slots);
+    w.max_waves = waves > 8 ? 8 : (int)waves;
+    w.items = (long long)w.max_waves * w.n_slots;
+    if (w.items > units * tiles) w.items = units * tiles;
+    if (w.items < units) w.items = units;
+    w.group_bytes = align_up((size_t)num_prefixes * sizeof(int2), 256);
+    w.o_bytes = (size_t)w.items * prefix::kRows * D * sizeof(float);
+    w.lse_bytes = (size_t)w.items * prefix::kRows * sizeof(float);
   }
-  w.total = w.list_bytes + w.o_bytes + w.lse_bytes;
+  w.total = w.list_bytes + w.group_bytes + w.o_bytes + w.lse_bytes;
   return w;
 }
 
@@ -1187,7 +1194,6 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
   int* err = nullptr;
   int sms = 0;
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
-  if (groups->num_prefixes > kMaxGridYZ) return MINIPIC_ERR_UNSUPPORTED;
   const PrefixWs w = prefix_ws(b->batch, num_q_heads, kv->num_kv_heads, kv->head_dim, b->max_blocks_per_seq,
                                groups->num_prefixes, groups->max_requests, groups->max_prefix_blocks, sms);
   if (!workspace || workspace_bytes < w.total || !aligned16(workspace)) return MINIPIC_ERR_WORKSPACE;
@@ -1198,14 +1204,15 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
   a.cu_requests = groups->cu_requests;
   a.prefix_blocks = groups->prefix_blocks;
   // groups that the planning bounds rule out share nothing
-  a.n_prefix = w.n_split > 0 ? groups->num_prefixes : 0;
+  a.n_prefix = w.items > 0 ? groups->num_prefixes : 0;
   a.max_requests = groups->max_requests;
-  a.prefix_split = w.n_split;
+  a.items = w.items;
   char* ws = static_cast<char*>(workspace) + w.list_bytes;
-  a.prefix_o = reinterpret_cast<const float*>(ws);
-  a.prefix_lse = reinterpret_cast<const float*>(ws + w.o_bytes);
+  a.group_items = reinterpret_cast<const int2*>(ws);
+  a.prefix_o = reinterpret_cast<const float*>(ws + w.group_bytes);
+  a.prefix_lse = reinterpret_cast<const float*>(ws + w.group_bytes + w.o_bytes);
   const cudaStream_t s = (cudaStream_t)stream;
-  if (w.n_split > 0) {
+  if (w.items > 0) {
     PrefillArgs p{};
     p.q = a.q;
     p.cu_q_lens = groups->cu_requests;
@@ -1231,10 +1238,12 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
     p.scale = a.scale;
     p.err = err;
     p.prefix_blocks = groups->prefix_blocks;
-    p.n_split = w.n_split;
-    p.part_o = reinterpret_cast<float*>(ws);
-    p.part_lse = reinterpret_cast<float*>(ws + w.o_bytes);
-    if (launch_prefix(p, s) != cudaSuccess) return MINIPIC_ERR_CUDA;
+    p.n_slots = w.n_slots;
+    p.max_waves = w.max_waves;
+    p.group_items = const_cast<int2*>(a.group_items);
+    p.part_o = const_cast<float*>(a.prefix_o);
+    p.part_lse = const_cast<float*>(a.prefix_lse);
+    if (launch_prefix(p, w.items, s) != cudaSuccess) return MINIPIC_ERR_CUDA;
   }
   return launch_decode_prefix(a, s) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }

@@ -109,8 +109,9 @@ struct Lay {
   static constexpr int MERGE = kWarps * MERGE_W;                // overlays stages, rows and meta
   static constexpr int TOTAL = MASK + (kChunk + 2 * kWarps) * 4;
   static_assert(MERGE <= TOTAL, "the merge overlays what the loop no longer reads");
-  static_assert(MERGE + 16 * prefix::kMaxSplit * 4 <= TOTAL, "the prefix's parts lie behind it");
-  static_assert((kListMaxCtas + prefix::kMaxSplit) * 8 * 4 <= STAGES, "so do the weights of the parts (half the CTAs for groups above 8)");
+  static_assert((2 * 257 + 2048) * 4 <= STAGES, "the groups and the lists' lengths overlay the stages");
+  static_assert(MERGE + 16 * prefix::kMaxParts * 4 <= TOTAL, "the prefix's parts lie behind it");
+  static_assert((kListMaxCtas + prefix::kMaxParts) * 8 * 4 <= STAGES, "so do the weights of the parts (half the CTAs for groups above 8)");
 };
 
 // Slot held by MMA fragment row g < 8 (row g + 8 holds slot + 2): rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9 are four
@@ -221,20 +222,26 @@ __device__ __forceinline__ uint32_t distance(int t, int b) {
 // the prefix that a request shares with its group; the attention to the prefix is joined with theirs in the merge.
 enum List { kAll, kSelected, kPrefix };
 
-// Blocks that request i of length L shares with its group: the group's, if the request holds them all.
-__device__ __forceinline__ int shared_blocks(const DecodeArgs& a, int i, int L) {
+// The group of request i of length L, and the blocks it shares: the group's, if the request holds them all (else 0).  cu
+// and nb: where the groups are read.
+struct Shared {
+  int p, q0, blocks;
+};
+__device__ __forceinline__ Shared shared_of(const DecodeArgs& a, const int* cu, const int* nb, int i, int L) {
   int lo = 0, hi = a.n_prefix;  // groups that begin at request i or before it
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu_requests + mid) <= i) lo = mid + 1;
+    if (cu[mid] <= i) lo = mid + 1;
     else hi = mid;
   }
-  if (lo == 0) return 0;
+  if (lo == 0) return Shared{0, 0, 0};
   bool bad;
-  const prefix::Group g =
-      prefix::group(a.cu_requests, a.prefix_blocks, lo - 1, a.batch, a.max_blocks, a.max_requests, bad);
-  return i >= g.q0 && i < g.q0 + g.n && L >= 16LL * g.blocks ? g.blocks : 0;
+  const prefix::Group g = prefix::group(cu[lo - 1], cu[lo], nb[lo - 1], a.batch, a.max_blocks, a.max_requests, bad);
+  const bool in = i >= g.q0 && i < g.q0 + g.n && L >= 16LL * g.blocks;
+  return Shared{lo - 1, g.q0, in ? g.blocks : 0};
 }
+// Groups that a CTA stages in shared memory (over its stages), and lengths of lists.
+constexpr int kStagedGroups = 256, kStagedLists = 2048;
 
 template <bool Q8, int D, int NT, bool DUAL, bool WTS, int NS, int CPS, List LIST>
 __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __grid_constant__ DecodeArgs a) {
@@ -255,10 +262,24 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   const int g8 = lane >> 2, tig = lane & 3;
   const int G = a.G, mb = a.max_blocks;
 
+  // kPrefix: the groups, staged while the stages hold nothing
+  const int* grp_cu = a.cu_requests;
+  const int* grp_nb = a.prefix_blocks;
+  if constexpr (LIST == kPrefix)
+    if (a.n_prefix > 0 && a.n_prefix <= kStagedGroups) {
+      int* st = reinterpret_cast<int*>(sgen);
+      for (int p = threadIdx.x; p <= a.n_prefix; p += NW * 32) {
+        st[p] = __ldg(a.cu_requests + p);
+        if (p < a.n_prefix) st[kStagedGroups + 1 + p] = __ldg(a.prefix_blocks + p);
+      }
+      grp_cu = st;
+      grp_nb = st + kStagedGroups + 1;
+      __syncthreads();
+    }
   // blocks that the list of request i, of length Li, holds for each of its kv heads
   auto listed = [&]([[maybe_unused]] int i, int Li) {
     const int n = blocks_of(Li, mb);
-    if constexpr (LIST == kPrefix) return n ? n - shared_blocks(a, i, Li) : 0;
+    if constexpr (LIST == kPrefix) return n ? n - shared_of(a, grp_cu, grp_nb, i, Li).blocks : 0;
     else return LIST == kSelected ? min(n, a.max_sel) : n;
   };
 
@@ -287,7 +308,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     int whole, last;      // one part of a pair per CTA; last to finish its pair
     int large, wide;      // the pair's key rows may need scaling: its queries are large; it was seen to need it
     int redo;             // the pair has to be gone through again, wide
-    int first;            // kPrefix: blocks that the pair's request shares, which its list leaves out
+    int first;            // kPrefix: blocks that the pair's request shares, which its list leaves out,
+    int pre_item, pre_parts, pre_q0;  // ... and the items of its group: first one, parts, the group's first request
   } sg;
   auto cta_total = [&](int v, int& before) {  // sum of v over the CTA, and over the threads before this one
     int pre = v;
@@ -314,12 +336,16 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     sg.r = -1;
     sg.large = sg.wide = sg.redo = 0;
   }
+  // kPrefix: the lists' lengths stay in shared memory between the two passes
+  [[maybe_unused]] int* lists = reinterpret_cast<int*>(sgen) + 2 * (kStagedGroups + 1);
+  const bool keep_lists = LIST == kPrefix && a.batch <= kStagedLists;
   long long total = 0, sum = 0;
   int pairs = 0, zero = 0, Li = 0, n = 0, before = 0;
   for (int base = 0; base < a.batch; base += NW * 32) {
     const int i = base + threadIdx.x;
     Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
     n = i < a.batch ? listed(i, Li) : 0;
+    if (keep_lists && i < a.batch) lists[i] = n;
     if ((Li < 0 || (long long)Li > 16LL * mb) && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
     total += sum = cta_total(n, before);
     pairs += __syncthreads_count(n > 0);
@@ -329,15 +355,28 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     if (blockIdx.x == 0)
       for (int p = threadIdx.x; p < a.n_prefix; p += NW * 32) {
         bool bad;
-        prefix::group(a.cu_requests, a.prefix_blocks, p, a.batch, mb, a.max_requests, bad);
+        prefix::group(grp_cu[p], grp_cu[p + 1], grp_nb[p], a.batch, mb, a.max_requests, bad);
         if (bad) atomicOr(a.err, kErrSeqLen);
       }
   }
+  // where part 0 of the attention of request i, head `head` of kv head hk, to its prefix is; the next part is kRows on
+  [[maybe_unused]] auto prefix_row = [&](int first_item, int parts, int q0, int i, int hk, int head) {
+    const int tq = 128 / G, t = i - q0, pair = t / (2 * tq), tile = (t - pair * 2 * tq) / tq;
+    const long long item = first_item + ((long long)pair * a.Hkv + hk) * parts;
+    return (size_t)item * prefix::kRows + 128 * tile + (t - (2 * pair + tile) * tq) * G + head;
+  };
+  // the first item and the parts of request i's group.  Groups that overlap (flagged) may lead out of the items: no part.
+  [[maybe_unused]] auto items_of = [&](const Shared& sh, int i) {
+    const int2 gi = __ldcg(a.group_items + sh.p);
+    const long long pair = (i - sh.q0) / (2 * (128 / G));
+    const bool ok = gi.x >= 0 && gi.y > 0 && gi.y <= prefix::kMaxParts && gi.x + (pair + 1) * a.Hkv * gi.y <= a.items;
+    return ok ? gi : make_int2(0, 0);
+  };
   // O (over its denominator, lse2 the log2 of that) joined with the n parts of the request's prefix, four dims; pl: their
-  // log2 denominators
-  [[maybe_unused]] auto join_prefix = [&](int n, const float* pl, const float* po, float4& O, float& lse2) {
+  // log2 denominators, `next` apart
+  [[maybe_unused]] auto join_prefix = [&](int n, const float* pl, int next, const float* po, float4& O, float& lse2) {
     float M = lse2;
-    for (int s = 0; s < n; ++s) M = fmaxf(M, pl[s]);
+    for (int s = 0; s < n; ++s) M = fmaxf(M, pl[s * next]);
     if (M == -CUDART_INF_F) return;
     float sum = exp2f(lse2 - M);
     O.x *= sum;
@@ -346,8 +385,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     O.w *= sum;
 #pragma unroll 4
     for (int s = 0; s < n; ++s) {
-      const float w = exp2f(pl[s] - M);
-      const float4 p = __ldcg(reinterpret_cast<const float4*>(po + (size_t)s * D));
+      const float w = exp2f(pl[s * next] - M);
+      const float4 p = __ldcg(reinterpret_cast<const float4*>(po + (size_t)s * (prefix::kRows * D)));
       sum += w;
       O.x = fmaf(p.x, w, O.x);
       O.y = fmaf(p.y, w, O.y);
@@ -362,19 +401,32 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + hq * D + dim) =
         make_uint2(ptx::pack_bf16(o.x, o.y), ptx::pack_bf16(o.z, o.w));
   };
+  // what a pair's request shares
+  [[maybe_unused]] auto enter = [&](int i, int Li) {
+    const Shared sh = shared_of(a, grp_cu, grp_nb, i, Li);
+    sg.first = sh.blocks;
+    sg.pre_q0 = sh.q0;
+    sg.pre_parts = 0;
+    if (sh.blocks > 0) {
+      const int2 gi = items_of(sh, i);
+      sg.pre_item = gi.x;
+      sg.pre_parts = gi.y;
+    }
+  };
   if (__syncthreads_or(zero)) {  // requests whose list is empty, shared out over the grid
     for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
       const int L = __ldg(a.seq_lens + i);
       if (listed(i, L)) continue;
       if constexpr (LIST == kPrefix) {
-        const int first = shared_blocks(a, i, L);
-        if (first > 0) {  // the request ends with its prefix
+        const Shared sh = shared_of(a, grp_cu, grp_nb, i, L);
+        if (L > 0 && sh.blocks > 0) {  // the request ends with its prefix
+          const int2 gi = items_of(sh, i);
           for (int e = threadIdx.x; e < a.Hq * (D / 4); e += NW * 32) {
-            const size_t hq = (size_t)i * a.Hq + e / (D / 4), at = hq * a.prefix_split;
-            const int dim = 4 * (e % (D / 4));
+            const int h = e / (D / 4), dim = 4 * (e % (D / 4));
+            const size_t at = prefix_row(gi.x, gi.y, sh.q0, i, h / G, h % G), hq = (size_t)i * a.Hq + h;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
             float lse2 = -CUDART_INF_F;
-            join_prefix(prefix::parts<D>(first, a.prefix_split), a.prefix_lse + at, a.prefix_o + at * D + dim, O, lse2);
+            join_prefix(gi.y, a.prefix_lse + at, prefix::kRows, a.prefix_o + at * D + dim, O, lse2);
             store4(hq, dim, O);
             if (a.lse && dim == 0) a.lse[hq] = lse2 * kLn2;
           }
@@ -395,9 +447,20 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     // keys, 8 heads: 11 us, against 12 to 13 in parts of 32 or whole) and else left whole (128 pairs of 64 blocks: 15 us
     // against 16 in halves), longer ones to 32 (8192 keys: 15.4 us against 16.3 in 16) or, above 8 heads, 64.
     const long long all_pairs = (long long)pairs * a.Hkv;
+    constexpr int kMostParts = NT == 1 ? kListMaxCtas : kListMaxCtas / 2;  // of a pair: the merge holds a weight for each
+    const long long grid = min((long long)gridDim.x, (long long)kMostParts);
     int part = total <= 64 * all_pairs ? 8 : (NT == 1 ? 32 : 64);
-    while (part <= kMinRange && total / part + all_pairs > (long long)gridDim.x) part = part == 16 ? 64 : part * 2;
-    const bool whole = part <= kMinRange;
+    while (part <= kMinRange && total / part + all_pairs > grid) part = part == 16 ? 64 : part * 2;
+    bool whole = part <= kMinRange;
+    // selected blocks and shared prefixes: also longer parts, one per CTA, where there are more CTAs than pairs: sum of
+    // ceil(blocks / part) <= total / part + pairs (against equal ranges, in which most CTAs walk two pairs or more, and
+    // join both: 64 pairs of 512 e4m3 blocks 43.2 -> 39.7 us; 256 pairs of 4 to 128 bf16 blocks behind prefixes, with
+    // those, 94 -> 70 us)
+    if (LIST != kAll && !whole && (long long)gridDim.x > all_pairs) {
+      const long long room = min((long long)kMostParts, gridDim.x - all_pairs);
+      part = (int)min((long long)(1 << 27), max((long long)kMinRange, (total + room - 1) / room));
+      whole = true;
+    }
     // else equal ranges of the list, of at least kMinRange blocks, but no fewer of them than pairs
     const long long want = max((total + kMinRange - 1) / kMinRange, all_pairs);
     const long long n_cta = max(1LL, min((long long)gridDim.x, want));  // 1: no request has a key
@@ -409,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       const int i = base + threadIdx.x;
       if (a.batch > NW * 32) {  // else the one pass above still holds them
         Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
-        n = i < a.batch ? listed(i, Li) : 0;
+        n = i < a.batch ? (keep_lists ? lists[i] : listed(i, Li)) : 0;
       }
       const int units = whole ? (n + part - 1) / part : n;
       if (a.batch > NW * 32 || whole) sum = cta_total(units, before);
@@ -420,7 +483,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         sg.hk = (int)((x0 - at) / units);
         sg.nblk = n;
         sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
-        sg.first = LIST == kPrefix ? blocks_of(Li, mb) - n : 0;
+        if constexpr (LIST == kPrefix) enter(i, Li);
         sg.whole = whole;
         if (whole) {
           sg.b_begin = (int)((long long)k * n / units);
@@ -946,12 +1009,14 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       }
     const int r = sg.r, hk = sg.hk, b_begin = sg.b_begin, nblk = sg.nblk, b_end = b0;
     // kPrefix: log2 denominators of the prefix's parts, behind what the merge overlays
-    [[maybe_unused]] const int n_pre = LIST == kPrefix && sg.first > 0 ? prefix::parts<D>(sg.first, a.prefix_split) : 0;
+    [[maybe_unused]] const int n_pre = LIST == kPrefix ? sg.pre_parts : 0;
     [[maybe_unused]] float* pre_lse = reinterpret_cast<float*>(sgen + LY::MERGE);
-    [[maybe_unused]] const size_t pre_at = ((size_t)r * a.Hq + (size_t)hk * G) * a.prefix_split;  // + head * prefix_split + part
-    if constexpr (LIST == kPrefix)
+    [[maybe_unused]] size_t pre_at = 0;  // head 0, part 0; heads are 1 apart, parts kRows
+    if constexpr (LIST == kPrefix) {
+      if (n_pre > 0) pre_at = prefix_row(sg.pre_item, n_pre, sg.pre_q0, r, hk, 0);
       for (int i = threadIdx.x; i < G * n_pre; i += NW * 32)
-        pre_lse[i] = __ldcg(a.prefix_lse + pre_at + (size_t)(i / n_pre) * a.prefix_split + i % n_pre);
+        pre_lse[i] = __ldcg(a.prefix_lse + pre_at + i / n_pre + (size_t)(i % n_pre) * prefix::kRows);
+    }
 
     // per-warp state: ms[16], l[16], mt[16], O[16][OST], by column
     {
@@ -1000,8 +1065,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
         O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
         float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
-        join_prefix(n_pre, pre_lse + head * n_pre, a.prefix_o + (pre_at + (size_t)head * a.prefix_split) * D + dim, O,
-                    lse2);
+        join_prefix(n_pre, pre_lse + head * n_pre, 1, a.prefix_o + (pre_at + head) * D + dim, O, lse2);
         const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
         store4(hq, dim, O);
         if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
@@ -1066,7 +1130,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         const int n_list = c2 - c1 + 1, n_part = n_list + n_pre;
         float* wt = reinterpret_cast<float*>(sgen);  // [part][G], over what the stages held
         auto slot = [&](int c) { return (size_t)(2 * (c1 + c) + (c == 0)) * G; };
-        [[maybe_unused]] auto pslot = [&](int c, int head) { return pre_at + (size_t)head * a.prefix_split + (c - n_list); };
+        [[maybe_unused]] auto pslot = [&](int c, int head) { return pre_at + head + (size_t)(c - n_list) * prefix::kRows; };
         for (int i = threadIdx.x; i < n_part * G; i += NW * 32) {
           const int c = i / G, head = i % G;
           if (LIST != kPrefix || c < n_list) wt[i] = __ldcg(a.part_ml + slot(c) + head);
@@ -1121,6 +1185,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     if (left <= 0) break;
     __syncthreads();  // the pair has been read
     if (threadIdx.x == 0) {
+      grp_cu = a.cu_requests;  // the staged groups are gone
+      grp_nb = a.prefix_blocks;
       sg.left = left;
       sg.wide = 0;
       sg.b_begin = 0;
@@ -1136,7 +1202,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         sg.r = min(i, a.batch - 1);
         sg.nblk = n;
         sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
-        sg.first = LIST == kPrefix ? blocks_of(Li, mb) - n : 0;
+        if constexpr (LIST == kPrefix) enter(i, Li);
       }
     }
     __syncthreads();

@@ -43,9 +43,11 @@ struct DecodeArgs {
   // shared prefixes (null: none), whose part of the attention a kernel before has computed
   const int32_t* cu_requests;    // [n_prefix + 1]
   const int32_t* prefix_blocks;  // [n_prefix]
-  int n_prefix, max_requests, prefix_split;
-  const float* prefix_o;         // [B][Hq][prefix_split][D]
-  const float* prefix_lse;       // [B][Hq][prefix_split] log2
+  int n_prefix, max_requests;
+  const int2* group_items;       // [n_prefix] first item and parts (written for groups that share something)
+  long long items;               // that the partial results have room for
+  const float* prefix_o;         // [items][256][D]
+  const float* prefix_lse;       // [items][256] log2
 };
 
 // Arguments of one prefill launch.
@@ -69,9 +71,10 @@ struct PrefillArgs {
   // shared prefixes (launch_prefix): a query row is a request, total_q the requests of the batch, `batch` the groups,
   // cu_q_lens their requests, kv_lens and the tables those of the requests, max_q_len a bound of a group's requests
   const int32_t* prefix_blocks;  // [batch]
-  int n_split;                   // parts of a prefix
-  float* part_o;                 // [total_q][Hq][n_split][D], divided by the part's denominator
-  float* part_lse;               // [total_q][Hq][n_split] log2 of it
+  int n_slots, max_waves;        // items that run at once, and in how many waves at most the prefixes are cut
+  int2* group_items;             // [batch] a group's first item and parts, written here
+  float* part_o;                 // [items][256][D], divided by the part's denominator
+  float* part_lse;               // [items][256] log2 of it
 };
 
 // Error bits (mirror MINIPIC_DEVERR_* of the public header).
@@ -97,6 +100,8 @@ DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs,
 // CTAs (of kListWarps warps), each with two partial results.
 constexpr int kListWarps = 4, kListMaxCtas = 4 * 160;
 DecodePlan plan_decode_list(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
+// The same for selected blocks and for what is left of a batch with shared prefixes: lists that may be short.
+DecodePlan plan_decode_lists(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan, cudaStream_t s);
 cudaError_t launch_decode_simt(const DecodeArgs& a, bool bf16, bool rotate, cudaStream_t s);
@@ -126,8 +131,9 @@ cudaError_t launch_prefill_pair(const PrefillArgs& a, bool rotate, cudaStream_t 
 cudaError_t launch_prefill_rotated(const PrefillArgs& a, cudaStream_t s);
 cudaError_t launch_prefill_pair_rotated(const PrefillArgs& a, cudaStream_t s);
 // The attention of groups of requests to the prefix they share, into partial results (bf16).
-cudaError_t launch_prefix(const PrefillArgs& a, cudaStream_t s);
-cudaError_t launch_prefix_pair(const PrefillArgs& a, cudaStream_t s);
+// items: their number, at most.
+cudaError_t launch_prefix(const PrefillArgs& a, long long items, cudaStream_t s);
+cudaError_t launch_prefix_pair(const PrefillArgs& a, long long items, cudaStream_t s);
 // One grid of prefill tiles followed by decode splits (both with rotation).
 cudaError_t launch_mixed(const PrefillArgs& p, const DecodeArgs& d, cudaStream_t s);
 // Head dim 128: one grid of CTA-pair prefill clusters and decode clusters.

@@ -125,15 +125,15 @@ __device__ __forceinline__ void rot_pack(U4& x, U4& y, const uint64_t (&c2)[4], 
 // One CTA computes query-tile pair `pair` of request r and kv head hk and
 // loads every K~/V box it reads itself.  vmap_p is the block view of the V pool
 // (make_pool_block_map).  With ROPE and not KROT the pool holds the keys rotated
-// already, in fp16.  PREFIX: r is a group of requests that share their first
-// blocks, one query row each; every row sees every key of part `split` of those
+// already, in fp16.  PREFIX: an item of a group of requests that share their first
+// blocks, one query row each; every row sees every key of the item's part of those
 // blocks, and the result goes to the partial results of the decode that joins it
 // with each request's other keys (decode_list.cuh).
 template <int D, bool ROPE, int NB = kNB, int NSK = kNSK, int NSV = kNSV, bool KROT = ROPE, bool PREFIX = false>
 __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CUtensorMap* vmap_p,
                                              const PrefillLaunch2& L, const int pair, const int n_pairs,
                                              const int hk, const int r, uint8_t* smem_raw,
-                                             [[maybe_unused]] const int split = 0) {
+                                             [[maybe_unused]] const prefix::Item* item = nullptr) {
   static_assert(!PREFIX || NB == prefix::kTileBlocks<D>, "the parts of a prefix are whole tiles");
   using G_ = PG2<D, NB, NSK, NSV>;
   constexpr int BN = G_::BN;
@@ -154,16 +154,13 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
   int q0, ql, kvl, t_first = 0, t_end = 0;  // PREFIX: key tiles t_first .. t_end - 1
   int trow = r;                             // row of the tables
   if constexpr (PREFIX) {
-    bool bad;
-    const prefix::Group gr = prefix::group(a.cu_q_lens, a.prefix_blocks, r, a.total_q, mb, a.max_q_len, bad);
-    if (gr.blocks == 0 || tok0 >= gr.n) return;
-    q0 = gr.q0;
-    ql = gr.n;
-    kvl = 16 * gr.blocks;
-    const int tiles = prefix::tiles<D>(gr.blocks), parts = prefix::parts<D>(gr.blocks, a.n_split);
-    if (split >= parts) return;
-    t_first = (int)((long long)split * tiles / parts);
-    t_end = (int)((long long)(split + 1) * tiles / parts);
+    q0 = item->g.q0;
+    ql = item->g.n;
+    kvl = 16 * item->g.blocks;
+    const int tiles = (item->g.blocks + NB - 1) / NB;  // at least as many as parts
+    t_first = (int)((long long)item->part * tiles / item->parts);
+    t_end = (int)((long long)(item->part + 1) * tiles / item->parts);
+    if (tid == 0 && item->index == item->first) a.group_items[item->p] = make_int2((int)item->first, item->parts);
     // the first request that holds the whole prefix; every warp looks for itself
     trow = -1;
     for (int i = 0; i < ql && trow < 0; i += 32) {
@@ -662,7 +659,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
     umma::fence_after_sync();
     const int hq = hk * G + rh;
     __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(q0 + tq) * a.Hq + hq) * D;
-    [[maybe_unused]] const size_t pi = PREFIX ? ((size_t)(q0 + tq) * a.Hq + hq) * a.n_split + split : 0;
+    [[maybe_unused]] const size_t pi = PREFIX ? (size_t)item->index * prefix::kRows + 128 * i + row : 0;
     const bool any = PREFIX ? l_run != 0.f : l_run > 0.f;  // PREFIX: a NaN sum stays one
     const float inv = any ? 1.f / l_run : 0.f;
 #pragma unroll

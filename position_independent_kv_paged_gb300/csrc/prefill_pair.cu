@@ -181,14 +181,14 @@ __device__ __forceinline__ void regs_dec() {
 // head hk (both CTAs of a cluster call it with the same item).  With ROPE and
 // not KROT the pool holds the keys rotated already, in fp16: the query is
 // prepared as with rotation and the key tiles go to the product as they arrive.
-// PREFIX: r is a group of requests that share their first blocks, one query row
-// each instead of a chunk; every row sees every key of part `split` of those
+// PREFIX: an item of a group of requests that share their first blocks, one query
+// row each instead of a chunk; every row sees every key of the item's part of those
 // blocks, and the result goes to the partial results of the decode that joins it
 // with each request's other keys (decode_list.cuh).
 template <bool ROPE, int NSK, int NSV, bool KROT = ROPE, bool PREFIX = false>
 __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensorMap& vmap, const PairLaunch& L,
                                          const int pair, const int hk, const int r, uint8_t* smem_raw,
-                                         [[maybe_unused]] const int split = 0) {
+                                         [[maybe_unused]] const prefix::Item* item = nullptr) {
   using P_ = PP<NSK, NSV>;
   const PrefillArgs& a = L.a;
   const uint32_t sbase = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -209,23 +209,21 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
   int q0, ql, kvl = 0, t_first = 0, t_end = 0;  // PREFIX: key tiles t_first .. t_end - 1
   int trow = r;                                  // row of the tables
   if constexpr (PREFIX) {
-    bool bad;
-    const prefix::Group gr = prefix::group(a.cu_q_lens, a.prefix_blocks, r, a.total_q, mb, a.max_q_len, bad);
-    if (gr.blocks == 0 || 2 * pair * TQ >= gr.n) return;  // decided alike in both CTAs of the pair
-    q0 = gr.q0;
-    ql = gr.n;
-    kvl = 16 * gr.blocks;
-    const int tiles = prefix::tiles<D>(gr.blocks), parts = prefix::parts<D>(gr.blocks, a.n_split);
-    if (split >= parts) return;
-    t_first = (int)((long long)split * tiles / parts);
-    t_end = (int)((long long)(split + 1) * tiles / parts);
+    q0 = item->g.q0;
+    ql = item->g.n;
+    kvl = 16 * item->g.blocks;
+    const int tiles = (item->g.blocks + kTileBlocks - 1) / kTileBlocks;  // at least as many as parts
+    t_first = (int)((long long)item->part * tiles / item->parts);
+    t_end = (int)((long long)(item->part + 1) * tiles / item->parts);
+    if (tid == 0 && crank == 0 && item->index == item->first)
+      a.group_items[item->p] = make_int2((int)item->first, item->parts);
     // the first request that holds the whole prefix; every warp looks for itself
     trow = -1;
     for (int i = 0; i < ql && trow < 0; i += 32) {
       const unsigned has = __ballot_sync(FULL, i + lane < ql && __ldg(a.kv_lens + q0 + min(i + lane, ql - 1)) >= kvl);
       if (has) trow = q0 + i + __ffs(has) - 1;
     }
-    if (trow < 0) return;
+    if (trow < 0) return;  // decided alike in both CTAs of the pair
   } else {
     q0 = a.cu_q_lens[r];
     ql = a.cu_q_lens[r + 1] - q0;
@@ -776,7 +774,7 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
     umma::fence_after_sync();
     const int hq = hk * G + rh;
     __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.out) + ((size_t)(q0 + tq) * a.Hq + hq) * D + 64 * h;
-    [[maybe_unused]] const size_t pi = PREFIX ? ((size_t)(q0 + tq) * a.Hq + hq) * a.n_split + split : 0;
+    [[maybe_unused]] const size_t pi = PREFIX ? (size_t)item->index * prefix::kRows + 128 * crank + row : 0;
     const bool any = PREFIX ? l_tot != 0.f : l_tot > 0.f;  // PREFIX: a NaN sum stays one
     const float inv = any ? 1.f / l_tot : 0.f;
 #pragma unroll
@@ -834,13 +832,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  smem_raw);
 }
 
-// Grid: 2 x query-tile pairs, kv head x part, group.
+// Grid: two CTAs an item.
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_pair_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                       const PairLaunch L) {
+                       const __grid_constant__ PairLaunch L) {
   extern __shared__ uint8_t smem_raw[];
-  pair_cta<true, kNSK, kNSV, true, true>(kmap, vmap, L, (int)(blockIdx.x >> 1), (int)(blockIdx.y % L.a.Hkv), blockIdx.z,
-                                         smem_raw, (int)(blockIdx.y / L.a.Hkv));
+  prefix::Item it;
+  if (!prefix::find_item<D>(L.a, L.tq, blockIdx.x >> 1, it)) return;
+  pair_cta<true, kNSK, kNSV, true, true>(kmap, vmap, L, it.pair, it.head, it.p, smem_raw, &it);
 }
 
 // Mixed continuous batch in one launch (the device side of interleaved
@@ -926,21 +925,19 @@ cudaError_t launch_mixed_t(const PrefillArgs& p, const DecodeArgs& d, cudaStream
   return cudaLaunchKernelEx(&cfg, mixed_pair_kernel<NT>, km, vm, kb, vb, L, d, (int)n_pre, (int)n_dec);
 }
 
-using PairKernel = void (*)(const CUtensorMap, const CUtensorMap, const PairLaunch);
-
-// kernel<<<(2 x pairs, gy, gz), clusters of two>>>
-cudaError_t launch_pairs(PairKernel kernel, bool (&done)[64], const PrefillArgs& a, int gy, int gz, cudaStream_t s) {
+// kernel<<<grid, clusters of two>>>
+template <typename K>
+cudaError_t launch_pairs(K kernel, bool (&done)[64], const PairLaunch& L, dim3 grid, cudaStream_t s) {
   using P_ = PP<kNSK, kNSV>;
+  const PrefillArgs& a = L.a;
   const int smem = P_::TOTAL + 1024;
   cudaError_t e = set_smem_once(kernel, smem, done);
   if (e != cudaSuccess) return e;
   CUtensorMap km, vm;
   const long long rows = (long long)a.num_blocks * a.Hkv * 16;
   if (!make_pool_map(&km, a.k_pool, rows, D) || !make_pool_map(&vm, a.v_pool, rows, D)) return cudaErrorInvalidValue;
-  PairLaunch L{a, 128 / a.G, 0};
-  L.n_pairs = (a.max_q_len + 2 * L.tq - 1) / (2 * L.tq);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * L.n_pairs), (unsigned)gy, (unsigned)gz);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = s;
@@ -957,7 +954,10 @@ cudaError_t launch_pairs(PairKernel kernel, bool (&done)[64], const PrefillArgs&
 template <bool ROPE, bool KROT = ROPE>
 cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
   static bool done[64] = {false};
-  return launch_pairs(prefill_pair_kernel<ROPE, kNSK, kNSV, KROT>, done, a, a.Hkv, a.batch, s);
+  PairLaunch L{a, 128 / a.G, 0};
+  L.n_pairs = (a.max_q_len + 2 * L.tq - 1) / (2 * L.tq);
+  return launch_pairs(prefill_pair_kernel<ROPE, kNSK, kNSV, KROT>, done, L,
+                      dim3((unsigned)(2 * L.n_pairs), (unsigned)a.Hkv, (unsigned)a.batch), s);
 }
 
 }  // namespace
@@ -971,10 +971,10 @@ cudaError_t launch_prefill_pair_rotated(const PrefillArgs& a, cudaStream_t s) {
   return a.D == D ? launch_t<true, false>(a, s) : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_prefix_pair(const PrefillArgs& a, cudaStream_t s) {
-  if (a.D != D) return cudaErrorInvalidValue;
+cudaError_t launch_prefix_pair(const PrefillArgs& a, long long items, cudaStream_t s) {
+  if (a.D != D || items > 0x3fffffffLL) return cudaErrorInvalidValue;
   static bool done[64] = {false};
-  return launch_pairs(prefix_pair_kernel, done, a, a.Hkv * a.n_split, a.batch, s);
+  return launch_pairs(prefix_pair_kernel, done, PairLaunch{a, 128 / a.G, 0}, dim3((unsigned)(2 * items)), s);
 }
 
 cudaError_t launch_mixed_pair(const PrefillArgs& p, const DecodeArgs& d, cudaStream_t s) {

@@ -38,20 +38,21 @@ cudaError_t launch_t(const PrefillArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Grid: query-tile pairs, kv head x part, group.
+// Grid: one CTA an item.
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                     const PrefillLaunch2 L) {
+                     const __grid_constant__ PrefillLaunch2 L) {
   extern __shared__ uint8_t smem_raw[];
-  prefill2_cta<64, true, kNB, kNSK, kNSV, true, true>(&kmap, &vmap, L, blockIdx.x, gridDim.x, blockIdx.y % L.a.Hkv,
-                                                      blockIdx.z, smem_raw, blockIdx.y / L.a.Hkv);
+  prefix::Item it;
+  if (!prefix::find_item<64>(L.a, L.tq, blockIdx.x, it)) return;
+  prefill2_cta<64, true, kNB, kNSK, kNSV, true, true>(&kmap, &vmap, L, it.pair, it.pair + 1, it.head, it.p, smem_raw, &it);
 }
 
 }  // namespace
 
-cudaError_t launch_prefix(const PrefillArgs& a, cudaStream_t s) {
-  if (a.D == 128) return launch_prefix_pair(a, s);
-  if (a.D != 64) return cudaErrorInvalidValue;
+cudaError_t launch_prefix(const PrefillArgs& a, long long items, cudaStream_t s) {
+  if (a.D == 128) return launch_prefix_pair(a, items, s);
+  if (a.D != 64 || items > 0x7fffffffLL) return cudaErrorInvalidValue;
   const int smem = PG2<64>::TOTAL + 1024;
   static bool done[64] = {false};
   cudaError_t e = set_smem_once(prefix_tc_kernel, smem, done);
@@ -60,10 +61,7 @@ cudaError_t launch_prefix(const PrefillArgs& a, cudaStream_t s) {
   const long long rows = (long long)a.num_blocks * a.Hkv * 16;
   if (!make_pool_map(&km, a.k_pool, rows, 64) || !make_pool_block_map(&vm, a.v_pool, rows, 64))
     return cudaErrorInvalidValue;
-  PrefillLaunch2 L{a, 128 / a.G};
-  const int n_pairs = (a.max_q_len + 2 * L.tq - 1) / (2 * L.tq);
-  const dim3 grid((unsigned)n_pairs, (unsigned)(a.Hkv * a.n_split), (unsigned)a.batch);
-  prefix_tc_kernel<<<grid, kThreads, smem, s>>>(km, vm, L);
+  prefix_tc_kernel<<<(unsigned)items, kThreads, smem, s>>>(km, vm, PrefillLaunch2{a, 128 / a.G});
   return cudaGetLastError();
 }
 

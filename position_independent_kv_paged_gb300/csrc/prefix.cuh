@@ -1,5 +1,5 @@
-// Shared prefixes: which blocks a group of requests shares, and how its keys are cut into parts.  The kernel that
-// computes the shared part and the one that computes the rest decide alike.
+// Shared prefixes: which blocks a group of requests shares, and how the attention to them is cut into items.  The
+// kernel that computes the shared part and the one that computes the rest decide alike what is shared.
 #pragma once
 
 #include "internal.h"
@@ -9,16 +9,23 @@ namespace prefix {
 
 // Groups of fewer requests read their keys one by one (sharing saves nothing then).
 constexpr int kMinRequests = 2;
+// Blocks of a key tile of the kernel that computes the shared part.
+template <int D>
+constexpr int kTileBlocks = D == 128 ? 10 : 6;
+// Rows of an item: two query tiles of 128 / G requests x the G heads of a kv head, each in 128 rows.
+constexpr int kRows = 256;
+// Parts of a prefix, at most (the merge of the other kernel holds a weight for each).
+constexpr int kMaxParts = 64;
+// What an item costs besides its tiles (start, query, end), in tiles.
+constexpr int kItemCost = 3;
 
 struct Group {
   int q0, n;   // requests q0 .. q0 + n - 1 of the batch
   int blocks;  // that they share (0: nothing)
 };
 
-// Group p as the tables allow it; `bad`: its numbers are outside the batch, the tables or the planning bound.
-__device__ __forceinline__ Group group(const int32_t* cu, const int32_t* blocks, int p, int batch, int max_blocks,
-                                       int max_requests, bool& bad) {
-  const int c0 = __ldg(cu + p), c1 = __ldg(cu + p + 1), nb = __ldg(blocks + p);
+// A group as the tables allow it; `bad`: its numbers are outside the batch, the tables or the planning bound.
+__device__ __forceinline__ Group group(int c0, int c1, int nb, int batch, int max_blocks, int max_requests, bool& bad) {
   bad = c0 < 0 || c1 < c0 || c1 > batch || (long long)c1 - c0 > max_requests || nb < 0 || nb > max_blocks;
   Group g;
   g.q0 = max(0, min(c0, batch));
@@ -26,21 +33,83 @@ __device__ __forceinline__ Group group(const int32_t* cu, const int32_t* blocks,
   g.blocks = g.n >= kMinRequests && g.n <= max_requests && nb > 0 && nb <= max_blocks ? nb : 0;
   return g;
 }
-
-// Blocks of a key tile of the kernel that computes the shared part.
-template <int D>
-constexpr int kTileBlocks = D == 128 ? 10 : 6;
-// Parts of a prefix, at most.
-constexpr int kMaxSplit = 64;
-
-// Key tiles of a prefix, and the parts it is cut into: n_split, or one a tile.
-template <int D>
-__device__ __forceinline__ int tiles(int blocks) {
-  return (blocks + kTileBlocks<D> - 1) / kTileBlocks<D>;
+__device__ __forceinline__ Group group(const PrefillArgs& a, int p) {
+  bool bad;
+  return group(__ldg(a.cu_q_lens + p), __ldg(a.cu_q_lens + p + 1), __ldg(a.prefix_blocks + p), a.total_q, a.max_blocks,
+               a.max_q_len, bad);
 }
+
+// One item: the rows of a pair of query tiles of a group and kv head, and part `part` of `parts` of the prefix.  Items
+// are numbered group by group, then pair, head, part; `first` is the group's first.
+struct Item {
+  int p, pair, head, part, parts;
+  long long first, index;
+  Group g;
+};
+
+// Item c of the batch (the whole warp calls; false: there are fewer).  The prefixes are cut so that the items of about
+// equal length fill `slots` places in as many waves as cost least.
 template <int D>
-__device__ __forceinline__ int parts(int blocks, int n_split) {
-  return min(n_split, tiles<D>(blocks));
+__device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
+  constexpr unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  auto tiles = [](int blocks) { return (blocks + kTileBlocks<D> - 1) / kTileBlocks<D>; };
+  auto units = [&](const Group& g) { return g.blocks ? (long long)((g.n + 2 * tq - 1) / (2 * tq)) * a.Hkv : 0LL; };
+  long long n_units = 0, work = 0;
+  int longest = 1;
+  for (int p = lane; p < a.batch; p += 32) {
+    const Group g = group(a, p);
+    n_units += units(g);
+    work += units(g) * tiles(g.blocks);
+    if (g.blocks) longest = max(longest, tiles(g.blocks));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    n_units += __shfl_xor_sync(FULL, n_units, o);
+    work += __shfl_xor_sync(FULL, work, o);
+  }
+  longest = __reduce_max_sync(FULL, longest);
+  int len = longest;  // tiles of an item, at most
+  long long least = ((n_units + a.n_slots - 1) / a.n_slots) * (longest + kItemCost);
+  for (int w = 1; w <= a.max_waves; ++w) {
+    const long long room = (long long)w * a.n_slots - n_units;  // sum of ceil(tiles / len) <= work / len + units
+    if (room <= 0) continue;
+    const int l = max((int)min((long long)longest, (work + room - 1) / room), (longest + kMaxParts - 1) / kMaxParts);
+    if ((long long)w * (l + kItemCost) < least) {
+      least = (long long)w * (l + kItemCost);
+      len = l;
+    }
+  }
+  long long before = 0;
+  for (int base = 0; base < a.batch; base += 32) {
+    Group g{0, 0, 0};
+    if (base + lane < a.batch) g = group(a, base + lane);
+    const int parts = g.blocks ? (tiles(g.blocks) + len - 1) / len : 0;
+    long long sum = units(g) * parts;  // ... of the lanes up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(FULL, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const unsigned has = __ballot_sync(FULL, c < before + sum);
+    if (has) {
+      const int l = __ffs(has) - 1;
+      it.p = base + l;
+      it.parts = __shfl_sync(FULL, parts, l);
+      it.first = before + __shfl_sync(FULL, sum - units(g) * parts, l);
+      it.index = c;
+      it.g.q0 = __shfl_sync(FULL, g.q0, l);
+      it.g.n = __shfl_sync(FULL, g.n, l);
+      it.g.blocks = __shfl_sync(FULL, g.blocks, l);
+      const long long k = c - it.first;
+      it.part = (int)(k % it.parts);
+      it.head = (int)(k / it.parts % a.Hkv);
+      it.pair = (int)(k / it.parts / a.Hkv);
+      return true;
+    }
+    before += __shfl_sync(FULL, sum, 31);
+  }
+  return false;
 }
 
 }  // namespace prefix
