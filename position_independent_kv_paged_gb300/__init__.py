@@ -925,27 +925,31 @@ def kv_evict(scores, block_tables, block_starts, seq_lens, budget: int, keep_fir
 
 
 # ---------------------------------------------------------------- selected blocks, shared prefixes
+# These calls are short on the device, so their host side counts: a step of decode makes five of them.  One pass of
+# checks per call (_args), no helper between it and the C call.
 
-def _table32(rope, d):
-    """Specs of a table for the calls that read its float32 form alone."""
+def _table32(rope):
+    """(float32 table, max_pos) for the calls that read that form alone."""
     f32 = rope.cos_sin if isinstance(rope, RopeTable) else rope
-    return "rope", f32, _torch().float32, (_sizes(f32, "rope", 2)[0], d)
+    return f32, _sizes(f32, "rope", 2)[0]
 
 
-def _means(fn, where, kv, specs, shape, cu_new_lens, kv_start, block_tables, rope, means, max_new_len, stream):
-    torch = _torch()
-    nb, hkv, _, d = shape
-    i32 = torch.int32
-    B, mb = _sizes(block_tables, "block_tables", 2)
-    _sizes(means, "means", 3)
-    code, table = _dtype_code(means), _table32(rope, d)
-    _args(("cu_new_lens", cu_new_lens, i32, (B + 1,)), ("kv_start", kv_start, i32, (B,)),
-          ("block_tables", block_tables, i32, (B, mb)), *specs, table, ("means", means, means.dtype, (nb, hkv, d)))
+def _table16(rope, bf16):
+    """(float32 table, float16 table, max_pos) for the calls that read the float32 and, for bf16, the float16 form."""
+    f32, f16 = (rope.cos_sin, rope.cos_sin_f16) if isinstance(rope, RopeTable) else (rope, None)
+    if bf16 and f16 is None:
+        raise TypeError("this call needs the RopeTable built by rope_table() (it carries the float16 table)")
+    return f32, f16, _sizes(f32, "rope", 2)[0]
+
+
+def _means(fn, where, kv, cu_new_lens, kv_start, block_tables, table, max_pos, d, means, max_new_len, stream):
+    B, mb = block_tables.shape
     if max_new_len is None:
         max_new_len = _longest(cu_new_lens, stream) if B else 0
-    ab = _Append(None, None, cu_new_lens.data_ptr(), kv_start.data_ptr(), block_tables.data_ptr(), B, int(max_new_len),
-                 int(max_new_len), mb)   # of the counts the call only asks whether there are any
-    rp = _Rope(table[1].data_ptr(), table[3][0], d, None, None)
+    n = int(max_new_len)   # of the counts the call only asks whether there are any
+    ab = _Append(None, None, cu_new_lens.data_ptr(), kv_start.data_ptr(), block_tables.data_ptr(), B, n, n, mb)
+    rp = _Rope(table.data_ptr(), max_pos, d, None, None)
+    code = _dtype_code(means)
     _check(_run(stream, lambda s: fn(code, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(ab), means.data_ptr(), s)),
            where)
 
@@ -956,25 +960,34 @@ def kv_block_means(cu_new_lens, kv_start, block_tables, k_pool, rope, means, max
     head_dim] of the pool's dtype receives the mean of each block's keys, each
     rotated by its slot.  Blocks that the append did not touch keep theirs.
     ``max_new_len`` as in ``kv_append``."""
-    L = load()
+    torch = _torch()
+    L = _lib or load()
     shape = nb, hkv, bs, d = _sizes(k_pool, "k_pool", 4)
+    B, mb = _sizes(block_tables, "block_tables", 2)
     _sizes(means, "means", 3)
-    _means(L.minipic_kv_block_means, "minipic_kv_block_means", _KV(k_pool.data_ptr(), None, nb, hkv, bs, d),
-           (("k_pool", k_pool, means.dtype, shape),), shape, cu_new_lens, kv_start, block_tables, rope, means,
-           max_new_len, stream)
+    (table, n), i32, dt = _table32(rope), torch.int32, means.dtype
+    _args(("cu_new_lens", cu_new_lens, i32, (B + 1,)), ("kv_start", kv_start, i32, (B,)),
+          ("block_tables", block_tables, i32, (B, mb)), ("k_pool", k_pool, dt, shape),
+          ("rope", table, torch.float32, (n, d)), ("means", means, dt, (nb, hkv, d)))
+    _means(L.minipic_kv_block_means, "minipic_kv_block_means", _KV(k_pool.data_ptr(), None, nb, hkv, bs, d), cu_new_lens,
+           kv_start, block_tables, table, n, d, means, max_new_len, stream)
 
 
 def kv_block_means_q8(cu_new_lens, kv_start, block_tables, k_pool, k_scale, rope, means, max_new_len=None, stream=None):
     """``kv_block_means`` over the e4m3 cache, after ``kv_append_q8``; ``means``
     float32 or bfloat16 (the dtype of the queries)."""
     torch = _torch()
-    L = load()
+    L = _lib or load()
     shape = nb, hkv, bs, d = _sizes(k_pool, "k_pool", 4)
-    _sizes(k_scale, "k_scale", 2)
+    B, mb = _sizes(block_tables, "block_tables", 2)
+    _sizes(means, "means", 3)
+    (table, n), i32, f32 = _table32(rope), torch.int32, torch.float32
+    _args(("cu_new_lens", cu_new_lens, i32, (B + 1,)), ("kv_start", kv_start, i32, (B,)),
+          ("block_tables", block_tables, i32, (B, mb)), ("k_pool", k_pool, torch.float8_e4m3fn, shape),
+          ("k_scale", k_scale, f32, (nb, hkv)), ("rope", table, f32, (n, d)), ("means", means, means.dtype, (nb, hkv, d)))
     _means(L.minipic_kv_block_means_q8, "minipic_kv_block_means_q8",
-           _KVQ8(k_pool.data_ptr(), None, k_scale.data_ptr(), None, nb, hkv, bs, d),
-           (("k_pool", k_pool, torch.float8_e4m3fn, shape), ("k_scale", k_scale, torch.float32, (nb, hkv))), shape,
-           cu_new_lens, kv_start, block_tables, rope, means, max_new_len, stream)
+           _KVQ8(k_pool.data_ptr(), None, k_scale.data_ptr(), None, nb, hkv, bs, d), cu_new_lens, kv_start, block_tables,
+           table, n, d, means, max_new_len, stream)
 
 
 def block_scores(q, means, block_tables, block_starts, seq_lens, q_pos, rope, scale: float = 0.0, out=None,
@@ -984,23 +997,21 @@ def block_scores(q, means, block_tables, block_starts, seq_lens, q_pos, rope, sc
     the mean score of the block's keys (q and ``means`` float32 or bfloat16);
     -inf past a request's length."""
     torch = _torch()
-    L = load()
+    L = _lib or load()
     B, Hq, d = _sizes(q, "q", 3)
     nb, hkv, _ = _sizes(means, "means", 3)
     mb = _sizes(block_tables, "block_tables", 2)[1]
-    code, i32, table = _dtype_code(q), torch.int32, _table32(rope, d)
-    _args(("q", q, q.dtype, (B, Hq, d)), ("means", means, q.dtype, (nb, hkv, d)),
-          ("block_tables", block_tables, i32, (B, mb)), ("block_starts", block_starts, i32, (B, mb)),
-          ("seq_lens", seq_lens, i32, (B,)), ("q_pos", q_pos, i32, (B,)), table,
-          ("out", out, torch.float32, (B, hkv, mb)))
-    rp = _Rope(table[1].data_ptr(), table[3][0], d, None, None)
+    (table, n), i32, f32, dt, code = _table32(rope), torch.int32, torch.float32, q.dtype, _dtype_code(q)
+    _args(("q", q, dt, (B, Hq, d)), ("means", means, dt, (nb, hkv, d)), ("block_tables", block_tables, i32, (B, mb)),
+          ("block_starts", block_starts, i32, (B, mb)), ("seq_lens", seq_lens, i32, (B,)), ("q_pos", q_pos, i32, (B,)),
+          ("rope", table, f32, (n, d)), ("out", out, f32, (B, hkv, mb)))
+    rp = _Rope(table.data_ptr(), n, d, None, None)
 
     def call(s):
-        o = torch.empty((B, hkv, mb), dtype=torch.float32, device=q.device) if out is None else out
+        o = torch.empty((B, hkv, mb), dtype=f32, device=q.device) if out is None else out
         sb = _Scores(q.data_ptr(), means.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(),
                      seq_lens.data_ptr(), q_pos.data_ptr(), B, mb, nb, hkv, d, o.data_ptr())
-        _check(L.minipic_block_scores(code, Hq, ctypes.byref(sb), ctypes.byref(rp), float(scale), s),
-               "minipic_block_scores")
+        _check(L.minipic_block_scores(code, Hq, ctypes.byref(sb), ctypes.byref(rp), scale, s), "minipic_block_scores")
         return o
     return _run(stream, call)
 
@@ -1012,16 +1023,14 @@ def block_select(scores, seq_lens, budget: int, keep_first: int = 1, keep_last: 
     and last ``keep_last`` and the best others by score (float32 [B,
     num_kv_heads, max_blocks]; NaN is the worst, of equal ones the lower index)."""
     torch = _torch()
-    L = load()
+    L = _lib or load()
     B, hkv, mb = shape = _sizes(scores, "scores", 3)
-    budget = int(budget)
-    _args(("scores", scores, torch.float32, shape), ("seq_lens", seq_lens, torch.int32, (B,)),
-          ("out", out, torch.int32, (B, hkv, budget)))
+    i32, budget = torch.int32, int(budget)
+    _args(("scores", scores, torch.float32, shape), ("seq_lens", seq_lens, i32, (B,)), ("out", out, i32, (B, hkv, budget)))
 
     def call(s):
-        o = torch.empty((B, hkv, max(budget, 0)), dtype=torch.int32, device=scores.device) if out is None else out
-        sb = _Select(scores.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), B, hkv, mb, budget, int(keep_first),
-                     int(keep_last))
+        o = torch.empty((B, hkv, max(budget, 0)), dtype=i32, device=scores.device) if out is None else out
+        sb = _Select(scores.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), B, hkv, mb, budget, keep_first, keep_last)
         _check(L.minipic_block_select(ctypes.byref(sb), s), "minipic_block_select")
         return o
     return _run(stream, call)
@@ -1033,58 +1042,63 @@ def attn_decode_selected_workspace_size(batch: int, num_q_heads: int, num_kv_hea
                                                                   max_selected, block_size))
 
 
-def _decode_selected(fn, where, struct, q, specs, block_tables, block_starts, seq_lens, q_pos, rope, selected, scale,
-                     out, lse, workspace, stream):
-    torch = _torch()
-    B, Hq, d = shape = _sizes(q, "q", 3)
-    mb = _sizes(block_tables, "block_tables", 2)[1]
-    S = _sizes(selected, "selected", 3)[2]
-    _, hkv, bs, kd = specs[0][3]
-    dt, code, i32 = q.dtype, _dtype_code(q), torch.int32
-    rope_specs = _rope16(rope, kd, code == BF16)
-    _args(("q", q, dt, (B, Hq, kd)), *specs, ("block_tables", block_tables, i32, (B, mb)),
-          ("block_starts", block_starts, i32, (B, mb)), ("seq_lens", seq_lens, i32, (B,)),
-          ("q_pos", q_pos, i32, (B,)), *rope_specs, ("selected", selected, i32, (B, hkv, S)),
-          ("out", out, dt, shape), ("lse", lse, torch.float32, (B, Hq)), *_any("workspace", workspace))
-    kv, rp = struct(specs), _rope16_struct(rope_specs)
-
-    def call(s):
-        o = torch.empty_like(q) if out is None else out
-        ws = workspace
-        if ws is None:
-            n = attn_decode_selected_workspace_size(B, Hq, hkv, d, S, bs)
-            ws = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
-        db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
-                     q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
-        _check(fn(code, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), float(scale), selected.data_ptr(), S,
-                  ws.data_ptr(), ws.nbytes, s), where)
-        return o, lse
-    return _run(stream, call)
-
-
 def attn_decode_selected(q, k_pool, v_pool, block_tables, block_starts, seq_lens, q_pos, rope, selected,
                          scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
     """``attn_decode`` over the selected blocks alone: kv head g of request r
     attends to blocks ``selected[r, g]`` of its table (int32 [B, num_kv_heads,
     n], as ``block_select`` writes them; -1: unused).  Returns (out, lse).  A
     workspace passed in must have been zeroed once."""
-    L = load()
-    shape = _sizes(k_pool, "k_pool", 4)
-    _sizes(q, "q", 3)
-    return _decode_selected(L.minipic_attn_decode_selected, "minipic_attn_decode_selected",
-                            lambda sp: _KV(sp[0][1].data_ptr(), sp[1][1].data_ptr(), *sp[0][3]), q,
-                            (("k_pool", k_pool, q.dtype, shape), ("v_pool", v_pool, q.dtype, shape)), block_tables,
-                            block_starts, seq_lens, q_pos, rope, selected, scale, out, lse, workspace, stream)
+    return _decode_selected(q, k_pool, v_pool, None, None, block_tables, block_starts, seq_lens, q_pos, rope, selected,
+                            scale, out, lse, workspace, stream)
 
 
 def attn_decode_selected_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, seq_lens, q_pos, rope,
                             selected, scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
     """``attn_decode_selected`` over the e4m3 cache (pools and scales as
     ``kv_append_q8`` writes them)."""
-    L = load()
-    return _decode_selected(L.minipic_attn_decode_selected_q8, "minipic_attn_decode_selected_q8", _kv_q8_struct, q,
-                            _kv_q8(k_pool, v_pool, k_scale, v_scale), block_tables, block_starts, seq_lens, q_pos,
-                            rope, selected, scale, out, lse, workspace, stream)
+    _sizes(k_scale, "k_scale", 2)
+    _sizes(v_scale, "v_scale", 2)
+    return _decode_selected(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, seq_lens, q_pos, rope,
+                            selected, scale, out, lse, workspace, stream)
+
+
+def _decode_selected(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, seq_lens, q_pos, rope, selected,
+                     scale, out, lse, workspace, stream):
+    torch = _torch()
+    L = _lib or load()
+    B, Hq, d = shape = _sizes(q, "q", 3)
+    kshape = nb, hkv, bs, kd = _sizes(k_pool, "k_pool", 4)
+    mb = _sizes(block_tables, "block_tables", 2)[1]
+    S = _sizes(selected, "selected", 3)[2]
+    q8, dt, code, i32, f32 = k_scale is not None, q.dtype, _dtype_code(q), torch.int32, torch.float32
+    table, table16, n = _table16(rope, code == BF16)
+    kdt = torch.float8_e4m3fn if q8 else dt
+    _args(("q", q, dt, (B, Hq, kd)), ("k_pool", k_pool, kdt, kshape), ("v_pool", v_pool, kdt, kshape),
+          ("k_scale", k_scale, f32, (nb, hkv)), ("v_scale", v_scale, f32, (nb, hkv)),
+          ("block_tables", block_tables, i32, (B, mb)), ("block_starts", block_starts, i32, (B, mb)),
+          ("seq_lens", seq_lens, i32, (B,)), ("q_pos", q_pos, i32, (B,)), ("rope", table, f32, (n, kd)),
+          ("rope f16", table16, torch.float16, (n, kd)), ("selected", selected, i32, (B, hkv, S)), ("out", out, dt, shape),
+          ("lse", lse, f32, (B, Hq)), *_any("workspace", workspace))
+    if q8:
+        fn, where = L.minipic_attn_decode_selected_q8, "minipic_attn_decode_selected_q8"
+        kv = _KVQ8(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, hkv, bs, kd)
+    else:
+        fn, where = L.minipic_attn_decode_selected, "minipic_attn_decode_selected"
+        kv = _KV(k_pool.data_ptr(), v_pool.data_ptr(), nb, hkv, bs, kd)
+    rp = _Rope(table.data_ptr(), n, kd, _ptr(table16), None)
+
+    def call(s):
+        o = torch.empty_like(q) if out is None else out
+        ws = workspace
+        if ws is None:
+            size = attn_decode_selected_workspace_size(B, Hq, hkv, d, S, bs)
+            ws = torch.zeros(max(size, 1), dtype=torch.uint8, device=q.device)
+        db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
+                     q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
+        _check(fn(code, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), scale, selected.data_ptr(), S,
+                  ws.data_ptr(), ws.nbytes, s), where)
+        return o, lse
+    return _run(stream, call)
 
 
 def attn_decode_prefix_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -1106,37 +1120,37 @@ def attn_decode_prefix(q, k_pool, v_pool, block_tables, block_starts, seq_lens, 
     device if None, which synchronizes).  Returns (out, lse) like
     ``attn_decode``.  A workspace passed in must have been zeroed once."""
     torch = _torch()
-    L = load()
-    kshape = _sizes(k_pool, "k_pool", 4)
-    _, hkv, bs, kd = kshape
+    L = _lib or load()
+    kshape = nb, hkv, bs, kd = _sizes(k_pool, "k_pool", 4)
     B, Hq, d = shape = _sizes(q, "q", 3)
     mb = _sizes(block_tables, "block_tables", 2)[1]
     P = _sizes(prefix_blocks, "prefix_blocks", 1)[0]
-    bf, i32 = torch.bfloat16, torch.int32
-    rope_specs = _rope16(rope, kd, True)
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    table, table16, n = _table16(rope, True)
     _args(("q", q, bf, (B, Hq, kd)), ("k_pool", k_pool, bf, kshape), ("v_pool", v_pool, bf, kshape),
           ("block_tables", block_tables, i32, (B, mb)), ("block_starts", block_starts, i32, (B, mb)),
-          ("seq_lens", seq_lens, i32, (B,)), ("q_pos", q_pos, i32, (B,)), *rope_specs,
-          ("cu_requests", cu_requests, i32, (P + 1,)), ("prefix_blocks", prefix_blocks, i32, (P,)),
-          ("out", out, bf, shape), ("lse", lse, torch.float32, (B, Hq)), *_any("workspace", workspace))
+          ("seq_lens", seq_lens, i32, (B,)), ("q_pos", q_pos, i32, (B,)), ("rope", table, f32, (n, kd)),
+          ("rope f16", table16, torch.float16, (n, kd)), ("cu_requests", cu_requests, i32, (P + 1,)),
+          ("prefix_blocks", prefix_blocks, i32, (P,)), ("out", out, bf, shape), ("lse", lse, f32, (B, Hq)),
+          *_any("workspace", workspace))
     if max_requests is None:
         max_requests = _longest(cu_requests, stream) if P else 0
     if max_prefix_blocks is None:
         with _on(stream):
             max_prefix_blocks = int(prefix_blocks.max().item()) if P else 0
-    kv, rp = _KV(k_pool.data_ptr(), v_pool.data_ptr(), *kshape), _rope16_struct(rope_specs)
-    groups = _Prefixes(cu_requests.data_ptr(), prefix_blocks.data_ptr(), P, int(max_requests), int(max_prefix_blocks))
+    kv, rp = _KV(k_pool.data_ptr(), v_pool.data_ptr(), nb, hkv, bs, kd), _Rope(table.data_ptr(), n, kd, _ptr(table16), None)
+    groups = _Prefixes(cu_requests.data_ptr(), prefix_blocks.data_ptr(), P, max_requests, max_prefix_blocks)
 
     def call(s):
         o = torch.empty_like(q) if out is None else out
         ws = workspace
         if ws is None:
-            n = attn_decode_prefix_workspace_size(B, Hq, hkv, d, mb, P, max_requests, max_prefix_blocks, bs)
-            ws = torch.zeros(max(n, 1), dtype=torch.uint8, device=q.device)
+            size = attn_decode_prefix_workspace_size(B, Hq, hkv, d, mb, P, max_requests, max_prefix_blocks, bs)
+            ws = torch.zeros(max(size, 1), dtype=torch.uint8, device=q.device)
         db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
                      q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
         _check(L.minipic_attn_decode_prefix(BF16, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db),
-                                            ctypes.byref(groups), float(scale), ws.data_ptr(), ws.nbytes, s),
+                                            ctypes.byref(groups), scale, ws.data_ptr(), ws.nbytes, s),
                "minipic_attn_decode_prefix")
         return o, lse
     return _run(stream, call)

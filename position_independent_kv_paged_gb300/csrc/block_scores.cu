@@ -10,8 +10,8 @@
 //
 // A summary is 1 / 32 of a block's keys and values, so this reads that part of what attention would, and instructions
 // bound it: widening, rotating and splitting a summary, whatever the number of query heads.  Packed fp32 arithmetic on
-// the scalar pipes took 27 us where this takes TIME1 (64 requests x 512 blocks, 4 heads a kv head), and 60 us
-// against TIME2 (8 x 8192, 8 heads): there each query head costs as much again as the products do here for eight.
+// the scalar pipes took 27 us where this takes 22 (64 requests x 512 blocks, 8 kv heads, 4 query heads each), and 60 us
+// against 42 (8 x 8192, 8 heads each): there each query head costs as much again as the products do here for eight.
 //
 // A warp takes 16 blocks (the rows of the product) through the kv heads of its CTA: the cosines and sines of the
 // blocks' starts stay in registers, and the next head's summaries load while it works on one.  A lane holds 8-element
@@ -287,17 +287,18 @@ cudaError_t launch_t(const ScoresArgs& a, int num_sms, cudaStream_t s) {
   constexpr int most_heads = 65536 / head_bytes;  // three CTAs of 64 KB an SM
   const cudaError_t e = set_smem_once(block_scores_kernel<T, D, NT>, most_heads * head_bytes, done);
   if (e != cudaSuccess) return e;
-  // Warps' steps of all heads, about four or more a resident warp: more heads a step read the starts' cosines less
-  // often, fewer even out the last wave.
-  const long long tiles = ((long long)a.max_blocks + kRows - 1) / kRows * a.batch, resident = 3LL * kWarps * num_sms;
-  long long heads_per = tiles * a.Hkv / (4 * resident);
+  // Two steps or more a resident warp in all: more heads a step read the starts' table rows less often, fewer even out
+  // the last wave (64 x 512 blocks, 8 heads: 1, 2, 4 and 8 heads a step take 31, 25, 22 and 24 us; 8 x 8192: 59, 50, 44
+  // and 42).
+  const long long steps = ((long long)a.max_blocks + kRows - 1) / kRows * a.batch, ctas = 3LL * num_sms;
+  long long heads_per = steps * a.Hkv / (2 * ctas * kWarps);
   heads_per = heads_per < 1 ? 1 : (heads_per > most_heads ? most_heads : heads_per);
   if (heads_per > a.Hkv) heads_per = a.Hkv;
   const long long gy = (a.Hkv + heads_per - 1) / heads_per;
   heads_per = (a.Hkv + gy - 1) / gy;  // as even as can be
-  long long gx = ((long long)a.max_blocks + kRows * kWarps - 1) / (kRows * kWarps);
-  const long long rows = gy * a.batch, most = (12LL * num_sms + rows - 1) / rows;
-  if (gx > most) gx = most;
+  // one wave of CTAs that walk their request, where that leaves each request several; else a step a warp
+  const long long most = ((long long)a.max_blocks + kRows * kWarps - 1) / (kRows * kWarps), wave = ctas / (gy * a.batch);
+  const long long gx = wave >= 8 && wave < most ? wave : most;
   const dim3 grid((unsigned)gx, (unsigned)gy, (unsigned)a.batch);
   block_scores_kernel<T, D, NT><<<grid, kThreads, (size_t)heads_per * head_bytes, s>>>(a, (int)heads_per);
   return cudaGetLastError();

@@ -6,10 +6,10 @@
 //
 // One CTA per (request, kv head).  Each thread keeps PER order-preserving integer images of its scores in
 // registers, in warp-contiguous rows of 32, so loads are whole lines and ballots give the order.  The threshold, the
-// image of the last candidate that stays, is built bit by bit from the top: the candidates at or above the trial
-// image are counted, and the bit stays where enough are.  A pass is PER comparisons, one warp reduction and one
-// barrier; it ends early when the count is met exactly, which scores of many bits do after about two thirds of them.  No
-// histogram: scores lie in few exponents, whose atomics would queue.
+// image of the last candidate that stays, is built from the top, two bits a pass: the candidates at or above each of
+// three trial images are counted, and the largest that enough reach stays.  A pass is 3 PER comparisons, three warp
+// sums (two of them in one word) and a barrier; it ends early when the count is met exactly, which scores of many bits do
+// after about two thirds of them.  No histogram: scores lie in few exponents, whose atomics would queue.
 #include <stdint.h>
 
 #include "internal.h"
@@ -26,20 +26,34 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Sum of v over the CTA in every thread; `slots` holds two rows of NW, used in turn, so one barrier a call.
-template <int NW>
-__device__ __forceinline__ int cta_sum(int v, int (*slots)[32], int turn) {
-  const int w = __reduce_add_sync(FULL, v), lane = threadIdx.x & 31;
-  if (lane == 0) slots[turn & 1][threadIdx.x >> 5] = w;
+// Sums of three counts over the CTA in every thread; `slots` holds two rows, used in turn, so one barrier a call.
+// PACKED: counts below 2^16 over the CTA, two of them in one sum.
+template <int NW, bool PACKED>
+__device__ __forceinline__ void cta_sums(int (&c)[3], int3 (*slots)[32], int turn) {
+  const int lane = threadIdx.x & 31;
+  int3 v;
+  if (PACKED) {
+    v.x = (int)__reduce_add_sync(FULL, (unsigned)c[0] | (unsigned)c[1] << 16);
+    v.y = 0;
+  } else {
+    v.x = __reduce_add_sync(FULL, c[0]);
+    v.y = __reduce_add_sync(FULL, c[1]);
+  }
+  v.z = __reduce_add_sync(FULL, c[2]);
+  if (lane == 0) slots[turn & 1][threadIdx.x >> 5] = v;
   __syncthreads();
-  return __reduce_add_sync(FULL, lane < NW ? slots[turn & 1][lane] : 0);
+  v = lane < NW ? slots[turn & 1][lane] : make_int3(0, 0, 0);
+  const unsigned x = __reduce_add_sync(FULL, (unsigned)v.x);
+  c[0] = PACKED ? (int)(x & 0xffffu) : (int)x;
+  c[1] = PACKED ? (int)(x >> 16) : __reduce_add_sync(FULL, v.y);
+  c[2] = __reduce_add_sync(FULL, v.z);
 }
 
 // PER = 0: any number of blocks, scores read again in each pass.
 template <int T, int PER>
 __global__ void __launch_bounds__(T) block_select_kernel(const SelectArgs a) {
   constexpr int NW = T / 32;
-  __shared__ int slots[2][32];
+  __shared__ int3 slots[2][32];
   __shared__ int2 s_before[32];
   const size_t row = blockIdx.x;
   const int r = (int)(row / a.Hkv), mb = a.max_blocks, S = a.budget;
@@ -72,16 +86,21 @@ __global__ void __launch_bounds__(T) block_select_kernel(const SelectArgs a) {
   uint32_t least = 0u;
   int reach = n, turn = 0;  // images >= least
 #pragma unroll 1
-  for (int bit = 31; bit >= 0 && reach != S; --bit) {
-    const uint32_t trial = least | (1u << bit);
-    int c = 0;
+  for (int bit = 30; bit >= 0 && reach != S; bit -= 2) {
+    int c[3] = {0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < (PER ? PER : per); ++j) c += at(j) >= trial;
-    c = cta_sum<NW>(c, slots, turn++);
-    if (c >= S) {
-      least = trial;
-      reach = c;
+    for (int j = 0; j < (PER ? PER : per); ++j) {
+      const uint32_t k = at(j);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) c[i] += k >= (least | (uint32_t)(i + 1) << bit);
     }
+    cta_sums<NW, PER != 0>(c, slots, turn++);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (c[i] >= S) {  // fewer reach a larger trial
+        least = (least & ~(3u << bit)) | (uint32_t)(i + 1) << bit;
+        reach = c[i];
+      }
   }
   // images above the threshold stay, of those at it the first S - (those above)
   int above = 0, equal = 0;
@@ -116,7 +135,7 @@ cudaError_t launch_block_select(const SelectArgs& a, cudaStream_t s) {
   const int mb = a.max_blocks;
   if (mb <= 512) block_select_kernel<128, 4><<<grid, 128, 0, s>>>(a);
   else if (mb <= 2048) block_select_kernel<256, 8><<<grid, 256, 0, s>>>(a);
-  else if (mb <= 8192) block_select_kernel<512, 16><<<grid, 512, 0, s>>>(a);
+  else if (mb <= 8192) block_select_kernel<1024, 8><<<grid, 1024, 0, s>>>(a);
   else if (mb <= 32768) block_select_kernel<1024, 32><<<grid, 1024, 0, s>>>(a);
   else block_select_kernel<1024, 0><<<grid, 1024, 0, s>>>(a);
   return cudaGetLastError();
