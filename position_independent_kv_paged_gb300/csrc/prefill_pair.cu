@@ -103,7 +103,7 @@ struct PP {
   // B_KROTL: this CTA's rotation warps; B_KROT: CTA 1's relay (in CTA 0);
   // B_QRDY, B_P: both CTAs' warps; B_VFULL: both CTAs' V copies (used in CTA 0)
   static constexpr int B_QRDY = B_MASK + kMaskRing, B_KROT = B_QRDY + 1;
-  static constexpr int B_P = B_KROT + NSK, B_KROTL = B_P + 2, NBARS = B_KROTL + NSK;
+  static constexpr int B_P = B_KROT + NSK, B_KROTL = B_P + 2, B_DONE = B_KROTL + NSK, NBARS = B_DONE + 1;
   static constexpr int OFF_BAR = (OFF_FLAG + 2 * 2 * 4 * 4 + 15) / 16 * 16;
   static constexpr int OFF_TSLOT = OFF_BAR + NBARS * 8;
   static constexpr int TOTAL = OFF_TSLOT + 16;
@@ -291,6 +291,7 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
       ptx::mbar_init(bar(P_::B_P + i), 2 * kSoftWarps);
     }
     ptx::mbar_init(bar(P_::B_PV), 1);
+    ptx::mbar_init(bar(P_::B_DONE), 1);
     ptx::mbar_init(bar(P_::B_QRDY), 8);
     for (int k = 0; k < kMaskRing; ++k) ptx::mbar_init(bar(P_::B_MASK + k), 1);
     ptx::fence_barrier_init();
@@ -483,6 +484,7 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
           if (t + NSV < n_kt) umma2::commit_mc(bar(P_::B_VFREE + sv), kPair);
           if (t + 2 < n_kt) ok = qk(t + 2);  // S_(t & 1) is free once PV(t) has read P_t
         }
+        if (ok) umma2::commit_mc(bar(P_::B_DONE), kPair);  // every product
         if (!ok) atomicOr(a.err, kErrTimeout);
       }
       __syncwarp();
@@ -755,14 +757,10 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
     // ---- epilogue: O / l -> global; this warp writes head dims 64 h .. 64 h + 63
     failed = failed || pv_late;
     bool have = n_kt > 0 && !failed;
-    // wait for the last two P V products in order: a parity wait is only
-    // meaningful for the barrier's current phase or the one before it, and
-    // PV(n_kt - 2) may still be running here (PV(n_kt - 3) is known complete)
-    if (have && n_kt > 1 && !__all_sync(FULL, ptx::mbar_wait(bar(P_::B_PV), (n_kt - 2) & 1))) {
-      have = false;
-      failed = true;
-    }
-    if (have && !__all_sync(FULL, ptx::mbar_wait(bar(P_::B_PV), (n_kt - 1) & 1))) {
+    // Wait for the last P V products on a barrier of their own, completed once.  B_PV's parity would not do: a parity
+    // wait is only meaningful for the barrier's current phase or the one before it, and here PV(n_kt - 2) may still be
+    // running, or PV(n_kt - 1) may have completed as well before a warp gets here.
+    if (have && !__all_sync(FULL, ptx::mbar_wait(bar(P_::B_DONE), 0))) {
       have = false;
       failed = true;
     }
