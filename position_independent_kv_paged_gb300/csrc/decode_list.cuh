@@ -36,7 +36,9 @@
 // read one block could share both, in a list ordered by physical block; not built.
 //  - The query is scaled by a power of two per head to a largest element in
 //    [1, 2) first, so that fp16 holds it whatever its size.
-//  - bf16: P is 2^(s - ms) in bf16 and V enters as it is.
+//  - bf16: P is 2^(s - ms) in bf16 and V enters as it is.  Over selected blocks and behind prefixes P is the sum of two
+//    bf16 parts, each a product (20 of 460 instructions a block): its rounding was the largest part of the error, 2.3e-3
+//    of the output's norm with it and 1.9e-3 without, of which 1.7e-3 are the output's own rounding.
 //  - e4m3: V bytes stay unscaled in the product; the block's scale rides on P.  P is
 //    2^(s + log2 vscale - mt + 7) in fp16 with a running reference mt of its own
 //    (so blocks whose scales differ by any factor keep fp16's full precision
@@ -219,8 +221,10 @@ __device__ __forceinline__ uint32_t distance(int t, int b) {
 //
 // LIST: which of a request's blocks a pair's list holds.  kAll: all of them.  kSelected: the entries of selected[r][kv
 // head], block numbers of the request's table, the first min(blocks, max_sel) of them.  kPrefix: the blocks behind
-// the prefix that a request shares with its group; the attention to the prefix is joined with theirs in the merge.
-enum List { kAll, kSelected, kPrefix };
+// the prefix that a request shares with its group; the attention to the prefix, which the kernel before in the stream
+// computes, is joined with theirs in the merge.  kApart: the same blocks, but requests that share leave their results to
+// a third kernel, so that nothing here waits for the first.  Either starts as soon as that one's last CTAs run.
+enum List { kAll, kSelected, kPrefix, kApart };
 
 // The group of request i of length L, and the blocks it shares: the group's, if the request holds them all (else 0).  cu
 // and nb: where the groups are read.
@@ -243,6 +247,12 @@ __device__ __forceinline__ Shared shared_of(const DecodeArgs& a, const int* cu, 
 // Groups that a CTA stages in shared memory (over its stages), and lengths of lists.
 constexpr int kStagedGroups = 256, kStagedLists = 2048;
 
+// Operands of P V: the parts that P is the sum of, and column tiles of all of them.
+template <bool Q8, List LIST, int NT>
+struct PartsOfP {
+  static constexpr int PARTS = !Q8 && LIST != kAll ? 2 : 1, N = PARTS * NT;
+};
+
 template <bool Q8, int D, int NT, bool DUAL, bool WTS, int NS, int CPS, List LIST>
 __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __grid_constant__ DecodeArgs a) {
   static_assert(!DUAL || (NT == 1 && Q8), "two half groups fill one column tile");
@@ -250,6 +260,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   using LN = Lines<D, Q8>;
   constexpr int BPS = LY::BPS;
   constexpr float kHead = Q8 ? kHeadQ8 : 0.f;
+  using PT = PartsOfP<Q8, LIST, NT>;
   constexpr int NW = kWarps;
   constexpr int NH = D / 32;  // 4-dim words of x (and of y) a thread holds per key: 4 at d 128, 2 at d 64
   constexpr unsigned FULL = 0xffffffffu;
@@ -262,10 +273,16 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   const int g8 = lane >> 2, tig = lane & 3;
   const int G = a.G, mb = a.max_blocks;
 
-  // kPrefix: the groups, staged while the stages hold nothing
+  constexpr bool SHARE = LIST == kPrefix || LIST == kApart;
+  // this kernel ends after the one before: its last CTA sees to that
+  auto leave = [&] {
+    if constexpr (SHARE)
+      if (blockIdx.x == gridDim.x - 1) ptx::wait_for_primary();
+  };
+  // SHARE: the groups, staged while the stages hold nothing
   const int* grp_cu = a.cu_requests;
   const int* grp_nb = a.prefix_blocks;
-  if constexpr (LIST == kPrefix)
+  if constexpr (SHARE)
     if (a.n_prefix > 0 && a.n_prefix <= kStagedGroups) {
       int* st = reinterpret_cast<int*>(sgen);
       for (int p = threadIdx.x; p <= a.n_prefix; p += NW * 32) {
@@ -279,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   // blocks that the list of request i, of length Li, holds for each of its kv heads
   auto listed = [&]([[maybe_unused]] int i, int Li) {
     const int n = blocks_of(Li, mb);
-    if constexpr (LIST == kPrefix) return n ? n - shared_of(a, grp_cu, grp_nb, i, Li).blocks : 0;
+    if constexpr (SHARE) return n ? n - shared_of(a, grp_cu, grp_nb, i, Li).blocks : 0;
     else return LIST == kSelected ? min(n, a.max_sel) : n;
   };
 
@@ -308,8 +325,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     int whole, last;      // one part of a pair per CTA; last to finish its pair
     int large, wide;      // the pair's key rows may need scaling: its queries are large; it was seen to need it
     int redo;             // the pair has to be gone through again, wide
-    int first;            // kPrefix: blocks that the pair's request shares, which its list leaves out,
-    int pre_item, pre_parts, pre_q0;  // ... and the items of its group: first one, parts, the group's first request
+    int first;            // SHARE: blocks that the pair's request shares, which its list leaves out,
+    int pre_p, pre_q0;    // ... its group, and the group's first request
   } sg;
   auto cta_total = [&](int v, int& before) {  // sum of v over the CTA, and over the threads before this one
     int pre = v;
@@ -336,9 +353,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     sg.r = -1;
     sg.large = sg.wide = sg.redo = 0;
   }
-  // kPrefix: the lists' lengths stay in shared memory between the two passes
+  // SHARE: the lists' lengths stay in shared memory between the two passes
   [[maybe_unused]] int* lists = reinterpret_cast<int*>(sgen) + 2 * (kStagedGroups + 1);
-  const bool keep_lists = LIST == kPrefix && a.batch <= kStagedLists;
+  const bool keep_lists = SHARE && a.batch <= kStagedLists;
   long long total = 0, sum = 0;
   int pairs = 0, zero = 0, Li = 0, n = 0, before = 0;
   for (int base = 0; base < a.batch; base += NW * 32) {
@@ -351,7 +368,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     pairs += __syncthreads_count(n > 0);
     zero |= i < a.batch && n == 0 && i % gridDim.x == blockIdx.x;
   }
-  if constexpr (LIST == kPrefix) {
+  if constexpr (SHARE) {
     if (blockIdx.x == 0)
       for (int p = threadIdx.x; p < a.n_prefix; p += NW * 32) {
         bool bad;
@@ -359,19 +376,6 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         if (bad) atomicOr(a.err, kErrSeqLen);
       }
   }
-  // where part 0 of the attention of request i, head `head` of kv head hk, to its prefix is; the next part is kRows on
-  [[maybe_unused]] auto prefix_row = [&](int first_item, int parts, int q0, int i, int hk, int head) {
-    const int tq = 128 / G, t = i - q0, pair = t / (2 * tq), tile = (t - pair * 2 * tq) / tq;
-    const long long item = first_item + ((long long)pair * a.Hkv + hk) * parts;
-    return (size_t)item * prefix::kRows + 128 * tile + (t - (2 * pair + tile) * tq) * G + head;
-  };
-  // the first item and the parts of request i's group.  Groups that overlap (flagged) may lead out of the items: no part.
-  [[maybe_unused]] auto items_of = [&](const Shared& sh, int i) {
-    const int2 gi = __ldcg(a.group_items + sh.p);
-    const long long pair = (i - sh.q0) / (2 * (128 / G));
-    const bool ok = gi.x >= 0 && gi.y > 0 && gi.y <= prefix::kMaxParts && gi.x + (pair + 1) * a.Hkv * gi.y <= a.items;
-    return ok ? gi : make_int2(0, 0);
-  };
   // O (over its denominator, lse2 the log2 of that) joined with the n parts of the request's prefix, four dims; pl: their
   // log2 denominators, `next` apart
   [[maybe_unused]] auto join_prefix = [&](int n, const float* pl, int next, const float* po, float4& O, float& lse2) {
@@ -397,7 +401,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
     lse2 = M + log2f(sum);
   };
-  [[maybe_unused]] auto store4 = [&](size_t hq, int dim, const float4& o) {
+  auto store4 = [&](size_t hq, int dim, const float4& o) {
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + hq * D + dim) =
         make_uint2(ptx::pack_bf16(o.x, o.y), ptx::pack_bf16(o.z, o.w));
   };
@@ -406,24 +410,25 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     const Shared sh = shared_of(a, grp_cu, grp_nb, i, Li);
     sg.first = sh.blocks;
     sg.pre_q0 = sh.q0;
-    sg.pre_parts = 0;
-    if (sh.blocks > 0) {
-      const int2 gi = items_of(sh, i);
-      sg.pre_item = gi.x;
-      sg.pre_parts = gi.y;
-    }
+    sg.pre_p = sh.p;
   };
   if (__syncthreads_or(zero)) {  // requests whose list is empty, shared out over the grid
     for (int i = blockIdx.x; i < a.batch; i += gridDim.x) {
       const int L = __ldg(a.seq_lens + i);
       if (listed(i, L)) continue;
-      if constexpr (LIST == kPrefix) {
+      if constexpr (SHARE) {
         const Shared sh = shared_of(a, grp_cu, grp_nb, i, L);
+        if (LIST == kApart && L > 0 && sh.blocks > 0) {
+          for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32) a.own_o[(size_t)i * a.Hq * D + e] = 0.f;
+          for (int e = threadIdx.x; e < a.Hq; e += NW * 32) a.own_lse[(size_t)i * a.Hq + e] = -CUDART_INF_F;
+          continue;
+        }
         if (L > 0 && sh.blocks > 0) {  // the request ends with its prefix
-          const int2 gi = items_of(sh, i);
+          ptx::wait_for_primary();
+          const int2 gi = prefix::items_of(a, sh.p, sh.q0, i);
           for (int e = threadIdx.x; e < a.Hq * (D / 4); e += NW * 32) {
             const int h = e / (D / 4), dim = 4 * (e % (D / 4));
-            const size_t at = prefix_row(gi.x, gi.y, sh.q0, i, h / G, h % G), hq = (size_t)i * a.Hq + h;
+            const size_t at = prefix::row_of(a, gi, sh.q0, i, h / G, h % G), hq = (size_t)i * a.Hq + h;
             float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
             float lse2 = -CUDART_INF_F;
             join_prefix(gi.y, a.prefix_lse + at, prefix::kRows, a.prefix_o + at * D + dim, O, lse2);
@@ -464,7 +469,10 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     // else equal ranges of the list, of at least kMinRange blocks, but no fewer of them than pairs
     const long long want = max((total + kMinRange - 1) / kMinRange, all_pairs);
     const long long n_cta = max(1LL, min((long long)gridDim.x, want));  // 1: no request has a key
-    if (blockIdx.x >= n_cta && !whole) return;
+    if (blockIdx.x >= n_cta && !whole) {
+      leave();
+      return;
+    }
     const long long x0 = whole ? blockIdx.x : blockIdx.x * total / n_cta;
     const long long x1 = (blockIdx.x + 1) * total / n_cta;
     long long first = 0;  // blocks or parts (of one kv head) of the requests before `base`
@@ -483,7 +491,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         sg.hk = (int)((x0 - at) / units);
         sg.nblk = n;
         sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
-        if constexpr (LIST == kPrefix) enter(i, Li);
+        if constexpr (SHARE) enter(i, Li);
         sg.whole = whole;
         if (whole) {
           sg.b_begin = (int)((long long)k * n / units);
@@ -503,7 +511,10 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       if (first * a.Hkv > x0) break;
     }
     __syncthreads();
-    if (sg.r < 0) return;  // more CTAs than parts
+    if (sg.r < 0) {  // more CTAs than parts
+      leave();
+      return;
+    }
   }
   constexpr float kFactor = 8192.f / D;
   int b0 = 0, span = 0, n_stage = 0;             // the chunk's first block, blocks, stages of this warp
@@ -548,7 +559,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   auto start_chunk = [&](bool first) {
     const int r = sg.r, hk = sg.hk;
     int tq = __ldg(a.q_pos + r);
-    const int at0 = LIST == kSelected ? 0 : b0 + (LIST == kPrefix ? sg.first : 0);  // the chunk's place in the tables
+    const int at0 = LIST == kSelected ? 0 : b0 + (SHARE ? sg.first : 0);  // the chunk's place in the tables
     const int* bt = a.block_tables + (size_t)r * mb + at0;
     const int* bs = a.block_starts + (size_t)r * mb + at0;
     // selected blocks: the list holds their numbers; one outside the request's blocks has no table entry
@@ -794,7 +805,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   // one step of the online softmax over 16 keys; m, ks and lv are those of the columns' block, wb the block
   // whose sum is recorded
   auto softmax = [&](auto plain, float (&sc)[NT][4], [[maybe_unused]] const float (&kf)[2], uint32_t m, float ks, float lv,
-                     int wb, uint32_t (&pb0)[NT], uint32_t (&pb1)[NT]) {
+                     int wb, uint32_t (&pb0)[PT::N], uint32_t (&pb1)[PT::N]) {
     const bool v0 = decltype(plain)::value || ((m >> ks0) & 1u), v1 = decltype(plain)::value || ((m >> (ks0 + 2)) & 1u);
     bool over = false;
     [[maybe_unused]] bool beyond = false;
@@ -864,14 +875,20 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         if (g8 < 2 && head < G && wb < b0 + span)
           w_base[(size_t)wb * G + head] = e == 0.f ? -CUDART_INF_F : (odd ? ms[nt][1] : ms[nt][0]) + log2f(e);
       }
-      pb0[nt] = ptx::movmatrix_trans(Q8 ? ptx::pack_f16(pv[0], pv[1]) : ptx::pack_bf16(pv[0], pv[1]));  // rows 0 .. 7
-      pb1[nt] = ptx::movmatrix_trans(Q8 ? ptx::pack_f16(pv[2], pv[3]) : ptx::pack_bf16(pv[2], pv[3]));  // 8 .. 15
+      const uint32_t p0 = Q8 ? ptx::pack_f16(pv[0], pv[1]) : ptx::pack_bf16(pv[0], pv[1]);  // rows 0 .. 7
+      const uint32_t p1 = Q8 ? ptx::pack_f16(pv[2], pv[3]) : ptx::pack_bf16(pv[2], pv[3]);  // 8 .. 15
+      pb0[nt] = ptx::movmatrix_trans(p0);
+      pb1[nt] = ptx::movmatrix_trans(p1);
+      if constexpr (PT::PARTS == 2) {
+        pb0[NT + nt] = ptx::movmatrix_trans(ptx::pack_bf16(pv[0] - ptx::bf_lo(p0), pv[1] - ptx::bf_hi(p0)));
+        pb1[NT + nt] = ptx::movmatrix_trans(ptx::pack_bf16(pv[2] - ptx::bf_lo(p1), pv[3] - ptx::bf_hi(p1)));
+      }
     }
   };
   // O^T += V^T P^T of one block
   const int v_key = Q8 ? lane & 15 : frag_slot(lane & 7) + 2 * (lane >> 4);
   const int v_chunk = Q8 ? lane >> 4 : (lane >> 3) & 1;
-  auto values = [&](auto plain, uint32_t vbase, uint32_t m, const uint32_t (&pb0)[NT], const uint32_t (&pb1)[NT]) {
+  auto values = [&](auto plain, uint32_t vbase, uint32_t m, const uint32_t (&pb0)[PT::N], const uint32_t (&pb1)[PT::N]) {
     constexpr bool part = !decltype(plain)::value;
     // which of this lane's four keys (slots 4 tig .. 4 tig + 3) count: as bytes (e4m3), or as halves (bf16: the
     // first two keys, the last two)
@@ -911,13 +928,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
           a3 &= use2;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) ptx::mma_bf16_16816(oacc[mm][nt], a0, a1, a2, a3, pb0[nt], pb1[nt]);
+        for (int nt = 0; nt < PT::N; ++nt) ptx::mma_bf16_16816(oacc[mm][nt % NT], a0, a1, a2, a3, pb0[nt], pb1[nt]);
       }
     }
   };
 
   auto pair = [&](auto plain, uint32_t kbase, uint32_t rowb, int i0, uint32_t m0, uint32_t m1) {
-    uint32_t bx[NT][2 * NH], by[NT][2 * NH], pb0[NT], pb1[NT];
+    uint32_t bx[NT][2 * NH], by[NT][2 * NH], pb0[PT::N], pb1[PT::N];
     float sc[NT][4], kf[2] = {1.f, 1.f};
     if constexpr (DUAL) {
       const int4 mc = meta[i0 + (tig >= 2 ? NW : 0)];  // of these score columns' block
@@ -1009,11 +1026,17 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       }
     const int r = sg.r, hk = sg.hk, b_begin = sg.b_begin, nblk = sg.nblk, b_end = b0;
     // kPrefix: log2 denominators of the prefix's parts, behind what the merge overlays
-    [[maybe_unused]] const int n_pre = LIST == kPrefix ? sg.pre_parts : 0;
+    int2 gi = make_int2(0, 0);  // the group's first item, parts
+    if (LIST == kPrefix && sg.first > 0) {
+      ptx::wait_for_primary();
+      gi = prefix::items_of(a, sg.pre_p, sg.pre_q0, r);
+    }
+    [[maybe_unused]] const int n_pre = gi.y;
+    [[maybe_unused]] const bool apart = LIST == kApart && sg.first > 0;
     [[maybe_unused]] float* pre_lse = reinterpret_cast<float*>(sgen + LY::MERGE);
     [[maybe_unused]] size_t pre_at = 0;  // head 0, part 0; heads are 1 apart, parts kRows
     if constexpr (LIST == kPrefix) {
-      if (n_pre > 0) pre_at = prefix_row(sg.pre_item, n_pre, sg.pre_q0, r, hk, 0);
+      if (n_pre > 0) pre_at = prefix::row_of(a, gi, sg.pre_q0, r, hk, 0);
       for (int i = threadIdx.x; i < G * n_pre; i += NW * 32)
         pre_lse[i] = __ldcg(a.prefix_lse + pre_at + i / n_pre + (size_t)(i % n_pre) * prefix::kRows);
     }
@@ -1097,7 +1120,10 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       O = Ls == 0.f ? 0.f : O / Ls * exp2f(e1) * exp2f(e - e1);
       const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
       const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
-      if (direct) {
+      if (direct && apart) {
+        a.own_o[hq * D + dim] = O;
+        if (dim == 0) a.own_lse[hq] = lse2;
+      } else if (direct) {
         static_cast<__nv_bfloat16*>(a.out)[hq * D + dim] = __float2bfloat16_rn(O);
         if (dim == 0 && a.lse) a.lse[hq] = lse2 * kLn2;
         if (WTS && dim == 0) a.w_lse[hq] = lse2;
@@ -1155,7 +1181,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
           if (lane == 0) {
             const float lse2 = Ls == 0.f ? -CUDART_INF_F : M + log2f(Ls);
             const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
-            if (a.lse) a.lse[hq] = lse2 * kLn2;
+            if (apart) a.own_lse[hq] = lse2;
+            else if (a.lse) a.lse[hq] = lse2 * kLn2;
             if (WTS) a.w_lse[hq] = lse2;
           }
         }
@@ -1175,8 +1202,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
             o.w = fmaf(p.w, w, o.w);
           }
           const size_t hq = (size_t)r * a.Hq + (size_t)hk * G + head;
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + hq * D + dim) =
-              make_uint2(ptx::pack_bf16(o.x, o.y), ptx::pack_bf16(o.z, o.w));
+          if (apart) *reinterpret_cast<float4*>(a.own_o + hq * D + dim) = o;
+          else store4(hq, dim, o);
         }
         if (threadIdx.x == 0) a.counters[(size_t)r * a.Hkv + hk] = 0;
       }
@@ -1202,12 +1229,13 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         sg.r = min(i, a.batch - 1);
         sg.nblk = n;
         sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
-        if constexpr (LIST == kPrefix) enter(i, Li);
+        if constexpr (SHARE) enter(i, Li);
       }
     }
     __syncthreads();
     if (sg.left <= 0) break;
   }
+  leave();
 }
 
 // kernel<<<...>>> with its shared memory; a.n_split CTAs.
@@ -1218,8 +1246,21 @@ cudaError_t launch_t(const DecodeArgs& a, cudaStream_t s) {
   static bool done[64] = {false};
   cudaError_t e = set_smem_once(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<a.n_split, kWarps * 32, smem, s>>>(a);
-  return cudaGetLastError();
+  if (!a.after_prefix) {
+    kernel<<<a.n_split, kWarps * 32, smem, s>>>(a);
+    return cudaGetLastError();
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.n_split);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 // Groups of up to 4 heads take two e4m3 blocks at once, of more than 8 two column tiles.

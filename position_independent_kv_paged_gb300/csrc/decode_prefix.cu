@@ -1,5 +1,5 @@
-// Decode of a batch whose requests share prefixes: the keys behind the prefixes, and the join with the attention to
-// those (the kernel is in decode_list.cuh; the shared part in prefill_pair.cu and prefill_tc.cu).
+// Decode of a batch whose requests share prefixes: the keys behind the prefixes, joined with the attention to those
+// (the kernel is in decode_list.cuh; the shared part in prefill_pair.cu and prefill_tc.cu).
 #include "decode_list.cuh"
 
 namespace minipic {

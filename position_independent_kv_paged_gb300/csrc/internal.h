@@ -48,6 +48,10 @@ struct DecodeArgs {
   long long items;               // that the partial results have room for
   const float* prefix_o;         // [items][256][D]
   const float* prefix_lse;       // [items][256] log2
+  bool after_prefix;             // the kernel before in the stream is that one: start while it ends
+  // kept apart (null: joined in the same kernel): the rest of the requests that share, over its denominator, and log2 of that
+  float* own_o;                  // [B][Hq][D]
+  float* own_lse;                // [B][Hq]
 };
 
 // Arguments of one prefill launch.
@@ -122,6 +126,8 @@ cudaError_t launch_decode_selected_q8(const DecodeArgs& a, cudaStream_t s);
 // The rest of a batch with shared prefixes, joined with the partial results of launch_prefix: bf16, tensor cores
 // (num_blocks > 0).
 cudaError_t launch_decode_prefix(const DecodeArgs& a, cudaStream_t s);
+// The same with the join in a kernel of its own (own_o set).
+cudaError_t launch_decode_apart(const DecodeArgs& a, cudaStream_t s);
 // w_raw and w_lse -> weights.
 cudaError_t launch_block_weights(const DecodeArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, bool rotate, cudaStream_t s);

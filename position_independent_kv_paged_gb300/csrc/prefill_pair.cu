@@ -835,6 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefix_pair_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const __grid_constant__ PairLaunch L) {
   extern __shared__ uint8_t smem_raw[];
+  ptx::launch_dependents();
   prefix::Item it;
   if (!prefix::find_item<D>(L.a, L.tq, blockIdx.x >> 1, it)) return;
   pair_cta<true, kNSK, kNSV, true, true>(kmap, vmap, L, it.pair, it.head, it.p, smem_raw, &it);

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ PrefillLaunch2 L) {
   extern __shared__ uint8_t smem_raw[];
+  ptx::launch_dependents();
   prefix::Item it;
   if (!prefix::find_item<64>(L.a, L.tq, blockIdx.x, it)) return;
   prefill2_cta<64, true, kNB, kNSK, kNSV, true, true>(&kmap, &vmap, L, it.pair, it.pair + 1, it.head, it.p, smem_raw, &it);

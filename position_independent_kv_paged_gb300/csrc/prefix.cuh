@@ -112,5 +112,21 @@ __device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
   return false;
 }
 
+// The first item and the parts of request i's group p, which begins at request q0 (as the kernel that computed them
+// wrote it).  Groups that overlap (flagged) may lead out of the items: no part.
+__device__ __forceinline__ int2 items_of(const DecodeArgs& a, int p, int q0, int i) {
+  const int2 gi = __ldcg(a.group_items + p);
+  const long long pair = (i - q0) / (2 * (128 / a.G));
+  const bool ok = gi.x >= 0 && gi.y > 0 && gi.y <= kMaxParts && gi.x + (pair + 1) * a.Hkv * gi.y <= a.items;
+  return ok ? gi : make_int2(0, 0);
+}
+// Row of part 0 of the attention of request i, head `head` of kv head hk, to its prefix; the next part is kRows on, the
+// next head 1.
+__device__ __forceinline__ size_t row_of(const DecodeArgs& a, int2 gi, int q0, int i, int hk, int head) {
+  const int tq = 128 / a.G, t = i - q0, pair = t / (2 * tq), tile = (t - pair * 2 * tq) / tq;
+  const long long item = gi.x + ((long long)pair * a.Hkv + hk) * gi.y;
+  return (size_t)item * kRows + 128 * tile + (t - (2 * pair + tile) * tq) * a.G + head;
+}
+
 }  // namespace prefix
 }  // namespace minipic

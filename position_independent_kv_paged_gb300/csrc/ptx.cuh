@@ -85,6 +85,10 @@ __device__ __forceinline__ bool mbar_wait_cl(uint32_t bar, uint32_t parity, uint
   }
   return true;
 }
+// Programmatic dependent launch: the next kernel of the stream may start once every CTA of this one has called this
+// (or ended); and wait, in that kernel, until this one has ended and its writes are visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Named barrier over `count` threads (a multiple of 32).
 __device__ __forceinline__ void named_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
