@@ -70,16 +70,21 @@ __device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
   }
   longest = __reduce_max_sync(FULL, longest);
   int len = longest;  // tiles of an item, at most
-  long long least = ((n_units + a.n_slots - 1) / a.n_slots) * (longest + kItemCost);
-  for (int w = 1; w <= a.max_waves; ++w) {
-    const long long room = (long long)w * a.n_slots - n_units;  // sum of ceil(tiles / len) <= work / len + units
-    if (room <= 0) continue;
-    const int l = max((int)min((long long)longest, (work + room - 1) / room), (longest + kMaxParts - 1) / kMaxParts);
-    if ((long long)w * (l + kItemCost) < least) {
-      least = (long long)w * (l + kItemCost);
-      len = l;
+  auto plan = [&](auto n_units, auto work) {
+    using I = decltype(work);
+    I least = (n_units + a.n_slots - 1) / a.n_slots * (longest + kItemCost);
+    for (int w = 1; w <= a.max_waves; ++w) {
+      if ((I)w * a.n_slots <= n_units) continue;
+      const I room = (I)w * a.n_slots - n_units;  // sum of ceil(tiles / len) <= work / len + units
+      const int l = max((int)min((I)longest, (work + room - 1) / room), (longest + kMaxParts - 1) / kMaxParts);
+      if ((I)w * (l + kItemCost) < least) {
+        least = (I)w * (l + kItemCost);
+        len = l;
+      }
     }
-  }
+  };
+  if (work < 1 << 24 && n_units < 1 << 12) plan((unsigned)n_units, (unsigned)work);  // 64-bit division is slow
+  else plan((unsigned long long)n_units, (unsigned long long)work);
   long long before = 0;
   for (int base = 0; base < a.batch; base += 32) {
     Group g{0, 0, 0};
@@ -101,7 +106,7 @@ __device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
       it.g.q0 = __shfl_sync(FULL, g.q0, l);
       it.g.n = __shfl_sync(FULL, g.n, l);
       it.g.blocks = __shfl_sync(FULL, g.blocks, l);
-      const long long k = c - it.first;
+      const unsigned k = (unsigned)(c - it.first);  // an index of the grid
       it.part = (int)(k % it.parts);
       it.head = (int)(k / it.parts % a.Hkv);
       it.pair = (int)(k / it.parts / a.Hkv);
