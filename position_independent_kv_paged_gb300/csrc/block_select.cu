@@ -8,8 +8,10 @@
 // registers, in warp-contiguous rows of 32, so loads are whole lines and ballots give the order.  The threshold, the
 // image of the last candidate that stays, is built from the top, two bits a pass: the candidates at or above each of
 // three trial images are counted, and the largest that enough reach stays.  A pass is 3 PER comparisons, three warp
-// sums (two of them in one word) and a barrier; it ends early when the count is met exactly, which scores of many bits do
-// after about two thirds of them.  No histogram: scores lie in few exponents, whose atomics would queue.
+// sums and a barrier.  When few images begin with the bits found so far (scores of many bits: after five passes of
+// sixteen) one warp takes those through the rest without barriers; it ends when the count is met exactly.  No
+// histogram: scores lie in few exponents, whose atomics would queue.  Bound by the latency of the passes: 512 rows of
+// 512 blocks take 4.9 us, 64 rows of 8192 blocks 11.7 us (their bytes: 0.2 and 0.3 us).
 #include <stdint.h>
 
 #include "internal.h"
@@ -27,27 +29,50 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
 }
 
 // Sums of three counts over the CTA in every thread; `slots` holds two rows, used in turn, so one barrier a call.
-// PACKED: counts below 2^16 over the CTA, two of them in one sum.
-template <int NW, bool PACKED>
+// PER: a warp's counts are at most 32 PER.  Warp sums are slow instructions (one a scheduler in many cycles), so where
+// the counts fit, all three share a word over the warp (10 bits each) and two do over the CTA (16 bits).
+template <int NW, int PER>
 __device__ __forceinline__ void cta_sums(int (&c)[3], int3 (*slots)[32], int turn) {
   const int lane = threadIdx.x & 31;
   int3 v;
-  if (PACKED) {
+  if (PER > 0 && 32 * PER < 1024) {
+    const unsigned x = __reduce_add_sync(FULL, (unsigned)(c[0] | c[1] << 10 | c[2] << 20));
+    v = make_int3((int)(x & 1023u) | (int)(x >> 10 & 1023u) << 16, 0, (int)(x >> 20));
+  } else if (PER > 0) {
     v.x = (int)__reduce_add_sync(FULL, (unsigned)c[0] | (unsigned)c[1] << 16);
     v.y = 0;
+    v.z = __reduce_add_sync(FULL, c[2]);
   } else {
     v.x = __reduce_add_sync(FULL, c[0]);
     v.y = __reduce_add_sync(FULL, c[1]);
+    v.z = __reduce_add_sync(FULL, c[2]);
   }
-  v.z = __reduce_add_sync(FULL, c[2]);
   if (lane == 0) slots[turn & 1][threadIdx.x >> 5] = v;
   __syncthreads();
   v = lane < NW ? slots[turn & 1][lane] : make_int3(0, 0, 0);
   const unsigned x = __reduce_add_sync(FULL, (unsigned)v.x);
-  c[0] = PACKED ? (int)(x & 0xffffu) : (int)x;
-  c[1] = PACKED ? (int)(x >> 16) : __reduce_add_sync(FULL, v.y);
+  c[0] = PER > 0 ? (int)(x & 0xffffu) : (int)x;
+  c[1] = PER > 0 ? (int)(x >> 16) : __reduce_add_sync(FULL, v.y);
   c[2] = __reduce_add_sync(FULL, v.z);
 }
+
+// Takes the largest digit that at least `want` images reach at bits `bit` and `bit` + 1 of the threshold.
+__device__ __forceinline__ void step(const int (&c)[3], int want, int bit, uint32_t& least, int& reach, int& top) {
+  const uint32_t before = least;
+  int above = c[0];
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (c[i] >= want) {  // fewer reach a larger trial
+      least = before | (uint32_t)(i + 1) << bit;
+      reach = c[i];
+      above = i < 2 ? c[i + 1 < 3 ? i + 1 : 2] : top;
+    }
+  top = above;
+}
+
+// Images that one warp finishes (rows of 512 / 8192 blocks: 4.9 / 11.7 us; with 256 of them 5.2 / 11.7, 512 7.9 / 12.1,
+// and all passes over all images 5.5 / 16.2).
+constexpr int kFew = 128;
 
 // PER = 0: any number of blocks, scores read again in each pass.
 template <int T, int PER>
@@ -55,6 +80,9 @@ __global__ void __launch_bounds__(T) block_select_kernel(const SelectArgs a) {
   constexpr int NW = T / 32;
   __shared__ int3 slots[2][32];
   __shared__ int2 s_before[32];
+  __shared__ uint32_t few[kFew];
+  __shared__ uint32_t s_least;
+  __shared__ int n_few;
   const size_t row = blockIdx.x;
   const int r = (int)(row / a.Hkv), mb = a.max_blocks, S = a.budget;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -82,11 +110,14 @@ __global__ void __launch_bounds__(T) block_select_kernel(const SelectArgs a) {
 #pragma unroll
   for (int j = 0; j < PER; ++j) key[j] = image(j);
   auto at = [&](int j) { return PER ? key[PER ? j : 0] : image(j); };
+  for (int i = threadIdx.x; i < kFew; i += T) few[i] = 0u;
+  if (threadIdx.x == 0) n_few = 0;
   // the largest threshold that at least S images reach (n > S, and held blocks are at most S)
   uint32_t least = 0u;
-  int reach = n, turn = 0;  // images >= least
+  int reach = n, top = 0, turn = 0;  // images >= least; images above those that begin with the bits of least
+  int bit = 30;
 #pragma unroll 1
-  for (int bit = 30; bit >= 0 && reach != S; bit -= 2) {
+  for (; bit >= 0 && reach != S && (reach - top > kFew || turn == 0); bit -= 2) {
     int c[3] = {0, 0, 0};
 #pragma unroll
     for (int j = 0; j < (PER ? PER : per); ++j) {
@@ -94,13 +125,38 @@ __global__ void __launch_bounds__(T) block_select_kernel(const SelectArgs a) {
 #pragma unroll
       for (int i = 0; i < 3; ++i) c[i] += k >= (least | (uint32_t)(i + 1) << bit);
     }
-    cta_sums<NW, PER != 0>(c, slots, turn++);
+    cta_sums<NW, PER>(c, slots, turn++);
+    step(c, S, bit, least, reach, top);
+  }
+  if (bit >= 0 && reach != S) {  // few images are left to choose from: one warp does
 #pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (c[i] >= S) {  // fewer reach a larger trial
-        least = (least & ~(3u << bit)) | (uint32_t)(i + 1) << bit;
-        reach = c[i];
+    for (int j = 0; j < (PER ? PER : per); ++j) {
+      const uint32_t k = at(j);
+      if (k != 0u && k - least < 4u << bit) few[atomicAdd(&n_few, 1)] = k;  // reach - top of them
+    }
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t k[kFew / 32];
+#pragma unroll
+      for (int j = 0; j < kFew / 32; ++j) k[j] = few[32 * j + lane];
+      reach -= top;
+      const int want = S - top;
+      top = 0;
+#pragma unroll 1
+      for (; bit >= 0 && reach != want; bit -= 2) {
+        int c = 0;
+#pragma unroll
+        for (int j = 0; j < kFew / 32; ++j)
+#pragma unroll
+          for (int i = 0; i < 3; ++i) c += k[j] >= (least | (uint32_t)(i + 1) << bit) ? 1 << 10 * i : 0;
+        c = (int)__reduce_add_sync(FULL, (unsigned)c);
+        const int c3[3] = {c & 1023, c >> 10 & 1023, c >> 20};
+        step(c3, want, bit, least, reach, top);
       }
+      if (lane == 0) s_least = least;
+    }
+    __syncthreads();
+    least = s_least;
   }
   // images above the threshold stay, of those at it the first S - (those above)
   int above = 0, equal = 0;
