@@ -9,9 +9,11 @@
 // are read again from the pool, so a summary is rounded once, however many calls filled the block (adding to a
 // rounded mean would round it at every step).  Sums are fp32.
 //
-// A warp per (block, kv head): D / 8 lanes hold 4 + 4 elements of a row's rotary pairs each, so 2 or 4 rows an
-// instruction; all rows are loaded before the first is used.  Rows past the block's last key are not read.  Bound by
-// memory: 16 D elements read for D written.
+// A warp per block and U kv heads: D / 8 lanes hold 4 + 4 elements of a row's rotary pairs each, so 2 or 4 rows an
+// instruction; all rows are loaded before the first is used, and the rotations serve all U heads.  Rows past the
+// block's last key are not read.  Bound by latency (counts, table entry, keys, one after another) up to a wave of
+// warps, then by memory: 16 D elements read for D written (26 MB of keys: 9.0 us with U = 2, 10.8 with
+// U = 1, whose rotations are half of what the L1 delivers, 9.4 with U = 4).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -21,7 +23,10 @@
 namespace minipic {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+// Warps of one kv head each above which a warp takes two: 16 per SM (a step of 128 requests, 1024 warps: 4.2 us with
+// one, 4.5 with two; chunks of 8320 warps: 10.8 and 9.0).
+constexpr long long kManyWarps = 16 * 152;
 constexpr unsigned FULL = 0xffffffffu;
 
 // Four consecutive elements of a row as loaded, and widened.
@@ -55,7 +60,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16(v[0], v[1]), ptx::pack_bf16(v[2], v[3]));
 }
 
-template <typename T, typename KV, int D>
+template <typename T, typename KV, int D, int U>
 __global__ void __launch_bounds__(kThreads) block_means_kernel(const MeansArgs a) {
   constexpr int LPR = D / 8;       // lanes of a row
   constexpr int RPI = 32 / LPR;    // rows of an instruction
@@ -69,12 +74,13 @@ __global__ void __launch_bounds__(kThreads) block_means_kernel(const MeansArgs a
     return;
   }
   const long long end = js + n;            // keys of the request after the append
-  const long long b0 = js >> 4, items = (((end + 15) >> 4) - b0) * a.Hkv;
+  const int per = (a.Hkv + U - 1) / U;     // warps of a block
+  const long long b0 = js >> 4, items = (((end + 15) >> 4) - b0) * per;
   const int row = lane / LPR, e0 = 4 * (lane % LPR);
   for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < items;
        i += (long long)gridDim.x * (kThreads / 32)) {
-    const long long b = b0 + i / a.Hkv;
-    const int g = (int)(i % a.Hkv);
+    const long long b = b0 + i / per;
+    const int g0 = (int)(i % per) * U;
     if (b >= a.max_blocks) {
       if (lane == 0) atomicOr(a.err, kErrSeqLen);
       continue;
@@ -85,60 +91,76 @@ __global__ void __launch_bounds__(kThreads) block_means_kernel(const MeansArgs a
       continue;
     }
     const int count = (int)min(16LL, end - 16 * b);
-    const KV* k = static_cast<const KV*>(a.k_pool) + ((size_t)phys * a.Hkv + g) * 16 * D;
-    Four<KV> x[IT], y[IT];
+    Four<KV> x[U][IT], y[U][IT];
+    float ks[U];
 #pragma unroll
-    for (int u = 0; u < IT; ++u) {
-      const int s = min(RPI * u + row, count - 1);
-      x[u].load(k + s * D + e0);
-      y[u].load(k + s * D + D / 2 + e0);
+    for (int w = 0; w < U; ++w) {
+      const size_t at = (size_t)phys * a.Hkv + min(g0 + w, a.Hkv - 1);
+      const KV* k = static_cast<const KV*>(a.k_pool) + at * 16 * D;
+      ks[w] = sizeof(KV) == 1 ? __ldg(a.k_scale + at) : 1.f;
+#pragma unroll
+      for (int u = 0; u < IT; ++u) {
+        const int s = min(RPI * u + row, count - 1);
+        x[w][u].load(k + s * D + e0);
+        y[w][u].load(k + s * D + D / 2 + e0);
+      }
     }
-    const float ks = sizeof(KV) == 1 ? __ldg(a.k_scale + (size_t)phys * a.Hkv + g) : 1.f;
-    float mx[4] = {0.f, 0.f, 0.f, 0.f}, my[4] = {0.f, 0.f, 0.f, 0.f};
+    float mx[U][4] = {}, my[U][4] = {};
 #pragma unroll
     for (int u = 0; u < IT; ++u) {
       const int s = RPI * u + row;
       if (s < count) {
         const float4 c = __ldg(reinterpret_cast<const float4*>(a.cos_sin + s * D + e0));
         const float4 n = __ldg(reinterpret_cast<const float4*>(a.cos_sin + s * D + D / 2 + e0));
-        const float4 xv = x[u].wide(), yv = y[u].wide();
-        const float xs[4] = {xv.x, xv.y, xv.z, xv.w}, ys[4] = {yv.x, yv.y, yv.z, yv.w};
         const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          mx[e] += fmaf(xs[e], cs[e], -ys[e] * sn[e]);
-          my[e] += fmaf(ys[e], cs[e], xs[e] * sn[e]);
+        for (int w = 0; w < U; ++w) {
+          const float4 xv = x[w][u].wide(), yv = y[w][u].wide();
+          const float xs[4] = {xv.x, xv.y, xv.z, xv.w}, ys[4] = {yv.x, yv.y, yv.z, yv.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            mx[w][e] += fmaf(xs[e], cs[e], -ys[e] * sn[e]);
+            my[w][e] += fmaf(ys[e], cs[e], xs[e] * sn[e]);
+          }
         }
       }
     }
-    const float f = ks / (float)count;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int w = 0; w < U; ++w) {
+      const float f = ks[w] / (float)count;
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) {
-        mx[e] += __shfl_xor_sync(FULL, mx[e], o);
-        my[e] += __shfl_xor_sync(FULL, my[e], o);
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int o = LPR; o < 32; o <<= 1) {
+          mx[w][e] += __shfl_xor_sync(FULL, mx[w][e], o);
+          my[w][e] += __shfl_xor_sync(FULL, my[w][e], o);
+        }
+        mx[w][e] *= f;
+        my[w][e] *= f;
       }
-      mx[e] *= f;
-      my[e] *= f;
-    }
-    if (row == 0) {
-      T* m = static_cast<T*>(a.means) + ((size_t)phys * a.Hkv + g) * D;
-      store4(m + e0, mx);
-      store4(m + D / 2 + e0, my);
+      if (row == 0 && g0 + w < a.Hkv) {
+        T* m = static_cast<T*>(a.means) + ((size_t)phys * a.Hkv + g0 + w) * D;
+        store4(m + e0, mx[w]);
+        store4(m + D / 2 + e0, my[w]);
+      }
     }
   }
 }
 
-template <typename T, typename KV>
-cudaError_t launch_t(const MeansArgs& a, cudaStream_t s) {
-  const long long items = ((a.max_new + 14LL) / 16 + 1) * a.Hkv;  // of a request, at most
+template <typename T, typename KV, int U>
+cudaError_t launch_u(const MeansArgs& a, cudaStream_t s) {
+  const long long items = ((a.max_new + 14LL) / 16 + 1) * ((a.Hkv + U - 1) / U);  // of a request, at most
   long long gx = (items + kThreads / 32 - 1) / (kThreads / 32);
   if (gx > 65535) gx = 65535;  // grid-stride beyond this
   const dim3 grid((unsigned)gx, (unsigned)a.batch);
-  if (a.D == 128) block_means_kernel<T, KV, 128><<<grid, kThreads, 0, s>>>(a);
-  else block_means_kernel<T, KV, 64><<<grid, kThreads, 0, s>>>(a);
+  if (a.D == 128) block_means_kernel<T, KV, 128, U><<<grid, kThreads, 0, s>>>(a);
+  else block_means_kernel<T, KV, 64, U><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
+}
+template <typename T, typename KV>
+cudaError_t launch_t(const MeansArgs& a, cudaStream_t s) {
+  const long long warps = ((a.max_new + 14LL) / 16 + 1) * a.Hkv * a.batch;
+  return warps > kManyWarps ? launch_u<T, KV, 2>(a, s) : launch_u<T, KV, 1>(a, s);
 }
 
 }  // namespace

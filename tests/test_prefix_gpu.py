@@ -239,6 +239,54 @@ def test_captured_and_on_a_side_stream(env):
     assert mp.device_error() == 0
 
 
+def test_many_requests_captured(env):
+    """A batch of many requests (its join runs as a kernel of its own) and a small one, captured over one workspace and
+    replayed in turn, with other batches in the same buffers between: requests that end, lose their prefix, or whose
+    group grows; the same bits as eager calls."""
+    torch, mp, dev = env
+    rng = np.random.default_rng(8)
+    for d, Hkv in ((128, 4), (64, 8)):
+        lens = [16 * 30 + int(x) for x in rng.integers(0, 200, 150)] + [0, 0] + [int(x) for x in rng.integers(1, 90, 148)]
+        big = groups(torch, dev, lens, [0, 100, 150], [30, 11], 2 * Hkv, Hkv, d, d)
+        small = groups(torch, dev, [700, 690, 31, 800], [0, 4], [40], 2 * Hkv, Hkv, d, d + 1)
+        rope = mp.rope_table(max(big["max_pos"], small["max_pos"]), d, big["base"], device=dev)
+        bounds = dict(max_requests=160, max_prefix_blocks=45)
+        n = max(mp.attn_decode_prefix_workspace_size(len(t["seq_lens"]), 2 * Hkv, Hkv, d, t["block_tables"].shape[1],
+                                                     len(t["blocks"]), 160, 45) for t in (big, small))
+        ws = torch.zeros(n, dtype=torch.uint8, device=dev)
+
+        def call(t, **kw):
+            return mp.attn_decode_prefix(t["q"], t["k_pool"], t["v_pool"], t["block_tables"], t["block_starts"],
+                                         t["seq_lens"], t["q_pos"], rope, t["cu"], t["blocks"], **bounds, **kw)[0]
+        graphs, outs = [], [torch.full_like(t["q"], 7.0) for t in (big, small)]
+        for t, out in zip((big, small), outs):
+            call(t, workspace=ws)
+            torch.cuda.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1]):
+                call(t, out=out, workspace=ws)
+        for step in range(4):
+            if step == 1:
+                big["seq_lens"][3] = 0
+                big["seq_lens"][7] = 16 * 30 - 5       # shorter than the prefix
+                big["q_pos"][7] = big["block_starts"][7, 29] + 11
+            if step == 2:
+                big["blocks"].copy_(i32(torch, dev, [0, 11]))
+            if step == 3:
+                big["blocks"].copy_(i32(torch, dev, [11, 11]))
+                big["cu"].copy_(i32(torch, dev, [0, 99, 99]))
+            for i in (0, 1, 0):
+                outs[i].fill_(7.0)
+                graphs[i].replay()
+            torch.cuda.synchronize()
+            assert not ws[:65536].any()
+            for t, out in zip((big, small), outs):
+                lse = torch.empty(t["q"].shape[:2], device=dev)
+                assert torch.equal(out, call(t, lse=lse)), (d, step)
+                check(env, t, (out, lse), f"d{d} step {step}")
+    assert mp.device_error() == 0
+
+
 def test_with_a_scale(env):
     torch, mp, dev = env
     for d in (64, 128):

@@ -70,6 +70,31 @@ def test_means(env, kv, dtype, Hkv, d):
     assert mp.device_error() == 0
 
 
+@pytest.mark.parametrize("kv,dtype,Hkv,d", [("f32", "f32", 3, 64), ("bf16", "bf16", 3, 128), ("e4m3", "bf16", 5, 64),
+                                            ("e4m3", "f32", 1, 128)])
+def test_means_of_many_blocks(env, kv, dtype, Hkv, d):
+    """Enough blocks that a warp takes two kv heads (an odd number of them too): the same bits as block by block."""
+    torch, mp, dev = env
+    n = 16 * (2700 // Hkv)
+    t = batch(torch, dev, [n + 21, 40], Hkv, Hkv, d, kv, 7 * d + Hkv)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    rope = mp.rope_table(16, d, t["base"], device=dev)
+    fn = mp.kv_block_means_q8 if kv == "e4m3" else mp.kv_block_means
+    pool = (t["k_pool"], t["k_scale"]) if kv == "e4m3" else (t["k_pool"],)
+    got, want = (torch.full((t["k_pool"].shape[0], Hkv, d), 7.0, dtype=dt, device=dev) for _ in range(2))
+    fn(i32(torch, dev, [0, n, n + 40]), i32(torch, dev, [21, 0]), t["block_tables"], *pool, rope, got)
+    for at in range(21, n + 21, 1600):
+        m = min(1600, n + 21 - at)
+        a = (i32(torch, dev, [0, m, m + (at == 21) * 40]), i32(torch, dev, [at, 0]), t["block_tables"])
+        fn(*a, *pool, rope, want)
+    assert torch.equal(got, want)
+    k = f64(t["k_pool"]) * f64(t["k_scale"])[..., None, None]
+    ref = osel.block_means(k, np.full(got.shape, 7.0), [0, n, n + 40], [21, 0], t["block_tables"].cpu().numpy(), t["base"])
+    a = np.abs(k).max(2)
+    tol = 24 * 2.0 ** -24 * (a + np.roll(a, d // 2, axis=-1)) + HALF[dtype] * np.abs(ref)
+    assert np.all(np.abs(f64(got) - ref) <= tol) and mp.device_error() == 0
+
+
 def test_means_skip_what_the_append_skips(env):
     torch, mp, dev = env
     nb, Hkv, d = 6, 2, 64
