@@ -556,9 +556,9 @@ typedef struct {
 } minipic_block_scores_batch;
 
 /* scores[r][g][b] = the largest over the query heads of kv head g of scale *
- * (R_{q_pos} q)^T (R_{block_starts} m), the mean score of block b's keys: fp32
- * arithmetic with rope->cos_sin, NaN if a product is.  -infinity past the request's
- * length, for a block id outside the pool and for a start outside [0, max_pos) (with
+ * (R_{q_pos} q)^T (R_{block_starts} m), the mean score of block b's keys, with
+ * rope->cos_sin, products and sums of fp32's precision; NaN if one of the two has an
+ * element that is not finite.  -infinity past the request's length, for a block id outside the pool and for a start outside [0, max_pos) (with
  * the error bits; a negative start is outside whatever its slots).  dtype is that of
  * q and means.  UNSUPPORTED above 65535 requests or kv heads, or for
  * max_blocks_per_seq of 2^27 or more.  Asynchronous on `stream`. */
@@ -630,7 +630,13 @@ size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_he
 /* minipic_attn_decode for such a batch: the same arguments, tables and result (each
  * request attends to all its seq_lens keys), with the groups.  Only full blocks are
  * shared, as in the prefix cache.  A request of a group that is shorter than the
- * prefix (an empty row of a padded batch) reads its own keys and shares nothing.
+ * prefix (an empty row of a padded batch) reads its own keys and shares nothing; so do
+ * the requests of a group with bad numbers or beyond the planning bounds
+ * (MINIPIC_DEVERR_SEQ_LEN).  The attention to a shared prefix has the arithmetic and the
+ * ranges of minipic_prefill_attn: rotated keys and scaled, rotated queries within
+ * fp16's range (else MINIPIC_DEVERR_RANGE), P and V bf16, V finite in blocks that a bad
+ * position masks too; the rest that of minipic_attn_decode_weights.  The workspace must
+ * have been zeroed once, like that one's, and serves one call at a time.
  * bf16 only (f32 returns UNSUPPORTED; head dim 64 or 128). */
 minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
                                           const minipic_rope* rope, const minipic_decode_batch* batch,

@@ -412,8 +412,8 @@ DecodePlan plan_decode_list(int batch, int Hkv, int G, int D, int max_blocks, bo
 
 DecodePlan plan_decode_lists(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms) {
   DecodePlan p = plan_decode_list(batch, Hkv, G, D, max_blocks, bf16, num_sms);
-  // With many more pairs than CTAs at once, a CTA each: equal ranges of the list would make every CTA cut, and join, two
-  // of them (2048 pairs of 1 to 32 blocks behind a prefix, with that: 381 us against 463).  With a few more, the
+  // With many more pairs than CTAs at once, a CTA each: equal ranges of the list would make every CTA cut, and join,
+  // two of them (2048 pairs of 1 to 32 blocks behind a prefix, with that: 381 us against 463).  With a few more, the
   // ranges' even end counts for more (512 pairs of 64 blocks: 39.6 us against 40.9).
   const long long pairs = (long long)batch * Hkv;
   if (bf16 && pairs >= 2LL * p.n_split && pairs < (1 << 20)) p.n_split += (int)pairs;
@@ -1149,7 +1149,8 @@ PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, 
     const int tq = 128 / G, tile = D == 128 ? prefix::kTileBlocks<128> : prefix::kTileBlocks<64>;
     w.n_slots = D == 128 ? (sms > 1 ? sms / 2 : 1) : sms;  // a cluster of two SMs an item, or one SM
     // query-tile pairs: of all requests together, and one more a group that ends inside one
-    const long long most = max_requests < batch ? max_requests : batch, groups = num_prefixes < batch ? num_prefixes : batch;
+    const long long most = max_requests < batch ? max_requests : batch;
+    const long long groups = num_prefixes < batch ? num_prefixes : batch;
     const long long each = groups * ((most + 2 * tq - 1) / (2 * tq)), all = batch / (2 * tq) + groups;
     const long long units = Hkv * (each < all ? each : all);
     const long long tiles = (max_prefix_blocks + tile - 1LL) / tile;
@@ -1157,7 +1158,8 @@ PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, 
     for (int n = 1; n <= 8; ++n) {
       const long long room = (long long)n * w.n_slots - units;
       if (room <= 0) continue;
-      const long long len = (units * tiles + room - 1) / room, cost = n * ((len < tiles ? len : tiles) + prefix::kItemCost);
+      const long long len = (units * tiles + room - 1) / room;
+      const long long cost = n * ((len < tiles ? len : tiles) + prefix::kItemCost);
       if (w.max_waves == 0 || cost < least) {
         least = cost;
         w.max_waves = n;
@@ -1170,8 +1172,9 @@ PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, 
     w.group_bytes = align_up((size_t)num_prefixes * sizeof(int2), 256);
     w.o_bytes = (size_t)w.items * prefix::kRows * D * sizeof(float);
     w.lse_bytes = (size_t)w.items * prefix::kRows * sizeof(float);
-    // With many requests the second kernel is long, and the first leaves SMs free: 24 of 152 through 290 us for 256
-    // requests of 8 x 8 heads.
+    // With many requests the own keys take long too: a kernel that waits for nothing of the first one runs beside it,
+    // where that leaves room, and the join is a third (256 requests, 64 / 8 heads: 310 us so, 349 with the join in the
+    // second; 64 requests, 28 / 4 heads: 73 and 67, a launch less counts for more there).
     w.apart = (long long)batch * Hkv >= 2LL * plan_decode_list(batch, Hkv, G, D, mb, true, sms).n_split;
     if (w.apart) {
       w.own_bytes = align_up((size_t)batch * Hq * D * sizeof(float), 256);
@@ -1208,7 +1211,8 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
     return MINIPIC_ERR_INVALID;
   if (groups->num_prefixes > 0 && (!groups->cu_requests || !groups->prefix_blocks)) return MINIPIC_ERR_INVALID;
   if (empty) return MINIPIC_OK;
-  if (!list_fits(*kv, *b) || kv->num_blocks == 0) return kv->num_blocks == 0 ? MINIPIC_ERR_INVALID : MINIPIC_ERR_UNSUPPORTED;
+  if (kv->num_blocks == 0) return MINIPIC_ERR_INVALID;
+  if (!list_fits(*kv, *b)) return MINIPIC_ERR_UNSUPPORTED;
   int* err = nullptr;
   int sms = 0;
   if (device_info(&err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
@@ -1221,9 +1225,9 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
   a.cs_f16 = rope->cos_sin_f16;
   a.cu_requests = groups->cu_requests;
   a.prefix_blocks = groups->prefix_blocks;
-  // groups that the planning bounds rule out share nothing
-  a.n_prefix = w.items > 0 ? groups->num_prefixes : 0;
+  a.n_prefix = groups->num_prefixes;  // with no room for items, none of them is within the planning bounds
   a.max_requests = groups->max_requests;
+  a.max_prefix = groups->max_prefix_blocks < a.max_blocks ? groups->max_prefix_blocks : a.max_blocks;
   a.items = w.items;
   char* ws = static_cast<char*>(workspace) + w.list_bytes;
   a.group_items = reinterpret_cast<const int2*>(ws);
@@ -1260,6 +1264,7 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
     p.scale = a.scale;
     p.err = err;
     p.prefix_blocks = groups->prefix_blocks;
+    p.max_prefix = a.max_prefix;
     p.n_slots = w.n_slots;
     p.max_waves = w.max_waves;
     p.group_items = const_cast<int2*>(a.group_items);
@@ -1268,7 +1273,8 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
     if (launch_prefix(p, w.items, s) != cudaSuccess) return MINIPIC_ERR_CUDA;
     a.after_prefix = true;
   }
-  return (w.apart ? launch_decode_apart(a, s) : launch_decode_prefix(a, s)) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+  const cudaError_t e = w.apart ? launch_decode_apart(a, s) : launch_decode_prefix(a, s);
+  return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }
 
 }  // extern "C"

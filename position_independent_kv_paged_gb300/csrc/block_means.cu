@@ -75,16 +75,13 @@ __global__ void __launch_bounds__(kThreads) block_means_kernel(const MeansArgs a
   }
   const long long end = js + n;            // keys of the request after the append
   const int per = (a.Hkv + U - 1) / U;     // warps of a block
-  const long long b0 = js >> 4, items = (((end + 15) >> 4) - b0) * per;
+  const long long b0 = js >> 4, b1 = min((end + 15) >> 4, (long long)a.max_blocks), items = (b1 - b0) * per;
+  if (end > 16LL * a.max_blocks && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.err, kErrSeqLen);
   const int row = lane / LPR, e0 = 4 * (lane % LPR);
   for (long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < items;
        i += (long long)gridDim.x * (kThreads / 32)) {
     const long long b = b0 + i / per;
     const int g0 = (int)(i % per) * U;
-    if (b >= a.max_blocks) {
-      if (lane == 0) atomicOr(a.err, kErrSeqLen);
-      continue;
-    }
     const int phys = __ldg(a.block_tables + (size_t)r * a.max_blocks + b);
     if (phys < 0 || phys >= a.num_blocks) {
       if (lane == 0) atomicOr(a.err, kErrBlockId);

@@ -37,8 +37,8 @@
 //  - The query is scaled by a power of two per head to a largest element in
 //    [1, 2) first, so that fp16 holds it whatever its size.
 //  - bf16: P is 2^(s - ms) in bf16 and V enters as it is.  Over selected blocks and behind prefixes P is the sum of two
-//    bf16 parts, each a product (20 of 460 instructions a block): its rounding was the largest part of the error, 2.3e-3
-//    of the output's norm with it and 1.9e-3 without, of which 1.7e-3 are the output's own rounding.
+//    bf16 parts, each a product (20 of 460 instructions a block, 39.6 -> 40.9 us for 512 lists of 64 blocks): its
+//    rounding was half of the error, 2.3e-3 of the output's norm with it and 1.7e-3, the output's own rounding, without.
 //  - e4m3: V bytes stay unscaled in the product; the block's scale rides on P.  P is
 //    2^(s + log2 vscale - mt + 7) in fp16 with a running reference mt of its own
 //    (so blocks whose scales differ by any factor keep fp16's full precision
@@ -240,7 +240,7 @@ __device__ __forceinline__ Shared shared_of(const DecodeArgs& a, const int* cu, 
   }
   if (lo == 0) return Shared{0, 0, 0};
   bool bad;
-  const prefix::Group g = prefix::group(cu[lo - 1], cu[lo], nb[lo - 1], a.batch, a.max_blocks, a.max_requests, bad);
+  const prefix::Group g = prefix::group(cu[lo - 1], cu[lo], nb[lo - 1], a.batch, a.max_prefix, a.max_requests, bad);
   const bool in = i >= g.q0 && i < g.q0 + g.n && L >= 16LL * g.blocks;
   return Shared{lo - 1, g.q0, in ? g.blocks : 0};
 }
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     if (blockIdx.x == 0)
       for (int p = threadIdx.x; p < a.n_prefix; p += NW * 32) {
         bool bad;
-        prefix::group(grp_cu[p], grp_cu[p + 1], grp_nb[p], a.batch, mb, a.max_requests, bad);
+        prefix::group(grp_cu[p], grp_cu[p + 1], grp_nb[p], a.batch, a.max_prefix, a.max_requests, bad);
         if (bad) atomicOr(a.err, kErrSeqLen);
       }
   }

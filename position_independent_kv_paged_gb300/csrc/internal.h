@@ -43,7 +43,7 @@ struct DecodeArgs {
   // shared prefixes (null: none), whose part of the attention a kernel before has computed
   const int32_t* cu_requests;    // [n_prefix + 1]
   const int32_t* prefix_blocks;  // [n_prefix]
-  int n_prefix, max_requests;
+  int n_prefix, max_requests, max_prefix;  // bounds of a group's requests and shared blocks
   const int2* group_items;       // [n_prefix] first item and parts (written for groups that share something)
   long long items;               // that the partial results have room for
   const float* prefix_o;         // [items][256][D]
@@ -75,6 +75,7 @@ struct PrefillArgs {
   // shared prefixes (launch_prefix): a query row is a request, total_q the requests of the batch, `batch` the groups,
   // cu_q_lens their requests, kv_lens and the tables those of the requests, max_q_len a bound of a group's requests
   const int32_t* prefix_blocks;  // [batch]
+  int max_prefix;                // bound of a prefix
   int n_slots, max_waves;        // items that run at once, and in how many waves at most the prefixes are cut
   int2* group_items;             // [batch] a group's first item and parts, written here
   float* part_o;                 // [items][256][D], divided by the part's denominator

@@ -24,18 +24,19 @@ struct Group {
   int blocks;  // that they share (0: nothing)
 };
 
-// A group as the tables allow it; `bad`: its numbers are outside the batch, the tables or the planning bound.
-__device__ __forceinline__ Group group(int c0, int c1, int nb, int batch, int max_blocks, int max_requests, bool& bad) {
-  bad = c0 < 0 || c1 < c0 || c1 > batch || (long long)c1 - c0 > max_requests || nb < 0 || nb > max_blocks;
+// A group as the tables and the planning bounds allow it (most_blocks: the lower bound of a prefix); `bad`: its numbers
+// are outside them or the batch.
+__device__ __forceinline__ Group group(int c0, int c1, int nb, int batch, int most_blocks, int max_requests, bool& bad) {
+  bad = c0 < 0 || c1 < c0 || c1 > batch || (long long)c1 - c0 > max_requests || nb < 0 || nb > most_blocks;
   Group g;
   g.q0 = max(0, min(c0, batch));
   g.n = max(0, min(c1, batch) - g.q0);
-  g.blocks = g.n >= kMinRequests && g.n <= max_requests && nb > 0 && nb <= max_blocks ? nb : 0;
+  g.blocks = g.n >= kMinRequests && g.n <= max_requests && nb > 0 && nb <= most_blocks ? nb : 0;
   return g;
 }
 __device__ __forceinline__ Group group(const PrefillArgs& a, int p) {
   bool bad;
-  return group(__ldg(a.cu_q_lens + p), __ldg(a.cu_q_lens + p + 1), __ldg(a.prefix_blocks + p), a.total_q, a.max_blocks,
+  return group(__ldg(a.cu_q_lens + p), __ldg(a.cu_q_lens + p + 1), __ldg(a.prefix_blocks + p), a.total_q, a.max_prefix,
                a.max_q_len, bad);
 }
 

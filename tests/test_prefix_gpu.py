@@ -190,6 +190,61 @@ def test_bad_group_data_is_flagged(env):
         assert torch.equal(got[:2], want[:2])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_groups_beyond_the_planning_bounds(env, d):
+    """More requests or longer prefixes than the call was told: flagged, and the requests share nothing."""
+    torch, mp, dev = env
+    t = groups(torch, dev, [700, 720, 740, 660, 500, 450], [0, 3, 6], [30, 20], 8, 2, d, 31)
+    for bounds, bad in ((dict(max_requests=3, max_prefix_blocks=29), True), (dict(max_requests=2, max_prefix_blocks=30), True),
+                        (dict(max_requests=3, max_prefix_blocks=1), True), (dict(max_requests=0, max_prefix_blocks=0), True),
+                        (dict(max_requests=1000, max_prefix_blocks=1000), False)):
+        got = run(env, t, **bounds)
+        assert mp.device_error(clear=True) == (4 if bad else 0), bounds
+        check(env, t, got, f"d{d} {bounds}")
+
+
+def test_more_groups_and_requests_than_are_staged(env):
+    """Hundreds of groups, thousands of requests, some without a key."""
+    torch, mp, dev = env
+    rng = np.random.default_rng(12)
+    for d, B, P in ((64, 2100, 700), (128, 600, 300)):
+        cu = [0] + sorted(int(x) for x in rng.integers(0, B + 1, P))
+        blocks = [int(x) for x in rng.integers(0, 6, P)]
+        lens = [0] * B
+        for p in range(P):
+            for r in range(cu[p], cu[p + 1]):
+                lens[r] = int(rng.integers(0, 16)) * int(rng.integers(0, 2)) + 16 * (blocks[p] - int(rng.random() < 0.1))
+        lens = [max(0, x) for x in lens]
+        t = groups(torch, dev, lens, cu, blocks, 2, 1, d, B)
+        check(env, t, run(env, t), f"{B} requests")
+    assert mp.device_error() == 0
+
+
+def test_calls_on_two_streams_at_once(env):
+    """Calls of both head dims on two streams, each with its workspace: the bits of the calls alone."""
+    torch, mp, dev = env
+    cases = [groups(torch, dev, [16 * nb + 30 * i for i in range(n)], [0, n], [nb], 8, 2, d, nb)
+             for nb, n, d in ((90, 40, 128), (60, 30, 64))]
+    ropes = [mp.rope_table(t["max_pos"], t["q"].shape[2], t["base"], device=dev) for t in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+
+    def call(i, **kw):
+        t = cases[i]
+        return mp.attn_decode_prefix(t["q"], t["k_pool"], t["v_pool"], t["block_tables"], t["block_starts"],
+                                     t["seq_lens"], t["q_pos"], ropes[i], t["cu"], t["blocks"], max_requests=40,
+                                     max_prefix_blocks=90, **kw)[0]
+    want = [call(i).clone() for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(call(i, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, want[i]) for x in got[i]), i
+    assert mp.device_error() == 0
+
+
 def test_captured_and_on_a_side_stream(env):
     """Capture runs nothing, replay equals the call, two captured graphs share a workspace one after the other, and a
     call on a side stream allocates and clears its own while the current one is behind."""
