@@ -9,12 +9,14 @@
 // into four chains that meet in fp32: the tensor core's own additions truncate.
 //
 // A summary is 1 / 32 of a block's keys and values, so this reads that part of what attention would, and instructions
-// bound it: widening, rotating and splitting a summary, whatever the number of query heads.  Packed fp32 arithmetic on
-// the scalar pipes took 27 us where this takes 22 (64 requests x 512 blocks, 8 kv heads, 4 query heads each), and 60 us
-// against 42 (8 x 8192, 8 heads each): there each query head costs as much again as the products do here for eight.
+// and their latency bound it: widening, rotating and splitting a summary, whatever the number of query heads (about 490
+// instructions for 16 blocks and a kv head, 40 % of the issue slots; 12 warps an SM).  64 requests x 512 blocks, 8 kv
+// heads, 4 query heads each: 21 us; 8 x 8192, 8 heads each: 39 us (packed fp32 arithmetic on the scalar pipes took 27
+// and 60: there each query head costs as much again as the products do here for eight).
 //
 // A warp takes 16 blocks (the rows of the product) through the kv heads of its CTA: the cosines and sines of the
-// blocks' starts stay in registers, and the next head's summaries load while it works on one.  A lane holds 8-element
+// blocks' starts stay in registers, and the next head's summaries load, a chunk at a time, as soon as this one's are
+// widened (all of them after the last chunk: 22 and 42 us).  A lane holds 8-element
 // chunks of the rotary pairs of two rows, x and y alike; which of its elements form a step of the contraction is free,
 // as long as the query's are in the same places (they are stored in that order, each lane's 16 bytes next to its
 // neighbour's).
@@ -80,9 +82,15 @@ __device__ __forceinline__ uint64_t two_rows(const Raw8<__nv_bfloat16>& a, const
 template <int D, int NT>
 constexpr int kHeadFloats = 2 * NT * 8 * D;
 
+// CTAs of an SM.  Two leave 255 registers: fp32 summaries or two column tiles at d 128 spill with three (64 x 512 blocks,
+// 8 kv heads: fp32 with 4 heads each 34.9 us against 23.0, with 16 52.3 and 33.2, bf16 with 16 35.0 and 29.5); the others
+// do not, and want the warps (bf16 with 4 heads, d 64: 12.0 us and 14.7).
+template <typename T, int D, int NT>
+constexpr int kCtas = D == 128 && (sizeof(T) == 4 || NT == 2) ? 2 : 3;
+
 // Grid: ranges of blocks, ranges of heads_per kv heads, requests.  NT: column tiles of 8 query heads.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, 3) block_scores_kernel(const ScoresArgs a, const int heads_per) {
+__global__ void __launch_bounds__(kThreads, kCtas<T, D, NT>) block_scores_kernel(const ScoresArgs a, const int heads_per) {
   constexpr int NC = D / 64;  // chunks of 8 + 8 elements of a lane and row
   // [kv head][column tile][x, y][chunk][quarter of a chunk pair][part][lane][4]
   extern __shared__ __align__(16) float sq[];
@@ -191,19 +199,18 @@ __global__ void __launch_bounds__(kThreads, 3) block_scores_kernel(const ScoresA
       }
     }
     Raw8<T> mx[2][NC], my[2][NC];
-    auto summaries = [&] {
+    auto summaries = [&](int k) {  // chunk k of both rows
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int k = 0; k < NC; ++k)
-          if (a.num_blocks > 0) {
-            mx[u][k].load(m[u] + 32 * k);
-            my[u][k].load(m[u] + D / 2 + 32 * k);
-          }
-        m[u] += D;
-      }
+      for (int u = 0; u < 2; ++u)
+        if (a.num_blocks > 0) {
+          mx[u][k].load(m[u] + 32 * k);
+          my[u][k].load(m[u] + D / 2 + 32 * k);
+        }
     };
-    summaries();
+#pragma unroll
+    for (int k = 0; k < NC; ++k) summaries(k);
+    m[0] += D;
+    m[1] += D;
     entries(w + warps);
 #pragma unroll
     for (int k = 0; k < NC; ++k)
@@ -229,7 +236,11 @@ __global__ void __launch_bounds__(kThreads, 3) block_scores_kernel(const ScoresA
           v[0][e] = ptx::sub2(ptx::mul2(x, c[k][e]), ptx::mul2(y, s[k][e]));
           v[1][e] = ptx::fma2(x, s[k][e], ptx::mul2(y, c[k][e]));
         }
-        if (k == NC - 1 && g + 1 < n_heads) summaries();
+        if (g + 1 < n_heads) summaries(k);  // the next head's, as soon as these are widened
+        if (k == NC - 1) {
+          m[0] += D;
+          m[1] += D;
+        }
 #pragma unroll
         for (int half = 0; half < 2; ++half)
 #pragma unroll
@@ -288,9 +299,9 @@ cudaError_t launch_t(const ScoresArgs& a, int num_sms, cudaStream_t s) {
   const cudaError_t e = set_smem_once(block_scores_kernel<T, D, NT>, most_heads * head_bytes, done);
   if (e != cudaSuccess) return e;
   // Two steps or more a resident warp in all: more heads a step read the starts' table rows less often, fewer even out
-  // the last wave (64 x 512 blocks, 8 heads: 1, 2, 4 and 8 heads a step take 31, 25, 22 and 24 us; 8 x 8192: 59, 50, 44
-  // and 42).
-  const long long steps = ((long long)a.max_blocks + kRows - 1) / kRows * a.batch, ctas = 3LL * num_sms;
+  // the last wave (64 x 512 blocks, 8 heads: 1, 2, 4 and 8 heads a step took 31, 25, 22 and 24 us; 8 x 8192: 59, 50, 44
+  // and 42; before the summaries loaded earlier).
+  const long long steps = ((long long)a.max_blocks + kRows - 1) / kRows * a.batch, ctas = (long long)kCtas<T, D, NT> * num_sms;
   long long heads_per = steps * a.Hkv / (2 * ctas * kWarps);
   heads_per = heads_per < 1 ? 1 : (heads_per > most_heads ? most_heads : heads_per);
   if (heads_per > a.Hkv) heads_per = a.Hkv;
