@@ -1,8 +1,8 @@
 // The best blocks of each (request, kv head) by score.
 //
-// With n blocks: all of them where n <= budget, else the first keep_first, the last keep_last and the best of the others
-// by score up to `budget` (NaN is the worst; of equal scores the lower index stays: the rule of kv_evict).  Their numbers are
-// written in ascending order, then -1.
+// With n blocks: all of them where n <= budget, else the first keep_first, the last keep_last and the best of the
+// others by score up to `budget` (NaN is the worst; of equal scores the lower index stays: the rule of kv_evict).  Their
+// numbers are written in ascending order, then -1.
 //
 // One CTA per (request, kv head).  Each thread keeps PER order-preserving integer images of its scores in
 // registers, in warp-contiguous rows of 32, so loads are whole lines and ballots give the order.  The threshold, the
