@@ -636,7 +636,8 @@ size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_he
  * ranges of minipic_prefill_attn: rotated keys and scaled, rotated queries within
  * fp16's range (else MINIPIC_DEVERR_RANGE), P and V bf16, V finite in blocks that a bad
  * position masks too; the rest that of minipic_attn_decode_weights.  The workspace must
- * have been zeroed once, like that one's, and serves one call at a time.
+ * have been zeroed once, like that one's, and serves one call at a time; out and lse do
+ * not overlap what the call reads.
  * bf16 only (f32 returns UNSUPPORTED; head dim 64 or 128). */
 minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
                                           const minipic_rope* rope, const minipic_decode_batch* batch,
