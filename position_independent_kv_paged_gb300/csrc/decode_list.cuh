@@ -444,14 +444,17 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         for (int e = threadIdx.x; e < a.Hq; e += NW * 32) a.lse[(size_t)i * a.Hq + e] = -CUDART_INF_F;
     }
   }
-  total *= a.Hkv;
+  // lists of many short pairs: a CTA takes two kv heads of a request, one after the other (always `whole` below)
+  const bool two = LIST != kAll && a.list_heads == 2;
+  const int n_heads = two ? a.Hkv / 2 : a.Hkv;  // what CTAs are numbered by: kv heads or pairs of them
+  total *= n_heads;
   {
     // A batch that does not fill the grid is cut into parts of pairs instead, one per CTA, so that no CTA walks two
     // pairs one after the other.  A part costs about 0.12 us a block, joining the parts of a pair about 5 us and more
     // with their number and the group's heads.  So pairs of up to 64 blocks are cut to 8 or 16 where that fits (1024
     // keys, 8 heads: 11 us, against 12 to 13 in parts of 32 or whole) and else left whole (128 pairs of 64 blocks: 15 us
     // against 16 in halves), longer ones to 32 (8192 keys: 15.4 us against 16.3 in 16) or, above 8 heads, 64.
-    const long long all_pairs = (long long)pairs * a.Hkv;
+    const long long all_pairs = (long long)pairs * n_heads;
     constexpr int kMostParts = NT == 1 ? kListMaxCtas : kListMaxCtas / 2;  // of a pair: the merge holds a weight for each
     const long long grid = min((long long)gridDim.x, (long long)kMostParts);
     int part = total <= 64 * all_pairs ? 8 : (NT == 1 ? 32 : 64);
@@ -484,11 +487,11 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       }
       const int units = whole ? (n + part - 1) / part : n;
       if (a.batch > NW * 32 || whole) sum = cta_total(units, before);
-      const long long at = (first + before) * a.Hkv;
-      if (x0 >= at && x0 < at + (long long)units * a.Hkv) {
+      const long long at = (first + before) * n_heads;
+      if (x0 >= at && x0 < at + (long long)units * n_heads) {
         const int k = (int)((x0 - at) % units);
         sg.r = i;
-        sg.hk = (int)((x0 - at) / units);
+        sg.hk = (int)((x0 - at) / units) * (two ? 2 : 1);
         sg.nblk = n;
         sg.L = min(Li, (int)min(16LL * mb, 2147483632LL));
         if constexpr (SHARE) enter(i, Li);
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         }
       }
       first += sum;
-      if (first * a.Hkv > x0) break;
+      if (first * n_heads > x0) break;
     }
     __syncthreads();
     if (sg.r < 0) {  // more CTAs than parts
@@ -1129,7 +1132,8 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         if (WTS && dim == 0) a.w_lse[hq] = lse2;
       } else {
         // a pair cut in front is this CTA's first (slot 0), one cut behind its last (slot 1)
-        const size_t pi = (size_t)(2 * blockIdx.x + (b_begin == 0)) * G + head;
+        // (of two kv heads that it takes alike, the second has the other slot)
+        const size_t pi = (size_t)(2 * blockIdx.x + ((b_begin == 0) != (two && (hk & 1)))) * G + head;
         a.part_o[pi * D + dim] = O;
         if (dim == 0) a.part_ml[pi] = lse2;
       }
@@ -1155,7 +1159,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         // (kPrefix: the parts of the prefix follow those of the list)
         const int n_list = c2 - c1 + 1, n_part = n_list + n_pre;
         float* wt = reinterpret_cast<float*>(sgen);  // [part][G], over what the stages held
-        auto slot = [&](int c) { return (size_t)(2 * (c1 + c) + (c == 0)) * G; };
+        auto slot = [&](int c) { return (size_t)(2 * (c1 + c) + ((c == 0) != (two && (hk & 1)))) * G; };
         [[maybe_unused]] auto pslot = [&](int c, int head) { return pre_at + head + (size_t)(c - n_list) * prefix::kRows; };
         for (int i = threadIdx.x; i < n_part * G; i += NW * 32) {
           const int c = i / G, head = i % G;
@@ -1207,6 +1211,15 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         }
         if (threadIdx.x == 0) a.counters[(size_t)r * a.Hkv + hk] = 0;
       }
+    }
+    if (two && !(hk & 1)) {  // the same blocks of the next kv head
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        sg.hk = hk + 1;
+        sg.wide = 0;
+      }
+      __syncthreads();
+      continue;
     }
     const int left = sg.left - (b_end - b_begin);
     if (left <= 0) break;

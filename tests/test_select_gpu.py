@@ -394,6 +394,31 @@ def test_lists_that_fill_the_grid_or_one_pair(env, kv, B, Hq, Hkv, d, S):
     assert mp.device_error() == 0
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 4, 128), (3, 3, 64), (24, 2, 128)])
+def test_many_lists_of_mixed_lengths(env, kv, Hq, Hkv, d):
+    """Several times more (request, kv head) pairs than CTAs, nearly all of a few blocks, some of none, three long
+    enough to be cut: the same bits twice on one workspace, whose counters end at zero."""
+    torch, mp, dev = env
+    rng = np.random.default_rng(Hq)
+    B = 1300 // Hkv
+    lens = [int(x) for x in rng.integers(0, 70, B)]
+    lens[5], lens[B // 2], lens[B - 1] = 9000, 7001, 12000
+    t = batch(torch, dev, lens, Hq, Hkv, d, kv, d + Hq)
+    S = 640
+    sel = np.full((B, Hkv, S), -1, np.int32)
+    for r, n in enumerate(lens):
+        for g in range(Hkv):
+            blocks = rng.permutation(-(-n // 16))[:S]
+            sel[r, g, :len(blocks)] = blocks
+    ws = torch.zeros(mp.attn_decode_selected_workspace_size(B, Hq, Hkv, d, S), dtype=torch.uint8, device=dev)
+    got = [run(env, t, i32(torch, dev, sel), workspace=ws) for _ in range(2)]
+    assert not ws[:65536].any()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    check(env, t, i32(torch, dev, sel), got[0])
+    assert mp.device_error() == 0
+
+
 def test_selected_with_a_scale(env):
     torch, mp, dev = env
     for kv in ("f32", "bf16"):
