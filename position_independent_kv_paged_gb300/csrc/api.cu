@@ -417,9 +417,10 @@ DecodePlan plan_decode_lists(int batch, int Hkv, int G, int D, int max_blocks, b
   // two of them (2048 pairs of 1 to 32 blocks behind a prefix, with that: 381 us against 463).  With a few more, the
   // ranges' even end counts for more (512 pairs of 64 blocks: 39.6 us against 40.9).  Two kv heads of a request a CTA,
   // one after the other, save a start (4096 pairs of 32 e4m3 blocks: 119 us against 138 with one; 2048 of 16 bf16
-  // blocks: 54 and 56, of 64: 113 both).
+  // blocks: 54 and 56, of 64: 113 both).  Beyond 65536 pairs the ranges hold many each, and partial results for every CTA
+  // would take gigabytes.
   const long long pairs = (long long)batch * Hkv;
-  if (bf16 && pairs >= 2LL * p.n_split && pairs < (1 << 20)) {
+  if (bf16 && pairs >= 2LL * p.n_split && pairs <= (1 << 16)) {
     p.list_heads = Hkv % 2 ? 1 : 2;
     p.n_split += (int)pairs / p.list_heads;
   }

@@ -419,6 +419,29 @@ def test_many_lists_of_mixed_lengths(env, kv, Hq, Hkv, d):
     assert mp.device_error() == 0
 
 
+def test_more_lists_than_get_a_cta_each(env):
+    """70000 (request, kv head) pairs of up to three blocks: every CTA walks a range of them."""
+    torch, mp, dev = env
+    B, Hkv, d, S = 8750, 8, 64, 3
+    g = torch.Generator(device=dev).manual_seed(3)
+    nb, mb, base = 512, 4, 1e4
+    t = dict(kv="bf16", Hkv=Hkv, base=base, max_pos=4096,
+             q=torch.randn(B, 8, d, generator=g, device=dev).bfloat16(),
+             block_tables=torch.randint(0, nb, (B, mb), generator=g, device=dev, dtype=torch.int32),
+             block_starts=torch.randint(0, 4000, (B, mb), generator=g, device=dev, dtype=torch.int32),
+             seq_lens=torch.randint(0, 16 * mb + 1, (B,), generator=g, device=dev, dtype=torch.int32),
+             q_pos=torch.randint(0, 4096, (B,), generator=g, device=dev, dtype=torch.int32))
+    for x in ("k_pool", "v_pool"):
+        t[x] = torch.randn(nb, Hkv, 16, d, generator=g, device=dev).bfloat16()
+    sel = torch.argsort(torch.rand(B, Hkv, mb, generator=g, device=dev), -1)[..., :S].int().contiguous()
+    sel[sel >= ((t["seq_lens"] + 15) // 16)[:, None, None]] = -1
+    out, lse = run(env, t, sel)
+    rows = torch.randperm(B, generator=g, device=dev)[:300]
+    part = {k: (v[rows] if k in ("q", "block_tables", "block_starts", "seq_lens", "q_pos") else v) for k, v in t.items()}
+    check(env, part, sel[rows], (out[rows], lse[rows]))
+    assert mp.device_error() == 0
+
+
 def test_selected_with_a_scale(env):
     torch, mp, dev = env
     for kv in ("f32", "bf16"):
