@@ -638,6 +638,7 @@ size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_he
  * position masks too; the rest that of minipic_attn_decode_weights.  The workspace must
  * have been zeroed once, like that one's, and serves one call at a time; out and lse do
  * not overlap what the call reads.
+ * Where the planning bounds say that sharing saves little, nothing is shared.
  * bf16 only (f32 returns UNSUPPORTED; head dim 64 or 128). */
 minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
                                           const minipic_rope* rope, const minipic_decode_batch* batch,

@@ -1139,6 +1139,11 @@ namespace {
 // the device, where the groups are; here their number is bounded, by the waves that would cost least if every group
 // were as large as the planning bounds allow (eight balance well enough).  No looser: the clusters that find no item
 // start and end all the same, and the next kernel waits for their start.
+// Fewer blocks that sharing saves, per CTA of the list decode, do not pay for the kernel that computes the shared part:
+// then every request reads its own (us without and with it, 32 / 8 heads, d 128, 8 x 512 tokens, 1 block a CTA:
+// 13.5 and 22.0; 16 x 2048, 34: 24.0 and 28.1; 2 x 32768, 36: 43.5 and 62.5; 16 x 4096, 67: 35.4 and 30.0; 64 x 2048 of
+// 28 / 4 heads, 71: 44.9 and 33.3).
+constexpr long long kShareAbove = 56;
 struct PrefixWs {
   DecodePlan plan;
   int n_slots, max_waves;
@@ -1152,7 +1157,10 @@ PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, 
   const int G = Hq / Hkv;
   w.plan = plan_decode_lists(batch, Hkv, G, D, mb, true, sms);
   w.list_bytes = decode_ws_weights(batch, Hq, Hkv, D, count_partials(w.plan, batch, Hq, G), 0).total;
-  if (num_prefixes > 0 && max_requests >= prefix::kMinRequests && max_prefix_blocks > 0 && G <= 16) {
+  const long long ctas = plan_decode_list(batch, Hkv, G, D, mb, true, sms).n_split;
+  const long long members = (long long)num_prefixes * max_requests < batch ? (long long)num_prefixes * max_requests : batch;
+  const long long saved = (members - num_prefixes) * Hkv * max_prefix_blocks;  // blocks and kv heads not read again
+  if (num_prefixes > 0 && max_requests >= prefix::kMinRequests && saved > kShareAbove * ctas && G <= 16) {
     const int tq = 128 / G, tile = D == 128 ? prefix::kTileBlocks<128> : prefix::kTileBlocks<64>;
     w.n_slots = D == 128 ? (sms > 1 ? sms / 2 : 1) : sms;  // a cluster of two SMs an item, or one SM
     // query-tile pairs: of all requests together, and one more a group that ends inside one
@@ -1182,7 +1190,7 @@ PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, 
     // With many requests the own keys take long too: a kernel that waits for nothing of the first one runs beside it,
     // where that leaves room, and the join is a third (256 requests, 64 / 8 heads: 310 us so, 349 with the join in the
     // second; 64 requests, 28 / 4 heads: 73 and 67, a launch less counts for more there).
-    w.apart = (long long)batch * Hkv >= 2LL * plan_decode_list(batch, Hkv, G, D, mb, true, sms).n_split;
+    w.apart = (long long)batch * Hkv >= 2 * ctas;
     if (w.apart) {
       w.own_bytes = align_up((size_t)batch * Hq * D * sizeof(float), 256);
       w.own_lse_bytes = align_up((size_t)batch * Hq * sizeof(float), 256);
@@ -1232,7 +1240,7 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
   a.cs_f16 = rope->cos_sin_f16;
   a.cu_requests = groups->cu_requests;
   a.prefix_blocks = groups->prefix_blocks;
-  a.n_prefix = groups->num_prefixes;  // with no room for items, none of them is within the planning bounds
+  a.n_prefix = groups->num_prefixes;
   a.max_requests = groups->max_requests;
   a.max_prefix = groups->max_prefix_blocks < a.max_blocks ? groups->max_prefix_blocks : a.max_blocks;
   a.items = w.items;

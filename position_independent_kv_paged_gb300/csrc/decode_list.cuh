@@ -226,7 +226,8 @@ __device__ __forceinline__ uint32_t distance(int t, int b) {
 // a third kernel, so that nothing here waits for the first.  Either starts as soon as that one's last CTAs run.
 enum List { kAll, kSelected, kPrefix, kApart };
 
-// The group of request i of length L, and the blocks it shares: the group's, if the request holds them all (else 0).  cu
+// The group of request i of length L, and the blocks it shares: the group's, if the request holds them all (else 0, as
+// where nothing is shared: no items).  cu
 // and nb: where the groups are read.
 struct Shared {
   int p, q0, blocks;
@@ -241,7 +242,7 @@ __device__ __forceinline__ Shared shared_of(const DecodeArgs& a, const int* cu, 
   if (lo == 0) return Shared{0, 0, 0};
   bool bad;
   const prefix::Group g = prefix::group(cu[lo - 1], cu[lo], nb[lo - 1], a.batch, a.max_prefix, a.max_requests, bad);
-  const bool in = i >= g.q0 && i < g.q0 + g.n && L >= 16LL * g.blocks;
+  const bool in = a.items > 0 && i >= g.q0 && i < g.q0 + g.n && L >= 16LL * g.blocks;
   return Shared{lo - 1, g.q0, in ? g.blocks : 0};
 }
 // Groups that a CTA stages in shared memory (over its stages), and lengths of lists.

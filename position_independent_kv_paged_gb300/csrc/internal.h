@@ -46,7 +46,7 @@ struct DecodeArgs {
   const int32_t* prefix_blocks;  // [n_prefix]
   int n_prefix, max_requests, max_prefix;  // bounds of a group's requests and shared blocks
   const int2* group_items;       // [n_prefix] first item and parts (written for groups that share something)
-  long long items;               // that the partial results have room for
+  long long items;               // that the partial results have room for (0: nothing is shared)
   const float* prefix_o;         // [items][256][D]
   const float* prefix_lse;       // [items][256] log2
   bool after_prefix;             // the kernel before in the stream is that one: start while it ends

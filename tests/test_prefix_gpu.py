@@ -44,8 +44,12 @@ def groups(torch, dev, lens, cu, blocks, Hq, Hkv, d, seed):
     return t
 
 
+WIDE = 10 ** 6   # a bound of the prefixes with which these small batches share (the exact one says that it does not pay)
+
+
 def run(env, t, rope=None, **kw):
     torch, mp, dev = env
+    kw.setdefault("max_prefix_blocks", WIDE)
     B, Hq, d = t["q"].shape
     rope = rope or mp.rope_table(t["max_pos"], d, t["base"], device=dev)
     lse = torch.full((B, Hq), float("nan"), device=dev)
@@ -111,17 +115,18 @@ def test_many_requests_and_long_prefixes(env, Hq, Hkv, d, B, nb):
     lens[B // 2] = 0
     t = groups(torch, dev, lens, [0, B], [nb], Hq, Hkv, d, B)
     mb = t["block_tables"].shape[1]
-    n = max(mp.attn_decode_prefix_workspace_size(B, Hq, Hkv, d, mb, 1, B + x, nb + x) for x in (0, 50))
+    n = max(mp.attn_decode_prefix_workspace_size(B, Hq, Hkv, d, mb, 1, B + x, y) for x, y in ((0, nb), (50, nb + WIDE)))
     ws = torch.zeros(n, dtype=torch.uint8, device=dev)
     first = None
+    check(env, t, run(env, t, workspace=ws, max_requests=B, max_prefix_blocks=nb), "exact bounds")
     for i in range(6):
-        got = run(env, t, workspace=ws, max_requests=B, max_prefix_blocks=nb)
+        got = run(env, t, workspace=ws, max_requests=B, max_prefix_blocks=nb + WIDE)
         assert not ws[:65536].any(), i
         if first is None:
             first = got
             check(env, t, got)
         assert torch.equal(first[0], got[0]) and torch.equal(first[1], got[1]), i
-    check(env, t, run(env, t, workspace=ws, max_requests=B + 50, max_prefix_blocks=nb + 50), "wide bounds")
+    check(env, t, run(env, t, workspace=ws, max_requests=B + 50, max_prefix_blocks=nb + WIDE), "wide bounds")
     assert mp.device_error() == 0
 
 
@@ -185,7 +190,7 @@ def test_bad_group_data_is_flagged(env):
     want = run(env, t)[0]
     for cu, blocks in (([0, 2, 9], [10, 12]), ([0, 2, 4], [10, 10 ** 6]), ([0, 2, 1], [10, 12]), ([0, 2, 4], [10, -3])):
         t["cu"], t["blocks"] = i32(torch, dev, cu), i32(torch, dev, blocks)
-        got = run(env, t, max_requests=2, max_prefix_blocks=12)[0]
+        got = run(env, t, max_requests=2)[0]
         assert mp.device_error(clear=True) == 4, (cu, blocks)
         assert torch.equal(got[:2], want[:2])
 
@@ -197,10 +202,22 @@ def test_groups_beyond_the_planning_bounds(env, d):
     t = groups(torch, dev, [700, 720, 740, 660, 500, 450], [0, 3, 6], [30, 20], 8, 2, d, 31)
     for bounds, bad in ((dict(max_requests=3, max_prefix_blocks=29), True), (dict(max_requests=2, max_prefix_blocks=30), True),
                         (dict(max_requests=3, max_prefix_blocks=1), True), (dict(max_requests=0, max_prefix_blocks=0), True),
-                        (dict(max_requests=1000, max_prefix_blocks=1000), False)):
+                        (dict(max_requests=1000, max_prefix_blocks=1000), False), (dict(max_requests=2), True),
+                        (dict(max_requests=3), False), (dict(max_requests=1), True)):
         got = run(env, t, **bounds)
         assert mp.device_error(clear=True) == (4 if bad else 0), bounds
         check(env, t, got, f"d{d} {bounds}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_group_beyond_the_bounds_another_within(env, d):
+    """The first group's prefix is longer than the call was told: flagged, its requests read their own keys; the second
+    group shares (the bounds say that it pays)."""
+    torch, mp, dev = env
+    t = groups(torch, dev, [16 * 60 + 3 * i for i in range(100)], [0, 50, 100], [58, 40], 16, 8, d, 37)
+    got = run(env, t, max_requests=50, max_prefix_blocks=50)
+    assert mp.device_error(clear=True) == 4
+    check(env, t, got, f"d{d}")
 
 
 def test_more_groups_and_requests_than_are_staged(env):
@@ -232,7 +249,7 @@ def test_calls_on_two_streams_at_once(env):
         t = cases[i]
         return mp.attn_decode_prefix(t["q"], t["k_pool"], t["v_pool"], t["block_tables"], t["block_starts"],
                                      t["seq_lens"], t["q_pos"], ropes[i], t["cu"], t["blocks"], max_requests=40,
-                                     max_prefix_blocks=90, **kw)[0]
+                                     max_prefix_blocks=WIDE, **kw)[0]
     want = [call(i).clone() for i in range(2)]
     torch.cuda.synchronize()
     got = [[], []]
@@ -253,7 +270,7 @@ def test_captured_and_on_a_side_stream(env):
              for nb, d in ((60, 128), (25, 64))]
     ropes = [mp.rope_table(t["max_pos"], t["q"].shape[2], t["base"], device=dev) for t in cases]
     want = [run(env, t, rope)[0] for t, rope in zip(cases, ropes)]
-    n = max(mp.attn_decode_prefix_workspace_size(9, 8, 2, t["q"].shape[2], t["block_tables"].shape[1], 1, 9, 60)
+    n = max(mp.attn_decode_prefix_workspace_size(9, 8, 2, t["q"].shape[2], t["block_tables"].shape[1], 1, 9, WIDE)
             for t in cases)
     ws = torch.zeros(n, dtype=torch.uint8, device=dev)
     outs = [torch.full_like(t["q"], 7.0) for t in cases]
@@ -262,7 +279,7 @@ def test_captured_and_on_a_side_stream(env):
         t = cases[i]
         return mp.attn_decode_prefix(t["q"], t["k_pool"], t["v_pool"], t["block_tables"], t["block_starts"],
                                      t["seq_lens"], t["q_pos"], ropes[i], t["cu"], t["blocks"], max_requests=9,
-                                     max_prefix_blocks=60, **kw)[0]
+                                     max_prefix_blocks=WIDE, **kw)[0]
     graphs = []
     for i in range(2):
         graphs.append(torch.cuda.CUDAGraph())
