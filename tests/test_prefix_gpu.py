@@ -105,7 +105,8 @@ def test_groups_of_any_kind(env, Hq, Hkv, d):
 
 
 @pytest.mark.parametrize("Hq,Hkv,d,B,nb", [(8, 2, 128, 150, 200), (16, 1, 128, 40, 700), (8, 2, 64, 150, 200),
-                                           (28, 4, 128, 64, 97), (16, 1, 64, 33, 333), (4, 4, 128, 300, 30)])
+                                           (28, 4, 128, 64, 97), (16, 1, 64, 33, 333), (4, 4, 128, 300, 30),
+                                           (4, 4, 128, 300, 10), (8, 4, 64, 320, 6)])
 def test_many_requests_and_long_prefixes(env, Hq, Hkv, d, B, nb):
     """More rows than a tile pair, prefixes of many tiles cut into parts: the same bits call after call on one
     workspace, whose counters end at zero; planning bounds larger than what comes change nothing."""
