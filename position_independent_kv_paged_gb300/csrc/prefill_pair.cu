@@ -575,9 +575,11 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
       // packed (f16 with rotation, bf16 without) into TMEM columns as the A operand
       
       // qc and qpos (row tid = row) were loaded before the setup
+      // (PREFIX: the row of a request that does not share is not used, and its position may be any number: clamped alike,
+      // but unflagged)
       int pos = qpos;
-      if (ROPE && row_ok && (pos < 0 || pos >= a.max_pos)) {
-        atomicOr(a.err, kErrPosition);
+      if (ROPE && (pos < 0 || pos >= a.max_pos)) {
+        if (row_ok) atomicOr(a.err, kErrPosition);
         pos = 0;
       }
       if constexpr (ROPE) {
