@@ -389,6 +389,8 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
       const int rtok = row / G, rh = row - rtok * G;
       const int tq = tok0 + i * TQ + rtok;
       const bool row_ok = rtok < TQ && tq < ql;
+      // PREFIX: the row of a request shorter than the prefix is not used; what its query and position hold is not flagged
+      const bool flags = row_ok && (!PREFIX || __ldg(a.kv_lens + q0 + tq) >= kvl);
       U4 qc[D / 8];
       int pos = 0;
       if (row_ok) {
@@ -402,7 +404,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
         if (ROPE) {
           pos = a.q_pos[q0 + tq];
           if (pos < 0 || pos >= a.max_pos) {
-            atomicOr(a.err, kErrPosition);
+            if (flags) atomicOr(a.err, kErrPosition);
             pos = 0;
           }
         }
@@ -429,7 +431,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
           wq = ptx::watch_h2(ptx::watch_h2(ptx::watch_h2(ptx::watch_h2(wq, qc[c].x), qc[c].y), qc[c].z), qc[c].w);
-        if (row_ok && wq != 0u) atomicOr(a.err, kErrRange);
+        if (flags && wq != 0u) atomicOr(a.err, kErrRange);
       } else {
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {

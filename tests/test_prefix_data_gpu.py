@@ -8,7 +8,7 @@ from test_prefix_gpu import check, env, groups, run  # noqa: F401  (env: a fixtu
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (32, 2, 128), (3, 3, 128)])
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 128), (32, 2, 128), (3, 3, 128), (8, 2, 64), (16, 1, 64)])
 def test_rows_that_do_not_share_hold_anything(env, Hq, Hkv, d):
     """Empty rows of a padded batch inside the group, with positions outside the table and queries of NaN and infinities:
     zeros and -inf for them, unflagged, and the other rows as ever."""
