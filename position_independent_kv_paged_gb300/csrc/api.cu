@@ -1184,7 +1184,7 @@ PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, 
     w.items = (long long)w.max_waves * w.n_slots;
     if (w.items > units * tiles) w.items = units * tiles;
     if (w.items < units) w.items = units;
-    w.group_bytes = align_up((size_t)num_prefixes * sizeof(int2), 256);
+    w.group_bytes = align_up(((size_t)num_prefixes + 1) * sizeof(int2), 256);
     w.o_bytes = (size_t)w.items * prefix::kRows * D * sizeof(float);
     w.lse_bytes = (size_t)w.items * prefix::kRows * sizeof(float);
     // With many requests the own keys take long too: a kernel that waits for nothing of the first one runs beside it,
@@ -1246,6 +1246,7 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
   a.items = w.items;
   char* ws = static_cast<char*>(workspace) + w.list_bytes;
   a.group_items = reinterpret_cast<const int2*>(ws);
+  a.n_groups = reinterpret_cast<int*>(ws + (size_t)groups->num_prefixes * sizeof(int2));
   a.prefix_o = reinterpret_cast<const float*>(ws + w.group_bytes);
   a.prefix_lse = reinterpret_cast<const float*>(ws + w.group_bytes + w.o_bytes);
   if (w.apart) {

@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const __grid_constant_
   constexpr int U = 4, T = 256;
   const int i = blockIdx.x, h0 = blockIdx.y * heads_per, n = min(heads_per, a.Hq - h0) * (D / 4);
   const int L = __ldg(a.seq_lens + i);
-  const Shared sh = shared_of(a, a.cu_requests, a.prefix_blocks, i, L);
+  const Shared sh = shared_of(a, a.cu_requests, a.prefix_blocks, *a.n_groups, i, L);
   if (L <= 0 || sh.blocks == 0) return;  // written by the kernel before
   const int2 gi = prefix::items_of(a, sh.p, sh.q0, i);
   for (int base = threadIdx.x; base < n; base += U * T) {

@@ -227,13 +227,12 @@ __device__ __forceinline__ uint32_t distance(int t, int b) {
 enum List { kAll, kSelected, kPrefix, kApart };
 
 // The group of request i of length L, and the blocks it shares: the group's, if the request holds them all (else 0, as
-// where nothing is shared: no items).  cu
-// and nb: where the groups are read.
+// where nothing is shared: no items).  cu and nb: where the n_groups groups that count are read.
 struct Shared {
   int p, q0, blocks;
 };
-__device__ __forceinline__ Shared shared_of(const DecodeArgs& a, const int* cu, const int* nb, int i, int L) {
-  int lo = 0, hi = a.n_prefix;  // groups that begin at request i or before it
+__device__ __forceinline__ Shared shared_of(const DecodeArgs& a, const int* cu, const int* nb, int n_groups, int i, int L) {
+  int lo = 0, hi = n_groups;  // groups that begin at request i or before it
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (cu[mid] <= i) lo = mid + 1;
@@ -283,21 +282,33 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   // SHARE: the groups, staged while the stages hold nothing
   const int* grp_cu = a.cu_requests;
   const int* grp_nb = a.prefix_blocks;
+  [[maybe_unused]] int n_groups = a.n_prefix;  // that count: those in front of the first with descending boundaries
   if constexpr (SHARE)
-    if (a.n_prefix > 0 && a.n_prefix <= kStagedGroups) {
+    if (a.n_prefix > 0) {
       int* st = reinterpret_cast<int*>(sgen);
+      const bool staged = a.n_prefix <= kStagedGroups;
+      bool down = false;
       for (int p = threadIdx.x; p <= a.n_prefix; p += NW * 32) {
-        st[p] = __ldg(a.cu_requests + p);
-        if (p < a.n_prefix) st[kStagedGroups + 1 + p] = __ldg(a.prefix_blocks + p);
+        const int c = __ldg(a.cu_requests + p);
+        if (staged) st[p] = c;
+        if (p < a.n_prefix) {
+          down |= __ldg(a.cu_requests + p + 1) < c;
+          if (staged) st[kStagedGroups + 1 + p] = __ldg(a.prefix_blocks + p);
+        }
       }
-      grp_cu = st;
-      grp_nb = st + kStagedGroups + 1;
-      __syncthreads();
+      if (staged) {
+        grp_cu = st;
+        grp_nb = st + kStagedGroups + 1;
+      }
+      if (__syncthreads_or(down))
+        for (n_groups = 0; grp_cu[n_groups] <= grp_cu[n_groups + 1];) ++n_groups;
+      // for the join in a kernel of its own
+      if (LIST == kApart && blockIdx.x == 0 && threadIdx.x == 0) *a.n_groups = n_groups;
     }
   // blocks that the list of request i, of length Li, holds for each of its kv heads
   auto listed = [&]([[maybe_unused]] int i, int Li) {
     const int n = blocks_of(Li, mb);
-    if constexpr (SHARE) return n ? n - shared_of(a, grp_cu, grp_nb, i, Li).blocks : 0;
+    if constexpr (SHARE) return n ? n - shared_of(a, grp_cu, grp_nb, n_groups, i, Li).blocks : 0;
     else return LIST == kSelected ? min(n, a.max_sel) : n;
   };
 
@@ -408,7 +419,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   };
   // what a pair's request shares
   [[maybe_unused]] auto enter = [&](int i, int Li) {
-    const Shared sh = shared_of(a, grp_cu, grp_nb, i, Li);
+    const Shared sh = shared_of(a, grp_cu, grp_nb, n_groups, i, Li);
     sg.first = sh.blocks;
     sg.pre_q0 = sh.q0;
     sg.pre_p = sh.p;
@@ -418,7 +429,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       const int L = __ldg(a.seq_lens + i);
       if (listed(i, L)) continue;
       if constexpr (SHARE) {
-        const Shared sh = shared_of(a, grp_cu, grp_nb, i, L);
+        const Shared sh = shared_of(a, grp_cu, grp_nb, n_groups, i, L);
         if (LIST == kApart && L > 0 && sh.blocks > 0) {
           for (int e = threadIdx.x; e < a.Hq * D; e += NW * 32) a.own_o[(size_t)i * a.Hq * D + e] = 0.f;
           for (int e = threadIdx.x; e < a.Hq; e += NW * 32) a.own_lse[(size_t)i * a.Hq + e] = -CUDART_INF_F;

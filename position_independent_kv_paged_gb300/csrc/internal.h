@@ -46,6 +46,7 @@ struct DecodeArgs {
   const int32_t* prefix_blocks;  // [n_prefix]
   int n_prefix, max_requests, max_prefix;  // bounds of a group's requests and shared blocks
   const int2* group_items;       // [n_prefix] first item and parts (written for groups that share something)
+  int* n_groups;                 // groups that count (own_o set: written by the list kernel, read by the join's)
   long long items;               // that the partial results have room for (0: nothing is shared)
   const float* prefix_o;         // [items][256][D]
   const float* prefix_lse;       // [items][256] log2

@@ -160,7 +160,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
     const int tiles = (item->g.blocks + NB - 1) / NB;  // at least as many as parts
     t_first = (int)((long long)item->part * tiles / item->parts);
     t_end = (int)((long long)(item->part + 1) * tiles / item->parts);
-    if (tid == 0 && item->index == item->first) a.group_items[item->p] = make_int2((int)item->first, item->parts);
+    if (tid == 0 && item->index == item->first) a.group_items[item->p] = make_int2(item->first, item->parts);
     // the first request that holds the whole prefix; every warp looks for itself
     trow = -1;
     for (int i = 0; i < ql && trow < 0; i += 32) {
@@ -390,7 +390,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
       const int tq = tok0 + i * TQ + rtok;
       const bool row_ok = rtok < TQ && tq < ql;
       // PREFIX: the row of a request shorter than the prefix is not used; what its query and position hold is not flagged
-      const bool flags = row_ok && (!PREFIX || __ldg(a.kv_lens + q0 + tq) >= kvl);
+      auto used = [&] { return row_ok && (!PREFIX || __ldg(a.kv_lens + q0 + tq) >= kvl); };
       U4 qc[D / 8];
       int pos = 0;
       if (row_ok) {
@@ -404,7 +404,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
         if (ROPE) {
           pos = a.q_pos[q0 + tq];
           if (pos < 0 || pos >= a.max_pos) {
-            if (flags) atomicOr(a.err, kErrPosition);
+            if (used()) atomicOr(a.err, kErrPosition);
             pos = 0;
           }
         }
@@ -431,7 +431,7 @@ __device__ __forceinline__ void prefill2_cta(const CUtensorMap* kmap_p, const CU
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
           wq = ptx::watch_h2(ptx::watch_h2(ptx::watch_h2(ptx::watch_h2(wq, qc[c].x), qc[c].y), qc[c].z), qc[c].w);
-        if (flags && wq != 0u) atomicOr(a.err, kErrRange);
+        if (wq != 0u && used()) atomicOr(a.err, kErrRange);
       } else {
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {

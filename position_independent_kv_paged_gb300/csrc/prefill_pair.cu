@@ -216,7 +216,7 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
     t_first = (int)((long long)item->part * tiles / item->parts);
     t_end = (int)((long long)(item->part + 1) * tiles / item->parts);
     if (tid == 0 && crank == 0 && item->index == item->first)
-      a.group_items[item->p] = make_int2((int)item->first, item->parts);
+      a.group_items[item->p] = make_int2(item->first, item->parts);
     // the first request that holds the whole prefix; every warp looks for itself
     trow = -1;
     for (int i = 0; i < ql && trow < 0; i += 32) {

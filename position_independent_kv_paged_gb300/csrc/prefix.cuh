@@ -19,19 +19,21 @@ constexpr int kMaxParts = 64;
 // What an item costs besides its tiles (start, query, end), in tiles.
 constexpr int kItemCost = 3;
 
+// Only groups in front of the first one whose boundaries descend count (that one is flagged): their boundaries ascend, so
+// that no two groups that share hold one request, and there are no more items than the host planned for.
 struct Group {
-  int q0, n;   // requests q0 .. q0 + n - 1 of the batch
+  int q0, n;   // requests q0 .. q0 + n - 1 of the batch (n -1: the boundaries descend)
   int blocks;  // that they share (0: nothing)
 };
 
 // A group as the tables and the planning bounds allow it (most_blocks: the lower bound of a prefix); `bad`: its numbers
-// are outside them or the batch.
+// are outside them or the batch, and it shares nothing.
 __device__ __forceinline__ Group group(int c0, int c1, int nb, int batch, int most_blocks, int max_requests, bool& bad) {
   bad = c0 < 0 || c1 < c0 || c1 > batch || (long long)c1 - c0 > max_requests || nb < 0 || nb > most_blocks;
   Group g;
-  g.q0 = max(0, min(c0, batch));
-  g.n = max(0, min(c1, batch) - g.q0);
-  g.blocks = g.n >= kMinRequests && g.n <= max_requests && nb > 0 && nb <= most_blocks ? nb : 0;
+  g.q0 = c0;
+  g.n = c1 < c0 ? -1 : (bad ? 0 : c1 - c0);
+  g.blocks = g.n >= kMinRequests ? nb : 0;
   return g;
 }
 __device__ __forceinline__ Group group(const PrefillArgs& a, int p) {
@@ -44,7 +46,7 @@ __device__ __forceinline__ Group group(const PrefillArgs& a, int p) {
 // are numbered group by group, then pair, head, part; `first` is the group's first.
 struct Item {
   int p, pair, head, part, parts;
-  long long first, index;
+  int first, index;  // places of the grid
   Group g;
 };
 
@@ -60,11 +62,17 @@ __device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
   auto units = [&](const Group& g) { return g.blocks ? (long long)((g.n + 2 * tq - 1) / (2 * tq)) * a.Hkv : 0LL; };
   long long n_units = 0, work = 0;
   int longest = 1;
-  for (int p = lane; p < a.batch; p += 32) {
-    const Group g = group(a, p);
-    n_units += units(g);
-    work += units(g) * tiles(g.blocks);
-    if (g.blocks) longest = max(longest, tiles(g.blocks));
+  int n_groups = a.batch;  // that count
+  for (int base = 0; base < n_groups; base += 32) {
+    Group g{0, 0, 0};
+    if (base + lane < n_groups) g = group(a, base + lane);
+    const unsigned down = __ballot_sync(FULL, g.n < 0);
+    if (down) n_groups = base + __ffs(down) - 1;
+    if (g.blocks && base + lane < n_groups) {
+      n_units += units(g);
+      work += units(g) * tiles(g.blocks);
+      longest = max(longest, tiles(g.blocks));
+    }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -89,9 +97,9 @@ __device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
   if (work < 1 << 24 && n_units < 1 << 12) plan((unsigned)n_units, (unsigned)work);  // 64-bit division is slow
   else plan((unsigned long long)n_units, (unsigned long long)work);
   long long before = 0;
-  for (int base = 0; base < a.batch; base += 32) {
+  for (int base = 0; base < n_groups; base += 32) {
     Group g{0, 0, 0};
-    if (base + lane < a.batch) g = group(a, base + lane);
+    if (base + lane < n_groups) g = group(a, base + lane);
     const int parts = g.blocks ? (tiles(g.blocks) + len - 1) / len : 0;
     long long sum = units(g) * parts;  // ... of the lanes up to this one
 #pragma unroll
@@ -104,12 +112,12 @@ __device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
       const int l = __ffs(has) - 1;
       it.p = base + l;
       it.parts = __shfl_sync(FULL, parts, l);
-      it.first = before + __shfl_sync(FULL, sum - units(g) * parts, l);
-      it.index = c;
+      it.first = (int)(before + __shfl_sync(FULL, sum - units(g) * parts, l));
+      it.index = (int)c;
       it.g.q0 = __shfl_sync(FULL, g.q0, l);
       it.g.n = __shfl_sync(FULL, g.n, l);
       it.g.blocks = __shfl_sync(FULL, g.blocks, l);
-      const unsigned k = (unsigned)(c - it.first);  // an index of the grid
+      const unsigned k = (unsigned)(it.index - it.first);
       it.part = (int)(k % it.parts);
       it.head = (int)(k / it.parts % a.Hkv);
       it.pair = (int)(k / it.parts / a.Hkv);
@@ -121,7 +129,7 @@ __device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
 }
 
 // The first item and the parts of request i's group p, which begins at request q0 (as the kernel that computed them
-// wrote it).  Groups that overlap (flagged) may lead out of the items: no part.
+// wrote it: each of its items has a CTA, see Group).
 __device__ __forceinline__ int2 items_of(const DecodeArgs& a, int p, int q0, int i) {
   const int2 gi = __ldcg(a.group_items + p);
   const long long pair = (i - q0) / (2 * (128 / a.G));

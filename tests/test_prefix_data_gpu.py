@@ -24,3 +24,38 @@ def test_rows_that_do_not_share_hold_anything(env, Hq, Hkv, d):
         t["q"][r] = float("nan") if r % 2 else float("inf")
     check(env, t, run(env, t), f"{Hq}/{Hkv} d{d}")
     assert mp.device_error() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_groups_share_nothing(env, d):
+    """Groups whose numbers lie outside the batch or the planning bounds, or whose boundaries descend, and every group
+    behind descending ones, are flagged and read their own keys: rows that they hold begin with different blocks."""
+    torch, mp, dev = env
+    t = groups(torch, dev, [400, 420, 440, 460, 500, 380, 0, 390], [0, 3], [10], 8, 2, d, 43)   # requests 0 .. 2 share
+    for cu, blocks in (([0, 3, 9], [10, 12]), ([0, 3, 8], [10, 33]), ([0, 3, 2, 6], [10, 12, 12]), ([-1, 3, 6], [10, 0]),
+                       ([3, 0, 8], [10, 12]), ([0, 3, 1, 8, 8], [10, 3, 12, 4]), ([0, 3, -5, 8], [10, 3, 12]),
+                       ([0, 3, 2 ** 31 - 1, 8, -2 ** 31, 8], [10, 12, 12, 12, 12]), ([-2 ** 31, 2 ** 31 - 1], [10])):
+        t["cu"], t["blocks"] = (torch.tensor(x, dtype=torch.int32, device=dev) for x in (cu, blocks))
+        got = run(env, t, max_requests=6, max_prefix_blocks=10 ** 6)
+        assert mp.device_error(clear=True) == 4, (cu, blocks)
+        check(env, t, got, f"d{d} {cu}")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,B", [(8, 8, 64, 200), (8, 8, 128, 160), (4, 2, 128, 60)])
+def test_overlapping_groups(env, Hq, Hkv, d, B):
+    """Groups that go over the same requests again and again (flagged), more than are staged among them: no item is left
+    without a CTA, whatever an earlier call left in the workspace, with the join in the same kernel or its own."""
+    torch, mp, dev = env
+    t = groups(torch, dev, [16 * 40 + 5 * i % 130 for i in range(B)], [0, B // 2], [40], Hq, Hkv, d, 47)
+    mb = t["block_tables"].shape[1]
+    ws = torch.zeros(max(mp.attn_decode_prefix_workspace_size(B, Hq, Hkv, d, mb, n, B, 10 ** 6) for n in (1, 9, 300)),
+                     dtype=torch.uint8, device=dev)
+    check(env, t, run(env, t, workspace=ws, max_requests=B), "one group")
+    assert mp.device_error() == 0
+    for n in (9, 300):
+        cu = [0] * (n - 7) + [B // 2, 0, B, 0, B, 3, B, 1]
+        t["cu"], t["blocks"] = (torch.tensor(x, dtype=torch.int32, device=dev) for x in (cu, [40] * n))
+        got = run(env, t, workspace=ws, max_requests=B)
+        assert mp.device_error(clear=True) == 4
+        check(env, t, got, f"{n} groups")
+        assert not ws[:65536].any()
