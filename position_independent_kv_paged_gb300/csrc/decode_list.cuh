@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   [[maybe_unused]] auto join_prefix = [&](int n, const float* pl, int next, const float* po, float4& O, float& lse2) {
     float M = lse2;
     for (int s = 0; s < n; ++s) M = fmaxf(M, pl[s * next]);
-    if (M == -CUDART_INF_F) return;
+    if (M == -CUDART_INF_F) M = 0.f;  // no key at all: every weight is 0 (or NaN, which fmaxf passes over)
     float sum = exp2f(lse2 - M);
     O.x *= sum;
     O.y *= sum;
@@ -409,9 +409,9 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
       O.z = fmaf(p.z, w, O.z);
       O.w = fmaf(p.w, w, O.w);
     }
-    const float inv = 1.f / sum;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-    lse2 = M + log2f(sum);
+    lse2 = sum == 0.f ? -CUDART_INF_F : M + log2f(sum);
   };
   auto store4 = [&](size_t hq, int dim, const float4& o) {
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + hq * D + dim) =

@@ -59,3 +59,21 @@ def test_overlapping_groups(env, Hq, Hkv, d, B):
         assert mp.device_error(clear=True) == 4
         check(env, t, got, f"{n} groups")
         assert not ws[:65536].any()
+
+
+@pytest.mark.parametrize("Hkv,d,B", [(2, 64, 6), (2, 128, 6), (8, 64, 160), (8, 128, 120)])
+def test_a_nan_query_shows(env, Hkv, d, B):
+    """A query with a NaN element makes its head's row NaN, lse too, and no other: for a request that ends with its
+    prefix, one whose own keys are all masked, and one with keys of its own; with the join in the same kernel or its own."""
+    torch, mp, dev = env
+    lens = [16 * 40 + 11 * i % 90 for i in range(B)]
+    lens[1], lens[3] = 16 * 40, 16 * 41
+    t = groups(torch, dev, lens, [0, B], [40], 2 * Hkv, Hkv, d, 53)
+    t["block_tables"][3, 40] = -1
+    for r in (1, 3, 4):
+        t["q"][r, 1, 7] = float("nan")
+    out, lse = run(env, t, max_requests=B)
+    assert mp.device_error(clear=True) == 1 | 16    # the block id, and a query outside fp16
+    nan = torch.zeros_like(lse, dtype=torch.bool)
+    nan[[1, 3, 4], 1] = True
+    assert torch.equal(lse.isnan(), nan) and torch.equal(out.isnan(), nan[..., None].expand_as(out))
