@@ -52,10 +52,10 @@
  *  allocating it; every call leaves those counters zero again (after a call that
  *  reports MINIPIC_DEVERR_TIMEOUT, zero it again before reuse).  The counters have
  *  64 KB to themselves in every decode call (minipic_attn_decode and its
- *  prerotated form, _mixed, _decode_q8, _decode_weights), so calls of any kind and
- *  shape may follow one another on one workspace that is large enough for each, as
- *  long as each has at most 16384 (request, kv head) pairs (else zero it when the
- *  shape or the call changes).  All calls are asynchronous on the
+ *  prerotated form, _mixed, _decode_q8, _decode_weights, _decode_selected and its q8
+ *  form, _decode_prefix; a call of more than 16384 (request, kv head) pairs clears
+ *  those past 64 KB itself), so calls of any kind and shape may follow one another on
+ *  one workspace that is large enough for each.  All calls are asynchronous on the
  *  given stream (cudaStream_t; NULL = legacy default stream) and act on the
  *  device current at the call.  Inputs must stay valid until the work completes.
  *  The library looks up the device address of its error word once per device

@@ -58,6 +58,14 @@ size_t counter_bytes(int batch, int Hkv) {
   return cnt > kCounterRegion ? cnt : kCounterRegion;
 }
 
+// Counters past the region that every call keeps for them lie where calls of fewer pairs keep their partial results:
+// cleared before the kernels (a memset of 4 bytes a pair, in calls of more than 16384 pairs alone).
+cudaError_t clear_far_counters(const DecodeArgs& a, cudaStream_t s) {
+  const size_t bytes = (size_t)a.batch * a.Hkv * sizeof(int);
+  if (!a.counters || bytes <= kCounterRegion) return cudaSuccess;
+  return cudaMemsetAsync(reinterpret_cast<char*>(a.counters) + kCounterRegion, 0, bytes - kCounterRegion, s);
+}
+
 DecodeWs decode_ws(int batch, int Hq, int Hkv, int D, int n_split) {
   return decode_ws_layout(batch, Hq, Hkv, D, n_split);
 }
@@ -186,7 +194,7 @@ long long count_partials(const DecodePlan& p, int batch, int Hq, int G) {
 
 // Place the workspace of an e4m3 or block-weight decode.
 minipic_status place_weights_ws(DecodeArgs& a, const DecodePlan& plan, void* block_weights, void* workspace,
-                                size_t workspace_bytes) {
+                                size_t workspace_bytes, cudaStream_t s) {
   const long long partials = count_partials(plan, a.batch, a.Hq, a.G);
   const DecodeWsW w = decode_ws_weights(a.batch, a.Hq, a.Hkv, a.D, partials, block_weights ? a.max_blocks : 0);
   if (w.total > 0 && (!workspace || workspace_bytes < w.total || !aligned16(workspace))) return MINIPIC_ERR_WORKSPACE;
@@ -195,6 +203,7 @@ minipic_status place_weights_ws(DecodeArgs& a, const DecodePlan& plan, void* blo
     a.counters = reinterpret_cast<int*>(p);
     a.part_o = reinterpret_cast<float*>(p + w.cnt_bytes);
     a.part_ml = reinterpret_cast<float*>(p + w.cnt_bytes + w.o_bytes);
+    if (clear_far_counters(a, s) != cudaSuccess) return MINIPIC_ERR_CUDA;
   }
   if (block_weights) {
     a.weights = block_weights;
@@ -224,7 +233,8 @@ minipic_status decode_common(minipic_dtype dtype, int32_t num_q_heads, const min
   const minipic_status st =
       build_decode(dtype, num_q_heads, kv, rope, b, scale, workspace, workspace_bytes, rotate, &a, &plan, &empty);
   if (st != MINIPIC_OK || empty) return st;
-  const cudaError_t e = launch_decode(a, dtype == MINIPIC_BF16, rotate, plan, stream);
+  cudaError_t e = clear_far_counters(a, stream);
+  if (e == cudaSuccess) e = launch_decode(a, dtype == MINIPIC_BF16, rotate, plan, stream);
   return e == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }
 
@@ -558,14 +568,15 @@ minipic_status minipic_attn_mixed(minipic_dtype dtype, int32_t num_q_heads, cons
   st = build_decode(dtype, num_q_heads, kv, rope, decode, scale, workspace, workspace_bytes, true, &d, &plan,
                     &d_empty);
   if (st != MINIPIC_OK) return st;
-  cudaError_t e = cudaSuccess;
   if (p_empty && d_empty) return MINIPIC_OK;
+  if (!p_empty && !d_empty && kv->num_blocks == 0) return MINIPIC_ERR_INVALID;
+  cudaError_t e = clear_far_counters(d, (cudaStream_t)stream);
+  if (e != cudaSuccess) return MINIPIC_ERR_CUDA;
   if (d_empty) {
     e = launch_prefill_tc(p, true, (cudaStream_t)stream);
   } else if (p_empty) {
     e = launch_decode(d, true, true, plan, (cudaStream_t)stream);
   } else {
-    if (kv->num_blocks == 0) return MINIPIC_ERR_INVALID;
     replan_mixed_decode(d, current_sms());
     e = launch_mixed(p, d, (cudaStream_t)stream);
   }
@@ -737,9 +748,9 @@ minipic_status minipic_attn_decode_weights(minipic_dtype dtype, int32_t num_q_he
   const DecodePlan plan = plan_decode_list(b->batch, kv->num_kv_heads, num_q_heads / kv->num_kv_heads, kv->head_dim,
                                            b->max_blocks_per_seq, bf16, sms);
   DecodeArgs a = decode_args(bf16, num_q_heads, kv, rope, b, scale, plan, err);
-  st = place_weights_ws(a, plan, block_weights, workspace, workspace_bytes);
-  if (st != MINIPIC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
+  st = place_weights_ws(a, plan, block_weights, workspace, workspace_bytes, s);
+  if (st != MINIPIC_OK) return st;
   a.cs_f16 = rope->cos_sin_f16;
   // the tensor-core kernel merges its parts itself; with no pool every key is masked
   const bool mma = plan.use_mma && kv->num_blocks > 0;
@@ -779,9 +790,9 @@ minipic_status minipic_attn_decode_q8(minipic_dtype dtype, int32_t num_q_heads, 
   DecodeArgs a = decode_args(bf16, num_q_heads, &pool, rope, b, scale, plan, err);
   a.k_scale = kv->k_scale;
   a.v_scale = kv->v_scale;
-  st = place_weights_ws(a, plan, block_weights, workspace, workspace_bytes);
-  if (st != MINIPIC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
+  st = place_weights_ws(a, plan, block_weights, workspace, workspace_bytes, s);
+  if (st != MINIPIC_OK) return st;
   a.cs_f16 = rope->cos_sin_f16;
   // the tensor-core kernel merges its parts itself; with no pool every key is masked
   const bool mma = plan.use_mma && kv->num_blocks > 0;
@@ -980,7 +991,7 @@ minipic_status decode_selected(minipic_dtype dtype, int32_t num_q_heads, const m
   a.v_scale = v_scale;
   a.selected = selected;
   a.max_sel = max_selected;
-  st = place_weights_ws(a, plan, nullptr, workspace, workspace_bytes);
+  st = place_weights_ws(a, plan, nullptr, workspace, workspace_bytes, s);
   if (st != MINIPIC_OK) return st;
   a.cs_f16 = rope->cos_sin_f16;
   // the tensor-core kernel merges its parts itself; with no pool every key is masked
@@ -1235,7 +1246,8 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
                                groups->num_prefixes, groups->max_requests, groups->max_prefix_blocks, sms);
   if (!workspace || workspace_bytes < w.total || !aligned16(workspace)) return MINIPIC_ERR_WORKSPACE;
   DecodeArgs a = decode_args(true, num_q_heads, kv, rope, b, scale, w.plan, err);
-  st = place_weights_ws(a, w.plan, nullptr, workspace, w.list_bytes);
+  const cudaStream_t s = (cudaStream_t)stream;
+  st = place_weights_ws(a, w.plan, nullptr, workspace, w.list_bytes, s);
   if (st != MINIPIC_OK) return st;
   a.cs_f16 = rope->cos_sin_f16;
   a.cu_requests = groups->cu_requests;
@@ -1253,7 +1265,6 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
     a.own_o = reinterpret_cast<float*>(ws + w.group_bytes + w.o_bytes + w.lse_bytes);
     a.own_lse = reinterpret_cast<float*>(ws + w.group_bytes + w.o_bytes + w.lse_bytes + w.own_bytes);
   }
-  const cudaStream_t s = (cudaStream_t)stream;
   if (w.items > 0) {
     PrefillArgs p{};
     p.q = a.q;

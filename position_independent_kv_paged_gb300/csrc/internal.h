@@ -275,7 +275,8 @@ cudaError_t launch_kv_offload(const OffloadArgs& a, bool to_host, int num_sms, c
 // Bytes at the start of every decode workspace that hold its completion counters
 // (more only where 16384 pairs of request and kv head do not do), whatever the
 // call, its shape and its split count: no call leaves anything else there, so
-// calls of all kinds on one workspace find the counters zero.
+// calls of all kinds on one workspace find the counters zero (those past the region,
+// where other calls' partial results lie, are cleared by the call that has them).
 constexpr size_t kCounterRegion = 65536;
 
 // Byte layout of the decode workspace: one completion counter per (request,

@@ -1,0 +1,59 @@
+"""Decode calls of more (request, kv head) pairs than the 64 KB of counters hold, on a workspace that other calls use."""
+
+import pytest
+
+from list_util import make_batch
+from test_prefix_gpu import env  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def calls(torch, mp, t, rope):
+    """(workspace bytes, call(workspace) -> out) of every decode call that cuts pairs, over one batch."""
+    B, Hq, d = t["q"].shape
+    Hkv, mb, dev = t["Hkv"], t["block_tables"].shape[1], t["q"].device
+    a = (t["q"], t["k_pool"], t["v_pool"], t["block_tables"], t["block_starts"], t["seq_lens"], t["q_pos"], rope)
+    sel = torch.arange(mb, dtype=torch.int32, device=dev).expand(B, Hkv, mb).contiguous()
+    cu = torch.tensor([0, B], dtype=torch.int32, device=dev)
+    none = torch.zeros(1, dtype=torch.int32, device=dev)
+    bw = torch.zeros(B, Hkv, mb, dtype=torch.bfloat16, device=dev)
+    return {
+        "attn_decode": (mp.decode_workspace_size(B, Hq, Hkv, d, mb),
+                        lambda ws: mp.attn_decode(*a, workspace=ws)[0]),
+        "weights": (mp.attn_decode_weights_workspace_size(B, Hq, Hkv, d, mb),
+                    lambda ws: mp.attn_decode_weights(*a, bw, workspace=ws)[0]),
+        "selected": (mp.attn_decode_selected_workspace_size(B, Hq, Hkv, d, mb),
+                     lambda ws: mp.attn_decode_selected(*a, sel, workspace=ws)[0]),
+        "prefix": (mp.attn_decode_prefix_workspace_size(B, Hq, Hkv, d, mb, 1, B, 0),
+                   lambda ws: mp.attn_decode_prefix(*a, cu, none, max_requests=B, max_prefix_blocks=0, workspace=ws)[0]),
+    }
+
+
+@pytest.mark.parametrize("Hkv", [8, 9])
+def test_one_workspace_for_more_than_16384_pairs(env, Hkv):
+    """Requests whose counters lie past 64 KB have their lists cut: the same bits on a workspace of zeros, after calls of
+    few requests have left their partial results there, and after their own kind."""
+    torch, mp, dev = env
+    B = 16384 // Hkv + 40
+    lens = [5 + r % 20 for r in range(B)]
+    for r in (B - 1, B - 7, B - 20, 3):
+        lens[r] = 16 * 1200 + r % 16
+    big = make_batch(torch, dev, lens, Hkv, Hkv, 64, "bf16", Hkv)
+    small = make_batch(torch, dev, [9000, 12000, 800, 7000], 4 * Hkv, Hkv, 64, "bf16", 3)
+    rope = mp.rope_table(max(big["max_pos"], small["max_pos"]), 64, big["base"], device=dev)
+    many, few = (calls(torch, mp, t, rope) for t in (big, small))
+    ws = torch.zeros(max(n for c in (many, few) for n, _ in c.values()), dtype=torch.uint8, device=dev)
+    assert B * Hkv > 16384
+    for name, (n, call) in many.items():
+        want = call(torch.zeros(n, dtype=torch.uint8, device=dev))
+        want_few = {}
+        for other, (m, dirty) in few.items():
+            want_few[other] = dirty(torch.zeros(m, dtype=torch.uint8, device=dev))
+            got = dirty(ws)
+            assert torch.equal(got, want_few[other]), other
+            ws[65536:].fill_(0x11)   # as partial results of any call would
+            assert torch.equal(call(ws), want), (name, other)
+            assert torch.equal(call(ws), want), (name, "again")
+            assert torch.equal(dirty(ws), want_few[other]), (other, "after", name)
+            assert not ws[:65536].any()
+    assert mp.device_error() == 0
