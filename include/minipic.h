@@ -586,7 +586,8 @@ typedef struct {
  * UNSUPPORTED for max_blocks_per_seq of 2^27 or more.  Asynchronous on `stream`. */
 minipic_status minipic_block_select(const minipic_block_select_batch* batch, minipic_stream_t stream);
 
-/* Workspace bytes of minipic_attn_decode_selected and its q8 form. */
+/* Workspace bytes of minipic_attn_decode_selected and its q8 form: enough for this
+ * shape and for every smaller batch and max_selected. */
 size_t minipic_attn_decode_selected_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                    int32_t head_dim, int32_t max_selected, int32_t block_size);
 
@@ -622,7 +623,8 @@ typedef struct {
   int32_t max_prefix_blocks;     /* an upper bound of every prefix (grid planning) */
 } minipic_prefix_groups;
 
-/* Workspace bytes of minipic_attn_decode_prefix for this shape. */
+/* Workspace bytes of minipic_attn_decode_prefix: enough for this shape and for every
+ * smaller batch, table, number of prefixes and bound. */
 size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                  int32_t head_dim, int32_t max_blocks_per_seq, int32_t num_prefixes,
                                                  int32_t max_requests, int32_t max_prefix_blocks, int32_t block_size);

@@ -1062,6 +1062,14 @@ def attn_decode_selected_q8(q, k_pool, v_pool, k_scale, v_scale, block_tables, b
                             selected, scale, out, lse, workspace, stream)
 
 
+def _fresh(size, device):
+    """A workspace of a decode call: zero where the counters lie."""
+    torch = _torch()
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+    ws[:65536].zero_()
+    return ws
+
+
 def _decode_selected(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_starts, seq_lens, q_pos, rope, selected,
                      scale, out, lse, workspace, stream):
     torch = _torch()
@@ -1091,8 +1099,7 @@ def _decode_selected(q, k_pool, v_pool, k_scale, v_scale, block_tables, block_st
         o = torch.empty_like(q) if out is None else out
         ws = workspace
         if ws is None:
-            size = attn_decode_selected_workspace_size(B, Hq, hkv, d, S, bs)
-            ws = torch.zeros(max(size, 1), dtype=torch.uint8, device=q.device)
+            ws = _fresh(attn_decode_selected_workspace_size(B, Hq, hkv, d, S, bs), q.device)
         db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
                      q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
         _check(fn(code, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db), scale, selected.data_ptr(), S,
@@ -1145,8 +1152,8 @@ def attn_decode_prefix(q, k_pool, v_pool, block_tables, block_starts, seq_lens, 
         o = torch.empty_like(q) if out is None else out
         ws = workspace
         if ws is None:
-            size = attn_decode_prefix_workspace_size(B, Hq, hkv, d, mb, P, max_requests, max_prefix_blocks, bs)
-            ws = torch.zeros(max(size, 1), dtype=torch.uint8, device=q.device)
+            ws = _fresh(attn_decode_prefix_workspace_size(B, Hq, hkv, d, mb, P, max_requests, max_prefix_blocks, bs),
+                        q.device)
         db = _Decode(q.data_ptr(), block_tables.data_ptr(), block_starts.data_ptr(), seq_lens.data_ptr(),
                      q_pos.data_ptr(), B, mb, o.data_ptr(), _ptr(lse))
         _check(L.minipic_attn_decode_prefix(BF16, Hq, ctypes.byref(kv), ctypes.byref(rp), ctypes.byref(db),

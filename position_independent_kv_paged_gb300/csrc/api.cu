@@ -430,7 +430,7 @@ DecodePlan plan_decode_lists(int batch, int Hkv, int G, int D, int max_blocks, b
   // blocks: 54 and 56, of 64: 113 both).  Beyond 65536 pairs the ranges hold many each, and partial results for every CTA
   // would take gigabytes.
   const long long pairs = (long long)batch * Hkv;
-  if (bf16 && pairs >= 2LL * p.n_split && pairs <= (1 << 16)) {
+  if (bf16 && pairs >= 2LL * p.n_split && pairs <= kMaxCtaPairs) {
     p.list_heads = Hkv % 2 ? 1 : 2;
     p.n_split += (int)pairs / p.list_heads;
   }
@@ -952,17 +952,30 @@ minipic_status minipic_kv_evict(minipic_dtype dtype, const minipic_kv_evict_batc
 
 namespace {
 
+// The size queries of these calls return what is enough for every smaller batch, table and bound too, so that a server
+// sizes one workspace for its largest; a call needs the bytes of its own plan.
+// Lists of the tensor-core kernel: its CTAs become no fewer with more pairs, but for the end of a CTA a pair.
+size_t most_list_bytes(int batch, int Hq, int Hkv, int D, int mb, int sms) {
+  size_t most = 0;
+  const long long last = kMaxCtaPairs / Hkv < 1 ? 1 : kMaxCtaPairs / Hkv;  // the largest batch of a CTA a pair
+  for (const int n : {batch, batch < last ? batch : (int)last}) {
+    const DecodePlan p = plan_decode_lists(n, Hkv, Hq / Hkv, D, mb, true, sms);
+    const size_t bytes = decode_ws_weights(n, Hq, Hkv, D, count_partials(p, n, Hq, Hq / Hkv), 0).total;
+    most = bytes > most ? bytes : most;
+  }
+  return most;
+}
+
 // Decode over selected blocks: lists of at most S blocks a pair.
 size_t selected_ws_size(int32_t batch, int32_t Hq, int32_t Hkv, int32_t D, int32_t S, int32_t bs) {
   if (batch <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || S <= 0 || bs <= 0 || Hq % Hkv) return 0;
   const int sms = current_sms();
-  size_t most = 0;
-  for (int bf16 = 0; bf16 < 2; ++bf16) {
-    const DecodePlan p = plan_decode_lists(batch, Hkv, Hq / Hkv, D, S, bf16 != 0, sms);
-    const size_t n = decode_ws_weights(batch, Hq, Hkv, D, count_partials(p, batch, Hq, Hq / Hkv), 0).total;
-    most = n > most ? n : most;
-  }
-  return most;
+  const size_t lists = most_list_bytes(batch, Hq, Hkv, D, S, sms);
+  // f32: n pairs below 4 an SM have min(ceil(4 SMs / n), ceil(S / 8)) splits at most
+  const long long target = 4LL * sms, splits = (S + 7LL) / 8, pairs = (long long)batch * Hkv;
+  const long long n = pairs < target ? pairs : target - 1, cut = target + n - 1 < n * splits ? target + n - 1 : n * splits;
+  const size_t simt = decode_ws_weights(batch, Hq, Hkv, D, splits > 1 ? cut * (Hq / Hkv) : 0, 0).total;
+  return simt > lists ? simt : lists;
 }
 
 minipic_status decode_selected(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
@@ -1155,6 +1168,25 @@ namespace {
 // 13.5 and 22.0; 16 x 2048, 34: 24.0 and 28.1; 2 x 32768, 36: 43.5 and 62.5; 16 x 4096, 67: 35.4 and 30.0; 64 x 2048 of
 // 28 / 4 heads, 71: 44.9 and 33.3).
 constexpr long long kShareAbove = 56;
+constexpr int kMaxWaves = 8;
+struct PrefixItems {
+  int n_slots;       // items at once: a cluster of two SMs each, or one SM
+  long long units;   // pairs of query tiles and kv heads, at most
+  long long tiles;   // of a prefix, at most
+};
+PrefixItems prefix_items(int batch, int Hkv, int G, int D, int num_prefixes, int max_requests, int max_prefix_blocks,
+                         int sms) {
+  PrefixItems it{};
+  const int tq = 128 / G, tile = D == 128 ? prefix::kTileBlocks<128> : prefix::kTileBlocks<64>;
+  it.n_slots = D == 128 ? (sms > 1 ? sms / 2 : 1) : sms;
+  // query-tile pairs: of all requests together, and one more a group that ends inside one
+  const long long most = max_requests < batch ? max_requests : batch;
+  const long long groups = num_prefixes < batch ? num_prefixes : batch;
+  const long long each = groups * ((most + 2 * tq - 1) / (2 * tq)), all = batch / (2 * tq) + groups;
+  it.units = Hkv * (each < all ? each : all);
+  it.tiles = (max_prefix_blocks + tile - 1LL) / tile;
+  return it;
+}
 struct PrefixWs {
   DecodePlan plan;
   int n_slots, max_waves;
@@ -1172,16 +1204,11 @@ PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, 
   const long long members = (long long)num_prefixes * max_requests < batch ? (long long)num_prefixes * max_requests : batch;
   const long long saved = (members - num_prefixes) * Hkv * max_prefix_blocks;  // blocks and kv heads not read again
   if (num_prefixes > 0 && max_requests >= prefix::kMinRequests && saved > kShareAbove * ctas && G <= 16) {
-    const int tq = 128 / G, tile = D == 128 ? prefix::kTileBlocks<128> : prefix::kTileBlocks<64>;
-    w.n_slots = D == 128 ? (sms > 1 ? sms / 2 : 1) : sms;  // a cluster of two SMs an item, or one SM
-    // query-tile pairs: of all requests together, and one more a group that ends inside one
-    const long long most = max_requests < batch ? max_requests : batch;
-    const long long groups = num_prefixes < batch ? num_prefixes : batch;
-    const long long each = groups * ((most + 2 * tq - 1) / (2 * tq)), all = batch / (2 * tq) + groups;
-    const long long units = Hkv * (each < all ? each : all);
-    const long long tiles = (max_prefix_blocks + tile - 1LL) / tile;
+    const PrefixItems it = prefix_items(batch, Hkv, G, D, num_prefixes, max_requests, max_prefix_blocks, sms);
+    const long long units = it.units, tiles = it.tiles;
+    w.n_slots = it.n_slots;
     long long least = 0;
-    for (int n = 1; n <= 8; ++n) {
+    for (int n = 1; n <= kMaxWaves; ++n) {
       const long long room = (long long)n * w.n_slots - units;
       if (room <= 0) continue;
       const long long len = (units * tiles + room - 1) / room;
@@ -1211,6 +1238,31 @@ PrefixWs prefix_ws(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, 
   return w;
 }
 
+// The most that prefix_ws asks for at this shape or any smaller one: not every batch that shares takes the most waves,
+// and a smaller one may share where this one does not.
+size_t prefix_ws_size(int batch, int Hq, int Hkv, int D, int mb, int num_prefixes, int max_requests,
+                      int max_prefix_blocks, int sms) {
+  const int G = Hq / Hkv;
+  size_t bytes = most_list_bytes(batch, Hq, Hkv, D, mb, sms);
+  const long long most = max_requests < batch ? max_requests : batch;
+  const long long groups = num_prefixes < batch ? num_prefixes : batch;
+  const long long members = groups * most < batch ? groups * most : batch;
+  // CTAs: as many as run at once, or as a smaller batch has blocks, of which a request has one at least
+  const long long resident = plan_decode_list(kMaxGridYZ, Hkv, G, D, mb, true, sms).n_split;
+  const bool shares = groups > 0 && most >= prefix::kMinRequests && G <= 16 &&
+                      (max_prefix_blocks > kShareAbove || (members - 1) * Hkv * max_prefix_blocks > kShareAbove * resident);
+  if (!shares) return bytes;
+  const PrefixItems it = prefix_items(batch, Hkv, G, D, num_prefixes, max_requests, max_prefix_blocks, sms);
+  long long items = kMaxWaves * it.n_slots;
+  if (items > it.units * it.tiles) items = it.units * it.tiles;
+  if (items < it.units) items = it.units;
+  bytes += align_up(((size_t)num_prefixes + 1) * sizeof(int2), 256);
+  bytes += (size_t)items * prefix::kRows * (D + 1) * sizeof(float);
+  if ((long long)batch * Hkv >= 2 * resident)  // apart
+    bytes += align_up((size_t)batch * Hq * D * sizeof(float), 256) + align_up((size_t)batch * Hq * sizeof(float), 256);
+  return bytes;
+}
+
 }  // namespace
 
 size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
@@ -1219,9 +1271,8 @@ size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_he
   if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_blocks_per_seq <= 0 ||
       block_size <= 0 || num_prefixes < 0 || max_requests < 0 || max_prefix_blocks < 0 || num_q_heads % num_kv_heads)
     return 0;
-  return prefix_ws(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_prefixes, max_requests,
-                   max_prefix_blocks, current_sms())
-      .total;
+  return prefix_ws_size(batch, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_prefixes, max_requests,
+                        max_prefix_blocks, current_sms());
 }
 
 minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,

@@ -110,6 +110,7 @@ constexpr int kListWarps = 4, kListMaxCtas = 4 * 160;
 DecodePlan plan_decode_list(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
 // The same for selected blocks and for what is left of a batch with shared prefixes: lists that may be short.
 DecodePlan plan_decode_lists(int batch, int Hkv, int G, int D, int max_blocks, bool bf16, int num_sms);
+constexpr long long kMaxCtaPairs = 1 << 16;  // (request, kv head) pairs that may have a CTA each there
 
 cudaError_t launch_decode(const DecodeArgs& a, bool bf16, bool rotate, const DecodePlan& plan, cudaStream_t s);
 cudaError_t launch_decode_simt(const DecodeArgs& a, bool bf16, bool rotate, cudaStream_t s);

@@ -3,7 +3,7 @@
 import pytest
 
 from list_util import make_batch
-from test_prefix_gpu import env  # noqa: F401  (a fixture)
+from test_prefix_gpu import env, groups  # noqa: F401  (env: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -56,4 +56,36 @@ def test_one_workspace_for_more_than_16384_pairs(env, Hkv):
             assert torch.equal(call(ws), want), (name, "again")
             assert torch.equal(dirty(ws), want_few[other]), (other, "after", name)
             assert not ws[:65536].any()
+    assert mp.device_error() == 0
+
+
+def first(t, n):
+    """The first n requests of a batch."""
+    rows = ("q", "block_tables", "block_starts", "seq_lens", "q_pos")
+    return {k: v[:n].contiguous() if k in rows else v for k, v in t.items()}
+
+
+def test_a_workspace_of_the_largest_batch_serves_smaller_ones(env):
+    """Batches that shrink request by request, as their plans change: a CTA a pair, the prefix kernel's waves."""
+    torch, mp, dev = env
+    t = make_batch(torch, dev, [3 + r % 30 for r in range(8193)], 8, 8, 64, "bf16", 5)
+    rope = mp.rope_table(t["max_pos"], 64, t["base"], device=dev)
+    ws = torch.zeros(mp.attn_decode_selected_workspace_size(8193, 8, 8, 64, 40), dtype=torch.uint8, device=dev)
+    for n in (8193, 8192, 8100, 75, 1):
+        s = first(t, n)
+        sel = torch.arange(40, dtype=torch.int32, device=dev).expand(n, 8, 40).contiguous()
+        a = (s["q"], s["k_pool"], s["v_pool"], s["block_tables"], s["block_starts"], s["seq_lens"], s["q_pos"], rope, sel)
+        assert torch.equal(mp.attn_decode_selected(*a, workspace=ws)[0], mp.attn_decode_selected(*a)[0]), n
+    del t, s, a
+    t = groups(torch, dev, [3200 + r % 90 for r in range(176)], [0, 176], [200], 128, 8, 128, 5)
+    rope = mp.rope_table(t["max_pos"], 128, t["base"], device=dev)
+    mb = t["block_tables"].shape[1]
+    ws = torch.zeros(mp.attn_decode_prefix_workspace_size(176, 128, 8, 128, mb, 1, 176, 200), dtype=torch.uint8, device=dev)
+    for n in (176, 175, 160, 159, 100, 33, 9, 2, 1):
+        s = first(t, n)
+        cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+        a = (s["q"], s["k_pool"], s["v_pool"], s["block_tables"], s["block_starts"], s["seq_lens"], s["q_pos"], rope, cu,
+             t["blocks"])
+        kw = dict(max_requests=n, max_prefix_blocks=200)
+        assert torch.equal(mp.attn_decode_prefix(*a, workspace=ws, **kw)[0], mp.attn_decode_prefix(*a, **kw)[0]), n
     assert mp.device_error() == 0
