@@ -370,12 +370,14 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
   const bool keep_lists = SHARE && a.batch <= kStagedLists;
   long long total = 0, sum = 0;
   int pairs = 0, zero = 0, Li = 0, n = 0, before = 0;
+  [[maybe_unused]] int longest = 0;  // of this thread's lists
   for (int base = 0; base < a.batch; base += NW * 32) {
     const int i = base + threadIdx.x;
     Li = i < a.batch ? __ldg(a.seq_lens + i) : 0;
     n = i < a.batch ? listed(i, Li) : 0;
     if (keep_lists && i < a.batch) lists[i] = n;
     if ((Li < 0 || (long long)Li > 16LL * mb) && blockIdx.x == 0) atomicOr(a.err, kErrSeqLen);
+    if constexpr (LIST != kAll) longest = max(longest, n);
     total += sum = cta_total(n, before);
     pairs += __syncthreads_count(n > 0);
     zero |= i < a.batch && n == 0 && i % gridDim.x == blockIdx.x;
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
         for (int e = threadIdx.x; e < a.Hq; e += NW * 32) a.lse[(size_t)i * a.Hq + e] = -CUDART_INF_F;
     }
   }
-  // lists of many short pairs: a CTA takes two kv heads of a request, one after the other (always `whole` below)
+  // lists of many short pairs: a CTA takes two kv heads of a request, one after the other (planned with a CTA a pair: always `whole` below)
   const bool two = LIST != kAll && a.list_heads == 2;
   const int n_heads = two ? a.Hkv / 2 : a.Hkv;  // what CTAs are numbered by: kv heads or pairs of them
   total *= n_heads;
@@ -475,11 +477,15 @@ __global__ void __launch_bounds__(kWarps * 32, CPS) decode_list_kernel(const __g
     // selected blocks and shared prefixes: also longer parts, one per CTA, where there are more CTAs than pairs: sum of
     // ceil(blocks / part) <= total / part + pairs (against equal ranges, in which most CTAs walk two pairs or more, and
     // join both: 64 pairs of 512 e4m3 blocks 43.2 -> 39.7 us; 256 pairs of 4 to 128 bf16 blocks behind prefixes, with
-    // those, 94 -> 70 us)
+    // those, 94 -> 70 us).  But no CTA's part gets longer than about two equal ranges: with few more CTAs than pairs
+    // parts are long, and so are long lists among short ones (bf16 blocks, whole parts and ranges; 448 pairs of 4 to 128:
+    // 48 us and 79, of 16 to 1024: 330 and 318, all but 8 of 64 and those of 8192: 1284 and 127; 256 pairs of 64 to 2048:
+    // 305 and 276; 408 pairs, all but 8 of 128 and those of 1024: 200 and 82).
     if (LIST != kAll && !whole && (long long)gridDim.x > all_pairs) {
       const long long room = min((long long)kMostParts, gridDim.x - all_pairs);
       part = (int)min((long long)(1 << 27), max((long long)kMinRange, (total + room - 1) / room));
-      whole = true;
+      const long long most = 2 * total / gridDim.x + kMinRange;
+      whole = a.list_heads > 0 || part <= most || !__syncthreads_or(longest > most);
     }
     // else equal ranges of the list, of at least kMinRange blocks, but no fewer of them than pairs
     const long long want = max((total + kMinRange - 1) / kMinRange, all_pairs);

@@ -40,7 +40,7 @@ struct DecodeArgs {
   // selected blocks (null: all)
   const int32_t* selected;   // [B][Hkv][max_sel] numbers of blocks in the request's table, -1: unused
   int max_sel;
-  int list_heads;            // kv heads of a request that a CTA of the list decode takes: 1 or 2
+  int list_heads;            // kv heads of a request that a CTA of the list decode takes, 1 or 2, if planned a CTA a pair
   // shared prefixes (null: none), whose part of the attention a kernel before has computed
   const int32_t* cu_requests;    // [n_prefix + 1]
   const int32_t* prefix_blocks;  // [n_prefix]
@@ -100,7 +100,7 @@ struct DecodePlan {
   int n_split;
   bool use_mma;
   int ctas_per_sm;  // tensor-core path: resident CTAs per SM (3 or 2; 1 for more than 8 heads per group)
-  int list_heads;     // kv heads of a request that a CTA of the list decode takes (2: an even number of them)
+  int list_heads;     // a CTA a pair: kv heads of a request that it takes, 1 or (of an even number of them) 2; else 0
 };
 DecodePlan plan_decode(int batch, int Hkv, int G, int D, int max_blocks, int bs, bool bf16, int num_sms);
 // Plan of the decode that takes all blocks as one list (e4m3, or bf16 with block
