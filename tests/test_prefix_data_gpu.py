@@ -77,3 +77,42 @@ def test_a_nan_query_shows(env, Hkv, d, B):
     nan = torch.zeros_like(lse, dtype=torch.bool)
     nan[[1, 3, 4], 1] = True
     assert torch.equal(lse.isnan(), nan) and torch.equal(out.isnan(), nan[..., None].expand_as(out))
+
+
+def shared_or_not(t):
+    """Bounds under which the kernel for shared prefixes runs, and ones under which nothing is shared."""
+    return (True, dict(max_requests=len(t["q"]), max_prefix_blocks=10 ** 6)), \
+           (False, dict(max_requests=len(t["q"]), max_prefix_blocks=int(t["blocks"].max())))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_outside_fp16(env, d):
+    """A key of a shared prefix outside fp16's range sets the range bit, and only rows of its kv head may be off; where the
+    bounds share nothing it is a key like any other."""
+    torch, mp, dev = env
+    t = groups(torch, dev, [16 * 12 + 9 * i for i in range(7)], [0, 4], [12], 8, 2, d, 59)
+    t["k_pool"][int(t["block_tables"][0, 3]), 1, 5, 9] = 2.0 ** 17
+    other = dict(t, q=t["q"][:, :4].contiguous(), Hkv=1, k_pool=t["k_pool"][:, :1], v_pool=t["v_pool"][:, :1])
+    for shared, bounds in shared_or_not(t):
+        out, lse = run(env, t, **bounds)
+        assert mp.device_error(clear=True) == (16 if shared else 0)
+        check(env, other, (out[:, :4], lse[:, :4]), f"kv head 0, d{d}")
+        assert shared or (out.isfinite().all() and lse.isfinite().all())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_blocks_that_start_before_position_0(env, d):
+    """In a shared prefix they are masked whole, where the bounds share nothing the slots before position 0 (flagged);
+    what the values of the masked slots hold does not show."""
+    torch, mp, dev = env
+    for start in (-5, -16, -10 ** 6):
+        t = groups(torch, dev, [16 * 12 + 9 * i for i in range(7)], [0, 7], [12], 8, 2, d, 61)
+        t["block_starts"][:, 4] = start
+        t["v_pool"][int(t["block_tables"][0, 4]), :, :min(16, -start)] = float("nan")
+        for shared, bounds in shared_or_not(t):
+            got = run(env, t, **bounds)
+            assert mp.device_error(clear=True) == 2
+            want = dict(t, block_starts=t["block_starts"].clone())
+            if shared:
+                want["block_starts"][:, 4] = -16
+            check(env, want, got, f"{start} shared {shared} d{d}")
