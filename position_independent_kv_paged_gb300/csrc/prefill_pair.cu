@@ -209,21 +209,16 @@ __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensor
   int q0, ql, kvl = 0, t_first = 0, t_end = 0;  // PREFIX: key tiles t_first .. t_end - 1
   int trow = r;                                  // row of the tables
   if constexpr (PREFIX) {
-    q0 = item->g.q0;
-    ql = item->g.n;
-    kvl = 16 * item->g.blocks;
-    const int tiles = (item->g.blocks + kTileBlocks - 1) / kTileBlocks;  // at least as many as parts
-    t_first = (int)((long long)item->part * tiles / item->parts);
-    t_end = (int)((long long)(item->part + 1) * tiles / item->parts);
     if (tid == 0 && crank == 0 && item->index == item->first)
       a.group_items[item->p] = make_int2(item->first, item->parts);
-    // the first request that holds the whole prefix; every warp looks for itself
-    trow = -1;
-    for (int i = 0; i < ql && trow < 0; i += 32) {
-      const unsigned has = __ballot_sync(FULL, i + lane < ql && __ldg(a.kv_lens + q0 + min(i + lane, ql - 1)) >= kvl);
-      if (has) trow = q0 + i + __ffs(has) - 1;
-    }
-    if (trow < 0) return;  // decided alike in both CTAs of the pair
+    const prefix::Work w = prefix::work_of<D>(a, *item);
+    if (w.row < 0) return;  // decided alike in both CTAs of the pair
+    q0 = w.q0;
+    ql = w.n;
+    kvl = w.keys;
+    t_first = w.t_first;
+    t_end = w.t_end;
+    trow = w.row;
   } else {
     q0 = a.cu_q_lens[r];
     ql = a.cu_q_lens[r + 1] - q0;

@@ -128,6 +128,25 @@ __device__ bool find_item(const PrefillArgs& a, int tq, long long c, Item& it) {
   return false;
 }
 
+// What an item computes: rows of requests q0 .. q0 + n - 1, key tiles t_first .. t_end - 1 of the first `keys` keys, by the
+// tables of request `row`, the first of the group that holds the whole prefix (-1: none does).  Every warp calls.
+struct Work {
+  int q0, n, keys, t_first, t_end, row;
+};
+template <int D>
+__device__ __forceinline__ Work work_of(const PrefillArgs& a, const Item& it) {
+  const int lane = threadIdx.x & 31;
+  const int tiles = (it.g.blocks + kTileBlocks<D> - 1) / kTileBlocks<D>;  // at least as many as parts
+  Work w{it.g.q0, it.g.n, 16 * it.g.blocks, (int)((long long)it.part * tiles / it.parts),
+         (int)((long long)(it.part + 1) * tiles / it.parts), -1};
+  for (int i = 0; i < w.n && w.row < 0; i += 32) {
+    const unsigned has = __ballot_sync(
+        0xffffffffu, i + lane < w.n && __ldg(a.kv_lens + w.q0 + min(i + lane, w.n - 1)) >= w.keys);
+    if (has) w.row = w.q0 + i + __ffs(has) - 1;
+  }
+  return w;
+}
+
 // The first item and the parts of request i's group p, which begins at request q0 (as the kernel that computed them
 // wrote it: each of its items has a CTA, see Group).
 __device__ __forceinline__ int2 items_of(const DecodeArgs& a, int p, int q0, int i) {
