@@ -1031,7 +1031,8 @@ minipic_status block_means(minipic_dtype dtype, const void* k_pool, const float*
   if (!b->cu_new_lens || !b->kv_start || !b->block_tables || !k_pool || !means) return MINIPIC_ERR_INVALID;
   if (!aligned16(k_pool) || !aligned16(means)) return MINIPIC_ERR_INVALID;
   MeansArgs a{};
-  if (device_info(&a.err, nullptr) != cudaSuccess) return MINIPIC_ERR_CUDA;
+  int sms = 0;
+  if (device_info(&a.err, &sms) != cudaSuccess) return MINIPIC_ERR_CUDA;
   a.k_pool = k_pool;
   a.k_scale = k_scale;
   a.cu_new = b->cu_new_lens;
@@ -1045,7 +1046,7 @@ minipic_status block_means(minipic_dtype dtype, const void* k_pool, const float*
   a.num_blocks = num_blocks;
   a.Hkv = Hkv;
   a.D = D;
-  return launch_block_means(a, dtype == MINIPIC_BF16, s) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
+  return launch_block_means(a, dtype == MINIPIC_BF16, sms, s) == cudaSuccess ? MINIPIC_OK : MINIPIC_ERR_CUDA;
 }
 
 }  // namespace

@@ -24,9 +24,9 @@ namespace minipic {
 namespace {
 
 constexpr int kThreads = 128;
-// Warps of one kv head each above which a warp takes two: 16 per SM (a step of 128 requests, 1024 warps: 4.2 us with
-// one, 4.5 with two; chunks of 8320 warps: 10.8 and 9.0).
-constexpr long long kManyWarps = 16 * 152;
+// Warps of one kv head each, per SM, above which a warp takes two (a step of 128 requests, 1024 warps on 152 SMs: 4.2 us
+// with one, 4.5 with two; chunks of 8320 warps: 10.8 and 9.0).
+constexpr long long kManyWarps = 16;
 constexpr unsigned FULL = 0xffffffffu;
 
 // Four consecutive elements of a row as loaded, and widened.
@@ -155,17 +155,18 @@ cudaError_t launch_u(const MeansArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 template <typename T, typename KV>
-cudaError_t launch_t(const MeansArgs& a, cudaStream_t s) {
+cudaError_t launch_t(const MeansArgs& a, int num_sms, cudaStream_t s) {
   const long long warps = ((a.max_new + 14LL) / 16 + 1) * a.Hkv * a.batch;
-  return warps > kManyWarps ? launch_u<T, KV, 2>(a, s) : launch_u<T, KV, 1>(a, s);
+  return warps > kManyWarps * num_sms ? launch_u<T, KV, 2>(a, s) : launch_u<T, KV, 1>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_block_means(const MeansArgs& a, bool bf16, cudaStream_t s) {
+cudaError_t launch_block_means(const MeansArgs& a, bool bf16, int num_sms, cudaStream_t s) {
   using B = __nv_bfloat16;
-  if (a.k_scale) return bf16 ? launch_t<B, __nv_fp8_e4m3>(a, s) : launch_t<float, __nv_fp8_e4m3>(a, s);
-  return bf16 ? launch_t<B, B>(a, s) : launch_t<float, float>(a, s);
+  using F8 = __nv_fp8_e4m3;
+  if (a.k_scale) return bf16 ? launch_t<B, F8>(a, num_sms, s) : launch_t<float, F8>(a, num_sms, s);
+  return bf16 ? launch_t<B, B>(a, num_sms, s) : launch_t<float, float>(a, num_sms, s);
 }
 
 }  // namespace minipic

@@ -231,7 +231,7 @@ struct MeansArgs {
   int batch, max_new, max_blocks, num_blocks, Hkv, D;
   int* err;
 };
-cudaError_t launch_block_means(const MeansArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_block_means(const MeansArgs& a, bool bf16, int num_sms, cudaStream_t s);
 
 // Mean score of every block of the tables for one query token per request.
 struct ScoresArgs {
