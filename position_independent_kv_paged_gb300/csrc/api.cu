@@ -1288,6 +1288,8 @@ minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_hea
   if (!groups || groups->num_prefixes < 0 || groups->max_requests < 0 || groups->max_prefix_blocks < 0)
     return MINIPIC_ERR_INVALID;
   if (groups->num_prefixes > 0 && (!groups->cu_requests || !groups->prefix_blocks)) return MINIPIC_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(groups->cu_requests) | reinterpret_cast<uintptr_t>(groups->prefix_blocks)) & 3u)
+    return MINIPIC_ERR_INVALID;
   if (empty) return MINIPIC_OK;
   if (kv->num_blocks == 0) return MINIPIC_ERR_INVALID;
   if (!list_fits(*kv, *b)) return MINIPIC_ERR_UNSUPPORTED;
