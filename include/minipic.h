@@ -558,8 +558,9 @@ typedef struct {
 /* scores[r][g][b] = the largest over the query heads of kv head g of scale *
  * (R_{q_pos} q)^T (R_{block_starts} m), the mean score of block b's keys, with
  * rope->cos_sin, products and sums of fp32's precision; NaN if one of the two has an
- * element that is not finite.  -infinity past the request's length, for a block id outside the pool and for a start outside [0, max_pos) (with
- * the error bits; a negative start is outside whatever its slots).  dtype is that of
+ * element that is not finite.  -infinity past the request's length, for a block id
+ * outside the pool and for a start outside [0, max_pos) (with the error bits; a
+ * negative start is outside whatever its slots).  dtype is that of
  * q and means.  UNSUPPORTED above 65535 requests or kv heads, or for
  * max_blocks_per_seq of 2^27 or more.  Asynchronous on `stream`. */
 minipic_status minipic_block_scores(minipic_dtype dtype, int32_t num_q_heads, const minipic_block_scores_batch* batch,
@@ -611,8 +612,9 @@ minipic_status minipic_attn_decode_selected_q8(minipic_dtype dtype, int32_t num_
 
 /* ------------------------------------------------------------------ shared prefixes
  * Batches whose requests begin with the same blocks at the same positions (a system
- * prompt, a document that many questions are about): their keys are read and rotated
- * once for the whole group. */
+ * prompt, a document that many questions are about): their keys are read from memory
+ * once for the whole group, and rotated once for every 2 * (128 / heads of a kv head)
+ * requests, instead of once for each. */
 typedef struct {
   const int32_t* cu_requests;    /* [num_prefixes + 1], ascending from >= 0 to <= batch: requests cu[p] .. cu[p+1]-1
                                     share prefix p; requests outside every group share nothing */
@@ -633,14 +635,19 @@ size_t minipic_attn_decode_prefix_workspace_size(int32_t batch, int32_t num_q_he
  * request attends to all its seq_lens keys), with the groups.  Only full blocks are
  * shared, as in the prefix cache.  A request of a group that is shorter than the
  * prefix (an empty row of a padded batch) reads its own keys and shares nothing; so do
- * the requests of a group with bad numbers or beyond the planning bounds
- * (MINIPIC_DEVERR_SEQ_LEN).  The attention to a shared prefix has the arithmetic and the
- * ranges of minipic_prefill_attn: rotated keys and scaled, rotated queries within
- * fp16's range (else MINIPIC_DEVERR_RANGE), P and V bf16, V finite in blocks that a bad
- * position masks too; the rest that of minipic_attn_decode_weights.  The workspace must
- * have been zeroed once, like that one's, and serves one call at a time; out and lse do
- * not overlap what the call reads.
- * Where the planning bounds say that sharing saves little, nothing is shared.
+ * the requests of a group with bad numbers or beyond the planning bounds, and of every
+ * group behind one whose boundaries descend (MINIPIC_DEVERR_SEQ_LEN).
+ * The attention to a shared prefix has the arithmetic and the ranges of
+ * minipic_attn_prefill: rotated keys and scaled, rotated queries within fp16's range
+ * (else MINIPIC_DEVERR_RANGE, and rows that read them are undefined), P and V
+ * bf16, a block that starts before position 0 masked whole, V finite in the slots that
+ * the table's end masks; the rest that of minipic_attn_decode_weights.
+ * Where shape and planning bounds say that sharing saves little, nothing is shared, and
+ * the latter's arithmetic and ranges hold for all keys; the bounds alone decide, so a
+ * call with other bounds may round differently.  Bounds much above what comes cost
+ * time (12 us and more for a batch that shares nothing after all).
+ * The workspace must have been zeroed once, like that one's, and serves one call at a
+ * time; out and lse do not overlap what the call reads.
  * bf16 only (f32 returns UNSUPPORTED; head dim 64 or 128). */
 minipic_status minipic_attn_decode_prefix(minipic_dtype dtype, int32_t num_q_heads, const minipic_kv_pool* kv,
                                           const minipic_rope* rope, const minipic_decode_batch* batch,

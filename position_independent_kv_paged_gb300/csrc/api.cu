@@ -1165,9 +1165,11 @@ namespace {
 // were as large as the planning bounds allow (eight balance well enough).  No looser: the clusters that find no item
 // start and end all the same, and the next kernel waits for their start.
 // Fewer blocks that sharing saves, per CTA of the list decode, do not pay for the kernel that computes the shared part:
-// then every request reads its own (us without and with it, 32 / 8 heads, d 128, 8 x 512 tokens, 1 block a CTA:
-// 13.5 and 22.0; 16 x 2048, 34: 24.0 and 28.1; 2 x 32768, 36: 43.5 and 62.5; 16 x 4096, 67: 35.4 and 30.0; 64 x 2048 of
-// 28 / 4 heads, 71: 44.9 and 33.3).
+// then every request reads its own (us without and with it, d 128, 32 / 8 heads, 8 x 512 tokens, 1 block a CTA: 13.5 and
+// 22.0; 16 x 2048, 34: 25.4 and 33.5; 12 x 4096, 49: 30.8 and 31.1; 24 x 2048, 52: 31.6 and 35.0; 64 x 1536 of 28 / 4
+// heads, 53: 37.8 and 36.3; 16 x 3584, 59: 34.2 and 34.0; 4 groups of 8 x 2048, 63: 47.1 and 40.7; 64 x 2048 of 28 / 4,
+// 71: 44.9 and 33.3).  One number does not fit all: 3 x 32768, 72, take 46.1 and 61.1, at d 64 16 x 4800, 59, 26.8 and
+// 31.2.
 constexpr long long kShareAbove = 56;
 constexpr int kMaxWaves = 8;
 struct PrefixItems {

@@ -8,11 +8,12 @@
 // with x1 the upper 11 bits, and x1 q1 + (x1 q2 + x2 q1) leaves out 2^-22 of a product.  The sums of the x1 q1 are cut
 // into four chains that meet in fp32: the tensor core's own additions truncate.
 //
-// A summary is 1 / 32 of a block's keys and values, so this reads that part of what attention would, and instructions
-// and their latency bound it: widening, rotating and splitting a summary, whatever the number of query heads (about 490
-// instructions for 16 blocks and a kv head, 40 % of the issue slots; 12 warps an SM).  64 requests x 512 blocks, 8 kv
-// heads, 4 query heads each: 21 us; 8 x 8192, 8 heads each: 39 us (packed fp32 arithmetic on the scalar pipes took 27
-// and 60: there each query head costs as much again as the products do here for eight).
+// A summary is 1 / 32 of a block's keys and values, so this reads that part of what attention would, and the latency of
+// loads and dependent instructions bounds it: 168 registers leave 12 warps an SM (10 active), which use 37 to 41 % of the
+// issue slots.  Widening, rotating and splitting a summary cost about 490 instructions for 16 blocks and a kv head, whatever
+// the number of query heads.  64 requests x 512 blocks, 8 kv heads, 4 query heads each: 21 us (floor 1.9 us); 8 x 8192,
+// 8 heads each: 39 us (packed fp32 arithmetic on the scalar pipes took 27 and 60: there each query head costs as much
+// again as the products do here for eight).
 //
 // A warp takes 16 blocks (the rows of the product) through the kv heads of its CTA: the cosines and sines of the
 // blocks' starts stay in registers, and the next head's summaries load, a chunk at a time, as soon as this one's are

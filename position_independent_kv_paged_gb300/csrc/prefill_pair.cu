@@ -184,7 +184,11 @@ __device__ __forceinline__ void regs_dec() {
 // PREFIX: an item of a group of requests that share their first blocks, one query
 // row each instead of a chunk; every row sees every key of the item's part of those
 // blocks, and the result goes to the partial results of the decode that joins it
-// with each request's other keys (decode_list.cuh).
+// with each request's other keys (decode_list.cuh).  Weights stay one bf16 number, as in
+// the prefill: as the sum of two (the second beside the first, in the columns of the
+// scores) the output's error falls from 2.3e-3 of its norm to 1.73e-3, where its own
+// rounding makes 1.66e-3, but 256 requests behind 32768 tokens take 391 us instead of
+// 303 (at head dim 64 414 and 351), 64 behind three documents 69 instead of 67.
 template <bool ROPE, int NSK, int NSV, bool KROT = ROPE, bool PREFIX = false>
 __device__ __forceinline__ void pair_cta(const CUtensorMap& kmap, const CUtensorMap& vmap, const PairLaunch& L,
                                          const int pair, const int hk, const int r, uint8_t* smem_raw,
