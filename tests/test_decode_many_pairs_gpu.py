@@ -89,3 +89,42 @@ def test_a_workspace_of_the_largest_batch_serves_smaller_ones(env):
         kw = dict(max_requests=n, max_prefix_blocks=200)
         assert torch.equal(mp.attn_decode_prefix(*a, workspace=ws, **kw)[0], mp.attn_decode_prefix(*a, **kw)[0]), n
     assert mp.device_error() == 0
+
+
+@pytest.mark.parametrize("Hkv,d", [(8, 64), (7, 128)])
+def test_many_pairs_behind_a_prefix_captured(env, Hkv, d):
+    """More pairs than counters, that share a prefix, with lists behind it that are cut: captured on a workspace that other
+    calls write to, replayed, and eager, each with the bits of a workspace of its own."""
+    torch, mp, dev = env
+    B, nb = 16384 // Hkv + 30, 40
+    own = [1 + r % 2 for r in range(B)]
+    for r in (B - 1, B - 5, B - 9, 2):
+        own[r] = 1500
+    long = make_batch(torch, dev, [16 * n - r % 16 for r, n in enumerate(own)], 2 * Hkv, Hkv, d, "bf16", d)
+    front = torch.arange(nb, dtype=torch.int32, device=dev)   # blocks of the longest list, shared by all
+    tables = torch.cat([long["block_tables"][2, front.long()].expand(B, nb), long["block_tables"]], 1).contiguous()
+    starts = torch.cat([(16 * front).expand(B, nb), long["block_starts"] + 16 * nb], 1).contiguous()
+    lens, pos = long["seq_lens"] + 16 * nb, long["q_pos"] + 16 * nb
+    rope = mp.rope_table(long["max_pos"] + 16 * nb, d, long["base"], device=dev)
+    cu, blocks = (torch.tensor(x, dtype=torch.int32, device=dev) for x in ([0, B], [nb]))
+    n = mp.attn_decode_prefix_workspace_size(B, 2 * Hkv, Hkv, d, tables.shape[1], 1, B, nb)
+    ws = torch.zeros(n, dtype=torch.uint8, device=dev)
+
+    def call(**kw):
+        return mp.attn_decode_prefix(long["q"], long["k_pool"], long["v_pool"], tables, starts, lens, pos, rope, cu, blocks,
+                                     max_requests=B, max_prefix_blocks=nb, **kw)[0]
+    want, out = call(), torch.full_like(long["q"], 7.0)
+    whole = mp.attn_decode(long["q"], long["k_pool"], long["v_pool"], tables, starts, lens, pos, rope)[0]
+    assert (want - whole).double().norm() <= 5e-3 * whole.double().norm()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out=out, workspace=ws)
+    for _ in range(2):
+        ws[65536:].fill_(0x11)
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and not ws[:65536].any()
+        ws[65536:].fill_(0x11)
+        assert torch.equal(call(workspace=ws), want)
+    assert mp.device_error() == 0
